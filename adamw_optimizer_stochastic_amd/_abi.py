@@ -17,7 +17,7 @@ ASR_OK, ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP = range(6)
 ASR_F32, ASR_BF16 = 0, 1
 ASR_ROUND_SR, ASR_ROUND_RN = 0, 1
 ASR_PROBE_READ, ASR_PROBE_WRITE, ASR_PROBE_COPY = 0, 1, 2
-ABI_VERSION = 107
+ABI_VERSION = 108
 
 STATUS_NAMES = {ASR_OK: "ASR_OK", ASR_EINVAL: "ASR_EINVAL", ASR_EDTYPE: "ASR_EDTYPE",
                 ASR_EALIGN: "ASR_EALIGN", ASR_EWORKSPACE: "ASR_EWORKSPACE",
@@ -97,6 +97,15 @@ _SIGNATURES = {
                                  _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64,
                                  _c.c_int32, _c.c_uint32, _c.c_uint32, _c.c_uint64,
                                  _c.c_void_p]),
+    "asr_quantize_i8_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int32]),
+    "asr_quantize_i8": (_c.c_int, [_c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64,
+                                   _c.c_int32, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int32,
+                                   _c.c_uint32, _c.c_uint32, _c.c_uint64, _c.c_void_p,
+                                   _c.c_size_t, _c.c_void_p]),
+    "asr_gemm_i8": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                               _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+                               _c.c_int64, _c.c_int64, _c.c_int32, _c.c_uint32, _c.c_uint32,
+                               _c.c_uint64, _c.c_void_p]),
     "asr_sr_bf16_given_bits": (_c.c_int, [_c.c_void_p] * 3 + [_c.c_int64, _c.c_void_p]),
 }
 
@@ -236,6 +245,23 @@ def asr_gemm_bf16(a, lda, b, ldb, c, ldc, c_f32, m, n, k, rounding, seed, step, 
                   stream):
     _check(lib().asr_gemm_bf16(a, lda, b, ldb, c, ldc, c_f32, m, n, k, rounding, seed, step,
                                base_index, stream), "asr_gemm_bf16")
+
+
+def asr_quantize_i8_workspace_bytes(rows, cols, transpose):
+    return int(lib().asr_quantize_i8_workspace_bytes(rows, cols, transpose))
+
+
+def asr_quantize_i8(x, dtype, ldx, rows, cols, transpose, q, ldq, scale, rounding, seed, step,
+                    base_index, workspace, workspace_bytes, stream):
+    _check(lib().asr_quantize_i8(x, dtype, ldx, rows, cols, transpose, q, ldq, scale, rounding,
+                                 seed, step, base_index, workspace, workspace_bytes, stream),
+           "asr_quantize_i8")
+
+
+def asr_gemm_i8(a, lda, b, ldb, scale_a, scale_b, c, ldc, c_f32, m, n, k, rounding, seed, step,
+                base_index, stream):
+    _check(lib().asr_gemm_i8(a, lda, b, ldb, scale_a, scale_b, c, ldc, c_f32, m, n, k, rounding,
+                             seed, step, base_index, stream), "asr_gemm_i8")
 
 
 def asr_random_uniform(out, dtype, n, low, high, seed, step, base_index, stream):

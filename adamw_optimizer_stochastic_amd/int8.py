@@ -1,0 +1,88 @@
+"""A linear layer whose three matrix products run in 8-bit integers.
+
+The layer's weights stay bf16 (the optimizers update them with stochastic
+rounding and no f32 master copy); every product quantises its operands on the
+way, with one scale for each row of both. Three products, with x (T, K), w
+(N, K) and the gradient dy (T, N):
+
+    y  = x  w^T    sums over K: scales for each token of x and channel of w
+    dx = dy w      sums over N: scales for each token of dy and input of w
+    dw = dy^T x    sums over T: scales for each output of dy and input of x
+
+x and w are rounded to nearest. dy is rounded stochastically (by default):
+its codes are then unbiased, so the quantisation of dy adds no bias to dx or
+dw. Element (t, n) of dy uses stream position base_index + t*N + n under key
+(seed, step), in both products.
+"""
+
+import torch
+
+from . import ops
+
+__all__ = ["linear_i8"]
+
+
+class _LinearI8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, grad_rounding, key):
+        ctx.save_for_backward(x, w)
+        ctx.grad_rounding, ctx.key = grad_rounding, key
+        qx, sx = ops.quantize_i8(x)
+        qw, sw = ops.quantize_i8(w)
+        return ops.gemm_i8(qx, qw, sx, sw)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w = ctx.saved_tensors
+        seed, step, base_index = ctx.key
+        stream = dict(rounding=ctx.grad_rounding, seed=seed, step=step, base_index=base_index)
+        if dy.stride(1) != 1 or dy.stride(0) < dy.shape[1]:
+            dy = dy.contiguous()   # an expanded or transposed gradient
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            qd, sd = ops.quantize_i8(dy, **stream)
+            qw, sw = ops.quantize_i8(w, transpose=True)
+            dx = ops.gemm_i8(qd, qw, sd, sw)
+        if ctx.needs_input_grad[1]:
+            qd, sd = ops.quantize_i8(dy, transpose=True, **stream)
+            qx, sx = ops.quantize_i8(x, transpose=True)
+            dw = ops.gemm_i8(qd, qx, sd, sx)
+        return dx, dw, None, None
+
+
+def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
+    """y = x w^T in 8-bit integer products, forward and backward.
+
+    x: bfloat16 (..., K); w: bfloat16 (N, K); y: bfloat16 (..., N). The
+    gradients are bfloat16. grad_rounding: "sr" (stochastic, under key (seed,
+    step), positions from base_index) or "rn", for the gradient's codes; give
+    every layer its own base_index (or seed) and every step its own step.
+    K, N and the number of tokens are below 2**17 (each is summed over once).
+    """
+    if grad_rounding not in ops.ROUNDING_CODE:
+        raise ValueError("grad_rounding must be 'sr' or 'rn'")
+    key = (ops._u32("seed", seed), ops._u32("step", step), ops._u64("base_index", base_index))
+    for t, name in ((x, "x"), (w, "w")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16 (got {t.dtype})")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on a GPU (got {t.device})")
+    if x.device != w.device:
+        raise ValueError("x and w must be on the same device")
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise ValueError(f"x must be (..., K) and w (N, K): got {tuple(x.shape)} and "
+                         f"{tuple(w.shape)}")
+    n, k = w.shape
+    tokens = x.numel() // k if k else x.shape[:-1].numel()
+    if max(tokens, n, k) >= 1 << 17:
+        raise ValueError("tokens, N and K must be below 2**17")
+    flat = x.reshape(tokens, k)
+    if flat.numel() and (flat.stride(1) != 1 or flat.stride(0) < k):
+        flat = flat.contiguous()
+    if w.numel() and (w.stride(1) != 1 or w.stride(0) < k):
+        w = w.contiguous()
+    y = _LinearI8.apply(flat, w, grad_rounding, key)
+    return y.reshape(*x.shape[:-1], n)

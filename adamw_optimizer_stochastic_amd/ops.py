@@ -320,6 +320,111 @@ def gemm_bf16(a, b, *, rounding="rn", seed=0, step=0, base_index=0, out=None, ou
     return out
 
 
+def _require_matrix(t, name, dtypes):
+    """t is a 2-D GPU tensor of one of `dtypes` whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU (got {t.device})")
+    if t.dtype not in dtypes or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D tensor of " +
+                        " or ".join(str(d).replace("torch.", "") for d in dtypes))
+    if t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    if t.numel() > 0 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+
+
+def _row_stride(t, least):
+    """Row stride of t, or `least` where there is no second row to walk to."""
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else max(least, 1)
+
+
+def _padded16(n):
+    return (n + 15) // 16 * 16
+
+
+def quantize_i8(x, *, transpose=False, rounding="rn", seed=0, step=0, base_index=0):
+    """8-bit codes of a float32 or bfloat16 matrix: (q, scale).
+
+    One scale a row, ``scale = max|x| / 127``: q is (R, C) int8 and
+    x is about ``q * scale[:, None]``. ``transpose=True``: one scale a COLUMN
+    of x, and q is the codes of x^T, (C, R) -- the operand of a product that
+    sums over x's rows. rounding "rn" (nearest, ties to even) or "sr"
+    (stochastic: x's element (i, j) uses stream position base_index + i*C +
+    j under key (seed, step), transposed or not). A row with an Inf or NaN
+    has scale NaN; one of zeros has scale 0.
+
+    q is a view of rows padded to a multiple of 16 bytes with zeros, which
+    ``gemm_i8`` takes as it is. x may have any row stride >= C.
+    """
+    if rounding not in ROUNDING_CODE:
+        raise ValueError("rounding must be 'rn' or 'sr'")
+    key = (_u32("seed", seed), _u32("step", step), _u64("base_index", base_index))
+    _require_matrix(x, "x", (torch.float32, torch.bfloat16))
+    rows, cols = x.shape
+    groups, length = (cols, rows) if transpose else (rows, cols)
+    ldq = max(_padded16(length), 16)
+    store = torch.empty((groups, ldq), dtype=torch.int8, device=x.device)
+    scale = torch.empty(groups, dtype=torch.float32, device=x.device)
+    need = _abi.asr_quantize_i8_workspace_bytes(rows, cols, int(transpose))
+    workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    with torch.cuda.device(x.device):
+        _abi.asr_quantize_i8(x.data_ptr(), _DTYPE_CODE[x.dtype], _row_stride(x, cols), rows, cols,
+                             int(transpose), store.data_ptr(), ldq, scale.data_ptr(),
+                             ROUNDING_CODE[rounding], *key,
+                             workspace.data_ptr() if need else None, need, _stream(x.device))
+    return store[:, :length], scale
+
+
+def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index=0, out=None,
+            out_f32=None):
+    """C = round((A B^T * scale_a[:, None]) * scale_b), rounded to bf16.
+
+    a (M x K) and b (N x K): int8, unit stride along K, row strides multiples
+    of 16 and 16-byte aligned starts (as ``quantize_i8`` lays them out); K
+    below 2**17, the sums exact integers. scale_a (M) and scale_b (N): float32.
+    Rounding, keys, ``out`` and ``out_f32`` as in ``gemm_bf16``.
+    """
+    if rounding not in ROUNDING_CODE:
+        raise ValueError("rounding must be 'rn' or 'sr'")
+    key = (_u32("seed", seed), _u32("step", step), _u64("base_index", base_index))
+    for t, name in ((a, "a"), (b, "b")):
+        _require_matrix(t, name, (torch.int8,))
+    if a.device != b.device:
+        raise ValueError("a and b must be on the same device")
+    if a.shape[1] != b.shape[1]:
+        raise ValueError(f"K mismatch: a is {tuple(a.shape)}, b is {tuple(b.shape)}")
+    m, k = a.shape
+    n = b.shape[0]
+    for t, size, name in ((scale_a, m, "scale_a"), (scale_b, n, "scale_b")):
+        _require_gpu(t, name)
+        if t.dtype != torch.float32 or tuple(t.shape) != (size,) or t.device != a.device:
+            raise ValueError(f"{name} must be a float32 tensor of shape ({size},) on a's device")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=a.device)
+    _require_matrix(out, "out", (torch.bfloat16,))
+    if tuple(out.shape) != (m, n) or out.device != a.device:
+        raise ValueError("out must be a bfloat16 (M, N) tensor on a's device")
+    outputs, f32_ptr = [_extent(out, "out")], None
+    if out_f32 is not None:
+        if out_f32.dtype != torch.float32 or tuple(out_f32.shape) != (m, n) \
+                or out_f32.device != a.device or out_f32.stride() != out.stride():
+            raise ValueError("out_f32 must be a float32 (M, N) tensor with out's strides")
+        f32_ptr = out_f32.data_ptr()
+        outputs.append(_extent(out_f32, "out_f32"))
+    check_disjoint(outputs)
+    for o in outputs:
+        for t, name in ((a, "a"), (b, "b"), (scale_a, "scale_a"), (scale_b, "scale_b")):
+            check_disjoint([o, _extent(t, name)])
+    with torch.cuda.device(a.device):
+        _abi.asr_gemm_i8(a.data_ptr(), _row_stride(a, max(_padded16(k), 16)), b.data_ptr(),
+                         _row_stride(b, max(_padded16(k), 16)), scale_a.data_ptr(), scale_b.data_ptr(),
+                         out.data_ptr(), _row_stride(out, n), f32_ptr, m, n, k,
+                         ROUNDING_CODE[rounding], *key, _stream(a.device))
+    return out
+
+
 class RoundingMode:
     """Rounding modes of the f32 -> bf16 conversion ("Add stochastic rounding
     and philox RNG helpers", discussion: stochastic rounding as a rounding

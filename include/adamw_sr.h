@@ -264,6 +264,67 @@ int asr_gemm_bf16(const uint16_t* a, int64_t lda, const uint16_t* b,
                   void* stream);
 
 /*
+ * 8-bit codes of a matrix with one scale a group, the operands of
+ * asr_gemm_i8. x is rows x cols, row i at x + i*ldx. A group is a row of x
+ * (transpose = 0) or a column of x (transpose = 1: q is then the transposed
+ * matrix, cols x rows, so that a group's codes are contiguous either way).
+ * For a group with largest magnitude amax:
+ *   scale = f32(amax / 127),
+ *   q = sign(x) * min(127, Q(|x| / scale)), of the exact quotient:
+ *   ASR_ROUND_RN: to nearest, ties to even;
+ *   ASR_ROUND_SR: floor(|x| / scale + r16 * 2**-16), r16 being the 16 bits of
+ *   stream position base_index + i*cols + j under key (seed, step) for x's
+ *   element (i, j), in both forms (rounding to either neighbour with
+ *   probabilities that make the code unbiased up to 2**-17 of a step).
+ * A group with an Inf or NaN gets scale NaN and codes 0; one whose scale
+ * would be below 2**-126 (all zeros, or all tiny) scale 0 and codes 0.
+ * Group g's codes start at q + g*ldq; they are followed by zeros up to the
+ * next multiple of 16.
+ * dtype: of x, ASR_F32 or ASR_BF16. scale: device, one f32 a group.
+ * Requirements: 0 <= rows, cols < 2**31; ldx >= cols; ldq a multiple of 16, at
+ * least the group's length; q 16-byte aligned; x and scale aligned to their
+ * elements (x's rows starting on 16-byte addresses take the vector path);
+ * rows <= 128 * 65535 in the transposed form; base_index + rows*cols <= 2**64;
+ * no buffer overlaps another. workspace: asr_quantize_i8_workspace_bytes
+ * bytes of device memory, 16-byte aligned (0 bytes, NULL allowed, unless
+ * transpose), as for asr_adamw_step.
+ * Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Runs
+ * on `stream`; does not synchronize.
+ */
+size_t asr_quantize_i8_workspace_bytes(int64_t rows, int64_t cols, int32_t transpose);
+int asr_quantize_i8(const void* x, int32_t dtype, int64_t ldx, int64_t rows,
+                    int64_t cols, int32_t transpose, int8_t* q, int64_t ldq,
+                    float* scale, int32_t rounding, uint32_t seed,
+                    uint32_t step, uint64_t base_index, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit integer GEMM with a scale for each row of both operands (for each
+ * token and each output channel of a linear layer y = x W^T):
+ *
+ *   C[m][n] = round((f32(sum_k A[m][k] * B[n][k]) * scale_a[m]) * scale_b[n])
+ *
+ * A (M x K) and B (N x K) are int8, row-major, K contiguous; the sum is exact
+ * (32-bit integers; any int8 values, -128 included), its conversion to f32
+ * and the two products are rounded to nearest, and C is rounded to bf16 by
+ * SR (position base_index + m*N + n under key (seed, step)) or RN, as
+ * asr_gemm_bf16 rounds. c_f32: NULL, or a device f32 buffer with row stride
+ * ldc that receives the value before that rounding.
+ * Bytes past a row's K codes are never used, whatever they hold.
+ * Requirements: 0 <= M, N < 2**31; 0 <= K < 2**17; lda, ldb multiples of 16,
+ * at least K and below 2**23; ldc >= N; a and b 16-byte aligned; scales, c and c_f32
+ * aligned to their element size; base_index + M*N <= 2**64; no output
+ * overlaps an input. M or N = 0 writes nothing; K = 0 writes products of 0.
+ * Errors: ASR_EINVAL, ASR_EALIGN, ASR_EHIP. Runs on `stream`; does not
+ * synchronize.
+ */
+int asr_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb,
+                const float* scale_a, const float* scale_b, uint16_t* c,
+                int64_t ldc, float* c_f32, int64_t m, int64_t n, int64_t k,
+                int32_t rounding, uint32_t seed, uint32_t step,
+                uint64_t base_index, void* stream);
+
+/*
  * Random numbers on the library's stream, beyond rounding.
  * ("Add stochastic rounding and philox RNG helpers", discussion: the
  * counter-based generator as a general facility for dropout and
@@ -379,7 +440,7 @@ const char* asr_last_error(void);
 /* ABI version of this header and library (major * 100 + minor). */
 int asr_abi_version(void);
 
-#define ASR_ABI_VERSION 107
+#define ASR_ABI_VERSION 108
 
 #ifdef __cplusplus
 }

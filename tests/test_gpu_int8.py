@@ -1,0 +1,303 @@
+"""The int8 quantiser, product and linear layer on the GPU.
+
+Everything here is exact, so everything is compared bit for bit: the codes and
+scales with the oracle's (formed in 64 bits), the product's f32 value with
+the oracle's int64 sums and binary32 products, its bf16 output with the
+oracle's rounding of that value. The linear layer's outputs equal the same
+products of the oracle's codes."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import int8 as o8
+from adamw_optimizer_stochastic_amd import linear_i8, ops, workloads as wl
+from _gpu_util import (gpu, require_gpu, announce, to_host, assert_bits_equal, f32_tensor,
+                       bf16_tensor)
+
+pytestmark = gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _matrix(rows, cols, dtype, seed, special=True):
+    """Normal values, rows of very different size, values on code borders,
+    zeros; as f32 values and as the device tensor."""
+    rng = np.random.default_rng([seed, rows, cols])
+    x = rng.standard_normal((rows, cols)) * 10.0 ** rng.integers(-3, 3, (rows, 1))
+    if special and rows * cols > 4:
+        x[rng.integers(0, rows)] = 0.0
+        i = rng.integers(0, rows)
+        x[i] = (rng.integers(-254, 255, cols) * 0.5)      # ties, with amax = 127
+        x[i, 0] = 127.0
+    x = x.astype(np.float32)
+    if dtype == "bf16":
+        bits = wl.f32_to_bf16_bits(x)
+        return oracle.bf16_to_f32(bits).reshape(rows, cols), bf16_tensor(bits.reshape(rows, cols))
+    return x, f32_tensor(x)
+
+
+def _check_codes(x, t, **kw):
+    q, s = ops.quantize_i8(t, **kw)
+    torch.cuda.synchronize()
+    want_q, want_s = o8.quantize(x, kw.get("transpose", False), kw.get("rounding", "rn"),
+                                 kw.get("seed", 0), kw.get("step", 0), kw.get("base_index", 0))
+    assert tuple(q.shape) == want_q.shape and q.dtype == torch.int8
+    got_s = to_host(s)
+    nan = np.isnan(want_s)
+    assert np.array_equal(np.isnan(got_s), nan)
+    assert_bits_equal(got_s[~nan], want_s[~nan], "scales")
+    assert np.array_equal(q.cpu().numpy(), want_q)
+    return q, s
+
+
+SHAPES = [(1, 1), (1, 8), (3, 7), (5, 16), (2, 2047), (9, 2049), (4, 4096), (3, 8200), (130, 70),
+          (129, 65), (257, 513), (1000, 33), (1, 9001)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("transpose", [False, True], ids=["rows", "columns"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_codes(shape, transpose, dtype):
+    announce("quantize", shape, transpose, dtype)
+    x, t = _matrix(*shape, dtype, 1)
+    q, _ = _check_codes(x, t, transpose=transpose)
+    if q.shape[1] % 16 and q.shape[0]:     # the padding behind every group's codes is zero
+        pad = torch.as_strided(q, (q.shape[0], 16 - q.shape[1] % 16), q.stride(),
+                               q.storage_offset() + q.shape[1])
+        assert not bool(pad.any())
+    for base in (0, 5, 2 ** 40 + 2):
+        _check_codes(x, t, transpose=transpose, rounding="sr", seed=11, step=7, base_index=base)
+
+
+def test_codes_of_special_values():
+    announce("quantize special")
+    x = np.zeros((8, 24), np.float32)
+    x[1, 3], x[2, 0], x[3, 23] = np.inf, np.nan, -np.inf
+    x[4] = 1e-39
+    x[5, :2] = 127 * 2.0 ** -126, 2.0 ** -149
+    x[6] = np.float32(3.4028234e38)
+    x[7] = -0.0
+    x[5, 2:] = np.linspace(0, 127 * 2.0 ** -126, 22).astype(np.float32)
+    for rounding in ("rn", "sr"):
+        _check_codes(x, f32_tensor(x), rounding=rounding, seed=3, step=1)
+        _check_codes(np.ascontiguousarray(x.T), f32_tensor(x.T), transpose=True,
+                     rounding=rounding, seed=3, step=1)
+
+
+@pytest.mark.parametrize("transpose", [False, True], ids=["rows", "columns"])
+def test_codes_of_strided_rows(transpose):
+    """Rows with a stride, starting off 16-byte boundaries."""
+    announce("quantize strided", transpose)
+    x, t = _matrix(37, 83, "bf16", 2)
+    for off, ld in ((0, 96), (1, 96), (3, 85)):
+        store = torch.full((37 * ld + 8,), 1e9, dtype=torch.bfloat16, device="cuda")
+        view = torch.as_strided(store, (37, 83), (ld, 1), off)
+        view.copy_(t)
+        _check_codes(x, view, transpose=transpose, rounding="sr", seed=1, step=1, base_index=1)
+
+
+def test_empty_groups():
+    announce("quantize empty")
+    for shape, transpose in (((0, 5), False), ((5, 0), False), ((0, 5), True), ((5, 0), True)):
+        x = torch.empty(shape, device="cuda")
+        q, s = ops.quantize_i8(x, transpose=transpose)
+        torch.cuda.synchronize()
+        assert tuple(q.shape) == (shape[::-1] if transpose else shape)
+        assert s.numel() == q.shape[0] and not bool(s.any())
+
+
+def test_stochastic_codes_are_unbiased():
+    """The mean over many keys of a code is x/s: each code is floor or ceil,
+    so its standard deviation is at most 1/2, and the mean over 400 keys of
+    4096 elements' errors at most 0.5 / sqrt(400 * 4096) = 3.9e-4; six of
+    those, plus the 2**-17 that 16 bits leave."""
+    announce("quantize unbiased")
+    x, t = _matrix(4, 1024, "f32", 3, special=False)
+    s = None
+    total = torch.zeros(4, 1024, dtype=torch.float64, device="cuda")
+    for k in range(400):
+        q, s = ops.quantize_i8(t, rounding="sr", seed=k, step=2)
+        total += q
+    err = to_host(total) / 400 - x.astype(np.float64) / to_host(s).astype(np.float64)[:, None]
+    err *= np.sign(x)
+    assert abs(err.mean()) < 6 * 0.5 / np.sqrt(400 * 4096) + 2.0 ** -17
+
+
+def _codes(rng, rows, k, ld, fill=77):
+    """int8 operand with row stride ld, garbage behind every row's K codes."""
+    full = np.full((rows, ld), fill, np.int8)
+    q = rng.integers(-128, 128, (rows, k)).astype(np.int8)
+    full[:, :k] = q
+    return q, torch.from_numpy(full).cuda()[:, :k]
+
+
+GEMM_SHAPES = [(1, 1, 1), (1, 16, 16), (1, 300, 100), (1, 4096, 4096), (2, 33, 64), (7, 130, 1000),
+               (16, 257, 513), (17, 64, 128), (33, 70, 65), (64, 64, 64), (65, 63, 127),
+               (100, 1000, 2049), (130, 4097, 144), (257, 259, 640), (520, 1100, 335),
+               (2100, 2100, 270), (4100, 4099, 143)]
+
+
+@pytest.mark.parametrize("shape", GEMM_SHAPES)
+def test_product(shape):
+    m, n, k = shape
+    announce("gemm_i8", shape)
+    rng = np.random.default_rng(shape)
+    ld = (k + 15) // 16 * 16
+    a, at = _codes(rng, m, k, ld)
+    b, bt = _codes(rng, n, k, ld + 16)
+    sa = (rng.random(m) * 0.1 + 1e-3).astype(np.float32)
+    sb = (rng.random(n) * 1e-3).astype(np.float32)
+    sat, sbt = f32_tensor(sa), f32_tensor(sb)
+    want = o8.gemm_f32(a, b, sa, sb)
+    for rounding, base in (("rn", 0), ("sr", 0), ("sr", 2 ** 33 + 3)):
+        c32 = torch.full((m, n), np.nan, device="cuda")
+        c = ops.gemm_i8(at, bt, sat, sbt, rounding=rounding, seed=9, step=4, base_index=base,
+                        out_f32=c32)
+        torch.cuda.synchronize()
+        assert_bits_equal(to_host(c32).reshape(-1), want.reshape(-1), "f32 value")
+        assert_bits_equal(to_host(c).reshape(-1),
+                          oracle.gemm_round(want, rounding, 9, 4, base).reshape(-1), rounding)
+        alone = ops.gemm_i8(at, bt, sat, sbt, rounding=rounding, seed=9, step=4, base_index=base)
+        assert torch.equal(alone.view(torch.int16), c.view(torch.int16))
+
+
+@pytest.mark.parametrize("m", [1, 5, 40, 300, 4100])
+def test_product_writes_nothing_else(m):
+    """Strided outputs, ragged and unaligned: what lies between the rows stays."""
+    announce("gemm_i8 strided out", m)
+    rng = np.random.default_rng(m)
+    n, k = 4109, 48
+    a, at = _codes(rng, m, k, 48)
+    b, bt = _codes(rng, n, k, 64)
+    sa, sb = np.ones(m, np.float32), np.full(n, 0.25, np.float32)
+    want = oracle.gemm_round(o8.gemm_f32(a, b, sa, sb), "sr", 1, 2, 0)
+    for ld, off in ((4112, 0), (4116, 4), (4111, 1)):
+        store = torch.full((m * ld + 8,), -7.0, dtype=torch.bfloat16, device="cuda")
+        out = torch.as_strided(store, (m, n), (ld, 1), off)
+        ops.gemm_i8(at, bt, f32_tensor(sa), f32_tensor(sb), rounding="sr", seed=1, step=2, out=out)
+        torch.cuda.synchronize()
+        assert_bits_equal(to_host(out).reshape(-1), want.reshape(-1), (ld, off))
+        out.fill_(-7.0)
+        assert bool((store == -7.0).all())
+
+
+def test_product_extremes():
+    """The largest sums (K = 2**17 - 1 of -128 * -128 stays below 2**31), NaN
+    scales, empty sums."""
+    announce("gemm_i8 extremes")
+    k = 2 ** 17 - 1
+    a = torch.full((3, 2 ** 17), -128, dtype=torch.int8, device="cuda")[:, :k]
+    one = torch.ones(3, device="cuda")
+    c32 = torch.empty((3, 3), device="cuda")
+    ops.gemm_i8(a, a, one, one, out=torch.empty((3, 3), dtype=torch.bfloat16, device="cuda"),
+                out_f32=c32)
+    assert bool((c32 == float(np.float32(k * 16384))).all())
+    nan = torch.tensor([1.0, float("nan"), 2.0], device="cuda")
+    c = ops.gemm_i8(a, a, nan, one)
+    assert torch.isnan(c[1]).all() and not torch.isnan(c[[0, 2]]).any()
+    empty = torch.empty((5, 0), dtype=torch.int8, device="cuda")
+    five = torch.ones(5, device="cuda")
+    assert not bool(ops.gemm_i8(empty, empty, five, five).any())
+    assert ops.gemm_i8(empty[:0], empty, five[:0], five).shape == (0, 5)
+
+
+def _bf16_of(x):
+    bits = wl.f32_to_bf16_bits(np.asarray(x, np.float32))
+    return oracle.bf16_to_f32(bits).reshape(x.shape), bf16_tensor(bits.reshape(x.shape))
+
+
+@pytest.mark.parametrize("shape", [(1, 16, 16), (5, 40, 24), (67, 512, 256), (130, 300, 1030),
+                                   (1, 4096, 1024), (300, 64, 7)])
+@pytest.mark.parametrize("grad_rounding", ["sr", "rn"])
+def test_linear(shape, grad_rounding):
+    t, n, k = shape
+    announce("linear_i8", shape, grad_rounding)
+    rng = np.random.default_rng(shape)
+    x, xt = _bf16_of(rng.standard_normal((t, k)))
+    w, wt = _bf16_of(rng.standard_normal((n, k)) * 0.02)
+    dy, dyt = _bf16_of(rng.standard_normal((t, n)) * 1e-3)
+    xt.requires_grad_()
+    wt.requires_grad_()
+    key = dict(seed=5, step=6, base_index=7)
+    y = linear_i8(xt, wt, grad_rounding=grad_rounding, **key)
+    dx, dw = torch.autograd.grad(y, (xt, wt), dyt)
+    torch.cuda.synchronize()
+
+    def product(left, right):
+        return oracle.gemm_round(o8.gemm_f32(left[0], right[0], left[1], right[1]), "rn")
+
+    assert_bits_equal(to_host(y).reshape(-1),
+                      product(o8.quantize(x), o8.quantize(w)).reshape(-1), "y")
+    want = product(o8.quantize(dy, False, grad_rounding, 5, 6, 7), o8.quantize(w, True))
+    assert_bits_equal(to_host(dx).reshape(-1), want.reshape(-1), "dx")
+    want = product(o8.quantize(dy, True, grad_rounding, 5, 6, 7), o8.quantize(x, True))
+    assert_bits_equal(to_host(dw).reshape(-1), want.reshape(-1), "dw")
+
+
+def test_linear_gradient_of_a_sum_and_shapes():
+    """A 3-D input, an expanded (broadcast) gradient, one input without a
+    gradient. Each product's codes are within half a step (one step for SR)
+    of the values, so y is within sum_k |x| sw/2 + |w| sx/2 + sx sw/4 of the
+    exact sum, plus the bf16 rounding and three binary32 ones."""
+    announce("linear_i8 shapes")
+    rng = np.random.default_rng(9)
+    x, xt = _bf16_of(rng.standard_normal((2, 3, 40)))
+    w, wt = _bf16_of(rng.standard_normal((24, 40)))
+    wt.requires_grad_()
+    y = linear_i8(xt, wt, seed=1)
+    assert y.shape == (2, 3, 24)
+    y.float().sum().backward()
+    assert wt.grad.shape == (24, 40) and xt.grad is None
+    x2 = x.reshape(6, 40).astype(np.float64)
+    sx = np.abs(x2).max(1)[:, None] / 127
+    sw = np.abs(w.astype(np.float64)).max(1)[None, :] / 127
+    bound = (np.abs(x2).sum(1)[:, None] * sw / 2 + np.abs(w).sum(1)[None, :] * sx / 2
+             + 40 * sx * sw / 4)
+    exact = x2 @ w.astype(np.float64).T
+    got = y.detach().float().cpu().numpy().reshape(6, 24)
+    assert np.all(np.abs(got - exact) <= 1.0001 * (bound + 2.0 ** -8 * (np.abs(exact) + bound)))
+    # dw = dy^T x with dy all ones: the codes of dy are exact (127 each)
+    dw = x2.sum(0)[None, :].repeat(24, 0)
+    sc = np.abs(x2).max(0)[None, :] / 127
+    err = 6 * sc / 2
+    assert np.all(np.abs(wt.grad.float().cpu().numpy() - dw)
+                  <= 1.0001 * (err + 2.0 ** -8 * (np.abs(dw) + err)))
+
+
+def test_other_stream_and_capture():
+    """The quantiser and product on a side stream, then captured and replayed."""
+    announce("int8 capture")
+    rng = np.random.default_rng(4)
+    x, xt = _bf16_of(rng.standard_normal((70, 300)))
+    w, wt = _bf16_of(rng.standard_normal((90, 300)))
+
+    def once():
+        qx, sx = ops.quantize_i8(xt, rounding="sr", seed=1, step=2)
+        qw, sw = ops.quantize_i8(wt)
+        qt, st = ops.quantize_i8(xt, transpose=True)
+        return ops.gemm_i8(qx, qw, sx, sw, rounding="sr", seed=3, step=4), qt, st
+
+    want = [to_host(v) for v in once()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = once()
+    side.synchronize()
+    for g, v in zip(got, want):
+        assert np.array_equal(to_host(g), v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = once()
+    for r in range(3):
+        for v in out:
+            v.fill_(0)
+        torch.zeros(1 << 20, device="cuda").sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, v in zip(out, want):
+            assert np.array_equal(to_host(g), v), r

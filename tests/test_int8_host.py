@@ -1,0 +1,103 @@
+"""Refusals of the int8 entry points (CPU only; no call here launches a kernel)."""
+
+import pytest
+import torch
+
+from adamw_optimizer_stochastic_amd import _abi, _build, linear_i8, ops
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not _build.is_built():
+        _build.build()
+
+
+def _status(fn, *args):
+    try:
+        fn(*args)
+    except _abi.AsrError as e:
+        return e.status
+    return _abi.ASR_OK
+
+
+def test_quantize_argument_errors():
+    E = _abi
+
+    def q(x=0x1000, dtype=E.ASR_BF16, ldx=64, rows=8, cols=60, transpose=0, q=0x4000, ldq=64,
+          scale=0x8000, rounding=E.ASR_ROUND_SR, base=0, ws=None, ws_bytes=0):
+        return _status(E.asr_quantize_i8, x, dtype, ldx, rows, cols, transpose, q, ldq, scale,
+                       rounding, 1, 2, base, ws, ws_bytes, None)
+
+    assert q(rows=-1) == E.ASR_EINVAL
+    assert q(cols=2 ** 31) == E.ASR_EINVAL
+    assert q(dtype=2) == E.ASR_EDTYPE
+    assert q(rounding=3) == E.ASR_EINVAL
+    assert q(x=0) == E.ASR_EINVAL
+    assert q(q=0) == E.ASR_EINVAL
+    assert q(scale=0) == E.ASR_EINVAL
+    assert q(ldx=59) == E.ASR_EINVAL
+    assert q(ldq=48) == E.ASR_EINVAL
+    assert q(ldq=72) == E.ASR_EINVAL
+    assert q(x=0x1001) == E.ASR_EALIGN
+    assert q(dtype=E.ASR_F32, x=0x1002) == E.ASR_EALIGN
+    assert q(q=0x4008) == E.ASR_EALIGN
+    assert q(scale=0x8002) == E.ASR_EALIGN
+    assert q(base=2 ** 64 - 8 * 60 + 1) == E.ASR_EINVAL
+    assert q(transpose=1, ldq=16) == E.ASR_EWORKSPACE
+    need = E.asr_quantize_i8_workspace_bytes(8, 60, 1)
+    assert need >= 60 * 4 and E.asr_quantize_i8_workspace_bytes(8, 60, 0) == 0
+    assert q(transpose=1, ldq=16, ws=0x10000, ws_bytes=need - 1) == E.ASR_EWORKSPACE
+    assert q(transpose=1, ldq=16, ws=0x10008, ws_bytes=need) == E.ASR_EWORKSPACE
+    assert q(transpose=1, rows=128 * 65535 + 1, ldq=128 * 65536, ws=0x10000,
+             ws_bytes=1 << 40) == E.ASR_EINVAL
+    assert q(rows=0, x=0, q=0, scale=0) == E.ASR_OK
+    assert q(cols=0, transpose=1, x=0, q=0, scale=0) == E.ASR_OK
+
+
+def test_gemm_i8_argument_errors():
+    E = _abi
+
+    def g(a=0x1000, lda=64, b=0x2000, ldb=64, sa=0x5000, sb=0x6000, c=0x3000, ldc=32, c32=None,
+          m=16, n=32, k=60, rounding=E.ASR_ROUND_SR, base=0):
+        return _status(E.asr_gemm_i8, a, lda, b, ldb, sa, sb, c, ldc, c32, m, n, k, rounding, 1,
+                       2, base, None)
+
+    assert g(m=-1) == E.ASR_EINVAL
+    assert g(n=2 ** 31) == E.ASR_EINVAL
+    assert g(k=2 ** 17, lda=2 ** 17, ldb=2 ** 17) == E.ASR_EINVAL
+    assert g(rounding=2) == E.ASR_EINVAL
+    for name in ("a", "b", "sa", "sb", "c"):
+        assert g(**{name: 0}) == E.ASR_EINVAL
+    assert g(lda=48) == E.ASR_EINVAL
+    assert g(ldc=31) == E.ASR_EINVAL
+    assert g(lda=2 ** 23) == E.ASR_EINVAL
+    assert g(ldb=72) == E.ASR_EALIGN
+    assert g(a=0x1008) == E.ASR_EALIGN
+    assert g(c=0x3001) == E.ASR_EALIGN
+    assert g(c32=0x3002) == E.ASR_EALIGN
+    assert g(sa=0x5001) == E.ASR_EALIGN
+    assert g(base=2 ** 64 - 16 * 32 + 1) == E.ASR_EINVAL
+    assert g(m=0, a=0, b=0, c=0, sa=0, sb=0) == E.ASR_OK
+
+
+def test_binding_refuses_what_is_not_on_a_gpu():
+    x = torch.zeros(4, 16)
+    q = torch.zeros(4, 16, dtype=torch.int8)
+    s = torch.zeros(4)
+    w = torch.zeros(4, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        ops.quantize_i8(x)
+    with pytest.raises(ValueError, match="GPU"):
+        ops.gemm_i8(q, q, s, s)
+    with pytest.raises(ValueError, match="GPU"):
+        linear_i8(w, w)
+    with pytest.raises(ValueError, match="rounding"):
+        ops.quantize_i8(x, rounding="up")
+    with pytest.raises(ValueError, match="rounding"):
+        linear_i8(w, w, grad_rounding="up")
+    with pytest.raises(TypeError):
+        ops.quantize_i8([1.0])
+    with pytest.raises(TypeError):
+        linear_i8(x, w)
+    with pytest.raises(ValueError, match="seed"):
+        ops.quantize_i8(x, seed=2 ** 32)
