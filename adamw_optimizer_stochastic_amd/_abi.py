@@ -44,6 +44,16 @@ class AsrTensor(ctypes.Structure):
     ]
 
 
+class AsrMuonTensor(ctypes.Structure):
+    """asr_muon_tensor (32 bytes)."""
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("momentum", ctypes.c_void_p),
+        ("base_index", ctypes.c_uint64),
+    ]
+
+
 # The same layout as a numpy structured dtype, so that a list's descriptors
 # can be filled column by column.
 ASR_TENSOR_DTYPE = None
@@ -106,6 +116,15 @@ _SIGNATURES = {
                                _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
                                _c.c_int64, _c.c_int64, _c.c_int32, _c.c_uint32, _c.c_uint32,
                                _c.c_uint64, _c.c_void_p]),
+    "asr_newton_schulz_workspace_bytes": (_c.c_size_t, [_c.c_int32, _c.c_int64, _c.c_int64]),
+    "asr_newton_schulz": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.POINTER(_c.c_void_p), _c.c_int32,
+                                     _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32] +
+                          [_c.c_double] * 4 + [_c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "asr_muon_step": (_c.c_int, [_c.POINTER(AsrMuonTensor), _c.c_int32, _c.c_int64, _c.c_int64,
+                                 _c.c_int32, _c.c_int32, _c.c_double, _c.c_double, _c.c_int32,
+                                 _c.c_double, _c.c_double, _c.c_int32] + [_c.c_double] * 4 +
+                      [_c.c_int64, _c.c_uint32, _c.c_int32, _c.c_void_p, _c.c_size_t,
+                       _c.c_void_p]),
     "asr_sr_bf16_given_bits": (_c.c_int, [_c.c_void_p] * 3 + [_c.c_int64, _c.c_void_p]),
 }
 
@@ -262,6 +281,31 @@ def asr_gemm_i8(a, lda, b, ldb, scale_a, scale_b, c, ldc, c_f32, m, n, k, roundi
                 base_index, stream):
     _check(lib().asr_gemm_i8(a, lda, b, ldb, scale_a, scale_b, c, ldc, c_f32, m, n, k, rounding,
                              seed, step, base_index, stream), "asr_gemm_i8")
+
+
+def asr_newton_schulz_workspace_bytes(n, rows, cols):
+    return int(lib().asr_newton_schulz_workspace_bytes(n, rows, cols))
+
+
+def asr_newton_schulz(g, out, rows, cols, g_dtype, steps, a, b, c, eps, workspace,
+                      workspace_bytes, stream):
+    """g, out: sequences of device addresses, one a matrix."""
+    n = len(g)
+    arr = ctypes.c_void_p * max(n, 1)
+    _check(lib().asr_newton_schulz(arr(*g), arr(*out), n, rows, cols, g_dtype, steps, a, b, c,
+                                   eps, workspace, workspace_bytes, stream), "asr_newton_schulz")
+
+
+def asr_muon_step(tensors, rows, cols, param_dtype, grad_dtype, lr, momentum, nesterov,
+                  weight_decay, lr_factor, ns_steps, ns_coefficients, eps, step, seed, rounding,
+                  workspace, workspace_bytes, stream):
+    """tensors: sequence of (param, grad, momentum, base_index)."""
+    n = len(tensors)
+    arr = (AsrMuonTensor * max(n, 1))(*tensors)
+    _check(lib().asr_muon_step(arr, n, rows, cols, param_dtype, grad_dtype, lr, momentum,
+                               nesterov, weight_decay, lr_factor, ns_steps, *ns_coefficients, eps,
+                               step, seed, rounding, workspace, workspace_bytes, stream),
+           "asr_muon_step")
 
 
 def asr_random_uniform(out, dtype, n, low, high, seed, step, base_index, stream):

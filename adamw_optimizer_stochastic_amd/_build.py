@@ -1,9 +1,10 @@
 """Build step: compiles the HIP sources into the in-tree shared library.
 
-Four translation units (csrc/adamw_sr.hip: the AdamW step, the generator and
+Five translation units (csrc/adamw_sr.hip: the AdamW step, the generator and
 the conversions; csrc/gemm_sr.hip: the GEMM; csrc/random.hip: uniform/normal
-draws and dropout; csrc/int8.hip: the int8 quantiser and product, on the K
-loop of csrc/mfma_loop.hpp; all include csrc/device.hpp, csrc/status.hpp and
+draws and dropout; csrc/int8.hip: the int8 quantiser and product; csrc/muon.hip:
+Newton-Schulz products and the Muon step, both on the K loop of
+csrc/mfma_loop.hpp; all include csrc/device.hpp, csrc/status.hpp and
 include/adamw_sr.h) -> libadamw_sr.so, for gfx950 only. Flags that matter
 for the arithmetic:
   -ffp-contract=off                          no fused multiply-adds (the
@@ -26,7 +27,8 @@ ROOT = os.path.dirname(PKG_DIR)
 SOURCES = [os.path.join(PKG_DIR, "csrc", "adamw_sr.hip"),
            os.path.join(PKG_DIR, "csrc", "gemm_sr.hip"),
            os.path.join(PKG_DIR, "csrc", "random.hip"),
-           os.path.join(PKG_DIR, "csrc", "int8.hip")]
+           os.path.join(PKG_DIR, "csrc", "int8.hip"),
+           os.path.join(PKG_DIR, "csrc", "muon.hip")]
 DEPENDS = SOURCES + [os.path.join(PKG_DIR, "csrc", "device.hpp"),
                      os.path.join(PKG_DIR, "csrc", "mfma_loop.hpp"),
                      os.path.join(PKG_DIR, "csrc", "status.hpp"),

@@ -1,0 +1,146 @@
+"""MuonSR: a torch.optim.Optimizer over the fused Muon step.
+
+Takes the arguments of torch.optim.Muon, for the 2-D parameters of hidden
+layers (embeddings, the output layer, norms and biases belong to AdamWSR), and
+this library's rounding: bf16 parameters are updated without an f32 master
+copy, by stochastic rounding under key (seed, step) at each element's
+position. Positions run over all parameters of the optimizer as in AdamWSR;
+``base_offset`` moves them, so that the two optimizers of one model need not
+share positions (give MuonSR the number of elements AdamWSR has).
+
+For each matrix: m = momentum*m + g (f32), u = g + momentum*m (nesterov) or m,
+p = p*(1 - lr*weight_decay) - lr*factor*O(u), O the Newton-Schulz
+orthogonalisation. Matrices of one shape go through the products together,
+which is what fills the chip with small ones.
+"""
+
+import torch
+
+from . import ops
+from .optim import _step_count
+
+__all__ = ["MuonSR"]
+
+
+class MuonSR(torch.optim.Optimizer):
+    def __init__(self, params, lr=1e-3, weight_decay=0.1, momentum=0.95, nesterov=True,
+                 ns_coefficients=ops.NS_COEFFICIENTS, eps=1e-7, ns_steps=5, adjust_lr_fn=None,
+                 *, seed=0, rounding="sr", base_offset=0):
+        if isinstance(lr, torch.Tensor):
+            raise NotImplementedError("MuonSR: tensor lr is not supported")
+        if not 0.0 <= lr:
+            raise ValueError(f"Invalid learning rate: {lr}")
+        if not 0.0 <= weight_decay:
+            raise ValueError(f"Invalid weight_decay value: {weight_decay}")
+        if not 0.0 <= momentum < 1.0:
+            raise ValueError(f"Invalid momentum value: {momentum}")
+        if not 0.0 <= eps:
+            raise ValueError(f"Invalid epsilon value: {eps}")
+        if not 1 <= ns_steps <= 64:
+            raise ValueError("ns_steps must be in [1, 64]")
+        if rounding not in ("sr", "rn"):
+            raise ValueError("rounding must be 'sr' or 'rn'")
+        if not (isinstance(seed, int) and 0 <= seed < (1 << 32)):
+            raise ValueError("seed must be an integer in [0, 2**32)")
+        adjust_lr_fn = "original" if adjust_lr_fn is None else adjust_lr_fn
+        ops.muon_lr_factor(1, 1, adjust_lr_fn)
+        self.seed = seed
+        self._base_index = {}
+        self._next_index = ops._u64("base_offset", base_offset)
+        self._workspaces = {}
+        defaults = dict(lr=lr, weight_decay=weight_decay, momentum=momentum, nesterov=nesterov,
+                        ns_coefficients=ops._coefficients(ns_coefficients), eps=eps,
+                        ns_steps=ns_steps, adjust_lr_fn=adjust_lr_fn, rounding=rounding)
+        super().__init__(params, defaults)
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        for p in self.param_groups[-1]["params"]:
+            if p.dim() != 2:
+                raise ValueError(f"MuonSR takes 2-D parameters (got shape {tuple(p.shape)})")
+            if p.is_sparse or p.is_complex() or p.dtype not in (torch.float32, torch.bfloat16):
+                raise NotImplementedError(
+                    f"MuonSR supports dense float32/bfloat16 params (got {p.dtype})")
+            self._base_index[p] = self._next_index
+            self._next_index += p.numel()
+
+    def base_index(self, p):
+        """Global position of element 0 of parameter p."""
+        return self._base_index[p]
+
+    def _init_state(self, p):
+        if len(self.state[p]) == 0:
+            self.state[p] = {"step": torch.tensor(0, dtype=torch.int64),
+                             "momentum_buffer": torch.zeros(p.shape, dtype=torch.float32,
+                                                            device=p.device)}
+
+    def _workspace(self, device, shapes):
+        """The workspace of this device and its current stream: a step only
+        reuses it behind the step before, in stream order."""
+        key = (device, torch.cuda.current_stream(device).cuda_stream)
+        ws = self._workspaces.get(key)
+        need = ops.muon_workspace_bytes(shapes)
+        if ws is None or ws.numel() < need:
+            ws = self._workspaces[key] = torch.empty(max(need, 1), dtype=torch.uint8,
+                                                     device=device)
+        return ws
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            batches = {}   # (device, step) -> params
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if p.grad.is_sparse:
+                    raise NotImplementedError("MuonSR does not support sparse gradients")
+                if not p.is_contiguous() or not p.grad.is_contiguous():
+                    raise NotImplementedError("MuonSR needs contiguous params and grads")
+                self._init_state(p)
+                t = int(self.state[p]["step"]) + 1
+                batches.setdefault((p.device, t), []).append(p)
+            for (device, t), ps in batches.items():
+                ops.muon_step(ps, [p.grad for p in ps],
+                              [self.state[p]["momentum_buffer"] for p in ps],
+                              [self._base_index[p] for p in ps], lr=group["lr"],
+                              momentum=group["momentum"], nesterov=group["nesterov"],
+                              weight_decay=group["weight_decay"], ns_steps=group["ns_steps"],
+                              ns_coefficients=group["ns_coefficients"], eps=group["eps"],
+                              adjust_lr=group["adjust_lr_fn"], step=t, seed=self.seed,
+                              rounding=group["rounding"],
+                              workspace=self._workspace(device, [p.shape for p in ps]))
+                for p in ps:
+                    self.state[p]["step"].fill_(t)
+        return loss
+
+    def state_dict(self):
+        sd = super().state_dict()
+        sd["muon_sr"] = {"seed": self.seed}
+        return sd
+
+    def load_state_dict(self, state_dict):
+        """Like torch's, except that the momentum stays float32 whatever the
+        parameter dtype (torch's loader would cast it)."""
+        extra = state_dict.get("muon_sr")
+        saved_state = state_dict.get("state", {})
+        plain = {k: v for k, v in state_dict.items() if k not in ("muon_sr", "state")}
+        plain["state"] = {}
+        super().load_state_dict(plain)
+        saved_ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        params = [p for g in self.param_groups for p in g["params"]]
+        for p in params:
+            self.state.pop(p, None)
+        for p, pid in zip(params, saved_ids):
+            st = saved_state.get(pid)
+            if st is None:
+                continue
+            self._init_state(p)
+            self.state[p]["step"].fill_(_step_count(st["step"]))
+            self.state[p]["momentum_buffer"].copy_(
+                st["momentum_buffer"].detach().reshape(p.shape))
+        if extra is not None:
+            self.seed = int(extra["seed"])

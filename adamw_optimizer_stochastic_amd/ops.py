@@ -425,6 +425,136 @@ def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index
     return out
 
 
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _coefficients(c):
+    c = tuple(float(x) for x in c)
+    if len(c) != 3:
+        raise ValueError("three Newton-Schulz coefficients (a, b, c) are needed")
+    return c
+
+
+def _ns_workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be on {device} and hold {need} bytes")
+    return workspace
+
+
+def newton_schulz(g, *, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, workspace=None):
+    """Orthogonalises a matrix, or each of a batch, by Newton-Schulz products.
+
+    g: float32 or bfloat16, (M, N) or (B, M, N), contiguous. X = g / (|g|_F +
+    eps), then ``steps`` times X = a X + (b A + c A A) X with A = X X^T (on
+    the short side); the result is bfloat16 (nearest even) of g's shape.
+    About 2e-3 of it (relative, Frobenius norm) from the exact value: f16
+    products with f32 sums, X held as two f16 numbers. A g of zeros gives
+    zeros, a matrix with an Inf or NaN only NaN. ``out``: bfloat16, g's shape,
+    contiguous (g itself if it is bfloat16).
+    """
+    coefficients = _coefficients(coefficients)
+    _require_gpu(g, "g")
+    if g.dtype not in _DTYPE_CODE or g.dim() not in (2, 3):
+        raise TypeError("g must be a float32 or bfloat16 tensor of 2 or 3 dimensions")
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    _require_gpu(out, "out")
+    if out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != g.device:
+        raise ValueError("out must be bfloat16 with g's shape, on g's device")
+    if out.data_ptr() != g.data_ptr() or g.dtype != torch.bfloat16:
+        check_disjoint([_extent(g, "g"), _extent(out, "out")])
+    rows, cols = g.shape[-2:]
+    n = g.shape[0] if g.dim() == 3 else 1
+    need = _abi.asr_newton_schulz_workspace_bytes(n, rows, cols)
+    workspace = _ns_workspace(workspace, need, g.device)
+    size, size_out = rows * cols * g.element_size(), rows * cols * 2
+    with torch.cuda.device(g.device):
+        _abi.asr_newton_schulz([g.data_ptr() + k * size for k in range(n)],
+                               [out.data_ptr() + k * size_out for k in range(n)], rows, cols,
+                               _DTYPE_CODE[g.dtype], operator.index(steps), *coefficients,
+                               float(eps), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream(g.device))
+    return out
+
+
+def muon_lr_factor(rows, cols, adjust_lr="original"):
+    """What Muon multiplies the learning rate of a (rows, cols) matrix by:
+    "original" sqrt(max(1, rows / cols)), or "match_rms_adamw" 0.2
+    sqrt(max(rows, cols)) (updates as large as AdamW's)."""
+    if adjust_lr == "original":
+        return max(1.0, rows / cols) ** 0.5 if cols else 1.0
+    if adjust_lr == "match_rms_adamw":
+        return 0.2 * max(rows, cols) ** 0.5
+    raise ValueError("adjust_lr must be 'original' or 'match_rms_adamw'")
+
+
+def muon_workspace_bytes(shapes):
+    """Workspace bytes of a muon_step over matrices of these shapes."""
+    count = {}
+    for s in shapes:
+        count[tuple(s)] = count.get(tuple(s), 0) + 1
+    return max((_abi.asr_newton_schulz_workspace_bytes(k, *s) for s, k in count.items()),
+               default=0)
+
+
+def muon_step(params, grads, momenta, base_indices, *, lr, momentum=0.95, nesterov=True,
+              weight_decay=0.0, ns_steps=5, ns_coefficients=NS_COEFFICIENTS, eps=1e-7,
+              adjust_lr="original", step, seed, rounding="sr", workspace=None):
+    """One Muon step over lists of matrices on one device (in place).
+
+    params: 2-D, f32 or bf16; grads: f32 or bf16; momenta: f32; all
+    contiguous, of one shape a matrix. m = momentum*m + g, u = g + momentum*m
+    (nesterov) or m, p = p*(1 - lr*weight_decay) - lr*factor*newton_schulz(u),
+    with factor = muon_lr_factor(rows, cols, adjust_lr). bf16 params are
+    rounded by ``rounding`` ("sr": element i of a matrix at position
+    base_index + i under key (seed, step), or "rn"). Matrices of one shape
+    and type go through the products together.
+    """
+    n = len(params)
+    if not (len(grads) == len(momenta) == len(base_indices) == n):
+        raise ValueError("all lists must have the same length")
+    if rounding not in ROUNDING_CODE:
+        raise ValueError("rounding must be 'sr' or 'rn'")
+    seed = _u32("seed", seed)
+    step = operator.index(step)
+    if not 1 <= step < (1 << 32):
+        raise ValueError("step must be in [1, 2**32 - 1]")
+    coefficients = _coefficients(ns_coefficients)
+    muon_lr_factor(1, 1, adjust_lr)
+    groups, spans, device = {}, [], None
+    for i, (p, g, m, base) in enumerate(zip(params, grads, momenta, base_indices)):
+        for t, name in ((p, "param"), (g, "grad"), (m, "momentum")):
+            _require_gpu(t, f"{name}[{i}]")
+            device = device or t.device
+            if t.device != device:
+                raise ValueError("all tensors must be on one device")
+            spans.append((t.data_ptr(), t.numel() * t.element_size(), f"{name}[{i}]"))
+        if p.dtype not in _DTYPE_CODE or g.dtype not in _DTYPE_CODE or p.dim() != 2:
+            raise TypeError(f"matrix {i}: params and grads must be 2-D float32 or bfloat16")
+        if m.dtype != torch.float32:
+            raise TypeError(f"matrix {i}: momenta must be float32")
+        if g.shape != p.shape or m.shape != p.shape:
+            raise ValueError(f"matrix {i}: param, grad and momentum differ in shape")
+        groups.setdefault((*p.shape, p.dtype, g.dtype), []).append(
+            (p.data_ptr(), g.data_ptr(), m.data_ptr(), _u64(f"base_indices[{i}]", base)))
+    if n == 0:
+        return
+    check_disjoint(spans)
+    need = max(_abi.asr_newton_schulz_workspace_bytes(len(ts), rows, cols)
+               for (rows, cols, _, _), ts in groups.items())
+    workspace = _ns_workspace(workspace, need, device)
+    with torch.cuda.device(device):
+        for (rows, cols, pt, gt), ts in groups.items():
+            _abi.asr_muon_step(ts, rows, cols, _DTYPE_CODE[pt], _DTYPE_CODE[gt], float(lr),
+                               float(momentum), int(bool(nesterov)), float(weight_decay),
+                               muon_lr_factor(rows, cols, adjust_lr), operator.index(ns_steps),
+                               coefficients, float(eps), step, seed, ROUNDING_CODE[rounding],
+                               workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream(device))
+
+
 class RoundingMode:
     """Rounding modes of the f32 -> bf16 conversion ("Add stochastic rounding
     and philox RNG helpers", discussion: stochastic rounding as a rounding

@@ -325,6 +325,70 @@ int asr_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb,
                 uint64_t base_index, void* stream);
 
 /*
+ * Orthogonalisation of n matrices of one shape by Newton-Schulz products:
+ *
+ *   X = G / (|G|_F + eps), its short side first;
+ *   steps times:  A = X X^T,  X <- a X + (b A + c A A) X;
+ *   out = bf16(X), in G's orientation, rounded to nearest even.
+ *
+ * With (a, b, c) = (3.4445, -4.775, 2.0315) and 5 steps, singular values from
+ * about 1/100 of |G|_F up come out between about 0.7 and 1.2 (the update of
+ * the Muon optimizer). The products run on the matrix cores with f16 operands
+ * and f32 sums, X itself held as two f16 numbers: the result is within about
+ * 2e-3 (relative, Frobenius norm) of the exact one, low-rank G included. The norm is
+ * summed in 64 bits. A G of zeros gives zeros; an Inf or NaN in G makes all
+ * of its result NaN.
+ *
+ * g, out: host arrays of n device pointers (read during the call only), each
+ * to rows x cols contiguous elements, of g_dtype (ASR_F32 or ASR_BF16) and of
+ * bf16. out[k] may be g[k] itself (bf16); otherwise no buffer overlaps another.
+ * Requirements: 0 <= rows, cols <= 2**20; 1 <= steps <= 64; eps >= 0; the coefficients
+ * must keep singular values in [0, 1] below 1.4 over the steps, and
+ * |b x^2 + c x^4| below 3.75 there. workspace:
+ * asr_newton_schulz_workspace_bytes(n, rows, cols) bytes of device memory,
+ * 256-byte aligned, overwritten in stream order: calls that may overlap need
+ * a workspace each. (About 8 bytes an element and 4 a squared short side; at
+ * most 16 matrices at a time, and of large ones about 4 GiB, are in flight
+ * together.)
+ * Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Runs
+ * on `stream`; does not synchronize; nothing is allocated.
+ */
+size_t asr_newton_schulz_workspace_bytes(int32_t n, int64_t rows, int64_t cols);
+int asr_newton_schulz(const void* const* g, uint16_t* const* out, int32_t n,
+                      int64_t rows, int64_t cols, int32_t g_dtype,
+                      int32_t steps, double a, double b, double c, double eps,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One Muon step over n matrices of one shape and type. For each, in binary32,
+ * every operation rounded on its own:
+ *   m <- momentum*m + g,   u = nesterov ? g + momentum*m : m,
+ *   O = the orthogonalisation of u as above (before its rounding to bf16),
+ *   p <- p*decay - eta*O,  decay = f32(1 - lr*weight_decay),
+ *                          eta = f32(lr*lr_factor).
+ * A bf16 parameter is rounded by SR (element (i, j) at position base_index +
+ * i*cols + j under key (seed, step)) or RN, an f32 one stored as computed (O
+ * keeps the accuracy above). lr_factor: the adjustment to the shape, for
+ * example sqrt(max(1, rows / cols)), or 0.2 sqrt(max(rows, cols)).
+ * lr, weight_decay, lr_factor >= 0; 0 <= momentum < 1; step in [1, 2**32 - 1].
+ * tensors: host array, read during the call only; buffers pairwise disjoint.
+ * Other arguments, workspace and errors as for asr_newton_schulz.
+ */
+typedef struct asr_muon_tensor {
+  void* param;          /* rows*cols elements of param_dtype, updated in place */
+  const void* grad;     /* rows*cols elements of grad_dtype, read only         */
+  float* momentum;      /* rows*cols f32, updated in place                     */
+  uint64_t base_index;  /* global position of element 0 (random-bit stream)    */
+} asr_muon_tensor;
+int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int64_t rows,
+                  int64_t cols, int32_t param_dtype, int32_t grad_dtype,
+                  double lr, double momentum, int32_t nesterov,
+                  double weight_decay, double lr_factor, int32_t ns_steps,
+                  double ns_a, double ns_b, double ns_c, double eps,
+                  int64_t step, uint32_t seed, int32_t rounding,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Random numbers on the library's stream, beyond rounding.
  * ("Add stochastic rounding and philox RNG helpers", discussion: the
  * counter-based generator as a general facility for dropout and

@@ -1,0 +1,175 @@
+"""Refusals of the Newton-Schulz and Muon entry points, and MuonSR's host side
+(CPU only; no call here launches a kernel)."""
+
+import ctypes
+
+import pytest
+import torch
+
+from adamw_optimizer_stochastic_amd import MuonSR, _abi, _build, ops
+
+NS = (3.4445, -4.7750, 2.0315)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not _build.is_built():
+        _build.build()
+
+
+def _status(fn, *args):
+    try:
+        fn(*args)
+    except _abi.AsrError as e:
+        return e.status
+    return _abi.ASR_OK
+
+
+def test_newton_schulz_argument_errors():
+    E = _abi
+    need = E.asr_newton_schulz_workspace_bytes(1, 40, 60)
+
+    def f(g=(0x1000,), out=(0x8000,), rows=40, cols=60, dtype=E.ASR_BF16, steps=5, coeffs=NS,
+          eps=1e-7, ws=0x100000, ws_bytes=need):
+        return _status(E.asr_newton_schulz, g, out, rows, cols, dtype, steps, *coeffs, eps, ws,
+                       ws_bytes, None)
+
+    assert f(rows=-1) == E.ASR_EINVAL
+    assert f(cols=2 ** 20 + 1) == E.ASR_EINVAL
+    assert f(dtype=7) == E.ASR_EDTYPE
+    assert f(steps=0) == E.ASR_EINVAL
+    assert f(steps=65) == E.ASR_EINVAL
+    assert f(eps=-1.0) == E.ASR_EINVAL
+    assert f(eps=float("nan")) == E.ASR_EINVAL
+    # singular values would leave the range the f16 operands are scaled for
+    assert f(coeffs=(8.0, -20.0, 14.0)) == E.ASR_EINVAL
+    assert f(coeffs=(float("nan"), 0.0, 0.0)) == E.ASR_EINVAL
+    assert f(coeffs=(1.0, 5.0, 0.0)) == E.ASR_EINVAL
+    assert f(g=(0,)) == E.ASR_EINVAL
+    assert f(out=(0,)) == E.ASR_EINVAL
+    assert f(g=(0x1001,)) == E.ASR_EALIGN
+    assert f(dtype=E.ASR_F32, g=(0x1002,)) == E.ASR_EALIGN
+    assert f(out=(0x8001,)) == E.ASR_EALIGN
+    assert f(ws=0) == E.ASR_EWORKSPACE
+    assert f(ws=0x100080) == E.ASR_EWORKSPACE
+    assert f(ws_bytes=need - 1) == E.ASR_EWORKSPACE
+    assert f(g=(), out=()) == E.ASR_OK
+    assert f(rows=0, g=(0,), out=(0,), ws=0, ws_bytes=0) == E.ASR_OK
+
+
+def test_accepted_coefficients():
+    """The usual choices pass the range check (the missing workspace is what
+    stops the call)."""
+    E = _abi
+    for c in (NS, (1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (2.0, -1.5, 0.5)):
+        got = _status(E.asr_newton_schulz, (0x1000,), (0x8000,), 8, 8, E.ASR_BF16, 5, *c, 1e-7, 0,
+                      0, None)
+        assert got == E.ASR_EWORKSPACE, c
+
+
+def test_workspace_bytes():
+    f = _abi.asr_newton_schulz_workspace_bytes
+    assert f(0, 8, 8) == 0 and f(1, 0, 8) == 0 and f(1, -1, 8) == 0
+    assert f(1, 300, 100) >= 8 * 100 * 300 + 4 * 100 * 100
+    one = f(1, 100, 300)
+    assert one >= 8 * 100 * 300 + 4 * 100 * 100
+    assert f(3, 100, 300) == 3 * one
+    assert f(16, 100, 300) == f(500, 100, 300) == 16 * one   # at most 16 at a time
+    big = f(1, 8192, 28672)
+    assert f(9, 8192, 28672) == max(1, (4 << 30) // big) * big
+
+
+def test_muon_argument_errors():
+    E = _abi
+    need = E.asr_newton_schulz_workspace_bytes(1, 40, 60)
+    good = (0x1000, 0x8000, 0x10000, 0)
+    assert ctypes.sizeof(E.AsrMuonTensor) == 32
+
+    def f(t=good, rows=40, cols=60, pt=E.ASR_BF16, gt=E.ASR_BF16, lr=0.1, mu=0.9, wd=0.1,
+          factor=1.0, steps=5, coeffs=NS, eps=1e-7, step=1, rounding=E.ASR_ROUND_SR,
+          ws=0x100000, ws_bytes=need):
+        return _status(E.asr_muon_step, [t], rows, cols, pt, gt, lr, mu, 1, wd, factor, steps,
+                       coeffs, eps, step, 0, rounding, ws, ws_bytes, None)
+
+    assert f(rows=-1) == E.ASR_EINVAL
+    assert f(pt=4) == E.ASR_EDTYPE
+    assert f(gt=4) == E.ASR_EDTYPE
+    for bad in (-0.1, float("inf"), float("nan")):
+        assert f(lr=bad) == E.ASR_EINVAL
+        assert f(wd=bad) == E.ASR_EINVAL
+        assert f(factor=bad) == E.ASR_EINVAL
+        assert f(mu=bad) == E.ASR_EINVAL
+    assert f(mu=1.0) == E.ASR_EINVAL
+    assert f(step=0) == E.ASR_EINVAL
+    assert f(step=2 ** 32) == E.ASR_EINVAL
+    assert f(rounding=2) == E.ASR_EINVAL
+    assert f(steps=0) == E.ASR_EINVAL
+    for i in range(3):
+        assert f(t=tuple(0 if j == i else v for j, v in enumerate(good))) == E.ASR_EINVAL
+    assert f(t=(0x1001, *good[1:])) == E.ASR_EALIGN
+    assert f(t=(0x1000, 0x8000, 0x10002, 0)) == E.ASR_EALIGN
+    assert f(ws=0) == E.ASR_EWORKSPACE
+    assert f(cols=0, ws=0, ws_bytes=0) == E.ASR_OK
+
+
+def test_binding_refusals():
+    x = torch.zeros(4, 6)
+    with pytest.raises(ValueError, match="GPU"):
+        ops.newton_schulz(x)
+    with pytest.raises(ValueError, match="three"):
+        ops.newton_schulz(x, coefficients=(1.0, 2.0))
+    with pytest.raises(ValueError, match="GPU"):
+        ops.muon_step([x], [x], [x], [0], lr=0.1, step=1, seed=0)
+    with pytest.raises(ValueError, match="length"):
+        ops.muon_step([x], [x], [], [0], lr=0.1, step=1, seed=0)
+    with pytest.raises(ValueError, match="adjust_lr"):
+        ops.muon_step([], [], [], [], lr=0.1, step=1, seed=0, adjust_lr="none")
+    with pytest.raises(ValueError, match="step"):
+        ops.muon_step([], [], [], [], lr=0.1, step=0, seed=0)
+    ops.muon_step([], [], [], [], lr=0.1, step=1, seed=0)
+
+
+def test_lr_factor():
+    f = ops.muon_lr_factor
+    assert f(100, 400) == 1.0 and f(400, 100) == 2.0
+    assert f(100, 400, "match_rms_adamw") == f(400, 100, "match_rms_adamw") == 0.2 * 20
+
+
+def _param(*shape, dtype=torch.float32):
+    return torch.nn.Parameter(torch.zeros(shape, dtype=dtype))
+
+
+def test_optimizer_refusals():
+    for kw in (dict(lr=-1.0), dict(weight_decay=-1.0), dict(momentum=1.0), dict(eps=-1.0),
+               dict(ns_steps=0), dict(rounding="up"), dict(seed=-1), dict(adjust_lr_fn="x"),
+               dict(base_offset=-1), dict(ns_coefficients=(1.0,))):
+        with pytest.raises(ValueError):
+            MuonSR([_param(4, 4)], **kw)
+    with pytest.raises(NotImplementedError):
+        MuonSR([_param(4, 4)], lr=torch.tensor(0.1))
+    with pytest.raises(ValueError, match="2-D"):
+        MuonSR([_param(4)])
+    with pytest.raises(NotImplementedError):
+        MuonSR([_param(4, 4, dtype=torch.float64)])
+
+
+def test_optimizer_positions_and_state():
+    a, b, c = _param(3, 4), _param(5, 2, dtype=torch.bfloat16), _param(2, 2)
+    opt = MuonSR([a, b], seed=7, base_offset=100)
+    opt.add_param_group(dict(params=[c], lr=0.5))
+    assert [opt.base_index(p) for p in (a, b, c)] == [100, 112, 122]
+    assert opt.param_groups[0]["adjust_lr_fn"] == "original"
+    for p in (a, b):
+        opt._init_state(p)
+    opt.state[b]["momentum_buffer"].fill_(1.0009765625)   # not a bf16 number
+    opt.state[b]["step"].fill_(2 ** 25 + 1)               # not a float32 number
+    sd = opt.state_dict()
+    other = MuonSR([_param(3, 4), _param(5, 2, dtype=torch.bfloat16)], seed=1)
+    other.add_param_group(dict(params=[_param(2, 2)]))
+    other.load_state_dict(sd)
+    p = other.param_groups[0]["params"][1]
+    assert other.seed == 7 and int(other.state[p]["step"]) == 2 ** 25 + 1
+    assert other.state[p]["momentum_buffer"].dtype == torch.float32
+    assert bool((other.state[p]["momentum_buffer"] == 1.0009765625).all())
+    assert other.param_groups[1]["lr"] == 0.5
+    opt.step()   # no gradients: nothing to do
