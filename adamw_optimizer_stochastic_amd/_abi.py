@@ -45,12 +45,15 @@ class AsrTensor(ctypes.Structure):
 
 
 class AsrMuonTensor(ctypes.Structure):
-    """asr_muon_tensor (32 bytes)."""
+    """asr_muon_tensor (56 bytes)."""
     _fields_ = [
         ("param", ctypes.c_void_p),
         ("grad", ctypes.c_void_p),
         ("momentum", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
         ("base_index", ctypes.c_uint64),
+        ("lr_factor", ctypes.c_double),
     ]
 
 
@@ -120,9 +123,10 @@ _SIGNATURES = {
     "asr_newton_schulz": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.POINTER(_c.c_void_p), _c.c_int32,
                                      _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32] +
                           [_c.c_double] * 4 + [_c.c_void_p, _c.c_size_t, _c.c_void_p]),
-    "asr_muon_step": (_c.c_int, [_c.POINTER(AsrMuonTensor), _c.c_int32, _c.c_int64, _c.c_int64,
-                                 _c.c_int32, _c.c_int32, _c.c_double, _c.c_double, _c.c_int32,
-                                 _c.c_double, _c.c_double, _c.c_int32] + [_c.c_double] * 4 +
+    "asr_muon_workspace_bytes": (_c.c_size_t, [_c.POINTER(AsrMuonTensor), _c.c_int32]),
+    "asr_muon_step": (_c.c_int, [_c.POINTER(AsrMuonTensor), _c.c_int32, _c.c_int32, _c.c_int32,
+                                 _c.c_double, _c.c_double, _c.c_int32, _c.c_double, _c.c_int32] +
+                      [_c.c_double] * 4 +
                       [_c.c_int64, _c.c_uint32, _c.c_int32, _c.c_void_p, _c.c_size_t,
                        _c.c_void_p]),
     "asr_sr_bf16_given_bits": (_c.c_int, [_c.c_void_p] * 3 + [_c.c_int64, _c.c_void_p]),
@@ -296,16 +300,22 @@ def asr_newton_schulz(g, out, rows, cols, g_dtype, steps, a, b, c, eps, workspac
                                    eps, workspace, workspace_bytes, stream), "asr_newton_schulz")
 
 
-def asr_muon_step(tensors, rows, cols, param_dtype, grad_dtype, lr, momentum, nesterov,
-                  weight_decay, lr_factor, ns_steps, ns_coefficients, eps, step, seed, rounding,
-                  workspace, workspace_bytes, stream):
-    """tensors: sequence of (param, grad, momentum, base_index)."""
-    n = len(tensors)
-    arr = (AsrMuonTensor * max(n, 1))(*tensors)
-    _check(lib().asr_muon_step(arr, n, rows, cols, param_dtype, grad_dtype, lr, momentum,
-                               nesterov, weight_decay, lr_factor, ns_steps, *ns_coefficients, eps,
-                               step, seed, rounding, workspace, workspace_bytes, stream),
-           "asr_muon_step")
+def muon_array(tensors):
+    """A ctypes array of asr_muon_tensor from (param, grad, momentum, rows,
+    cols, base_index, lr_factor) tuples, for the entry points below."""
+    return (AsrMuonTensor * max(len(tensors), 1))(*tensors)
+
+
+def asr_muon_workspace_bytes(array, n):
+    return int(lib().asr_muon_workspace_bytes(array, n))
+
+
+def asr_muon_step(array, n, param_dtype, grad_dtype, lr, momentum, nesterov, weight_decay,
+                  ns_steps, ns_coefficients, eps, step, seed, rounding, workspace,
+                  workspace_bytes, stream):
+    _check(lib().asr_muon_step(array, n, param_dtype, grad_dtype, lr, momentum, nesterov,
+                               weight_decay, ns_steps, *ns_coefficients, eps, step, seed,
+                               rounding, workspace, workspace_bytes, stream), "asr_muon_step")
 
 
 def asr_random_uniform(out, dtype, n, low, high, seed, step, base_index, stream):

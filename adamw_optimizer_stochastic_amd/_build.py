@@ -44,6 +44,12 @@ FLAGS = [
     "-Wall", "-Wextra", "-Wno-unused-command-line-argument",
 ]
 
+# Accumulators of the matrix instructions in VGPRs: in a workgroup of 4 waves
+# the compiler otherwise puts them in AGPRs and moves them to VGPRs and back in
+# every K tile (192 moves beside 16 instructions, 128 x 128 tile).
+_VGPR_ACC = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+SOURCE_FLAGS = {"int8.hip": _VGPR_ACC, "muon.hip": _VGPR_ACC}
+
 
 def hipcc():
     path = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -65,7 +71,8 @@ def build(out_path=LIB_PATH, extra_flags=(), verbose=False):
         jobs = []
         for src in SOURCES:
             obj = os.path.join(objdir, os.path.basename(src) + ".o")
-            cmd = [hipcc(), *compile_flags, *extra_flags, "-I", os.path.join(ROOT, "include"),
+            own = SOURCE_FLAGS.get(os.path.basename(src), [])
+            cmd = [hipcc(), *compile_flags, *own, *extra_flags, "-I", os.path.join(ROOT, "include"),
                    "-c", src, "-o", obj]
             jobs.append((cmd, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                     stderr=subprocess.STDOUT, text=True)))

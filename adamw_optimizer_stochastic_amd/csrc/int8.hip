@@ -34,7 +34,7 @@ struct GroupScale {
   float s;     // the scale the group's codes are divided by, times k
   float inv;   // 1 / s
   float k;     // power of two that keeps every product with s a normal number
-  bool live;   // false: every code is 0 (no element, only tiny ones, Inf or NaN)
+  uint32_t live;  // 0: every code is 0 (no element, only tiny ones, Inf or NaN)
 };
 
 // The scale to store for a group whose largest |x| has these bits, and what
@@ -181,19 +181,20 @@ __global__ __launch_bounds__(256) void quantize_rows(QuantArgs a) {
   }
 }
 
-// Column maxima of one chunk of rows: a workgroup takes 512 columns, each
-// wave every fourth row.
+// Column maxima of one chunk of rows: a workgroup takes 128 columns (256
+// bytes of a bf16 row) and 16 rows at a time. Few chunks, so that the second
+// kernel reads few of them; narrow strips, so that few chunks fill the chip.
 template <typename S>
 __global__ __launch_bounds__(256) void column_maxima(QuantArgs a) {
-  __shared__ uint32_t tops[4][512];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 512 + lane * 8;
+  __shared__ uint32_t tops[16][128 + 4];
+  const int cg = threadIdx.x % 16, rr = threadIdx.x / 16;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 128, col = c0 + cg * 8;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.chunk;
   const int64_t r1 = min(a.rows, r0 + a.chunk);
   uint32_t top[8] = {};
   if (col < a.cols) {
 #pragma unroll 4
-    for (int64_t r = r0 + wave; r < r1; r += 4) {
+    for (int64_t r = r0 + rr; r < r1; r += 16) {
       float t[8];
       load8<S>(static_cast<const S*>(a.x) + r * a.ldx, col, a.cols, a.vec, t);
 #pragma unroll
@@ -201,40 +202,29 @@ __global__ __launch_bounds__(256) void column_maxima(QuantArgs a) {
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) tops[wave][lane * 8 + e] = top[e];
+  for (int e = 0; e < 8; ++e) tops[rr][cg * 8 + e] = top[e];
   __syncthreads();
-  for (int c = threadIdx.x; c < 512; c += 256) {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 512 + c;
-    if (at < a.cols)
-      a.part[static_cast<int64_t>(blockIdx.y) * a.cols + at] =
-          max(max(tops[0][c], tops[1][c]), max(tops[2][c], tops[3][c]));
+  if (threadIdx.x < 128 && c0 + threadIdx.x < a.cols) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, tops[i][threadIdx.x]);
+    a.part[static_cast<int64_t>(blockIdx.y) * a.cols + c0 + threadIdx.x] = m;
   }
 }
 
 // Codes of a tile of 128 rows x 64 columns of x, written as 64 rows of 128
 // codes of the transposed result. A thread takes 4 consecutive rows of 8
-// columns at a time, so 4 codes of one column make one LDS word.
+// columns, so 4 codes of one column make one LDS word.
 template <typename S, bool SR>
 __global__ __launch_bounds__(256) void quantize_columns(QuantArgs a) {
   constexpr int kWords = 33;  // LDS words a column: 32 and one against bank conflicts
   __shared__ uint32_t tile[64 * kWords];
-  __shared__ uint32_t tops[64];
+  __shared__ uint32_t tops[4][64];
+  __shared__ __align__(16) GroupScale scales[64];
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 64;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 128;
-  if (threadIdx.x < 64) {
-    uint32_t top = 0;
-    if (c0 + threadIdx.x < a.cols)
-      for (int c = 0; c < a.chunks; ++c)
-        top = max(top, a.part[static_cast<int64_t>(c) * a.cols + c0 + threadIdx.x]);
-    tops[threadIdx.x] = top;
-    GroupScale g;
-    const float s = group_scale(top, g);
-    if (blockIdx.y == 0 && c0 + threadIdx.x < a.cols) a.scale[c0 + threadIdx.x] = s;
-  }
-  __syncthreads();
   const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;  // 8 columns, rows rg * 4 .. + 3
   const int64_t col = c0 + cg * 8;
-  uint32_t packed[8] = {};
   float x[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -246,6 +236,14 @@ __global__ __launch_bounds__(256) void quantize_columns(QuantArgs a) {
       for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
     }
   }
+  const int c = threadIdx.x % 64, quarter = threadIdx.x / 64;
+  uint32_t top = 0;
+  if (c0 + c < a.cols) {
+#pragma unroll 8
+    for (int p = quarter; p < a.chunks; p += 4)
+      top = max(top, a.part[static_cast<int64_t>(p) * a.cols + c0 + c]);
+  }
+  tops[quarter][c] = top;
   uint32_t bits[4][8] = {};
   if constexpr (SR) {
 #pragma unroll
@@ -253,24 +251,29 @@ __global__ __launch_bounds__(256) void quantize_columns(QuantArgs a) {
       random8(a.base_index + static_cast<uint64_t>(r0 + rg * 4 + i) * static_cast<uint64_t>(a.cols) +
                   static_cast<uint64_t>(col), a.seed, a.step, bits[i]);
   }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    GroupScale g;
+    const float s = group_scale(max(max(tops[0][c], tops[1][c]), max(tops[2][c], tops[3][c])), g);
+    scales[c] = g;
+    if (blockIdx.y == 0 && c0 + c < a.cols) a.scale[c0 + c] = s;
+  }
+  __syncthreads();
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    GroupScale g;
-    group_scale(tops[cg * 8 + e], g);
+    const GroupScale g = scales[cg * 8 + e];
     int32_t q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = quantize<SR>(x[i][e], g, bits[i][e]);
-    packed[e] = pack4(q);
+    tile[(cg * 8 + e) * kWords + rg] = pack4(q);
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) tile[(cg * 8 + e) * kWords + rg] = packed[e];
   __syncthreads();
   for (int t = threadIdx.x; t < 64 * 8; t += 256) {
-    const int c = t / 8, part = t % 8;
+    const int cc = t / 8, part = t % 8;
     const int64_t r = r0 + part * 16;
-    if (c0 + c < a.cols && r < a.rows) {
-      const uint32_t* w = tile + c * kWords + part * 4;
-      *reinterpret_cast<asr::u32x4*>(a.q + (c0 + c) * a.ldq + r) = asr::u32x4{w[0], w[1], w[2], w[3]};
+    if (c0 + cc < a.cols && r < a.rows) {
+      const uint32_t* w = tile + cc * kWords + part * 4;
+      *reinterpret_cast<asr::u32x4*>(a.q + (c0 + cc) * a.ldq + r) = asr::u32x4{w[0], w[1], w[2], w[3]};
     }
   }
 }
@@ -307,7 +310,7 @@ using Tiny = asr_mfma::Tile<64, 64, 32, 32, 4>;
 // REST: K is not a multiple of 16 (a variant of its own: its byte loads cost
 // the largest tile registers that it has not got).
 template <typename T, int ROUND, bool REST>
-__global__ __launch_bounds__(T::kThreads) void gemm_i8(GemmArgs args) {
+__global__ __launch_bounds__(T::kThreads, T::kMinWaves) void gemm_i8(GemmArgs args) {
   using E = asr_mfma::ElemI8;
   __shared__ __align__(1024) unsigned char smem[T::kLoopLds];
   uint32_t tm, tn;
@@ -436,6 +439,97 @@ __global__ __launch_bounds__(T::kThreads) void gemm_i8(GemmArgs args) {
   });
 }
 
+// A few rows of A (decoding): bound by reading B once. A workgroup takes 16
+// rows of B against MB blocks of 16 rows of A; its 8 waves split K in units of
+// 128 bytes, with every load straight into the operand registers of a 16x16x64
+// instruction (B on its row side, so a lane ends with 4 consecutive columns of
+// one row of C). The waves' integer sums meet in LDS: no order to care for.
+template <int MB, int ROUND>
+__global__ __launch_bounds__(512) void gemm_i8_few(GemmArgs args) {
+  using asr_mfma::i32x4;
+  constexpr int kWaves = 8;
+  __shared__ i32x4 sums[kWaves][MB][64];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  // rows past the end are clamped: they only feed outputs that are not stored
+  const int8_t* pb = args.b + min(n0 + (lane & 15u), static_cast<int64_t>(args.n - 1)) * args.ldb;
+  const int8_t* pa[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+    pa[i] = args.a + min(static_cast<int64_t>(16 * i + (lane & 15u)), static_cast<int64_t>(args.m - 1)) * args.lda;
+  const int32_t k_lane = static_cast<int32_t>(lane >> 4) * 32;
+  i32x4 acc[MB] = {};
+  const int32_t whole = args.k / 128;
+  auto step = [&](int32_t k) {
+    i32x4 b[2], a[MB][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      b[h] = *reinterpret_cast<const i32x4*>(pb + k + k_lane + 16 * h);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) a[i][h] = *reinterpret_cast<const i32x4*>(pa[i] + k + k_lane + 16 * h);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[h], a[i][h], acc[i], 0, 0, 0);
+  };
+  int32_t u = static_cast<int32_t>(wave);
+#pragma unroll 4
+  for (; u < whole; u += kWaves) step(u * 128);
+  if (args.k % 128 != 0 && u == whole) {
+    // the last codes: whole 16-byte chunks by one load, the rest byte by byte
+    auto tail = [&](const int8_t* row, int32_t k) {
+      if (k + 16 <= args.k) return *reinterpret_cast<const i32x4*>(row + k);
+      uint32_t w[4] = {};
+#pragma unroll
+      for (int e = 0; e < 15; ++e)
+        if (k + e < args.k) w[e / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + e])) << (8 * (e % 4));
+      return i32x4{static_cast<int32_t>(w[0]), static_cast<int32_t>(w[1]),
+                   static_cast<int32_t>(w[2]), static_cast<int32_t>(w[3])};
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int32_t k = whole * 128 + k_lane + 16 * h;
+      const i32x4 b = tail(pb, k);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, tail(pa[i], k), acc[i], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i) sums[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave >= MB) return;
+  i32x4 t = sums[0][wave][lane];
+#pragma unroll
+  for (int v = 1; v < kWaves; ++v) t += sums[v][wave][lane];
+  const int64_t m = 16 * wave + (lane & 15u), n = n0 + 4 * (lane >> 4);
+  if (m >= args.m || n >= args.n) return;
+  const float sa = args.sa[m];
+  uint32_t r16[4] = {}, h[4];
+  float x[4];
+  if constexpr (ROUND == ASR_ROUND_SR)
+    asr_mfma::random4(args.base_index + static_cast<uint64_t>(m) * static_cast<uint64_t>(args.n) +
+                          static_cast<uint64_t>(n), args.pos4 != 0, args.seed, args.step, r16);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float sb = args.sb[min(n + e, static_cast<int64_t>(args.n - 1))];
+    x[e] = (static_cast<float>(t[e]) * sa) * sb;
+    h[e] = round_one<ROUND>(x[e], r16[e]);
+  }
+  const int64_t at = m * args.ldc + n;
+  const int count = static_cast<int>(min(int64_t{4}, args.n - n));
+  if (args.vec4 && count == 4) {
+    asr::store_vec_bf16<false, 4>(args.c + at, h);
+    if (args.c32) asr::store_vec<false, 4>(args.c32 + at, x);
+  } else {
+    asr::store_range_bf16<4>(args.c, at, 0, count, h);
+    if (args.c32) asr::store_range<4>(args.c32, at, 0, count, x);
+  }
+}
+
 }  // namespace asr_i8
 
 // =========================================================== host side
@@ -451,11 +545,12 @@ bool aligned_to(const void* p, uintptr_t a) {
 
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 
-// Rows a workgroup of column_maxima takes: enough chunks to fill the chip,
-// no more than 64, so that the second pass's read of their maxima stays small.
-int64_t chunk_rows(int64_t rows) {
-  const int64_t chunks = std::clamp<int64_t>((rows + 63) / 64, 1, 64);
-  return (rows + chunks - 1) / chunks;
+// Rows a workgroup of column_maxima takes (a multiple of 64): enough chunks for
+// about 1024 workgroups, no more than 64 of them.
+int64_t chunk_rows(int64_t rows, int64_t cols) {
+  const int64_t strips = (cols + 127) / 128;
+  const int64_t chunks = std::clamp<int64_t>(1024 / strips, 1, 64);
+  return ((rows + chunks - 1) / chunks + 63) / 64 * 64;
 }
 
 template <typename F>
@@ -474,7 +569,7 @@ hipError_t launch_quantize(asr_i8::QuantArgs& a, bool transpose, hipStream_t s) 
     return launch(&quantize_rows<S, SR, 256>, dim3(static_cast<uint32_t>(a.rows)), 256, &a, s);
   }
   const hipError_t e =
-      launch(&column_maxima<S>, dim3(static_cast<uint32_t>((a.cols + 511) / 512),
+      launch(&column_maxima<S>, dim3(static_cast<uint32_t>((a.cols + 127) / 128),
                                      static_cast<uint32_t>(a.chunks)), 256, &a, s);
   if (e != hipSuccess) return e;
   return launch(&quantize_columns<S, SR>, dim3(static_cast<uint32_t>((a.cols + 63) / 64),
@@ -496,13 +591,21 @@ hipError_t launch_gemm(asr_i8::GemmArgs args, int32_t rounding, hipStream_t s) {
              : launch(&gemm_i8<T, ASR_ROUND_RN, false>, grid, T::kThreads, &args, s);
 }
 
+template <int MB>
+hipError_t launch_few(asr_i8::GemmArgs args, int32_t rounding, hipStream_t s) {
+  using namespace asr_i8;
+  const dim3 grid(static_cast<uint32_t>((args.n + 15) / 16));
+  return rounding == ASR_ROUND_SR ? launch(&gemm_i8_few<MB, ASR_ROUND_SR>, grid, 512, &args, s)
+                                  : launch(&gemm_i8_few<MB, ASR_ROUND_RN>, grid, 512, &args, s);
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t asr_quantize_i8_workspace_bytes(int64_t rows, int64_t cols, int32_t transpose) {
   if (!transpose || rows <= 0 || cols <= 0 || rows >= kMaxDim || cols >= kMaxDim) return 0;
-  const int64_t chunk = chunk_rows(rows), chunks = (rows + chunk - 1) / chunk;
+  const int64_t chunk = chunk_rows(rows, cols), chunks = (rows + chunk - 1) / chunk;
   return static_cast<size_t>((chunks * cols * 4 + 255) / 256 * 256);
 }
 
@@ -547,7 +650,7 @@ int asr_quantize_i8(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int
   a.seed = seed;
   a.step = step;
   a.vec = aligned_to(x, 16) && (rows == 1 || ldx * size % 16 == 0);
-  a.chunk = static_cast<int32_t>(length > 0 ? chunk_rows(rows > 0 ? rows : 1) : 1);
+  a.chunk = static_cast<int32_t>(length > 0 ? chunk_rows(rows > 0 ? rows : 1, cols) : 1);
   a.chunks = static_cast<int32_t>((rows + a.chunk - 1) / a.chunk);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool sr = rounding == ASR_ROUND_SR;
@@ -615,7 +718,13 @@ int asr_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb, cons
   if (tiles(64) > 0x7FFFFFFFull) return fail(ASR_EINVAL, "gemm_i8: too many tiles");
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e;
-  if (tiles(256) >= 256) e = launch_gemm<asr_i8::Big>(g, rounding, s);
+#ifndef ASR_I8_FEW
+#define ASR_I8_FEW 64
+#endif
+  if (m <= std::min(ASR_I8_FEW, 16)) e = launch_few<1>(g, rounding, s);
+  else if (m <= std::min(ASR_I8_FEW, 32)) e = launch_few<2>(g, rounding, s);
+  else if (m <= std::min(ASR_I8_FEW, 64)) e = launch_few<4>(g, rounding, s);
+  else if (tiles(256) >= 256) e = launch_gemm<asr_i8::Big>(g, rounding, s);
   else if (tiles(128) > 256) e = launch_gemm<asr_i8::Small>(g, rounding, s);
   else if (tiles(128) > 128) e = launch_gemm<asr_i8::Small8>(g, rounding, s);
   else e = launch_gemm<asr_i8::Tiny>(g, rounding, s);

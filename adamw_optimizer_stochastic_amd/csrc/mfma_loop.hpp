@@ -67,6 +67,10 @@ struct Tile {
   static constexpr int kWavesN = BN / WN;
   static constexpr int kWaves = (BM / WM) * kWavesN;
   static constexpr int kThreads = kWaves * 64;
+  // Waves a SIMD that the LDS leaves room for (two, or one for a 4-wave
+  // workgroup that has a compute unit to itself).
+  static constexpr int kMinWaves =
+      kWaves <= 4 && STAGES_ * (BM_ + BN_) * kRowBytes > 80 * 1024 ? 1 : 2;
   static constexpr int kFragM = WM / 32, kFragN = WN / 32;
   static constexpr int kSlabs = (BM + BN) / 8;                // wave-wide copies a K tile
   static constexpr int kCopyWaves = kWaves > 4 ? 4 : kWaves;  // one a SIMD

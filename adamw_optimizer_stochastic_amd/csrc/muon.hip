@@ -7,9 +7,12 @@
 //
 // Every product is C = P * Q^T with K contiguous in both operands: A = X X^T
 // and A A = A A^T (A is symmetric) as they stand, and B X as B * Y^T with Y =
-// X^T kept beside X. The last product's epilogue writes its result both ways,
-// the turned copy through the LDS the K loop has left; A and B need one half
-// of their tiles, mirrored by the same means.
+// X^T kept beside X. That product's epilogue writes its result both ways, the
+// turned copy through the LDS the K loop has left; A and B need one half of
+// their tiles, mirrored by the same means. One launch does one product for all
+// matrices of a list, whatever their shapes: what is left over of the chip's
+// last round of tiles is paid once a list, not once a matrix. A matrix
+// small enough for one workgroup's LDS goes through all steps in one launch.
 //
 // Precision: the matrix instructions take 16-bit operands. In bf16 the
 // result is 1e-2 (Gaussian) to 2e-1 (low rank) from the 64-bit one. Here the
@@ -26,46 +29,102 @@
 
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 #include <string>
 
 #pragma clang fp contract(off)
 
 namespace asr_muon {
 
+using asr_mfma::f16x8;
 using asr_mfma::static_for;
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kMaxBatch = 16;   // matrices of one launch
-constexpr int kMaxParts = 1024; // partial sums of one matrix's squared norm
+constexpr int kMaxBatch = 32;    // matrices of one launch
+constexpr int kMaxParts = 1024;  // partial sums of one matrix's squared norm
 
-struct Matrices {
-  const void* g[kMaxBatch];
-  float* m[kMaxBatch];      // momentum (NULL without)
-  void* p[kMaxBatch];       // weights, or the result
-  uint64_t base[kMaxBatch];
+// One matrix of a launch.
+struct Desc {
+  const void* g;
+  float* m;        // momentum (NULL without)
+  void* p;         // weights, or the result
+  uint64_t base;   // stream position of the weights' element 0
+  int64_t ws;      // its part of the workspace
+  int32_t rows, cols;
+  float eta;       // p <- p * decay - eta * O
+  uint32_t first;  // its first workgroup in this launch
 };
 
+__host__ __device__ constexpr int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// A matrix's part of the workspace: X and Y = X^T (f16, rows padded to 128
+// bytes; Y twice, since the product that makes the next X reads all of the
+// last Y), the low parts, A, B and the norm's partial sums. X, A and B are
+// held times sx and sa, powers of two that keep their entries near 1 and
+// |X| <= 1.4, |A|, |B| <= 3.75 inside f16.
+struct Layout {
+  bool wide;  // the matrix itself has its short side first
+  int32_t s, t, ld_s, ld_t;
+  int64_t x, y, y_stride, lo, a, b, parts, bytes;
+  float sx, sa;
+  __host__ __device__ Layout(int32_t rows, int32_t cols) {
+    wide = rows <= cols;
+    s = wide ? rows : cols;
+    t = wide ? cols : rows;
+    ld_s = static_cast<int32_t>(up(s, 64));
+    ld_t = static_cast<int32_t>(up(t, 64));
+    const int64_t across = up(static_cast<int64_t>(s) * ld_t * 2, 1024);
+    const int64_t down = up(static_cast<int64_t>(t) * ld_s * 2, 1024);
+    const int64_t square = up(static_cast<int64_t>(s) * ld_s * 2, 1024);
+    x = 0;
+    y = across;
+    y_stride = down;
+    lo = y + 2 * down;
+    a = lo + (wide ? across : down);
+    b = a + square;
+    parts = b + square;
+    bytes = parts + kMaxParts * 8;
+    int32_t half = 0, whole = 0;  // floor(log2(s t) / 2), floor(log2 s)
+    while (int64_t{4} << (2 * half) <= static_cast<int64_t>(s) * t) ++half;
+    while (2 << whole <= s) ++whole;
+    sx = static_cast<float>(1 << (half < 14 ? half : 14));
+    sa = static_cast<float>(1 << (whole < 14 ? whole : 14));
+  }
+};
+
+// Workgroups of sum_squares for a matrix, and the elements each takes.
+__host__ __device__ inline int64_t part_size(int64_t numel) {
+  int64_t parts = (numel + 8191) / 8192;
+  if (parts > kMaxParts) parts = kMaxParts;
+  return up((numel + parts - 1) / parts, 2048);
+}
+
 struct PrepareArgs {
-  Matrices mat;
-  int64_t rows, cols, numel, chunk;
+  Desc d[kMaxBatch];
   char* ws;
-  int64_t stride;                  // workspace bytes a matrix
-  int64_t parts, direct, turned, lo;  // offsets in it
-  int64_t ld_direct, ld_turned;    // elements
-  double eps, scale;
+  double eps;
   float momentum;
-  int32_t nesterov, parts_n;
+  int32_t nesterov, count;
   uint32_t vec;
 };
 
-// U of 8 consecutive elements: the gradient, or the momentum step's update.
-template <typename G, bool MUON>
-__device__ __forceinline__ void momentum_update(const float (&g)[8], float (&m)[8], float mu,
-                                                bool nesterov, bool fresh, float (&u)[8]) {
+// The matrix that workgroup b belongs to.
+__device__ __forceinline__ int matrix_of(const Desc* d, int count, uint32_t b) {
+  const int lane = threadIdx.x & 63;
+  const bool reached = lane < count && d[lane < count ? lane : 0].first <= b;
+  return __builtin_amdgcn_readfirstlane(__popcll(__ballot(reached)) - 1);
+}
+
+// U of V consecutive elements: the gradient, or the momentum step's update;
+// `fresh` does the momentum's own step, otherwise m has it already.
+template <bool MUON, int V>
+__device__ __forceinline__ void momentum_update(const float (&g)[V], float (&m)[V], float mu,
+                                                bool nesterov, bool fresh, float (&u)[V]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < V; ++e) {
     if constexpr (MUON) {
       if (fresh) m[e] = mu * m[e] + g[e];
       u[e] = nesterov ? g[e] + mu * m[e] : m[e];
@@ -75,15 +134,31 @@ __device__ __forceinline__ void momentum_update(const float (&g)[8], float (&m)[
   }
 }
 
+// Sum of a workgroup's values in a fixed order; every thread gets it.
+template <int THREADS>
+__device__ __forceinline__ double group_sum(double x, double* lds) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+  if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
+  __syncthreads();
+  double sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) sum += lds[w];
+  return sum;
+}
+
 // Sum of squares of one chunk of U, in 64 bits; the momentum is updated on
 // the way. Memory bound: 2 (bf16 gradient) + 8 bytes an element.
 template <typename G, bool MUON>
 __global__ __launch_bounds__(256) void sum_squares(PrepareArgs a) {
-  const int k = blockIdx.y;
-  const G* g = static_cast<const G*>(a.mat.g[k]);
-  float* m = a.mat.m[k];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
-  const int64_t i1 = min(a.numel, i0 + a.chunk);
+  __shared__ double lds[4];
+  const int k = matrix_of(a.d, a.count, blockIdx.x);
+  const Desc& d = a.d[k];
+  const G* g = static_cast<const G*>(d.g);
+  float* m = d.m;
+  const int64_t numel = static_cast<int64_t>(d.rows) * d.cols, chunk = part_size(numel);
+  const uint32_t part = blockIdx.x - d.first;
+  const int64_t i0 = part * chunk, i1 = min(numel, i0 + chunk);
   double sum = 0.0;
   for (int64_t i = i0 + threadIdx.x * 8; i < i1; i += 256 * 8) {
     const int n = static_cast<int>(min(int64_t{8}, i1 - i));
@@ -96,7 +171,7 @@ __global__ __launch_bounds__(256) void sum_squares(PrepareArgs a) {
       asr::load_range<8>(g, i, 0, n, gx);
       if constexpr (MUON) asr::load_range<8>(m, i, 0, n, mx);
     }
-    momentum_update<G, MUON>(gx, mx, a.momentum, a.nesterov, true, u);
+    momentum_update<MUON>(gx, mx, a.momentum, a.nesterov, true, u);
     if constexpr (MUON) {
       if (whole) asr::store_vec<false, 8>(m + i, mx);
       else asr::store_range<8>(m, i, 0, n, mx);
@@ -105,14 +180,9 @@ __global__ __launch_bounds__(256) void sum_squares(PrepareArgs a) {
     for (int e = 0; e < 8; ++e)
       if (e < n) sum += static_cast<double>(u[e]) * static_cast<double>(u[e]);
   }
-  __shared__ double sums[4];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-  if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = sum;
-  __syncthreads();
+  sum = group_sum<256>(sum, lds);
   if (threadIdx.x == 0)
-    reinterpret_cast<double*>(a.ws + k * a.stride + a.parts)[blockIdx.x] =
-        (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    reinterpret_cast<double*>(a.ws + d.ws + Layout(d.rows, d.cols).parts)[part] = sum;
 }
 
 // X0 as hi + lo, and hi turned, for one 64 x 64 tile, with zeros up to the
@@ -121,35 +191,37 @@ template <typename G, bool MUON>
 __global__ __launch_bounds__(256) void scale_matrix(PrepareArgs a) {
   constexpr int kLd = 72;  // f16 a row of the turned tile
   __shared__ __align__(16) _Float16 tile[64 * kLd];
-  __shared__ double sums[4];
-  const int k = blockIdx.z;
-  char* ws = a.ws + k * a.stride;
-  const double* parts = reinterpret_cast<const double*>(ws + a.parts);
+  __shared__ double lds[4];
+  const int k = matrix_of(a.d, a.count, blockIdx.x);
+  const Desc& d = a.d[k];
+  const int32_t rows = d.rows, cols = d.cols;
+  const Layout l(rows, cols);
+  char* ws = a.ws + d.ws;
+  const int64_t numel = static_cast<int64_t>(rows) * cols, chunk = part_size(numel);
+  const double* parts = reinterpret_cast<const double*>(ws + l.parts);
   double sum = 0.0;
-  for (int i = threadIdx.x; i < a.parts_n; i += 256) sum += parts[i];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-  if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = sum;
-  __syncthreads();
-  const double norm = __builtin_sqrt((sums[0] + sums[1]) + (sums[2] + sums[3]));
-  const double factor = a.scale / (norm + a.eps);
+  for (int64_t i = threadIdx.x; i * chunk < numel; i += 256) sum += parts[i];
+  const double norm = __builtin_sqrt(group_sum<256>(sum, lds));
+  const double factor = static_cast<double>(l.sx) / (norm + a.eps);
 
-  const G* g = static_cast<const G*>(a.mat.g[k]);
-  const float* m = a.mat.m[k];
-  _Float16* hi_out = reinterpret_cast<_Float16*>(ws + a.direct);
-  _Float16* lo_out = reinterpret_cast<_Float16*>(ws + a.lo);
-  _Float16* turned = reinterpret_cast<_Float16*>(ws + a.turned);
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
+  const G* g = static_cast<const G*>(d.g);
+  const float* m = d.m;
+  const int64_t ld_direct = l.wide ? l.ld_t : l.ld_s, ld_turned = l.wide ? l.ld_s : l.ld_t;
+  _Float16* hi_out = reinterpret_cast<_Float16*>(ws + (l.wide ? l.x : l.y));
+  _Float16* lo_out = reinterpret_cast<_Float16*>(ws + l.lo);
+  _Float16* turned = reinterpret_cast<_Float16*>(ws + (l.wide ? l.y : l.x));
+  const uint32_t t = blockIdx.x - d.first, across = static_cast<uint32_t>((cols + 63) / 64);
+  const int64_t r0 = static_cast<int64_t>(t / across) * 64, c0 = static_cast<int64_t>(t % across) * 64;
   const int cg = threadIdx.x & 7;
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     const int rr = (threadIdx.x >> 3) + 32 * pass;
     const int64_t r = r0 + rr, c = c0 + cg * 8;
     float gx[8] = {}, mx[8] = {}, u[8];
-    if (r < a.rows) {
-      const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.cols - c)));
-      const int64_t i = r * a.cols + c;
-      if (a.vec && n == 8 && a.cols % 8 == 0) {
+    if (r < rows) {
+      const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, cols - c)));
+      const int64_t i = r * cols + c;
+      if (a.vec && n == 8 && cols % 8 == 0) {
         asr::load_vec<false, 8>(g + i, gx);
         if constexpr (MUON) asr::load_vec<false, 8>(m + i, mx);
       } else {
@@ -157,20 +229,20 @@ __global__ __launch_bounds__(256) void scale_matrix(PrepareArgs a) {
         if constexpr (MUON) asr::load_range<8>(m, i, 0, n, mx);
       }
     }
-    momentum_update<G, MUON>(gx, mx, a.momentum, a.nesterov, false, u);
-    asr_mfma::f16x8 hi, lo;
+    momentum_update<MUON>(gx, mx, a.momentum, a.nesterov, false, u);
+    f16x8 hi, lo;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float x = static_cast<float>(static_cast<double>(u[e]) * factor);
       // (elements past the matrix stay zero whatever the factor is)
-      const float y = r < a.rows && c + e < a.cols ? x : 0.0f;
+      const float y = r < rows && c + e < cols ? x : 0.0f;
       hi[e] = static_cast<_Float16>(y);
       lo[e] = static_cast<_Float16>(y - static_cast<float>(hi[e]));
       tile[(cg * 8 + e) * kLd + rr] = hi[e];
     }
-    if (r < a.rows) {
-      *reinterpret_cast<asr_mfma::f16x8*>(hi_out + r * a.ld_direct + c) = hi;
-      *reinterpret_cast<asr_mfma::f16x8*>(lo_out + r * a.ld_direct + c) = lo;
+    if (r < rows) {
+      *reinterpret_cast<f16x8*>(hi_out + r * ld_direct + c) = hi;
+      *reinterpret_cast<f16x8*>(lo_out + r * ld_direct + c) = lo;
     }
   }
   __syncthreads();
@@ -178,38 +250,36 @@ __global__ __launch_bounds__(256) void scale_matrix(PrepareArgs a) {
   for (int pass = 0; pass < 2; ++pass) {
     const int cc = (threadIdx.x >> 3) + 32 * pass;
     const int64_t c = c0 + cc, r = r0 + cg * 8;
-    if (c < a.cols)
-      *reinterpret_cast<asr_mfma::f16x8*>(turned + c * a.ld_turned + r) =
-          *reinterpret_cast<const asr_mfma::f16x8*>(tile + cc * kLd + cg * 8);
+    if (c < cols)
+      *reinterpret_cast<f16x8*>(turned + c * ld_turned + r) =
+          *reinterpret_cast<const f16x8*>(tile + cc * kLd + cg * 8);
   }
 }
 
 // ---------------------------------------------------------------- products
 enum Mode {
-  kGram,    // D = alpha * acc, symmetric
-  kSquare,  // D = beta * C + alpha * acc, symmetric
-  kUpdate,  // v = beta * (C + lo) + alpha * acc; D, lo = v in two parts; D turned
-  kFinal    // o = (beta * (C + lo) + alpha * acc) * out_scale: the result, or the weights' step
+  kGram,    // A = X X^T
+  kSquare,  // B = b A + c A A
+  kUpdate,  // X <- a X + B X, in two parts, and the high one turned
+  kFinal    // the same, into the result or the weights
+};
+
+// What becomes of O: the result in bf16, or p <- round(p * decay - eta * O).
+enum Out { kOutBf16, kOutWeightBf16Sr, kOutWeightBf16Rn, kOutWeightF32 };
+
+struct OutArgs {
+  float decay;
+  uint32_t seed, step;
+  uint32_t vec8;  // runs of 8 of every matrix's rows start on 16-byte addresses
 };
 
 struct ProductArgs {
-  Matrices mat;            // kFinal
+  Desc d[kMaxBatch];
   char* ws;
-  int64_t stride;
-  int64_t a, b, c, lo, d, turned;  // offsets of a matrix's buffers
-  uint32_t ld_a, ld_b;             // bytes
-  int64_t ld_d, ld_turned;         // elements (C and lo have D's)
-  int32_t m, n, kbytes;
-  uint32_t tiles_m, tiles_n, tiles, batch;
-  float alpha, beta;
-  // kFinal
-  float out_scale, decay, eta;
-  int64_t ld_out;
-  uint32_t seed, step, vec4, pos4;
+  float a, b, c;
+  int32_t count, y;  // which Y holds the current X^T
+  OutArgs out;
 };
-
-// What kFinal does with o: the result in bf16, or p <- round(p * decay - eta * o).
-enum Out { kOutBf16, kOutWeightBf16Sr, kOutWeightBf16Rn, kOutWeightF32 };
 
 // Tile t of the lower triangle, rows in order.
 __device__ __forceinline__ void triangle_tile(uint32_t t, uint32_t& tm, uint32_t& tn) {
@@ -220,184 +290,406 @@ __device__ __forceinline__ void triangle_tile(uint32_t t, uint32_t& tm, uint32_t
   tn = t - r * (r + 1) / 2;
 }
 
+__host__ __device__ inline int64_t tiles_of(int mode, int32_t rows, int32_t cols, int tile) {
+  const int64_t tm = (rows + tile - 1) / tile, tn = (cols + tile - 1) / tile;
+  if (mode != kGram && mode != kSquare) return tm * tn;
+  const int64_t ts = tm < tn ? tm : tn;
+  return ts * (ts + 1) / 2;
+}
+
 template <typename T>
 constexpr int lds_bytes() {
   const int turned = T::BN * (T::BM + 8) * 2;
   return turned > T::kLoopLds ? turned : T::kLoopLds;
 }
 
-template <int OUT>
-__device__ __forceinline__ void store_out(const ProductArgs& args, int k, int64_t m, int64_t n,
-                                          const float (&v)[4]) {
-  // runs of 4 that are whole and aligned move as vectors
-  const bool full = args.vec4 && n + 4 <= args.n;
-  const int count = static_cast<int>(min(int64_t{4}, static_cast<int64_t>(args.n) - n));
-  const int64_t at = m * args.ld_out + n;
+// V consecutive elements (V = 4 or 8) of O from element `at` of a matrix, `n`
+// of them inside it; vec: they are whole and aligned.
+template <int OUT, int V>
+__device__ __forceinline__ void store_out(const OutArgs& out, const Desc& d, int64_t at, int n,
+                                          bool vec, const float (&o)[V]) {
+  if constexpr (OUT == kOutWeightF32) {
+    float* p = static_cast<float*>(d.p);
+    float x[V];
+    if (vec) asr::load_vec<false, V>(p + at, x);
+    else asr::load_range<V>(p, at, 0, n, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = x[e] * out.decay - d.eta * o[e];
+    if (vec) asr::store_vec<false, V>(p + at, x);
+    else asr::store_range<V>(p, at, 0, n, x);
+    return;
+  }
+  uint16_t* p = static_cast<uint16_t*>(d.p);
+  uint32_t h[V];
   if constexpr (OUT == kOutBf16) {
-    uint16_t* d = static_cast<uint16_t*>(args.mat.p[k]);
-    uint32_t h[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = asr::round_rn(__float_as_uint(v[e] * args.out_scale));
-    if (full) asr::store_vec_bf16<false, 4>(d + at, h);
-    else asr::store_range_bf16<4>(d, at, 0, count, h);
-  } else if constexpr (OUT == kOutWeightF32) {
-    float* p = static_cast<float*>(args.mat.p[k]);
-    float x[4];
-    if (full) asr::load_vec<false, 4>(p + at, x);
-    else asr::load_range<4>(p, at, 0, count, x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = x[e] * args.decay - args.eta * (v[e] * args.out_scale);
-    if (full) asr::store_vec<false, 4>(p + at, x);
-    else asr::store_range<4>(p, at, 0, count, x);
+    for (int e = 0; e < V; ++e) h[e] = asr::round_rn(__float_as_uint(o[e]));
   } else {
-    uint16_t* p = static_cast<uint16_t*>(args.mat.p[k]);
-    float x[4];
-    if (full) asr::load_vec<false, 4>(p + at, x);
-    else asr::load_range<4>(p, at, 0, count, x);
-    uint32_t r16[4] = {}, h[4];
-    if constexpr (OUT == kOutWeightBf16Sr)
-      asr_mfma::random4(args.mat.base[k] + static_cast<uint64_t>(at),
-                        args.pos4 && (args.mat.base[k] & 3u) == 0, args.seed, args.step, r16);
+    float x[V];
+    if (vec) asr::load_vec<false, V>(p + at, x);
+    else asr::load_range<V>(p, at, 0, n, x);
+    const uint64_t pos = d.base + static_cast<uint64_t>(at);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float y = x[e] * args.decay - args.eta * (v[e] * args.out_scale);
-      h[e] = OUT == kOutWeightBf16Sr ? asr::round_sr(__float_as_uint(y), r16[e])
-                                     : asr::round_rn(__float_as_uint(y));
+    for (int q = 0; q < V / 4; ++q) {
+      uint32_t r16[4] = {};
+      if constexpr (OUT == kOutWeightBf16Sr)
+        asr_mfma::random4(pos + 4 * q, (pos & 3u) == 0, out.seed, out.step, r16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y = x[4 * q + e] * out.decay - d.eta * o[4 * q + e];
+        h[4 * q + e] = OUT == kOutWeightBf16Sr ? asr::round_sr(__float_as_uint(y), r16[e])
+                                               : asr::round_rn(__float_as_uint(y));
+      }
     }
-    if (full) asr::store_vec_bf16<false, 4>(p + at, h);
-    else asr::store_range_bf16<4>(p, at, 0, count, h);
+  }
+  if (vec) asr::store_vec_bf16<false, V>(p + at, h);
+  else asr::store_range_bf16<V>(p, at, 0, n, h);
+}
+
+// One element of O.
+template <int OUT>
+__device__ __forceinline__ void store_out1(const OutArgs& out, const Desc& d, int64_t at, float o) {
+  if constexpr (OUT == kOutBf16) {
+    static_cast<uint16_t*>(d.p)[at] = static_cast<uint16_t>(asr::round_rn(__float_as_uint(o)));
+  } else if constexpr (OUT == kOutWeightF32) {
+    float* p = static_cast<float*>(d.p) + at;
+    *p = *p * out.decay - d.eta * o;
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(d.p) + at;
+    const uint32_t y = __float_as_uint(asr::bf16_bits_to_f32(*p) * out.decay - d.eta * o);
+    uint32_t r16[4] = {};
+    const uint64_t pos = d.base + static_cast<uint64_t>(at);
+    if constexpr (OUT == kOutWeightBf16Sr) asr_mfma::random4(pos & ~uint64_t{3}, true, out.seed, out.step, r16);
+    const uint32_t e = static_cast<uint32_t>(pos) & 3u;
+    const uint32_t r = e == 0 ? r16[0] : e == 1 ? r16[1] : e == 2 ? r16[2] : r16[3];
+    *p = static_cast<uint16_t>(OUT == kOutWeightBf16Sr ? asr::round_sr(y, r) : asr::round_rn(y));
   }
 }
 
 template <typename T, int MODE, int OUT>
-__global__ __launch_bounds__(T::kThreads) void product(ProductArgs args) {
+__global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs args) {
   using E = asr_mfma::ElemF16;
   constexpr bool kSymmetric = MODE == kGram || MODE == kSquare;
   __shared__ __align__(1024) unsigned char smem[lds_bytes<T>()];
-  const uint32_t t = asr_mfma::xcd_order(blockIdx.x, args.tiles * args.batch);
-  const uint32_t k = t / args.tiles;
-  uint32_t tm, tn;
-  if constexpr (kSymmetric) triangle_tile(t % args.tiles, tm, tn);
-  else asr_mfma::grouped_tile(t % args.tiles, args.tiles_m, args.tiles_n, tm, tn);
-  const int64_t m0 = static_cast<int64_t>(tm) * T::BM, n0 = static_cast<int64_t>(tn) * T::BN;
-  char* ws = args.ws + static_cast<int64_t>(k) * args.stride;
-  E::acc acc[T::kFragM][T::kFragN] = {};
-  asr_mfma::Operands op;
-  op.a = ws + args.a + m0 * args.ld_a;
-  op.b = ws + args.b + n0 * args.ld_b;
-  op.ld_a = args.ld_a;
-  op.ld_b = args.ld_b;
-  op.last_a = args.m - 1 - static_cast<int32_t>(m0);
-  op.last_b = args.n - 1 - static_cast<int32_t>(n0);
-  op.kbytes = args.kbytes;
-  asr_mfma::mfma_loop<T, E>(op, smem, acc);
+  const int k = matrix_of(args.d, args.count, blockIdx.x);
+  const Desc& d = args.d[k];
+  const Layout l(d.rows, d.cols);
+  char* ws = args.ws + d.ws;
+  // operands, output size and strides of this product
+  const int32_t m_all = kSymmetric ? l.s : d.rows, n_all = kSymmetric ? l.s : d.cols;
+  const int64_t y_now = l.y + args.y * l.y_stride, y_next = l.y + (args.y ^ 1) * l.y_stride;
+  const int64_t direct = l.wide ? l.x : y_now;
+  const int64_t ld_d = kSymmetric ? l.ld_s : l.wide ? l.ld_t : l.ld_s;
+  const int64_t ld_turned = kSymmetric ? l.ld_s : l.wide ? l.ld_s : l.ld_t;
 
+  const uint32_t tiles = static_cast<uint32_t>(tiles_of(MODE, d.rows, d.cols, T::BM));
+  const uint32_t t = asr_mfma::xcd_order(blockIdx.x - d.first, tiles);
+  uint32_t tm, tn;
+  if constexpr (kSymmetric)
+    triangle_tile(t, tm, tn);
+  else
+    asr_mfma::grouped_tile(t, static_cast<uint32_t>((m_all + T::BM - 1) / T::BM),
+                           static_cast<uint32_t>((n_all + T::BN - 1) / T::BN), tm, tn);
+  const int64_t m0 = static_cast<int64_t>(tm) * T::BM, n0 = static_cast<int64_t>(tn) * T::BN;
+  E::acc acc[T::kFragM][T::kFragN] = {};
+  {
+    asr_mfma::Operands op;
+    op.ld_a = op.ld_b = static_cast<uint32_t>((MODE == kGram ? l.ld_t : l.ld_s) * 2);
+    op.kbytes = static_cast<int32_t>(op.ld_a);
+    op.a = ws + (MODE == kGram ? l.x : MODE == kSquare ? l.a : l.wide ? l.b : y_now) + m0 * op.ld_a;
+    op.b = ws + (MODE == kGram ? l.x : MODE == kSquare ? l.a : l.wide ? y_now : l.b) + n0 * op.ld_b;
+    op.last_a = m_all - 1 - static_cast<int32_t>(m0);
+    op.last_b = n_all - 1 - static_cast<int32_t>(n0);
+    asr_mfma::mfma_loop<T, E>(op, smem, acc);
+  }
+
+  // A lane holds runs of 4 columns of a row; v_permlane32_swap pairs lanes l
+  // and l + 32 into runs of 8: columns 16 p + 8 half .. + 7 of a 32 x 32
+  // block, so every access below is 16 bytes.
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t wm = wave / T::kWavesN, wn = wave % T::kWavesN;
   const uint32_t row = lane & 31u, half = lane >> 5;
-  const _Float16* c_in = reinterpret_cast<const _Float16*>(ws + args.c);
-  _Float16* lo_io = reinterpret_cast<_Float16*>(ws + args.lo);
-  _Float16* d_out = reinterpret_cast<_Float16*>(ws + args.d);
-
-  if constexpr (MODE == kFinal) {
-    static_for<T::kFragM>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      const int64_t m = m0 + wm * T::WM + i * 32 + row;
-      if (m >= args.m) return;
-      static_for<T::kFragN>([&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        static_for<4>([&](auto qc) {
-          constexpr int q = decltype(qc)::value;
-          const int64_t n = n0 + wn * T::WN + j * 32 + 8 * q + 4 * half;
-          if (n >= args.n) return;
-          const f16x4 hi = *reinterpret_cast<const f16x4*>(c_in + m * args.ld_d + n);
-          const f16x4 lo = *reinterpret_cast<const f16x4*>(lo_io + m * args.ld_d + n);
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = args.beta * (static_cast<float>(hi[e]) + static_cast<float>(lo[e])) +
-                   args.alpha * acc[i][j][4 * q + e];
-          store_out<OUT>(args, k, m, n, v);
-        });
-      });
-    });
-    return;
-  }
+  const _Float16* c_in = reinterpret_cast<const _Float16*>(ws + (MODE == kSquare ? l.a : direct));
+  _Float16* lo_io = reinterpret_cast<_Float16*>(ws + l.lo);
+  _Float16* d_out = reinterpret_cast<_Float16*>(
+      ws + (MODE == kGram ? l.a : MODE == kSquare ? l.b : l.wide ? l.x : y_next));
+  const float inv_sa = 1.0f / l.sa;
+  const float alpha = MODE == kGram ? l.sa / (l.sx * l.sx) : MODE == kSquare ? args.c * inv_sa : inv_sa;
+  const float beta = MODE == kSquare ? args.b : args.a;
+  const float inv_sx = 1.0f / l.sx;
 
   // The turned copy goes through LDS: element (m, n) of the tile at n * kLd + m.
   constexpr int kLd = T::BM + 8;
   _Float16* tile = reinterpret_cast<_Float16*>(smem);
-  const bool turn = !kSymmetric || tm != tn;
-  __syncthreads();  // every wave has read the last K tile
+  const bool turn = MODE == kUpdate || (kSymmetric && tm != tn);
+  if constexpr (MODE != kFinal) __syncthreads();  // every wave has read the last K tile
   static_for<T::kFragM>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
     const uint32_t mt = wm * T::WM + i * 32 + row;
     const int64_t m = m0 + mt;
-    const bool live = m < args.m;
+    const bool live = m < m_all;
     static_for<T::kFragN>([&](auto jc) {
       constexpr int j = decltype(jc)::value;
       static_for<2>([&](auto pc) {
         constexpr int p = decltype(pc)::value;
-        uint32_t w[2][2], wl[2][2];
+        const uint32_t nt = wn * T::WN + j * 32 + 16 * p + 8 * half;
+        const int64_t n = n0 + nt;
+        float v[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t nt = wn * T::WN + j * 32 + 16 * p + 8 * h + 4 * half;
-          const int64_t n = n0 + nt;
-          f16x4 hi = {}, lo = {};
-          if constexpr (MODE != kGram) {
-            if (live && n < args.ld_d) {
-              hi = *reinterpret_cast<const f16x4*>(c_in + m * args.ld_d + n);
-              if constexpr (MODE == kUpdate)
-                lo = *reinterpret_cast<const f16x4*>(lo_io + m * args.ld_d + n);
-            }
-          }
-          f16x4 vh, vl;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = args.alpha * acc[i][j][8 * p + 4 * h + e];
-            if constexpr (MODE == kSquare) v = args.beta * static_cast<float>(hi[e]) + v;
-            if constexpr (MODE == kUpdate)
-              v = args.beta * (static_cast<float>(hi[e]) + static_cast<float>(lo[e])) + v;
-            if (!live || n + e >= args.n) v = 0.0f;  // the padding reads as zeros
-            vh[e] = static_cast<_Float16>(v);
-            vl[e] = static_cast<_Float16>(v - static_cast<float>(vh[e]));
-            if (turn) tile[(nt + e) * kLd + mt] = vh[e];
-          }
-          w[h][0] = __builtin_bit_cast(uint32_t, f16x2{vh[0], vh[1]});
-          w[h][1] = __builtin_bit_cast(uint32_t, f16x2{vh[2], vh[3]});
-          wl[h][0] = __builtin_bit_cast(uint32_t, f16x2{vl[0], vl[1]});
-          wl[h][1] = __builtin_bit_cast(uint32_t, f16x2{vl[2], vl[3]});
+        for (int e = 0; e < 4; ++e) {
+          const auto r = __builtin_amdgcn_permlane32_swap(
+              __float_as_uint(acc[i][j][8 * p + e]), __float_as_uint(acc[i][j][8 * p + 4 + e]),
+              false, false);
+          v[e] = alpha * __uint_as_float(r[0]);
+          v[4 + e] = alpha * __uint_as_float(r[1]);
         }
-        // lanes l and l + 32 pair their runs of 4 into one 16-byte store each
-        const int64_t n16 = n0 + wn * T::WN + j * 32 + 16 * p;
-        auto put = [&](_Float16* d, const uint32_t (&x)[2][2]) {
-          const auto s0 = __builtin_amdgcn_permlane32_swap(x[0][0], x[1][0], false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(x[0][1], x[1][1], false, false);
-          if (live && n16 < args.ld_d)
-            *reinterpret_cast<asr::u32x4*>(d + m * args.ld_d + n16 + 8 * half) =
-                asr::u32x4{s0[0], s1[0], s0[1], s1[1]};
-        };
-        put(d_out, w);
-        if constexpr (MODE == kUpdate) put(lo_io, wl);
+        const bool inside = live && n < ld_d;  // (ld_d is a multiple of 64)
+        if constexpr (MODE != kGram) {
+          f16x8 hi = {}, lo = {};
+          if (inside) {
+            hi = *reinterpret_cast<const f16x8*>(c_in + m * ld_d + n);
+            if constexpr (MODE != kSquare) lo = *reinterpret_cast<const f16x8*>(lo_io + m * ld_d + n);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = MODE == kSquare ? static_cast<float>(hi[e])
+                                            : static_cast<float>(hi[e]) + static_cast<float>(lo[e]);
+            v[e] = beta * x + v[e];
+          }
+        }
+        if constexpr (MODE == kFinal) {
+          if (live && n < n_all) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= inv_sx;
+            const int count = static_cast<int>(min(int64_t{8}, n_all - n));
+            store_out<OUT, 8>(args.out, d, m * n_all + n, count, args.out.vec8 && count == 8, v);
+          }
+        } else {
+          f16x8 hi, lo;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = live && n + e < n_all ? v[e] : 0.0f;  // the padding reads as zeros
+            hi[e] = static_cast<_Float16>(x);
+            lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
+            if (turn) tile[(nt + e) * kLd + mt] = hi[e];
+          }
+          if (inside) {
+            *reinterpret_cast<f16x8*>(d_out + m * ld_d + n) = hi;
+            if constexpr (MODE == kUpdate) *reinterpret_cast<f16x8*>(lo_io + m * ld_d + n) = lo;
+          }
+        }
       });
     });
   });
-  if (!turn) return;
-  __syncthreads();
-  _Float16* t_out = reinterpret_cast<_Float16*>(ws + args.turned);
-  for (int q = threadIdx.x; q < T::BN * (T::BM / 8); q += T::kThreads) {
-    const int nt = q / (T::BM / 8), c8 = q % (T::BM / 8) * 8;
-    if (n0 + nt < args.n && m0 + c8 < args.ld_turned)
-      *reinterpret_cast<asr_mfma::f16x8*>(t_out + (n0 + nt) * args.ld_turned + m0 + c8) =
-          *reinterpret_cast<const asr_mfma::f16x8*>(tile + nt * kLd + c8);
+  if constexpr (MODE != kFinal) {
+    if (!turn) return;
+    __syncthreads();
+    _Float16* t_out = reinterpret_cast<_Float16*>(
+        ws + (MODE == kGram ? l.a : MODE == kSquare ? l.b : l.wide ? y_next : l.x));
+    for (int q = threadIdx.x; q < T::BN * (T::BM / 8); q += T::kThreads) {
+      const int nt = q / (T::BM / 8), c8 = q % (T::BM / 8) * 8;
+      if (n0 + nt < n_all && m0 + c8 < ld_turned)
+        *reinterpret_cast<f16x8*>(t_out + (n0 + nt) * ld_turned + m0 + c8) =
+            *reinterpret_cast<const f16x8*>(tile + nt * kLd + c8);
+    }
   }
 }
 
 using Big = asr_mfma::Tile<256, 256, 128, 64, 2>;
+using Mid = asr_mfma::Tile<192, 192, 96, 96, 3>;
 using Small = asr_mfma::Tile<128, 128, 64, 64, 2>;
 using Small8 = asr_mfma::Tile<128, 128, 64, 32, 3>;
 using Tiny = asr_mfma::Tile<64, 64, 32, 32, 4>;
+
+// ------------------------------------------------------- one workgroup
+// All steps of a small matrix in one workgroup of 16 waves: X stays in f32 in
+// the accumulator registers (32 x 32 blocks, kBlocks of them a wave), its f16
+// copy lies in LDS both ways, and a X + B X accumulates onto a X. 5 launches'
+// worth of latency a step becomes three barriers.
+constexpr int kSmallWaves = 16;
+constexpr int kSmallBlocks = 3;
+constexpr int kSmallLds = 159 * 1024;
+
+__host__ __device__ inline bool is_small(int32_t rows, int32_t cols) {
+  const int64_t s = up(rows < cols ? rows : cols, 32), t = up(rows < cols ? cols : rows, 32);
+  return s <= 128 && (s / 32) * (t / 32) <= kSmallWaves * kSmallBlocks &&
+         2 * (s * (t + 8) + t * (s + 8) + 2 * s * (s + 8)) <= kSmallLds;
+}
+
+struct SmallArgs {
+  Desc d[kMaxBatch];
+  double eps;
+  float a, b, c, momentum;
+  int32_t nesterov, steps;
+  OutArgs out;
+};
+
+template <typename G>
+__device__ __forceinline__ float one_value(const G* p, uint32_t i) {
+  if constexpr (sizeof(G) == 4) return p[i];
+  else return asr::bf16_bits_to_f32(p[i]);
+}
+
+// A value the compiler has to take as new: what is computed from it is not
+// kept in registers from one part of the kernel to the next (the index
+// arithmetic of all parts together would not fit beside X).
+__device__ __forceinline__ int32_t fresh(int32_t x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
+template <typename G, bool MUON, int OUT>
+__global__ __launch_bounds__(kSmallWaves * 64) void small_matrix(SmallArgs args) {
+  using E = asr_mfma::ElemF16;
+  __shared__ __align__(16) unsigned char smem[kSmallLds];
+  __shared__ double lds[kSmallWaves];
+  const Desc& d = args.d[blockIdx.x];
+  const Layout l(d.rows, d.cols);
+  const int32_t s = l.s, t = l.t;
+  const int32_t sb = (s + 31) / 32, tb = (t + 31) / 32;  // blocks a side
+  const int32_t ld_x = tb * 32 + 8, ld_y = sb * 32 + 8;  // (8: against bank conflicts)
+  _Float16* x = reinterpret_cast<_Float16*>(smem);
+  _Float16* y = x + sb * 32 * ld_x;
+  _Float16* gram = y + tb * 32 * ld_y;
+  _Float16* poly = gram + sb * 32 * ld_y;
+  const int32_t lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const G* g = static_cast<const G*>(d.g);
+
+  // Block b of this wave is block (i, j) of X; register r of it is row
+  // i * 32 + lane % 32, column j * 32 + 8 (r / 4) + 4 (lane / 32) + r % 4.
+  E::acc xr[kSmallBlocks];
+  auto each_block = [&](auto&& f) {
+    static_for<kSmallBlocks>([&](auto bc) {
+      const int32_t at = fresh(wave) + decltype(bc)::value * kSmallWaves;
+      if (at < sb * tb) f(xr[decltype(bc)::value], at / tb, at % tb);
+    });
+  };
+  // (element (m, n) of X in the matrix's own order; at most 2**16 elements)
+  const int32_t by_m = l.wide ? t : 1, by_n = l.wide ? 1 : s;
+  double sum = 0.0;
+  each_block([&](E::acc& xb, int32_t i, int32_t j) {
+    const int32_t m = i * 32 + row;
+    static_for<4>([&](auto qc) {
+      constexpr int q = decltype(qc)::value;
+      const int32_t n = j * 32 + 8 * q + 4 * half;
+      float gx[4] = {}, mx[4] = {}, u[4];
+      const uint32_t at = static_cast<uint32_t>(m * by_m + n * by_n);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (m < s && n + e < t) {
+          gx[e] = one_value(g, at + e * by_n);
+          if constexpr (MUON) mx[e] = d.m[at + e * by_n];
+        }
+      }
+      momentum_update<MUON>(gx, mx, args.momentum, args.nesterov, true, u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = m < s && n + e < t;
+        if constexpr (MUON) {
+          if (in) d.m[at + e * by_n] = mx[e];
+        }
+        xb[4 * q + e] = in ? u[e] : 0.0f;
+        sum += static_cast<double>(xb[4 * q + e]) * static_cast<double>(xb[4 * q + e]);
+      }
+    });
+  });
+  const double norm = __builtin_sqrt(group_sum<kSmallWaves * 64>(sum, lds));
+  const double factor = static_cast<double>(l.sx) / (norm + args.eps);
+  each_block([&](E::acc& xb, int32_t i, int32_t j) {
+    const int32_t m = i * 32 + row, n = j * 32 + 4 * half;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      // (what lies past the matrix stays zero whatever the factor is)
+      const bool in = m < s && n + 8 * (r / 4) + r % 4 < t;
+      xb[r] = in ? static_cast<float>(static_cast<double>(xb[r]) * factor) : 0.0f;
+    }
+  });
+
+  const float gram_scale = l.sa / (l.sx * l.sx), inv_sa = 1.0f / l.sa;
+  const bool squares = wave < sb * sb;  // this wave's block of A and B
+  const int32_t si = wave / sb, sj = wave % sb;
+  auto frag = [&](const _Float16* base, int32_t ld, int32_t block, int32_t kk) {
+    return *reinterpret_cast<const f16x8*>(base + (block * 32 + row) * ld + 16 * kk + 8 * half);
+  };
+  // c += the block of rows pa of p times rows qa of q, over `blocks` * 32 of K
+  auto dot = [&](E::acc& c, const _Float16* q, int32_t ld_q, int32_t qa, const _Float16* p,
+                 int32_t ld_p, int32_t pa, int32_t blocks) {
+    for (int32_t kk = 0; kk < blocks; ++kk) {
+      const f16x8 q0 = frag(q, ld_q, qa, 2 * kk), p0 = frag(p, ld_p, pa, 2 * kk);
+      const f16x8 q1 = frag(q, ld_q, qa, 2 * kk + 1), p1 = frag(p, ld_p, pa, 2 * kk + 1);
+      c = E::mfma(q0, p0, c);
+      c = E::mfma(q1, p1, c);
+    }
+  };
+  auto put4 = [&](_Float16* at, float v0, float v1, float v2, float v3) {
+    *reinterpret_cast<f16x4*>(at) = f16x4{static_cast<_Float16>(v0), static_cast<_Float16>(v1),
+                                          static_cast<_Float16>(v2), static_cast<_Float16>(v3)};
+  };
+  for (int step = 0; step < args.steps; ++step) {
+    each_block([&](E::acc& xb, int32_t i, int32_t j) {
+      _Float16* to_x = x + (i * 32 + row) * ld_x + j * 32 + 4 * half;
+      _Float16* to_y = y + (j * 32 + 4 * half) * ld_y + i * 32 + row;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        put4(to_x + 8 * q, xb[4 * q], xb[4 * q + 1], xb[4 * q + 2], xb[4 * q + 3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to_y[(8 * q + e) * ld_y] = static_cast<_Float16>(xb[4 * q + e]);
+      }
+    });
+    __syncthreads();
+    E::acc aa = {};
+    if (squares) {
+dot(aa, x, ld_x, sj, x, ld_x, si, tb);
+      _Float16* to = gram + (si * 32 + row) * ld_y + sj * 32 + 4 * half;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) aa[r] *= gram_scale;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) put4(to + 8 * q, aa[4 * q], aa[4 * q + 1], aa[4 * q + 2], aa[4 * q + 3]);
+    }
+    __syncthreads();
+    if (squares) {
+      E::acc bb = {};
+dot(bb, gram, ld_y, sj, gram, ld_y, si, sb);
+      _Float16* to = poly + (si * 32 + row) * ld_y + sj * 32 + 4 * half;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) bb[r] = args.b * aa[r] + args.c * inv_sa * bb[r];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) put4(to + 8 * q, bb[4 * q], bb[4 * q + 1], bb[4 * q + 2], bb[4 * q + 3]);
+    }
+    __syncthreads();
+    each_block([&](E::acc& xb, int32_t i, int32_t j) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) xb[r] *= args.a * l.sa;
+dot(xb, y, ld_y, j, poly, ld_y, i, sb);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) xb[r] *= inv_sa;
+    });
+    __syncthreads();  // every wave has read X^T and B
+  }
+
+  const float inv_sx = 1.0f / l.sx;
+  each_block([&](E::acc& xb, int32_t i, int32_t j) {
+    const int32_t m = i * 32 + row;
+    if (m >= s) return;
+    static_for<4>([&](auto qc) {
+      constexpr int q = decltype(qc)::value;
+      const int32_t n = j * 32 + 8 * q + 4 * half;
+      const int count = min(4, t - n);
+      if (count <= 0) return;
+      const float o[4] = {xb[4 * q] * inv_sx, xb[4 * q + 1] * inv_sx, xb[4 * q + 2] * inv_sx,
+                          xb[4 * q + 3] * inv_sx};
+      if (l.wide) {
+        store_out<OUT, 4>(args.out, d, m * t + n, count, args.out.vec8 && count == 4, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < count) store_out1<OUT>(args.out, d, (n + e) * s + m, o[e]);
+      }
+    });
+  });
+}
 
 }  // namespace asr_muon
 
@@ -416,93 +708,118 @@ bool aligned_to(const void* p, uintptr_t a) {
 constexpr int64_t kMaxSide = int64_t{1} << 20;
 constexpr int64_t kWorkspaceAim = int64_t{4} << 30;
 
-int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-
-// A matrix's part of the workspace: X and Y = X^T (f16, rows padded to 128
-// bytes; Y twice, since the product that makes the next X reads all of the
-// last Y), the low parts, A, B and the norm's partial sums.
-struct Layout {
-  int64_t s, t, ld_s, ld_t;
-  bool wide;  // the matrix itself has its short side first
-  int64_t x, y[2], lo, a, b, parts, stride;
-  Layout(int64_t rows, int64_t cols) {
-    wide = rows <= cols;
-    s = std::min(rows, cols);
-    t = std::max(rows, cols);
-    ld_s = up(s, 64);
-    ld_t = up(t, 64);
-    const int64_t across = s * ld_t * 2, down = t * ld_s * 2, square = s * ld_s * 2;
-    int64_t at = 0;
-    auto take = [&](int64_t bytes) {
-      const int64_t here = at;
-      at += up(bytes, 1024);
-      return here;
-    };
-    x = take(across);
-    y[0] = take(down);
-    y[1] = take(down);
-    lo = take(wide ? across : down);
-    a = take(square);
-    b = take(square);
-    parts = take(kMaxParts * 8);
-    stride = at;
-  }
-};
-
-int32_t chunk_of(int32_t n, int64_t rows, int64_t cols) {
-  const int64_t stride = Layout(rows, cols).stride;
-  return static_cast<int32_t>(
-      std::min<int64_t>({n, kMaxBatch, std::max<int64_t>(1, kWorkspaceAim / stride)}));
-}
-
 template <typename F>
-hipError_t launch(F* f, dim3 grid, int threads, void* args, hipStream_t s) {
+hipError_t launch(F* f, uint32_t grid, int threads, void* args, hipStream_t s) {
   void* argv[] = {args};
-  return hipLaunchKernel(reinterpret_cast<const void*>(f), grid, dim3(threads), argv, 0, s);
+  return hipLaunchKernel(reinterpret_cast<const void*>(f), dim3(grid), dim3(threads), argv, 0, s);
 }
 
 template <typename T, int MODE, int OUT>
 hipError_t launch_tile(ProductArgs& a, hipStream_t s) {
-  a.tiles_m = static_cast<uint32_t>((a.m + T::BM - 1) / T::BM);
-  a.tiles_n = static_cast<uint32_t>((a.n + T::BN - 1) / T::BN);
-  a.tiles = MODE == kGram || MODE == kSquare ? a.tiles_m * (a.tiles_m + 1) / 2
-                                             : a.tiles_m * a.tiles_n;
-  return launch(&product<T, MODE, OUT>, dim3(a.tiles * a.batch), T::kThreads, &a, s);
+  uint32_t total = 0;
+  for (int k = 0; k < a.count; ++k) {
+    a.d[k].first = total;
+    total += static_cast<uint32_t>(tiles_of(MODE, a.d[k].rows, a.d[k].cols, T::BM));
+  }
+  return launch(&product<T, MODE, OUT>, total, T::kThreads, &a, s);
 }
 
-// The tile by how many of them there are for the chip's 256 compute units.
+// Time of a launch in one tile size: its matrices' tiles, in order, go to the
+// next free of the chip's slots (`slots` tiles run at once); a tile costs
+// `fixed` and `per_k` for every 64 of K.
+double launch_time(int mode, const ProductArgs& a, int tile, int slots, double fixed, double per_k) {
+  // free[i] slots are free at when[i]; few different times ever coexist
+  double when[kMaxBatch + 2] = {0.0};
+  int free[kMaxBatch + 2] = {slots};
+  int levels = 1;
+  double end = 0.0;
+  for (int k = 0; k < a.count; ++k) {
+    const Layout l(a.d[k].rows, a.d[k].cols);
+    const double cost = fixed + per_k * ((mode == kGram ? l.ld_t : l.ld_s) / 64);
+    int64_t n = tiles_of(mode, a.d[k].rows, a.d[k].cols, tile);
+    if (n > 4 * slots) {  // whole rounds at once
+      const int64_t rounds = n / slots - 2;
+      for (int i = 0; i < levels; ++i) when[i] += rounds * cost;
+      n -= rounds * slots;
+    }
+    while (n > 0) {
+      int first = 0;
+      for (int i = 1; i < levels; ++i)
+        if (when[i] < when[first]) first = i;
+      const int take = static_cast<int>(std::min<int64_t>(n, free[first]));
+      const double done = when[first] + cost;
+      end = std::max(end, done);
+      n -= take;
+      free[first] -= take;
+      int same = -1;
+      for (int i = 0; i < levels; ++i)
+        if (when[i] == done) same = i;
+      if (same >= 0) free[same] += take;
+      else if (free[first] == 0) when[first] = done, free[first] = take;
+      else if (levels < kMaxBatch + 2) when[levels] = done, free[levels++] = take;
+      else when[first] = done, free[first] += take;  // (no room: a little late)
+      if (free[first] == 0) {
+        --levels;
+        when[first] = when[levels];
+        free[first] = free[levels];
+      }
+    }
+  }
+  for (int i = 0; i < levels; ++i) end = std::max(end, when[i]);
+  return end;
+}
+
+#ifndef ASR_MUON_TILE
+#define ASR_MUON_TILE -1
+#endif
+
 template <int MODE, int OUT = kOutBf16>
 hipError_t launch_product(ProductArgs& a, hipStream_t s) {
-  auto tiles = [&](int64_t t) {
-    const int64_t tm = (a.m + t - 1) / t, tn = (a.n + t - 1) / t;
-    return (MODE == kGram || MODE == kSquare ? tm * (tm + 1) / 2 : tm * tn) * a.batch;
-  };
-  if (tiles(256) >= 256) return launch_tile<Big, MODE, OUT>(a, s);
-  if (tiles(128) > 256) return launch_tile<Small, MODE, OUT>(a, s);
-  if (tiles(128) > 128) return launch_tile<Small8, MODE, OUT>(a, s);
-  return launch_tile<Tiny, MODE, OUT>(a, s);
+  struct Choice { int tile, slots; double fixed, per_k; };
+  // microseconds
+  constexpr Choice choices[] = {{256, 256, 14.0, 1.6}, {192, 256, 10.0, 1.05},
+                                {128, 512, 8.0, 1.05}, {128, 256, 5.0, 0.6}, {64, 512, 4.0, 0.45}};
+  int best = ASR_MUON_TILE;
+  if (best < 0) {
+    double least = 0.0;
+    for (int i = 0; i < 5; ++i) {
+      const double t = launch_time(MODE, a, choices[i].tile, choices[i].slots, choices[i].fixed,
+                                   choices[i].per_k);
+      if (best < 0 || t < least) best = i, least = t;
+    }
+  }
+  switch (best) {
+    case 0: return launch_tile<Big, MODE, OUT>(a, s);
+    case 1: return launch_tile<Mid, MODE, OUT>(a, s);
+    case 2: return launch_tile<Small, MODE, OUT>(a, s);
+    case 3: return launch_tile<Small8, MODE, OUT>(a, s);
+    default: return launch_tile<Tiny, MODE, OUT>(a, s);
+  }
 }
 
+// What a call does with every matrix of its list.
 struct Settings {
-  int64_t rows, cols;
   int32_t g_dtype, steps;
   double a, b, c, eps;
+  float momentum;
+  bool nesterov;
+  OutArgs out;
   char* ws;
   hipStream_t stream;
 };
 
 // Largest singular value the polynomial lets any of [0, 1] reach in `steps`
-// steps, and the largest |b l + c l^2| it meets: what the f16 operands' scales
-// (2**14 at most) have to hold.
+// steps, and the largest |b x^2 + c x^4| it meets: what the f16 operands'
+// scales (2**14 at most) have to hold.
 bool coefficients_ok(double a, double b, double c, int steps) {
   if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
   double top = 1.0;
   for (int k = 0; k < steps; ++k) {
     double next = 0.0;
     for (int i = 0; i <= 256; ++i) {
-      const double x = top * i / 256, l = x * x;
-      if (std::fabs(b * l + c * l * l) > 3.75) return false;
-      next = std::max(next, std::fabs(x * (a + b * l + c * l * l)));
+      const double x = top * i / 256, q = x * x;
+      if (std::fabs(b * q + c * q * q) > 3.75) return false;
+      next = std::max(next, std::fabs(x * (a + b * q + c * q * q)));
     }
     if (next > 1.4) return false;
     if (next <= top) return true;  // the later steps stay inside what was looked at
@@ -511,108 +828,118 @@ bool coefficients_ok(double a, double b, double c, int steps) {
   return true;
 }
 
-template <int OUT, bool MUON>
-hipError_t run(const Settings& st, const Matrices& mat, int32_t batch, ProductArgs last,
-               float momentum, bool nesterov) {
-  const Layout l(st.rows, st.cols);
-  auto power = [](double x) { return std::ldexp(1.0, std::min(14, static_cast<int>(std::lround(std::log2(x))))); };
-  const double sx = power(std::sqrt(static_cast<double>(l.s) * static_cast<double>(l.t)));
-  const double sa = power(static_cast<double>(l.s));
-
-  PrepareArgs pa{};
-  pa.mat = mat;
-  pa.rows = st.rows;
-  pa.cols = st.cols;
-  pa.numel = st.rows * st.cols;
-  const int64_t parts = std::clamp<int64_t>((pa.numel + 8191) / 8192, 1, kMaxParts);
-  pa.chunk = up((pa.numel + parts - 1) / parts, 2048);
-  pa.parts_n = static_cast<int32_t>((pa.numel + pa.chunk - 1) / pa.chunk);
-  pa.ws = st.ws;
-  pa.stride = l.stride;
-  pa.parts = l.parts;
-  pa.direct = l.wide ? l.x : l.y[0];
-  pa.turned = l.wide ? l.y[0] : l.x;
-  pa.lo = l.lo;
-  pa.ld_direct = l.wide ? l.ld_t : l.ld_s;
-  pa.ld_turned = l.wide ? l.ld_s : l.ld_t;
-  pa.eps = st.eps;
-  pa.scale = sx;
-  pa.momentum = momentum;
-  pa.nesterov = nesterov;
-  pa.vec = 1;
-  for (int32_t k = 0; k < batch; ++k)
-    pa.vec = pa.vec && aligned_to(mat.g[k], 16) && (!MUON || aligned_to(mat.m[k], 16));
-  const dim3 grid1(static_cast<uint32_t>(pa.parts_n), static_cast<uint32_t>(batch));
-  const dim3 grid2(static_cast<uint32_t>((st.cols + 63) / 64), static_cast<uint32_t>((st.rows + 63) / 64),
-                   static_cast<uint32_t>(batch));
-  hipError_t e;
-  if (st.g_dtype == ASR_F32) {
-    e = launch(&sum_squares<float, MUON>, grid1, 256, &pa, st.stream);
-    if (e == hipSuccess) e = launch(&scale_matrix<float, MUON>, grid2, 256, &pa, st.stream);
-  } else {
-    e = launch(&sum_squares<uint16_t, MUON>, grid1, 256, &pa, st.stream);
-    if (e == hipSuccess) e = launch(&scale_matrix<uint16_t, MUON>, grid2, 256, &pa, st.stream);
+template <typename G, bool MUON, int OUT>
+hipError_t run_small(const Settings& st, const Desc* const* list, int32_t n) {
+  SmallArgs a{};
+  a.eps = st.eps;
+  a.a = static_cast<float>(st.a);
+  a.b = static_cast<float>(st.b);
+  a.c = static_cast<float>(st.c);
+  a.momentum = st.momentum;
+  a.nesterov = st.nesterov;
+  a.steps = st.steps;
+  a.out = st.out;
+  for (int32_t k0 = 0; k0 < n; k0 += kMaxBatch) {
+    const int32_t count = std::min(kMaxBatch, n - k0);
+    for (int32_t k = 0; k < count; ++k) a.d[k] = *list[k0 + k];
+    const hipError_t e = launch(&small_matrix<G, MUON, OUT>, static_cast<uint32_t>(count),
+                                kSmallWaves * 64, &a, st.stream);
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
+}
 
-  ProductArgs gram{};
-  gram.ws = st.ws;
-  gram.stride = l.stride;
-  gram.batch = static_cast<uint32_t>(batch);
-  gram.a = gram.b = l.x;
-  gram.ld_a = gram.ld_b = static_cast<uint32_t>(l.ld_t * 2);
-  gram.kbytes = static_cast<int32_t>(l.ld_t * 2);
-  gram.m = gram.n = static_cast<int32_t>(l.s);
-  gram.d = gram.turned = l.a;
-  gram.ld_d = gram.ld_turned = l.ld_s;
-  gram.alpha = static_cast<float>(sa / (sx * sx));
-  ProductArgs square = gram;
-  square.a = square.b = square.c = l.a;
-  square.ld_a = square.ld_b = static_cast<uint32_t>(l.ld_s * 2);
-  square.kbytes = static_cast<int32_t>(l.ld_s * 2);
-  square.d = square.turned = l.b;
-  square.alpha = static_cast<float>(st.c / sa);
-  square.beta = static_cast<float>(st.b);
-  for (int32_t i = 0; i < st.steps && e == hipSuccess; ++i) {
-    e = launch_product<kGram>(gram, st.stream);
-    if (e == hipSuccess) e = launch_product<kSquare>(square, st.stream);
-    if (e != hipSuccess) break;
-    // B X in the matrix's own orientation: rows of B (or Y) by rows of Y (or B)
-    const int64_t y = l.y[i & 1], y_next = l.y[(i & 1) ^ 1];
-    ProductArgs u = i + 1 < st.steps ? square : last;
-    u.ws = st.ws;
-    u.stride = l.stride;
-    u.batch = gram.batch;
-    u.a = l.wide ? l.b : y;
-    u.b = l.wide ? y : l.b;
-    u.ld_a = u.ld_b = static_cast<uint32_t>(l.ld_s * 2);
-    u.kbytes = static_cast<int32_t>(l.ld_s * 2);
-    u.m = static_cast<int32_t>(st.rows);
-    u.n = static_cast<int32_t>(st.cols);
-    u.c = l.wide ? l.x : y;
-    u.lo = l.lo;
-    u.d = l.wide ? l.x : y_next;
-    u.turned = l.wide ? y_next : l.x;
-    u.ld_d = pa.ld_direct;
-    u.ld_turned = pa.ld_turned;
-    u.alpha = static_cast<float>(1.0 / sa);
-    u.beta = static_cast<float>(st.a);
-    u.out_scale = static_cast<float>(1.0 / sx);
-    if (i + 1 < st.steps) {
-      e = launch_product<kUpdate>(u, st.stream);
-    } else {
-      u.mat = mat;
-      e = launch_product<kFinal, OUT>(u, st.stream);
-    }
+// One group of matrices that share a workspace, the longest K first.
+template <typename G, bool MUON, int OUT>
+hipError_t run_group(const Settings& st, const Desc* const* list, int32_t count) {
+  PrepareArgs pa{};
+  pa.ws = st.ws;
+  pa.eps = st.eps;
+  pa.momentum = st.momentum;
+  pa.nesterov = st.nesterov;
+  pa.count = count;
+  pa.vec = 1;
+  int64_t at = 0;
+  uint32_t total = 0;
+  for (int32_t k = 0; k < count; ++k) {
+    Desc& d = pa.d[k];
+    d = *list[k];
+    d.ws = at;
+    at += Layout(d.rows, d.cols).bytes;
+    pa.vec = pa.vec && aligned_to(d.g, 16) && (!MUON || aligned_to(d.m, 16));
+    const int64_t numel = static_cast<int64_t>(d.rows) * d.cols;
+    d.first = total;
+    total += static_cast<uint32_t>((numel + part_size(numel) - 1) / part_size(numel));
+  }
+  hipError_t e = launch(&sum_squares<G, MUON>, total, 256, &pa, st.stream);
+  if (e != hipSuccess) return e;
+  total = 0;
+  for (int32_t k = 0; k < count; ++k) {
+    pa.d[k].first = total;
+    total += static_cast<uint32_t>(((pa.d[k].rows + 63) / 64) * ((pa.d[k].cols + 63) / 64));
+  }
+  e = launch(&scale_matrix<G, MUON>, total, 256, &pa, st.stream);
+  if (e != hipSuccess) return e;
+
+  ProductArgs a{};
+  std::copy(pa.d, pa.d + count, a.d);
+  a.ws = st.ws;
+  a.a = static_cast<float>(st.a);
+  a.b = static_cast<float>(st.b);
+  a.c = static_cast<float>(st.c);
+  a.count = count;
+  a.out = st.out;
+  for (int32_t i = 0; i < st.steps; ++i) {
+    a.y = i & 1;
+    if ((e = launch_product<kGram>(a, st.stream)) != hipSuccess) return e;
+    if ((e = launch_product<kSquare>(a, st.stream)) != hipSuccess) return e;
+    if (i + 1 < st.steps) e = launch_product<kUpdate>(a, st.stream);
+    else e = launch_product<kFinal, OUT>(a, st.stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// The list's order: matrices for one workgroup first, then the others by
+// falling long side, cut into groups of at most kMaxBatch whose workspace stays
+// near kWorkspaceAim (one matrix, if it alone needs more).
+bool goes_before(int32_t r0, int32_t c0, int32_t r1, int32_t c1) {
+  const bool s0 = is_small(r0, c0), s1 = is_small(r1, c1);
+  if (s0 != s1) return s0;
+  return std::max(r0, c0) > std::max(r1, c1);
+}
+
+template <typename Shape>
+int32_t group_end(int32_t k0, int32_t n, Shape shape, int64_t& bytes) {
+  bytes = 0;
+  int32_t k = k0;
+  for (; k < n && k - k0 < kMaxBatch; ++k) {
+    const auto [r, c] = shape(k);
+    const int64_t b = Layout(r, c).bytes;
+    if (k > k0 && bytes + b > kWorkspaceAim) break;
+    bytes += b;
+  }
+  return k;
+}
+
+template <typename G, bool MUON, int OUT>
+hipError_t run(const Settings& st, const Desc* const* list, int32_t n) {
+  int32_t small = 0;
+  while (small < n && is_small(list[small]->rows, list[small]->cols)) ++small;
+  hipError_t e = run_small<G, MUON, OUT>(st, list, small);
+  for (int32_t k0 = small; k0 < n && e == hipSuccess;) {
+    int64_t bytes;
+    const int32_t k1 = group_end(k0, n, [&](int32_t k) { return std::pair(list[k]->rows, list[k]->cols); }, bytes);
+    e = run_group<G, MUON, OUT>(st, list + k0, k1 - k0);
+    k0 = k1;
   }
   return e;
 }
 
-int check(const char* who, int32_t n, int64_t rows, int64_t cols, int32_t g_dtype, int32_t steps,
-          double a, double b, double c, double eps) {
+int check(const char* who, int32_t n, int32_t g_dtype, int32_t steps, double a, double b, double c,
+          double eps) {
   const std::string w(who);
   if (n < 0) return fail(ASR_EINVAL, w + ": a negative number of matrices");
-  if (rows < 0 || cols < 0 || rows > kMaxSide || cols > kMaxSide)
-    return fail(ASR_EINVAL, w + ": rows and cols must be in [0, 2**20]");
   if (g_dtype != ASR_F32 && g_dtype != ASR_BF16) return fail(ASR_EDTYPE, w + ": unknown dtype");
   if (steps < 1 || steps > 64) return fail(ASR_EINVAL, w + ": steps must be in [1, 64]");
   if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(ASR_EINVAL, w + ": eps must be finite, >= 0");
@@ -622,10 +949,29 @@ int check(const char* who, int32_t n, int64_t rows, int64_t cols, int32_t g_dtyp
   return ASR_OK;
 }
 
+bool sides_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows <= kMaxSide && cols <= kMaxSide;
+}
+
 int check_workspace(const char* who, void* ws, size_t bytes, size_t need) {
-  if (!ws || !aligned_to(ws, 256) || bytes < need)
+  if (need > 0 && (!ws || !aligned_to(ws, 256) || bytes < need))
     return fail(ASR_EWORKSPACE, std::string(who) + ": workspace NULL, too small or not 256-byte aligned");
   return ASR_OK;
+}
+
+struct Shape { int32_t rows, cols; };
+
+// Workspace of n matrices whose shapes are in list order (see goes_before).
+size_t list_bytes(const Shape* shapes, int32_t n) {
+  int32_t k0 = 0;
+  while (k0 < n && is_small(shapes[k0].rows, shapes[k0].cols)) ++k0;
+  int64_t most = 0;
+  while (k0 < n) {
+    int64_t bytes;
+    k0 = group_end(k0, n, [&](int32_t k) { return std::pair(shapes[k].rows, shapes[k].cols); }, bytes);
+    most = std::max(most, bytes);
+  }
+  return static_cast<size_t>(most);
 }
 
 }  // namespace
@@ -633,106 +979,123 @@ int check_workspace(const char* who, void* ws, size_t bytes, size_t need) {
 extern "C" {
 
 size_t asr_newton_schulz_workspace_bytes(int32_t n, int64_t rows, int64_t cols) {
-  if (n <= 0 || rows <= 0 || cols <= 0 || rows > kMaxSide || cols > kMaxSide) return 0;
-  return static_cast<size_t>(chunk_of(n, rows, cols) * Layout(rows, cols).stride);
+  if (n <= 0 || rows <= 0 || cols <= 0 || !sides_ok(rows, cols) ||
+      is_small(static_cast<int32_t>(rows), static_cast<int32_t>(cols)))
+    return 0;
+  int64_t bytes;
+  group_end(0, n, [&](int32_t) { return std::pair(static_cast<int32_t>(rows), static_cast<int32_t>(cols)); }, bytes);
+  return static_cast<size_t>(bytes);
 }
 
 int asr_newton_schulz(const void* const* g, uint16_t* const* out, int32_t n, int64_t rows,
                       int64_t cols, int32_t g_dtype, int32_t steps, double a, double b, double c,
                       double eps, void* workspace, size_t workspace_bytes, void* stream) {
   const char* who = "newton_schulz";
-  if (int rc = check(who, n, rows, cols, g_dtype, steps, a, b, c, eps)) return rc;
+  if (int rc = check(who, n, g_dtype, steps, a, b, c, eps)) return rc;
+  if (!sides_ok(rows, cols)) return fail(ASR_EINVAL, "newton_schulz: rows and cols must be in [0, 2**20]");
   if (n == 0 || rows == 0 || cols == 0) return ok();
   if (!g || !out) return fail(ASR_EINVAL, "newton_schulz: null array");
+  Settings st{g_dtype, steps, a, b, c, eps, 0.0f, false, {}, static_cast<char*>(workspace),
+              static_cast<hipStream_t>(stream)};
+  st.out.vec8 = cols % 8 == 0;
   for (int32_t k = 0; k < n; ++k) {
     if (!g[k] || !out[k]) return fail(ASR_EINVAL, "newton_schulz: null matrix");
     if (!aligned_to(g[k], g_dtype == ASR_F32 ? 4 : 2) || !aligned_to(out[k], 2))
       return fail(ASR_EALIGN, "newton_schulz: matrices must be aligned to their element size");
+    st.out.vec8 = st.out.vec8 && aligned_to(out[k], 16);
   }
   if (int rc = check_workspace(who, workspace, workspace_bytes,
                                asr_newton_schulz_workspace_bytes(n, rows, cols)))
     return rc;
-  const Settings st{rows, cols, g_dtype, steps, a, b, c, eps, static_cast<char*>(workspace),
-                    static_cast<hipStream_t>(stream)};
-  const int32_t chunk = chunk_of(n, rows, cols);
-  for (int32_t k0 = 0; k0 < n; k0 += chunk) {
-    const int32_t batch = std::min(chunk, n - k0);
-    Matrices mat{};
-    ProductArgs last{};
-    last.ld_out = cols;
-    last.vec4 = cols % 4 == 0;
-    for (int32_t k = 0; k < batch; ++k) {
-      mat.g[k] = g[k0 + k];
-      mat.p[k] = out[k0 + k];
-      last.vec4 = last.vec4 && aligned_to(mat.p[k], 8);
-    }
-    const hipError_t e = run<kOutBf16, false>(st, mat, batch, last, 0.0f, false);
-    if (e != hipSuccess) return hip_fail(e, "newton_schulz launch");
+  std::unique_ptr<Desc[]> descs(new (std::nothrow) Desc[n]);
+  std::unique_ptr<const Desc*[]> list(new (std::nothrow) const Desc*[n]);
+  if (!descs || !list) return fail(ASR_EINVAL, "newton_schulz: out of host memory");
+  for (int32_t k = 0; k < n; ++k) {
+    descs[k] = Desc{g[k], nullptr, out[k], 0, 0, static_cast<int32_t>(rows), static_cast<int32_t>(cols), 0.0f, 0};
+    list[k] = &descs[k];
   }
-  return ok();
+  const hipError_t e = g_dtype == ASR_F32 ? run<float, false, kOutBf16>(st, list.get(), n)
+                                          : run<uint16_t, false, kOutBf16>(st, list.get(), n);
+  return e == hipSuccess ? ok() : hip_fail(e, "newton_schulz launch");
 }
 
-int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int64_t rows, int64_t cols,
-                  int32_t param_dtype, int32_t grad_dtype, double lr, double momentum,
-                  int32_t nesterov, double weight_decay, double lr_factor, int32_t ns_steps,
-                  double ns_a, double ns_b, double ns_c, double eps, int64_t step, uint32_t seed,
-                  int32_t rounding, void* workspace, size_t workspace_bytes, void* stream) {
+size_t asr_muon_workspace_bytes(const asr_muon_tensor* tensors, int32_t n) {
+  if (!tensors || n <= 0) return 0;
+  std::unique_ptr<Shape[]> shapes(new (std::nothrow) Shape[n]);
+  if (!shapes) return 0;
+  int32_t live = 0;
+  for (int32_t k = 0; k < n; ++k) {
+    const asr_muon_tensor& t = tensors[k];
+    if (!sides_ok(t.rows, t.cols)) return 0;
+    if (t.rows > 0 && t.cols > 0)
+      shapes[live++] = Shape{static_cast<int32_t>(t.rows), static_cast<int32_t>(t.cols)};
+  }
+  std::sort(shapes.get(), shapes.get() + live, [](const Shape& x, const Shape& y) {
+    return goes_before(x.rows, x.cols, y.rows, y.cols);
+  });
+  return list_bytes(shapes.get(), live);
+}
+
+int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int32_t param_dtype, int32_t grad_dtype,
+                  double lr, double momentum, int32_t nesterov, double weight_decay,
+                  int32_t ns_steps, double ns_a, double ns_b, double ns_c, double eps, int64_t step,
+                  uint32_t seed, int32_t rounding, void* workspace, size_t workspace_bytes,
+                  void* stream) {
   const char* who = "muon";
-  if (int rc = check(who, n, rows, cols, grad_dtype, ns_steps, ns_a, ns_b, ns_c, eps)) return rc;
+  if (int rc = check(who, n, grad_dtype, ns_steps, ns_a, ns_b, ns_c, eps)) return rc;
   if (param_dtype != ASR_F32 && param_dtype != ASR_BF16)
     return fail(ASR_EDTYPE, "muon: unknown param dtype");
   if (rounding != ASR_ROUND_SR && rounding != ASR_ROUND_RN)
     return fail(ASR_EINVAL, "muon: rounding must be ASR_ROUND_SR or ASR_ROUND_RN");
   if (!(lr >= 0.0) || !std::isfinite(lr) || !(weight_decay >= 0.0) || !std::isfinite(weight_decay) ||
-      !(lr_factor >= 0.0) || !std::isfinite(lr_factor) || !(momentum >= 0.0 && momentum < 1.0))
-    return fail(ASR_EINVAL, "muon: lr, weight_decay and lr_factor finite and >= 0, momentum in [0, 1)");
+      !(momentum >= 0.0 && momentum < 1.0))
+    return fail(ASR_EINVAL, "muon: lr and weight_decay finite and >= 0, momentum in [0, 1)");
   if (step < 1 || step >= (int64_t{1} << 32))
     return fail(ASR_EINVAL, "muon: step must be in [1, 2**32 - 1]");
-  if (n == 0 || rows == 0 || cols == 0) return ok();
+  if (n == 0) return ok();
   if (!tensors) return fail(ASR_EINVAL, "muon: null list");
+  std::unique_ptr<Desc[]> descs(new (std::nothrow) Desc[n]);
+  std::unique_ptr<const Desc*[]> list(new (std::nothrow) const Desc*[n]);
+  if (!descs || !list) return fail(ASR_EINVAL, "muon: out of host memory");
+  Settings st{grad_dtype, ns_steps, ns_a, ns_b, ns_c, eps, static_cast<float>(momentum),
+              nesterov != 0, {}, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)};
+  st.out.decay = static_cast<float>(1.0 - lr * weight_decay);
+  st.out.seed = seed;
+  st.out.step = static_cast<uint32_t>(step);
+  st.out.vec8 = 1;
+  int32_t live = 0;
   for (int32_t k = 0; k < n; ++k) {
     const asr_muon_tensor& t = tensors[k];
+    if (!sides_ok(t.rows, t.cols)) return fail(ASR_EINVAL, "muon: rows and cols must be in [0, 2**20]");
+    if (!(t.lr_factor >= 0.0) || !std::isfinite(t.lr_factor))
+      return fail(ASR_EINVAL, "muon: lr_factor must be finite and >= 0");
+    if (t.rows == 0 || t.cols == 0) continue;
     if (!t.param || !t.grad || !t.momentum) return fail(ASR_EINVAL, "muon: null buffer");
     if (!aligned_to(t.param, param_dtype == ASR_F32 ? 4 : 2) ||
         !aligned_to(t.grad, grad_dtype == ASR_F32 ? 4 : 2) || !aligned_to(t.momentum, 4))
       return fail(ASR_EALIGN, "muon: buffers must be aligned to their element size");
+    st.out.vec8 = st.out.vec8 && t.cols % 8 == 0 && aligned_to(t.param, 16);
+    descs[live] = Desc{t.grad, t.momentum, t.param, t.base_index, 0, static_cast<int32_t>(t.rows),
+                       static_cast<int32_t>(t.cols), static_cast<float>(lr * t.lr_factor), 0};
+    list[live] = &descs[live];
+    ++live;
   }
-  if (int rc = check_workspace(who, workspace, workspace_bytes,
-                               asr_newton_schulz_workspace_bytes(n, rows, cols)))
+  if (int rc = check_workspace(who, workspace, workspace_bytes, asr_muon_workspace_bytes(tensors, n)))
     return rc;
-  const Settings st{rows, cols, grad_dtype, ns_steps, ns_a, ns_b, ns_c, eps,
-                    static_cast<char*>(workspace), static_cast<hipStream_t>(stream)};
-  const int32_t chunk = chunk_of(n, rows, cols);
-  for (int32_t k0 = 0; k0 < n; k0 += chunk) {
-    const int32_t batch = std::min(chunk, n - k0);
-    Matrices mat{};
-    ProductArgs last{};
-    last.ld_out = cols;
-    last.vec4 = cols % 4 == 0;
-    last.pos4 = cols % 4 == 0;
-    last.decay = static_cast<float>(1.0 - lr * weight_decay);
-    last.eta = static_cast<float>(lr * lr_factor);
-    last.seed = seed;
-    last.step = static_cast<uint32_t>(step);
-    for (int32_t k = 0; k < batch; ++k) {
-      const asr_muon_tensor& t = tensors[k0 + k];
-      mat.g[k] = t.grad;
-      mat.m[k] = t.momentum;
-      mat.p[k] = t.param;
-      mat.base[k] = t.base_index;
-      last.vec4 = last.vec4 && aligned_to(t.param, param_dtype == ASR_F32 ? 16 : 8);
-    }
-    const float mu = static_cast<float>(momentum);
-    hipError_t e;
-    if (param_dtype == ASR_F32)
-      e = run<kOutWeightF32, true>(st, mat, batch, last, mu, nesterov != 0);
-    else if (rounding == ASR_ROUND_SR)
-      e = run<kOutWeightBf16Sr, true>(st, mat, batch, last, mu, nesterov != 0);
-    else
-      e = run<kOutWeightBf16Rn, true>(st, mat, batch, last, mu, nesterov != 0);
-    if (e != hipSuccess) return hip_fail(e, "muon launch");
-  }
-  return ok();
+  if (live == 0) return ok();
+  std::sort(list.get(), list.get() + live, [](const Desc* x, const Desc* y) {
+    return goes_before(x->rows, x->cols, y->rows, y->cols);
+  });
+  hipError_t e;
+  auto go = [&](auto g) {
+    using G = decltype(g);
+    if (param_dtype == ASR_F32) return run<G, true, kOutWeightF32>(st, list.get(), live);
+    if (rounding == ASR_ROUND_SR) return run<G, true, kOutWeightBf16Sr>(st, list.get(), live);
+    return run<G, true, kOutWeightBf16Rn>(st, list.get(), live);
+  };
+  if (grad_dtype == ASR_F32) e = go(float{});
+  else e = go(uint16_t{});
+  return e == hipSuccess ? ok() : hip_fail(e, "muon launch");
 }
 
 }  // extern "C"

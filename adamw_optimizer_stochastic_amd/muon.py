@@ -10,7 +10,7 @@ share positions (give MuonSR the number of elements AdamWSR has).
 
 For each matrix: m = momentum*m + g (f32), u = g + momentum*m (nesterov) or m,
 p = p*(1 - lr*weight_decay) - lr*factor*O(u), O the Newton-Schulz
-orthogonalisation. Matrices of one shape go through the products together,
+orthogonalisation. All matrices of a group go through the products together,
 which is what fills the chip with small ones.
 """
 

@@ -491,12 +491,9 @@ def muon_lr_factor(rows, cols, adjust_lr="original"):
 
 
 def muon_workspace_bytes(shapes):
-    """Workspace bytes of a muon_step over matrices of these shapes."""
-    count = {}
-    for s in shapes:
-        count[tuple(s)] = count.get(tuple(s), 0) + 1
-    return max((_abi.asr_newton_schulz_workspace_bytes(k, *s) for s, k in count.items()),
-               default=0)
+    """Workspace bytes that hold a muon_step over matrices of these shapes."""
+    arr = _abi.muon_array([(None, None, None, r, c, 0, 1.0) for r, c in shapes])
+    return _abi.asr_muon_workspace_bytes(arr, len(shapes))
 
 
 def muon_step(params, grads, momenta, base_indices, *, lr, momentum=0.95, nesterov=True,
@@ -509,8 +506,8 @@ def muon_step(params, grads, momenta, base_indices, *, lr, momentum=0.95, nester
     (nesterov) or m, p = p*(1 - lr*weight_decay) - lr*factor*newton_schulz(u),
     with factor = muon_lr_factor(rows, cols, adjust_lr). bf16 params are
     rounded by ``rounding`` ("sr": element i of a matrix at position
-    base_index + i under key (seed, step), or "rn"). Matrices of one shape
-    and type go through the products together.
+    base_index + i under key (seed, step), or "rn"). Matrices of one type go
+    through the products together, whatever their shapes.
     """
     n = len(params)
     if not (len(grads) == len(momenta) == len(base_indices) == n):
@@ -537,21 +534,22 @@ def muon_step(params, grads, momenta, base_indices, *, lr, momentum=0.95, nester
             raise TypeError(f"matrix {i}: momenta must be float32")
         if g.shape != p.shape or m.shape != p.shape:
             raise ValueError(f"matrix {i}: param, grad and momentum differ in shape")
-        groups.setdefault((*p.shape, p.dtype, g.dtype), []).append(
-            (p.data_ptr(), g.data_ptr(), m.data_ptr(), _u64(f"base_indices[{i}]", base)))
+        rows, cols = p.shape
+        groups.setdefault((p.dtype, g.dtype), []).append(
+            (p.data_ptr(), g.data_ptr(), m.data_ptr(), rows, cols,
+             _u64(f"base_indices[{i}]", base), muon_lr_factor(rows, cols, adjust_lr)))
     if n == 0:
         return
     check_disjoint(spans)
-    need = max(_abi.asr_newton_schulz_workspace_bytes(len(ts), rows, cols)
-               for (rows, cols, _, _), ts in groups.items())
+    groups = {key: (_abi.muon_array(ts), len(ts)) for key, ts in groups.items()}
+    need = max(_abi.asr_muon_workspace_bytes(arr, k) for arr, k in groups.values())
     workspace = _ns_workspace(workspace, need, device)
     with torch.cuda.device(device):
-        for (rows, cols, pt, gt), ts in groups.items():
-            _abi.asr_muon_step(ts, rows, cols, _DTYPE_CODE[pt], _DTYPE_CODE[gt], float(lr),
+        for (pt, gt), (arr, k) in groups.items():
+            _abi.asr_muon_step(arr, k, _DTYPE_CODE[pt], _DTYPE_CODE[gt], float(lr),
                                float(momentum), int(bool(nesterov)), float(weight_decay),
-                               muon_lr_factor(rows, cols, adjust_lr), operator.index(ns_steps),
-                               coefficients, float(eps), step, seed, ROUNDING_CODE[rounding],
-                               workspace.data_ptr(),
+                               operator.index(ns_steps), coefficients, float(eps), step, seed,
+                               ROUNDING_CODE[rounding], workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), _stream(device))
 
 

@@ -347,9 +347,9 @@ int asr_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb,
  * |b x^2 + c x^4| below 3.75 there. workspace:
  * asr_newton_schulz_workspace_bytes(n, rows, cols) bytes of device memory,
  * 256-byte aligned, overwritten in stream order: calls that may overlap need
- * a workspace each. (About 8 bytes an element and 4 a squared short side; at
- * most 16 matrices at a time, and of large ones about 4 GiB, are in flight
- * together.)
+ * a workspace each. (About 8 bytes an element and 4 a squared short side, for
+ * at most 32 matrices at a time, and of large ones about 4 GiB; none for matrices
+ * that one workgroup holds, such as 128 x 128 or 64 x 512.)
  * Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Runs
  * on `stream`; does not synchronize; nothing is allocated.
  */
@@ -360,7 +360,7 @@ int asr_newton_schulz(const void* const* g, uint16_t* const* out, int32_t n,
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * One Muon step over n matrices of one shape and type. For each, in binary32,
+ * One Muon step over n matrices, of any shapes and of one type. For each, in binary32,
  * every operation rounded on its own:
  *   m <- momentum*m + g,   u = nesterov ? g + momentum*m : m,
  *   O = the orthogonalisation of u as above (before its rounding to bf16),
@@ -372,20 +372,23 @@ int asr_newton_schulz(const void* const* g, uint16_t* const* out, int32_t n,
  * example sqrt(max(1, rows / cols)), or 0.2 sqrt(max(rows, cols)).
  * lr, weight_decay, lr_factor >= 0; 0 <= momentum < 1; step in [1, 2**32 - 1].
  * tensors: host array, read during the call only; buffers pairwise disjoint.
- * Other arguments, workspace and errors as for asr_newton_schulz.
+ * workspace: asr_muon_workspace_bytes(tensors, n) bytes (only the shapes
+ * matter), as for asr_newton_schulz; other arguments and errors as there.
  */
 typedef struct asr_muon_tensor {
   void* param;          /* rows*cols elements of param_dtype, updated in place */
   const void* grad;     /* rows*cols elements of grad_dtype, read only         */
   float* momentum;      /* rows*cols f32, updated in place                     */
+  int64_t rows, cols;   /* in [0, 2**20]; an empty matrix is skipped           */
   uint64_t base_index;  /* global position of element 0 (random-bit stream)    */
+  double lr_factor;     /* finite, >= 0                                        */
 } asr_muon_tensor;
-int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int64_t rows,
-                  int64_t cols, int32_t param_dtype, int32_t grad_dtype,
-                  double lr, double momentum, int32_t nesterov,
-                  double weight_decay, double lr_factor, int32_t ns_steps,
-                  double ns_a, double ns_b, double ns_c, double eps,
-                  int64_t step, uint32_t seed, int32_t rounding,
+size_t asr_muon_workspace_bytes(const asr_muon_tensor* tensors, int32_t n);
+int asr_muon_step(const asr_muon_tensor* tensors, int32_t n,
+                  int32_t param_dtype, int32_t grad_dtype, double lr,
+                  double momentum, int32_t nesterov, double weight_decay,
+                  int32_t ns_steps, double ns_a, double ns_b, double ns_c,
+                  double eps, int64_t step, uint32_t seed, int32_t rounding,
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /*

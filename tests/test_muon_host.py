@@ -27,9 +27,9 @@ def _status(fn, *args):
 
 def test_newton_schulz_argument_errors():
     E = _abi
-    need = E.asr_newton_schulz_workspace_bytes(1, 40, 60)
+    need = E.asr_newton_schulz_workspace_bytes(1, 400, 600)
 
-    def f(g=(0x1000,), out=(0x8000,), rows=40, cols=60, dtype=E.ASR_BF16, steps=5, coeffs=NS,
+    def f(g=(0x1000,), out=(0x80000,), rows=400, cols=600, dtype=E.ASR_BF16, steps=5, coeffs=NS,
           eps=1e-7, ws=0x100000, ws_bytes=need):
         return _status(E.asr_newton_schulz, g, out, rows, cols, dtype, steps, *coeffs, eps, ws,
                        ws_bytes, None)
@@ -49,7 +49,7 @@ def test_newton_schulz_argument_errors():
     assert f(out=(0,)) == E.ASR_EINVAL
     assert f(g=(0x1001,)) == E.ASR_EALIGN
     assert f(dtype=E.ASR_F32, g=(0x1002,)) == E.ASR_EALIGN
-    assert f(out=(0x8001,)) == E.ASR_EALIGN
+    assert f(out=(0x80001,)) == E.ASR_EALIGN
     assert f(ws=0) == E.ASR_EWORKSPACE
     assert f(ws=0x100080) == E.ASR_EWORKSPACE
     assert f(ws_bytes=need - 1) == E.ASR_EWORKSPACE
@@ -62,54 +62,69 @@ def test_accepted_coefficients():
     stops the call)."""
     E = _abi
     for c in (NS, (1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (2.0, -1.5, 0.5)):
-        got = _status(E.asr_newton_schulz, (0x1000,), (0x8000,), 8, 8, E.ASR_BF16, 5, *c, 1e-7, 0,
+        got = _status(E.asr_newton_schulz, (0x1000,), (0x8000,), 300, 300, E.ASR_BF16, 5, *c, 1e-7, 0,
                       0, None)
         assert got == E.ASR_EWORKSPACE, c
 
 
 def test_workspace_bytes():
     f = _abi.asr_newton_schulz_workspace_bytes
-    assert f(0, 8, 8) == 0 and f(1, 0, 8) == 0 and f(1, -1, 8) == 0
-    assert f(1, 300, 100) >= 8 * 100 * 300 + 4 * 100 * 100
-    one = f(1, 100, 300)
-    assert one >= 8 * 100 * 300 + 4 * 100 * 100
-    assert f(3, 100, 300) == 3 * one
-    assert f(16, 100, 300) == f(500, 100, 300) == 16 * one   # at most 16 at a time
+    assert f(0, 800, 800) == 0 and f(1, 0, 8) == 0 and f(1, -1, 8) == 0
+    one = f(1, 200, 300)
+    assert one >= 8 * 200 * 300 + 4 * 200 * 200
+    assert f(1, 300, 200) >= 8 * 200 * 300 + 4 * 200 * 200
+    assert f(3, 200, 300) == 3 * one
+    assert f(32, 200, 300) == f(500, 200, 300) == 32 * one   # at most 32 at a time
     big = f(1, 8192, 28672)
     assert f(9, 8192, 28672) == max(1, (4 << 30) // big) * big
+    # a matrix that one workgroup holds needs none
+    assert f(7, 128, 128) == f(7, 64, 512) == f(7, 1, 1) == 0
+    # a list of several shapes: groups of it share the workspace, so more
+    # matrices never need less, and small ones add nothing
+    w = ops.muon_workspace_bytes
+    assert w([(200, 300)]) == one and w([(200, 300), (64, 64), (0, 5)]) == one
+    assert w([(200, 300), (300, 200)]) == one + f(1, 300, 200)
+    assert w([]) == 0 and w([(64, 64)] * 40) == 0
+    assert w([(200, 300)] * 40) == 32 * one
 
 
 def test_muon_argument_errors():
     E = _abi
-    need = E.asr_newton_schulz_workspace_bytes(1, 40, 60)
-    good = (0x1000, 0x8000, 0x10000, 0)
-    assert ctypes.sizeof(E.AsrMuonTensor) == 32
+    need = E.asr_newton_schulz_workspace_bytes(1, 400, 600)
+    good = (0x1000, 0x80000, 0x100000, 400, 600, 0, 1.0)
+    assert ctypes.sizeof(E.AsrMuonTensor) == 56
 
-    def f(t=good, rows=40, cols=60, pt=E.ASR_BF16, gt=E.ASR_BF16, lr=0.1, mu=0.9, wd=0.1,
-          factor=1.0, steps=5, coeffs=NS, eps=1e-7, step=1, rounding=E.ASR_ROUND_SR,
-          ws=0x100000, ws_bytes=need):
-        return _status(E.asr_muon_step, [t], rows, cols, pt, gt, lr, mu, 1, wd, factor, steps,
+    def f(t=good, pt=E.ASR_BF16, gt=E.ASR_BF16, lr=0.1, mu=0.9, wd=0.1, steps=5, coeffs=NS,
+          eps=1e-7, step=1, rounding=E.ASR_ROUND_SR, ws=0x1000000, ws_bytes=need):
+        return _status(E.asr_muon_step, E.muon_array([t]), 1, pt, gt, lr, mu, 1, wd, steps,
                        coeffs, eps, step, 0, rounding, ws, ws_bytes, None)
 
-    assert f(rows=-1) == E.ASR_EINVAL
+    def but(i, v):
+        return tuple(v if j == i else x for j, x in enumerate(good))
+
+    assert f(t=but(3, -1)) == E.ASR_EINVAL
+    assert f(t=but(4, 2 ** 20 + 1)) == E.ASR_EINVAL
     assert f(pt=4) == E.ASR_EDTYPE
     assert f(gt=4) == E.ASR_EDTYPE
     for bad in (-0.1, float("inf"), float("nan")):
         assert f(lr=bad) == E.ASR_EINVAL
         assert f(wd=bad) == E.ASR_EINVAL
-        assert f(factor=bad) == E.ASR_EINVAL
+        assert f(t=but(6, bad)) == E.ASR_EINVAL
         assert f(mu=bad) == E.ASR_EINVAL
     assert f(mu=1.0) == E.ASR_EINVAL
     assert f(step=0) == E.ASR_EINVAL
     assert f(step=2 ** 32) == E.ASR_EINVAL
     assert f(rounding=2) == E.ASR_EINVAL
     assert f(steps=0) == E.ASR_EINVAL
+    assert f(eps=-1.0) == E.ASR_EINVAL
     for i in range(3):
-        assert f(t=tuple(0 if j == i else v for j, v in enumerate(good))) == E.ASR_EINVAL
-    assert f(t=(0x1001, *good[1:])) == E.ASR_EALIGN
-    assert f(t=(0x1000, 0x8000, 0x10002, 0)) == E.ASR_EALIGN
+        assert f(t=but(i, 0)) == E.ASR_EINVAL
+    assert f(t=but(0, 0x1001)) == E.ASR_EALIGN
+    assert f(t=but(2, 0x100002)) == E.ASR_EALIGN
     assert f(ws=0) == E.ASR_EWORKSPACE
-    assert f(cols=0, ws=0, ws_bytes=0) == E.ASR_OK
+    assert f(ws=0x1000080) == E.ASR_EWORKSPACE
+    assert f(ws_bytes=need - 1) == E.ASR_EWORKSPACE
+    assert f(t=but(4, 0), ws=0, ws_bytes=0) == E.ASR_OK
 
 
 def test_binding_refusals():
