@@ -119,6 +119,12 @@ _SIGNATURES = {
                                _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
                                _c.c_int64, _c.c_int64, _c.c_int32, _c.c_uint32, _c.c_uint32,
                                _c.c_uint64, _c.c_void_p]),
+    "asr_linear_i8_workspace_bytes": (_c.c_size_t, [_c.c_int64] * 3 + [_c.c_int32]),
+    "asr_linear_i8_forward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 3 + [_c.c_int64] * 3 +
+                              [_c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "asr_linear_i8_backward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 5 + [_c.c_int64] * 3 +
+                               [_c.c_int32, _c.c_uint32, _c.c_uint32, _c.c_uint64, _c.c_void_p,
+                                _c.c_size_t, _c.c_void_p]),
     "asr_newton_schulz_workspace_bytes": (_c.c_size_t, [_c.c_int32, _c.c_int64, _c.c_int64]),
     "asr_newton_schulz": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.POINTER(_c.c_void_p), _c.c_int32,
                                      _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32] +
@@ -285,6 +291,23 @@ def asr_gemm_i8(a, lda, b, ldb, scale_a, scale_b, c, ldc, c_f32, m, n, k, roundi
                 base_index, stream):
     _check(lib().asr_gemm_i8(a, lda, b, ldb, scale_a, scale_b, c, ldc, c_f32, m, n, k, rounding,
                              seed, step, base_index, stream), "asr_gemm_i8")
+
+
+def asr_linear_i8_workspace_bytes(tokens, n, k, backward):
+    return int(lib().asr_linear_i8_workspace_bytes(tokens, n, k, backward))
+
+
+def asr_linear_i8_forward(x, ldx, w, ldw, y, ldy, tokens, n, k, workspace, workspace_bytes,
+                          stream):
+    _check(lib().asr_linear_i8_forward(x, ldx, w, ldw, y, ldy, tokens, n, k, workspace,
+                                       workspace_bytes, stream), "asr_linear_i8_forward")
+
+
+def asr_linear_i8_backward(x, ldx, w, ldw, dy, lddy, dx, lddx, dw, lddw, tokens, n, k, rounding,
+                           seed, step, base_index, workspace, workspace_bytes, stream):
+    _check(lib().asr_linear_i8_backward(x, ldx, w, ldw, dy, lddy, dx, lddx, dw, lddw, tokens, n,
+                                        k, rounding, seed, step, base_index, workspace,
+                                        workspace_bytes, stream), "asr_linear_i8_backward")
 
 
 def asr_newton_schulz_workspace_bytes(n, rows, cols):

@@ -17,37 +17,47 @@ dw. Element (t, n) of dy uses stream position base_index + t*N + n under key
 
 import torch
 
-from . import ops
+from . import _abi, ops
 
 __all__ = ["linear_i8"]
 
 
 class _LinearI8(torch.autograd.Function):
+    """x (T, K) and w (N, K), rows contiguous; the checks are linear_i8's."""
+
     @staticmethod
     def forward(ctx, x, w, grad_rounding, key):
         ctx.save_for_backward(x, w)
         ctx.grad_rounding, ctx.key = grad_rounding, key
-        qx, sx = ops.quantize_i8(x)
-        qw, sw = ops.quantize_i8(w)
-        return ops.gemm_i8(qx, qw, sx, sw)
+        (t, k), n, device = x.shape, w.shape[0], x.device
+        y = torch.empty((t, n), dtype=torch.bfloat16, device=device)
+        need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 0)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        with ops._on(device):
+            _abi.asr_linear_i8_forward(x.data_ptr(), ops._row_stride(x, k), w.data_ptr(),
+                                       ops._row_stride(w, k), y.data_ptr(), n, t, n, k,
+                                       ws.data_ptr(), need, ops._stream(device))
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w = ctx.saved_tensors
-        seed, step, base_index = ctx.key
-        stream = dict(rounding=ctx.grad_rounding, seed=seed, step=step, base_index=base_index)
-        if dy.stride(1) != 1 or dy.stride(0) < dy.shape[1]:
+        (t, k), n, device = x.shape, w.shape[0], x.device
+        if dy.stride(1) != 1 or dy.stride(0) < n:
             dy = dy.contiguous()   # an expanded or transposed gradient
-        dx = dw = None
-        if ctx.needs_input_grad[0]:
-            qd, sd = ops.quantize_i8(dy, **stream)
-            qw, sw = ops.quantize_i8(w, transpose=True)
-            dx = ops.gemm_i8(qd, qw, sd, sw)
-        if ctx.needs_input_grad[1]:
-            qd, sd = ops.quantize_i8(dy, transpose=True, **stream)
-            qx, sx = ops.quantize_i8(x, transpose=True)
-            dw = ops.gemm_i8(qd, qx, sd, sx)
+        want_x, want_w = ctx.needs_input_grad[:2]
+        dx = torch.empty((t, k), dtype=torch.bfloat16, device=device) if want_x else None
+        dw = torch.empty((n, k), dtype=torch.bfloat16, device=device) if want_w else None
+        need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 1)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        with ops._on(device):
+            _abi.asr_linear_i8_backward(
+                x.data_ptr(), ops._row_stride(x, k), w.data_ptr(), ops._row_stride(w, k),
+                dy.data_ptr(), ops._row_stride(dy, n), dx.data_ptr() if want_x else None, k,
+                dw.data_ptr() if want_w else None, k, t, n, k,
+                ops.ROUNDING_CODE[ctx.grad_rounding], *ctx.key, ws.data_ptr(), need,
+                ops._stream(device))
         return dx, dw, None, None
 
 
@@ -68,7 +78,7 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be bfloat16 (got {t.dtype})")
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"{name} must be on a GPU (got {t.device})")
     if x.device != w.device:
         raise ValueError("x and w must be on the same device")
@@ -84,5 +94,7 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
         flat = flat.contiguous()
     if w.numel() and (w.stride(1) != 1 or w.stride(0) < k):
         w = w.contiguous()
+    if key[2] + tokens * n > 1 << 64:
+        raise ValueError("base_index + tokens*N exceeds 2**64")
     y = _LinearI8.apply(flat, w, grad_rounding, key)
     return y.reshape(*x.shape[:-1], n)

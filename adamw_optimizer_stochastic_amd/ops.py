@@ -6,6 +6,7 @@ HIP stream of the tensors' device. All arithmetic runs in the library's
 kernels; there is no CPU path.
 """
 
+import contextlib
 import operator
 
 import numpy as np
@@ -27,8 +28,23 @@ def _require_gpu(t, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+# torch's own short way to the current stream's handle, where it has one
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """A context in which `device` is the current one (no more than a
+    comparison where it is already)."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _uint(name, x, bits):
@@ -324,24 +340,33 @@ def _require_matrix(t, name, dtypes):
     """t is a 2-D GPU tensor of one of `dtypes` whose rows are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {t.device})")
     if t.dtype not in dtypes or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D tensor of " +
                         " or ".join(str(d).replace("torch.", "") for d in dtypes))
-    if t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit stride along its rows")
-    if t.numel() > 0 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows must not overlap")
+    if not t.is_contiguous() and t.numel() > 0:
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit stride along its rows")
+        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{name}: rows must not overlap")
 
 
 def _row_stride(t, least):
     """Row stride of t, or `least` where there is no second row to walk to."""
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else max(least, 1)
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 and cols > 0 else max(least, 1)
 
 
 def _padded16(n):
     return (n + 15) // 16 * 16
+
+
+def _key(seed, step, base_index):
+    if type(seed) is type(step) is type(base_index) is int and 0 <= seed < 1 << 32 \
+            and 0 <= step < 1 << 32 and 0 <= base_index < 1 << 64:
+        return seed, step, base_index
+    return _u32("seed", seed), _u32("step", step), _u64("base_index", base_index)
 
 
 def quantize_i8(x, *, transpose=False, rounding="rn", seed=0, step=0, base_index=0):
@@ -360,21 +385,24 @@ def quantize_i8(x, *, transpose=False, rounding="rn", seed=0, step=0, base_index
     """
     if rounding not in ROUNDING_CODE:
         raise ValueError("rounding must be 'rn' or 'sr'")
-    key = (_u32("seed", seed), _u32("step", step), _u64("base_index", base_index))
+    key = _key(seed, step, base_index)
     _require_matrix(x, "x", (torch.float32, torch.bfloat16))
     rows, cols = x.shape
+    device = x.device
     groups, length = (cols, rows) if transpose else (rows, cols)
     ldq = max(_padded16(length), 16)
-    store = torch.empty((groups, ldq), dtype=torch.int8, device=x.device)
-    scale = torch.empty(groups, dtype=torch.float32, device=x.device)
-    need = _abi.asr_quantize_i8_workspace_bytes(rows, cols, int(transpose))
-    workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    with torch.cuda.device(x.device):
+    store = torch.empty((groups, ldq), dtype=torch.int8, device=device)
+    scale = torch.empty(groups, dtype=torch.float32, device=device)
+    workspace, need = None, 0
+    if transpose:
+        need = _abi.asr_quantize_i8_workspace_bytes(rows, cols, 1)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    with _on(device):
         _abi.asr_quantize_i8(x.data_ptr(), _DTYPE_CODE[x.dtype], _row_stride(x, cols), rows, cols,
-                             int(transpose), store.data_ptr(), ldq, scale.data_ptr(),
+                             1 if transpose else 0, store.data_ptr(), ldq, scale.data_ptr(),
                              ROUNDING_CODE[rounding], *key,
-                             workspace.data_ptr() if need else None, need, _stream(x.device))
-    return store[:, :length], scale
+                             workspace.data_ptr() if need else None, need, _stream(device))
+    return (store if ldq == length else store[:, :length]), scale
 
 
 def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index=0, out=None,
@@ -388,40 +416,44 @@ def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index
     """
     if rounding not in ROUNDING_CODE:
         raise ValueError("rounding must be 'rn' or 'sr'")
-    key = (_u32("seed", seed), _u32("step", step), _u64("base_index", base_index))
-    for t, name in ((a, "a"), (b, "b")):
-        _require_matrix(t, name, (torch.int8,))
-    if a.device != b.device:
+    key = _key(seed, step, base_index)
+    _require_matrix(a, "a", (torch.int8,))
+    _require_matrix(b, "b", (torch.int8,))
+    device = a.device
+    if b.device != device:
         raise ValueError("a and b must be on the same device")
-    if a.shape[1] != b.shape[1]:
+    (m, k), (n, kb) = a.shape, b.shape
+    if k != kb:
         raise ValueError(f"K mismatch: a is {tuple(a.shape)}, b is {tuple(b.shape)}")
-    m, k = a.shape
-    n = b.shape[0]
     for t, size, name in ((scale_a, m, "scale_a"), (scale_b, n, "scale_b")):
         _require_gpu(t, name)
-        if t.dtype != torch.float32 or tuple(t.shape) != (size,) or t.device != a.device:
+        if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != size or t.device != device:
             raise ValueError(f"{name} must be a float32 tensor of shape ({size},) on a's device")
-    if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=a.device)
-    _require_matrix(out, "out", (torch.bfloat16,))
-    if tuple(out.shape) != (m, n) or out.device != a.device:
-        raise ValueError("out must be a bfloat16 (M, N) tensor on a's device")
-    outputs, f32_ptr = [_extent(out, "out")], None
-    if out_f32 is not None:
-        if out_f32.dtype != torch.float32 or tuple(out_f32.shape) != (m, n) \
-                or out_f32.device != a.device or out_f32.stride() != out.stride():
-            raise ValueError("out_f32 must be a float32 (M, N) tensor with out's strides")
-        f32_ptr = out_f32.data_ptr()
-        outputs.append(_extent(out_f32, "out_f32"))
-    check_disjoint(outputs)
-    for o in outputs:
-        for t, name in ((a, "a"), (b, "b"), (scale_a, "scale_a"), (scale_b, "scale_b")):
-            check_disjoint([o, _extent(t, name)])
-    with torch.cuda.device(a.device):
-        _abi.asr_gemm_i8(a.data_ptr(), _row_stride(a, max(_padded16(k), 16)), b.data_ptr(),
-                         _row_stride(b, max(_padded16(k), 16)), scale_a.data_ptr(), scale_b.data_ptr(),
-                         out.data_ptr(), _row_stride(out, n), f32_ptr, m, n, k,
-                         ROUNDING_CODE[rounding], *key, _stream(a.device))
+    f32_ptr = None
+    if out is None and out_f32 is None:
+        out, ldc = torch.empty((m, n), dtype=torch.bfloat16, device=device), max(n, 1)
+    else:   # caller's memory: it may not be what the product reads
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=device)
+        _require_matrix(out, "out", (torch.bfloat16,))
+        if tuple(out.shape) != (m, n) or out.device != device:
+            raise ValueError("out must be a bfloat16 (M, N) tensor on a's device")
+        ldc, outputs = _row_stride(out, n), [_extent(out, "out")]
+        if out_f32 is not None:
+            if out_f32.dtype != torch.float32 or tuple(out_f32.shape) != (m, n) \
+                    or out_f32.device != device or out_f32.stride() != out.stride():
+                raise ValueError("out_f32 must be a float32 (M, N) tensor with out's strides")
+            f32_ptr = out_f32.data_ptr()
+            outputs.append(_extent(out_f32, "out_f32"))
+        check_disjoint(outputs)
+        for o in outputs:
+            for t, name in ((a, "a"), (b, "b"), (scale_a, "scale_a"), (scale_b, "scale_b")):
+                check_disjoint([o, _extent(t, name)])
+    ldk = max(_padded16(k), 16)
+    with _on(device):
+        _abi.asr_gemm_i8(a.data_ptr(), _row_stride(a, ldk), b.data_ptr(), _row_stride(b, ldk),
+                         scale_a.data_ptr(), scale_b.data_ptr(), out.data_ptr(), ldc, f32_ptr, m,
+                         n, k, ROUNDING_CODE[rounding], *key, _stream(device))
     return out
 
 
@@ -460,17 +492,18 @@ def newton_schulz(g, *, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=Non
         raise TypeError("g must be a float32 or bfloat16 tensor of 2 or 3 dimensions")
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
-    _require_gpu(out, "out")
-    if out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != g.device:
-        raise ValueError("out must be bfloat16 with g's shape, on g's device")
-    if out.data_ptr() != g.data_ptr() or g.dtype != torch.bfloat16:
-        check_disjoint([_extent(g, "g"), _extent(out, "out")])
+    else:
+        _require_gpu(out, "out")
+        if out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != g.device:
+            raise ValueError("out must be bfloat16 with g's shape, on g's device")
+        if out.data_ptr() != g.data_ptr() or g.dtype != torch.bfloat16:
+            check_disjoint([_extent(g, "g"), _extent(out, "out")])
     rows, cols = g.shape[-2:]
     n = g.shape[0] if g.dim() == 3 else 1
     need = _abi.asr_newton_schulz_workspace_bytes(n, rows, cols)
     workspace = _ns_workspace(workspace, need, g.device)
     size, size_out = rows * cols * g.element_size(), rows * cols * 2
-    with torch.cuda.device(g.device):
+    with _on(g.device):
         _abi.asr_newton_schulz([g.data_ptr() + k * size for k in range(n)],
                                [out.data_ptr() + k * size_out for k in range(n)], rows, cols,
                                _DTYPE_CODE[g.dtype], operator.index(steps), *coefficients,
@@ -544,7 +577,7 @@ def muon_step(params, grads, momenta, base_indices, *, lr, momentum=0.95, nester
     groups = {key: (_abi.muon_array(ts), len(ts)) for key, ts in groups.items()}
     need = max(_abi.asr_muon_workspace_bytes(arr, k) for arr, k in groups.values())
     workspace = _ns_workspace(workspace, need, device)
-    with torch.cuda.device(device):
+    with _on(device):
         for (pt, gt), (arr, k) in groups.items():
             _abi.asr_muon_step(arr, k, _DTYPE_CODE[pt], _DTYPE_CODE[gt], float(lr),
                                float(momentum), int(bool(nesterov)), float(weight_decay),

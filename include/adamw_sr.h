@@ -284,7 +284,8 @@ int asr_gemm_bf16(const uint16_t* a, int64_t lda, const uint16_t* b,
  * Requirements: 0 <= rows, cols < 2**31; ldx >= cols; ldq a multiple of 16, at
  * least the group's length; q 16-byte aligned; x and scale aligned to their
  * elements (x's rows starting on 16-byte addresses take the vector path);
- * rows <= 128 * 65535 in the transposed form; base_index + rows*cols <= 2**64;
+ * rows < 2**30, and at most 2**30 tiles of 128 rows x 64 columns in the
+ * transposed form; base_index + rows*cols <= 2**64;
  * no buffer overlaps another. workspace: asr_quantize_i8_workspace_bytes
  * bytes of device memory, 16-byte aligned (0 bytes, NULL allowed, unless
  * transpose), as for asr_adamw_step.
@@ -323,6 +324,42 @@ int asr_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb,
                 int64_t ldc, float* c_f32, int64_t m, int64_t n, int64_t k,
                 int32_t rounding, uint32_t seed, uint32_t step,
                 uint64_t base_index, void* stream);
+
+/*
+ * A linear layer's three products in 8-bit integers, from bf16 matrices:
+ *   forward:   y  = x w^T     x (tokens x k), w (n x k), y (tokens x n)
+ *   backward:  dx = dy w      (NULL dx: not wanted; w is then not read)
+ *              dw = dy^T x    (NULL dw: not wanted; x is then not read)
+ * Each is asr_gemm_i8 (rounded to nearest) of the codes asr_quantize_i8 gives:
+ * of the rows of x and w; of the rows of dy and the columns of w; of the
+ * columns of dy and x. x and w are rounded to nearest, dy by `rounding`:
+ * ASR_ROUND_SR (key (seed, step), element (t, j) at base_index + t*n + j, the
+ * same bits in both products) or ASR_ROUND_RN. Results are those of the
+ * separate calls bit for bit; what one matrix's two forms share is read and
+ * drawn once.
+ * Requirements: 0 <= tokens, n, k < 2**17; row strides (in elements) at least
+ * the rows' lengths; matrices aligned to 2 bytes (rows starting on 16-byte
+ * addresses take the vector paths); base_index + tokens*n <= 2**64; no output
+ * overlaps an input. workspace: asr_linear_i8_workspace_bytes(tokens, n, k,
+ * backward) bytes of device memory, 256-byte aligned, overwritten in stream
+ * order (the codes: about one byte an element of every matrix read).
+ * Errors: ASR_EINVAL, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Run on `stream`;
+ * do not synchronize.
+ */
+size_t asr_linear_i8_workspace_bytes(int64_t tokens, int64_t n, int64_t k,
+                                     int32_t backward);
+int asr_linear_i8_forward(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                          int64_t ldw, uint16_t* y, int64_t ldy,
+                          int64_t tokens, int64_t n, int64_t k,
+                          void* workspace, size_t workspace_bytes,
+                          void* stream);
+int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                           int64_t ldw, const uint16_t* dy, int64_t lddy,
+                           uint16_t* dx, int64_t lddx, uint16_t* dw,
+                           int64_t lddw, int64_t tokens, int64_t n, int64_t k,
+                           int32_t rounding, uint32_t seed, uint32_t step,
+                           uint64_t base_index, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /*
  * Orthogonalisation of n matrices of one shape by Newton-Schulz products:

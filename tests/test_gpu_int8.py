@@ -269,6 +269,73 @@ def test_linear_gradient_of_a_sum_and_shapes():
                   <= 1.0001 * (err + 2.0 ** -8 * (np.abs(dw) + err)))
 
 
+@pytest.mark.parametrize("want", ["x", "w"])
+@pytest.mark.parametrize("shape", [(33, 70, 50), (129, 4500, 40), (260, 130, 4200)])
+def test_linear_one_gradient(shape, want):
+    """Only dx or only dw, more strips of columns than a tile joins itself,
+    rows with a stride; the same bits as with both."""
+    t, n, k = shape
+    announce("linear_i8 one gradient", shape, want)
+    rng = np.random.default_rng(shape)
+    x, xt = _bf16_of(rng.standard_normal((t, k)))
+    w, wt = _bf16_of(rng.standard_normal((n, k)))
+    dy, dyt = _bf16_of(rng.standard_normal((t, n)))
+    wide = torch.zeros((t, n + 3), dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:n + 2] = dyt
+
+    def grads(need_x, need_w, d):
+        a, b = xt.detach().requires_grad_(need_x), wt.detach().requires_grad_(need_w)
+        y = linear_i8(a, b, seed=5, step=6, base_index=7)
+        return torch.autograd.grad(y, [v for v, r in ((a, need_x), (b, need_w)) if r], d)
+
+    dx, dw = grads(True, True, dyt)
+    got = grads(want == "x", want == "w", wide[:, 2:n + 2])[0]
+    torch.cuda.synchronize()
+    both = dx if want == "x" else dw
+    assert torch.equal(got.view(torch.int16), both.view(torch.int16))
+    qd = o8.quantize(dy, want == "w", "sr", 5, 6, 7)
+    q2 = o8.quantize(w if want == "x" else x, True)
+    ref = oracle.gemm_round(o8.gemm_f32(qd[0], q2[0], qd[1], q2[1]), "rn")
+    assert_bits_equal(to_host(got).reshape(-1), ref.reshape(-1), want)
+
+
+def test_linear_empty_sums():
+    announce("linear_i8 empty")
+    for t, n, k in ((0, 4, 8), (4, 0, 8), (4, 8, 0), (0, 0, 0)):
+        x = torch.ones((t, k), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+        w = torch.ones((n, k), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+        y = linear_i8(x, w)
+        assert y.shape == (t, n) and not bool(y.any())
+        dx, dw = torch.autograd.grad(y, (x, w), torch.ones_like(y))
+        torch.cuda.synchronize()
+        assert dx.shape == x.shape and dw.shape == w.shape
+        assert not bool(dx.any()) and not bool(dw.any())
+
+
+def test_codes_next_to_borders():
+    """Every code border and its neighbours, for scales of every size: what the
+    short way decides and what it leaves to the exact one meet here."""
+    announce("quantize borders")
+    rng = np.random.default_rng(8)
+    rows = []
+    for amax in (127.0, 1.0, 3.7e-3, 1e30, 1e-20, 2.0 ** -100, 2.0 ** -119, 0.9999999, 100.0):
+        s = float(o8.scale_of(np.float32(amax)))
+        v = (np.arange(0, 255) * 0.5 * s).astype(np.float32)
+        v = np.concatenate([v, np.nextafter(v, np.float32(0)), np.nextafter(v, np.float32(1e38)),
+                            (v * (1 + 1e-5)).astype(np.float32), (v * (1 - 1e-4)).astype(np.float32)])
+        v = np.minimum(v, np.float32(amax)) * rng.choice([-1, 1], v.size).astype(np.float32)
+        v[rng.integers(0, v.size)] = amax
+        rows.append(v)
+    x = np.stack(rows).astype(np.float32)
+    for transpose in (False, True):
+        y = np.ascontiguousarray(x.T) if transpose else x
+        _check_codes(y, f32_tensor(y), transpose=transpose)
+        for step in range(4):
+            _check_codes(y, f32_tensor(y), transpose=transpose, rounding="sr", seed=2, step=step)
+    small = np.where(rng.random((64, 512)) < 0.5, 2.0 ** -17, 1.0).astype(np.float32) * 127
+    _check_codes(small, f32_tensor(small), rounding="sr", seed=1, step=1)
+
+
 def test_other_stream_and_capture():
     """The quantiser and product on a side stream, then captured and replayed."""
     announce("int8 capture")

@@ -48,8 +48,9 @@ def test_quantize_argument_errors():
     assert need >= 60 * 4 and E.asr_quantize_i8_workspace_bytes(8, 60, 0) == 0
     assert q(transpose=1, ldq=16, ws=0x10000, ws_bytes=need - 1) == E.ASR_EWORKSPACE
     assert q(transpose=1, ldq=16, ws=0x10008, ws_bytes=need) == E.ASR_EWORKSPACE
-    assert q(transpose=1, rows=128 * 65535 + 1, ldq=128 * 65536, ws=0x10000,
-             ws_bytes=1 << 40) == E.ASR_EINVAL
+    assert q(transpose=1, rows=2 ** 30, ldq=2 ** 30, ws=0x10000, ws_bytes=1 << 50) == E.ASR_EINVAL
+    assert q(transpose=1, rows=2 ** 29, cols=2 ** 20, ldx=2 ** 20, ldq=2 ** 29, ws=0x10000,
+             ws_bytes=1 << 50) == E.ASR_EINVAL
     assert q(rows=0, x=0, q=0, scale=0) == E.ASR_OK
     assert q(cols=0, transpose=1, x=0, q=0, scale=0) == E.ASR_OK
 
@@ -101,3 +102,47 @@ def test_binding_refuses_what_is_not_on_a_gpu():
         linear_i8(x, w)
     with pytest.raises(ValueError, match="seed"):
         ops.quantize_i8(x, seed=2 ** 32)
+
+
+def test_linear_argument_errors():
+    E = _abi
+    need = [E.asr_linear_i8_workspace_bytes(40, 24, 56, b) for b in (0, 1)]
+    assert need[0] >= (40 + 24) * 64 and need[1] >= 40 * 32 + 24 * 48 + 56 * 32 + 56 * 48
+    for bad in ((-1, 4, 4), (4, 2 ** 17, 4), (0, 4, 4)):
+        assert E.asr_linear_i8_workspace_bytes(*bad, 0) == 0
+
+    def fwd(x=0x1000, ldx=56, w=0x8000, ldw=56, y=0x10000, ldy=24, t=40, n=24, k=56, ws=0x100000,
+            ws_bytes=need[0]):
+        return _status(E.asr_linear_i8_forward, x, ldx, w, ldw, y, ldy, t, n, k, ws, ws_bytes,
+                       None)
+
+    assert fwd(t=-1) == E.ASR_EINVAL
+    assert fwd(n=2 ** 17) == E.ASR_EINVAL
+    assert fwd(k=2 ** 17) == E.ASR_EINVAL
+    for name in ("x", "w", "y"):
+        assert fwd(**{name: 0}) == E.ASR_EINVAL
+        assert fwd(**{name: 0x1001}) == E.ASR_EALIGN
+    for name, ld in (("ldx", 55), ("ldw", 55), ("ldy", 23)):
+        assert fwd(**{name: ld}) == E.ASR_EINVAL
+    assert fwd(ws=0) == E.ASR_EWORKSPACE
+    assert fwd(ws=0x100080) == E.ASR_EWORKSPACE
+    assert fwd(ws_bytes=need[0] - 1) == E.ASR_EWORKSPACE
+    assert fwd(t=0, x=0, y=0, ws=0) == E.ASR_OK
+
+    def bwd(x=0x1000, w=0x8000, dy=0x10000, lddy=24, dx=0x20000, dw=0x30000, t=40, n=24, k=56,
+            rounding=E.ASR_ROUND_SR, base=0, ws=0x100000, ws_bytes=need[1]):
+        return _status(E.asr_linear_i8_backward, x, 56, w, 56, dy, lddy, dx, 56, dw, 56, t, n, k,
+                       rounding, 1, 2, base, ws, ws_bytes, None)
+
+    assert bwd(t=2 ** 17) == E.ASR_EINVAL
+    assert bwd(rounding=2) == E.ASR_EINVAL
+    for name in ("x", "w", "dy"):
+        assert bwd(**{name: 0}) == E.ASR_EINVAL
+        assert bwd(**{name: 0x1001}) == E.ASR_EALIGN
+    assert bwd(dx=0x20001) == E.ASR_EALIGN
+    assert bwd(dw=0x30001) == E.ASR_EALIGN
+    assert bwd(lddy=23) == E.ASR_EINVAL
+    assert bwd(base=2 ** 64 - 40 * 24 + 1) == E.ASR_EINVAL
+    assert bwd(ws=0) == E.ASR_EWORKSPACE
+    assert bwd(ws_bytes=need[1] - 1) == E.ASR_EWORKSPACE
+    assert bwd(dx=0, dw=0, ws=0) == E.ASR_OK
