@@ -87,9 +87,9 @@ struct Layout {
     b = a + square;
     parts = b + square;
     bytes = parts + kMaxParts * 8;
-    int32_t half = 0, whole = 0;  // floor(log2(s t) / 2), floor(log2 s)
-    while (int64_t{4} << (2 * half) <= static_cast<int64_t>(s) * t) ++half;
-    while (2 << whole <= s) ++whole;
+    // floor(log2(s t) / 2) and floor(log2 s)
+    const int32_t half = (63 - __builtin_clzll(static_cast<uint64_t>(s) * static_cast<uint64_t>(t))) / 2;
+    const int32_t whole = 31 - __builtin_clz(static_cast<uint32_t>(s));
     sx = static_cast<float>(1 << (half < 14 ? half : 14));
     sa = static_cast<float>(1 << (whole < 14 ? whole : 14));
   }
@@ -113,6 +113,7 @@ struct PrepareArgs {
 
 // The matrix that workgroup b belongs to.
 __device__ __forceinline__ int matrix_of(const Desc* d, int count, uint32_t b) {
+  if (count == 1) return 0;
   const int lane = threadIdx.x & 63;
   const bool reached = lane < count && d[lane < count ? lane : 0].first <= b;
   return __builtin_amdgcn_readfirstlane(__popcll(__ballot(reached)) - 1);
@@ -281,6 +282,20 @@ struct ProductArgs {
   OutArgs out;
 };
 
+// Of a lane's two f16 values v0, v1 of one row m in neighbouring columns n, n +
+// 1, and its neighbour lane's (row m ^ 1): an even lane gets column n of rows m,
+// m + 1, an odd one column n + 1 of rows m - 1, m -- a whole LDS word of the
+// turned tile instead of two halves.
+__device__ __forceinline__ uint32_t turn_pair(float v0, float v1, uint32_t sel) {
+  const uint32_t mine = __builtin_bit_cast(uint32_t, f16x2{static_cast<_Float16>(v0), static_cast<_Float16>(v1)});
+  const uint32_t other = static_cast<uint32_t>(
+      __builtin_amdgcn_mov_dpp(static_cast<int>(mine), 0xB1, 0xF, 0xF, true));  // quad_perm 1 0 3 2
+  return __builtin_amdgcn_perm(other, mine, sel);
+}
+__device__ __forceinline__ uint32_t turn_selector(uint32_t lane) {
+  return lane & 1u ? 0x03020706u : 0x05040100u;
+}
+
 // Tile t of the lower triangle, rows in order.
 __device__ __forceinline__ void triangle_tile(uint32_t t, uint32_t& tm, uint32_t& tn) {
   uint32_t r = static_cast<uint32_t>((__builtin_sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
@@ -346,26 +361,6 @@ __device__ __forceinline__ void store_out(const OutArgs& out, const Desc& d, int
   else asr::store_range_bf16<V>(p, at, 0, n, h);
 }
 
-// One element of O.
-template <int OUT>
-__device__ __forceinline__ void store_out1(const OutArgs& out, const Desc& d, int64_t at, float o) {
-  if constexpr (OUT == kOutBf16) {
-    static_cast<uint16_t*>(d.p)[at] = static_cast<uint16_t>(asr::round_rn(__float_as_uint(o)));
-  } else if constexpr (OUT == kOutWeightF32) {
-    float* p = static_cast<float*>(d.p) + at;
-    *p = *p * out.decay - d.eta * o;
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(d.p) + at;
-    const uint32_t y = __float_as_uint(asr::bf16_bits_to_f32(*p) * out.decay - d.eta * o);
-    uint32_t r16[4] = {};
-    const uint64_t pos = d.base + static_cast<uint64_t>(at);
-    if constexpr (OUT == kOutWeightBf16Sr) asr_mfma::random4(pos & ~uint64_t{3}, true, out.seed, out.step, r16);
-    const uint32_t e = static_cast<uint32_t>(pos) & 3u;
-    const uint32_t r = e == 0 ? r16[0] : e == 1 ? r16[1] : e == 2 ? r16[2] : r16[3];
-    *p = static_cast<uint16_t>(OUT == kOutWeightBf16Sr ? asr::round_sr(y, r) : asr::round_rn(y));
-  }
-}
-
 template <typename T, int MODE, int OUT>
 __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs args) {
   using E = asr_mfma::ElemF16;
@@ -423,6 +418,7 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
   constexpr int kLd = T::BM + 8;
   _Float16* tile = reinterpret_cast<_Float16*>(smem);
   const bool turn = MODE == kUpdate || (kSymmetric && tm != tn);
+  const uint32_t turn_sel = turn_selector(lane);
   if constexpr (MODE != kFinal) __syncthreads();  // every wave has read the last K tile
   static_for<T::kFragM>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
@@ -470,9 +466,15 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float x = live && n + e < n_all ? v[e] : 0.0f;  // the padding reads as zeros
+            v[e] = x;
             hi[e] = static_cast<_Float16>(x);
             lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
-            if (turn) tile[(nt + e) * kLd + mt] = hi[e];
+          }
+          if (turn) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+              *reinterpret_cast<uint32_t*>(tile + (nt + e + (lane & 1u)) * kLd + (mt & ~1u)) =
+                  turn_pair(v[e], v[e + 1], turn_sel);
           }
           if (inside) {
             *reinterpret_cast<f16x8*>(d_out + m * ld_d + n) = hi;
@@ -505,8 +507,8 @@ using Tiny = asr_mfma::Tile<64, 64, 32, 32, 4>;
 // ------------------------------------------------------- one workgroup
 // All steps of a small matrix in one workgroup of 16 waves: X stays in f32 in
 // the accumulator registers (32 x 32 blocks, kBlocks of them a wave), its f16
-// copy lies in LDS both ways, and a X + B X accumulates onto a X. 5 launches'
-// worth of latency a step becomes three barriers.
+// copy lies in LDS both ways, and a X + B X accumulates onto a X. Three
+// launches a step become four barriers.
 constexpr int kSmallWaves = 16;
 constexpr int kSmallBlocks = 3;
 constexpr int kSmallLds = 159 * 1024;
@@ -514,7 +516,7 @@ constexpr int kSmallLds = 159 * 1024;
 __host__ __device__ inline bool is_small(int32_t rows, int32_t cols) {
   const int64_t s = up(rows < cols ? rows : cols, 32), t = up(rows < cols ? cols : rows, 32);
   return s <= 128 && (s / 32) * (t / 32) <= kSmallWaves * kSmallBlocks &&
-         2 * (s * (t + 8) + t * (s + 8) + 2 * s * (s + 8)) <= kSmallLds;
+         2 * (s * (t + 8) + t * (s + 8) + 2 * s * (s + 8)) <= kSmallLds && 4 * s * (t + 4) <= kSmallLds;
 }
 
 struct SmallArgs {
@@ -522,14 +524,9 @@ struct SmallArgs {
   double eps;
   float a, b, c, momentum;
   int32_t nesterov, steps;
+  uint32_t vec;  // gradient and momentum start on 16-byte addresses
   OutArgs out;
 };
-
-template <typename G>
-__device__ __forceinline__ float one_value(const G* p, uint32_t i) {
-  if constexpr (sizeof(G) == 4) return p[i];
-  else return asr::bf16_bits_to_f32(p[i]);
-}
 
 // A value the compiler has to take as new: what is computed from it is not
 // kept in registers from one part of the kernel to the next (the index
@@ -566,34 +563,43 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_matrix(SmallArgs args)
       if (at < sb * tb) f(xr[decltype(bc)::value], at / tb, at % tb);
     });
   };
-  // (element (m, n) of X in the matrix's own order; at most 2**16 elements)
-  const int32_t by_m = l.wide ? t : 1, by_n = l.wide ? 1 : s;
+  // U comes in, and O goes out, 8 elements of a thread at a time in memory's
+  // order, through an f32 copy of X in the LDS (that the f16 ones then take).
+  float* stage = reinterpret_cast<float*>(smem);
+  const int32_t ld_f = tb * 32 + 4;
+  const int32_t cols = d.cols, numel = d.rows * cols;
+  const bool vec = args.vec && cols % 8 == 0;
+  // f(first element, how many, row and column of element e of the run)
+  auto each_run = [&](auto&& f) {
+    for (int32_t i = static_cast<int32_t>(threadIdx.x) * 8; i < numel; i += kSmallWaves * 64 * 8) f(i, min(8, numel - i));
+  };
+  auto stage_at = [&](int32_t i) {
+    const int32_t r = i / cols, c = i - r * cols;
+    return l.wide ? r * ld_f + c : c * ld_f + r;
+  };
   double sum = 0.0;
-  each_block([&](E::acc& xb, int32_t i, int32_t j) {
-    const int32_t m = i * 32 + row;
-    static_for<4>([&](auto qc) {
-      constexpr int q = decltype(qc)::value;
-      const int32_t n = j * 32 + 8 * q + 4 * half;
-      float gx[4] = {}, mx[4] = {}, u[4];
-      const uint32_t at = static_cast<uint32_t>(m * by_m + n * by_n);
+  each_run([&](int32_t i, int32_t n) {
+    float gx[8], mx[8] = {}, u[8];
+    if (vec) {
+      asr::load_vec<false, 8>(g + i, gx);
+      if constexpr (MUON) asr::load_vec<false, 8>(d.m + i, mx);
+    } else {
+      asr::load_range<8>(g, i, 0, n, gx);
+      if constexpr (MUON) asr::load_range<8>(d.m, i, 0, n, mx);
+    }
+    momentum_update<MUON>(gx, mx, args.momentum, args.nesterov, true, u);
+    if constexpr (MUON) {
+      if (vec) asr::store_vec<false, 8>(d.m + i, mx);
+      else asr::store_range<8>(d.m, i, 0, n, mx);
+    }
+    const int32_t at = stage_at(i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (m < s && n + e < t) {
-          gx[e] = one_value(g, at + e * by_n);
-          if constexpr (MUON) mx[e] = d.m[at + e * by_n];
-        }
+    for (int e = 0; e < 8; ++e) {
+      if (e < n) {
+        sum += static_cast<double>(u[e]) * static_cast<double>(u[e]);
+        stage[vec ? (l.wide ? at + e : at + e * ld_f) : stage_at(i + e)] = u[e];
       }
-      momentum_update<MUON>(gx, mx, args.momentum, args.nesterov, true, u);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = m < s && n + e < t;
-        if constexpr (MUON) {
-          if (in) d.m[at + e * by_n] = mx[e];
-        }
-        xb[4 * q + e] = in ? u[e] : 0.0f;
-        sum += static_cast<double>(xb[4 * q + e]) * static_cast<double>(xb[4 * q + e]);
-      }
-    });
+    }
   });
   const double norm = __builtin_sqrt(group_sum<kSmallWaves * 64>(sum, lds));
   const double factor = static_cast<double>(l.sx) / (norm + args.eps);
@@ -601,15 +607,20 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_matrix(SmallArgs args)
     const int32_t m = i * 32 + row, n = j * 32 + 4 * half;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      // (what lies past the matrix stays zero whatever the factor is)
+      // (what lies past the matrix is zero whatever the factor is)
       const bool in = m < s && n + 8 * (r / 4) + r % 4 < t;
-      xb[r] = in ? static_cast<float>(static_cast<double>(xb[r]) * factor) : 0.0f;
+      const float u = in ? stage[m * ld_f + n + 8 * (r / 4) + r % 4] : 0.0f;
+      xb[r] = in ? static_cast<float>(static_cast<double>(u) * factor) : 0.0f;
     }
   });
+  __syncthreads();  // the f16 copies take the LDS over
 
+  const uint32_t turn_sel = turn_selector(static_cast<uint32_t>(lane));
   const float gram_scale = l.sa / (l.sx * l.sx), inv_sa = 1.0f / l.sa;
-  const bool squares = wave < sb * sb;  // this wave's block of A and B
-  const int32_t si = wave / sb, sj = wave % sb;
+  // this wave's block of A and B, in the lower triangle: the LDS reads of the
+  // operands are what bounds a step
+  const bool squares = wave < sb * (sb + 1) / 2;
+  const int32_t si = wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3, sj = wave - si * (si + 1) / 2;
   auto frag = [&](const _Float16* base, int32_t ld, int32_t block, int32_t kk) {
     return *reinterpret_cast<const f16x8*>(base + (block * 32 + row) * ld + 16 * kk + 8 * half);
   };
@@ -627,36 +638,47 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_matrix(SmallArgs args)
     *reinterpret_cast<f16x4*>(at) = f16x4{static_cast<_Float16>(v0), static_cast<_Float16>(v1),
                                           static_cast<_Float16>(v2), static_cast<_Float16>(v3)};
   };
+  // block (si, sj) of a symmetric matrix, and its mirror
+  auto put_square = [&](_Float16* base, const E::acc& v) {
+    _Float16* to = base + (si * 32 + row) * ld_y + sj * 32 + 4 * half;
+    _Float16* mirror = base + (sj * 32 + 4 * half + (lane & 1)) * ld_y + si * 32 + (row & ~1);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      put4(to + 8 * q, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      if (si != sj) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+          *reinterpret_cast<uint32_t*>(mirror + (8 * q + e) * ld_y) = turn_pair(v[4 * q + e], v[4 * q + e + 1], turn_sel);
+      }
+    }
+  };
   for (int step = 0; step < args.steps; ++step) {
     each_block([&](E::acc& xb, int32_t i, int32_t j) {
       _Float16* to_x = x + (i * 32 + row) * ld_x + j * 32 + 4 * half;
-      _Float16* to_y = y + (j * 32 + 4 * half) * ld_y + i * 32 + row;
+      _Float16* to_y = y + (j * 32 + 4 * half + (lane & 1)) * ld_y + i * 32 + (row & ~1);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         put4(to_x + 8 * q, xb[4 * q], xb[4 * q + 1], xb[4 * q + 2], xb[4 * q + 3]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) to_y[(8 * q + e) * ld_y] = static_cast<_Float16>(xb[4 * q + e]);
+        for (int e = 0; e < 4; e += 2)
+          *reinterpret_cast<uint32_t*>(to_y + (8 * q + e) * ld_y) = turn_pair(xb[4 * q + e], xb[4 * q + e + 1], turn_sel);
       }
     });
     __syncthreads();
     E::acc aa = {};
     if (squares) {
 dot(aa, x, ld_x, sj, x, ld_x, si, tb);
-      _Float16* to = gram + (si * 32 + row) * ld_y + sj * 32 + 4 * half;
 #pragma unroll
       for (int r = 0; r < 16; ++r) aa[r] *= gram_scale;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) put4(to + 8 * q, aa[4 * q], aa[4 * q + 1], aa[4 * q + 2], aa[4 * q + 3]);
+      put_square(gram, aa);
     }
     __syncthreads();
     if (squares) {
       E::acc bb = {};
 dot(bb, gram, ld_y, sj, gram, ld_y, si, sb);
-      _Float16* to = poly + (si * 32 + row) * ld_y + sj * 32 + 4 * half;
 #pragma unroll
       for (int r = 0; r < 16; ++r) bb[r] = args.b * aa[r] + args.c * inv_sa * bb[r];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) put4(to + 8 * q, bb[4 * q], bb[4 * q + 1], bb[4 * q + 2], bb[4 * q + 3]);
+      put_square(poly, bb);
     }
     __syncthreads();
     each_block([&](E::acc& xb, int32_t i, int32_t j) {
@@ -671,23 +693,20 @@ dot(xb, y, ld_y, j, poly, ld_y, i, sb);
 
   const float inv_sx = 1.0f / l.sx;
   each_block([&](E::acc& xb, int32_t i, int32_t j) {
-    const int32_t m = i * 32 + row;
-    if (m >= s) return;
-    static_for<4>([&](auto qc) {
-      constexpr int q = decltype(qc)::value;
-      const int32_t n = j * 32 + 8 * q + 4 * half;
-      const int count = min(4, t - n);
-      if (count <= 0) return;
-      const float o[4] = {xb[4 * q] * inv_sx, xb[4 * q + 1] * inv_sx, xb[4 * q + 2] * inv_sx,
-                          xb[4 * q + 3] * inv_sx};
-      if (l.wide) {
-        store_out<OUT, 4>(args.out, d, m * t + n, count, args.out.vec8 && count == 4, o);
-      } else {
+    float* to = stage + (i * 32 + row) * ld_f + j * 32 + 4 * half;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < count) store_out1<OUT>(args.out, d, (n + e) * s + m, o[e]);
-      }
-    });
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<asr::f32x4*>(to + 8 * q) = asr::f32x4{xb[4 * q] * inv_sx, xb[4 * q + 1] * inv_sx,
+                                                              xb[4 * q + 2] * inv_sx, xb[4 * q + 3] * inv_sx};
+  });
+  __syncthreads();
+  each_run([&](int32_t i, int32_t n) {
+    float o[8] = {};
+    const int32_t at = stage_at(i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) o[e] = stage[vec ? (l.wide ? at + e : at + e * ld_f) : stage_at(i + e)];
+    store_out<OUT, 8>(args.out, d, i, n, args.out.vec8 && n == 8, o);
   });
 }
 
@@ -841,7 +860,11 @@ hipError_t run_small(const Settings& st, const Desc* const* list, int32_t n) {
   a.out = st.out;
   for (int32_t k0 = 0; k0 < n; k0 += kMaxBatch) {
     const int32_t count = std::min(kMaxBatch, n - k0);
-    for (int32_t k = 0; k < count; ++k) a.d[k] = *list[k0 + k];
+    a.vec = 1;
+    for (int32_t k = 0; k < count; ++k) {
+      a.d[k] = *list[k0 + k];
+      a.vec = a.vec && aligned_to(a.d[k].g, 16) && (!MUON || aligned_to(a.d[k].m, 16));
+    }
     const hipError_t e = launch(&small_matrix<G, MUON, OUT>, static_cast<uint32_t>(count),
                                 kSmallWaves * 64, &a, st.stream);
     if (e != hipSuccess) return e;
