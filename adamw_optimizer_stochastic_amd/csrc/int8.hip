@@ -464,7 +464,7 @@ struct GemmArgs {
   uint32_t tiles_m, tiles_n;
   uint32_t seed, step;
   uint32_t vec4;   // runs of 4 outputs start on 8-byte (f32: 16-byte) addresses
-  uint32_t vec16;  // runs of 8 outputs start on 16-byte addresses
+  uint32_t vec16;  // runs of 8 outputs start on 16-byte addresses, also f32 ones
   uint32_t pos4;   // runs of 4 outputs start on stream positions divisible by 4
 };
 
@@ -484,6 +484,7 @@ using Tiny = asr_mfma::Tile<64, 64, 32, 32, 4>;
 template <typename T, int ROUND, bool REST>
 __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void gemm_i8(GemmArgs args) {
   using E = asr_mfma::ElemI8;
+  static_assert(asr_mfma::Rows<T>::kBytes <= T::kLoopLds, "the slices lie in the ring");
   __shared__ __align__(1024) unsigned char smem[T::kLoopLds];
   uint32_t tm, tn;
   asr_mfma::grouped_tile(asr_mfma::xcd_order(blockIdx.x, args.tiles_m * args.tiles_n),
@@ -503,7 +504,7 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void gemm_i8(GemmArgs ar
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t wm = wave / T::kWavesN, wn = wave % T::kWavesN;
-  const uint32_t row = lane & 31u, half = lane >> 5;
+  [[maybe_unused]] const uint32_t row = lane & 31u, half = lane >> 5;
 
   // The last K % 16 codes of every row, byte by byte (what lies behind a
   // row's end is not read); lanes of the upper half hold zeros.
@@ -532,81 +533,50 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void gemm_i8(GemmArgs ar
     }
   }
 
-  // Each lane scales and rounds its own runs of 4 columns (one Philox call a
-  // run, as the keying lays them out); v_permlane32_swap then pairs lanes l
-  // and l + 32 into runs of 8 for one 16-byte store. Both lanes of a pair
-  // take that store only when all 16 columns of the pair lie in the row.
-  static_for<T::kFragN>([&](auto jc) {
-    constexpr int j = decltype(jc)::value;
-    const int64_t nj = n0 + wn * T::WN + j * 32;
-    float sb[4][4];
+  // Scaled, rounded and stored in runs of 8 columns, whole lines at a time.
+  using Rows = asr_mfma::Rows<T>;
+  static_assert(32 % Rows::kGroups == 0, "a lane's columns are those of every pass");
+  __syncthreads();  // the last K tile is read
+  uint32_t* slice = reinterpret_cast<uint32_t*>(smem) + wave * (Rows::kSliceBytes / 4);
+  uint32_t row0, col;
+  Rows::place(0, lane, row0, col);
+  const int64_t n = n0 + wn * T::WN + col;
+  const int count = static_cast<int>(max(int64_t{0}, min(int64_t{8}, args.n - n)));
+  float sb[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+  for (int e = 0; e < 8; ++e) sb[e] = args.sb[min(n + e, static_cast<int64_t>(args.n - 1))];
+  static_for<T::kFragM>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    Rows::put(slice, acc[i], lane);
+    static_for<Rows::kPasses>([&](auto pc) {
+      constexpr int p = decltype(pc)::value;
+      uint32_t r, same_col, raw[8];
+      Rows::place(p, lane, r, same_col);
+      Rows::get(slice, r, col, raw);
+      const int64_t m = m0 + wm * T::WM + i * 32 + r;
+      if (m >= args.m || count == 0) return;
+      const float sa = args.sa[m];
+      uint32_t r0[4] = {}, r1[4] = {}, h[8];
+      if constexpr (ROUND == ASR_ROUND_SR) {
+        const uint64_t pos = args.base_index + static_cast<uint64_t>(m) * static_cast<uint64_t>(args.n) +
+                             static_cast<uint64_t>(n);
+        asr_mfma::random4(pos, args.pos4 != 0, args.seed, args.step, r0);
+        asr_mfma::random4(pos + 4, args.pos4 != 0, args.seed, args.step, r1);
+      }
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sb[q][e] = args.sb[min(nj + 8 * q + 4 * half + e, static_cast<int64_t>(args.n - 1))];
-    static_for<T::kFragM>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      const int64_t m = m0 + wm * T::WM + i * 32 + row;
-      const float sa = args.sa[min(m, static_cast<int64_t>(args.m - 1))];
-      static_for<2>([&](auto pc) {
-        constexpr int p = decltype(pc)::value;
-        uint32_t w[2][2];
-        float xs[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t n = nj + 16 * p + 8 * h + 4 * half;
-          uint32_t r16[4] = {};
-          if constexpr (ROUND == ASR_ROUND_SR)
-            asr_mfma::random4(args.base_index + static_cast<uint64_t>(m) * static_cast<uint64_t>(args.n) +
-                                  static_cast<uint64_t>(n),
-                              args.pos4 != 0, args.seed, args.step, r16);
-          uint32_t u[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            xs[h][e] = (static_cast<float>(acc[i][j][8 * p + 4 * h + e]) * sa) * sb[2 * p + h][e];
-            u[e] = round_one<ROUND>(xs[h][e], r16[e]);
-          }
-          w[h][0] = u[0] | (u[1] << 16);
-          w[h][1] = u[2] | (u[3] << 16);
-        }
-        const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
-        const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
-        const int64_t n16 = nj + 16 * p;
-        if (m < args.m) {
-          if (args.vec16 && n16 + 16 <= args.n) {
-            *reinterpret_cast<asr::u32x4*>(args.c + m * args.ldc + n16 + 8 * half) =
-                asr::u32x4{s0[0], s1[0], s0[1], s1[1]};
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int64_t n = n16 + 8 * h + 4 * half;
-              uint16_t* d = args.c + m * args.ldc + n;
-              if (args.vec4 && n + 4 <= args.n) {
-                *reinterpret_cast<asr::u32x2*>(d) = asr::u32x2{w[h][0], w[h][1]};
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (n + e < args.n) d[e] = static_cast<uint16_t>(w[h][e / 2] >> (16 * (e % 2)));
-              }
-            }
-          }
-          if (args.c32) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int64_t n = n16 + 8 * h + 4 * half;
-              float* d = args.c32 + m * args.ldc + n;
-              if (args.vec4 && n + 4 <= args.n) {
-                *reinterpret_cast<asr::f32x4*>(d) = asr::f32x4{xs[h][0], xs[h][1], xs[h][2], xs[h][3]};
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (n + e < args.n) d[e] = xs[h][e];
-              }
-            }
-          }
-        }
-      });
+      for (int e = 0; e < 8; ++e) {
+        x[e] = (static_cast<float>(static_cast<int32_t>(raw[e])) * sa) * sb[e];
+        h[e] = round_one<ROUND>(x[e], e < 4 ? r0[e] : r1[e - 4]);
+      }
+      const int64_t at = m * args.ldc + n;
+      if (args.vec16 && count == 8) {
+        asr::store_vec_bf16<false, 8>(args.c + at, h);
+        if (args.c32) asr::store_vec<false, 8>(args.c32 + at, x);
+      } else {
+        asr::store_range_bf16<8>(args.c, at, 0, count, h);
+        if (args.c32) asr::store_range<8>(args.c32, at, 0, count, x);
+      }
     });
   });
 }
@@ -880,7 +850,7 @@ asr_i8::GemmArgs gemm_args(const int8_t* a, int64_t lda, const int8_t* b, int64_
   g.n = static_cast<int32_t>(n);
   g.k = static_cast<int32_t>(k);
   g.vec4 = ldc % 4 == 0 && aligned_to(c, 8) && (!c_f32 || aligned_to(c_f32, 16));
-  g.vec16 = ldc % 8 == 0 && aligned_to(c, 16);
+  g.vec16 = ldc % 8 == 0 && aligned_to(c, 16) && (!c_f32 || aligned_to(c_f32, 16));
   return g;
 }
 

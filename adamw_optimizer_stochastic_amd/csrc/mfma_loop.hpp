@@ -283,6 +283,55 @@ __device__ __forceinline__ void mfma_loop(const Operands& op, unsigned char* sme
   for (; kt < ktiles; ++kt) tile_body(kt, std::integral_constant<int, 0>{});
 }
 
+// The wave's 32 rows i * 32 .. + 31 of its accumulators, turned through a slice
+// of LDS of its own into runs of 8 columns whose lanes cover whole rows: a
+// store of 16 bytes a lane then writes whole 128-byte lines (64 f16 columns),
+// where the accumulators' own order touches 32 lines with 32 bytes each, four
+// times the address cycles. (The 256 x 256 product that updates X spent
+// 16 us a tile on them, of 73.) Lanes l and l ^ 1 hold neighbouring rows of
+// the same columns.
+template <typename T>
+struct Rows {
+  static constexpr int kGroups = T::WN / 8;             // runs of 8 a row
+  static constexpr int kPasses = 32 * kGroups / 64;     // runs a lane gets
+  static constexpr int kLd = T::WN + 4;                 // words: no bank conflicts either way
+  static constexpr int kSliceBytes = 32 * kLd * 4;
+  static constexpr int kBytes = T::kWaves * kSliceBytes;
+  static_assert(32 * kGroups % 64 == 0, "whole passes");
+
+  // Row in the block and first column in the wave's tile of this lane's run.
+  static __device__ __forceinline__ void place(int pass, uint32_t lane, uint32_t& row, uint32_t& col) {
+    const uint32_t pair = (static_cast<uint32_t>(pass) * 64 + lane) >> 1;
+    row = pair / kGroups * 2 + (lane & 1u);
+    col = pair % kGroups * 8;
+  }
+  template <typename Acc>
+  static __device__ __forceinline__ void put(uint32_t* slice, const Acc (&acc)[T::kFragN], uint32_t lane) {
+    uint32_t* to = slice + (lane & 31u) * kLd + 4 * (lane >> 5);
+    static_for<T::kFragN>([&](auto jc) {
+      static_for<4>([&](auto qc) {
+        constexpr int j = decltype(jc)::value, q = decltype(qc)::value;
+        // (each element as a value first: a bit cast of an element of the
+        // reference took element 0 of the vector)
+        const auto v0 = acc[j][4 * q], v1 = acc[j][4 * q + 1], v2 = acc[j][4 * q + 2], v3 = acc[j][4 * q + 3];
+        *reinterpret_cast<asr::u32x4*>(to + j * 32 + 8 * q) =
+            asr::u32x4{__builtin_bit_cast(uint32_t, v0), __builtin_bit_cast(uint32_t, v1),
+                       __builtin_bit_cast(uint32_t, v2), __builtin_bit_cast(uint32_t, v3)};
+      });
+    });
+  }
+  // (a wave's LDS accesses complete in order: no wait between put and get)
+  static __device__ __forceinline__ void get(const uint32_t* slice, uint32_t row, uint32_t col, uint32_t (&v)[8]) {
+    const asr::u32x4 a = *reinterpret_cast<const asr::u32x4*>(slice + row * kLd + col);
+    const asr::u32x4 b = *reinterpret_cast<const asr::u32x4*>(slice + row * kLd + col + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  }
+};
+
 // Index of workgroup b in an order that gives each XCD (b % 8) a contiguous
 // range of `total`.
 __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total) {

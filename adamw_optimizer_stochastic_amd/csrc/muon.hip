@@ -312,10 +312,26 @@ __host__ __device__ inline int64_t tiles_of(int mode, int32_t rows, int32_t cols
   return ts * (ts + 1) / 2;
 }
 
+// The turned copy's stage in LDS, beside the waves' slices: element (m, n) of
+// the tile at row n, rows taken a phase at a time (half of the 256 tile's, for
+// room). Its 16-byte chunks are XOR-swizzled by n / 8, which is what differs
+// between the lanes that write at once.
+template <typename T>
+struct Turn {
+  static constexpr int kPhases = T::BM == 256 ? 2 : 1;
+  static constexpr int kBlocks = T::kFragM / kPhases;      // blocks of 32 rows a wave, a phase
+  static constexpr int kRows = T::BM / kPhases;
+  static constexpr int kBytes = T::BN * kRows * 2;
+  static constexpr int kLds = asr_mfma::Rows<T>::kBytes + kBytes;
+  static_assert(kRows % 64 == 0, "whole groups of 8 chunks");
+  static __device__ __forceinline__ uint32_t at(uint32_t n, uint32_t chunk) {
+    return n * kRows + ((chunk ^ ((n >> 3) & 7u)) << 3);
+  }
+};
+
 template <typename T>
 constexpr int lds_bytes() {
-  const int turned = T::BN * (T::BM + 8) * 2;
-  return turned > T::kLoopLds ? turned : T::kLoopLds;
+  return Turn<T>::kLds > T::kLoopLds ? Turn<T>::kLds : T::kLoopLds;
 }
 
 // V consecutive elements (V = 4 or 8) of O from element `at` of a matrix, `n`
@@ -386,6 +402,35 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
     asr_mfma::grouped_tile(t, static_cast<uint32_t>((m_all + T::BM - 1) / T::BM),
                            static_cast<uint32_t>((n_all + T::BN - 1) / T::BN), tm, tn);
   const int64_t m0 = static_cast<int64_t>(tm) * T::BM, n0 = static_cast<int64_t>(tn) * T::BN;
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t wm = wave / T::kWavesN, wn = wave % T::kWavesN;
+  const _Float16* c_in = reinterpret_cast<const _Float16*>(ws + (MODE == kSquare ? l.a : direct));
+  _Float16* lo_io = reinterpret_cast<_Float16*>(ws + l.lo);
+
+  // What C adds, for the 32 rows of block i: 16 bytes a lane and pass.
+  using Rows = asr_mfma::Rows<T>;
+  constexpr int P = Rows::kPasses;
+  auto fetch = [&](int i, f16x8 (&hi)[P], f16x8 (&lo)[P]) {
+    static_for<P>([&](auto pc) {
+      constexpr int p = decltype(pc)::value;
+      uint32_t row, col;
+      Rows::place(p, lane, row, col);
+      const int64_t m = m0 + wm * T::WM + i * 32 + row, n = n0 + wn * T::WN + col;
+      hi[p] = f16x8{};
+      lo[p] = f16x8{};
+      if (m < m_all && n < ld_d) {  // (ld_d is a multiple of 64)
+        hi[p] = *reinterpret_cast<const f16x8*>(c_in + m * ld_d + n);
+        if constexpr (MODE != kSquare) lo[p] = *reinterpret_cast<const f16x8*>(lo_io + m * ld_d + n);
+      }
+    });
+  };
+  // The smallest tile fetches it before the K loop: a latency of its own at
+  // the end of a short loop otherwise.
+  constexpr bool kEarly = MODE != kGram && T::WM == 32;
+  [[maybe_unused]] f16x8 early_hi[P], early_lo[P];
+  if constexpr (kEarly) fetch(0, early_hi, early_lo);
+
   E::acc acc[T::kFragM][T::kFragN] = {};
   {
     asr_mfma::Operands op;
@@ -398,15 +443,6 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
     asr_mfma::mfma_loop<T, E>(op, smem, acc);
   }
 
-  // A lane holds runs of 4 columns of a row; v_permlane32_swap pairs lanes l
-  // and l + 32 into runs of 8: columns 16 p + 8 half .. + 7 of a 32 x 32
-  // block, so every access below is 16 bytes.
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t wm = wave / T::kWavesN, wn = wave % T::kWavesN;
-  const uint32_t row = lane & 31u, half = lane >> 5;
-  const _Float16* c_in = reinterpret_cast<const _Float16*>(ws + (MODE == kSquare ? l.a : direct));
-  _Float16* lo_io = reinterpret_cast<_Float16*>(ws + l.lo);
   _Float16* d_out = reinterpret_cast<_Float16*>(
       ws + (MODE == kGram ? l.a : MODE == kSquare ? l.b : l.wide ? l.x : y_next));
   const float inv_sa = 1.0f / l.sa;
@@ -414,39 +450,32 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
   const float beta = MODE == kSquare ? args.b : args.a;
   const float inv_sx = 1.0f / l.sx;
 
-  // The turned copy goes through LDS: element (m, n) of the tile at n * kLd + m.
-  constexpr int kLd = T::BM + 8;
-  _Float16* tile = reinterpret_cast<_Float16*>(smem);
+  uint32_t* slice = reinterpret_cast<uint32_t*>(smem) + wave * (Rows::kSliceBytes / 4);
+  _Float16* tile = reinterpret_cast<_Float16*>(smem + Rows::kBytes);
   const bool turn = MODE == kUpdate || (kSymmetric && tm != tn);
   const uint32_t turn_sel = turn_selector(lane);
-  if constexpr (MODE != kFinal) __syncthreads();  // every wave has read the last K tile
-  static_for<T::kFragM>([&](auto ic) {
-    constexpr int i = decltype(ic)::value;
-    const uint32_t mt = wm * T::WM + i * 32 + row;
-    const int64_t m = m0 + mt;
-    const bool live = m < m_all;
-    static_for<T::kFragN>([&](auto jc) {
-      constexpr int j = decltype(jc)::value;
-      static_for<2>([&](auto pc) {
+  static_for<Turn<T>::kPhases>([&](auto phase_c) {
+    constexpr int phase = decltype(phase_c)::value;
+    // the last K tile is read, or the last phase's turned rows
+    if (phase == 0 || turn) __syncthreads();
+    static_for<Turn<T>::kBlocks>([&](auto bc) {
+      constexpr int block = decltype(bc)::value, i = phase * Turn<T>::kBlocks + block;
+      f16x8 hi_in[P], lo_in[P];
+      if constexpr (MODE != kGram && !kEarly) fetch(i, hi_in, lo_in);
+      Rows::put(slice, acc[i], lane);
+      static_for<P>([&](auto pc) {
         constexpr int p = decltype(pc)::value;
-        const uint32_t nt = wn * T::WN + j * 32 + 16 * p + 8 * half;
-        const int64_t n = n0 + nt;
+        uint32_t row, col, raw[8];
+        Rows::place(p, lane, row, col);
+        Rows::get(slice, row, col, raw);
+        const uint32_t nt = wn * T::WN + col;
+        const int64_t m = m0 + wm * T::WM + i * 32 + row, n = n0 + nt;
+        const bool live = m < m_all;
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const auto r = __builtin_amdgcn_permlane32_swap(
-              __float_as_uint(acc[i][j][8 * p + e]), __float_as_uint(acc[i][j][8 * p + 4 + e]),
-              false, false);
-          v[e] = alpha * __uint_as_float(r[0]);
-          v[4 + e] = alpha * __uint_as_float(r[1]);
-        }
-        const bool inside = live && n < ld_d;  // (ld_d is a multiple of 64)
+        for (int e = 0; e < 8; ++e) v[e] = alpha * __uint_as_float(raw[e]);
         if constexpr (MODE != kGram) {
-          f16x8 hi = {}, lo = {};
-          if (inside) {
-            hi = *reinterpret_cast<const f16x8*>(c_in + m * ld_d + n);
-            if constexpr (MODE != kSquare) lo = *reinterpret_cast<const f16x8*>(lo_io + m * ld_d + n);
-          }
+          const f16x8 hi = kEarly ? early_hi[p] : hi_in[p], lo = kEarly ? early_lo[p] : lo_in[p];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float x = MODE == kSquare ? static_cast<float>(hi[e])
@@ -465,37 +494,41 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
           f16x8 hi, lo;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float x = live && n + e < n_all ? v[e] : 0.0f;  // the padding reads as zeros
-            v[e] = x;
-            hi[e] = static_cast<_Float16>(x);
-            lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
+            v[e] = live && n + e < n_all ? v[e] : 0.0f;  // the padding reads as zeros
+            hi[e] = static_cast<_Float16>(v[e]);
+            lo[e] = static_cast<_Float16>(v[e] - static_cast<float>(hi[e]));
           }
           if (turn) {
+            const uint32_t mt = wm * (Turn<T>::kBlocks * 32) + block * 32 + row;
 #pragma unroll
             for (int e = 0; e < 8; e += 2)
-              *reinterpret_cast<uint32_t*>(tile + (nt + e + (lane & 1u)) * kLd + (mt & ~1u)) =
+              *reinterpret_cast<uint32_t*>(tile + Turn<T>::at(nt + e + (lane & 1u), mt >> 3) + (mt & 6u)) =
                   turn_pair(v[e], v[e + 1], turn_sel);
           }
-          if (inside) {
+          if (live && n < ld_d) {
             *reinterpret_cast<f16x8*>(d_out + m * ld_d + n) = hi;
             if constexpr (MODE == kUpdate) *reinterpret_cast<f16x8*>(lo_io + m * ld_d + n) = lo;
           }
         }
       });
     });
-  });
-  if constexpr (MODE != kFinal) {
-    if (!turn) return;
-    __syncthreads();
-    _Float16* t_out = reinterpret_cast<_Float16*>(
-        ws + (MODE == kGram ? l.a : MODE == kSquare ? l.b : l.wide ? y_next : l.x));
-    for (int q = threadIdx.x; q < T::BN * (T::BM / 8); q += T::kThreads) {
-      const int nt = q / (T::BM / 8), c8 = q % (T::BM / 8) * 8;
-      if (n0 + nt < n_all && m0 + c8 < ld_turned)
-        *reinterpret_cast<f16x8*>(t_out + (n0 + nt) * ld_turned + m0 + c8) =
-            *reinterpret_cast<const f16x8*>(tile + nt * kLd + c8);
+    if constexpr (MODE != kFinal) {
+      if (turn) {
+        __syncthreads();
+        _Float16* t_out = reinterpret_cast<_Float16*>(
+            ws + (MODE == kGram ? l.a : MODE == kSquare ? l.b : l.wide ? y_next : l.x));
+        constexpr int kChunks = Turn<T>::kRows / 8, kWaveChunks = Turn<T>::kBlocks * 4;
+        for (uint32_t q = threadIdx.x; q < T::BN * kChunks; q += T::kThreads) {
+          const uint32_t nt = q / kChunks, chunk = q % kChunks;
+          const int64_t m = m0 + chunk / kWaveChunks * T::WM + phase * (Turn<T>::kBlocks * 32) +
+                            chunk % kWaveChunks * 8;
+          if (n0 + nt < n_all && m < ld_turned)
+            *reinterpret_cast<f16x8*>(t_out + (n0 + nt) * ld_turned + m) =
+                *reinterpret_cast<const f16x8*>(tile + Turn<T>::at(nt, chunk));
+        }
+      }
     }
-  }
+  });
 }
 
 using Big = asr_mfma::Tile<256, 256, 128, 64, 2>;
@@ -503,6 +536,7 @@ using Mid = asr_mfma::Tile<192, 192, 96, 96, 3>;
 using Small = asr_mfma::Tile<128, 128, 64, 64, 2>;
 using Small8 = asr_mfma::Tile<128, 128, 64, 32, 3>;
 using Tiny = asr_mfma::Tile<64, 64, 32, 32, 4>;
+using Tiny8 = asr_mfma::Tile<64, 64, 32, 32, 8>;  // the same, alone on a compute unit
 
 // ------------------------------------------------------- one workgroup
 // All steps of a small matrix in one workgroup of 16 waves: X stays in f32 in
@@ -797,11 +831,12 @@ hipError_t launch_product(ProductArgs& a, hipStream_t s) {
   struct Choice { int tile, slots; double fixed, per_k; };
   // microseconds
   constexpr Choice choices[] = {{256, 256, 14.0, 1.6}, {192, 256, 10.0, 1.05},
-                                {128, 512, 8.0, 1.05}, {128, 256, 5.0, 0.6}, {64, 512, 4.0, 0.45}};
+                                {128, 512, 8.0, 1.05}, {128, 256, 5.0, 0.6}, {64, 512, 4.0, 0.45},
+                                {64, 256, 4.0, 0.3}};
   int best = ASR_MUON_TILE;
   if (best < 0) {
     double least = 0.0;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 6; ++i) {
       const double t = launch_time(MODE, a, choices[i].tile, choices[i].slots, choices[i].fixed,
                                    choices[i].per_k);
       if (best < 0 || t < least) best = i, least = t;
@@ -812,7 +847,8 @@ hipError_t launch_product(ProductArgs& a, hipStream_t s) {
     case 1: return launch_tile<Mid, MODE, OUT>(a, s);
     case 2: return launch_tile<Small, MODE, OUT>(a, s);
     case 3: return launch_tile<Small8, MODE, OUT>(a, s);
-    default: return launch_tile<Tiny, MODE, OUT>(a, s);
+    case 4: return launch_tile<Tiny, MODE, OUT>(a, s);
+    default: return launch_tile<Tiny8, MODE, OUT>(a, s);
   }
 }
 
