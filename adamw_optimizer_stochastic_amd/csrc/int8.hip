@@ -479,6 +479,18 @@ using Small = asr_mfma::Tile<128, 128, 64, 64, 2>;
 using Small8 = asr_mfma::Tile<128, 128, 64, 32, 3>;
 using Tiny = asr_mfma::Tile<64, 64, 32, 32, 4>;
 
+// `count` (4, or fewer at a row's end) outputs from C's element `at`.
+__device__ __forceinline__ void store4(const GemmArgs& args, int64_t at, int count, const uint32_t (&h)[4],
+                                       const float (&x)[4]) {
+  if (args.vec4 && count == 4) {
+    asr::store_vec_bf16<false, 4>(args.c + at, h);
+    if (args.c32) asr::store_vec<false, 4>(args.c32 + at, x);
+  } else {
+    asr::store_range_bf16<4>(args.c, at, 0, count, h);
+    if (args.c32) asr::store_range<4>(args.c32, at, 0, count, x);
+  }
+}
+
 // REST: K is not a multiple of 16 (a variant of its own: its byte loads cost
 // the largest tile registers that it has not got).
 template <typename T, int ROUND, bool REST>
@@ -574,8 +586,10 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void gemm_i8(GemmArgs ar
         asr::store_vec_bf16<false, 8>(args.c + at, h);
         if (args.c32) asr::store_vec<false, 8>(args.c32 + at, x);
       } else {
-        asr::store_range_bf16<8>(args.c, at, 0, count, h);
-        if (args.c32) asr::store_range<8>(args.c32, at, 0, count, x);
+        const uint32_t h0[4] = {h[0], h[1], h[2], h[3]}, h1[4] = {h[4], h[5], h[6], h[7]};
+        const float x0[4] = {x[0], x[1], x[2], x[3]}, x1[4] = {x[4], x[5], x[6], x[7]};
+        store4(args, at, min(count, 4), h0, x0);
+        store4(args, at + 4, count - 4, h1, x1);
       }
     });
   });
@@ -669,15 +683,7 @@ __global__ __launch_bounds__(512) void gemm_i8_few(GemmArgs args) {
     x[e] = (static_cast<float>(t[e]) * sa) * sb;
     h[e] = round_one<ROUND>(x[e], r16[e]);
   }
-  const int64_t at = m * args.ldc + n;
-  const int count = static_cast<int>(min(int64_t{4}, args.n - n));
-  if (args.vec4 && count == 4) {
-    asr::store_vec_bf16<false, 4>(args.c + at, h);
-    if (args.c32) asr::store_vec<false, 4>(args.c32 + at, x);
-  } else {
-    asr::store_range_bf16<4>(args.c, at, 0, count, h);
-    if (args.c32) asr::store_range<4>(args.c32, at, 0, count, x);
-  }
+  store4(args, m * args.ldc + n, static_cast<int>(min(int64_t{4}, args.n - n)), h, x);
 }
 
 // C = 0 (a linear layer's sums over nothing).

@@ -32,6 +32,7 @@
 #include <memory>
 #include <new>
 #include <string>
+#include <utility>
 
 #pragma clang fp contract(off)
 
@@ -272,6 +273,7 @@ struct OutArgs {
   float decay;
   uint32_t seed, step;
   uint32_t vec8;  // runs of 8 of every matrix's rows start on 16-byte addresses
+  uint32_t vec4;  // runs of 4 on 8-byte ones (f32: 16)
 };
 
 struct ProductArgs {
@@ -488,7 +490,14 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= inv_sx;
             const int count = static_cast<int>(min(int64_t{8}, n_all - n));
-            store_out<OUT, 8>(args.out, d, m * n_all + n, count, args.out.vec8 && count == 8, v);
+            const int64_t at = m * n_all + n;
+            if (args.out.vec8 && count == 8) {
+              store_out<OUT, 8>(args.out, d, at, 8, true, v);
+            } else {
+              const float v0[4] = {v[0], v[1], v[2], v[3]}, v1[4] = {v[4], v[5], v[6], v[7]};
+              store_out<OUT, 4>(args.out, d, at, min(count, 4), args.out.vec4 && count >= 4, v0);
+              store_out<OUT, 4>(args.out, d, at + 4, count - 4, args.out.vec4 && count == 8, v1);
+            }
           }
         } else {
           f16x8 hi, lo;
@@ -535,8 +544,7 @@ using Big = asr_mfma::Tile<256, 256, 128, 64, 2>;
 using Mid = asr_mfma::Tile<192, 192, 96, 96, 3>;
 using Small = asr_mfma::Tile<128, 128, 64, 64, 2>;
 using Small8 = asr_mfma::Tile<128, 128, 64, 32, 3>;
-using Tiny = asr_mfma::Tile<64, 64, 32, 32, 4>;
-using Tiny8 = asr_mfma::Tile<64, 64, 32, 32, 8>;  // the same, alone on a compute unit
+using Tiny = asr_mfma::Tile<64, 64, 32, 32, 3>;
 
 // ------------------------------------------------------- one workgroup
 // All steps of a small matrix in one workgroup of 16 waves: X stays in f32 in
@@ -777,10 +785,33 @@ hipError_t launch_tile(ProductArgs& a, hipStream_t s) {
   return launch(&product<T, MODE, OUT>, total, T::kThreads, &a, s);
 }
 
+// A tile size: `slots` of them run at once; one costs `fixed` microseconds
+// (`store` more where it updates X and the chip is full: the traffic of the
+// epilogues) and for every 64 of K `alone` to `full`, by how many of the slots
+// are taken. Fitted to one-round launches of 1024^2 to 4096^2 and 8 x 1024 x 4096
+// (microseconds a product, 256 / 192 / 128 / 128 in 8 waves / 64 tile):
+//   A of 1024^2 28/24/16/13/8.5, of 2048^2 44/37/26/22/28, of 4096^2
+//   92/82/109/118/160; X of 1024^2 34/30/18/15/10, of 4096^2
+//   135/173/150/178/230, of 8 x 1024 x 4096 116/174/134/154/191.
+struct Choice {
+  int tile, slots;
+  double fixed, store, alone, full;
+};
+constexpr Choice kChoices[] = {{256, 256, 14.0, 16.0, 1.35, 1.6},
+                               {192, 256, 10.0, 8.0, 0.9, 1.1},
+                               {128, 512, 8.0, 8.0, 0.62, 1.05},
+                               {128, 256, 5.0, 4.0, 0.57, 0.6},
+                               {64, 768, 4.0, 3.0, 0.3, 0.65}};
+
 // Time of a launch in one tile size: its matrices' tiles, in order, go to the
-// next free of the chip's slots (`slots` tiles run at once); a tile costs
-// `fixed` and `per_k` for every 64 of K.
-double launch_time(int mode, const ProductArgs& a, int tile, int slots, double fixed, double per_k) {
+// next free slot.
+double launch_time(int mode, const ProductArgs& a, const Choice& c) {
+  const int slots = c.slots;
+  int64_t tiles = 0;
+  for (int k = 0; k < a.count; ++k) tiles += tiles_of(mode, a.d[k].rows, a.d[k].cols, c.tile);
+  const double taken = std::clamp((static_cast<double>(tiles) - 128.0) / (slots - 128.0), 0.0, 1.0);
+  const double fixed = c.fixed + (mode == kGram || mode == kSquare ? 0.0 : c.store * taken);
+  const double per_k = c.alone + (c.full - c.alone) * taken;
   // free[i] slots are free at when[i]; few different times ever coexist
   double when[kMaxBatch + 2] = {0.0};
   int free[kMaxBatch + 2] = {slots};
@@ -789,7 +820,7 @@ double launch_time(int mode, const ProductArgs& a, int tile, int slots, double f
   for (int k = 0; k < a.count; ++k) {
     const Layout l(a.d[k].rows, a.d[k].cols);
     const double cost = fixed + per_k * ((mode == kGram ? l.ld_t : l.ld_s) / 64);
-    int64_t n = tiles_of(mode, a.d[k].rows, a.d[k].cols, tile);
+    int64_t n = tiles_of(mode, a.d[k].rows, a.d[k].cols, c.tile);
     if (n > 4 * slots) {  // whole rounds at once
       const int64_t rounds = n / slots - 2;
       for (int i = 0; i < levels; ++i) when[i] += rounds * cost;
@@ -828,17 +859,11 @@ double launch_time(int mode, const ProductArgs& a, int tile, int slots, double f
 
 template <int MODE, int OUT = kOutBf16>
 hipError_t launch_product(ProductArgs& a, hipStream_t s) {
-  struct Choice { int tile, slots; double fixed, per_k; };
-  // microseconds
-  constexpr Choice choices[] = {{256, 256, 14.0, 1.6}, {192, 256, 10.0, 1.05},
-                                {128, 512, 8.0, 1.05}, {128, 256, 5.0, 0.6}, {64, 512, 4.0, 0.45},
-                                {64, 256, 4.0, 0.3}};
   int best = ASR_MUON_TILE;
   if (best < 0) {
     double least = 0.0;
-    for (int i = 0; i < 6; ++i) {
-      const double t = launch_time(MODE, a, choices[i].tile, choices[i].slots, choices[i].fixed,
-                                   choices[i].per_k);
+    for (int i = 0; i < 5; ++i) {
+      const double t = launch_time(MODE, a, kChoices[i]);
       if (best < 0 || t < least) best = i, least = t;
     }
   }
@@ -847,8 +872,7 @@ hipError_t launch_product(ProductArgs& a, hipStream_t s) {
     case 1: return launch_tile<Mid, MODE, OUT>(a, s);
     case 2: return launch_tile<Small, MODE, OUT>(a, s);
     case 3: return launch_tile<Small8, MODE, OUT>(a, s);
-    case 4: return launch_tile<Tiny, MODE, OUT>(a, s);
-    default: return launch_tile<Tiny8, MODE, OUT>(a, s);
+    default: return launch_tile<Tiny, MODE, OUT>(a, s);
   }
 }
 
@@ -1020,14 +1044,15 @@ int check_workspace(const char* who, void* ws, size_t bytes, size_t need) {
 
 struct Shape { int32_t rows, cols; };
 
-// Workspace of n matrices whose shapes are in list order (see goes_before).
-size_t list_bytes(const Shape* shapes, int32_t n) {
+// Workspace of n matrices in list order (see goes_before).
+template <typename F>
+size_t list_bytes(int32_t n, F shape) {
   int32_t k0 = 0;
-  while (k0 < n && is_small(shapes[k0].rows, shapes[k0].cols)) ++k0;
+  while (k0 < n && is_small(shape(k0).first, shape(k0).second)) ++k0;
   int64_t most = 0;
   while (k0 < n) {
     int64_t bytes;
-    k0 = group_end(k0, n, [&](int32_t k) { return std::pair(shapes[k].rows, shapes[k].cols); }, bytes);
+    k0 = group_end(k0, n, shape, bytes);
     most = std::max(most, bytes);
   }
   return static_cast<size_t>(most);
@@ -1057,11 +1082,13 @@ int asr_newton_schulz(const void* const* g, uint16_t* const* out, int32_t n, int
   Settings st{g_dtype, steps, a, b, c, eps, 0.0f, false, {}, static_cast<char*>(workspace),
               static_cast<hipStream_t>(stream)};
   st.out.vec8 = cols % 8 == 0;
+  st.out.vec4 = cols % 4 == 0;
   for (int32_t k = 0; k < n; ++k) {
     if (!g[k] || !out[k]) return fail(ASR_EINVAL, "newton_schulz: null matrix");
     if (!aligned_to(g[k], g_dtype == ASR_F32 ? 4 : 2) || !aligned_to(out[k], 2))
       return fail(ASR_EALIGN, "newton_schulz: matrices must be aligned to their element size");
     st.out.vec8 = st.out.vec8 && aligned_to(out[k], 16);
+    st.out.vec4 = st.out.vec4 && aligned_to(out[k], 8);
   }
   if (int rc = check_workspace(who, workspace, workspace_bytes,
                                asr_newton_schulz_workspace_bytes(n, rows, cols)))
@@ -1092,7 +1119,7 @@ size_t asr_muon_workspace_bytes(const asr_muon_tensor* tensors, int32_t n) {
   std::sort(shapes.get(), shapes.get() + live, [](const Shape& x, const Shape& y) {
     return goes_before(x.rows, x.cols, y.rows, y.cols);
   });
-  return list_bytes(shapes.get(), live);
+  return list_bytes(live, [&](int32_t k) { return std::pair(shapes[k].rows, shapes[k].cols); });
 }
 
 int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int32_t param_dtype, int32_t grad_dtype,
@@ -1121,7 +1148,7 @@ int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int32_t param_dtype
   st.out.decay = static_cast<float>(1.0 - lr * weight_decay);
   st.out.seed = seed;
   st.out.step = static_cast<uint32_t>(step);
-  st.out.vec8 = 1;
+  st.out.vec8 = st.out.vec4 = 1;
   int32_t live = 0;
   for (int32_t k = 0; k < n; ++k) {
     const asr_muon_tensor& t = tensors[k];
@@ -1134,17 +1161,18 @@ int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int32_t param_dtype
         !aligned_to(t.grad, grad_dtype == ASR_F32 ? 4 : 2) || !aligned_to(t.momentum, 4))
       return fail(ASR_EALIGN, "muon: buffers must be aligned to their element size");
     st.out.vec8 = st.out.vec8 && t.cols % 8 == 0 && aligned_to(t.param, 16);
+    st.out.vec4 = st.out.vec4 && t.cols % 4 == 0 && aligned_to(t.param, param_dtype == ASR_F32 ? 16 : 8);
     descs[live] = Desc{t.grad, t.momentum, t.param, t.base_index, 0, static_cast<int32_t>(t.rows),
                        static_cast<int32_t>(t.cols), static_cast<float>(lr * t.lr_factor), 0};
     list[live] = &descs[live];
     ++live;
   }
-  if (int rc = check_workspace(who, workspace, workspace_bytes, asr_muon_workspace_bytes(tensors, n)))
-    return rc;
   if (live == 0) return ok();
   std::sort(list.get(), list.get() + live, [](const Desc* x, const Desc* y) {
     return goes_before(x->rows, x->cols, y->rows, y->cols);
   });
+  const size_t need = list_bytes(live, [&](int32_t k) { return std::pair(list[k]->rows, list[k]->cols); });
+  if (int rc = check_workspace(who, workspace, workspace_bytes, need)) return rc;
   hipError_t e;
   auto go = [&](auto g) {
     using G = decltype(g);
