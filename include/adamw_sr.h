@@ -284,8 +284,8 @@ int asr_gemm_bf16(const uint16_t* a, int64_t lda, const uint16_t* b,
  * Requirements: 0 <= rows, cols < 2**31; ldx >= cols; ldq a multiple of 16, at
  * least the group's length; q 16-byte aligned; x and scale aligned to their
  * elements (x's rows starting on 16-byte addresses take the vector path);
- * rows < 2**30, and at most 2**30 tiles of 128 rows x 64 columns in the
- * transposed form; base_index + rows*cols <= 2**64;
+ * fewer than 2**24 workgroups: of one row (four, up to 2048 columns), or in
+ * the transposed form of one tile of 128 rows x 64 columns; base_index + rows*cols <= 2**64;
  * no buffer overlaps another. workspace: asr_quantize_i8_workspace_bytes
  * bytes of device memory, 16-byte aligned (0 bytes, NULL allowed, unless
  * transpose), as for asr_adamw_step.
@@ -373,7 +373,7 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
  * the Muon optimizer). The products run on the matrix cores with f16 operands
  * and f32 sums, X itself held as two f16 numbers: the result is within about
  * 2e-3 (relative, Frobenius norm) of the exact one, low-rank G included. The norm is
- * summed in 64 bits. A G of zeros gives zeros; an Inf or NaN in G makes all
+ * summed in 64 bits. A G of zeros gives zeros (with eps > 0); an Inf or NaN in G makes all
  * of its result NaN.
  *
  * g, out: host arrays of n device pointers (read during the call only), each

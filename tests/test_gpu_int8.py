@@ -139,7 +139,7 @@ def _codes(rng, rows, k, ld, fill=77):
 GEMM_SHAPES = [(1, 1, 1), (1, 16, 16), (1, 300, 100), (1, 4096, 4096), (2, 33, 64), (7, 130, 1000),
                (16, 257, 513), (17, 64, 128), (33, 70, 65), (64, 64, 64), (65, 63, 127),
                (100, 1000, 2049), (130, 4097, 144), (257, 259, 640), (520, 1100, 335),
-               (2100, 2100, 270), (4100, 4099, 143)]
+               (2100, 2100, 270), (4100, 4099, 143), (4200, 4300, 160), (1500, 1500, 256)]
 
 
 @pytest.mark.parametrize("shape", GEMM_SHAPES)
@@ -368,3 +368,100 @@ def test_other_stream_and_capture():
         torch.cuda.synchronize()
         for g, v in zip(out, want):
             assert np.array_equal(to_host(g), v), r
+
+
+def test_offsets_past_32_bits():
+    """More than 2**32 elements: the codes of sampled rows and columns (whose
+    stream positions pass 2**32 too) and sampled outputs of a product."""
+    announce("int8 past 32 bits")
+    rows, cols = 70000, 65536
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    for i in range(0, rows, 10000):
+        x[i:i + 10000].normal_(generator=gen)
+    pick = [0, 1, 65535, 65536, 69999]
+    for rounding in ("rn", "sr"):
+        q, s = ops.quantize_i8(x, rounding=rounding, seed=3, step=4, base_index=1)
+        for r in pick:
+            want, sw = o8.quantize(x[r:r + 1].float().cpu().numpy(), False, rounding, 3, 4,
+                                   1 + r * cols)
+            assert np.array_equal(q[r:r + 1].cpu().numpy(), want) and to_host(s)[r] == sw[0]
+    q, s = ops.quantize_i8(x, transpose=True)
+    for c in (0, 32767, 65535):
+        want, sw = o8.quantize(x[:, c:c + 1].float().cpu().numpy(), True)
+        assert np.array_equal(q[c:c + 1].cpu().numpy(), want) and to_host(s)[c] == sw[0]
+    del x, s
+    a, b = q[:, :64], q[:64000, 1024:1088]
+    sa, sb = torch.rand(65536, device="cuda"), torch.rand(64000, device="cuda")
+    c = ops.gemm_i8(a, b, sa, sb, rounding="sr", seed=1, step=2)
+    ri, ci = [0, 1, 33000, 65535], [0, 7, 31999, 63999]
+    want = o8.gemm_f32(a[ri].cpu().numpy(), b[ci].cpu().numpy(), to_host(sa)[ri], to_host(sb)[ci])
+    rr, cc = np.meshgrid(ri, ci, indexing="ij")
+    want = oracle.gemm_round_at(want.reshape(-1), rr.reshape(-1), cc.reshape(-1), 64000, 1, 2)
+    assert_bits_equal(to_host(c[ri][:, ci]).reshape(-1), want, "sampled outputs")
+
+
+def test_two_streams_at_once():
+    """Two linear layers on two streams at once, forward and backward: each
+    call's workspace is its own."""
+    announce("linear_i8 two streams")
+    rng = np.random.default_rng(6)
+    layers = []
+    for k in range(2):
+        x, xt = _bf16_of(rng.standard_normal((400 + k, 520)))
+        w, wt = _bf16_of(rng.standard_normal((610, 520)))
+        dy, dyt = _bf16_of(rng.standard_normal((400 + k, 610)))
+        layers.append((xt.requires_grad_(), wt.requires_grad_(), dyt))
+
+    def run(k):
+        x, w, dy = layers[k]
+        y = linear_i8(x, w, seed=k)
+        return [y.detach(), *torch.autograd.grad(y, (x, w), dy)]
+
+    want = [[to_host(t) for t in run(k)] for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k].append(run(k))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for out in got[k]:
+            for g, v in zip(out, want[k]):
+                assert np.array_equal(to_host(g), v), k
+
+
+def test_captured_forward_and_backward():
+    """Forward and backward of the layer in one graph (on leaves of its own),
+    replayed on new data."""
+    announce("linear_i8 capture")
+    rng = np.random.default_rng(7)
+    data = [[_bf16_of(rng.standard_normal(s))[1] for s in ((70, 130), (90, 130), (70, 90))]
+            for _ in range(3)]
+
+    def run(x, w, dy):
+        x, w = x.detach().requires_grad_(), w.detach().requires_grad_()
+        y = linear_i8(x, w, seed=2, step=3)
+        return [y.detach(), *torch.autograd.grad(y, (x, w), dy)]
+
+    want = [[to_host(t) for t in run(*d)] for d in data]
+    held = [torch.zeros_like(t) for t in data[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(*held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(*held)
+    for d, ref in zip(data, want):
+        for h, t in zip(held, d):
+            h.copy_(t)
+        graph.replay()
+        torch.randn(1 << 16, device="cuda").sum().item()
+        torch.cuda.synchronize()
+        for g, v in zip(out, ref):
+            assert np.array_equal(to_host(g), v)

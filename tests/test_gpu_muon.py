@@ -79,7 +79,8 @@ def test_newton_schulz(shape, kind):
 
 
 @pytest.mark.parametrize("shape", [(16, 1024, 1024), (16, 1536, 512), (12, 1600, 1700),
-                                   (3, 300, 2000), (40, 48, 64), (1, 4352, 4096)])
+                                   (3, 300, 2000), (40, 48, 64), (1, 4352, 4096),
+                                   (8, 1024, 2000), (2, 2048, 2048)])
 def test_batches(shape):
     """Every tile (the number of tiles picks it) and more matrices than one
     launch takes; each matrix's result is that of the matrix alone, bit for
@@ -341,3 +342,73 @@ def test_training_step_with_int8_products():
     one, two = train(), train()
     for a, b in zip(one, two):
         assert np.array_equal(a, b)
+
+
+def test_long_mixed_list():
+    """More matrices than one launch takes, large and small ones of both
+    orientations mixed, ragged widths: each ends as it does alone."""
+    announce("muon mixed list")
+    shapes = [(130 + 2 * (i % 7), 140 + 3 * (i % 5)) for i in range(37)]
+    shapes[3:3] = [(20 + i, 40 + 5 * (i % 3)) for i in range(35)]
+    shapes[50] = (700, 260)
+    shapes[20] = (260, 900)
+    ps, gs, ms = _state(shapes, torch.bfloat16, torch.float32, seed=7)
+    bases = [17 + 1000 * i for i in range(len(shapes))]
+    hp = dict(lr=0.02, weight_decay=0.1, step=5, seed=2)
+    pa, ma = [p.clone() for p in ps], [m.clone() for m in ms]
+    ops.muon_step(pa, gs, ma, bases, **hp)
+    for i in range(len(shapes)):
+        p, m = ps[i].clone(), ms[i].clone()
+        ops.muon_step([p], [gs[i]], [m], [bases[i]], **hp)
+        assert torch.equal(p.view(torch.int16), pa[i].view(torch.int16)), (i, shapes[i])
+        assert torch.equal(m, ma[i]), (i, shapes[i])
+
+
+def test_unaligned_matrices():
+    """Weights, gradients and momenta that start on no vector boundary."""
+    announce("muon unaligned")
+    for shape in ((40, 64), (200, 264), (264, 200)):
+        for pt in (torch.bfloat16, torch.float32):
+            (p,), (g,), (m,) = _state([shape], pt, torch.bfloat16, seed=11)
+            a, b = p.clone(), m.clone()
+            ops.muon_step([a], [g], [b], [3], lr=0.02, step=1, seed=5)
+
+            def off(t):
+                store = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+                store[1:].copy_(t.reshape(-1))
+                return store[1:].view(t.shape)
+
+            q, h, n = off(p), off(g), off(m)
+            ops.muon_step([q], [h], [n], [3], lr=0.02, step=1, seed=5)
+            assert torch.equal(q, a) and torch.equal(n, b), (shape, pt)
+
+
+def test_two_streams_at_once():
+    """Two optimizers' steps on two streams at once, each with its workspace."""
+    announce("muon two streams")
+    shapes = [(300, 500), (500, 300), (64, 64)]
+    start = [_state(shapes, torch.bfloat16, torch.bfloat16, seed=20 + k) for k in range(2)]
+
+    def make(k):
+        params = [torch.nn.Parameter(p.clone()) for p in start[k][0]]
+        for p, g in zip(params, start[k][1]):
+            p.grad = g.clone()
+        return params, MuonSR(params, lr=0.02, seed=k)
+
+    want = []
+    for k in range(2):
+        params, opt = make(k)
+        for _ in range(4):
+            opt.step()
+        want.append([to_host(p) for p in params])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    made = [make(k) for k in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (params, opt), st in zip(made, streams):
+            with torch.cuda.stream(st):
+                opt.step()
+    torch.cuda.synchronize()
+    for k in range(2):
+        for p, v in zip(made[k][0], want[k]):
+            assert np.array_equal(to_host(p), v)

@@ -48,7 +48,8 @@ def test_quantize_argument_errors():
     assert need >= 60 * 4 and E.asr_quantize_i8_workspace_bytes(8, 60, 0) == 0
     assert q(transpose=1, ldq=16, ws=0x10000, ws_bytes=need - 1) == E.ASR_EWORKSPACE
     assert q(transpose=1, ldq=16, ws=0x10008, ws_bytes=need) == E.ASR_EWORKSPACE
-    assert q(transpose=1, rows=2 ** 30, ldq=2 ** 30, ws=0x10000, ws_bytes=1 << 50) == E.ASR_EINVAL
+    assert q(rows=2 ** 26) == E.ASR_EINVAL          # 2**24 workgroups of four rows
+    assert q(rows=2 ** 24, cols=4096, ldx=4096, ldq=4096) == E.ASR_EINVAL
     assert q(transpose=1, rows=2 ** 29, cols=2 ** 20, ldx=2 ** 20, ldq=2 ** 29, ws=0x10000,
              ws_bytes=1 << 50) == E.ASR_EINVAL
     assert q(rows=0, x=0, q=0, scale=0) == E.ASR_OK
