@@ -809,7 +809,8 @@ hipError_t launch_tiles(asr_i8::QuantArgs& a, hipStream_t s) {
 constexpr int64_t kMaxBlocks = 0xFFFFFF;
 
 bool too_many_blocks(int64_t rows, int64_t cols, bool transpose) {
-  if (transpose) return ((cols + 63) / 64) * ((rows + 127) / 128) > kMaxBlocks;
+  // (the kernels count rows in 32 bits, 32 at a time past the last one)
+  if (transpose) return ((cols + 63) / 64) * ((rows + 127) / 128) > kMaxBlocks || rows > kMaxDim - 64;
   return (cols <= 2048 ? (rows + 3) / 4 : rows) > kMaxBlocks;
 }
 
@@ -1067,7 +1068,9 @@ int asr_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb, cons
     return fail(ASR_EALIGN, "gemm_i8: scales and outputs must be aligned to their element size");
   if (static_cast<uint64_t>(m) * static_cast<uint64_t>(n) - 1 > ~base_index)
     return fail(ASR_EINVAL, "gemm_i8: base_index + m*n exceeds 2**64");
-  if (((m + 63) / 64) * ((n + 63) / 64) > 0x7FFFFFFF) return fail(ASR_EINVAL, "gemm_i8: too many tiles");
+  // (launches of fewer than 2**32 threads, with room for a last round of halves)
+  if (((m + 255) / 256) * ((n + 255) / 256) > (int64_t{1} << 23) - kCus)
+    return fail(ASR_EINVAL, "gemm_i8: too many tiles");
   asr_i8::GemmArgs g = gemm_args(a, lda, b, ldb, scale_a, scale_b, c, ldc, c_f32, m, n, k);
   g.base_index = base_index;
   g.seed = seed;

@@ -285,8 +285,8 @@ int asr_gemm_bf16(const uint16_t* a, int64_t lda, const uint16_t* b,
  * least the group's length; q 16-byte aligned; x and scale aligned to their
  * elements (x's rows starting on 16-byte addresses take the vector path);
  * fewer than 2**24 workgroups: of one row (four, up to 2048 columns), or in
- * the transposed form of one tile of 128 rows x 64 columns; base_index + rows*cols <= 2**64;
- * no buffer overlaps another. workspace: asr_quantize_i8_workspace_bytes
+ * the transposed form of one tile of 128 rows x 64 columns (and rows at most
+ * 2**31 - 64); base_index + rows*cols <= 2**64; no buffer overlaps another. workspace: asr_quantize_i8_workspace_bytes
  * bytes of device memory, 16-byte aligned (0 bytes, NULL allowed, unless
  * transpose), as for asr_adamw_step.
  * Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Runs
@@ -314,8 +314,9 @@ int asr_quantize_i8(const void* x, int32_t dtype, int64_t ldx, int64_t rows,
  * Bytes past a row's K codes are never used, whatever they hold.
  * Requirements: 0 <= M, N < 2**31; 0 <= K < 2**17; lda, ldb multiples of 16,
  * at least K and below 2**23; ldc >= N; a and b 16-byte aligned; scales, c and c_f32
- * aligned to their element size; base_index + M*N <= 2**64; no output
- * overlaps an input. M or N = 0 writes nothing; K = 0 writes products of 0.
+ * aligned to their element size; at most 2**23 - 256 tiles of 256 x 256;
+ * base_index + M*N <= 2**64; no output overlaps an input. M or N = 0 writes
+ * nothing; K = 0 writes products of 0.
  * Errors: ASR_EINVAL, ASR_EALIGN, ASR_EHIP. Runs on `stream`; does not
  * synchronize.
  */

@@ -147,3 +147,21 @@ def test_linear_argument_errors():
     assert bwd(ws=0) == E.ASR_EWORKSPACE
     assert bwd(ws_bytes=need[1] - 1) == E.ASR_EWORKSPACE
     assert bwd(dx=0, dw=0, ws=0) == E.ASR_OK
+
+
+def test_sizes_past_a_launch_are_refused():
+    """Sizes that the arguments' ranges allow and a launch, or a kernel's own
+    32-bit counting, does not."""
+    E = _abi
+    big = 2 ** 31 - 1
+    ws = E.asr_quantize_i8_workspace_bytes(big, 1, 1)
+    for rows, cols, transpose in ((big, 1, 1), (2 ** 31 - 63, 1, 1), (2 ** 27, 2 ** 12, 1),
+                                  (2 ** 24, 4096, 0), (2 ** 26, 1, 0)):
+        length = rows if transpose else cols
+        assert _status(E.asr_quantize_i8, 0x1000, E.ASR_BF16, cols, rows, cols, transpose, 0x2000,
+                       (length + 15) // 16 * 16, 0x3000, E.ASR_ROUND_RN, 0, 0, 0, 0x4000,
+                       max(ws, E.asr_quantize_i8_workspace_bytes(rows, cols, 1)), None) \
+            == E.ASR_EINVAL
+    for m, n in ((5, big), (big, 5), (256, 2 ** 31 - 256 * 256 + 1), (2 ** 30, 2 ** 30)):
+        assert _status(E.asr_gemm_i8, 0x1000, 16, 0x2000, 16, 0x3000, 0x4000, 0x5000, n, None, m,
+                       n, 16, E.ASR_ROUND_RN, 0, 0, 0, None) == E.ASR_EINVAL
