@@ -709,7 +709,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_matrix(SmallArgs args)
     __syncthreads();
     E::acc aa = {};
     if (squares) {
-dot(aa, x, ld_x, sj, x, ld_x, si, tb);
+      dot(aa, x, ld_x, sj, x, ld_x, si, tb);
 #pragma unroll
       for (int r = 0; r < 16; ++r) aa[r] *= gram_scale;
       put_square(gram, aa);
@@ -717,7 +717,7 @@ dot(aa, x, ld_x, sj, x, ld_x, si, tb);
     __syncthreads();
     if (squares) {
       E::acc bb = {};
-dot(bb, gram, ld_y, sj, gram, ld_y, si, sb);
+      dot(bb, gram, ld_y, sj, gram, ld_y, si, sb);
 #pragma unroll
       for (int r = 0; r < 16; ++r) bb[r] = args.b * aa[r] + args.c * inv_sa * bb[r];
       put_square(poly, bb);
@@ -726,7 +726,7 @@ dot(bb, gram, ld_y, sj, gram, ld_y, si, sb);
     each_block([&](E::acc& xb, int32_t i, int32_t j) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) xb[r] *= args.a * l.sa;
-dot(xb, y, ld_y, j, poly, ld_y, i, sb);
+      dot(xb, y, ld_y, j, poly, ld_y, i, sb);
 #pragma unroll
       for (int r = 0; r < 16; ++r) xb[r] *= inv_sa;
     });

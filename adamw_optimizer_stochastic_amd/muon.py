@@ -11,7 +11,8 @@ share positions (give MuonSR the number of elements AdamWSR has).
 For each matrix: m = momentum*m + g (f32), u = g + momentum*m (nesterov) or m,
 p = p*(1 - lr*weight_decay) - lr*factor*O(u), O the Newton-Schulz
 orthogonalisation. All matrices of a group go through the products together,
-which is what fills the chip with small ones.
+which is what fills the chip with small ones. A step captured into a graph
+repeats its number, learning rate and bits on every replay.
 """
 
 import torch
@@ -47,7 +48,6 @@ class MuonSR(torch.optim.Optimizer):
         self.seed = seed
         self._base_index = {}
         self._next_index = ops._u64("base_offset", base_offset)
-        self._workspaces = {}
         defaults = dict(lr=lr, weight_decay=weight_decay, momentum=momentum, nesterov=nesterov,
                         ns_coefficients=ops._coefficients(ns_coefficients), eps=eps,
                         ns_steps=ns_steps, adjust_lr_fn=adjust_lr_fn, rounding=rounding)
@@ -70,20 +70,12 @@ class MuonSR(torch.optim.Optimizer):
 
     def _init_state(self, p):
         if len(self.state[p]) == 0:
+            if p.is_cuda and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("MuonSR: take one step before capturing one (a replay would "
+                                   "start from a momentum of zeros every time)")
             self.state[p] = {"step": torch.tensor(0, dtype=torch.int64),
                              "momentum_buffer": torch.zeros(p.shape, dtype=torch.float32,
                                                             device=p.device)}
-
-    def _workspace(self, device, shapes):
-        """The workspace of this device and its current stream: a step only
-        reuses it behind the step before, in stream order."""
-        key = (device, torch.cuda.current_stream(device).cuda_stream)
-        ws = self._workspaces.get(key)
-        need = ops.muon_workspace_bytes(shapes)
-        if ws is None or ws.numel() < need:
-            ws = self._workspaces[key] = torch.empty(max(need, 1), dtype=torch.uint8,
-                                                     device=device)
-        return ws
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -103,7 +95,7 @@ class MuonSR(torch.optim.Optimizer):
                 self._init_state(p)
                 t = int(self.state[p]["step"]) + 1
                 batches.setdefault((p.device, t), []).append(p)
-            for (device, t), ps in batches.items():
+            for (_, t), ps in batches.items():
                 ops.muon_step(ps, [p.grad for p in ps],
                               [self.state[p]["momentum_buffer"] for p in ps],
                               [self._base_index[p] for p in ps], lr=group["lr"],
@@ -111,8 +103,7 @@ class MuonSR(torch.optim.Optimizer):
                               weight_decay=group["weight_decay"], ns_steps=group["ns_steps"],
                               ns_coefficients=group["ns_coefficients"], eps=group["eps"],
                               adjust_lr=group["adjust_lr_fn"], step=t, seed=self.seed,
-                              rounding=group["rounding"],
-                              workspace=self._workspace(device, [p.shape for p in ps]))
+                              rounding=group["rounding"])
                 for p in ps:
                     self.state[p]["step"].fill_(t)
         return loss

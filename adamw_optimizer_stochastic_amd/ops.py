@@ -467,9 +467,13 @@ def _coefficients(c):
     return c
 
 
-def _ns_workspace(workspace, need, device):
+def _ns_workspace(workspace, need, device, spans):
+    """The caller's workspace, checked against the buffers at `spans`, or one
+    of torch's for this call and stream (its own in every captured graph)."""
     if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    _require_gpu(workspace, "workspace")
+    check_disjoint([*spans, _extent(workspace, "workspace")])
     if workspace.device != device or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be on {device} and hold {need} bytes")
     return workspace
@@ -498,10 +502,11 @@ def newton_schulz(g, *, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=Non
             raise ValueError("out must be bfloat16 with g's shape, on g's device")
         if out.data_ptr() != g.data_ptr() or g.dtype != torch.bfloat16:
             check_disjoint([_extent(g, "g"), _extent(out, "out")])
+    spans = [_extent(g, "g")] + ([_extent(out, "out")] if out.data_ptr() != g.data_ptr() else [])
     rows, cols = g.shape[-2:]
     n = g.shape[0] if g.dim() == 3 else 1
     need = _abi.asr_newton_schulz_workspace_bytes(n, rows, cols)
-    workspace = _ns_workspace(workspace, need, g.device)
+    workspace = _ns_workspace(workspace, need, g.device, spans)
     size, size_out = rows * cols * g.element_size(), rows * cols * 2
     with _on(g.device):
         _abi.asr_newton_schulz([g.data_ptr() + k * size for k in range(n)],
@@ -524,7 +529,8 @@ def muon_lr_factor(rows, cols, adjust_lr="original"):
 
 
 def muon_workspace_bytes(shapes):
-    """Workspace bytes that hold a muon_step over matrices of these shapes."""
+    """Workspace bytes that hold a muon_step over matrices of these shapes, all
+    of one type of param and grad (of several: the largest of each one's)."""
     arr = _abi.muon_array([(None, None, None, r, c, 0, 1.0) for r, c in shapes])
     return _abi.asr_muon_workspace_bytes(arr, len(shapes))
 
@@ -576,7 +582,7 @@ def muon_step(params, grads, momenta, base_indices, *, lr, momentum=0.95, nester
     check_disjoint(spans)
     groups = {key: (_abi.muon_array(ts), len(ts)) for key, ts in groups.items()}
     need = max(_abi.asr_muon_workspace_bytes(arr, k) for arr, k in groups.values())
-    workspace = _ns_workspace(workspace, need, device)
+    workspace = _ns_workspace(workspace, need, device, spans)
     with _on(device):
         for (pt, gt), (arr, k) in groups.items():
             _abi.asr_muon_step(arr, k, _DTYPE_CODE[pt], _DTYPE_CODE[gt], float(lr),

@@ -412,3 +412,71 @@ def test_two_streams_at_once():
     for k in range(2):
         for p, v in zip(made[k][0], want[k]):
             assert np.array_equal(to_host(p), v)
+
+
+def test_optimizer_over_two_types():
+    """Matrices of two types in one group of the optimizer, whose own lists
+    need more workspace than the list of both: as a step for each type."""
+    announce("MuonSR two types")
+    shapes = [(1024, 1040), (40, 1040)] * 20
+    dtypes = [torch.bfloat16, torch.float32] * 20
+    ps, gs, ms = [], [], []
+    for i in range(2):
+        p, g, m = _state(shapes[i::2], dtypes[i], dtypes[i], seed=i)
+        ps.append(p), gs.append(g), ms.append([torch.zeros_like(x) for x in m])
+    params = [torch.nn.Parameter(ps[k % 2][k // 2].clone()) for k in range(40)]
+    opt = MuonSR(params, lr=0.02, seed=4)
+    for k, p in enumerate(params):
+        p.grad = gs[k % 2][k // 2]
+    opt.step()
+    bases = [opt.base_index(p) for p in params]
+    for i in range(2):
+        ops.muon_step(ps[i], gs[i], ms[i], bases[i::2], lr=0.02, weight_decay=0.1, step=1, seed=4)
+        for p, q, m in zip(params[i::2], ps[i], ms[i]):
+            assert torch.equal(p.detach(), q)
+            assert torch.equal(opt.state[p]["momentum_buffer"], m)
+
+
+def test_captured_optimizer():
+    """MuonSR's step in two graphs, replayed in turn, against eager steps (a
+    captured step repeats its number); a first step is not captured."""
+    announce("MuonSR capture")
+    shapes = [(300, 200), (64, 64), (130, 260)]
+    ps, gs, _ = _state(shapes, torch.bfloat16, torch.bfloat16, seed=6)
+    params = [torch.nn.Parameter(p.clone()) for p in ps]
+    opt = MuonSR(params, lr=0.02, seed=4)
+    for p, g in zip(params, gs):
+        p.grad = g
+    opt.step()   # step 1; the graphs hold steps 2 and 3
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            opt.step()
+    ms = [torch.zeros(s, device="cuda") for s in shapes]
+    bases = [opt.base_index(p) for p in params]
+    for step in (1, 2, 3, 2, 3, 3):
+        ops.muon_step(ps, gs, ms, bases, lr=0.02, weight_decay=0.1, step=step, seed=4)
+        if step > 1:
+            graphs[step - 2].replay()
+            torch.randn(1 << 18, device="cuda").sum().item()
+        torch.cuda.synchronize()
+        for p, q in zip(params, ps):
+            assert torch.equal(p.detach().view(torch.int16), q.view(torch.int16)), step
+
+
+def test_workspace_may_not_be_the_data():
+    announce("muon workspace overlap")
+    g = torch.ones(200, 300, dtype=torch.bfloat16, device="cuda")
+    need = ops.muon_workspace_bytes([(200, 300)])
+    raw = torch.zeros(need + 2 * g.numel(), dtype=torch.uint8, device="cuda")
+    out = raw[need:].view(torch.bfloat16).view(200, 300)
+    with pytest.raises(ValueError, match="share memory"):
+        ops.newton_schulz(g, out=out, workspace=raw)
+    with pytest.raises(ValueError, match="contiguous"):
+        ops.newton_schulz(g, workspace=torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2])
+    with pytest.raises(ValueError, match="share memory"):
+        ops.muon_step([g], [out], [torch.zeros(200, 300, device="cuda")], [0], lr=0.1, step=1,
+                      seed=0, workspace=raw)
+    assert bool((g == 1).all()) and bool((out == 0).all())
+    ops.newton_schulz(g, out=out, workspace=raw[:need])
+    assert torch.equal(out, ops.newton_schulz(g))

@@ -188,3 +188,33 @@ def test_optimizer_positions_and_state():
     assert bool((other.state[p]["momentum_buffer"] == 1.0009765625).all())
     assert other.param_groups[1]["lr"] == 0.5
     opt.step()   # no gradients: nothing to do
+
+
+def test_optimizer_step_leaves_workspaces_to_each_call(monkeypatch):
+    """Types of one group go through the products apart, and the most that one
+    type's list needs can be more than what the whole list needs (its groups of
+    32 mix large and small matrices): a workspace sized for the whole list is
+    too small."""
+    big, low = [(1024, 1040)] * 20, [(40, 1040)] * 20
+    mixed = [s for pair in zip(big, low) for s in pair]
+    assert ops.muon_workspace_bytes(big) > ops.muon_workspace_bytes(mixed)
+    calls = []
+    monkeypatch.setattr(ops, "muon_step", lambda *a, **kw: calls.append((a, kw)))
+    params = [_param(4, 6), _param(4, 6, dtype=torch.bfloat16), _param(4, 6)]
+    opt = MuonSR(params, seed=3)
+    for p in params[:2]:
+        p.grad = torch.ones_like(p)
+    opt.step()
+    (args, kw), = calls
+    assert [p.dtype for p in args[0]] == [torch.float32, torch.bfloat16]
+    assert kw.get("workspace") is None and kw["step"] == 1 and args[3] == [0, 24]
+
+
+def test_first_step_is_not_captured(monkeypatch):
+    """Its momentum of zeros would be part of the graph."""
+    class OnGpu:
+        is_cuda, shape, device = True, (4, 6), "cpu"
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    opt = MuonSR([_param(4, 6)])
+    with pytest.raises(RuntimeError, match="before capturing"):
+        opt._init_state(OnGpu())
