@@ -150,7 +150,8 @@ __device__ __forceinline__ double group_sum(double x, double* lds) {
 }
 
 // Sum of squares of one chunk of U, in 64 bits; the momentum is updated on
-// the way. Memory bound: 2 (bf16 gradient) + 8 bytes an element.
+// the way. Memory bound: 2 (bf16 gradient) + 8 bytes an element; 138e6 elements
+// in 250 us, 5.5 TB/s.
 template <typename G, bool MUON>
 __global__ __launch_bounds__(256) void sum_squares(PrepareArgs a) {
   __shared__ double lds[4];
@@ -188,7 +189,9 @@ __global__ __launch_bounds__(256) void sum_squares(PrepareArgs a) {
 }
 
 // X0 as hi + lo, and hi turned, for one 64 x 64 tile, with zeros up to the
-// leading dimensions (the K loops read whole 128-byte lines).
+// leading dimensions (the K loops read whole 128-byte lines). Memory bound: 6
+// bytes an element read (2 without momentum) and 6 written; 138e6 in 342 us,
+// 4.8 TB/s.
 template <typename G, bool MUON>
 __global__ __launch_bounds__(256) void scale_matrix(PrepareArgs a) {
   constexpr int kLd = 72;  // f16 a row of the turned tile
@@ -379,6 +382,16 @@ __device__ __forceinline__ void store_out(const OutArgs& out, const Desc& d, int
   else asr::store_range_bf16<V>(p, at, 0, n, h);
 }
 
+// One product for all matrices of the launch. The K loop alone runs at 1288
+// TFLOP/s on large matrices (f16 products of the library: 1481 for 8192^3);
+// what it leaves is the epilogue, which nothing else covers: a tile that
+// updates X reads 4 and writes 6 bytes an element, all tiles of a round at
+// once. 4096 x 4096, 1024 x 4096, 14336 x 4096 and 4096 x 14336 together: A 611
+// to 643 us, B 221, the new X 1080, the weights 1110 (in 256 tiles, A in 192).
+// 8 x 1024 x 4096: A 62-71, B 23-27, X 113-124 (360 MB, 3.2 TB/s), where the 52 us
+// of K loops are less than the traffic. X and what the last product adds to
+// are fetched a block ahead of their use (4096 x 14336: 4132 against 4168 us for all
+// five steps).
 template <typename T, int MODE, int OUT>
 __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs args) {
   using E = asr_mfma::ElemF16;
@@ -430,8 +443,8 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
   // The smallest tile fetches it before the K loop: a latency of its own at
   // the end of a short loop otherwise.
   constexpr bool kEarly = MODE != kGram && T::WM == 32;
-  [[maybe_unused]] f16x8 early_hi[P], early_lo[P];
-  if constexpr (kEarly) fetch(0, early_hi, early_lo);
+  [[maybe_unused]] f16x8 hi_in[2][P], lo_in[2][P];  // of this block and the next
+  if constexpr (kEarly) fetch(0, hi_in[0], lo_in[0]);
 
   E::acc acc[T::kFragM][T::kFragN] = {};
   {
@@ -456,14 +469,14 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
   _Float16* tile = reinterpret_cast<_Float16*>(smem + Rows::kBytes);
   const bool turn = MODE == kUpdate || (kSymmetric && tm != tn);
   const uint32_t turn_sel = turn_selector(lane);
+  if constexpr (MODE != kGram && !kEarly) fetch(0, hi_in[0], lo_in[0]);
   static_for<Turn<T>::kPhases>([&](auto phase_c) {
     constexpr int phase = decltype(phase_c)::value;
     // the last K tile is read, or the last phase's turned rows
     if (phase == 0 || turn) __syncthreads();
     static_for<Turn<T>::kBlocks>([&](auto bc) {
       constexpr int block = decltype(bc)::value, i = phase * Turn<T>::kBlocks + block;
-      f16x8 hi_in[P], lo_in[P];
-      if constexpr (MODE != kGram && !kEarly) fetch(i, hi_in, lo_in);
+      if constexpr (MODE != kGram && i + 1 < T::kFragM) fetch(i + 1, hi_in[(i + 1) & 1], lo_in[(i + 1) & 1]);
       Rows::put(slice, acc[i], lane);
       static_for<P>([&](auto pc) {
         constexpr int p = decltype(pc)::value;
@@ -477,7 +490,7 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = alpha * __uint_as_float(raw[e]);
         if constexpr (MODE != kGram) {
-          const f16x8 hi = kEarly ? early_hi[p] : hi_in[p], lo = kEarly ? early_lo[p] : lo_in[p];
+          const f16x8 hi = hi_in[i & 1][p], lo = lo_in[i & 1][p];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float x = MODE == kSquare ? static_cast<float>(hi[e])
@@ -548,9 +561,11 @@ using Tiny = asr_mfma::Tile<64, 64, 32, 32, 3>;
 
 // ------------------------------------------------------- one workgroup
 // All steps of a small matrix in one workgroup of 16 waves: X stays in f32 in
-// the accumulator registers (32 x 32 blocks, kBlocks of them a wave), its f16
-// copy lies in LDS both ways, and a X + B X accumulates onto a X. Three
-// launches a step become four barriers.
+// the accumulator registers (32 x 32 blocks, kSmallBlocks of them a wave), its
+// f16 copy lies in LDS both ways, and a X + B X accumulates onto a X. Three
+// launches a step become four barriers. Bound by the latency of dependent
+// products and LDS accesses on one compute unit: 128 x 128 takes 25 us, where
+// the 17 launches of the other way took 78.
 constexpr int kSmallWaves = 16;
 constexpr int kSmallBlocks = 3;
 constexpr int kSmallLds = 159 * 1024;
