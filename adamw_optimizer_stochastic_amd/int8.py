@@ -69,6 +69,10 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
     step), positions from base_index) or "rn", for the gradient's codes; give
     every layer its own base_index (or seed) and every step its own step.
     K, N and the number of tokens are below 2**17 (each is summed over once).
+
+    Forward and backward can be captured into a graph together; as with any
+    operator under torch's autograd, no eager graph of the same leaves may be
+    alive then (the gradient's accumulation would run on that graph's stream).
     """
     if grad_rounding not in ops.ROUNDING_CODE:
         raise ValueError("grad_rounding must be 'sr' or 'rn'")

@@ -465,3 +465,53 @@ def test_captured_forward_and_backward():
         torch.cuda.synchronize()
         for g, v in zip(out, ref):
             assert np.array_equal(to_host(g), v)
+
+
+def _product_bound(a, b, step_a):
+    """What a product of int8 codes of a and b (rows, to one scale each) may be
+    off their exact product: codes of a within step_a of a step (1/2 nearest, 1
+    stochastic), of b within 1/2, then the bf16 rounding of a value that may be off
+    already and three binary32 roundings (the 1.0001)."""
+    sa, sb = np.abs(a).max(1)[:, None] / 127, np.abs(b).max(1)[None, :] / 127
+    off = (step_a * sa * np.abs(b).sum(1)[None, :] + np.abs(a).sum(1)[:, None] * sb / 2
+           + a.shape[1] * step_a * sa * sb / 2)
+    return 1.0001 * (off + 2.0 ** -8 * (np.abs(a @ b.T) + off))
+
+
+@pytest.mark.parametrize("grad_rounding,step", [("rn", 0.5), ("sr", 1.0)])
+@pytest.mark.parametrize("shape", [(9, 17, 12), (20, 33, 24), (33, 7, 9), (70, 130, 90),
+                                   (300, 33, 500)])
+def test_gradients_against_formula_and_differences(shape, grad_rounding, step):
+    """dx = dy w and dw = dy^T x within what their codes may be off, and against
+    differences of <dy, y>: y is linear in x and in w but for the codes, so a
+    step of any length does, here one along the gradient."""
+    t, n, k = shape
+    announce("linear_i8 gradients", shape, grad_rounding)
+    rng = np.random.default_rng(shape)
+    (x, xt), (w, wt), (dy, dyt) = (_bf16_of(rng.standard_normal(s))
+                                   for s in ((t, k), (n, k), (t, n)))
+    xt.requires_grad_(), wt.requires_grad_()
+    y = linear_i8(xt, wt, seed=3, step=4, grad_rounding=grad_rounding)
+    dx, dw = torch.autograd.grad(y, (xt, wt), dyt)
+    x, w, dy = (v.astype(np.float64) for v in (x, w, dy))
+    values = {}
+    for name, got, a, b in (("y", y, x, w), ("dx", dx, dy, w.T), ("dw", dw, dy.T, x.T)):
+        values[name] = got.detach().double().cpu().numpy()
+        limit = _product_bound(a, b, 0.5 if name == "y" else step)
+        assert np.all(np.abs(values[name] - a @ b.T) <= limit), name
+
+    def moved(v, g):
+        """v a step along g, as a bf16 tensor and its exact value."""
+        return _bf16_of(v + 2 * g / np.sqrt(np.mean(g * g)))
+
+    for name, a, b in (("dx", dy, w.T), ("dw", dy.T, x.T)):
+        new, newt = moved(x if name == "dx" else w, values[name])
+        x1, w1 = (new.astype(np.float64), w) if name == "dx" else (x, new.astype(np.float64))
+        y1 = linear_i8(newt if name == "dx" else xt.detach(), wt.detach() if name == "dx" else newt)
+        change = np.sum(dy * (y1.double().cpu().numpy() - values["y"]))
+        along = x1 - x if name == "dx" else w1 - w
+        limit = (np.sum(_product_bound(a, b, step) * np.abs(along))
+                 + np.sum(np.abs(dy) * (_product_bound(x, w, 0.5) + _product_bound(x1, w1, 0.5))))
+        if t * n * k < 20000:   # (a worst case added up over more says nothing)
+            assert limit < 0.5 * abs(change)
+        assert abs(change - np.sum(values[name] * along)) <= limit, name
