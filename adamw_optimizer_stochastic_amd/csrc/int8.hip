@@ -520,8 +520,10 @@ __device__ __forceinline__ void store4(const GemmArgs& args, int64_t at, int cou
 // the epilogue is the part no other work covers, so its stores go in whole
 // lines. REST: K is not a multiple of 16 (a variant of
 // its own: its byte loads cost the largest tile registers that it has not
-// got). smem: T's kLoopLds bytes.
-template <typename T, int ROUND, bool REST>
+// got). SPLIT: groups of T's waves that walk a share of K each (the integer sums
+// are the same in any order), joined in LDS, and share the epilogue. smem: SPLIT
+// times T's kLoopLds bytes.
+template <typename T, int ROUND, bool REST, int SPLIT = 1>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& args, int64_t m0, int64_t n0, unsigned char* smem) {
   using E = asr_mfma::ElemI8;
   static_assert(asr_mfma::Rows<T>::kBytes <= T::kLoopLds, "the slices lie in the ring");
@@ -534,16 +536,29 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& args, int64_t m0, int6
   op.last_a = args.m - 1 - static_cast<int32_t>(m0);
   op.last_b = args.n - 1 - static_cast<int32_t>(n0);
   op.kbytes = args.k & ~15;
-  asr_mfma::mfma_loop<T, E>(op, smem, acc);
-
+  op.ktiles = asr_mfma::ktiles_of(op.kbytes);
   const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t wave = all_waves % T::kWaves;
+  [[maybe_unused]] const uint32_t group = SPLIT > 1 ? all_waves / T::kWaves : 0;
+  if constexpr (SPLIT > 1) {
+    op.ktiles = (op.ktiles + SPLIT - 1) / SPLIT;
+    const int32_t from = static_cast<int32_t>(group) * op.ktiles * asr_mfma::kRowBytes;
+    op.kbytes = max(0, min(op.kbytes - from, op.ktiles * asr_mfma::kRowBytes));
+    // (a group past K reads nothing; its pointers stay inside the rows)
+    op.a += op.kbytes > 0 ? from : 0;
+    op.b += op.kbytes > 0 ? from : 0;
+    asr_mfma::mfma_loop<T, E>(op, smem + group * T::kLoopLds, acc);
+  } else {
+    asr_mfma::mfma_loop<T, E>(op, smem, acc);
+  }
+
   const uint32_t wm = wave / T::kWavesN, wn = wave % T::kWavesN;
   [[maybe_unused]] const uint32_t row = lane & 31u, half = lane >> 5;
 
   // The last K % 16 codes of every row, byte by byte (what lies behind a
   // row's end is not read); lanes of the upper half hold zeros.
-  if constexpr (REST) {
+  if constexpr (REST) if (group == 0) {
     const int rest = args.k & 15;
     auto last_codes = [&](const int8_t* base, int64_t ld, int64_t r) {
       const int8_t* p = base + r * ld + (args.k - rest);
@@ -572,7 +587,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& args, int64_t m0, int6
   using Rows = asr_mfma::Rows<T>;
   static_assert(32 % Rows::kGroups == 0, "a lane's columns are those of every pass");
   __syncthreads();  // the last K tile is read
-  uint32_t* slice = reinterpret_cast<uint32_t*>(smem) + wave * (Rows::kSliceBytes / 4);
+  static_assert(SPLIT == 1 || (T::kFragM == 1 && Rows::kPasses % SPLIT == 0), "passes shared evenly");
+  uint32_t* first = reinterpret_cast<uint32_t*>(smem) + wave * (Rows::kSliceBytes / 4);
+  uint32_t* slice = first + group * (Rows::kBytes / 4);
   uint32_t row0, col;
   Rows::place(0, lane, row0, col);
   const int64_t n = n0 + wn * T::WN + col;
@@ -583,11 +600,18 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& args, int64_t m0, int6
   static_for<T::kFragM>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
     Rows::put(slice, acc[i], lane);
-    static_for<Rows::kPasses>([&](auto pc) {
-      constexpr int p = decltype(pc)::value;
+    if constexpr (SPLIT > 1) __syncthreads();
+    static_for<Rows::kPasses / SPLIT>([&](auto pc) {
       uint32_t r, same_col, raw[8];
-      Rows::place(p, lane, r, same_col);
-      Rows::get(slice, r, col, raw);
+      Rows::place(decltype(pc)::value * SPLIT + static_cast<int>(group), lane, r, same_col);
+      Rows::get(first, r, col, raw);
+#pragma unroll
+      for (int g = 1; g < SPLIT; ++g) {
+        uint32_t more[8];
+        Rows::get(first + g * (Rows::kBytes / 4), r, col, more);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) raw[e] += more[e];
+      }
       const int64_t m = m0 + wm * T::WM + i * 32 + r;
       if (m >= args.m || count == 0) return;
       const float sa = args.sa[m];
@@ -618,13 +642,13 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& args, int64_t m0, int6
   });
 }
 
-template <typename T, int ROUND, bool REST>
-__global__ __launch_bounds__(T::kThreads, T::kMinWaves) void gemm_i8(GemmArgs args) {
-  __shared__ __align__(1024) unsigned char smem[T::kLoopLds];
+template <typename T, int ROUND, bool REST, int SPLIT>
+__global__ __launch_bounds__(SPLIT * T::kThreads, T::kMinWaves) void gemm_i8(GemmArgs args) {
+  __shared__ __align__(1024) unsigned char smem[SPLIT * T::kLoopLds];
   uint32_t tm, tn;
   asr_mfma::grouped_tile(asr_mfma::xcd_order(blockIdx.x, args.tiles_m * args.tiles_n),
                          args.tiles_m, args.tiles_n, tm, tn);
-  gemm_tile<T, ROUND, REST>(args, static_cast<int64_t>(tm) * T::BM, static_cast<int64_t>(tn) * T::BN, smem);
+  gemm_tile<T, ROUND, REST, SPLIT>(args, static_cast<int64_t>(tm) * T::BM, static_cast<int64_t>(tn) * T::BN, smem);
 }
 
 // Big tiles for as many whole rounds of the chip as there are, and what is left
@@ -648,7 +672,8 @@ __global__ __launch_bounds__(Big::kThreads, Big::kMinWaves) void gemm_i8_halves(
   }
 }
 
-// A few rows of A (decoding): bound by reading B once. A workgroup takes 16
+// A few rows of A (decoding): bound by reading B once (1 x 28672 x 8192, 235 MB:
+// 41.8 us, 5.6 TB/s). A workgroup takes 16
 // rows of B against MB blocks of 16 rows of A; its 8 waves split K in units of
 // 128 bytes, with every load straight into the operand registers of a 16x16x64
 // instruction (B on its row side, so a lane ends with 4 consecutive columns of
@@ -859,7 +884,7 @@ struct Parts {
   }
 };
 
-template <typename T>
+template <typename T, int SPLIT = 1>
 hipError_t launch_gemm(asr_i8::GemmArgs args, int32_t rounding, hipStream_t s) {
   using namespace asr_i8;
   args.tiles_m = static_cast<uint32_t>((args.m + T::BM - 1) / T::BM);
@@ -867,10 +892,10 @@ hipError_t launch_gemm(asr_i8::GemmArgs args, int32_t rounding, hipStream_t s) {
   const int64_t grid = static_cast<int64_t>(args.tiles_m) * args.tiles_n;
   const bool rest = args.k % 16 != 0;
   if (rounding == ASR_ROUND_SR)
-    return rest ? launch(&gemm_i8<T, ASR_ROUND_SR, true>, grid, T::kThreads, &args, s)
-               : launch(&gemm_i8<T, ASR_ROUND_SR, false>, grid, T::kThreads, &args, s);
-  return rest ? launch(&gemm_i8<T, ASR_ROUND_RN, true>, grid, T::kThreads, &args, s)
-             : launch(&gemm_i8<T, ASR_ROUND_RN, false>, grid, T::kThreads, &args, s);
+    return rest ? launch(&gemm_i8<T, ASR_ROUND_SR, true, SPLIT>, grid, SPLIT * T::kThreads, &args, s)
+               : launch(&gemm_i8<T, ASR_ROUND_SR, false, SPLIT>, grid, SPLIT * T::kThreads, &args, s);
+  return rest ? launch(&gemm_i8<T, ASR_ROUND_RN, true, SPLIT>, grid, SPLIT * T::kThreads, &args, s)
+             : launch(&gemm_i8<T, ASR_ROUND_RN, false, SPLIT>, grid, SPLIT * T::kThreads, &args, s);
 }
 
 constexpr int64_t kCus = 256;  // compute units of an MI355X, one big tile each
@@ -903,13 +928,17 @@ hipError_t launch_few(asr_i8::GemmArgs args, int32_t rounding, hipStream_t s) {
 hipError_t product(const asr_i8::GemmArgs& g, int32_t rounding, hipStream_t s) {
   const int64_t m = g.m, n = g.n;
   auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
-  // Few rows: reading B is all there is. The kernel for them reads it at 4.3
-  // TB/s (1 x 14336 x 4096: 13.6 us); the 64 x 64 tile walks K alone where N
-  // gives few tiles (16 x 1024 x 4096: 5.9 against 11.1 us, 16 x 256 x 14336: 14.8
-  // against 30), but shares A better where there are many (16 x 14336 x
-  // 4096: 19.7 against 15.3 us; 64 x 4096 x 4096: 12.3 against 11.1).
+  // Few rows: reading B is all there is, and the kernel for them keeps more of
+  // it in flight than tiles do, with one workgroup for 16 columns on every
+  // compute unit (16 x 4096 x 4096: 7.3 us against 9.2 in 64 x 64 tiles; 16 x
+  // 256 x 14336: 14.8 against 21.9; 32 x 5120 x 5120, more of them than
+  // compute units: 16.0 against 10.8), or for any N up to 4 rows (1 x 28672 x
+  // 8192: 41.8 against 53.4), unless K is too short to split (1 x 100000 x 64:
+  // 21.0 against 11.3) or most compute units get one tile of two K ranges
+  // (1 x 14336 x 4096: 16.0 against 13.7, 4.3 TB/s; 1 x 8192 x 4096: 9.8 against 10.1).
   // (n below 2**26: a launch's threads)
-  if ((m <= 4 && n < (int64_t{1} << 26)) || (m <= 32 && m * n <= (int64_t{1} << 17)))
+  const bool one_each = n > 64 * (kCus / 2) && n <= 64 * kCus && g.k >= 2048;
+  if ((m <= 32 && n <= 16 * kCus) || (m <= 4 && g.k >= 512 && n < (int64_t{1} << 26) && !one_each))
     return m <= 16 ? launch_few<1>(g, rounding, s) : launch_few<2>(g, rounding, s);
   // (1000 x 14336 x 4096, 224 tiles of 256: 63 us, 80 us in 128 x 128 tiles;
   // 512 x 14336 x 4096, 112 of them: 55 and 44 us)
@@ -918,6 +947,9 @@ hipError_t product(const asr_i8::GemmArgs& g, int32_t rounding, hipStream_t s) {
   if (tiles(256) >= 192) return launch_gemm<asr_i8::Big>(g, rounding, s);
   if (tiles(128) > 256) return launch_gemm<asr_i8::Small>(g, rounding, s);
   if (tiles(128) > 128) return launch_gemm<asr_i8::Small8>(g, rounding, s);
+  // one tile or none a compute unit: two K ranges in it (333 x 1009 x 1111: 8.6 ->
+  // 8.1 us, 256 x 4096 x 4096: 12.2 -> 10.2, 100 x 200 x 8192: 19.4 -> 14.6)
+  if (tiles(64) <= kCus) return launch_gemm<asr_i8::Tiny, 2>(g, rounding, s);
   return launch_gemm<asr_i8::Tiny>(g, rounding, s);
 }
 

@@ -121,17 +121,23 @@ __device__ __forceinline__ void barrier_lds() {
 // One output tile's operands: `a` and `b` point at the tile's first rows;
 // last_a and last_b are the tile-relative indexes of the operands' last rows
 // (rows past them are clamped: they only feed outputs that are not stored).
-// kbytes: bytes of K, a multiple of 16; ld_a, ld_b in bytes, below 2**23.
+// kbytes: bytes of K, a multiple of 16; ktiles: K tiles to walk, at least those
+// that hold them (what lies past K counts as zeros, unread); ld_a, ld_b in
+// bytes, below 2**23.
 struct Operands {
   const char* a;
   const char* b;
   uint32_t ld_a, ld_b;
   int32_t last_a, last_b;
-  int32_t kbytes;
+  int32_t kbytes, ktiles;
 };
 
+__host__ __device__ constexpr int32_t ktiles_of(int32_t kbytes) { return (kbytes + kRowBytes - 1) / kRowBytes; }
+
 // acc[i][j] += the wave's 32 x 32 blocks of A * B^T over all of K. smem: T's
-// kLoopLds bytes. Every wave of the workgroup calls it. On return no copy is
+// kLoopLds bytes. Every wave of the workgroup calls it; a workgroup of several
+// times T's waves walks as many K ranges at once, each in an LDS part of its own,
+// with one ktiles for all of them (the barriers are the workgroup's). On return no copy is
 // in flight, but other waves may still read the LDS: a barrier has to come
 // before it is written.
 template <typename T, typename E>
@@ -141,11 +147,11 @@ __device__ __forceinline__ void mfma_loop(const Operands& op, unsigned char* sme
   constexpr int BM = T::BM, STAGES = T::STAGES;
   constexpr int kSteps = kRowBytes / 32;
   const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % T::kWaves;
   const bool copier = T::kCopyWaves == T::kWaves || wave < static_cast<uint32_t>(T::kCopyWaves);
   const uint32_t wm = wave / T::kWavesN, wn = wave % T::kWavesN;
   const uint32_t frag_row = lane & 31u, frag_half = lane >> 5;
-  const int ktiles = (op.kbytes + kRowBytes - 1) / kRowBytes;
+  const int ktiles = op.ktiles;
   const int kfull = op.kbytes / kRowBytes;
   if (ktiles == 0) return;
 
@@ -173,7 +179,7 @@ __device__ __forceinline__ void mfma_loop(const Operands& op, unsigned char* sme
         16, off, 0, 0, 0);
   };
   auto copy = [&](int stage, int j, int kt) { copy_at(stage, j, kt, voff[j]); };
-  // the last K tile when K is not a multiple of 128 bytes: chunks past K read zeros
+  // K tiles that K does not fill: chunks past K read zeros
   auto copy_tail = [&](int stage, int j, int kt) {
     const uint32_t row = (wave + j * T::kCopyWaves) * 8 + lane / 8;
     const int k = kt * kRowBytes + static_cast<int>(T::chunk_pos(row, lane % 8)) * 16;
@@ -213,7 +219,7 @@ __device__ __forceinline__ void mfma_loop(const Operands& op, unsigned char* sme
 
   int cur = 0;  // LDS buffer of tile kt
   // LOAD: the copies this body issues, of tile kt + STAGES: 0 none, 1 a whole
-  // tile, 2 the partial last one.
+  // tile, 2 one that K does not fill.
   auto tile_body = [&](int kt, auto load_c) {
     constexpr int LOAD = decltype(load_c)::value;
     const unsigned char* sa = smem + cur * T::kStageBytes;
@@ -276,10 +282,7 @@ __device__ __forceinline__ void mfma_loop(const Operands& op, unsigned char* sme
   };
   int kt = 0;
   for (; kt + STAGES < kfull; ++kt) tile_body(kt, std::integral_constant<int, 1>{});
-  if (kfull < ktiles && kt + STAGES == kfull) {
-    tile_body(kt, std::integral_constant<int, 2>{});
-    ++kt;
-  }
+  for (; kt + STAGES < ktiles; ++kt) tile_body(kt, std::integral_constant<int, 2>{});
   for (; kt < ktiles; ++kt) tile_body(kt, std::integral_constant<int, 0>{});
 }
 

@@ -451,6 +451,7 @@ __global__ __launch_bounds__(T::kThreads, T::kMinWaves) void product(ProductArgs
     asr_mfma::Operands op;
     op.ld_a = op.ld_b = static_cast<uint32_t>((MODE == kGram ? l.ld_t : l.ld_s) * 2);
     op.kbytes = static_cast<int32_t>(op.ld_a);
+    op.ktiles = asr_mfma::ktiles_of(op.kbytes);
     op.a = ws + (MODE == kGram ? l.x : MODE == kSquare ? l.a : l.wide ? l.b : y_now) + m0 * op.ld_a;
     op.b = ws + (MODE == kGram ? l.x : MODE == kSquare ? l.a : l.wide ? y_now : l.b) + n0 * op.ld_b;
     op.last_a = m_all - 1 - static_cast<int32_t>(m0);

@@ -515,3 +515,13 @@ def test_gradients_against_formula_and_differences(shape, grad_rounding, step):
         if t * n * k < 20000:   # (a worst case added up over more says nothing)
             assert limit < 0.5 * abs(change)
         assert abs(change - np.sum(values[name] * along)) <= limit, name
+
+
+@pytest.mark.parametrize("shape", [(65, 63, 8191), (40, 300, 1100), (40, 4500, 130), (3, 9000, 2070),
+                                   (6, 5000, 500), (40, 70, 15), (700, 1700, 200), (2, 9000, 300),
+                                   (64, 64, 256), (200, 100, 2 ** 17 - 1)])
+def test_product_in_two_ranges_of_k(shape):
+    """Products of few tiles, whose workgroups walk two ranges of K at once (the
+    second one empty, shorter, or ending inside a row's last codes), and their
+    neighbours that do not."""
+    test_product(shape)
