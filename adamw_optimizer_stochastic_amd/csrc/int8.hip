@@ -135,13 +135,6 @@ __device__ __forceinline__ void load8(const S* row, int64_t j, int64_t cols, boo
   }
 }
 
-__device__ __forceinline__ void random8(uint64_t p, uint32_t seed, uint32_t step,
-                                        uint32_t (&lo)[4], uint32_t (&hi)[4]) {
-  const bool aligned = (p & 3u) == 0;
-  asr_mfma::random4(p, aligned, seed, step, lo);
-  asr_mfma::random4(p + 4, aligned, seed, step, hi);
-}
-
 // A matrix of a launch, and the codes wanted of it: of its rows, of its
 // columns, or both.
 struct QuantJob {
@@ -223,10 +216,13 @@ __global__ __launch_bounds__(256) void quantize_rows(QuantArgs args) {
   if (lane == 0) a.s_row[row] = s;
   int8_t* q = a.q_row + row * a.ld_row;
   auto codes = [&](int32_t run, const float (&t)[8]) {
-    uint32_t r0[4] = {}, r1[4] = {};
-    if constexpr (SR)
-      random8(a.base + static_cast<uint64_t>(row) * static_cast<uint64_t>(a.cols) +
-                  static_cast<uint64_t>(run) * 8, args.seed, args.step, r0, r1);
+    uint32_t bits[8] = {};
+    if constexpr (SR) {
+      const uint64_t p = a.base + static_cast<uint64_t>(row) * static_cast<uint64_t>(a.cols) +
+                         static_cast<uint64_t>(run) * 8;
+      asr_mfma::random_run<8>(p, (p & 3u) == 0, args.seed, args.step, bits);
+    }
+    const uint32_t r0[4] = {bits[0], bits[1], bits[2], bits[3]}, r1[4] = {bits[4], bits[5], bits[6], bits[7]};
     const float t0[4] = {t[0], t[1], t[2], t[3]}, t1[4] = {t[4], t[5], t[6], t[7]};
     *reinterpret_cast<asr::u32x2*>(q + static_cast<int64_t>(run) * 8) =
         asr::u32x2{codes4<SR>(t0, g, r0), codes4<SR>(t1, g, r1)};
@@ -425,20 +421,21 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[i][e] = raw[i].get(e);
     if (tr + 1 < tr1) fetch(tr + 1);
-    uint32_t bits[4][2][4] = {};
+    uint32_t bits[4][8] = {};
     if constexpr (SR) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        random8(a.base + static_cast<uint64_t>(r0 + rg * 4 + i) * static_cast<uint64_t>(a.cols) +
-                    static_cast<uint64_t>(col), args.seed, args.step, bits[i][0], bits[i][1]);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t p = a.base + static_cast<uint64_t>(r0 + rg * 4 + i) * static_cast<uint64_t>(a.cols) +
+                           static_cast<uint64_t>(col);
+        asr_mfma::random_run<8>(p, (p & 3u) == 0, args.seed, args.step, bits[i]);
+      }
     }
     __syncthreads();  // the scales are there, the last tile's codes are read
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const GroupScale g = lds.col_scale[cg * 8 + e];
       const float v[4] = {x[0][e], x[1][e], x[2][e], x[3][e]};
-      const uint32_t r[4] = {bits[0][e / 4][e % 4], bits[1][e / 4][e % 4], bits[2][e / 4][e % 4],
-                             bits[3][e / 4][e % 4]};
+      const uint32_t r[4] = {bits[0][e], bits[1][e], bits[2][e], bits[3][e]};
       lds.tile[(cg * 8 + e) * kWords + rg] = codes4<SR>(v, g, r);
     }
     if (a.q_row) {
@@ -448,7 +445,9 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
         const GroupScale g = lds.row_scale[rg * 4 + i];
         const float v0[4] = {x[i][0], x[i][1], x[i][2], x[i][3]};
         const float v1[4] = {x[i][4], x[i][5], x[i][6], x[i][7]};
-        const asr::u32x2 w = {codes4<SR>(v0, g, bits[i][0]), codes4<SR>(v1, g, bits[i][1])};
+        const uint32_t b0[4] = {bits[i][0], bits[i][1], bits[i][2], bits[i][3]};
+        const uint32_t b1[4] = {bits[i][4], bits[i][5], bits[i][6], bits[i][7]};
+        const asr::u32x2 w = {codes4<SR>(v0, g, b0), codes4<SR>(v1, g, b1)};
         if (r < a.rows && col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16)
           *reinterpret_cast<asr::u32x2*>(a.q_row + r * a.ld_row + col) = w;
       }
@@ -615,18 +614,17 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& args, int64_t m0, int6
       const int64_t m = m0 + wm * T::WM + i * 32 + r;
       if (m >= args.m || count == 0) return;
       const float sa = args.sa[m];
-      uint32_t r0[4] = {}, r1[4] = {}, h[8];
+      uint32_t bits[8] = {}, h[8];
       if constexpr (ROUND == ASR_ROUND_SR) {
         const uint64_t pos = args.base_index + static_cast<uint64_t>(m) * static_cast<uint64_t>(args.n) +
                              static_cast<uint64_t>(n);
-        asr_mfma::random4(pos, args.pos4 != 0, args.seed, args.step, r0);
-        asr_mfma::random4(pos + 4, args.pos4 != 0, args.seed, args.step, r1);
+        asr_mfma::random_run<8>(pos, args.pos4 != 0, args.seed, args.step, bits);
       }
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] = (static_cast<float>(static_cast<int32_t>(raw[e])) * sa) * sb[e];
-        h[e] = round_one<ROUND>(x[e], e < 4 ? r0[e] : r1[e - 4]);
+        h[e] = round_one<ROUND>(x[e], bits[e]);
       }
       const int64_t at = m * args.ldc + n;
       if (args.vec16 && count == 8) {
@@ -753,7 +751,7 @@ __global__ __launch_bounds__(512) void gemm_i8_few(GemmArgs args) {
   uint32_t r16[4] = {}, h[4];
   float x[4];
   if constexpr (ROUND == ASR_ROUND_SR)
-    asr_mfma::random4(args.base_index + static_cast<uint64_t>(m) * static_cast<uint64_t>(args.n) +
+    asr_mfma::random_run<4>(args.base_index + static_cast<uint64_t>(m) * static_cast<uint64_t>(args.n) +
                           static_cast<uint64_t>(n), args.pos4 != 0, args.seed, args.step, r16);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {

@@ -365,17 +365,14 @@ __device__ __forceinline__ void store_out(const OutArgs& out, const Desc& d, int
     if (vec) asr::load_vec<false, V>(p + at, x);
     else asr::load_range<V>(p, at, 0, n, x);
     const uint64_t pos = d.base + static_cast<uint64_t>(at);
+    uint32_t r16[V] = {};
+    if constexpr (OUT == kOutWeightBf16Sr)
+      asr_mfma::random_run<V>(pos, (pos & 3u) == 0, out.seed, out.step, r16);
 #pragma unroll
-    for (int q = 0; q < V / 4; ++q) {
-      uint32_t r16[4] = {};
-      if constexpr (OUT == kOutWeightBf16Sr)
-        asr_mfma::random4(pos + 4 * q, (pos & 3u) == 0, out.seed, out.step, r16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float y = x[4 * q + e] * out.decay - d.eta * o[4 * q + e];
-        h[4 * q + e] = OUT == kOutWeightBf16Sr ? asr::round_sr(__float_as_uint(y), r16[e])
-                                               : asr::round_rn(__float_as_uint(y));
-      }
+    for (int e = 0; e < V; ++e) {
+      const float y = x[e] * out.decay - d.eta * o[e];
+      h[e] = OUT == kOutWeightBf16Sr ? asr::round_sr(__float_as_uint(y), r16[e])
+                                     : asr::round_rn(__float_as_uint(y));
     }
   }
   if (vec) asr::store_vec_bf16<false, V>(p + at, h);
