@@ -515,7 +515,8 @@ __device__ __forceinline__ void store4(const GemmArgs& args, int64_t at, int cou
 }
 
 // The tile of C from (m0, n0). Bound by the matrix instructions and what keeps
-// them fed (58% of the cycles busy at 8192 x 14336 x 4096, 433 us, 2.2 POP/s);
+// them fed (58% of the cycles busy at 8192 x 14336 x 4096: 433-444 us, 2.2 POP/s;
+// 450 with stochastic rounding);
 // the epilogue is the part no other work covers, so its stores go in whole
 // lines. REST: K is not a multiple of 16 (a variant of
 // its own: its byte loads cost the largest tile registers that it has not

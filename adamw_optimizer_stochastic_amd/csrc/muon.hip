@@ -383,10 +383,10 @@ __device__ __forceinline__ void store_out(const OutArgs& out, const Desc& d, int
 // TFLOP/s on large matrices (f16 products of the library: 1481 for 8192^3);
 // what it leaves is the epilogue, which nothing else covers: a tile that
 // updates X reads 4 and writes 6 bytes an element, all tiles of a round at
-// once. 4096 x 4096, 1024 x 4096, 14336 x 4096 and 4096 x 14336 together: A 611
-// to 643 us, B 221, the new X 1080, the weights 1110 (in 256 tiles, A in 192).
-// 8 x 1024 x 4096: A 62-71, B 23-27, X 113-124 (360 MB, 3.2 TB/s), where the 52 us
-// of K loops are less than the traffic. X and what the last product adds to
+// once. 4096 x 4096, 1024 x 4096, 14336 x 4096 and 4096 x 14336 together: A 620
+// to 680 us, B 210-230, the new X 1040-1100, the weights 1085-1110 (in 256
+// tiles, A in 192). 8 x 1024 x 4096: A 62-70, B 23-27, X 111-122, where the 52 us of K
+// loops are less than the traffic. X and what the last product adds to
 // are fetched a block ahead of their use (4096 x 14336: 4132 against 4168 us for all
 // five steps).
 template <typename T, int MODE, int OUT>
