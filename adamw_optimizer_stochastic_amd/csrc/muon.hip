@@ -723,8 +723,10 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_matrix(SmallArgs args)
     E::acc aa = {};
     if (squares) {
       dot(aa, x, ld_x, sj, x, ld_x, si, tb);
+      // (b A takes the same rounded A as c A A: near singular values of 1 the two
+      // terms' slopes, -4.8 and 4.1, all but cancel what the rounding costs)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) aa[r] *= gram_scale;
+      for (int r = 0; r < 16; ++r) aa[r] = static_cast<float>(static_cast<_Float16>(aa[r] * gram_scale));
       put_square(gram, aa);
     }
     __syncthreads();

@@ -485,7 +485,7 @@ def newton_schulz(g, *, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=Non
     g: float32 or bfloat16, (M, N) or (B, M, N), contiguous. X = g / (|g|_F +
     eps), then ``steps`` times X = a X + (b A + c A A) X with A = X X^T (on
     the short side); the result is bfloat16 (nearest even) of g's shape.
-    About 2e-3 of it (relative, Frobenius norm) from the exact value: f16
+    2e-3 to 3e-3 of it (relative, Frobenius norm) from the exact value: f16
     products with f32 sums, X held as two f16 numbers. A g of zeros gives
     zeros, a matrix with an Inf or NaN only NaN. ``out``: bfloat16, g's shape,
     contiguous (g itself if it is bfloat16).

@@ -372,8 +372,10 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
  * With (a, b, c) = (3.4445, -4.775, 2.0315) and 5 steps, singular values from
  * about 1/100 of |G|_F up come out between about 0.7 and 1.2 (the update of
  * the Muon optimizer). The products run on the matrix cores with f16 operands
- * and f32 sums, X itself held as two f16 numbers: the result is within about
- * 2e-3 (relative, Frobenius norm) of the exact one, low-rank G included. The norm is
+ * and f32 sums, X itself held as two f16 numbers: the result is within 2e-3 to
+ * 3e-3 (relative, Frobenius norm, the bf16 rounding included) of the exact one,
+ * low-rank G included; a G of one row or column, whose few roundings do not
+ * average, within 4.5e-2 at worst. The norm is
  * summed in 64 bits. A G of zeros gives zeros (with eps > 0); an Inf or NaN in G makes all
  * of its result NaN.
  *
