@@ -54,6 +54,7 @@ def uniform_(tensor, low=0.0, high=1.0, *, seed, step=0, base_index=0):
         _abi.asr_random_uniform(tensor.data_ptr(), code, tensor.numel(), float(low), float(high),
                                 _u32("seed", seed), _u32("step", step), _u64(base_index),
                                 _stream(tensor.device))
+    ops._written(tensor)
     return tensor
 
 
@@ -66,6 +67,7 @@ def normal_(tensor, mean=0.0, std=1.0, *, seed, step=0, base_index=0):
         _abi.asr_random_normal(tensor.data_ptr(), code, tensor.numel(), float(mean), float(std),
                                _u32("seed", seed), _u32("step", step), _u64(base_index),
                                _stream(tensor.device))
+    ops._written(tensor)
     return tensor
 
 
@@ -99,4 +101,6 @@ def dropout(x, p=0.5, *, seed, step=0, base_index=0, training=True, inplace=Fals
         _abi.asr_dropout(x.data_ptr(), y.data_ptr(), mask.data_ptr() if mask is not None else None,
                          code, x.numel(), float(p), _u32("seed", seed), _u32("step", step),
                          _u64(base_index), _stream(x.device))
+    if inplace:
+        ops._written(y)
     return (y, mask.view(torch.bool)) if return_mask else y
