@@ -470,6 +470,7 @@ def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index
 
 
 NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+MUON_MAX_SIDE = 1 << 20
 
 
 def _coefficients(c):
@@ -587,6 +588,9 @@ def muon_step(params, grads, momenta, base_indices, *, lr, momentum=0.95, nester
         if g.shape != p.shape or m.shape != p.shape:
             raise ValueError(f"matrix {i}: param, grad and momentum differ in shape")
         rows, cols = p.shape
+        # (the library's own limit, here for all types' lists before the first is launched)
+        if max(rows, cols) > MUON_MAX_SIDE:
+            raise ValueError(f"matrix {i}: sides must be at most 2**20")
         groups.setdefault((p.dtype, g.dtype), []).append(
             (p.data_ptr(), g.data_ptr(), m.data_ptr(), rows, cols,
              _u64(f"base_indices[{i}]", base), muon_lr_factor(rows, cols, adjust_lr)))

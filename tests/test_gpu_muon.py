@@ -480,3 +480,16 @@ def test_workspace_may_not_be_the_data():
     assert bool((g == 1).all()) and bool((out == 0).all())
     ops.newton_schulz(g, out=out, workspace=raw[:need])
     assert torch.equal(out, ops.newton_schulz(g))
+
+
+def test_refused_list_changes_nothing():
+    """A matrix that only a later type's list would refuse: no matrix of the
+    types before it has moved, so a step taken again is not taken twice."""
+    announce("muon refusal before the first launch")
+    (p,), (g,), (m,) = _state([(40, 70)], torch.bfloat16, torch.bfloat16)
+    long = [torch.zeros(1, 2 ** 20 + 1, device="cuda") for _ in range(3)]
+    q, n = p.clone(), m.clone()
+    with pytest.raises((ValueError, ops.AsrError), match="2\\*\\*20"):
+        ops.muon_step([q, long[0]], [g, long[1]], [n, long[2]], [0, 0], lr=0.1, step=1, seed=0)
+    torch.cuda.synchronize()
+    assert torch.equal(q, p) and torch.equal(n, m)
