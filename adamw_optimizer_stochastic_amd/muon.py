@@ -15,6 +15,9 @@ which is what fills the chip with small ones. A step captured into a graph
 repeats its number, learning rate and bits on every replay.
 """
 
+import math
+import operator
+
 import torch
 
 from . import ops
@@ -23,44 +26,66 @@ from .optim import _step_count
 __all__ = ["MuonSR"]
 
 
+def _checked(group):
+    """A group's options as a step takes them, or an error."""
+    o = {k: group[k] for k in ("lr", "weight_decay", "momentum", "nesterov", "ns_coefficients",
+                               "eps", "ns_steps", "adjust_lr_fn", "rounding")}
+    if isinstance(o["lr"], torch.Tensor):
+        raise NotImplementedError("MuonSR: tensor lr is not supported")
+    if not 0.0 <= o["lr"] < math.inf:
+        raise ValueError(f"Invalid learning rate: {o['lr']}")
+    if not 0.0 <= o["weight_decay"] < math.inf:
+        raise ValueError(f"Invalid weight_decay value: {o['weight_decay']}")
+    if not 0.0 <= o["momentum"] < 1.0:
+        raise ValueError(f"Invalid momentum value: {o['momentum']}")
+    if not 0.0 <= o["eps"] < math.inf:
+        raise ValueError(f"Invalid epsilon value: {o['eps']}")
+    if not 1 <= o["ns_steps"] <= 64:
+        raise ValueError("ns_steps must be in [1, 64]")
+    if o["rounding"] not in ("sr", "rn"):
+        raise ValueError("rounding must be 'sr' or 'rn'")
+    o["ns_steps"] = operator.index(o["ns_steps"])
+    o["ns_coefficients"] = ops._coefficients(o["ns_coefficients"])
+    if o["adjust_lr_fn"] is None:
+        o["adjust_lr_fn"] = "original"
+    ops.muon_lr_factor(1, 1, o["adjust_lr_fn"])
+    return o
+
+
+def _check_param(p):
+    if p.dim() != 2:
+        raise ValueError(f"MuonSR takes 2-D parameters (got shape {tuple(p.shape)})")
+    if p.is_sparse or p.is_complex() or p.dtype not in (torch.float32, torch.bfloat16):
+        raise NotImplementedError(f"MuonSR supports dense float32/bfloat16 params (got {p.dtype})")
+    if max(p.shape) > ops.MUON_MAX_SIDE:
+        raise ValueError(f"MuonSR takes sides of at most 2**20 (got shape {tuple(p.shape)})")
+
+
 class MuonSR(torch.optim.Optimizer):
     def __init__(self, params, lr=1e-3, weight_decay=0.1, momentum=0.95, nesterov=True,
                  ns_coefficients=ops.NS_COEFFICIENTS, eps=1e-7, ns_steps=5, adjust_lr_fn=None,
                  *, seed=0, rounding="sr", base_offset=0):
-        if isinstance(lr, torch.Tensor):
-            raise NotImplementedError("MuonSR: tensor lr is not supported")
-        if not 0.0 <= lr:
-            raise ValueError(f"Invalid learning rate: {lr}")
-        if not 0.0 <= weight_decay:
-            raise ValueError(f"Invalid weight_decay value: {weight_decay}")
-        if not 0.0 <= momentum < 1.0:
-            raise ValueError(f"Invalid momentum value: {momentum}")
-        if not 0.0 <= eps:
-            raise ValueError(f"Invalid epsilon value: {eps}")
-        if not 1 <= ns_steps <= 64:
-            raise ValueError("ns_steps must be in [1, 64]")
-        if rounding not in ("sr", "rn"):
-            raise ValueError("rounding must be 'sr' or 'rn'")
         if not (isinstance(seed, int) and 0 <= seed < (1 << 32)):
             raise ValueError("seed must be an integer in [0, 2**32)")
-        adjust_lr_fn = "original" if adjust_lr_fn is None else adjust_lr_fn
-        ops.muon_lr_factor(1, 1, adjust_lr_fn)
         self.seed = seed
         self._base_index = {}
         self._next_index = ops._u64("base_offset", base_offset)
-        defaults = dict(lr=lr, weight_decay=weight_decay, momentum=momentum, nesterov=nesterov,
-                        ns_coefficients=ops._coefficients(ns_coefficients), eps=eps,
-                        ns_steps=ns_steps, adjust_lr_fn=adjust_lr_fn, rounding=rounding)
+        defaults = _checked(dict(lr=lr, weight_decay=weight_decay, momentum=momentum,
+                                 nesterov=nesterov, ns_coefficients=ns_coefficients, eps=eps,
+                                 ns_steps=ns_steps, adjust_lr_fn=adjust_lr_fn, rounding=rounding))
         super().__init__(params, defaults)
 
     def add_param_group(self, param_group):
         super().add_param_group(param_group)
-        for p in self.param_groups[-1]["params"]:
-            if p.dim() != 2:
-                raise ValueError(f"MuonSR takes 2-D parameters (got shape {tuple(p.shape)})")
-            if p.is_sparse or p.is_complex() or p.dtype not in (torch.float32, torch.bfloat16):
-                raise NotImplementedError(
-                    f"MuonSR supports dense float32/bfloat16 params (got {p.dtype})")
+        group = self.param_groups[-1]
+        try:   # (torch's own form of the group is what is checked; a refused one leaves again)
+            group.update(_checked(group))
+            for p in group["params"]:
+                _check_param(p)
+        except Exception:
+            self.param_groups.pop()
+            raise
+        for p in group["params"]:
             self._base_index[p] = self._next_index
             self._next_index += p.numel()
 

@@ -218,3 +218,42 @@ def test_first_step_is_not_captured(monkeypatch):
     opt = MuonSR([_param(4, 6)])
     with pytest.raises(RuntimeError, match="before capturing"):
         opt._init_state(OnGpu())
+
+
+BAD_OPTIONS = (dict(lr=-1.0), dict(lr=float("inf")), dict(weight_decay=-1.0),
+               dict(weight_decay=float("nan")), dict(momentum=1.0), dict(momentum=2.0),
+               dict(eps=-1.0), dict(eps=float("inf")), dict(ns_steps=0), dict(ns_steps=65),
+               dict(rounding="xx"), dict(adjust_lr_fn="x"), dict(ns_coefficients=(1.0,)))
+
+
+@pytest.mark.parametrize("kw", BAD_OPTIONS, ids=str)
+def test_options_of_a_group_are_checked(kw):
+    """As the constructor's are; the refused group leaves nothing behind."""
+    a = _param(4, 6)
+    opt = MuonSR([a], base_offset=5)
+    with pytest.raises(ValueError):
+        MuonSR([_param(4, 6)], **kw)
+    with pytest.raises(ValueError):
+        MuonSR([dict(params=[_param(4, 6)], **kw)])
+    with pytest.raises(ValueError):
+        opt.add_param_group(dict(params=[_param(4, 6)], **kw))
+    assert len(opt.param_groups) == 1 and len(opt._base_index) == 1 and opt._next_index == 29
+
+
+def test_refused_groups_leave_nothing_behind():
+    opt = MuonSR([_param(4, 6)])
+    tensor_lr, float_steps = dict(lr=torch.tensor(0.1)), dict(ns_steps=2.5)
+    for params, kw, error in (([_param(4)], {}, ValueError),
+                              ([_param(3, 3), _param(2, 2, 2)], {}, ValueError),
+                              ([_param(0, 2 ** 20 + 1)], {}, ValueError),
+                              ([_param(3, 3, dtype=torch.float64)], {}, NotImplementedError),
+                              ([_param(3, 3)], tensor_lr, NotImplementedError),
+                              ([_param(3, 3)], float_steps, TypeError)):
+        with pytest.raises(error):
+            opt.add_param_group(dict(params=params, **kw))
+        assert len(opt.param_groups) == 1 and len(opt._base_index) == 1
+    b = _param(2, 5)
+    opt.add_param_group(dict(params=(p for p in [b]), adjust_lr_fn=None, ns_coefficients=[2, -1.5, 0.5]))
+    assert opt.base_index(b) == 24   # the refused ones took no positions
+    assert opt.param_groups[1]["adjust_lr_fn"] == "original"
+    assert opt.param_groups[1]["ns_coefficients"] == (2.0, -1.5, 0.5)
