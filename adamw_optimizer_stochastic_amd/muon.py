@@ -10,7 +10,11 @@ share positions (give MuonSR the number of elements AdamWSR has).
 
 For each matrix: m = momentum*m + g (f32), u = g + momentum*m (nesterov) or m,
 p = p*(1 - lr*weight_decay) - lr*factor*O(u), O the Newton-Schulz
-orthogonalisation. All matrices of a group go through the products together,
+orthogonalisation. torch.optim.Muon keeps the average (1 - momentum)*m instead
+and divides by max(|u|, eps) where this divides by |u| + eps: with a momentum
+that stays the same the steps are the same but for eps, with one that changes
+they are not (there the average's weight of old gradients stays, here their
+sum's). All matrices of a group go through the products together,
 which is what fills the chip with small ones. A step captured into a graph
 repeats its number, learning rate and bits on every replay.
 """
@@ -140,23 +144,41 @@ class MuonSR(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """Like torch's, except that the momentum stays float32 whatever the
-        parameter dtype (torch's loader would cast it)."""
+        parameter dtype (torch's loader would cast it).
+
+        Also takes a state of torch.optim.Muon, whose buffer is 1 - momentum times
+        this one's and which counts no steps (here from 0); options it does not have
+        stay as they are. A state that does not fit is refused before anything changes.
+        """
         extra = state_dict.get("muon_sr")
-        saved_state = state_dict.get("state", {})
-        plain = {k: v for k, v in state_dict.items() if k not in ("muon_sr", "state")}
-        plain["state"] = {}
-        super().load_state_dict(plain)
-        saved_ids = [i for g in state_dict["param_groups"] for i in g["params"]]
-        params = [p for g in self.param_groups for p in g["params"]]
-        for p in params:
-            self.state.pop(p, None)
-        for p, pid in zip(params, saved_ids):
-            st = saved_state.get(pid)
-            if st is None:
-                continue
+        saved_state, saved_groups = state_dict.get("state", {}), state_dict["param_groups"]
+        groups, loaded = [], []
+        for group, saved in zip(self.param_groups, saved_groups):
+            merged = {k: v for k, v in group.items() if k not in ("params", "param_names")} | saved
+            groups.append(merged | _checked(merged))
+            for p, pid in zip(group["params"], saved["params"]):
+                st = saved_state.get(pid)
+                if st is None:
+                    continue
+                m = st.get("momentum_buffer")
+                if not isinstance(m, torch.Tensor) or m.numel() != p.numel():
+                    raise ValueError("MuonSR: the state of a parameter of shape "
+                                     f"{tuple(p.shape)} has no momentum_buffer of its size")
+                ours = "step" in st
+                loaded.append((p, _step_count(st["step"]) if ours else 0, m.detach().reshape(p.shape),
+                               1.0 if ours else 1.0 - merged["momentum"]))
+        if len(groups) == len(saved_groups):
+            saved_groups = groups   # (a different number of groups is torch's to refuse)
+        super().load_state_dict({**{k: v for k, v in state_dict.items() if k != "muon_sr"},
+                                 "state": {}, "param_groups": saved_groups})
+        for group in self.param_groups:
+            for p in group["params"]:
+                self.state.pop(p, None)
+        for p, step, m, scale in loaded:
             self._init_state(p)
-            self.state[p]["step"].fill_(_step_count(st["step"]))
-            self.state[p]["momentum_buffer"].copy_(
-                st["momentum_buffer"].detach().reshape(p.shape))
+            self.state[p]["step"].fill_(step)
+            self.state[p]["momentum_buffer"].copy_(m)
+            if scale != 1.0:
+                self.state[p]["momentum_buffer"].div_(scale)
         if extra is not None:
             self.seed = int(extra["seed"])

@@ -493,3 +493,60 @@ def test_refused_list_changes_nothing():
         ops.muon_step([q, long[0]], [g, long[1]], [n, long[2]], [0, 0], lr=0.1, step=1, seed=0)
     torch.cuda.synchronize()
     assert torch.equal(q, p) and torch.equal(n, m)
+
+
+def _newton_schulz_bf16(u):
+    """The scheme that torch.optim.Muon's documentation names: products of bf16
+    matrices (sums in binary64 here, every result rounded to bf16)."""
+    def r(x):
+        return x.to(torch.bfloat16).double()
+
+    a, b, c = om.COEFFICIENTS
+    x = r(u if u.shape[0] <= u.shape[1] else u.T)
+    x = r(x / torch.linalg.norm(x))
+    for _ in range(5):
+        gram = r(x @ x.T)
+        x = r(a * x + r(b * gram + c * r(gram @ gram)) @ x)
+    return x if u.shape[0] <= u.shape[1] else x.T
+
+
+@pytest.mark.parametrize("nesterov", [True, False], ids=["nesterov", "plain"])
+@pytest.mark.parametrize("adjust", [None, "match_rms_adamw"])
+def test_against_torch_muon(adjust, nesterov):
+    """Three steps of torch.optim.Muon (on the CPU) and of MuonSR on f32 weights,
+    then a fourth of a MuonSR that was given torch's state: apart by twice what
+    the bf16 scheme and this one are off, a step (a wrong scale of the momentum
+    would turn u: the gradients of the steps are independent)."""
+    announce("MuonSR against torch.optim.Muon", adjust, nesterov)
+    shapes = [(48, 96), (150, 200), (200, 70)]
+    kw = dict(lr=0.05, weight_decay=0.2, momentum=0.9, nesterov=nesterov, adjust_lr_fn=adjust)
+    start = [_matrix("normal", *s, seed=i, dtype=torch.float32) * 20 for i, s in enumerate(shapes)]
+    theirs = [torch.nn.Parameter(p.cpu()) for p in start]
+    mine = [torch.nn.Parameter(p.clone()) for p in start]
+    opt_t, opt_m = torch.optim.Muon(theirs, **kw), MuonSR(mine, **kw)
+    limit, m64 = [0.0] * 3, [torch.zeros(s, dtype=torch.float64, device="cuda") for s in shapes]
+
+    def one(params, opt, t):
+        for i, (p, q) in enumerate(zip(theirs, params)):
+            g = _matrix("normal", *shapes[i], seed=10 * t + i, dtype=torch.float32)
+            p.grad, q.grad = g.cpu(), g
+            m64[i] = 0.9 * m64[i] + g.double()
+            u = g.double() + 0.9 * m64[i] if nesterov else m64[i]
+            o = om.newton_schulz(u)
+            off = om.relative(_newton_schulz_bf16(u), o) + om.relative(om.newton_schulz_f16(u), o) + SUMS
+            eta = 0.05 * ops.muon_lr_factor(*shapes[i], adjust or "original")
+            limit[i] += 2 * off * eta * torch.linalg.norm(o).item()
+        opt_t.step()
+        opt.step()
+        for i, (p, q) in enumerate(zip(theirs, params)):
+            d = torch.linalg.norm(p.detach().double() - q.detach().double().cpu()).item()
+            assert d <= limit[i], (t, i)
+
+    for t in (1, 2, 3):
+        one(mine, opt_m, t)
+    moved = [torch.nn.Parameter(p.detach().cuda()) for p in theirs]
+    opt = MuonSR(moved, lr=1.0)
+    opt.load_state_dict(opt_t.state_dict())
+    assert opt.param_groups[0]["lr"] == 0.05
+    limit = [0.0] * 3
+    one(moved, opt, 4)

@@ -257,3 +257,49 @@ def test_refused_groups_leave_nothing_behind():
     assert opt.base_index(b) == 24   # the refused ones took no positions
     assert opt.param_groups[1]["adjust_lr_fn"] == "original"
     assert opt.param_groups[1]["ns_coefficients"] == (2.0, -1.5, 0.5)
+
+
+def test_state_of_torch_muon_is_taken():
+    """Its buffer is 1 - momentum times this one's; it has no step count and no
+    rounding."""
+    a, b = _param(3, 4), _param(5, 2)
+    theirs = torch.optim.Muon([dict(params=[a], momentum=0.5), dict(params=[b], lr=0.25)])
+    for p in (a, b):
+        p.grad = torch.full_like(p, 3.0)
+    theirs.step()
+    mine = [_param(3, 4), _param(5, 2, dtype=torch.bfloat16)]
+    opt = MuonSR([dict(params=[p]) for p in mine], seed=3, rounding="rn")
+    opt.load_state_dict(theirs.state_dict())
+    for p in mine:   # one step's sum is its gradient; two factors and a quotient rounded to binary32
+        st = opt.state[p]
+        assert st["momentum_buffer"].dtype == torch.float32 and int(st["step"]) == 0
+        assert torch.allclose(st["momentum_buffer"], torch.full((), 3.0), rtol=2.0 ** -21)
+    one, two = opt.param_groups
+    assert (one["momentum"], two["momentum"], two["lr"]) == (0.5, 0.95, 0.25)
+    assert one["adjust_lr_fn"] == "original" and one["rounding"] == "rn" and opt.seed == 3
+
+
+def test_state_that_does_not_fit_changes_nothing():
+    p = _param(3, 4)
+    opt = MuonSR([p], lr=0.5, seed=3)
+    opt._init_state(p)
+    opt.state[p]["momentum_buffer"].fill_(2.0)
+    opt.state[p]["step"].fill_(4)
+    good = opt.state_dict()
+
+    def but(state=None, **group):
+        sd = dict(good, param_groups=[dict(good["param_groups"][0], **group)])
+        return sd if state is None else dict(sd, state={0: state})
+
+    for sd, match in ((but(dict(step=1, exp_avg=torch.ones(3, 4))), "momentum_buffer"),
+                      (but(dict(step=1, momentum_buffer=torch.ones(3, 5))), "momentum_buffer"),
+                      (but(dict(step=1.5, momentum_buffer=torch.ones(3, 4))), "step count"),
+                      (but(lr=-1.0), "learning rate"), (but(rounding="xx"), "rounding")):
+        with pytest.raises(ValueError, match=match):
+            opt.load_state_dict(sd)
+        assert opt.param_groups[0]["lr"] == 0.5 and int(opt.state[p]["step"]) == 4
+        assert bool((opt.state[p]["momentum_buffer"] == 2.0).all())
+    with pytest.raises(ValueError, match="parameter group"):
+        opt.load_state_dict(dict(good, param_groups=good["param_groups"] * 2))
+    opt.load_state_dict(good)
+    assert int(opt.state[p]["step"]) == 4
