@@ -182,11 +182,23 @@ class AdamWSR(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """Like torch's, except that the moment states stay float32 whatever
-        the parameter dtype (torch's loader would cast them to it)."""
+        the parameter dtype (torch's loader would cast them to it). Options that
+        a saved group lacks (the rounding, in one of torch.optim.AdamW) stay as
+        they are."""
         extra = state_dict.get("adamw_sr")
         saved_state = state_dict.get("state", {})
         plain = {k: v for k, v in state_dict.items() if k not in ("adamw_sr", "state")}
         plain["state"] = {}
+        for g in plain["param_groups"]:
+            on = [k for k in ("amsgrad", "maximize", "capturable", "differentiable") if g.get(k)]
+            coupled = not g.get("decoupled_weight_decay", True) and g.get("weight_decay", 0) != 0
+            if on or coupled or isinstance(g["lr"], torch.Tensor):
+                raise NotImplementedError("AdamWSR: the state's groups use " + (
+                    " and ".join(on) or "a tensor lr or weight decay in the gradient"))
+        if len(plain["param_groups"]) == len(self.param_groups):
+            plain["param_groups"] = [
+                {k: v for k, v in mine.items() if k not in ("params", "param_names")} | g
+                for mine, g in zip(self.param_groups, plain["param_groups"])]
         super().load_state_dict(plain)
         saved_ids = [i for g in state_dict["param_groups"] for i in g["params"]]
         params = [p for g in self.param_groups for p in g["params"]]

@@ -126,3 +126,27 @@ def test_moment_states_are_views_of_flat_buffers():
     assert opt.state[late]["exp_avg"].untyped_storage().data_ptr() != \
         opt.state[ps[0]]["exp_avg"].untyped_storage().data_ptr()
     assert int(opt.state[late]["step"]) == 0
+
+
+def test_state_of_torch_adamw_is_taken(monkeypatch):
+    """Its groups have no rounding: this optimizer's stays, and a step runs with
+    it. Groups whose options are not computed here are refused."""
+    from adamw_optimizer_stochastic_amd import optim as optim_mod
+    p, q = (torch.nn.Parameter(torch.zeros(6)) for _ in range(2))
+    p.grad, q.grad = torch.ones(6), torch.ones(6)
+    theirs = torch.optim.AdamW([p], lr=0.5)
+    theirs.step()
+    opt = AdamWSR([q], rounding="rn")
+    opt.load_state_dict(theirs.state_dict())
+    seen = []
+    monkeypatch.setattr(optim_mod.ops, "adamw_step", lambda *a, **kw: seen.append(kw))
+    monkeypatch.setattr(opt, "_workspace", lambda device, numels: None)
+    opt.step()
+    assert (seen[0]["rounding"], seen[0]["lr"], seen[0]["step"]) == ("rn", 0.5, 2)
+    for kw in (dict(amsgrad=True), dict(maximize=True)):
+        other = torch.optim.AdamW([p], **kw)
+        with pytest.raises(NotImplementedError, match=next(iter(kw))):
+            opt.load_state_dict(other.state_dict())
+    with pytest.raises(NotImplementedError, match="weight decay"):
+        opt.load_state_dict(torch.optim.Adam([p], weight_decay=0.1).state_dict())
+    assert opt.param_groups[0]["lr"] == 0.5
