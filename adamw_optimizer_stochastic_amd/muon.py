@@ -112,16 +112,16 @@ class MuonSR(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        for group in self.param_groups:
+        live = [[p for p in g["params"] if p.grad is not None] for g in self.param_groups]
+        for p in (p for ps in live for p in ps):   # all of them, before the first moves
+            if p.grad.is_sparse:
+                raise NotImplementedError("MuonSR does not support sparse gradients")
+            if not p.is_contiguous() or not p.grad.is_contiguous():
+                raise NotImplementedError("MuonSR needs contiguous params and grads")
+            self._init_state(p)
+        for group, params in zip(self.param_groups, live):
             batches = {}   # (device, step) -> params
-            for p in group["params"]:
-                if p.grad is None:
-                    continue
-                if p.grad.is_sparse:
-                    raise NotImplementedError("MuonSR does not support sparse gradients")
-                if not p.is_contiguous() or not p.grad.is_contiguous():
-                    raise NotImplementedError("MuonSR needs contiguous params and grads")
-                self._init_state(p)
+            for p in params:
                 t = int(self.state[p]["step"]) + 1
                 batches.setdefault((p.device, t), []).append(p)
             for (_, t), ps in batches.items():

@@ -303,3 +303,21 @@ def test_state_that_does_not_fit_changes_nothing():
         opt.load_state_dict(dict(good, param_groups=good["param_groups"] * 2))
     opt.load_state_dict(good)
     assert int(opt.state[p]["step"]) == 4
+
+
+def test_refused_gradient_moves_nothing(monkeypatch):
+    """A gradient of a later group that the step refuses is found before the first
+    group moves."""
+    calls = []
+    monkeypatch.setattr(ops, "muon_step", lambda *a, **kw: calls.append(a))
+    a, b = _param(4, 6), _param(4, 6)
+    opt = MuonSR([dict(params=[a]), dict(params=[b], lr=0.5)])
+    a.grad = torch.ones(4, 6)
+    for bad in (torch.ones(6, 4).t(), torch.eye(4, 6).to_sparse()):
+        b.grad = bad
+        with pytest.raises(NotImplementedError):
+            opt.step()
+        assert not calls and int(opt.state[a].get("step", 0)) == 0
+    b.grad = torch.ones(4, 6)
+    opt.step()
+    assert len(calls) == 2 and int(opt.state[a]["step"]) == int(opt.state[b]["step"]) == 1
