@@ -21,7 +21,9 @@
 // use hi, the term a X uses both. What rounding hi costs then only enters
 // through B X, so directions with small singular values, which a
 // multiplies by hundreds over the steps, are not drowned in the rounding of the large
-// ones: 3e-4 to 2e-3 on the same matrices, about a bf16 rounding.
+// ones: 3e-4 to 2e-3 on the same matrices, about a bf16 rounding. That is an
+// average of many roundings: short sides below 16, equal entries and orthogonal
+// rows leave few or equal ones, up to 1.4e-2 on some 40,000 simulated matrices.
 #include "mfma_loop.hpp"
 #include "status.hpp"
 

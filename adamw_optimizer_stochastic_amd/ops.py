@@ -498,8 +498,12 @@ def newton_schulz(g, *, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=Non
     g: float32 or bfloat16, (M, N) or (B, M, N), contiguous. X = g / (|g|_F +
     eps), then ``steps`` times X = a X + (b A + c A A) X with A = X X^T (on
     the short side); the result is bfloat16 (nearest even) of g's shape.
-    2e-3 to 3e-3 of it (relative, Frobenius norm) from the exact value: f16
-    products with f32 sums, X held as two f16 numbers. A g of zeros gives
+    f16 products with f32 sums, X held as two f16 numbers, so the result is off
+    the exact one (relative, Frobenius norm, its bf16 rounding apart) by up to
+    3e-3 for entries of varied size and a short side of 64 or more, 4e-3 for one
+    of 16 to 63, and 1.8e-2 where few or equal roundings do not average: shorter
+    sides, entries of one magnitude, orthogonal rows, a single entry. A norm below
+    1e-5 eps falls under f16's range: up to 4.1e-5 off in all. A g of zeros gives
     zeros, a matrix with an Inf or NaN only NaN. ``out``: bfloat16, g's shape,
     contiguous (g itself if it is bfloat16).
     """

@@ -372,11 +372,18 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
  * With (a, b, c) = (3.4445, -4.775, 2.0315) and 5 steps, singular values from
  * about 1/100 of |G|_F up come out between about 0.7 and 1.2 (the update of
  * the Muon optimizer). The products run on the matrix cores with f16 operands
- * and f32 sums, X itself held as two f16 numbers: the result is within 2e-3 to
- * 3e-3 (relative, Frobenius norm, the bf16 rounding included) of the exact one,
- * low-rank G included; a G of one row or column, whose few roundings do not
- * average, within 4.5e-2 at worst. The norm is
- * summed in 64 bits. A G of zeros gives zeros (with eps > 0); an Inf or NaN in G makes all
+ * and f32 sums, X itself held as two f16 numbers. With these coefficients the
+ * result is off the exact one (relative, Frobenius norm; rounding it to bf16 adds
+ * its own 1.7e-3) by up to
+ *   3e-3    entries of varied size (Gaussian, uniform, of any rank), short side 64
+ *           or more;
+ *   4e-3    the same, short side 16 to 63;
+ *   1.8e-2  where the roundings are few or alike and do not average: short sides
+ *           below 16, entries of one magnitude (ones, signs), orthogonal rows, a
+ *           single entry. (One singular value alone: 4.5e-2 at the very worst.)
+ * A G with |G|_F below 1e-5 eps falls under f16's range as X: O, itself below 5e-3
+ * then, is off by up to 4.1e-5 in all. The norm is summed in 64 bits. A G of
+ * zeros gives zeros (with eps > 0); an Inf or NaN in G makes all
  * of its result NaN.
  *
  * g, out: host arrays of n device pointers (read during the call only), each

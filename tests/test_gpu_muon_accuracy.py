@@ -5,7 +5,7 @@ The other tests hold the kernel to the error that its scheme of roundings has
 on the same input; these hold the scheme itself to what is documented. O is
 taken unrounded: a Muon step on f32 zeros with lr 1, no momentum and no decay
 leaves -O. The ceilings: the scheme in binary64 (oracle.muon.newton_schulz_f16)
-on 12,000 matrices of 1 to 200 by 1 to 4099 was off by at most
+on some 40,000 matrices of 1 to 200 by 1 to 4099 was off by at most
 
   2.4e-3  varied entries (Gaussian, uniform, low rank, rank one, strong
           directions over a floor), short side 64 and more;
@@ -176,3 +176,19 @@ def test_step_with_a_bad_gradient(shape):
     assert _same(ps[1], p) and torch.equal(ms[1], m)
     assert bool(torch.isnan(ps[0]).all())
     assert torch.equal(torch.isnan(ms[0]), torch.isnan(bad))
+
+
+@pytest.mark.parametrize("shape", [(1, 7), (64, 64)] + LARGE)
+def test_norm_far_below_eps(shape):
+    """X below f16's range: each of its elements is off by at most half of f16's
+    smallest number over X's scale, 2**-25 / sx with sx > sqrt(s t) / 2, so X by
+    2**-24 in the Frobenius norm, a step, and the result by 2**-24 * (3.4445**5 +
+    .. + 3.4445) = 2**-24 * 682 = 4.1e-5 (B X adds less than 5 X**3 = 1e-9 a step: X is
+    below 5e-4 throughout)."""
+    announce("newton_schulz below eps", shape)
+    for scale in (1e-13, 1e-14, 1e-16):
+        g = _matrix("normal", *shape, 5)
+        g = g / torch.linalg.norm(g) * scale
+        want = om.newton_schulz(g)
+        d = torch.linalg.norm(ops.newton_schulz(g).double() - want).item()
+        assert d <= 4.1e-5 + BF16 * torch.linalg.norm(want).item()
