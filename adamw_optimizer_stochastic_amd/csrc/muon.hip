@@ -870,19 +870,13 @@ double launch_time(int mode, const ProductArgs& a, const Choice& c) {
   return end;
 }
 
-#ifndef ASR_MUON_TILE
-#define ASR_MUON_TILE -1
-#endif
-
 template <int MODE, int OUT = kOutBf16>
 hipError_t launch_product(ProductArgs& a, hipStream_t s) {
-  int best = ASR_MUON_TILE;
-  if (best < 0) {
-    double least = 0.0;
-    for (int i = 0; i < 5; ++i) {
-      const double t = launch_time(MODE, a, kChoices[i]);
-      if (best < 0 || t < least) best = i, least = t;
-    }
+  int best = 0;
+  double least = launch_time(MODE, a, kChoices[0]);
+  for (int i = 1; i < 5; ++i) {
+    const double t = launch_time(MODE, a, kChoices[i]);
+    if (t < least) best = i, least = t;
   }
   switch (best) {
     case 0: return launch_tile<Big, MODE, OUT>(a, s);
@@ -895,7 +889,7 @@ hipError_t launch_product(ProductArgs& a, hipStream_t s) {
 
 // What a call does with every matrix of its list.
 struct Settings {
-  int32_t g_dtype, steps;
+  int32_t steps;
   double a, b, c, eps;
   float momentum;
   bool nesterov;
@@ -1096,7 +1090,7 @@ int asr_newton_schulz(const void* const* g, uint16_t* const* out, int32_t n, int
   if (!sides_ok(rows, cols)) return fail(ASR_EINVAL, "newton_schulz: rows and cols must be in [0, 2**20]");
   if (n == 0 || rows == 0 || cols == 0) return ok();
   if (!g || !out) return fail(ASR_EINVAL, "newton_schulz: null array");
-  Settings st{g_dtype, steps, a, b, c, eps, 0.0f, false, {}, static_cast<char*>(workspace),
+  Settings st{steps, a, b, c, eps, 0.0f, false, {}, static_cast<char*>(workspace),
               static_cast<hipStream_t>(stream)};
   st.out.vec8 = cols % 8 == 0;
   st.out.vec4 = cols % 4 == 0;
@@ -1160,7 +1154,7 @@ int asr_muon_step(const asr_muon_tensor* tensors, int32_t n, int32_t param_dtype
   std::unique_ptr<Desc[]> descs(new (std::nothrow) Desc[n]);
   std::unique_ptr<const Desc*[]> list(new (std::nothrow) const Desc*[n]);
   if (!descs || !list) return fail(ASR_EINVAL, "muon: out of host memory");
-  Settings st{grad_dtype, ns_steps, ns_a, ns_b, ns_c, eps, static_cast<float>(momentum),
+  Settings st{ns_steps, ns_a, ns_b, ns_c, eps, static_cast<float>(momentum),
               nesterov != 0, {}, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)};
   st.out.decay = static_cast<float>(1.0 - lr * weight_decay);
   st.out.seed = seed;

@@ -372,9 +372,9 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
  * With (a, b, c) = (3.4445, -4.775, 2.0315) and 5 steps, singular values from
  * about 1/100 of |G|_F up come out between about 0.7 and 1.2 (the update of
  * the Muon optimizer). The products run on the matrix cores with f16 operands
- * and f32 sums, X itself held as two f16 numbers. With these coefficients the
- * result is off the exact one (relative, Frobenius norm; rounding it to bf16 adds
- * its own 1.7e-3) by up to
+ * and f32 sums, X itself held as two f16 numbers. After these 5 steps the result is
+ * off the exact one (relative, Frobenius norm; rounding it to bf16 adds its own
+ * 1.7e-3) by up to
  *   3e-3    entries of varied size (Gaussian, uniform, of any rank), short side 64
  *           or more;
  *   4e-3    the same, short side 16 to 63;
