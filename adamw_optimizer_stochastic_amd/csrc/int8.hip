@@ -929,14 +929,21 @@ hipError_t product(const asr_i8::GemmArgs& g, int32_t rounding, hipStream_t s) {
   auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
   // Few rows: reading B is all there is, and the kernel for them keeps more of
   // it in flight than tiles do, with one workgroup for 16 columns on every
-  // compute unit (16 x 4096 x 4096: 7.3 us against 9.2 in 64 x 64 tiles; 16 x
+  // compute unit (16 x 4096 x 4096: 7.2 us against 9.0 in 64 x 64 tiles; 16 x
   // 256 x 14336: 14.8 against 21.9; 32 x 5120 x 5120, more of them than
   // compute units: 16.0 against 10.8), or for any N up to 4 rows (1 x 28672 x
-  // 8192: 41.8 against 53.4), unless K is too short to split (1 x 100000 x 64:
-  // 21.0 against 11.3) or most compute units get one tile of two K ranges
-  // (1 x 14336 x 4096: 16.0 against 13.7, 4.3 TB/s; 1 x 8192 x 4096: 9.8 against 10.1).
+  // 8192: 41.7 against 53.2; 1 x 16384 x 8192: 25.8 against 33.6; 1 x 14336 x 7168
+  // in rows of 7184 bytes: 23.7 against 24.2), unless K is too short to split (1 x
+  // 100000 x 64: 21.0 against 11.3). Rows a multiple of 4096 bytes apart meet in the
+  // same memory channels, which costs this kernel, whose workgroup reads 16 rows at
+  // one place, more than the tile (1 x 14336 x 4096: 15.8 against 13.6, in rows of
+  // 4224 bytes 13.4 against 13.7; 4 x 10240 x 3584 in rows of 4096: 11.9 against
+  // 11.0), as long as most compute units get one tile (1 x 8192 x 4096: 10.4
+  // against 11.0; 1 x 16400 x 4096: 17.6 against 20.3) of a K up to 4096 (2048: 10.1
+  // against 10.4; 8192: 24.9 against 29.6). (Not followed: 4 rows of 14336 columns
+  // with a longer K, 7168: 23.8 against 20.9.) All with B from memory.
   // (n below 2**26: a launch's threads)
-  const bool one_each = n > 64 * (kCus / 2) && n <= 64 * kCus && g.k >= 2048;
+  const bool one_each = n > 64 * (kCus / 2) && n <= 64 * kCus && g.k >= 2560 && g.k <= 4096 && g.ldb % 4096 == 0;
   if ((m <= 32 && n <= 16 * kCus) || (m <= 4 && g.k >= 512 && n < (int64_t{1} << 26) && !one_each))
     return m <= 16 ? launch_few<1>(g, rounding, s) : launch_few<2>(g, rounding, s);
   // (1000 x 14336 x 4096, 224 tiles of 256: 63 us, 80 us in 128 x 128 tiles;

@@ -525,3 +525,22 @@ def test_product_in_two_ranges_of_k(shape):
     second one empty, shorter, or ending inside a row's last codes), and their
     neighbours that do not."""
     test_product(shape)
+
+
+@pytest.mark.parametrize("ld", [4096, 4112, 8192])
+@pytest.mark.parametrize("m,n,k", [(1, 8200, 2559), (1, 8200, 2561), (4, 9000, 4096), (3, 8192, 2600),
+                                   (2, 16400, 2600), (5, 8200, 2600)])
+def test_product_of_few_rows_and_row_strides(m, n, k, ld):
+    """Up to 4 rows take one kernel or the other by how far B's rows are apart;
+    the codes behind a row's K are never used."""
+    announce("gemm_i8 row strides", m, n, k, ld)
+    rng = np.random.default_rng([m, n, k, ld])
+    a, at = _codes(rng, m, k, 4096)
+    b, bt = _codes(rng, n, k, ld)
+    sa, sb = rng.random(m).astype(np.float32), rng.random(n).astype(np.float32)
+    c32 = torch.full((m, n), np.nan, device="cuda")
+    c = ops.gemm_i8(at, bt, f32_tensor(sa), f32_tensor(sb), rounding="sr", seed=3, step=1, out_f32=c32)
+    torch.cuda.synchronize()
+    want = o8.gemm_f32(a, b, sa, sb)
+    assert_bits_equal(to_host(c32).reshape(-1), want.reshape(-1), "f32 value")
+    assert_bits_equal(to_host(c).reshape(-1), oracle.gemm_round(want, "sr", 3, 1, 0).reshape(-1), "sr")
