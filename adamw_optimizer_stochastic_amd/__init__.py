@@ -10,7 +10,8 @@ include/adamw_sr.h); this package is its Python binding:
   * ``linear_i8`` a linear layer whose products run in int8, with its gradients;
   * ``random`` uniform/normal draws and dropout on the same stream;
   * ``AdamWSR`` the optimizer (a torch.optim.AdamW drop-in);
-  * ``MuonSR`` the Muon optimizer for matrices (torch.optim.Muon's arguments);
+  * ``MuonSR`` the Muon optimizer for matrices (torch.optim.Muon's arguments;
+    the momentum is a sum of gradients, not torch's average of them);
   * ``workloads`` seeded synthetic inputs for tests and the benchmark.
 The library is loaded on first use; if it is missing, calls raise.
 """

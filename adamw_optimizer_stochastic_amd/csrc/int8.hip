@@ -172,9 +172,11 @@ __device__ __forceinline__ const QuantJob& job_of(const QuantArgs& a) {
 // One row by LANES lanes (64: four rows a workgroup, 256: one). The first
 // KEEP runs of 8 a lane holds stay in registers between the pass for the
 // maximum and the pass for the codes; a longer row's others are read again.
-// Bound by memory: x and w of a linear layer, 4096 and 14336 rows of 4096 bf16
-// (226 MB with the codes), take 49-57 us, 4.0-4.6 TB/s; one row of 4096 takes
-// 3 us, its latency.
+// x and w of a linear layer, 4096 and 14336 rows of 4096 bf16 (226 MB with the
+// codes), take 49-57 us, 4.0-4.6 TB/s, 1.35 to 1.55 times a copy's time: a workgroup
+// holds one row from its load through two reductions to its store, with no other
+// in flight. 14336 rows alone: 37-41 us to nearest, 53-58 stochastic (the random
+// bits). One row of 4096 takes 3 us, its latency.
 template <typename S, bool SR, int LANES>
 __global__ __launch_bounds__(256) void quantize_rows(QuantArgs args) {
   constexpr int KEEP = 4;
@@ -515,7 +517,7 @@ __device__ __forceinline__ void store4(const GemmArgs& args, int64_t at, int cou
 }
 
 // The tile of C from (m0, n0). Bound by the matrix instructions and what keeps
-// them fed (58% of the cycles busy at 8192 x 14336 x 4096: 433-444 us, 2.2 POP/s;
+// them fed (58% of the cycles busy at 8192 x 14336 x 4096: 433-472 us by box, 2.0-2.2 POP/s;
 // 450 with stochastic rounding);
 // the epilogue is the part no other work covers, so its stores go in whole
 // lines. REST: K is not a multiple of 16 (a variant of

@@ -440,8 +440,8 @@ def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index
         _require_gpu(t, name)
         if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != size or t.device != device:
             raise ValueError(f"{name} must be a float32 tensor of shape ({size},) on a's device")
-    f32_ptr = None
-    if out is None and out_f32 is None:
+    f32_ptr, given = None, [t for t in (out, out_f32) if t is not None]
+    if not given:
         out, ldc = torch.empty((m, n), dtype=torch.bfloat16, device=device), max(n, 1)
     else:   # caller's memory: it may not be what the product reads
         if out is None:
@@ -465,7 +465,8 @@ def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index
         _abi.asr_gemm_i8(a.data_ptr(), _row_stride(a, ldk), b.data_ptr(), _row_stride(b, ldk),
                          scale_a.data_ptr(), scale_b.data_ptr(), out.data_ptr(), ldc, f32_ptr, m,
                          n, k, ROUNDING_CODE[rounding], *key, _stream(device))
-    _written([out] if out_f32 is None else [out, out_f32])
+    if given:
+        _written(given)
     return out
 
 

@@ -394,7 +394,8 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
  * |b x^2 + c x^4| below 3.75 there. workspace:
  * asr_newton_schulz_workspace_bytes(n, rows, cols) bytes of device memory,
  * 256-byte aligned, overwritten in stream order: calls that may overlap need
- * a workspace each. (About 8 bytes an element and 4 a squared short side, for
+ * a workspace each. (About 8 bytes an element and 4 a squared short side, both
+ * sides counted up to the next multiple of 64, for
  * at most 32 matrices at a time, and of large ones about 4 GiB; none for matrices
  * that one workgroup holds, such as 128 x 128 or 64 x 512.)
  * Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Runs

@@ -544,3 +544,26 @@ def test_product_of_few_rows_and_row_strides(m, n, k, ld):
     want = o8.gemm_f32(a, b, sa, sb)
     assert_bits_equal(to_host(c32).reshape(-1), want.reshape(-1), "f32 value")
     assert_bits_equal(to_host(c).reshape(-1), oracle.gemm_round(want, "sr", 3, 1, 0).reshape(-1), "sr")
+
+
+def test_last_positions():
+    """Positions up to the last one, 2**64 - 1 (a run of 8 that goes past a row's
+    end draws from position 0 on, and uses none of it)."""
+    announce("int8 last positions")
+    x, t = _matrix(5, 70, "f32", 12)
+    top = 2 ** 64 - 5 * 70
+    for transpose in (False, True):
+        _check_codes(x, t, transpose=transpose, rounding="sr", seed=4, step=9, base_index=top)
+    rng = np.random.default_rng(12)
+    for m, n, k in ((3, 37, 600), (70, 65, 40)):
+        a, at = _codes(rng, m, k, (k + 15) // 16 * 16)
+        b, bt = _codes(rng, n, k, (k + 15) // 16 * 16)
+        sa, sb = rng.random(m).astype(np.float32), rng.random(n).astype(np.float32)
+        base = 2 ** 64 - m * n
+        c = ops.gemm_i8(at, bt, f32_tensor(sa), f32_tensor(sb), rounding="sr", seed=4, step=9,
+                        base_index=base)
+        want = oracle.gemm_round(o8.gemm_f32(a, b, sa, sb), "sr", 4, 9, base)
+        assert_bits_equal(to_host(c).reshape(-1), want.reshape(-1), (m, n, k))
+        with pytest.raises(ops.AsrError, match="2\\*\\*64"):
+            ops.gemm_i8(at, bt, f32_tensor(sa), f32_tensor(sb), rounding="sr", seed=4, step=9,
+                        base_index=base + 1)

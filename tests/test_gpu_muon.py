@@ -550,3 +550,19 @@ def test_against_torch_muon(adjust, nesterov):
     assert opt.param_groups[0]["lr"] == 0.05
     limit = [0.0] * 3
     one(moved, opt, 4)
+
+
+def test_positions_past_the_last():
+    """Global positions wrap modulo 2**64."""
+    announce("muon positions wrap")
+    shapes = [(40, 70), (200, 264), (130, 515)]
+    ps, gs, ms = _state(shapes, torch.bfloat16, torch.bfloat16, seed=31)
+    bases = [2 ** 64 - 1000, 2 ** 64 - 4, 2 ** 64 - 3]
+    p32, m32 = [p.float() for p in ps], [m.clone() for m in ms]
+    hp = dict(lr=0.02, weight_decay=0.1, step=2 ** 32 - 1, seed=2 ** 32 - 1)
+    ops.muon_step(p32, gs, m32, bases, **hp)
+    ops.muon_step(ps, gs, ms, bases, **hp)
+    torch.cuda.synchronize()
+    for p, y, base in zip(ps, p32, bases):
+        want = oracle.gemm_round(to_host(y), "sr", 2 ** 32 - 1, 2 ** 32 - 1, base)
+        assert_bits_equal(to_host(p).reshape(-1), want.reshape(-1), base)
