@@ -17,7 +17,7 @@ ASR_OK, ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP = range(6)
 ASR_F32, ASR_BF16 = 0, 1
 ASR_ROUND_SR, ASR_ROUND_RN = 0, 1
 ASR_PROBE_READ, ASR_PROBE_WRITE, ASR_PROBE_COPY = 0, 1, 2
-ABI_VERSION = 108
+ABI_VERSION = 109
 
 STATUS_NAMES = {ASR_OK: "ASR_OK", ASR_EINVAL: "ASR_EINVAL", ASR_EDTYPE: "ASR_EDTYPE",
                 ASR_EALIGN: "ASR_EALIGN", ASR_EWORKSPACE: "ASR_EWORKSPACE",
@@ -125,6 +125,39 @@ _SIGNATURES = {
     "asr_linear_i8_backward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 5 + [_c.c_int64] * 3 +
                                [_c.c_int32, _c.c_uint32, _c.c_uint32, _c.c_uint64, _c.c_void_p,
                                 _c.c_size_t, _c.c_void_p]),
+    "asr_linear_i8_forward_saved": (_c.c_int, [_c.c_void_p, _c.c_int64] * 4 + [_c.c_void_p] +
+                                    [_c.c_int64] * 3 + [_c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "asr_linear_i8_backward_saved": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p] +
+                                     [_c.c_void_p, _c.c_int64] * 4 + [_c.c_int64] * 3 +
+                                     [_c.c_int32, _c.c_uint32, _c.c_uint32, _c.c_uint64,
+                                      _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "asr_pack_i8": (_c.c_int, [_c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64,
+                               _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int32, _c.c_uint32,
+                               _c.c_uint32, _c.c_uint64, _c.c_void_p]),
+    "asr_unpack_i8": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_int64,
+                                 _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_void_p]),
+    "asr_layer_norm_forward": (_c.c_int, [_c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int64,
+                                          _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int32,
+                                          _c.c_double, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                          _c.c_int64, _c.c_void_p, _c.c_void_p]),
+    "asr_layer_norm_backward_workspace_bytes": (_c.c_size_t, [_c.c_int64] * 2),
+    "asr_layer_norm_backward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 3 + [_c.c_void_p] * 2 +
+                                [_c.c_int32, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int32] +
+                                [_c.c_void_p] * 4 + [_c.c_size_t, _c.c_void_p]),
+    "asr_silu_mul_forward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 2 +
+                             [_c.c_int32, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int64] +
+                             [_c.c_void_p] * 4 + [_c.c_int64, _c.c_void_p]),
+    "asr_silu_mul_backward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 3 + [_c.c_void_p] * 4 +
+                              [_c.c_int64, _c.c_int32, _c.c_int64, _c.c_int64] +
+                              [_c.c_void_p, _c.c_int64] * 2 + [_c.c_void_p]),
+    "asr_embedding_forward": (_c.c_int, [_c.c_void_p, _c.c_int32, _c.c_int64, _c.c_void_p,
+                                         _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64,
+                                         _c.c_double, _c.c_void_p, _c.c_void_p]),
+    "asr_embedding_backward_workspace_bytes": (_c.c_size_t, [_c.c_int64] * 3),
+    "asr_embedding_backward": (_c.c_int, [_c.c_void_p, _c.c_int32, _c.c_int64, _c.c_void_p,
+                                          _c.c_int64, _c.c_int32, _c.c_int64, _c.c_int64,
+                                          _c.c_double, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                          _c.c_size_t, _c.c_void_p]),
     "asr_newton_schulz_workspace_bytes": (_c.c_size_t, [_c.c_int32, _c.c_int64, _c.c_int64]),
     "asr_newton_schulz": (_c.c_int, [_c.POINTER(_c.c_void_p), _c.POINTER(_c.c_void_p), _c.c_int32,
                                      _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32] +
@@ -308,6 +341,80 @@ def asr_linear_i8_backward(x, ldx, w, ldw, dy, lddy, dx, lddx, dw, lddw, tokens,
     _check(lib().asr_linear_i8_backward(x, ldx, w, ldw, dy, lddy, dx, lddx, dw, lddw, tokens, n,
                                         k, rounding, seed, step, base_index, workspace,
                                         workspace_bytes, stream), "asr_linear_i8_backward")
+
+
+def asr_linear_i8_forward_saved(x, ldx, w, ldw, y, ldy, q, ldq, scale, tokens, n, k, workspace,
+                                workspace_bytes, stream):
+    _check(lib().asr_linear_i8_forward_saved(x, ldx, w, ldw, y, ldy, q, ldq, scale, tokens, n, k,
+                                             workspace, workspace_bytes, stream),
+           "asr_linear_i8_forward_saved")
+
+
+def asr_linear_i8_backward_saved(q, ldq, scale, w, ldw, dy, lddy, dx, lddx, dw, lddw, tokens, n,
+                                 k, rounding, seed, step, base_index, workspace, workspace_bytes,
+                                 stream):
+    _check(lib().asr_linear_i8_backward_saved(q, ldq, scale, w, ldw, dy, lddy, dx, lddx, dw, lddw,
+                                              tokens, n, k, rounding, seed, step, base_index,
+                                              workspace, workspace_bytes, stream),
+           "asr_linear_i8_backward_saved")
+
+
+def asr_pack_i8(x, dtype, ldx, rows, cols, q, ldq, scale, rounding, seed, step, base_index,
+                stream):
+    _check(lib().asr_pack_i8(x, dtype, ldx, rows, cols, q, ldq, scale, rounding, seed, step,
+                             base_index, stream), "asr_pack_i8")
+
+
+def asr_unpack_i8(q, ldq, scale, rows, cols, x, dtype, ldx, stream):
+    _check(lib().asr_unpack_i8(q, ldq, scale, rows, cols, x, dtype, ldx, stream),
+           "asr_unpack_i8")
+
+
+def asr_layer_norm_forward(x, dtype, ldx, rows, cols, weight, bias, param_dtype, eps, y, stat, q,
+                           ldq, scale, stream):
+    _check(lib().asr_layer_norm_forward(x, dtype, ldx, rows, cols, weight, bias, param_dtype, eps,
+                                        y, stat, q, ldq, scale, stream), "asr_layer_norm_forward")
+
+
+def asr_layer_norm_backward_workspace_bytes(rows, cols):
+    return int(lib().asr_layer_norm_backward_workspace_bytes(rows, cols))
+
+
+def asr_layer_norm_backward(dy, ld_dy, x, ldx, q, ldq, scale, stat, dtype, rows, cols, weight,
+                            param_dtype, dx, dweight, dbias, workspace, workspace_bytes, stream):
+    _check(lib().asr_layer_norm_backward(dy, ld_dy, x, ldx, q, ldq, scale, stat, dtype, rows,
+                                         cols, weight, param_dtype, dx, dweight, dbias, workspace,
+                                         workspace_bytes, stream), "asr_layer_norm_backward")
+
+
+def asr_silu_mul_forward(gate, ld_gate, up, ld_up, dtype, rows, cols, y, ld_y, q_gate, s_gate,
+                         q_up, s_up, ldq, stream):
+    _check(lib().asr_silu_mul_forward(gate, ld_gate, up, ld_up, dtype, rows, cols, y, ld_y,
+                                      q_gate, s_gate, q_up, s_up, ldq, stream),
+           "asr_silu_mul_forward")
+
+
+def asr_silu_mul_backward(dy, ld_dy, gate, ld_gate, up, ld_up, q_gate, s_gate, q_up, s_up, ldq,
+                          dtype, rows, cols, dgate, ld_dgate, dup, ld_dup, stream):
+    _check(lib().asr_silu_mul_backward(dy, ld_dy, gate, ld_gate, up, ld_up, q_gate, s_gate, q_up,
+                                       s_up, ldq, dtype, rows, cols, dgate, ld_dgate, dup, ld_dup,
+                                       stream), "asr_silu_mul_backward")
+
+
+def asr_embedding_forward(ids, ids_64, n, table, dtype, ld, vocab, dim, scale, y, stream):
+    _check(lib().asr_embedding_forward(ids, ids_64, n, table, dtype, ld, vocab, dim, scale, y,
+                                       stream), "asr_embedding_forward")
+
+
+def asr_embedding_backward_workspace_bytes(n, vocab, dim):
+    return int(lib().asr_embedding_backward_workspace_bytes(n, vocab, dim))
+
+
+def asr_embedding_backward(ids, ids_64, n, dy, ld_dy, dtype, vocab, dim, scale, padding_idx,
+                           dtable, workspace, workspace_bytes, stream):
+    _check(lib().asr_embedding_backward(ids, ids_64, n, dy, ld_dy, dtype, vocab, dim, scale,
+                                        padding_idx, dtable, workspace, workspace_bytes, stream),
+           "asr_embedding_backward")
 
 
 def asr_newton_schulz_workspace_bytes(n, rows, cols):

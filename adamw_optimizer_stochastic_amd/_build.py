@@ -1,11 +1,13 @@
 """Build step: compiles the HIP sources into the in-tree shared library.
 
-Five translation units (csrc/adamw_sr.hip: the AdamW step, the generator and
+Seven translation units (csrc/adamw_sr.hip: the AdamW step, the generator and
 the conversions; csrc/gemm_sr.hip: the GEMM; csrc/random.hip: uniform/normal
 draws and dropout; csrc/int8.hip: the int8 quantiser and product; csrc/muon.hip:
 Newton-Schulz products and the Muon step, both on the K loop of
-csrc/mfma_loop.hpp; all include csrc/device.hpp, csrc/status.hpp and
-include/adamw_sr.h) -> libadamw_sr.so, for gfx950 only. Flags that matter
+csrc/mfma_loop.hpp; csrc/layers.hip: 8-bit activations, layer norm and gated
+SiLU; csrc/embedding.hip: the lookup and its gradient, both on csrc/rows.hpp;
+all include csrc/device.hpp, csrc/status.hpp and include/adamw_sr.h, the ones
+with 8-bit codes csrc/codes.hpp) -> libadamw_sr.so, for gfx950 only. Flags that matter
 for the arithmetic:
   -ffp-contract=off                          no fused multiply-adds (the
                                              sources also say so by pragma)
@@ -28,9 +30,13 @@ SOURCES = [os.path.join(PKG_DIR, "csrc", "adamw_sr.hip"),
            os.path.join(PKG_DIR, "csrc", "gemm_sr.hip"),
            os.path.join(PKG_DIR, "csrc", "random.hip"),
            os.path.join(PKG_DIR, "csrc", "int8.hip"),
-           os.path.join(PKG_DIR, "csrc", "muon.hip")]
+           os.path.join(PKG_DIR, "csrc", "muon.hip"),
+           os.path.join(PKG_DIR, "csrc", "layers.hip"),
+           os.path.join(PKG_DIR, "csrc", "embedding.hip")]
 DEPENDS = SOURCES + [os.path.join(PKG_DIR, "csrc", "device.hpp"),
                      os.path.join(PKG_DIR, "csrc", "mfma_loop.hpp"),
+                     os.path.join(PKG_DIR, "csrc", "codes.hpp"),
+                     os.path.join(PKG_DIR, "csrc", "rows.hpp"),
                      os.path.join(PKG_DIR, "csrc", "status.hpp"),
                      os.path.join(ROOT, "include", "adamw_sr.h")]
 LIB_NAME = "libadamw_sr.so"

@@ -1,0 +1,603 @@
+// Embedding: y[t] = scale * w[ids[t]], and the table's gradient
+//   dw[v] = scale * (sum of dy[t] over the tokens t with ids[t] = v, in their order),
+// a row of no token 0. Sums in f32, one rounding at the end; the order of the
+// additions is fixed by ids alone, so equal calls give equal bits.
+//
+// The gradient in three steps. (1) Tokens sorted by id, stable: 8 bits (or
+// fewer) of the id a pass, up to 8192 tokens in one workgroup's LDS. Ids outside
+// the table and the padding id get the key `vocab` and end up last. (2) One launch
+// whose first workgroups sum the sorted rows, `chunk` positions each, and whose
+// others write the rows of no token; a run of one id inside a chunk is
+// finished there, one that crosses a chunk's border leaves an f32 partial sum.
+// (3) These are joined in order. Every row of dw is written once.
+#include "rows.hpp"
+#include "status.hpp"
+
+#include <adamw_sr.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+#include <type_traits>
+
+#pragma clang fp contract(off)
+
+namespace asr_embed {
+
+using namespace asr_rows;
+
+constexpr int kTile = 8192;     // tokens a workgroup sorts
+constexpr int kBins = 256;
+constexpr uint32_t kPast = 0xFFFFFFFFu;   // key of places past the last token
+
+struct Ids {
+  const void* ids;
+  uint32_t wide;    // 64-bit ids
+  int64_t n, vocab, padding;   // padding: the id without a gradient, or -1
+};
+
+__device__ __forceinline__ int64_t id_at(const Ids& a, int64_t i) {
+  return a.wide ? static_cast<const int64_t*>(a.ids)[i] : static_cast<int64_t>(static_cast<const int32_t*>(a.ids)[i]);
+}
+
+__device__ __forceinline__ uint32_t key_at(const Ids& a, int64_t i) {
+  const int64_t id = id_at(a, i);
+  return static_cast<uint32_t>(id >= 0 && id < a.vocab && id != a.padding ? id : a.vocab);
+}
+
+// ------------------------------------------------------------- forward
+struct Lookup {
+  Ids ids;
+  const void* table;
+  void* y;
+  int64_t ld, dim;
+  float scale;
+  int32_t log_lanes;    // lanes a row: 8 columns each
+  uint32_t strips, items;
+};
+
+// Rows of up to 8 << log_lanes columns side by side; an id outside the table gives NaN.
+template <typename S>
+__global__ __launch_bounds__(256) void lookup(Lookup a) {
+  for (uint32_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+    const uint32_t up = item / a.strips, strip = item - up * a.strips;
+    const int64_t t = (static_cast<int64_t>(up) << (8 - a.log_lanes)) + (threadIdx.x >> a.log_lanes);
+    const int64_t col = ((static_cast<int64_t>(strip) << a.log_lanes) + (threadIdx.x & ((1u << a.log_lanes) - 1))) * 8;
+    const int64_t count = t < a.ids.n ? a.dim - col : 0;
+    if (count <= 0) continue;
+    const int64_t id = id_at(a.ids, t);
+    const bool there = id >= 0 && id < a.ids.vocab;
+    Run<S> r;
+    r.load(static_cast<const S*>(a.table) + (there ? id : 0) * a.ld + col, there ? count : 0);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = there ? r.get(e) * a.scale : __builtin_nanf("");
+    store8(static_cast<S*>(a.y) + t * a.dim + col, count, x);
+  }
+}
+
+// ---------------------------------------------------------------- sort
+struct Sort {
+  Ids ids;
+  const uint32_t* keys_in;   // NULL: the first pass, from the ids
+  const uint32_t* toks_in;
+  uint32_t* keys;
+  uint32_t* toks;
+  uint32_t* hist;            // [digit][tile], of several tiles
+  uint8_t* touched;          // one byte an id: whether it has a token
+  uint32_t tiles, shift, bits, passes;
+};
+
+// The place of each of a tile's keys when the tile is ordered by one digit, stable.
+// A thread holds the keys at wave * 64 R + r * 64 + lane; counts[digit][wave]. A
+// round of 64 keys finds the lanes of its own digit by ballots, the first of
+// them adds their number to the wave's count. Ends with counts holding the
+// place of each digit's first key of each wave.
+template <int R>
+__device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t shift, uint32_t bits, uint32_t* counts,
+                                            uint32_t* totals, uint32_t (&place)[R]) {
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, mask = (1u << bits) - 1u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) counts[i * 1024 + threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t digit = (key[r] >> shift) & mask;
+    uint64_t peers = ~uint64_t{0};
+    for (uint32_t b = 0; b < bits; ++b) {
+      const bool one = (digit >> b) & 1u;
+      const uint64_t with = __builtin_amdgcn_ballot_w64(one);
+      peers &= one ? with : ~with;
+    }
+    const uint32_t first = static_cast<uint32_t>(__builtin_ctzll(peers));
+    uint32_t before = 0;
+    if (lane == first) before = atomicAdd(&counts[digit * 16 + wave], static_cast<uint32_t>(__builtin_popcountll(peers)));
+    before = static_cast<uint32_t>(__shfl(static_cast<int>(before), static_cast<int>(first)));
+    place[r] = before + static_cast<uint32_t>(__builtin_popcountll(peers & ((uint64_t{1} << lane) - 1)));
+  }
+  __syncthreads();
+  // exclusive sums over counts, 4 a thread
+  uint32_t c[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = sum;
+    sum += counts[threadIdx.x * 4 + i];
+  }
+  uint32_t upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t below = static_cast<uint32_t>(__shfl_up(static_cast<int>(upto), d));
+    if (lane >= static_cast<uint32_t>(d)) upto += below;
+  }
+  if (lane == 63) totals[wave] = upto;
+  __syncthreads();
+  uint32_t base = upto - sum;
+#pragma unroll
+  for (int i = 0; i < 15; ++i) base += static_cast<uint32_t>(i) < wave ? totals[i] : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) counts[threadIdx.x * 4 + i] = base + c[i];
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) place[r] += counts[((key[r] >> shift) & mask) * 16 + wave];
+}
+
+// Up to 1024 R tokens, all passes; flags of the ids that have one. (Bound by the
+// latency of its steps: one workgroup, three passes of four barriers.)
+template <int R>
+__global__ __launch_bounds__(1024) void sort_one(Sort a) {
+  __shared__ uint32_t counts[kBins * 16], totals[16], keys[R * 1024];
+  __shared__ uint16_t toks[R * 1024];
+  const uint32_t at = (threadIdx.x >> 6) * (64 * R) + (threadIdx.x & 63u);
+  uint32_t key[R], tok[R], place[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    tok[r] = at + r * 64;
+    key[r] = tok[r] < a.ids.n ? key_at(a.ids, tok[r]) : kPast;
+  }
+  for (int64_t i = threadIdx.x; i < (a.ids.vocab + 15) / 16; i += 1024)
+    reinterpret_cast<asr::u32x4*>(a.touched)[i] = asr::u32x4{0, 0, 0, 0};
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (key[r] < a.ids.vocab) a.touched[key[r]] = 1;
+  for (uint32_t pass = 0; pass < a.passes; ++pass) {
+    tile_places<R>(key, pass * a.bits, a.bits, counts, totals, place);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      keys[place[r]] = key[r];
+      toks[place[r]] = static_cast<uint16_t>(tok[r]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      key[r] = keys[at + r * 64];
+      tok[r] = toks[at + r * 64];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t i = at + r * 64;
+    if (i < a.ids.n) {
+      a.keys[i] = key[r];
+      a.toks[i] = tok[r];
+    }
+  }
+}
+
+// More tokens: tiles of 8192, a pass at a time. The digits of each tile are counted,
+__device__ __forceinline__ uint32_t sort_key(const Sort& a, int64_t i) {
+  return i >= a.ids.n ? kPast : a.keys_in ? a.keys_in[i] : key_at(a.ids, i);
+}
+
+__global__ __launch_bounds__(1024) void count_digits(Sort a) {
+  __shared__ uint32_t counts[kBins];
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * kTile;
+  const uint32_t mask = (1u << a.bits) - 1u;
+  if (threadIdx.x < kBins) counts[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int64_t i = start + r * 1024 + threadIdx.x;
+    if (i < a.ids.n) {
+      const uint32_t key = sort_key(a, i);
+      atomicAdd(&counts[(key >> a.shift) & mask], 1u);
+      if (!a.keys_in && key < a.ids.vocab) a.touched[key] = 1;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kBins) a.hist[static_cast<int64_t>(threadIdx.x) * a.tiles + blockIdx.x] = counts[threadIdx.x];
+}
+
+// the counts of all digits and tiles become places (one workgroup),
+__global__ __launch_bounds__(1024) void scan_counts(uint32_t* hist, int64_t count) {
+  __shared__ uint32_t totals[16];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  uint32_t carry = 0;
+  for (int64_t start = 0; start < count; start += 4096) {
+    uint32_t c[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t k = start + threadIdx.x * 4 + i;
+      c[i] = sum;
+      sum += k < count ? hist[k] : 0u;
+    }
+    uint32_t upto = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t below = static_cast<uint32_t>(__shfl_up(static_cast<int>(upto), d));
+      if (lane >= static_cast<uint32_t>(d)) upto += below;
+    }
+    if (lane == 63) totals[wave] = upto;
+    __syncthreads();
+    uint32_t base = carry + upto - sum;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      base += static_cast<uint32_t>(i) < wave ? totals[i] : 0u;
+      carry += totals[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t k = start + threadIdx.x * 4 + i;
+      if (k < count) hist[k] = base + c[i];
+    }
+    __syncthreads();  // (totals are read)
+  }
+}
+
+// and each tile's keys go there.
+__global__ __launch_bounds__(1024) void scatter_digits(Sort a) {
+  __shared__ uint32_t counts[kBins * 16], totals[16];
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * kTile;
+  const uint32_t at = (threadIdx.x >> 6) * 512 + (threadIdx.x & 63u), mask = (1u << a.bits) - 1u;
+  uint32_t key[8], place[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) key[r] = sort_key(a, start + at + r * 64);
+  tile_places<8>(key, a.shift, a.bits, counts, totals, place);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int64_t i = start + at + r * 64;
+    if (i < a.ids.n) {
+      const uint32_t digit = (key[r] >> a.shift) & mask;
+      const uint32_t to = a.hist[static_cast<int64_t>(digit) * a.tiles + blockIdx.x] + place[r] - counts[digit * 16];
+      a.keys[to] = key[r];
+      a.toks[to] = a.toks_in ? a.toks_in[i] : static_cast<uint32_t>(i);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void clear_flags(uint8_t* touched, int64_t vocab) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < (vocab + 15) / 16; i += static_cast<int64_t>(gridDim.x) * 256)
+    reinterpret_cast<asr::u32x4*>(touched)[i] = asr::u32x4{0, 0, 0, 0};
+}
+
+// ---------------------------------------------------------------- sums
+struct Sums {
+  const uint32_t* keys;
+  const uint32_t* toks;
+  const uint8_t* touched;    // NULL: no id has a token
+  const void* dy;
+  void* dw;
+  float* part;               // [chunk][head, tail][dim]: runs that cross a border
+  int64_t n, vocab, dim, ld;
+  int64_t fill_rows;         // rows a filling workgroup looks after
+  float scale;
+  int32_t chunk;             // sorted positions a chunk
+  int32_t chunks, log_lanes;
+  uint32_t strips, sum_blocks;
+};
+
+template <typename S>
+__global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
+  const int lanes = 1 << a.log_lanes;
+  const int64_t lane = threadIdx.x & (lanes - 1);
+  if (blockIdx.x >= a.sum_blocks) {
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * a.fill_rows;
+    const int64_t v1 = min(a.vocab, v0 + a.fill_rows);
+    const float zero[8] = {};
+    for (int64_t v = v0 + (threadIdx.x >> a.log_lanes); v < v1; v += 256 >> a.log_lanes) {
+      if (a.touched && a.touched[v]) continue;
+      S* row = static_cast<S*>(a.dw) + v * a.dim;
+      for (int64_t col = lane * 8; col < a.dim; col += lanes * 8) store8(row + col, a.dim - col, zero);
+    }
+    return;
+  }
+  const uint32_t up = blockIdx.x / a.strips, strip = blockIdx.x - up * a.strips;
+  const int64_t c = (static_cast<int64_t>(up) << (8 - a.log_lanes)) + (threadIdx.x >> a.log_lanes);
+  const int64_t col = (static_cast<int64_t>(strip) * lanes + lane) * 8, count = a.dim - col;
+  if (c >= a.chunks || count <= 0) return;
+  const int64_t i0 = c * a.chunk, i1 = min(a.n, i0 + a.chunk);
+  const S* dy = static_cast<const S*>(a.dy) + col;
+  const uint32_t vocab = static_cast<uint32_t>(a.vocab);
+  const uint32_t before = i0 > 0 ? a.keys[i0 - 1] : kPast, after = i1 < a.n ? a.keys[i1] : kPast;
+  uint32_t run = kPast;
+  bool head = false;
+  float acc[8] = {};
+  auto flush = [&](bool tail) {
+    if (head || tail) {
+      store8(a.part + (c * 2 + (head ? 0 : 1)) * a.dim + col, count, acc);
+    } else {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = acc[e] * a.scale;
+      store8(static_cast<S*>(a.dw) + static_cast<int64_t>(run) * a.dim + col, count, x);
+    }
+  };
+  constexpr int kAhead = 4;   // rows in flight
+  for (int64_t i = i0; i < i1; i += kAhead) {
+    uint32_t key[kAhead];
+    Run<S> row[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      key[k] = i + k < i1 ? a.keys[i + k] : kPast;
+      const int64_t t = key[k] < vocab ? a.toks[i + k] : 0;
+      row[k].load(dy + t * a.ld, key[k] < vocab ? count : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (key[k] >= vocab) continue;    // (only such follow)
+      if (key[k] != run) {
+        if (run != kPast) flush(false);
+        run = key[k];
+        head = i + k == i0 && run == before;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += row[k].get(e);
+    }
+  }
+  if (run != kPast) flush(after == run);
+}
+
+// The runs that cross chunks: the chunk where one begins adds its tail and the
+// heads of the chunks after it, in 4 shares side by side joined in their order.
+template <typename S>
+__global__ __launch_bounds__(1024) void join_runs(Sums a) {
+  __shared__ asr::f32x4 lds[1024];
+  const int64_t c = blockIdx.x, i0 = c * a.chunk, i1 = i0 + a.chunk;
+  if (i1 >= a.n) return;
+  const uint32_t run = a.keys[i1];
+  if (run >= a.vocab || a.keys[i1 - 1] != run) return;
+  if (i0 > 0 && a.keys[i0 - 1] == run) return;   // it began before
+  int64_t lo = c + 1, hi = a.chunks;              // the run starts chunk lo, and no chunk from hi on
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (a.keys[mid * a.chunk] == run) lo = mid;
+    else hi = mid;
+  }
+  const int64_t heads = hi - (c + 1), share = threadIdx.x / 256, each = (heads + 3) / 4;
+  const int64_t from = c + 1 + share * each, to = min(hi, from + each);
+  const int64_t col = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x % 256) * 4;
+  const int left = static_cast<int>(max(int64_t{0}, min(int64_t{4}, a.dim - col)));
+  asr::f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](int64_t slot) {
+    const float* p = a.part + slot * a.dim + col;
+    if (left == 4) {
+      t += *reinterpret_cast<const f32x4_any*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < left) t[e] += p[e];
+    }
+  };
+  if (share == 0) add(c * 2 + 1);
+#pragma unroll 4
+  for (int64_t k = from; k < to; ++k) add(k * 2);
+  lds[threadIdx.x] = t;
+  __syncthreads();
+  if (share == 0) {
+    S* out = static_cast<S*>(a.dw) + static_cast<int64_t>(run) * a.dim + col;
+#pragma unroll
+    for (int k = 1; k < 4; ++k) t += lds[k * 256 + threadIdx.x];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e < left) {
+        if constexpr (std::is_same_v<S, float>) out[e] = t[e] * a.scale;
+        else out[e] = static_cast<uint16_t>(bf16_pair(t[e] * a.scale, 0.0f));
+      }
+    }
+  }
+}
+
+}  // namespace asr_embed
+
+// =========================================================== host side
+namespace {
+
+using asr_host::fail;
+using asr_host::hip_fail;
+using asr_host::ok;
+using namespace asr_embed;
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int64_t kMaxDim = int64_t{1} << 31;
+constexpr int64_t kMaxCols = int64_t{1} << 24;
+constexpr int64_t kMaxBytes = int64_t{1} << 39;   // of a table: fewer than 2**24 workgroups write its gradient
+constexpr int64_t kMaxChunks = 1024;              // of sorted tokens: what the join of one id walks
+constexpr int64_t kFillBytes = 65536;             // of a workgroup that writes rows of no token
+
+template <typename... A>
+hipError_t launch(void (*f)(A...), dim3 grid, int threads, hipStream_t s, std::common_type_t<A>... args) {
+  void* argv[] = {&args...};
+  return hipLaunchKernel(reinterpret_cast<const void*>(f), grid, dim3(threads), argv, 0, s);
+}
+
+// log2 of the lanes of a row: 8 columns each, at most a workgroup
+int32_t lanes_of(int64_t dim) {
+  int32_t l = 0;
+  while (l < 8 && (int64_t{8} << l) < dim) ++l;
+  return l;
+}
+
+struct Cut {
+  int32_t chunk, chunks;
+  int64_t tiles;
+  explicit Cut(int64_t n) {
+    // 16 positions a chunk at least: fewer leave more partial sums than rows are saved
+    int64_t c = 16;
+    while ((n + c - 1) / c > kMaxChunks) c *= 2;
+    chunk = static_cast<int32_t>(c);
+    chunks = static_cast<int32_t>((n + c - 1) / c);
+    tiles = (n + kTile - 1) / kTile;
+  }
+};
+
+// The buffers of the gradient in its workspace, each on a 256-byte boundary.
+struct Buffers {
+  char* base;
+  int64_t at = 0;
+  uint32_t *keys[2], *toks[2], *hist;
+  uint8_t* touched;
+  float* part;
+  template <typename P>
+  P* take(int64_t count) {
+    P* p = reinterpret_cast<P*>(base + at);
+    at += (count * static_cast<int64_t>(sizeof(P)) + 255) / 256 * 256;
+    return p;
+  }
+  Buffers(void* ws, int64_t n, int64_t vocab, int64_t dim) : base(static_cast<char*>(ws)) {
+    const Cut cut(n);
+    const bool several = cut.tiles > 1;
+    keys[0] = take<uint32_t>(n);
+    toks[0] = take<uint32_t>(n);
+    keys[1] = take<uint32_t>(several ? n : 0);
+    toks[1] = take<uint32_t>(several ? n : 0);
+    hist = take<uint32_t>(several ? kBins * cut.tiles : 0);
+    touched = take<uint8_t>((vocab + 15) / 16 * 16);
+    part = take<float>(static_cast<int64_t>(cut.chunks) * 2 * dim);
+  }
+};
+
+int check_table(int64_t n, int64_t vocab, int64_t dim, int32_t dtype) {
+  if (n < 0 || n >= kMaxDim || vocab < 0 || vocab >= kMaxDim)
+    return fail(ASR_EINVAL, "embedding: tokens and vocabulary must be in [0, 2**31)");
+  if (dim < 0 || dim > kMaxCols) return fail(ASR_EINVAL, "embedding: dim must be in [0, 2**24]");
+  if (dtype != ASR_F32 && dtype != ASR_BF16) return fail(ASR_EDTYPE, "embedding: unknown dtype");
+  return ASR_OK;
+}
+
+hipError_t sort_tokens(const Ids& ids, const Buffers& b, const Cut& cut, const uint32_t*& keys, const uint32_t*& toks,
+                       hipStream_t s) {
+  Sort a{};
+  a.ids = ids;
+  a.touched = b.touched;
+  uint32_t bits = 1;
+  while ((ids.vocab >> bits) != 0) ++bits;   // of the key `vocab`, the largest
+  a.passes = (bits + 7) / 8;
+  a.bits = (bits + a.passes - 1) / a.passes;
+  a.keys = b.keys[0];
+  a.toks = b.toks[0];
+  keys = a.keys;
+  toks = a.toks;
+  if (ids.n <= 1024) return launch(&sort_one<1>, dim3(1), 1024, s, a);
+  if (ids.n <= 2048) return launch(&sort_one<2>, dim3(1), 1024, s, a);
+  if (ids.n <= 4096) return launch(&sort_one<4>, dim3(1), 1024, s, a);
+  if (ids.n <= kTile) return launch(&sort_one<8>, dim3(1), 1024, s, a);
+  a.hist = b.hist;
+  a.tiles = static_cast<uint32_t>(cut.tiles);
+  hipError_t e = launch(&clear_flags, dim3(static_cast<uint32_t>(std::min<int64_t>((ids.vocab + 4095) / 4096, 1024))), 256, s,
+                        b.touched, ids.vocab);
+  for (uint32_t pass = 0; pass < a.passes && e == hipSuccess; ++pass) {
+    a.shift = pass * a.bits;
+    a.keys = b.keys[pass % 2];
+    a.toks = b.toks[pass % 2];
+    e = launch(&count_digits, dim3(a.tiles), 1024, s, a);
+    if (e == hipSuccess) e = launch(&scan_counts, dim3(1), 1024, s, b.hist, static_cast<int64_t>(kBins) * cut.tiles);
+    if (e == hipSuccess) e = launch(&scatter_digits, dim3(a.tiles), 1024, s, a);
+    a.keys_in = a.keys;
+    a.toks_in = a.toks;
+  }
+  keys = a.keys;
+  toks = a.toks;
+  return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+int asr_embedding_forward(const void* ids, int32_t ids_64, int64_t n, const void* table, int32_t dtype, int64_t ld,
+                          int64_t vocab, int64_t dim, double scale, void* y, void* stream) {
+  if (int rc = check_table(n, vocab, dim, dtype)) return rc;
+  if (!std::isfinite(static_cast<float>(scale))) return fail(ASR_EINVAL, "embedding: scale must be finite in binary32");
+  if (n == 0 || dim == 0) return ok();
+  if (!ids || !y || (vocab > 0 && !table)) return fail(ASR_EINVAL, "embedding: null pointer");
+  if (ld < dim) return fail(ASR_EINVAL, "embedding: a row stride is below the row's length");
+  const uintptr_t size = dtype == ASR_F32 ? 4 : 2;
+  if (!aligned_to(ids, ids_64 ? 8 : 4) || !aligned_to(table, size) || !aligned_to(y, size))
+    return fail(ASR_EALIGN, "embedding: a pointer is not aligned to its elements");
+  Lookup a{};
+  a.ids = Ids{ids, ids_64 ? 1u : 0u, n, vocab, -1};
+  a.table = table;
+  a.y = y;
+  a.ld = ld;
+  a.dim = dim;
+  a.scale = static_cast<float>(scale);
+  a.log_lanes = lanes_of(dim);
+  a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
+  const int64_t rows = 256 >> a.log_lanes, up = (n + rows - 1) / rows;
+  if (up * a.strips >= kMaxDim) return fail(ASR_EINVAL, "embedding: too much for one call");
+  a.items = static_cast<uint32_t>(up * a.strips);
+  const uint32_t grid = std::min(a.items, 1u << 22);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = launch(dtype == ASR_F32 ? &lookup<float> : &lookup<uint16_t>, dim3(grid), 256, s, a);
+  return e == hipSuccess ? ok() : hip_fail(e, "embedding launch");
+}
+
+size_t asr_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
+  if (n <= 0 || n >= kMaxDim || vocab <= 0 || vocab >= kMaxDim || dim <= 0 || dim > kMaxCols) return 0;
+  return static_cast<size_t>(Buffers(nullptr, n, vocab, dim).at);
+}
+
+int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const void* dy, int64_t ld_dy, int32_t dtype,
+                           int64_t vocab, int64_t dim, double scale, int64_t padding_idx, void* dtable,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_table(n, vocab, dim, dtype)) return rc;
+  if (!std::isfinite(static_cast<float>(scale))) return fail(ASR_EINVAL, "embedding: scale must be finite in binary32");
+  if (padding_idx < -1 || padding_idx >= std::max<int64_t>(vocab, 1))
+    return fail(ASR_EINVAL, "embedding: padding_idx must be an id of the table, or -1");
+  if (vocab == 0 || dim == 0) return ok();
+  const int64_t size = dtype == ASR_F32 ? 4 : 2;
+  if (vocab > kMaxBytes / (dim * size)) return fail(ASR_EINVAL, "embedding: the table is too large for one call");
+  if (!dtable || (n > 0 && (!ids || !dy))) return fail(ASR_EINVAL, "embedding: null pointer");
+  if (n > 0 && ld_dy < dim) return fail(ASR_EINVAL, "embedding: a row stride is below the row's length");
+  if (!aligned_to(ids, ids_64 ? 8 : 4) || !aligned_to(dy, size) || !aligned_to(dtable, size))
+    return fail(ASR_EALIGN, "embedding: a pointer is not aligned to its elements");
+  if (n > 0 && (!workspace || !aligned_to(workspace, 256) ||
+                workspace_bytes < asr_embedding_backward_workspace_bytes(n, vocab, dim)))
+    return fail(ASR_EWORKSPACE, "embedding: workspace NULL, too small or not 256-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Sums a{};
+  a.dy = dy;
+  a.dw = dtable;
+  a.n = n;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.ld = ld_dy;
+  a.scale = static_cast<float>(scale);
+  a.log_lanes = lanes_of(dim);
+  a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
+  const int64_t side = 256 >> a.log_lanes;
+  a.fill_rows = std::max<int64_t>(1, (kFillBytes / (dim * size) + side - 1) / side) * side;
+  hipError_t e = hipSuccess;
+  if (n > 0) {
+    const Buffers b(workspace, n, vocab, dim);
+    const Cut cut(n);
+    a.touched = b.touched;
+    a.part = b.part;
+    a.chunk = cut.chunk;
+    a.chunks = cut.chunks;
+    a.sum_blocks = static_cast<uint32_t>((cut.chunks + side - 1) / side * a.strips);
+    e = sort_tokens(Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, b, cut, a.keys, a.toks, s);
+  }
+  const int64_t grid = a.sum_blocks + (vocab + a.fill_rows - 1) / a.fill_rows;
+  if (e == hipSuccess)
+    e = launch(dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>, dim3(static_cast<uint32_t>(grid)), 256, s, a);
+  if (e == hipSuccess && a.chunks > 1)
+    e = launch(dtype == ASR_F32 ? &join_runs<float> : &join_runs<uint16_t>,
+               dim3(static_cast<uint32_t>(a.chunks), static_cast<uint32_t>((dim + 1023) / 1024)), 1024, s, a);
+  return e == hipSuccess ? ok() : hip_fail(e, "embedding launch");
+}
+
+}  // extern "C"

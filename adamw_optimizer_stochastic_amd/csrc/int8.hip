@@ -5,16 +5,12 @@
 //   s = f32(max|x| / 127),  q = sign(x) * min(127, Q(|x| / s)),
 // where Q rounds the EXACT quotient: to nearest, ties to even, or
 // stochastically, floor(|x|/s + r16/65536) with the 16 bits of the element's
-// stream position. The decision is exact and needs no division: with c =
-// (k + 1) - r16/65536 (at most 24 bits, so exact in binary32), |x|/s + r16/65536
-// reaches k + 1 exactly when fma(-c, s, |x|) >= 0, and one rounding keeps a
-// sign. k comes from |x| * (1/s), off by at most one, and two such tests
-// settle it; to nearest is the same with r16 = 32768 and a step back from an
-// odd tie.
+// stream position (codes.hpp).
 //
 // product: C[m][n] = round((f32(sum_k A[m][k] B[n][k]) * sa[m]) * sb[n]), the
 // sum exact in 32-bit integers (K < 2**17), so it does not depend on how K
 // is split or ordered.
+#include "codes.hpp"
 #include "mfma_loop.hpp"
 #include "status.hpp"
 
@@ -30,111 +26,6 @@ namespace asr_i8 {
 using asr_mfma::static_for;
 
 // ------------------------------------------------------------- quantiser
-struct __align__(16) GroupScale {
-  float s;        // the scale the group's codes are divided by, times k
-  float inv;      // 1 / s
-  float k;        // power of two that keeps every product with s a normal number
-  uint32_t live;  // all ones, or 0: every code is 0 (no element, only tiny ones, Inf or NaN)
-};
-
-// The scale to store for a group whose largest |x| has these bits, and what
-// the codes need. Below 127 * 2**-126 the scale would be subnormal: such a
-// group is stored as zeros. Inf or NaN anywhere makes the scale NaN, which
-// every product with the group then shows.
-__device__ __forceinline__ float group_scale(uint32_t max_bits, GroupScale& g) {
-  const float s = __uint_as_float(max_bits) / 127.0f;
-  const bool finite = max_bits < 0x7F800000u;
-  const bool live = finite && s >= 0x1p-126f;
-  g.live = live ? 0xFFFFFFFFu : 0u;
-  g.k = s < 0x1p-60f ? 0x1p64f : 1.0f;
-  g.s = live ? s * g.k : 1.0f;
-  g.inv = 1.0f / g.s;
-  return finite ? (live ? s : 0.0f) : __uint_as_float(0x7FC00000u);
-}
-
-// The exact code of any element (of a live group).
-template <bool SR>
-__device__ __forceinline__ int32_t exact_code(float x, const GroupScale& g, uint32_t r16) {
-  const float ax = __builtin_fabsf(x) * g.k;
-  const float r = SR ? static_cast<float>(r16) * 0x1p-16f : 0.5f;
-  float q = __builtin_floorf(__builtin_fmaf(ax, g.inv, r));
-  if (__builtin_fmaf(-((q + 1.0f) - r), g.s, ax) >= 0.0f) {
-    q += 1.0f;
-  } else if (__builtin_fmaf(-(q - r), g.s, ax) < 0.0f) {
-    q -= 1.0f;
-  }
-  int32_t i = static_cast<int32_t>(q);
-  if constexpr (!SR) {
-    if ((i & 1) && __builtin_fmaf(-(q - 0.5f), g.s, ax) == 0.0f) i -= 1;
-  }
-  i = min(i, 127);
-  return x < 0.0f ? -i : i;
-}
-
-// Codes of 4 elements of one group, packed. With the exact decision for every
-// element its arithmetic is what bounds the kernels, so the usual case is short: |x| * (1/s) is off by less than
-// 2**-16 here, so a value further than that from a border has its code from
-// one multiply-add (to nearest: onto 1.5 * 2**23, whose low byte is then the
-// code; stochastic: floor of the quotient plus 1 + r16/65536). A wave that
-// has an element nearer (1e-4) than that decides these exactly: 40 instructions an
-// element instead of 6. (58.7e6 bf16 values, rows, RN: 43 us, 58 us with the
-// exact decision for all.)
-
-// Byte 0 of four words. (As asm: the compiler takes the permutes apart into
-// 16-bit shifts and merges, three times as many instructions.)
-__device__ __forceinline__ uint32_t pack_bytes(uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
-  uint32_t lo, hi, all;
-  asm("v_perm_b32 %0, %1, %2, %3" : "=v"(lo) : "v"(u1), "v"(u0), "s"(0x0C0C0400u));
-  asm("v_perm_b32 %0, %1, %2, %3" : "=v"(hi) : "v"(u3), "v"(u2), "s"(0x0C0C0400u));
-  asm("v_perm_b32 %0, %1, %2, %3" : "=v"(all) : "v"(hi), "v"(lo), "s"(0x05040100u));
-  return all;
-}
-
-template <bool SR>
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], const GroupScale& g,
-                                           const uint32_t (&r16)[4]) {
-  constexpr float kByte = 12582912.0f;  // 1.5 * 2**23
-  uint32_t u[4];
-  float off[4];  // distance from the middle between two borders
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (SR) {
-      const float one_r = __uint_as_float(0x3F800000u | (r16[e] << 7));  // 1 + r16 / 65536
-      const float v = __builtin_fmaf(__builtin_fabsf(x[e]), g.inv, one_r);
-      const float f = __builtin_floorf(v);
-      off[e] = (v - f) - 0.5f;
-      u[e] = __float_as_uint(__builtin_copysignf(__builtin_fminf(f - 1.0f, 127.0f), x[e]) + kByte);
-    } else {
-      const float t = __builtin_fmaf(x[e], g.inv, kByte);
-      off[e] = __builtin_fmaf(x[e], g.inv, -(t - kByte));
-      u[e] = __float_as_uint(t);
-    }
-  }
-  float most = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(off[0]), __builtin_fabsf(off[1])),
-                               __builtin_fmaxf(__builtin_fabsf(off[2]), __builtin_fabsf(off[3])));
-  // (a scaled group, k != 1, takes the exact way: its inv is that of the scaled s)
-  if (__builtin_amdgcn_ballot_w64(most > 0.4999f || g.k != 1.0f) != 0) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      u[e] = static_cast<uint32_t>(exact_code<SR>(g.live ? x[e] : 0.0f, g, r16[e]));
-  }
-  return pack_bytes(u[0], u[1], u[2], u[3]) & g.live;
-}
-
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-// 8 consecutive elements from column j of a row (j a multiple of 8); past
-// `cols` they are zero.
-template <typename S>
-__device__ __forceinline__ void load8(const S* row, int64_t j, int64_t cols, bool vec,
-                                      float (&x)[8]) {
-  if (vec && j + 8 <= cols) {
-    asr::load_vec<false, 8>(row + j, x);
-  } else {
-    asr::load_range<8>(row, j, 0, static_cast<int>(max(int64_t{0}, min(int64_t{8}, cols - j))), x);
-  }
-}
-
 // A matrix of a launch, and the codes wanted of it: of its rows, of its
 // columns, or both.
 struct QuantJob {
@@ -145,6 +36,7 @@ struct QuantJob {
   float* s_col;
   uint32_t* part_row;   // row maxima of each strip of 256 columns
   uint32_t* part_col;   // column maxima of each chunk of rows
+  const float* weigh;   // column codes are of x[r][c] * weigh[r] (NULL: of x)
   int64_t ldx, ld_row, ld_col;
   uint64_t base;
   int32_t rows, cols, chunk, strips, tiles;
@@ -241,11 +133,15 @@ __global__ __launch_bounds__(256) void quantize_rows(QuantArgs args) {
   }
 }
 
+__device__ __forceinline__ float row_weight(const QuantJob& a, int64_t r) {
+  return a.weigh && r < a.rows ? a.weigh[r] : 1.0f;
+}
+
 // Column maxima of one chunk of rows, and if wanted the row maxima of one
 // strip: a workgroup takes 256 columns (512 bytes of a bf16 row), 8 rows at a
 // time. Few chunks, so that the second kernel reads few of them. Bound by
 // memory: 8192 x 4096 bf16 (67 MB) in 11.5-12.5 us, 5.4-5.8 TB/s.
-template <typename S>
+template <typename S, bool WEIGH>
 __global__ __launch_bounds__(256) void maxima(QuantArgs args) {
   __shared__ uint32_t tops[8][256 + 4];
   const QuantJob& a = job_of(args);
@@ -264,10 +160,12 @@ __global__ __launch_bounds__(256) void maxima(QuantArgs args) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t across = 0;
+      [[maybe_unused]] const float weight = WEIGH ? row_weight(a, r + 8 * i) : 1.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t v = abs_bits(t[i][e]);
-        top[e] = max(top[e], v);
+        if constexpr (WEIGH) top[e] = max(top[e], abs_bits(t[i][e] * weight));
+        else top[e] = max(top[e], v);
         across = max(across, v);
       }
       if (a.part_row) {
@@ -300,35 +198,6 @@ __global__ __launch_bounds__(256) void join_strips(uint32_t* part, int32_t rows,
   part[r] = m;
 }
 
-// 8 elements as they lie in memory.
-template <typename S>
-struct Raw8;
-template <>
-struct Raw8<uint16_t> {
-  asr::u32x4 w;
-  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const asr::u32x4*>(p); }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = (__float_as_uint(x[2 * k]) >> 16) | (__float_as_uint(x[2 * k + 1]) & 0xFFFF0000u);
-  }
-  __device__ __forceinline__ float get(int e) const {
-    return __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-  }
-};
-template <>
-struct Raw8<float> {
-  asr::f32x4 w[2];
-  __device__ __forceinline__ void load(const float* p) {
-    w[0] = reinterpret_cast<const asr::f32x4*>(p)[0];
-    w[1] = reinterpret_cast<const asr::f32x4*>(p)[1];
-  }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    w[0] = asr::f32x4{x[0], x[1], x[2], x[3]};
-    w[1] = asr::f32x4{x[4], x[5], x[6], x[7]};
-  }
-  __device__ __forceinline__ float get(int e) const { return w[e / 4][e % 4]; }
-};
-
 // Codes of 64 columns x `tiles` times 128 rows, tile by tile: of the columns,
 // written as 64 rows of the transposed result, and if wanted of the rows (which
 // share the random bits, most of the stochastic form's work). A thread takes
@@ -346,7 +215,7 @@ struct TileLds {
   GroupScale row_scale[128];
 };
 
-template <typename S, bool SR>
+template <typename S, bool SR, bool WEIGH>
 __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const QuantJob& a, TileLds& lds) {
   constexpr int kWords = 33;
   const int32_t across = (a.cols + 63) / 64;
@@ -374,7 +243,7 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
     }
   };
   fetch(tr0);
-  if (a.chunks == 0) {  // this tile is all of its columns
+  if (!WEIGH && a.chunks == 0) {  // this tile is all of its columns
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       uint32_t top = 0;
@@ -423,6 +292,11 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[i][e] = raw[i].get(e);
     if (tr + 1 < tr1) fetch(tr + 1);
+    [[maybe_unused]] float weight[4];
+    if constexpr (WEIGH) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) weight[i] = row_weight(a, r0 + rg * 4 + i);
+    }
     uint32_t bits[4][8] = {};
     if constexpr (SR) {
 #pragma unroll
@@ -436,7 +310,11 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const GroupScale g = lds.col_scale[cg * 8 + e];
-      const float v[4] = {x[0][e], x[1][e], x[2][e], x[3][e]};
+      float v[4] = {x[0][e], x[1][e], x[2][e], x[3][e]};
+      if constexpr (WEIGH) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= weight[i];
+      }
       const uint32_t r[4] = {bits[0][e], bits[1][e], bits[2][e], bits[3][e]};
       lds.tile[(cg * 8 + e) * kWords + rg] = codes4<SR>(v, g, r);
     }
@@ -466,12 +344,64 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
   }
 }
 
-template <typename S>
+template <typename S, bool WEIGH>
 __global__ __launch_bounds__(256) void quantize_tiles(QuantArgs args) {
   __shared__ TileLds lds;
   const QuantJob& a = job_of(args);
-  if (a.sr) quantize_strip<S, true>(args, a, lds);
-  else quantize_strip<S, false>(args, a, lds);
+  if (a.sr) quantize_strip<S, true, WEIGH>(args, a, lds);
+  else quantize_strip<S, false, WEIGH>(args, a, lds);
+}
+
+// Codes turned round: q (rows x cols, padded with zeros to a multiple of 16
+// columns) to qt (cols x rows, likewise), and a scale of 1 for each of qt's rows.
+// A tile of 128 x 128; a thread turns 8 rows of 8 columns, 4 x 4 bytes at a time
+// by byte permutes, so that LDS holds whole words of a column.
+struct TurnArgs {
+  const int8_t* q;
+  int8_t* qt;
+  float* ones;
+  int64_t ldq, ldt;
+  int32_t rows, cols, tiles_c;
+};
+
+__global__ __launch_bounds__(256) void turn_codes(TurnArgs a) {
+  constexpr int kWords = 33;
+  __shared__ uint32_t tile[128 * kWords];
+  const int32_t tc = blockIdx.x % a.tiles_c, tr = blockIdx.x / a.tiles_c;
+  const int64_t c0 = static_cast<int64_t>(tc) * 128, r0 = static_cast<int64_t>(tr) * 128;
+  const int cg = threadIdx.x % 16, rg = threadIdx.x / 16;   // 8 columns, rows rg * 8 .. + 7
+  const int64_t col = c0 + cg * 8, padded = (static_cast<int64_t>(a.cols) + 15) / 16 * 16;
+  asr::u32x2 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + rg * 8 + i;
+    w[i] = r < a.rows && col < padded ? *reinterpret_cast<const asr::u32x2*>(a.q + r * a.ldq + col) : asr::u32x2{0, 0};
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)      // 4 rows
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 4 columns
+      const uint32_t lo01 = __builtin_amdgcn_perm(w[i * 4 + 1][h], w[i * 4][h], 0x05010400u);
+      const uint32_t hi01 = __builtin_amdgcn_perm(w[i * 4 + 1][h], w[i * 4][h], 0x07030602u);
+      const uint32_t lo23 = __builtin_amdgcn_perm(w[i * 4 + 3][h], w[i * 4 + 2][h], 0x05010400u);
+      const uint32_t hi23 = __builtin_amdgcn_perm(w[i * 4 + 3][h], w[i * 4 + 2][h], 0x07030602u);
+      uint32_t* to = tile + (cg * 8 + h * 4) * kWords + rg * 2 + i;
+      to[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+      to[kWords] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+      to[2 * kWords] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+      to[3 * kWords] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int cc = (k * 256 + threadIdx.x) / 8, part = threadIdx.x % 8;
+    const int64_t r = r0 + part * 16;
+    if (c0 + cc < a.cols && r < a.rows) {
+      const uint32_t* t = tile + cc * kWords + part * 4;
+      *reinterpret_cast<asr::u32x4*>(a.qt + (c0 + cc) * a.ldt + r) = asr::u32x4{t[0], t[1], t[2], t[3]};
+    }
+  }
+  if (tr == 0 && threadIdx.x < 128 && c0 + threadIdx.x < a.cols) a.ones[c0 + threadIdx.x] = 1.0f;
 }
 
 // --------------------------------------------------------------- product
@@ -822,14 +752,14 @@ hipError_t launch_rows(asr_i8::QuantArgs& a, hipStream_t s) {
 }
 
 // Column codes of every job, and row codes of those that want them too.
-template <typename S>
+template <typename S, bool WEIGH = false>
 hipError_t launch_tiles(asr_i8::QuantArgs& a, hipStream_t s) {
   constexpr int32_t kJoin = 16;  // strips a tile reads itself: half a matrix row's bytes at most
   int64_t total = 0;
   // One tile of rows finds its columns' maxima itself, in one launch: 128 x 64 to
   // 8192 6.5 to 8.0 us instead of 10.0 to 11.9. (A strip of two tiles, walked twice
   // by its workgroup: 10.1 to 12.3 against 10.6 to 11.9.)
-  const bool alone = a.count == 1 && !a.j[0].q_row && a.j[0].rows <= 128;
+  const bool alone = !WEIGH && a.count == 1 && !a.j[0].q_row && a.j[0].rows <= 128;
   for (int k = 0; k < a.count; ++k) {
     asr_i8::QuantJob& j = a.j[k];
     const Cut cut(j.rows, j.cols);
@@ -840,7 +770,7 @@ hipError_t launch_tiles(asr_i8::QuantArgs& a, hipStream_t s) {
     j.blocks = static_cast<uint32_t>(cut.strips * cut.chunks);
     total += j.blocks;
   }
-  hipError_t e = alone ? hipSuccess : launch(&asr_i8::maxima<S>, total, 256, &a, s);
+  hipError_t e = alone ? hipSuccess : launch(&asr_i8::maxima<S, WEIGH>, total, 256, &a, s);
   total = 0;
   for (int k = 0; k < a.count && e == hipSuccess; ++k) {
     asr_i8::QuantJob& j = a.j[k];
@@ -858,7 +788,7 @@ hipError_t launch_tiles(asr_i8::QuantArgs& a, hipStream_t s) {
     j.blocks = static_cast<uint32_t>(across * ((down + j.tiles - 1) / j.tiles));
     total += j.blocks;
   }
-  return e == hipSuccess ? launch(&asr_i8::quantize_tiles<S>, total, 256, &a, s) : e;
+  return e == hipSuccess ? launch(&asr_i8::quantize_tiles<S, WEIGH>, total, 256, &a, s) : e;
 }
 
 // A launch has fewer than 2**32 threads: of 256-thread workgroups, this many.
@@ -1047,6 +977,17 @@ int check_operand(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   return ASR_OK;
 }
 
+// The codes of a linear layer's input, kept for its backward pass.
+int check_saved(const int8_t* q, int64_t ldq, const float* scale, int64_t tokens, int64_t k) {
+  if (tokens == 0 || k == 0) return ok();
+  if (!q || !scale) return fail(ASR_EINVAL, "linear_i8: null pointer");
+  if (ldq % 16 != 0 || ldq < padded16(k) || ldq >= asr_mfma::kMaxLdBytes)
+    return fail(ASR_EINVAL, "linear_i8: ldq must be a multiple of 16 and hold a token's codes up to a multiple of 16");
+  if (!aligned_to(q, 16) || !aligned_to(scale, 4))
+    return fail(ASR_EALIGN, "linear_i8: codes aligned to 16 bytes, scales to 4");
+  return ASR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1157,9 +1098,9 @@ size_t asr_linear_i8_workspace_bytes(int64_t tokens, int64_t n, int64_t k, int32
                                       : LinearForward(nullptr, tokens, n, k).bytes);
 }
 
-int asr_linear_i8_forward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, uint16_t* y,
-                          int64_t ldy, int64_t tokens, int64_t n, int64_t k, void* workspace,
-                          size_t workspace_bytes, void* stream) {
+static int linear_forward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, uint16_t* y,
+                          int64_t ldy, int8_t* q, int64_t ldq, float* scale, int64_t tokens, int64_t n, int64_t k,
+                          void* workspace, size_t workspace_bytes, void* stream) {
   if (int rc = check_linear(tokens, n, k)) return rc;
   if (int rc = check_operand(x, ldx, tokens, k)) return rc;
   if (int rc = check_operand(w, ldw, n, k)) return rc;
@@ -1175,7 +1116,11 @@ int asr_linear_i8_forward(const uint16_t* x, int64_t ldx, const uint16_t* w, int
   if (!workspace || !aligned_to(workspace, 256) ||
       workspace_bytes < asr_linear_i8_workspace_bytes(tokens, n, k, 0))
     return fail(ASR_EWORKSPACE, "linear_i8: workspace NULL, too small or not 256-byte aligned");
-  const LinearForward f(workspace, tokens, n, k);
+  LinearForward f(workspace, tokens, n, k);
+  if (q) {  // x's codes go to the caller
+    f.qx = q;
+    f.sx = scale;
+  }
   asr_i8::QuantArgs a{};
   a.count = 2;
   a.j[0] = matrix_job(x, ldx, 2, tokens, k);
@@ -1184,23 +1129,42 @@ int asr_linear_i8_forward(const uint16_t* x, int64_t ldx, const uint16_t* w, int
   a.j[1] = matrix_job(w, ldw, 2, n, k);
   a.j[1].q_row = f.qw;
   a.j[1].s_row = f.sw;
-  a.j[0].ld_row = a.j[1].ld_row = padded16(k);
+  const int64_t ld = q ? ldq : padded16(k);
+  a.j[0].ld_row = ld;
+  a.j[1].ld_row = padded16(k);
   hipError_t e = launch_rows<uint16_t, false>(a, s);
   if (e == hipSuccess)
-    e = product(gemm_args(f.qx, padded16(k), f.qw, padded16(k), f.sx, f.sw, y, ldy, nullptr, tokens, n, k),
+    e = product(gemm_args(f.qx, ld, f.qw, padded16(k), f.sx, f.sw, y, ldy, nullptr, tokens, n, k),
                 ASR_ROUND_RN, s);
   return e == hipSuccess ? ok() : hip_fail(e, "linear_i8 launch");
 }
 
-int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
-                           const uint16_t* dy, int64_t lddy, uint16_t* dx, int64_t lddx, uint16_t* dw,
+int asr_linear_i8_forward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, uint16_t* y,
+                          int64_t ldy, int64_t tokens, int64_t n, int64_t k, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  return linear_forward(x, ldx, w, ldw, y, ldy, nullptr, 0, nullptr, tokens, n, k, workspace, workspace_bytes, stream);
+}
+
+int asr_linear_i8_forward_saved(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, uint16_t* y,
+                                int64_t ldy, int8_t* q, int64_t ldq, float* scale, int64_t tokens, int64_t n,
+                                int64_t k, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_linear(tokens, n, k)) return rc;
+  if (int rc = check_saved(q, ldq, scale, tokens, k)) return rc;
+  if (n == 0 && tokens > 0 && k > 0)
+    return fail(ASR_EINVAL, "linear_i8: without outputs there is no product to keep x's codes of");
+  return linear_forward(x, ldx, w, ldw, y, ldy, q, ldq, scale, tokens, n, k, workspace, workspace_bytes, stream);
+}
+
+// The backward products; x or its codes (saved).
+static int linear_backward(const uint16_t* x, int64_t ldx, const int8_t* q, int64_t ldq, const float* scale,
+                           const uint16_t* w, int64_t ldw, const uint16_t* dy, int64_t lddy, uint16_t* dx, int64_t lddx, uint16_t* dw,
                            int64_t lddw, int64_t tokens, int64_t n, int64_t k, int32_t rounding,
                            uint32_t seed, uint32_t step, uint64_t base_index, void* workspace,
                            size_t workspace_bytes, void* stream) {
   if (int rc = check_linear(tokens, n, k)) return rc;
   if (rounding != ASR_ROUND_SR && rounding != ASR_ROUND_RN)
     return fail(ASR_EINVAL, "linear_i8: rounding must be ASR_ROUND_SR or ASR_ROUND_RN");
-  if (dw)
+  if (dw && !q)
     if (int rc = check_operand(x, ldx, tokens, k)) return rc;
   if (dx)
     if (int rc = check_operand(w, ldw, n, k)) return rc;
@@ -1242,13 +1206,20 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, in
     d.s_col = f.sdt;
     d.part_col = f.pd;
     d.ld_col = padded16(tokens);
+    d.weigh = q ? scale : nullptr;
     a.j[a.count++] = d;
-    asr_i8::QuantJob& j = a.j[a.count++];
-    j = matrix_job(x, ldx, 2, tokens, k);
-    j.q_col = f.qxt;
-    j.s_col = f.sxt;
-    j.part_col = f.px;
-    j.ld_col = padded16(tokens);
+    if (!q) {
+      asr_i8::QuantJob& j = a.j[a.count++];
+      j = matrix_job(x, ldx, 2, tokens, k);
+      j.q_col = f.qxt;
+      j.s_col = f.sxt;
+      j.part_col = f.px;
+      j.ld_col = padded16(tokens);
+    } else {
+      asr_i8::TurnArgs t{q, f.qxt, f.sxt, ldq, padded16(tokens), static_cast<int32_t>(tokens), static_cast<int32_t>(k),
+                         static_cast<int32_t>((k + 127) / 128)};
+      e = launch(&asr_i8::turn_codes, t.tiles_c * ((tokens + 127) / 128), 256, &t, s);
+    }
   } else {  // only the rows of dy
     a.count = 1;
     a.j[0] = d;
@@ -1263,7 +1234,7 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, in
     j.part_col = f.pw;
     j.ld_col = padded16(n);
   }
-  if (e == hipSuccess) e = launch_tiles<uint16_t>(a, s);
+  if (e == hipSuccess) e = dw && q ? launch_tiles<uint16_t, true>(a, s) : launch_tiles<uint16_t>(a, s);
   if (e == hipSuccess && dx)
     e = product(gemm_args(f.qd, padded16(n), f.qwt, padded16(n), f.sd, f.swt, dx, lddx, nullptr, tokens, k, n),
                 ASR_ROUND_RN, s);
@@ -1271,6 +1242,27 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, in
     e = product(gemm_args(f.qdt, padded16(tokens), f.qxt, padded16(tokens), f.sdt, f.sxt, dw, lddw, nullptr, n, k,
                           tokens), ASR_ROUND_RN, s);
   return e == hipSuccess ? ok() : hip_fail(e, "linear_i8 launch");
+}
+
+int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, const uint16_t* dy,
+                           int64_t lddy, uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw, int64_t tokens,
+                           int64_t n, int64_t k, int32_t rounding, uint32_t seed, uint32_t step, uint64_t base_index,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  return linear_backward(x, ldx, nullptr, 0, nullptr, w, ldw, dy, lddy, dx, lddx, dw, lddw, tokens, n, k, rounding,
+                         seed, step, base_index, workspace, workspace_bytes, stream);
+}
+
+int asr_linear_i8_backward_saved(const int8_t* q, int64_t ldq, const float* scale, const uint16_t* w, int64_t ldw,
+                                 const uint16_t* dy, int64_t lddy, uint16_t* dx, int64_t lddx, uint16_t* dw,
+                                 int64_t lddw, int64_t tokens, int64_t n, int64_t k, int32_t rounding, uint32_t seed,
+                                 uint32_t step, uint64_t base_index, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (int rc = check_linear(tokens, n, k)) return rc;
+  if (n == 0) dw = nullptr;   // (of no elements)
+  if (dw)
+    if (int rc = check_saved(q, ldq, scale, tokens, k)) return rc;
+  return linear_backward(nullptr, 0, q, ldq, scale, w, ldw, dy, lddy, dx, lddx, dw, lddw, tokens, n, k, rounding,
+                         seed, step, base_index, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

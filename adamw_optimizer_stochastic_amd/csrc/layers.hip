@@ -1,0 +1,996 @@
+// The layers between a model's products, and activations kept in 8 bits for
+// the backward pass.
+//
+// 8-bit activations: a block is 128 consecutive columns of a row (the last one
+// shorter) and has one scale: codes and scale as in codes.hpp. What they stand
+// for is f32(q * s). 1.03 bytes an element.
+//
+// layer norm of a row x of C columns:
+//   mean = sum x / C, var = sum (x - mean)^2 / C, rstd = 1 / sqrt(var + eps),
+//   xh = (x - mean) rstd, y = xh w + b;
+//   with g = dy w: dx = rstd (g - sum g / C - xh sum(g xh) / C),
+//   dw = sum over rows of dy xh, db = sum over rows of dy.
+// mean and var are summed in 64 bits (as fast here as in 32: the passes wait for
+// memory) and kept for the backward pass as two f32 numbers for the mean and
+// one for rstd. Or the pass keeps the 8-bit codes of xh instead of x: their
+// definition is the codes of the 64-bit xh, so that no rounding on the way
+// decides one, and gradients use what the codes stand for.
+//
+// gated SiLU: y = g sig(g) u, du = dy g sig(g), dg = dy u sig(g) (1 + g (1 - sig(g))),
+// from g and u themselves or from their 8-bit codes.
+//
+// All of it is bound by memory; each kernel reads its inputs once and holds
+// them in registers. 8 columns a lane, so 16 lanes hold a block of codes.
+#include "mfma_loop.hpp"
+#include "rows.hpp"
+#include "status.hpp"
+
+#include <adamw_sr.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+#include <type_traits>
+
+#pragma clang fp contract(off)
+
+namespace asr_layers {
+
+using namespace asr_rows;
+
+constexpr int kBlockCols = 128;  // columns that share a scale
+
+// ------------------------------------------------ elementwise over rows
+// A workgroup of 256 lanes is 16 groups of 16 lanes, a block of 128 columns each: 2**side
+// blocks of a row side by side, and 16 >> side rows. Items of work are numbered
+// row groups first, chunks of a row within.
+struct Grid {
+  int64_t rows;
+  int32_t cols, blocks;   // blocks of 128 columns in a row
+  int32_t side, chunks;   // log2 of blocks side by side; chunks of them in a row
+  uint32_t items;
+};
+
+struct Place {
+  int64_t row, col;
+  int32_t block;
+  int64_t count;     // columns from col to the row's end, 0 or less: none
+  int64_t padded;    // the same for stored codes, whose rows end at a multiple of 16
+};
+
+__device__ __forceinline__ Place place_of(const Grid& g, uint32_t item) {
+  const uint32_t chunks = static_cast<uint32_t>(g.chunks);
+  const uint32_t up = item / chunks, chunk = item - up * chunks;
+  const int group = threadIdx.x / 16;
+  Place p;
+  p.row = static_cast<int64_t>(up) * (16 >> g.side) + (group >> g.side);
+  p.block = static_cast<int32_t>(chunk << g.side) + (group & ((1 << g.side) - 1));
+  p.col = static_cast<int64_t>(p.block) * kBlockCols + threadIdx.x % 16 * 8;
+  const bool there = p.row < g.rows && p.block < g.blocks;
+  p.count = there ? g.cols - p.col : 0;
+  p.padded = there ? (static_cast<int64_t>(g.cols) + 15) / 16 * 16 - p.col : 0;
+  return p;
+}
+
+// Codes of 8 columns in a block that 16 lanes hold, and the block's scale.
+template <bool SR>
+__device__ __forceinline__ asr::u32x2 block_codes(const float (&x)[8], const uint32_t (&r)[8], float& scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, asr_i8::abs_bits(x[e]));
+  top = reduce16(top, [](uint32_t a, uint32_t b) { return max(a, b); });
+  asr_i8::GroupScale g;
+  scale = asr_i8::group_scale(top, g);
+  const float x0[4] = {x[0], x[1], x[2], x[3]}, x1[4] = {x[4], x[5], x[6], x[7]};
+  const uint32_t r0[4] = {r[0], r[1], r[2], r[3]}, r1[4] = {r[4], r[5], r[6], r[7]};
+  return asr::u32x2{asr_i8::codes4<SR>(x0, g, r0), asr_i8::codes4<SR>(x1, g, r1)};
+}
+
+struct Codes {
+  int8_t* q;
+  float* s;       // rows x blocks
+  int64_t ld;     // of q, a multiple of 8
+};
+
+__device__ __forceinline__ void store_codes(const Codes& c, const Grid& g, const Place& p, asr::u32x2 w, float scale) {
+  if (p.padded > 0) *reinterpret_cast<asr::u32x2*>(c.q + p.row * c.ld + p.col) = w;
+  if (threadIdx.x % 16 == 0 && p.count > 0) c.s[p.row * g.blocks + p.block] = scale;
+}
+
+// 8 codes and their block's scale as loaded; q's rows are padded to 16 bytes.
+struct Stored {
+  asr::u32x2 w;
+  float s;
+  __device__ __forceinline__ void load(const int8_t* q, const float* s_, bool there) {
+    w = there ? *reinterpret_cast<const asr::u32x2*>(q) : asr::u32x2{0, 0};
+    s = there ? *s_ : 0.0f;
+  }
+  __device__ __forceinline__ float get(int e) const {
+    return static_cast<float>(static_cast<int32_t>(w[e / 4] << (24 - e % 4 * 8)) >> 24) * s;
+  }
+};
+
+__device__ __forceinline__ Stored stored_at(const Codes& c, const Grid& g, const Place& p) {
+  Stored s;
+  s.load(c.q + p.row * c.ld + p.col, c.s + p.row * g.blocks + p.block, p.count > 0);
+  return s;
+}
+
+struct Pack {
+  Grid g;
+  void* x;       // read by pack, written by unpack
+  int64_t ldx;
+  Codes c;
+  uint64_t base;
+  uint32_t seed, step;
+};
+
+template <typename S, bool SR>
+__global__ __launch_bounds__(256) void pack(Pack a) {
+  for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
+    const Place p = place_of(a.g, item);
+    Run<S> raw;
+    raw.load(static_cast<const S*>(a.x) + p.row * a.ldx + p.col, p.count);
+    uint32_t bits[8] = {};
+    if constexpr (SR) {
+      const uint64_t at = a.base + static_cast<uint64_t>(p.row) * static_cast<uint64_t>(a.g.cols) +
+                          static_cast<uint64_t>(p.col);
+      asr_mfma::random_run<8>(at, (at & 3u) == 0, a.seed, a.step, bits);
+    }
+    float x[8], scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = raw.get(e);
+    const asr::u32x2 w = block_codes<SR>(x, bits, scale);
+    store_codes(a.c, a.g, p, w, scale);
+  }
+}
+
+template <typename S>
+__global__ __launch_bounds__(256) void unpack(Pack a) {
+  for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
+    const Place p = place_of(a.g, item);
+    const Stored c = stored_at(a.c, a.g, p);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = c.get(e);
+    store8(static_cast<S*>(a.x) + p.row * a.ldx + p.col, p.count, x);
+  }
+}
+
+// --------------------------------------------------------- gated SiLU
+struct Silu {
+  Grid g;
+  const void* gate;
+  const void* up;
+  const void* dy;
+  void* y;
+  void* dgate;
+  void* dup;
+  Codes cg, cu;
+  int64_t ld_gate, ld_up, ld_dy, ld_y, ld_dgate, ld_dup;
+};
+
+// 1 / (1 + exp(-x)). For bf16 values the exponential and reciprocal
+// instructions, which are off by 2**-20 of the value at most for |x| < 16 (and
+// where x is larger by |x| 2**-23): far below the output's 2**-9. f32 values take
+// the accurate functions.
+template <typename S>
+__device__ __forceinline__ float sigmoid(float x) {
+  if constexpr (std::is_same_v<S, float>) return 1.0f / (1.0f + expf(-x));
+  else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
+template <typename S, bool SAVE>
+__global__ __launch_bounds__(256) void silu_forward(Silu a) {
+  for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
+    const Place p = place_of(a.g, item);
+    Run<S> rg, ru;
+    rg.load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
+    ru.load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
+    float g[8], u[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] = rg.get(e);
+      u[e] = ru.get(e);
+      y[e] = g[e] * sigmoid<S>(g[e]) * u[e];
+    }
+    store8(static_cast<S*>(a.y) + p.row * a.ld_y + p.col, p.count, y);
+    if constexpr (SAVE) {
+      const uint32_t none[8] = {};
+      float scale;
+      asr::u32x2 w = block_codes<false>(g, none, scale);
+      store_codes(a.cg, a.g, p, w, scale);
+      w = block_codes<false>(u, none, scale);
+      store_codes(a.cu, a.g, p, w, scale);
+    }
+  }
+}
+
+template <typename S, bool SAVED>
+__global__ __launch_bounds__(256) void silu_backward(Silu a) {
+  for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
+    const Place p = place_of(a.g, item);
+    Run<S> rd;
+    rd.load(static_cast<const S*>(a.dy) + p.row * a.ld_dy + p.col, p.count);
+    std::conditional_t<SAVED, Stored, Run<S>> rg, ru;
+    if constexpr (SAVED) {
+      rg = stored_at(a.cg, a.g, p);
+      ru = stored_at(a.cu, a.g, p);
+    } else {
+      rg.load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
+      ru.load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
+    }
+    float dg[8], du[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = rg.get(e), d = rd.get(e), sig = sigmoid<S>(g);
+      du[e] = d * (g * sig);
+      dg[e] = d * ru.get(e) * (sig * (1.0f + g * (1.0f - sig)));
+    }
+    store8(static_cast<S*>(a.dgate) + p.row * a.ld_dgate + p.col, p.count, dg);
+    store8(static_cast<S*>(a.dup) + p.row * a.ld_dup + p.col, p.count, du);
+  }
+}
+
+// ---------------------------------------------------------- layer norm
+// What the backward pass needs of a row.
+struct __align__(16) RowStat {
+  float mean, rest;   // their sum is the mean
+  float rstd, none;
+};
+
+struct Norm {
+  const void* x;
+  const void* w;
+  const void* b;
+  const void* dy;
+  void* y;
+  void* dx;
+  RowStat* stat;
+  float* part;        // backward: sums of a workgroup's rows, [workgroup][dw, db][cols]
+  void* dw;
+  void* db;
+  Codes c;
+  int64_t rows, ldx, ld_dy;
+  int32_t cols, blocks;
+  double eps, inv_cols;
+  float inv_cols32;
+  uint32_t w_bf16, alone;   // alone: one workgroup, whose sums are the result
+};
+
+// The sum over the waves of a row (LANES / 64 of them), in every lane.
+template <int LANES, int THREADS>
+__device__ __forceinline__ double row_sum(double v, double* lds) {
+  v = wave_sum(v);
+  if constexpr (LANES > 64) {
+    constexpr int kWaves = LANES / 64;
+    __syncthreads();  // (what was summed before has been read)
+    if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += lds[threadIdx.x / LANES * kWaves + i];
+  }
+  return v;
+}
+
+__device__ __forceinline__ RowStat stat_of(double mean, double rstd) {
+  RowStat s;
+  s.mean = static_cast<float>(mean);
+  s.rest = static_cast<float>(mean - static_cast<double>(s.mean));
+  s.rstd = static_cast<float>(rstd);
+  s.none = 0.0f;
+  return s;
+}
+
+__device__ __forceinline__ float normal(float x, const RowStat& s) { return ((x - s.mean) - s.rest) * s.rstd; }
+
+// The sum of 8 columns, and of their squared distances to a mean, in 64 bits.
+__device__ __forceinline__ double sum8(const float (&x)[8]) {
+  double t = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t += static_cast<double>(x[e]);
+  return t;
+}
+
+__device__ __forceinline__ double squares8(const float (&x)[8], int64_t count, double mean) {
+  double t = 0.0;
+  if (count >= 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double d = static_cast<double>(x[e]) - mean;
+      t = __builtin_fma(d, d, t);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e) {
+      const double d = static_cast<double>(x[e]) - mean;
+      if (e < count) t = __builtin_fma(d, d, t);
+    }
+  }
+  return t;
+}
+
+// Codes of the normalised values of 8 columns, decided in 64 bits: with the largest
+// |x - mean| of the block, from its largest and smallest x (16 lanes).
+__device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t count, double mean, double rstd,
+                                                 float& scale) {
+  float hi = -__builtin_inff(), lo = __builtin_inff();
+  if (count >= 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      hi = __builtin_fmaxf(hi, x[e]);
+      lo = __builtin_fminf(lo, x[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e) {
+      hi = e < count ? __builtin_fmaxf(hi, x[e]) : hi;
+      lo = e < count ? __builtin_fminf(lo, x[e]) : lo;
+    }
+  }
+  hi = reduce16(hi, [](float a, float b) { return __builtin_fmaxf(a, b); });
+  lo = reduce16(lo, [](float a, float b) { return __builtin_fminf(a, b); });
+  // (a NaN or Inf in the row has made the mean one)
+  const double top = __builtin_fmax(__builtin_fabs(static_cast<double>(hi) - mean),
+                                    __builtin_fabs(static_cast<double>(lo) - mean)) * rstd;
+  const float s = static_cast<float>(top / 127.0);
+  const bool finite = s < __builtin_inff();    // (false for NaN)
+  const bool live = finite && s >= 0x1p-126f;
+  scale = finite ? (live ? s : 0.0f) : __uint_as_float(0x7FC00000u);
+  const double turn = live ? rstd / static_cast<double>(s) : 0.0;
+  uint32_t u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double t = __builtin_rint((static_cast<double>(x[e]) - mean) * turn);
+    const int32_t k = live && e < count ? static_cast<int32_t>(__builtin_fmin(__builtin_fmax(t, -127.0), 127.0)) : 0;
+    u[e] = static_cast<uint32_t>(k);
+  }
+  return asr::u32x2{asr_i8::pack_bytes(u[0], u[1], u[2], u[3]), asr_i8::pack_bytes(u[4], u[5], u[6], u[7])};
+}
+
+// Rows of up to LANES * KEEP * 8 columns, held in registers by LANES lanes.
+template <typename S, int LANES, int KEEP, bool SAVE>
+__global__ __launch_bounds__(256) void norm_rows(Norm a) {
+  __shared__ double lds[4];
+  const int lane = threadIdx.x % LANES;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const bool live = row < a.rows;
+  const S* x = static_cast<const S*>(a.x) + row * a.ldx;
+  float keep[KEEP][8];
+  double total = 0.0;
+  Run<S> raw[KEEP];
+#pragma unroll
+  for (int v = 0; v < KEEP; ++v) {
+    const int64_t col = (lane + v * LANES) * 8;
+    raw[v].load(x + col, live ? a.cols - col : 0);
+  }
+#pragma unroll
+  for (int v = 0; v < KEEP; ++v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) keep[v][e] = raw[v].get(e);
+    total += sum8(keep[v]);
+  }
+  const double mean = row_sum<LANES, 256>(total, lds) * a.inv_cols;
+  double squares = 0.0;
+#pragma unroll
+  for (int v = 0; v < KEEP; ++v) squares += squares8(keep[v], a.cols - (lane + v * LANES) * 8, mean);
+  const double var = row_sum<LANES, 256>(squares, lds) * a.inv_cols;
+  const double rstd = 1.0 / __builtin_sqrt(var + a.eps);
+  const RowStat stat = stat_of(mean, rstd);
+  if (a.stat && live && lane == 0) a.stat[row] = stat;
+  S* y = static_cast<S*>(a.y) + row * static_cast<int64_t>(a.cols);
+#pragma unroll
+  for (int v = 0; v < KEEP; ++v) {
+    const int64_t col = (lane + v * LANES) * 8, count = live ? a.cols - col : 0;
+    if constexpr (SAVE) {
+      float scale;
+      const asr::u32x2 codes = norm_codes(keep[v], count, mean, rstd, scale);
+      if (live && col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16) {
+        *reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col) = codes;
+        if (lane % 16 == 0 && count > 0) a.c.s[row * a.blocks + col / kBlockCols] = scale;
+      }
+    }
+    float w[8], b[8], out[8];
+    if (a.w) load_params(a.w, a.w_bf16, col, count, w);
+    if (a.b) load_params(a.b, a.w_bf16, col, count, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      out[e] = normal(keep[v][e], stat);
+      if (a.w) out[e] *= w[e];
+      if (a.b) out[e] += b[e];
+    }
+    store8(y + col, count, out);
+  }
+}
+
+// Longer rows: a workgroup each, read three times.
+template <typename S, bool SAVE>
+__global__ __launch_bounds__(256) void norm_long_rows(Norm a) {
+  __shared__ double lds[4];
+  const int64_t row = blockIdx.x;
+  const S* x = static_cast<const S*>(a.x) + row * a.ldx;
+  const int64_t padded = (static_cast<int64_t>(a.cols) + 127) / 128 * 128;  // (16 lanes stay together)
+  auto values = [&](int64_t col, float (&v)[8]) {
+    Run<S> raw;
+    raw.load(x + col, a.cols - col);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = raw.get(e);
+  };
+  double total = 0.0;
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
+    float v[8];
+    values(col, v);
+    total += sum8(v);
+  }
+  const double mean = row_sum<256, 256>(total, lds) * a.inv_cols;
+  double squares = 0.0;
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
+    float v[8];
+    values(col, v);
+    squares += squares8(v, a.cols - col, mean);
+  }
+  const double var = row_sum<256, 256>(squares, lds) * a.inv_cols;
+  const double rstd = 1.0 / __builtin_sqrt(var + a.eps);
+  const RowStat stat = stat_of(mean, rstd);
+  if (a.stat && threadIdx.x == 0) a.stat[row] = stat;
+  S* y = static_cast<S*>(a.y) + row * static_cast<int64_t>(a.cols);
+  // (whole waves: reduce16 wants every lane of a wave active)
+  for (int64_t start = 0; start < padded; start += 2048) {
+    const int64_t col = start + threadIdx.x * 8, count = a.cols - col;
+    float v[8], w[8], b[8], out[8];
+    values(col, v);
+    if constexpr (SAVE) {
+      float scale;
+      const asr::u32x2 codes = norm_codes(v, count, mean, rstd, scale);
+      if (col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16) {
+        *reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col) = codes;
+        if (threadIdx.x % 16 == 0 && count > 0) a.c.s[row * a.blocks + col / kBlockCols] = scale;
+      }
+    }
+    if (a.w) load_params(a.w, a.w_bf16, col, count, w);
+    if (a.b) load_params(a.b, a.w_bf16, col, count, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      out[e] = normal(v[e], stat);
+      if (a.w) out[e] *= w[e];
+      if (a.b) out[e] += b[e];
+    }
+    store8(y + col, count, out);
+  }
+}
+
+// Normalised values of 8 columns for the backward pass: from x, or from the codes.
+template <typename S, bool SAVED>
+struct Normalised {
+  std::conditional_t<SAVED, Stored, Run<S>> v;
+  __device__ __forceinline__ void load(const Norm& a, int64_t row, int64_t col, int64_t count) {
+    if constexpr (SAVED) {
+      v.load(a.c.q + row * a.c.ld + col, a.c.s + row * a.blocks + col / kBlockCols, count > 0);
+    } else {
+      v.load(static_cast<const S*>(a.x) + row * a.ldx + col, count);
+    }
+  }
+  __device__ __forceinline__ float get(int e, const RowStat& s) const {
+    if constexpr (SAVED) return v.get(e);
+    else return normal(v.get(e), s);
+  }
+};
+
+__device__ __forceinline__ void store_param(void* p, bool bf16, int64_t i, float x) {
+  if (bf16) static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(bf16_pair(x, 0.0f));
+  else static_cast<float*>(p)[i] = x;
+}
+
+// dx, and the sums over rows for dw and db. A row of up to LANES * 8 columns takes
+// LANES lanes of a workgroup of 1024, its next row `gridDim` times 1024 / LANES
+// further. A lane keeps its columns' sums over all of its rows in registers, the
+// next row is loaded while this one is worked on, and one barrier a row joins
+// the waves' sums (two sets of them in turn). In the end the groups' sums meet
+// in LDS. (16 columns a lane would take more registers than 16 waves have.)
+template <typename S, bool SAVED, int LANES>
+__global__ __launch_bounds__(1024) void norm_backward(Norm a) {
+  constexpr int kGroups = 1024 / LANES, kWaves = LANES / 64, kCols = LANES * 8;
+  __shared__ float sums[kGroups * kCols];
+  __shared__ f32x2 joint[2][16];
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const int64_t col = lane * 8;
+  float w[8], dw[8] = {}, db[8] = {};
+  if (a.w) {
+    load_params(a.w, a.w_bf16, col, a.cols - col, w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+  }
+  Run<S> dy, dy_next;
+  Normalised<S, SAVED> xh, xh_next;
+  RowStat stat, stat_next;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups;
+  auto fetch = [&](int64_t row) {
+    const bool live = row < a.rows;
+    const int64_t count = live ? a.cols - col : 0;
+    stat_next = live ? a.stat[row] : RowStat{0.0f, 0.0f, 0.0f, 0.0f};
+    dy_next.load(static_cast<const S*>(a.dy) + row * a.ld_dy + col, count);
+    xh_next.load(a, row, col, count);
+  };
+  int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups;
+  fetch(first + group);
+  for (int turn = 0; first < a.rows; first += stride, turn ^= 1) {
+    const int64_t row = first + group;
+    stat = stat_next;
+    dy = dy_next;
+    xh = xh_next;
+    if (first + stride < a.rows) fetch(row + stride);
+    f32x2 c = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = dy.get(e), h = xh.get(e, stat), g = d * w[e];
+      c.x += g;
+      c.y = __builtin_fmaf(g, h, c.y);
+      dw[e] = __builtin_fmaf(d, h, dw[e]);
+      db[e] += d;
+    }
+    c.x = wave_sum(c.x);
+    c.y = wave_sum(c.y);
+    if constexpr (kWaves > 1) {
+      if (threadIdx.x % 64 == 0) joint[turn][threadIdx.x / 64] = c;
+      __syncthreads();
+      c = f32x2{0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        c.x += joint[turn][group * kWaves + i].x;
+        c.y += joint[turn][group * kWaves + i].y;
+      }
+    }
+    if (a.dx) {
+      const float m = c.x * a.inv_cols32, k = c.y * a.inv_cols32;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (dy.get(e) * w[e] - m - xh.get(e, stat) * k) * stat.rstd;
+      store8(static_cast<S*>(a.dx) + row * static_cast<int64_t>(a.cols) + col, row < a.rows ? a.cols - col : 0, x);
+    }
+  }
+  auto finish = [&](const float (&mine)[8], void* result, int which) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[group * kCols + col + e] = mine[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.cols; i += 1024) {
+      float t = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) t += sums[k * kCols + i];
+      if (a.alone) store_param(result, a.w_bf16, i, t);
+      else a.part[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.cols + i] = t;
+    }
+  };
+  if (a.dw) finish(dw, a.dw, 0);
+  if (a.db) finish(db, a.db, 1);
+}
+
+// Longer rows: dx by a workgroup a row, in two passes over it.
+template <typename S, bool SAVED>
+__global__ __launch_bounds__(256) void norm_backward_long(Norm a) {
+  __shared__ double lds[4];
+  const int64_t row = blockIdx.x;
+  const RowStat stat = a.stat[row];
+  double c0 = 0.0, c1 = 0.0;
+  auto values = [&](int64_t col, float (&g)[8], float (&h)[8]) {
+    const int64_t count = a.cols - col;
+    Run<S> dy;
+    Normalised<S, SAVED> xh;
+    dy.load(static_cast<const S*>(a.dy) + row * a.ld_dy + col, count);
+    xh.load(a, row, col, count);
+    float w[8];
+    if (a.w) load_params(a.w, a.w_bf16, col, count, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] = a.w ? dy.get(e) * w[e] : dy.get(e);
+      h[e] = xh.get(e, stat);
+    }
+  };
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
+    float g[8], h[8];
+    values(col, g, h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c0 += static_cast<double>(g[e]);
+      c1 = __builtin_fma(static_cast<double>(g[e]), static_cast<double>(h[e]), c1);
+    }
+  }
+  const float m = static_cast<float>(row_sum<256, 256>(c0, lds) * a.inv_cols);
+  const float k = static_cast<float>(row_sum<256, 256>(c1, lds) * a.inv_cols);
+  S* out = static_cast<S*>(a.dx) + row * static_cast<int64_t>(a.cols);
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
+    float g[8], h[8], x[8];
+    values(col, g, h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (g[e] - m - h[e] * k) * stat.rstd;
+    store8(out + col, a.cols - col, x);
+  }
+}
+
+// And their sums over rows: a workgroup takes 2048 columns of a share of the rows.
+template <typename S, bool SAVED>
+__global__ __launch_bounds__(256) void norm_columns_long(Norm a, int64_t share, int32_t strips) {
+  const int32_t strip = blockIdx.x % strips, part = blockIdx.x / strips;
+  const int64_t col = (static_cast<int64_t>(strip) * 256 + threadIdx.x) * 8, count = a.cols - col;
+  if (count <= 0) return;
+  const int64_t r0 = part * share, r1 = min(a.rows, r0 + share);
+  float dw[8] = {}, db[8] = {};
+  for (int64_t row = r0; row < r1; ++row) {
+    const RowStat stat = a.stat[row];
+    Run<S> dy;
+    Normalised<S, SAVED> xh;
+    dy.load(static_cast<const S*>(a.dy) + row * a.ld_dy + col, count);
+    xh.load(a, row, col, count);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dw[e] = __builtin_fmaf(dy.get(e), xh.get(e, stat), dw[e]);
+      db[e] += dy.get(e);
+    }
+  }
+  float* out = a.part + static_cast<int64_t>(part) * 2 * a.cols + col;
+  store8(out, count, dw);
+  store8(out + a.cols, count, db);
+}
+
+// dw and db from the workgroups' sums: 64 columns a workgroup, 4 a lane, 16
+// shares of the workgroups side by side, joined in LDS in their order.
+__global__ __launch_bounds__(256) void norm_params(Norm a, int32_t parts) {
+  __shared__ asr::f32x4 lds[256];
+  const int which = blockIdx.y, share = threadIdx.x / 16;
+  void* result = which ? a.db : a.dw;
+  if (!result) return;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x % 16 * 4;
+  asr::f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int32_t each = (parts + 15) / 16, p1 = min(parts, (share + 1) * each);
+  const int left = static_cast<int>(min(int64_t{4}, a.cols - col));
+  if (left == 4) {
+#pragma unroll 8
+    for (int32_t p = share * each; p < p1; ++p)
+      t += *reinterpret_cast<const f32x4_any*>(a.part + (static_cast<int64_t>(p) * 2 + which) * a.cols + col);
+  } else {
+    for (int32_t p = share * each; p < p1; ++p)
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < left) t[e] += a.part[(static_cast<int64_t>(p) * 2 + which) * a.cols + col + e];
+  }
+  lds[threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.x < 16) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t += lds[i * 16 + threadIdx.x];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) store_param(result, a.w_bf16, col + e, t[e]);
+  }
+}
+
+}  // namespace asr_layers
+
+// =========================================================== host side
+namespace {
+
+using asr_host::fail;
+using asr_host::hip_fail;
+using asr_host::ok;
+using namespace asr_layers;
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int64_t kMaxDim = int64_t{1} << 31;
+constexpr int64_t kMaxItems = int64_t{1} << 31;
+constexpr int64_t kMaxGrid = int64_t{1} << 22;   // workgroups of the kernels that loop over items
+constexpr int64_t kMaxBlocks = 0xFFFFFF;         // of 256 threads in a launch of fewer than 2**32
+
+template <typename... A>
+hipError_t launch(void (*f)(A...), dim3 grid, int threads, hipStream_t s, std::common_type_t<A>... args) {
+  void* argv[] = {&args...};
+  return hipLaunchKernel(reinterpret_cast<const void*>(f), grid, dim3(threads), argv, 0, s);
+}
+
+int64_t blocks_of(int64_t cols) { return (cols + kBlockCols - 1) / kBlockCols; }
+
+// false: more work than one call takes
+bool make_grid(Grid& g, int64_t rows, int64_t cols) {
+  g.rows = rows;
+  g.cols = static_cast<int32_t>(cols);
+  g.blocks = static_cast<int32_t>(blocks_of(cols));
+  g.side = 0;
+  while (g.side < 4 && (1 << g.side) < g.blocks) ++g.side;
+  g.chunks = (g.blocks + (1 << g.side) - 1) >> g.side;
+  const int64_t up = (rows + (16 >> g.side) - 1) / (16 >> g.side);
+  if (up > kMaxItems / g.chunks - 1) return false;
+  g.items = static_cast<uint32_t>(up * g.chunks);
+  return true;
+}
+
+uint32_t grid_of(const Grid& g) { return static_cast<uint32_t>(std::min<int64_t>(g.items, kMaxGrid)); }
+
+int check_size(const char* what, int64_t rows, int64_t cols, int32_t dtype) {
+  if (rows < 0 || cols < 0 || rows >= kMaxDim || cols >= kMaxDim - 4096)
+    return fail(ASR_EINVAL, std::string(what) + ": rows must be in [0, 2**31), columns in [0, 2**31 - 4096)");
+  if (dtype != ASR_F32 && dtype != ASR_BF16) return fail(ASR_EDTYPE, std::string(what) + ": unknown dtype");
+  return ASR_OK;
+}
+
+// A matrix of the call with row stride ld (in elements).
+int check_matrix(const char* what, const void* p, int64_t ld, int64_t cols, int32_t dtype) {
+  if (!p) return fail(ASR_EINVAL, std::string(what) + ": null pointer");
+  if (ld < cols) return fail(ASR_EINVAL, std::string(what) + ": a row stride is below the row's length");
+  if (!aligned_to(p, dtype == ASR_F32 ? 4 : 2))
+    return fail(ASR_EALIGN, std::string(what) + ": a pointer is not aligned to its elements");
+  return ASR_OK;
+}
+
+int check_codes(const char* what, const int8_t* q, int64_t ldq, const float* s, int64_t cols) {
+  if (!q || !s) return fail(ASR_EINVAL, std::string(what) + ": null pointer");
+  if (ldq % 16 != 0 || ldq < (cols + 15) / 16 * 16)
+    return fail(ASR_EINVAL, std::string(what) + ": rows of codes must lie a multiple of 16 bytes apart that holds "
+                                                "the columns up to a multiple of 16");
+  if (!aligned_to(q, 16) || !aligned_to(s, 4))
+    return fail(ASR_EALIGN, std::string(what) + ": codes aligned to 16 bytes, scales to 4");
+  return ASR_OK;
+}
+
+int done(hipError_t e, const char* what) { return e == hipSuccess ? ok() : hip_fail(e, what); }
+
+// The largest number of workgroups whose sums the norm's backward pass joins.
+constexpr int64_t kNormGrid = 256;
+constexpr int64_t kMaxNorm = int64_t{1} << 24;   // columns of a row
+
+int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
+  if (int rc = check_size("layer_norm", rows, cols, dtype)) return rc;
+  if (param_dtype != ASR_F32 && param_dtype != ASR_BF16) return fail(ASR_EDTYPE, "layer_norm: unknown param_dtype");
+  if (cols > kMaxNorm) return fail(ASR_EINVAL, "layer_norm: at most 2**24 columns");
+  if (rows > kMaxBlocks) return fail(ASR_EINVAL, "layer_norm: rows must be below 2**24");
+  return ASR_OK;
+}
+
+template <typename S, bool SAVE>
+hipError_t norm_forward(const Norm& a, hipStream_t s) {
+  const auto one = [&](auto* f, int rows_each) {
+    return launch(f, dim3(static_cast<uint32_t>((a.rows + rows_each - 1) / rows_each)), 256, s, a);
+  };
+  if (a.cols <= 512) return one(&norm_rows<S, 64, 1, SAVE>, 4);
+  if (a.cols <= 1024) return one(&norm_rows<S, 64, 2, SAVE>, 4);
+  if (a.cols <= 2048) return one(&norm_rows<S, 64, 4, SAVE>, 4);
+  if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 1);
+  if (a.cols <= 8192) return one(&norm_rows<S, 256, 4, SAVE>, 1);
+  if (a.cols <= 16384) return one(&norm_rows<S, 256, 8, SAVE>, 1);
+  return one(&norm_long_rows<S, SAVE>, 1);
+}
+
+template <typename S, bool SAVED>
+hipError_t norm_back(Norm a, hipStream_t s) {
+  const bool sums = a.dw || a.db;
+  int64_t parts = 0;
+  hipError_t e = hipSuccess;
+  const auto one = [&](auto* f, int groups) {
+    parts = std::min<int64_t>((a.rows + groups - 1) / groups, kNormGrid);
+    a.alone = sums && parts == 1;
+    e = launch(f, dim3(static_cast<uint32_t>(parts)), 1024, s, a);
+  };
+  if (a.cols <= 512) one(&norm_backward<S, SAVED, 64>, 16);
+  else if (a.cols <= 1024) one(&norm_backward<S, SAVED, 128>, 8);
+  else if (a.cols <= 2048) one(&norm_backward<S, SAVED, 256>, 4);
+  else if (a.cols <= 4096) one(&norm_backward<S, SAVED, 512>, 2);
+  else if (a.cols <= 8192) one(&norm_backward<S, SAVED, 1024>, 1);
+  else {
+    if (a.dx) e = launch(&norm_backward_long<S, SAVED>, dim3(static_cast<uint32_t>(a.rows)), 256, s, a);
+    if (e == hipSuccess && sums) {
+      parts = std::min<int64_t>(a.rows, kNormGrid);
+      const int64_t share = (a.rows + parts - 1) / parts;
+      parts = (a.rows + share - 1) / share;
+      const int32_t strips = static_cast<int32_t>((static_cast<int64_t>(a.cols) + 2047) / 2048);
+      e = launch(&norm_columns_long<S, SAVED>, dim3(static_cast<uint32_t>(parts * strips)), 256, s, a, share, strips);
+    }
+  }
+  if (e == hipSuccess && sums && !a.alone)
+    e = launch(&norm_params, dim3(static_cast<uint32_t>((static_cast<int64_t>(a.cols) + 63) / 64), 2), 256, s, a,
+               static_cast<int32_t>(parts));
+  return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+int asr_pack_i8(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int64_t cols, int8_t* q, int64_t ldq,
+                float* scale, int32_t rounding, uint32_t seed, uint32_t step, uint64_t base_index, void* stream) {
+  if (int rc = check_size("pack_i8", rows, cols, dtype)) return rc;
+  if (rounding != ASR_ROUND_SR && rounding != ASR_ROUND_RN)
+    return fail(ASR_EINVAL, "pack_i8: rounding must be ASR_ROUND_SR or ASR_ROUND_RN");
+  if (rows == 0 || cols == 0) return ok();
+  if (int rc = check_matrix("pack_i8", x, ldx, cols, dtype)) return rc;
+  if (int rc = check_codes("pack_i8", q, ldq, scale, cols)) return rc;
+  if (static_cast<uint64_t>(rows) * static_cast<uint64_t>(cols) - 1 > ~base_index)
+    return fail(ASR_EINVAL, "pack_i8: base_index + rows*cols exceeds 2**64");
+  Pack a{};
+  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "pack_i8: the matrix is too large for one call");
+  a.x = const_cast<void*>(x);
+  a.ldx = ldx;
+  a.c = Codes{q, scale, ldq};
+  a.base = base_index;
+  a.seed = seed;
+  a.step = step;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool sr = rounding == ASR_ROUND_SR;
+  auto* f = dtype == ASR_F32 ? (sr ? &pack<float, true> : &pack<float, false>)
+                             : (sr ? &pack<uint16_t, true> : &pack<uint16_t, false>);
+  return done(launch(f, dim3(grid_of(a.g)), 256, s, a), "pack_i8 launch");
+}
+
+int asr_unpack_i8(const int8_t* q, int64_t ldq, const float* scale, int64_t rows, int64_t cols, void* x,
+                  int32_t dtype, int64_t ldx, void* stream) {
+  if (int rc = check_size("unpack_i8", rows, cols, dtype)) return rc;
+  if (rows == 0 || cols == 0) return ok();
+  if (int rc = check_codes("unpack_i8", q, ldq, scale, cols)) return rc;
+  if (int rc = check_matrix("unpack_i8", x, ldx, cols, dtype)) return rc;
+  Pack a{};
+  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "unpack_i8: the matrix is too large for one call");
+  a.x = x;
+  a.ldx = ldx;
+  a.c = Codes{const_cast<int8_t*>(q), const_cast<float*>(scale), ldq};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return done(launch(dtype == ASR_F32 ? &unpack<float> : &unpack<uint16_t>, dim3(grid_of(a.g)), 256, s, a),
+              "unpack_i8 launch");
+}
+
+int asr_silu_mul_forward(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype,
+                         int64_t rows, int64_t cols, void* y, int64_t ld_y, int8_t* q_gate, float* s_gate,
+                         int8_t* q_up, float* s_up, int64_t ldq, void* stream) {
+  if (int rc = check_size("silu_mul", rows, cols, dtype)) return rc;
+  if (rows == 0 || cols == 0) return ok();
+  if (int rc = check_matrix("silu_mul", gate, ld_gate, cols, dtype)) return rc;
+  if (int rc = check_matrix("silu_mul", up, ld_up, cols, dtype)) return rc;
+  if (int rc = check_matrix("silu_mul", y, ld_y, cols, dtype)) return rc;
+  const bool save = q_gate || s_gate || q_up || s_up;
+  if (save) {
+    if (int rc = check_codes("silu_mul", q_gate, ldq, s_gate, cols)) return rc;
+    if (int rc = check_codes("silu_mul", q_up, ldq, s_up, cols)) return rc;
+  }
+  Silu a{};
+  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "silu_mul: the matrix is too large for one call");
+  a.gate = gate;
+  a.up = up;
+  a.y = y;
+  a.ld_gate = ld_gate;
+  a.ld_up = ld_up;
+  a.ld_y = ld_y;
+  a.cg = Codes{q_gate, s_gate, ldq};
+  a.cu = Codes{q_up, s_up, ldq};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  auto* f = dtype == ASR_F32 ? (save ? &silu_forward<float, true> : &silu_forward<float, false>)
+                             : (save ? &silu_forward<uint16_t, true> : &silu_forward<uint16_t, false>);
+  return done(launch(f, dim3(grid_of(a.g)), 256, s, a), "silu_mul launch");
+}
+
+int asr_silu_mul_backward(const void* dy, int64_t ld_dy, const void* gate, int64_t ld_gate, const void* up,
+                          int64_t ld_up, const int8_t* q_gate, const float* s_gate, const int8_t* q_up,
+                          const float* s_up, int64_t ldq, int32_t dtype, int64_t rows, int64_t cols, void* dgate,
+                          int64_t ld_dgate, void* dup, int64_t ld_dup, void* stream) {
+  if (int rc = check_size("silu_mul", rows, cols, dtype)) return rc;
+  if (rows == 0 || cols == 0) return ok();
+  if (int rc = check_matrix("silu_mul", dy, ld_dy, cols, dtype)) return rc;
+  if (int rc = check_matrix("silu_mul", dgate, ld_dgate, cols, dtype)) return rc;
+  if (int rc = check_matrix("silu_mul", dup, ld_dup, cols, dtype)) return rc;
+  const bool saved = q_gate || s_gate || q_up || s_up;
+  if (saved) {
+    if (gate || up) return fail(ASR_EINVAL, "silu_mul: gate and up, or their codes, not both");
+    if (int rc = check_codes("silu_mul", q_gate, ldq, s_gate, cols)) return rc;
+    if (int rc = check_codes("silu_mul", q_up, ldq, s_up, cols)) return rc;
+  } else {
+    if (int rc = check_matrix("silu_mul", gate, ld_gate, cols, dtype)) return rc;
+    if (int rc = check_matrix("silu_mul", up, ld_up, cols, dtype)) return rc;
+  }
+  Silu a{};
+  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "silu_mul: the matrix is too large for one call");
+  a.gate = gate;
+  a.up = up;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.dup = dup;
+  a.ld_gate = ld_gate;
+  a.ld_up = ld_up;
+  a.ld_dy = ld_dy;
+  a.ld_dgate = ld_dgate;
+  a.ld_dup = ld_dup;
+  a.cg = Codes{const_cast<int8_t*>(q_gate), const_cast<float*>(s_gate), ldq};
+  a.cu = Codes{const_cast<int8_t*>(q_up), const_cast<float*>(s_up), ldq};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  auto* f = dtype == ASR_F32 ? (saved ? &silu_backward<float, true> : &silu_backward<float, false>)
+                             : (saved ? &silu_backward<uint16_t, true> : &silu_backward<uint16_t, false>);
+  return done(launch(f, dim3(grid_of(a.g)), 256, s, a), "silu_mul launch");
+}
+
+int asr_layer_norm_forward(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int64_t cols,
+                           const void* weight, const void* bias, int32_t param_dtype, double eps, void* y,
+                           float* stat, int8_t* q, int64_t ldq, float* scale, void* stream) {
+  if (int rc = check_norm(rows, cols, dtype, param_dtype)) return rc;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(ASR_EINVAL, "layer_norm: eps must be finite and >= 0");
+  if (rows == 0 || cols == 0) return ok();
+  if (int rc = check_matrix("layer_norm", x, ldx, cols, dtype)) return rc;
+  if (int rc = check_matrix("layer_norm", y, cols, cols, dtype)) return rc;
+  if (!aligned_to(weight, param_dtype == ASR_F32 ? 4 : 2) || !aligned_to(bias, param_dtype == ASR_F32 ? 4 : 2))
+    return fail(ASR_EALIGN, "layer_norm: weight and bias aligned to their elements");
+  if (!aligned_to(stat, 16)) return fail(ASR_EALIGN, "layer_norm: stat aligned to 16 bytes");
+  if (q || scale)
+    if (int rc = check_codes("layer_norm", q, ldq, scale, cols)) return rc;
+  Norm a{};
+  a.x = x;
+  a.w = weight;
+  a.b = bias;
+  a.y = y;
+  a.stat = reinterpret_cast<RowStat*>(stat);
+  a.c = Codes{q, scale, ldq};
+  a.rows = rows;
+  a.ldx = ldx;
+  a.cols = static_cast<int32_t>(cols);
+  a.blocks = static_cast<int32_t>(blocks_of(cols));
+  a.eps = eps;
+  a.inv_cols = 1.0 / static_cast<double>(cols);
+  a.w_bf16 = param_dtype == ASR_BF16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = dtype == ASR_F32 ? (q ? norm_forward<float, true>(a, s) : norm_forward<float, false>(a, s))
+                                        : (q ? norm_forward<uint16_t, true>(a, s) : norm_forward<uint16_t, false>(a, s));
+  return done(e, "layer_norm launch");
+}
+
+size_t asr_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || rows > kMaxBlocks || cols > kMaxNorm) return 0;
+  return static_cast<size_t>(std::min<int64_t>(rows, kNormGrid) * 2 * cols * 4);
+}
+
+int asr_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const int8_t* q, int64_t ldq,
+                            const float* scale, const float* stat, int32_t dtype, int64_t rows, int64_t cols,
+                            const void* weight, int32_t param_dtype, void* dx, void* dweight, void* dbias,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_norm(rows, cols, dtype, param_dtype)) return rc;
+  if (cols == 0 || (!dx && !dweight && !dbias)) return ok();
+  const uintptr_t wide = param_dtype == ASR_F32 ? 4 : 2;
+  if (!aligned_to(weight, wide) || !aligned_to(dweight, wide) || !aligned_to(dbias, wide))
+    return fail(ASR_EALIGN, "layer_norm: weight, dweight and dbias aligned to their elements");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Norm a{};
+  a.cols = static_cast<int32_t>(cols);
+  a.dw = dweight;
+  a.db = dbias;
+  a.w_bf16 = param_dtype == ASR_BF16;
+  if (rows == 0) {  // empty sums
+    if (!dweight && !dbias) return ok();
+    return done(launch(&norm_params, dim3(static_cast<uint32_t>((cols + 63) / 64), 2), 256, s, a, 0), "layer_norm launch");
+  }
+  if (int rc = check_matrix("layer_norm", dy, ld_dy, cols, dtype)) return rc;
+  if (dx)
+    if (int rc = check_matrix("layer_norm", dx, cols, cols, dtype)) return rc;
+  if (q || scale) {
+    if (x) return fail(ASR_EINVAL, "layer_norm: x or its codes, not both");
+    if (int rc = check_codes("layer_norm", q, ldq, scale, cols)) return rc;
+  } else if (int rc = check_matrix("layer_norm", x, ldx, cols, dtype)) {
+    return rc;
+  }
+  if (!stat) return fail(ASR_EINVAL, "layer_norm: null pointer");
+  if (!aligned_to(stat, 16)) return fail(ASR_EALIGN, "layer_norm: stat aligned to 16 bytes");
+  if ((dweight || dbias) && (!workspace || !aligned_to(workspace, 16) ||
+                             workspace_bytes < asr_layer_norm_backward_workspace_bytes(rows, cols)))
+    return fail(ASR_EWORKSPACE, "layer_norm: workspace NULL, too small or not 16-byte aligned");
+  a.x = x;
+  a.w = weight;
+  a.dy = dy;
+  a.dx = dx;
+  a.stat = reinterpret_cast<RowStat*>(const_cast<float*>(stat));
+  a.part = static_cast<float*>(workspace);
+  a.c = Codes{const_cast<int8_t*>(q), const_cast<float*>(scale), ldq};
+  a.rows = rows;
+  a.ldx = ldx;
+  a.ld_dy = ld_dy;
+  a.blocks = static_cast<int32_t>(blocks_of(cols));
+  a.inv_cols = 1.0 / static_cast<double>(cols);
+  a.inv_cols32 = static_cast<float>(a.inv_cols);
+  const hipError_t e = dtype == ASR_F32 ? (q ? norm_back<float, true>(a, s) : norm_back<float, false>(a, s))
+                                        : (q ? norm_back<uint16_t, true>(a, s) : norm_back<uint16_t, false>(a, s));
+  return done(e, "layer_norm launch");
+}
+
+}  // extern "C"

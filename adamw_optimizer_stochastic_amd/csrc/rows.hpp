@@ -1,0 +1,133 @@
+// Pieces of the kernels that walk rows of a matrix: 8 columns a lane, loads and
+// stores of 16 bytes from any element's address, and reductions over lanes.
+#pragma once
+
+#include "codes.hpp"
+
+#pragma clang fp contract(off)
+
+namespace asr_rows {
+
+// Element-aligned vectors: global accesses of 16 bytes need no more than that,
+// so rows of any width and views from any element keep the wide form.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// 8 columns of a row as they lie in memory. count: how many of them there are
+// (8 or more: all; the others read as 0).
+template <typename S>
+struct Run;
+template <>
+struct Run<uint16_t> {
+  asr::u32x4 w;
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t count) {
+    if (count >= 8) {
+      w = *reinterpret_cast<const u32x4_any*>(p);
+    } else {
+      w = asr::u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < count) w[e / 2] |= static_cast<uint32_t>(p[e]) << (e % 2 * 16);
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    return __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+  }
+};
+template <>
+struct Run<float> {
+  asr::f32x4 w[2];
+  __device__ __forceinline__ void load(const float* p, int64_t count) {
+    if (count >= 8) {
+      w[0] = reinterpret_cast<const f32x4_any*>(p)[0];
+      w[1] = reinterpret_cast<const f32x4_any*>(p)[1];
+    } else {
+      w[0] = w[1] = asr::f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < count) w[e / 4][e % 4] = p[e];
+    }
+  }
+  __device__ __forceinline__ float get(int e) const { return w[e / 4][e % 4]; }
+};
+
+// Two f32 to two bf16 (low half first), to nearest, ties to even.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, asr::bf16x2));
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int64_t count, const float (&x)[8]) {
+  const asr::u32x4 w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
+  if (count >= 8) {
+    *reinterpret_cast<u32x4_any*>(p) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < count) p[e] = static_cast<uint16_t>(w[e / 2] >> (e % 2 * 16));
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, int64_t count, const float (&x)[8]) {
+  if (count >= 8) {
+    reinterpret_cast<f32x4_any*>(p)[0] = f32x4_any{x[0], x[1], x[2], x[3]};
+    reinterpret_cast<f32x4_any*>(p)[1] = f32x4_any{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < count) p[e] = x[e];
+  }
+}
+
+// 8 parameters (a norm's weight or bias) of either type.
+__device__ __forceinline__ void load_params(const void* p, bool bf16, int64_t col, int64_t count, float (&x)[8]) {
+  if (bf16) {
+    Run<uint16_t> r;
+    r.load(static_cast<const uint16_t*>(p) + col, count);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = r.get(e);
+  } else {
+    Run<float> r;
+    r.load(static_cast<const float*>(p) + col, count);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = r.get(e);
+  }
+}
+
+// A value from the lane N places round the 16 lanes of a row (every lane of
+// the wave active).
+template <int N>
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xF, 0xF, true));
+}
+template <int N>
+__device__ __forceinline__ float turned(float v) {
+  return __uint_as_float(turned<N>(__float_as_uint(v)));
+}
+template <int N>
+__device__ __forceinline__ double turned(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(turned<N>(static_cast<uint32_t>(u))) |
+                                        static_cast<uint64_t>(turned<N>(static_cast<uint32_t>(u >> 32))) << 32);
+}
+
+// Over 16 lanes, the result in each of them (the same bits: every step adds
+// the two halves of one set).
+template <typename V, typename F>
+__device__ __forceinline__ V reduce16(V v, F f) {
+  v = f(v, turned<8>(v));
+  v = f(v, turned<4>(v));
+  v = f(v, turned<2>(v));
+  return f(v, turned<1>(v));
+}
+
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
+  v = reduce16(v, [](V a, V b) { return a + b; });
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+}  // namespace asr_rows

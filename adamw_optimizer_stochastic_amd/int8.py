@@ -13,6 +13,14 @@ x and w are rounded to nearest. dy is rounded stochastically (by default):
 its codes are then unbiased, so the quantisation of dy adds no bias to dx or
 dw. Element (t, n) of dy uses stream position base_index + t*N + n under key
 (seed, step), in both products.
+
+With saved="i8" the layer keeps x's codes of the first product, one byte an
+element, instead of x. The third product takes them as they are: x is about s[t]
+X[t, k], so the token's scale goes into dy before dy's column codes are taken,
+
+    dw = (s dy)^T X   scales for each output of s dy, X's codes turned round
+
+and x is rounded once, not a second time along its columns.
 """
 
 import torch
@@ -61,7 +69,49 @@ class _LinearI8(torch.autograd.Function):
         return dx, dw, None, None
 
 
-def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
+class _LinearI8Saved(torch.autograd.Function):
+    """The same, keeping x's codes instead of x."""
+
+    @staticmethod
+    def forward(ctx, x, w, grad_rounding, key):
+        (t, k), n, device = x.shape, w.shape[0], x.device
+        y = torch.empty((t, n), dtype=torch.bfloat16, device=device)
+        q = torch.empty((t, max(ops._padded16(k), 16)), dtype=torch.int8, device=device)
+        scale = torch.empty(t, dtype=torch.float32, device=device)
+        ctx.save_for_backward(q, scale, w)
+        ctx.grad_rounding, ctx.key = grad_rounding, key
+        need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 0)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        with ops._on(device):
+            _abi.asr_linear_i8_forward_saved(
+                x.data_ptr(), ops._row_stride(x, k), w.data_ptr(), ops._row_stride(w, k),
+                y.data_ptr(), n, q.data_ptr(), q.shape[1], scale.data_ptr(), t, n, k,
+                ws.data_ptr(), need, ops._stream(device))
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        q, scale, w = ctx.saved_tensors
+        (t, n), k, device = dy.shape, w.shape[1], dy.device
+        if dy.stride(1) != 1 or dy.stride(0) < n:
+            dy = dy.contiguous()   # an expanded or transposed gradient
+        want_x, want_w = ctx.needs_input_grad[:2]
+        dx = torch.empty((t, k), dtype=torch.bfloat16, device=device) if want_x else None
+        dw = torch.empty((n, k), dtype=torch.bfloat16, device=device) if want_w else None
+        need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 1)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        with ops._on(device):
+            _abi.asr_linear_i8_backward_saved(
+                q.data_ptr(), q.shape[1], scale.data_ptr(), w.data_ptr(), ops._row_stride(w, k),
+                dy.data_ptr(), ops._row_stride(dy, n), dx.data_ptr() if want_x else None, k,
+                dw.data_ptr() if want_w else None, k, t, n, k,
+                ops.ROUNDING_CODE[ctx.grad_rounding], *ctx.key, ws.data_ptr(), need,
+                ops._stream(device))
+        return dx, dw, None, None
+
+
+def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr", saved="input"):
     """y = x w^T in 8-bit integer products, forward and backward.
 
     x: bfloat16 (..., K); w: bfloat16 (N, K); y: bfloat16 (..., N). The
@@ -69,6 +119,9 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
     step), positions from base_index) or "rn", for the gradient's codes; give
     every layer its own base_index (or seed) and every step its own step.
     K, N and the number of tokens are below 2**17 (each is summed over once).
+    saved: "input" keeps x for w's gradient, "i8" the codes of the forward
+    product (half the bytes; y and dx are the same, and a token with an Inf or
+    NaN in x makes all of w's gradient NaN).
 
     Forward and backward can be captured into a graph together; as with any
     operator under torch's autograd, no eager graph of the same leaves may be
@@ -76,6 +129,8 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
     """
     if grad_rounding not in ops.ROUNDING_CODE:
         raise ValueError("grad_rounding must be 'sr' or 'rn'")
+    if saved not in ("input", "i8"):
+        raise ValueError("saved must be 'input' or 'i8'")
     key = (ops._u32("seed", seed), ops._u32("step", step), ops._u64("base_index", base_index))
     for t, name in ((x, "x"), (w, "w")):
         if not isinstance(t, torch.Tensor):
@@ -100,5 +155,6 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr"):
         w = w.contiguous()
     if key[2] + tokens * n > 1 << 64:
         raise ValueError("base_index + tokens*N exceeds 2**64")
-    y = _LinearI8.apply(flat, w, grad_rounding, key)
+    layer = _LinearI8Saved if saved == "i8" and n > 0 and k > 0 else _LinearI8
+    y = layer.apply(flat, w, grad_rounding, key)
     return y.reshape(*x.shape[:-1], n)

@@ -470,6 +470,64 @@ def gemm_i8(a, b, scale_a, scale_b, *, rounding="rn", seed=0, step=0, base_index
     return out
 
 
+PACK_COLUMNS = 128   # columns of a row that share a scale in pack_i8
+
+
+def _code_buffers(rows, cols, device):
+    """Buffers for pack_i8's codes (rows padded to 16 bytes) and scales."""
+    return (torch.empty((rows, max(_padded16(cols), 16)), dtype=torch.int8, device=device),
+            torch.empty((rows, (cols + PACK_COLUMNS - 1) // PACK_COLUMNS), dtype=torch.float32,
+                        device=device))
+
+
+def pack_i8(x, *, rounding="rn", seed=0, step=0, base_index=0):
+    """8-bit codes of a float32 or bfloat16 matrix to keep it by: (q, scale).
+
+    One scale for every 128 columns of a row (the last block has the rest), so
+    x is about ``q * scale`` with scale repeated over its columns, within half
+    a step (1/254 of the block's largest magnitude). Codes, rounding, random
+    bits and the treatment of zeros, Inf and NaN as in ``quantize_i8``, a block in a
+    row's place. q is a (R, C) view of rows padded to 16 bytes, scale (R,
+    ceil(C / 128)); ``unpack_i8`` takes them as they are.
+    """
+    if rounding not in ROUNDING_CODE:
+        raise ValueError("rounding must be 'rn' or 'sr'")
+    key = _key(seed, step, base_index)
+    _require_matrix(x, "x", (torch.float32, torch.bfloat16))
+    rows, cols = x.shape
+    device = x.device
+    store, scale = _code_buffers(rows, cols, device)
+    with _on(device):
+        _abi.asr_pack_i8(x.data_ptr(), _DTYPE_CODE[x.dtype], _row_stride(x, cols), rows, cols,
+                         store.data_ptr(), store.shape[1], scale.data_ptr(),
+                         ROUNDING_CODE[rounding], *key, _stream(device))
+    return (store if store.shape[1] == cols else store[:, :cols]), scale
+
+
+def unpack_i8(q, scale, *, dtype=torch.bfloat16):
+    """The float32 or bfloat16 matrix that ``pack_i8``'s codes stand for: q *
+    scale in float32, rounded to nearest. q: int8 (R, C), rows a multiple of 16
+    bytes apart with room for C up to one, on a 16-byte address."""
+    if dtype not in _DTYPE_CODE:
+        raise TypeError("dtype must be float32 or bfloat16")
+    _require_matrix(q, "q", (torch.int8,))
+    rows, cols = q.shape
+    device = q.device
+    _require_gpu(scale, "scale")
+    if scale.dtype != torch.float32 or scale.device != device or \
+            tuple(scale.shape) != (rows, (cols + PACK_COLUMNS - 1) // PACK_COLUMNS):
+        raise ValueError("scale must be float32 (R, ceil(C / 128)) on q's device")
+    ldq = _row_stride(q, max(_padded16(cols), 16))
+    if q.numel() and q.storage_offset() + (rows - 1) * ldq + _padded16(cols) > \
+            q.untyped_storage().nbytes():
+        raise ValueError("q's last row must have room up to a multiple of 16 bytes")
+    x = torch.empty((rows, cols), dtype=dtype, device=device)
+    with _on(device):
+        _abi.asr_unpack_i8(q.data_ptr(), ldq, scale.data_ptr(), rows, cols, x.data_ptr(),
+                           _DTYPE_CODE[dtype], max(cols, 1), _stream(device))
+    return x
+
+
 NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 MUON_MAX_SIDE = 1 << 20
 

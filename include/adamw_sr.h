@@ -363,6 +363,156 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
                            size_t workspace_bytes, void* stream);
 
 /*
+ * The same layer with x kept in 8 bits between the two calls. The forward
+ * call also writes x's row codes and scales, those of its product
+ * (asr_quantize_i8 of x's rows, to nearest): q (tokens rows ldq bytes apart) and
+ * scale (tokens). The backward call takes them in x's place. With X the codes and s the scales,
+ *   dw[n][k] = sum_t dy[t][n] s[t] X[t][k]:
+ * the token's scale goes into the gradient, z = f32(dy[t][n] * s[t]), and
+ * dw = asr_gemm_i8 of the codes of z's columns (by `rounding`, with dy's own
+ * positions) and X turned round, with the scales of z and 1. x is rounded
+ * once, in the forward product; dx is the same as above. A token with an Inf
+ * or NaN in x makes all of dw NaN.
+ * Requirements: as above; ldq a multiple of 16, at least k up to a multiple of
+ * 16 and below 2**23; q 16-byte aligned, scale 4-byte aligned; n > 0 in the
+ * forward call. The workspaces are those of the calls above.
+ */
+int asr_linear_i8_forward_saved(const uint16_t* x, int64_t ldx,
+                                const uint16_t* w, int64_t ldw, uint16_t* y,
+                                int64_t ldy, int8_t* q, int64_t ldq,
+                                float* scale, int64_t tokens, int64_t n,
+                                int64_t k, void* workspace,
+                                size_t workspace_bytes, void* stream);
+int asr_linear_i8_backward_saved(const int8_t* q, int64_t ldq,
+                                 const float* scale, const uint16_t* w,
+                                 int64_t ldw, const uint16_t* dy, int64_t lddy,
+                                 uint16_t* dx, int64_t lddx, uint16_t* dw,
+                                 int64_t lddw, int64_t tokens, int64_t n,
+                                 int64_t k, int32_t rounding, uint32_t seed,
+                                 uint32_t step, uint64_t base_index,
+                                 void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Activations in 8 bits, with one scale for every 128 consecutive columns of a
+ * row (the last block of a row has the rest). Codes and scale of a block are
+ * those asr_quantize_i8 gives a row of the block's elements (x's element (i, j)
+ * at stream position base_index + i*cols + j); what they stand for is f32(q *
+ * scale), which asr_unpack_i8 writes, to nearest if x is bf16. x: rows x cols of
+ * dtype, row i at x + i*ldx; q: row i at q + i*ldq, followed by zeros up to the
+ * next multiple of 16; scale: rows x ceil(cols / 128) f32, contiguous.
+ * Requirements: 0 <= rows < 2**31, 0 <= cols < 2**31 - 4096; ldx >= cols; ldq a
+ * multiple of 16 that holds the columns up to a multiple of 16; q 16-byte
+ * aligned, x and scale aligned to their elements; fewer than 2**31 times 2048
+ * elements' room; base_index + rows*cols <= 2**64; no buffer overlaps another.
+ * Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EHIP. Run on `stream`; do not
+ * synchronize.
+ */
+int asr_pack_i8(const void* x, int32_t dtype, int64_t ldx, int64_t rows,
+                int64_t cols, int8_t* q, int64_t ldq, float* scale,
+                int32_t rounding, uint32_t seed, uint32_t step,
+                uint64_t base_index, void* stream);
+int asr_unpack_i8(const int8_t* q, int64_t ldq, const float* scale,
+                  int64_t rows, int64_t cols, void* x, int32_t dtype,
+                  int64_t ldx, void* stream);
+
+/*
+ * Layer norm of rows of `cols` elements:
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   xh = (x - mean) * rstd,  y = xh * weight + bias,
+ * and its gradients, with g = dy * weight:
+ *   dx = rstd * (g - sum g / cols - xh * sum (g xh) / cols),
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy.
+ * mean and rstd are formed in 64 bits, the rest in 32; the sums over rows take an order
+ * that depends on the sizes only. weight, bias: cols elements of param_dtype,
+ * NULL: 1 and 0. stat: NULL, or rows x 4 f32 that the backward call takes.
+ * q, scale: NULL, or they receive asr_pack_i8's codes (to nearest) of xh,
+ * computed in 64 bits; the backward call then takes them, with x NULL, and uses what
+ * they stand for. dx, dweight, dbias: NULL where not wanted; dweight and dbias
+ * of param_dtype, not accumulated into.
+ * y and dx have contiguous rows and x's dtype, as dy. An Inf or NaN in a row makes
+ * its y and dx NaN.
+ * Requirements: 0 <= rows < 2**24, 0 <= cols <= 2**24; row strides at least
+ * cols; ldq, q and scale as for asr_pack_i8; eps >= 0, finite; stat 16-byte
+ * aligned, the rest aligned to its elements; no output overlaps an input, but
+ * y may be x (with its row stride cols) unless x is kept for the backward call.
+ * workspace (with dweight or dbias):
+ * asr_layer_norm_backward_workspace_bytes(rows, cols) bytes of device memory,
+ * 16-byte aligned. Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE,
+ * ASR_EHIP. Run on `stream`; do not synchronize.
+ */
+int asr_layer_norm_forward(const void* x, int32_t dtype, int64_t ldx,
+                           int64_t rows, int64_t cols, const void* weight,
+                           const void* bias, int32_t param_dtype, double eps,
+                           void* y, float* stat, int8_t* q, int64_t ldq,
+                           float* scale, void* stream);
+size_t asr_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+int asr_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x,
+                            int64_t ldx, const int8_t* q, int64_t ldq,
+                            const float* scale, const float* stat,
+                            int32_t dtype, int64_t rows, int64_t cols,
+                            const void* weight, int32_t param_dtype, void* dx,
+                            void* dweight, void* dbias, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * The gated activation of an MLP, sig(g) = 1 / (1 + exp(-g)):
+ *   y = g sig(g) u,   dup = dy g sig(g),
+ *   dgate = dy u sig(g) (1 + g (1 - sig(g))).
+ * All matrices rows x cols of dtype with row strides of their own, so that
+ * gate and up may be the halves of one matrix, as may their gradients. q_gate,
+ * s_gate, q_up, s_up: NULL, or they receive asr_pack_i8's codes (to nearest) of
+ * gate and up, both with row stride ldq; the backward call takes either gate and
+ * up or these, and then uses what they stand for.
+ * Requirements: sizes, codes and alignment as for asr_pack_i8; row strides at least
+ * cols; no output overlaps an input, but in the forward call y may be gate or
+ * up, and in the backward call dgate may be dy, gate or up, and dup another of them (with the same
+ * stride). Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EHIP. Run on
+ * `stream`; do not synchronize.
+ */
+int asr_silu_mul_forward(const void* gate, int64_t ld_gate, const void* up,
+                         int64_t ld_up, int32_t dtype, int64_t rows,
+                         int64_t cols, void* y, int64_t ld_y, int8_t* q_gate,
+                         float* s_gate, int8_t* q_up, float* s_up, int64_t ldq,
+                         void* stream);
+int asr_silu_mul_backward(const void* dy, int64_t ld_dy, const void* gate,
+                          int64_t ld_gate, const void* up, int64_t ld_up,
+                          const int8_t* q_gate, const float* s_gate,
+                          const int8_t* q_up, const float* s_up, int64_t ldq,
+                          int32_t dtype, int64_t rows, int64_t cols,
+                          void* dgate, int64_t ld_dgate, void* dup,
+                          int64_t ld_dup, void* stream);
+
+/*
+ * Embedding: y[t] = f32(table[ids[t]]) * f32(scale), rounded to nearest, and
+ * the table's gradient dtable[v] = (sum of dy[t], ids[t] = v) * f32(scale),
+ * summed in f32 in an order that ids fixes (equal calls give equal bits) and
+ * rounded once; rows of ids without a token are 0, and dtable is written whole.
+ * ids: n ids on the device, 64-bit (ids_64 = 1) or 32-bit integers. An id outside
+ * [0, vocab) gives a row of NaN and no gradient; padding_idx (-1: none) an
+ * ordinary row and no gradient. table: vocab rows, ld elements apart; y and
+ * dtable contiguous; dy's rows ld_dy elements apart; all of dtype.
+ * Requirements: 0 <= n, vocab < 2**31; 0 <= dim <= 2**24; a table of at most 2**39 bytes;
+ * row strides at least dim; pointers aligned to their elements; scale finite
+ * in binary32; no output overlaps an input. workspace:
+ * asr_embedding_backward_workspace_bytes(n, vocab, dim) bytes of device
+ * memory, 256-byte aligned (0 bytes, NULL allowed, for n = 0). Errors:
+ * ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Run on
+ * `stream`; do not synchronize.
+ */
+int asr_embedding_forward(const void* ids, int32_t ids_64, int64_t n,
+                          const void* table, int32_t dtype, int64_t ld,
+                          int64_t vocab, int64_t dim, double scale, void* y,
+                          void* stream);
+size_t asr_embedding_backward_workspace_bytes(int64_t n, int64_t vocab,
+                                              int64_t dim);
+int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n,
+                           const void* dy, int64_t ld_dy, int32_t dtype,
+                           int64_t vocab, int64_t dim, double scale,
+                           int64_t padding_idx, void* dtable, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
  * Orthogonalisation of n matrices of one shape by Newton-Schulz products:
  *
  *   X = G / (|G|_F + eps), its short side first;
@@ -555,7 +705,7 @@ const char* asr_last_error(void);
 /* ABI version of this header and library (major * 100 + minor). */
 int asr_abi_version(void);
 
-#define ASR_ABI_VERSION 108
+#define ASR_ABI_VERSION 109
 
 #ifdef __cplusplus
 }

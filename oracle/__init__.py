@@ -56,4 +56,4 @@ from .gemm import (  # noqa: F401,E402
     gemm_exact, gemm_exact_scalar, gemm_dot, abs_products, f32_sum_bound,
     gemm_round, gemm_round_at,
 )
-from . import rng, int8, muon  # noqa: F401,E402
+from . import rng, int8, muon, layers  # noqa: F401,E402
