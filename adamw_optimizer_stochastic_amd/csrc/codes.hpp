@@ -28,13 +28,16 @@ struct __align__(16) GroupScale {
 // group is stored as zeros. Inf or NaN anywhere makes the scale NaN, which
 // every product with the group then shows.
 __device__ __forceinline__ float group_scale(uint32_t max_bits, GroupScale& g) {
-  const float s = __uint_as_float(max_bits) / 127.0f;
+  // (top / 127 rounded to nearest, without a division: an estimate by the rounded
+  // 1/127 and one correction, equal for every 24-bit top)
+  const float top = __uint_as_float(max_bits), guess = top * (1.0f / 127.0f);
+  const float s = __builtin_fmaf(__builtin_fmaf(-127.0f, guess, top), 1.0f / 127.0f, guess);
   const bool finite = max_bits < 0x7F800000u;
   const bool live = finite && s >= 0x1p-126f;
   g.live = live ? 0xFFFFFFFFu : 0u;
   g.k = s < 0x1p-60f ? 0x1p64f : 1.0f;
   g.s = live ? s * g.k : 1.0f;
-  g.inv = 1.0f / g.s;
+  g.inv = __builtin_amdgcn_rcpf(g.s);   // off by 2**-23 of itself at most
   return finite ? (live ? s : 0.0f) : __uint_as_float(0x7FC00000u);
 }
 
@@ -59,7 +62,7 @@ __device__ __forceinline__ int32_t exact_code(float x, const GroupScale& g, uint
 
 // Codes of 4 elements of one group, packed. With the exact decision for every
 // element its arithmetic is what bounds the kernels, so the usual case is short: |x| * (1/s) is off by less than
-// 2**-16 here, so a value further than that from a border has its code from
+// 2**-15 here, so a value further than that from a border has its code from
 // one multiply-add (to nearest: onto 1.5 * 2**23, whose low byte is then the
 // code; stochastic: floor of the quotient plus 1 + r16/65536). A wave that
 // has an element nearer (1e-4) than that decides these exactly: 40 instructions an

@@ -3,13 +3,13 @@
 // a row of no token 0. Sums in f32, one rounding at the end; the order of the
 // additions is fixed by ids alone, so equal calls give equal bits.
 //
-// The gradient in three steps. (1) Tokens sorted by id, stable: 8 bits (or
-// fewer) of the id a pass, up to 8192 tokens in one workgroup's LDS. Ids outside
-// the table and the padding id get the key `vocab` and end up last. (2) One launch
-// whose first workgroups sum the sorted rows, `chunk` positions each, and whose
-// others write the rows of no token; a run of one id inside a chunk is
-// finished there, one that crosses a chunk's border leaves an f32 partial sum.
-// (3) These are joined in order. Every row of dw is written once.
+// The gradient's steps. (1) Tokens are sorted by id, stable: 8 bits (or fewer) of the
+// id a pass. Ids outside the table and the padding id get the key `vocab` and end up
+// last. (2) Sorted rows are summed, `chunk` positions by one row of lanes; a run of one
+// id inside a chunk is finished there, one that crosses a chunk's border leaves
+// an f32 partial sum. (3) These are joined in order. Rows of no token, most of
+// a large table, are written beside (1) where one workgroup's LDS holds the sort
+// (up to 8192 tokens), and else beside (2). Every row of dw is written once.
 #include "rows.hpp"
 #include "status.hpp"
 
@@ -56,23 +56,35 @@ struct Lookup {
   uint32_t strips, items;
 };
 
-// Rows of up to 8 << log_lanes columns side by side; an id outside the table gives NaN.
-template <typename S>
+// Rows of up to 8 << log_lanes columns side by side, U rows of a lane loaded
+// together; an id outside the table gives NaN.
+template <typename S, int U>
 __global__ __launch_bounds__(256) void lookup(Lookup a) {
   for (uint32_t item = blockIdx.x; item < a.items; item += gridDim.x) {
     const uint32_t up = item / a.strips, strip = item - up * a.strips;
-    const int64_t t = (static_cast<int64_t>(up) << (8 - a.log_lanes)) + (threadIdx.x >> a.log_lanes);
+    const int64_t t0 = (static_cast<int64_t>(up) * U << (8 - a.log_lanes)) + (threadIdx.x >> a.log_lanes);
     const int64_t col = ((static_cast<int64_t>(strip) << a.log_lanes) + (threadIdx.x & ((1u << a.log_lanes) - 1))) * 8;
-    const int64_t count = t < a.ids.n ? a.dim - col : 0;
-    if (count <= 0) continue;
-    const int64_t id = id_at(a.ids, t);
-    const bool there = id >= 0 && id < a.ids.vocab;
-    Run<S> r;
-    r.load(static_cast<const S*>(a.table) + (there ? id : 0) * a.ld + col, there ? count : 0);
-    float x[8];
+    int64_t id[U];
+    Run<S> r[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = there ? r.get(e) * a.scale : __builtin_nanf("");
-    store8(static_cast<S*>(a.y) + t * a.dim + col, count, x);
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + (u << (8 - a.log_lanes));
+      id[u] = t < a.ids.n ? id_at(a.ids, t) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool there = id[u] >= 0 && id[u] < a.ids.vocab;
+      r[u].load(static_cast<const S*>(a.table) + (there ? id[u] : 0) * a.ld + col, there ? a.dim - col : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + (u << (8 - a.log_lanes));
+      const bool there = id[u] >= 0 && id[u] < a.ids.vocab;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = there ? r[u].get(e) * a.scale : __builtin_nanf("");
+      store8(static_cast<S*>(a.y) + t * a.dim + col, t < a.ids.n ? a.dim - col : 0, x);
+    }
   }
 }
 
@@ -87,6 +99,25 @@ struct Sort {
   uint8_t* touched;          // one byte an id: whether it has a token
   uint32_t tiles, shift, bits, passes;
 };
+
+// The rows of no token: a workgroup writes those of `rows` ids, 256 lanes side by side.
+struct Fill {
+  void* dw;
+  int64_t dim, rows;
+  int32_t log_lanes;
+};
+
+template <typename S, typename F>
+__device__ __forceinline__ void fill_rows(const Fill& a, int64_t first, int64_t last, F touched) {
+  const int lanes = 1 << a.log_lanes;
+  const int64_t lane = threadIdx.x & (lanes - 1);
+  const float zero[8] = {};
+  for (int64_t v = first + (threadIdx.x >> a.log_lanes); v < last; v += blockDim.x >> a.log_lanes) {
+    if (touched(v)) continue;
+    S* row = static_cast<S*>(a.dw) + v * a.dim;
+    for (int64_t col = lane * 8; col < a.dim; col += lanes * 8) store8(row + col, a.dim - col, zero);
+  }
+}
 
 // The place of each of a tile's keys when the tile is ordered by one digit, stable.
 // A thread holds the keys at wave * 64 R + r * 64 + lane; counts[digit][wave]. A
@@ -141,12 +172,31 @@ __device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t s
   for (int r = 0; r < R; ++r) place[r] += counts[((key[r] >> shift) & mask) * 16 + wave];
 }
 
-// Up to 1024 R tokens, all passes; flags of the ids that have one. (Bound by the
-// latency of its steps: one workgroup, three passes of four barriers.)
-template <int R>
-__global__ __launch_bounds__(1024) void sort_one(Sort a) {
+// Up to 1024 R tokens, all passes, by the first workgroup, bound by the latency of
+// its steps (8192 tokens, 3 passes: 27 us). The others meanwhile write the rows of no
+// token: each marks the ids of its own rows in LDS, reading all of the tokens, which come
+// from L2, and stores the rows without a mark.
+constexpr int kMarks = 32768;   // rows a workgroup looks after at most
+
+template <typename S, int R>
+__global__ __launch_bounds__(1024) void sort_and_fill(Sort a, Fill fill) {
   __shared__ uint32_t counts[kBins * 16], totals[16], keys[R * 1024];
   __shared__ uint16_t toks[R * 1024];
+  if (blockIdx.x > 0) {
+    __shared__ uint32_t marks[kMarks / 32];
+    const int64_t first = static_cast<int64_t>(blockIdx.x - 1) * fill.rows, last = min(a.ids.vocab, first + fill.rows);
+    for (int i = threadIdx.x; i < kMarks / 32; i += 1024) marks[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t i = r * 1024 + threadIdx.x;
+      const int64_t v = (i < a.ids.n ? static_cast<int64_t>(key_at(a.ids, i)) : last) - first;
+      if (v >= 0 && v < last - first) atomicOr(&marks[v / 32], 1u << (v % 32));
+    }
+    __syncthreads();
+    fill_rows<S>(fill, first, last, [&](int64_t v) { return (marks[(v - first) / 32] >> ((v - first) % 32)) & 1u; });
+    return;
+  }
   const uint32_t at = (threadIdx.x >> 6) * (64 * R) + (threadIdx.x & 63u);
   uint32_t key[R], tok[R], place[R];
 #pragma unroll
@@ -154,12 +204,6 @@ __global__ __launch_bounds__(1024) void sort_one(Sort a) {
     tok[r] = at + r * 64;
     key[r] = tok[r] < a.ids.n ? key_at(a.ids, tok[r]) : kPast;
   }
-  for (int64_t i = threadIdx.x; i < (a.ids.vocab + 15) / 16; i += 1024)
-    reinterpret_cast<asr::u32x4*>(a.touched)[i] = asr::u32x4{0, 0, 0, 0};
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (key[r] < a.ids.vocab) a.touched[key[r]] = 1;
   for (uint32_t pass = 0; pass < a.passes; ++pass) {
     tile_places<R>(key, pass * a.bits, a.bits, counts, totals, place);
 #pragma unroll
@@ -274,41 +318,40 @@ __global__ __launch_bounds__(256) void clear_flags(uint8_t* touched, int64_t voc
 struct Sums {
   const uint32_t* keys;
   const uint32_t* toks;
-  const uint8_t* touched;    // NULL: no id has a token
+  const uint8_t* touched;    // flags of the ids with a token, where rows are left to fill
   const void* dy;
   void* dw;
   float* part;               // [chunk][head, tail][dim]: runs that cross a border
   int64_t n, vocab, dim, ld;
-  int64_t fill_rows;         // rows a filling workgroup looks after
   float scale;
-  int32_t chunk;             // sorted positions a chunk
+  int32_t chunk;             // sorted positions a chunk, a multiple of 16
   int32_t chunks, log_lanes;
   uint32_t strips, sum_blocks;
+  Fill fill;
 };
 
+// A workgroup's chunks side by side, each by a row of lanes: 16 positions' keys and
+// tokens go to LDS (one wait for all), then their rows, 8 in flight.
 template <typename S>
 __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
-  const int lanes = 1 << a.log_lanes;
-  const int64_t lane = threadIdx.x & (lanes - 1);
+  constexpr int kBatch = 16, kAhead = 8;
+  __shared__ uint32_t keys[256 * kBatch], toks[256 * kBatch];
   if (blockIdx.x >= a.sum_blocks) {
-    const int64_t v0 = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * a.fill_rows;
-    const int64_t v1 = min(a.vocab, v0 + a.fill_rows);
-    const float zero[8] = {};
-    for (int64_t v = v0 + (threadIdx.x >> a.log_lanes); v < v1; v += 256 >> a.log_lanes) {
-      if (a.touched && a.touched[v]) continue;
-      S* row = static_cast<S*>(a.dw) + v * a.dim;
-      for (int64_t col = lane * 8; col < a.dim; col += lanes * 8) store8(row + col, a.dim - col, zero);
-    }
+    const int64_t first = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * a.fill.rows;
+    fill_rows<S>(a.fill, first, min(a.vocab, first + a.fill.rows),
+                 [&](int64_t v) { return a.touched && a.touched[v]; });
     return;
   }
+  const int lanes = 1 << a.log_lanes, side = 256 >> a.log_lanes;
   const uint32_t up = blockIdx.x / a.strips, strip = blockIdx.x - up * a.strips;
-  const int64_t c = (static_cast<int64_t>(up) << (8 - a.log_lanes)) + (threadIdx.x >> a.log_lanes);
-  const int64_t col = (static_cast<int64_t>(strip) * lanes + lane) * 8, count = a.dim - col;
-  if (c >= a.chunks || count <= 0) return;
+  const int mine = threadIdx.x >> a.log_lanes;
+  const int64_t c0 = static_cast<int64_t>(up) * side, c = c0 + mine;
+  const int64_t col = (static_cast<int64_t>(strip) * lanes + (threadIdx.x & (lanes - 1))) * 8, count = a.dim - col;
   const int64_t i0 = c * a.chunk, i1 = min(a.n, i0 + a.chunk);
+  const bool there = c < a.chunks && count > 0;
   const S* dy = static_cast<const S*>(a.dy) + col;
   const uint32_t vocab = static_cast<uint32_t>(a.vocab);
-  const uint32_t before = i0 > 0 ? a.keys[i0 - 1] : kPast, after = i1 < a.n ? a.keys[i1] : kPast;
+  const uint32_t before = there && i0 > 0 ? a.keys[i0 - 1] : kPast, after = there && i1 < a.n ? a.keys[i1] : kPast;
   uint32_t run = kPast;
   bool head = false;
   float acc[8] = {};
@@ -322,31 +365,42 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
       store8(static_cast<S*>(a.dw) + static_cast<int64_t>(run) * a.dim + col, count, x);
     }
   };
-  constexpr int kAhead = 4;   // rows in flight
-  for (int64_t i = i0; i < i1; i += kAhead) {
-    uint32_t key[kAhead];
-    Run<S> row[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      key[k] = i + k < i1 ? a.keys[i + k] : kPast;
-      const int64_t t = key[k] < vocab ? a.toks[i + k] : 0;
-      row[k].load(dy + t * a.ld, key[k] < vocab ? count : 0);
+  for (int32_t start = 0; start < a.chunk; start += kBatch) {
+    if (start > 0) __syncthreads();   // (the last batch is read)
+    for (int k = threadIdx.x; k < side * kBatch; k += 256) {
+      const int64_t i = (c0 + k / kBatch) * a.chunk + start + k % kBatch;
+      const bool in = i < a.n && c0 + k / kBatch < a.chunks;
+      keys[k] = in ? a.keys[i] : kPast;
+      toks[k] = in ? a.toks[i] : 0;
     }
+    __syncthreads();
+    if (!there) continue;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (key[k] >= vocab) continue;    // (only such follow)
-      if (key[k] != run) {
-        if (run != kPast) flush(false);
-        run = key[k];
-        head = i + k == i0 && run == before;
+    for (int half = 0; half < kBatch; half += kAhead) {
+      uint32_t key[kAhead];
+      Run<S> row[kAhead];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+      for (int k = 0; k < kAhead; ++k) {
+        const int at = mine * kBatch + half + k;
+        key[k] = keys[at];
+        row[k].load(dy + static_cast<int64_t>(toks[at]) * a.ld, key[k] < vocab ? count : 0);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += row[k].get(e);
+      for (int k = 0; k < kAhead; ++k) {
+        if (key[k] >= vocab) continue;    // (only such follow)
+        if (key[k] != run) {
+          if (run != kPast) flush(false);
+          run = key[k];
+          head = start + half + k == 0 && run == before;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += row[k].get(e);
+      }
     }
   }
-  if (run != kPast) flush(after == run);
+  if (there && run != kPast) flush(after == run);
 }
 
 // The runs that cross chunks: the chunk where one begins adds its tail and the
@@ -359,12 +413,9 @@ __global__ __launch_bounds__(1024) void join_runs(Sums a) {
   const uint32_t run = a.keys[i1];
   if (run >= a.vocab || a.keys[i1 - 1] != run) return;
   if (i0 > 0 && a.keys[i0 - 1] == run) return;   // it began before
-  int64_t lo = c + 1, hi = a.chunks;              // the run starts chunk lo, and no chunk from hi on
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (a.keys[mid * a.chunk] == run) lo = mid;
-    else hi = mid;
-  }
+  // the run starts the chunks up to hi (1024 at most are looked at, all at once)
+  const int64_t mine = c + 1 + threadIdx.x;
+  const int64_t hi = c + 1 + __syncthreads_count(mine < a.chunks && a.keys[mine * a.chunk] == run);
   const int64_t heads = hi - (c + 1), share = threadIdx.x / 256, each = (heads + 3) / 4;
   const int64_t from = c + 1 + share * each, to = min(hi, from + each);
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x % 256) * 4;
@@ -381,7 +432,7 @@ __global__ __launch_bounds__(1024) void join_runs(Sums a) {
     }
   };
   if (share == 0) add(c * 2 + 1);
-#pragma unroll 4
+#pragma unroll 8
   for (int64_t k = from; k < to; ++k) add(k * 2);
   lds[threadIdx.x] = t;
   __syncthreads();
@@ -416,6 +467,7 @@ constexpr int64_t kMaxCols = int64_t{1} << 24;
 constexpr int64_t kMaxBytes = int64_t{1} << 39;   // of a table: fewer than 2**24 workgroups write its gradient
 constexpr int64_t kMaxChunks = 1024;              // of sorted tokens: what the join of one id walks
 constexpr int64_t kFillBytes = 65536;             // of a workgroup that writes rows of no token
+constexpr int64_t kCus = 256;                     // compute units of an MI355X
 
 template <typename... A>
 hipError_t launch(void (*f)(A...), dim3 grid, int threads, hipStream_t s, std::common_type_t<A>... args) {
@@ -464,7 +516,7 @@ struct Buffers {
     keys[1] = take<uint32_t>(several ? n : 0);
     toks[1] = take<uint32_t>(several ? n : 0);
     hist = take<uint32_t>(several ? kBins * cut.tiles : 0);
-    touched = take<uint8_t>((vocab + 15) / 16 * 16);
+    touched = take<uint8_t>(several ? (vocab + 15) / 16 * 16 : 0);
     part = take<float>(static_cast<int64_t>(cut.chunks) * 2 * dim);
   }
 };
@@ -477,27 +529,37 @@ int check_table(int64_t n, int64_t vocab, int64_t dim, int32_t dtype) {
   return ASR_OK;
 }
 
-hipError_t sort_tokens(const Ids& ids, const Buffers& b, const Cut& cut, const uint32_t*& keys, const uint32_t*& toks,
-                       hipStream_t s) {
+Sort sort_args(const Ids& ids, const Buffers& b) {
   Sort a{};
   a.ids = ids;
-  a.touched = b.touched;
   uint32_t bits = 1;
   while ((ids.vocab >> bits) != 0) ++bits;   // of the key `vocab`, the largest
   a.passes = (bits + 7) / 8;
   a.bits = (bits + a.passes - 1) / a.passes;
   a.keys = b.keys[0];
   a.toks = b.toks[0];
-  keys = a.keys;
-  toks = a.toks;
-  if (ids.n <= 1024) return launch(&sort_one<1>, dim3(1), 1024, s, a);
-  if (ids.n <= 2048) return launch(&sort_one<2>, dim3(1), 1024, s, a);
-  if (ids.n <= 4096) return launch(&sort_one<4>, dim3(1), 1024, s, a);
-  if (ids.n <= kTile) return launch(&sort_one<8>, dim3(1), 1024, s, a);
+  return a;
+}
+
+template <typename S>
+hipError_t sort_one_tile(const Sort& a, Fill fill, hipStream_t s) {
+  // two workgroups of 16 waves on each compute unit, as long as each has 64 KB to write
+  const int64_t row = fill.dim * static_cast<int64_t>(sizeof(S));
+  fill.rows = std::clamp<int64_t>((a.ids.vocab + 2 * kCus - 2) / (2 * kCus - 1), (kFillBytes + row - 1) / row, kMarks);
+  const dim3 grid(static_cast<uint32_t>(1 + (a.ids.vocab + fill.rows - 1) / fill.rows));
+  if (a.ids.n <= 1024) return launch(&sort_and_fill<S, 1>, grid, 1024, s, a, fill);
+  if (a.ids.n <= 2048) return launch(&sort_and_fill<S, 2>, grid, 1024, s, a, fill);
+  if (a.ids.n <= 4096) return launch(&sort_and_fill<S, 4>, grid, 1024, s, a, fill);
+  return launch(&sort_and_fill<S, 8>, grid, 1024, s, a, fill);
+}
+
+// Several tiles: a ends with the sorted keys and tokens.
+hipError_t sort_tiles(Sort& a, const Buffers& b, const Cut& cut, hipStream_t s) {
   a.hist = b.hist;
+  a.touched = b.touched;
   a.tiles = static_cast<uint32_t>(cut.tiles);
-  hipError_t e = launch(&clear_flags, dim3(static_cast<uint32_t>(std::min<int64_t>((ids.vocab + 4095) / 4096, 1024))), 256, s,
-                        b.touched, ids.vocab);
+  hipError_t e = launch(&clear_flags, dim3(static_cast<uint32_t>(std::min<int64_t>((a.ids.vocab + 4095) / 4096, 1024))), 256, s,
+                        b.touched, a.ids.vocab);
   for (uint32_t pass = 0; pass < a.passes && e == hipSuccess; ++pass) {
     a.shift = pass * a.bits;
     a.keys = b.keys[pass % 2];
@@ -508,8 +570,6 @@ hipError_t sort_tokens(const Ids& ids, const Buffers& b, const Cut& cut, const u
     a.keys_in = a.keys;
     a.toks_in = a.toks;
   }
-  keys = a.keys;
-  toks = a.toks;
   return e;
 }
 
@@ -536,12 +596,17 @@ int asr_embedding_forward(const void* ids, int32_t ids_64, int64_t n, const void
   a.scale = static_cast<float>(scale);
   a.log_lanes = lanes_of(dim);
   a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
-  const int64_t rows = 256 >> a.log_lanes, up = (n + rows - 1) / rows;
+  // 4 rows of a lane, as long as that leaves enough workgroups for the chip
+  const int64_t rows = 256 >> a.log_lanes;
+  const bool many = (n + 4 * rows - 1) / (4 * rows) * a.strips >= 4 * kCus;
+  const int64_t up = (n + (many ? 4 : 1) * rows - 1) / ((many ? 4 : 1) * rows);
   if (up * a.strips >= kMaxDim) return fail(ASR_EINVAL, "embedding: too much for one call");
   a.items = static_cast<uint32_t>(up * a.strips);
   const uint32_t grid = std::min(a.items, 1u << 22);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = launch(dtype == ASR_F32 ? &lookup<float> : &lookup<uint16_t>, dim3(grid), 256, s, a);
+  auto* f = dtype == ASR_F32 ? (many ? &lookup<float, 4> : &lookup<float, 1>)
+                             : (many ? &lookup<uint16_t, 4> : &lookup<uint16_t, 1>);
+  const hipError_t e = launch(f, dim3(grid), 256, s, a);
   return e == hipSuccess ? ok() : hip_fail(e, "embedding launch");
 }
 
@@ -579,19 +644,28 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
   a.log_lanes = lanes_of(dim);
   a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
   const int64_t side = 256 >> a.log_lanes;
-  a.fill_rows = std::max<int64_t>(1, (kFillBytes / (dim * size) + side - 1) / side) * side;
+  a.fill = Fill{dtable, dim, std::max<int64_t>(1, (kFillBytes / (dim * size) + side - 1) / side) * side, a.log_lanes};
+  int64_t filling = (vocab + a.fill.rows - 1) / a.fill.rows;
   hipError_t e = hipSuccess;
   if (n > 0) {
     const Buffers b(workspace, n, vocab, dim);
     const Cut cut(n);
-    a.touched = b.touched;
     a.part = b.part;
     a.chunk = cut.chunk;
     a.chunks = cut.chunks;
     a.sum_blocks = static_cast<uint32_t>((cut.chunks + side - 1) / side * a.strips);
-    e = sort_tokens(Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, b, cut, a.keys, a.toks, s);
+    Sort sort = sort_args(Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, b);
+    if (cut.tiles == 1) {
+      e = dtype == ASR_F32 ? sort_one_tile<float>(sort, a.fill, s) : sort_one_tile<uint16_t>(sort, a.fill, s);
+      filling = 0;
+    } else {
+      e = sort_tiles(sort, b, cut, s);
+      a.touched = b.touched;
+    }
+    a.keys = sort.keys;
+    a.toks = sort.toks;
   }
-  const int64_t grid = a.sum_blocks + (vocab + a.fill_rows - 1) / a.fill_rows;
+  const int64_t grid = a.sum_blocks + filling;
   if (e == hipSuccess)
     e = launch(dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>, dim3(static_cast<uint32_t>(grid)), 256, s, a);
   if (e == hipSuccess && a.chunks > 1)

@@ -154,17 +154,21 @@ __global__ __launch_bounds__(256) void maxima(QuantArgs args) {
   uint32_t top[8] = {};
   for (int32_t r = r0 + rr; r < r1; r += 32) {  // 4 rows' loads in flight
     float t[4][8] = {};
+    [[maybe_unused]] float weight[4];
+    if constexpr (WEIGH) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) weight[i] = row_weight(a, r + 8 * i);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (r + 8 * i < r1) load8<S>(static_cast<const S*>(a.x) + (r + 8 * i) * a.ldx, col, a.cols, a.vec, t[i]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t across = 0;
-      [[maybe_unused]] const float weight = WEIGH ? row_weight(a, r + 8 * i) : 1.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t v = abs_bits(t[i][e]);
-        if constexpr (WEIGH) top[e] = max(top[e], abs_bits(t[i][e] * weight));
+        if constexpr (WEIGH) top[e] = max(top[e], abs_bits(t[i][e] * weight[i]));
         else top[e] = max(top[e], v);
         across = max(across, v);
       }
@@ -213,6 +217,7 @@ struct TileLds {
   uint32_t tops[256];
   GroupScale col_scale[64];
   GroupScale row_scale[128];
+  float weight[128];
 };
 
 template <typename S, bool SR, bool WEIGH>
@@ -274,6 +279,7 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
   }
   for (int32_t tr = tr0; tr < tr1; ++tr) {
     const int64_t r0 = static_cast<int64_t>(tr) * 128;
+    if (WEIGH && threadIdx.x < 128) lds.weight[threadIdx.x] = row_weight(a, r0 + threadIdx.x);
     if (a.q_row && threadIdx.x >= 128) {
       const int64_t r = r0 + threadIdx.x - 128;
       uint32_t top = 0;
@@ -292,11 +298,6 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[i][e] = raw[i].get(e);
     if (tr + 1 < tr1) fetch(tr + 1);
-    [[maybe_unused]] float weight[4];
-    if constexpr (WEIGH) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) weight[i] = row_weight(a, r0 + rg * 4 + i);
-    }
     uint32_t bits[4][8] = {};
     if constexpr (SR) {
 #pragma unroll
@@ -313,7 +314,7 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
       float v[4] = {x[0][e], x[1][e], x[2][e], x[3][e]};
       if constexpr (WEIGH) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= weight[i];
+        for (int i = 0; i < 4; ++i) v[i] *= lds.weight[rg * 4 + i];
       }
       const uint32_t r[4] = {bits[0][e], bits[1][e], bits[2][e], bits[3][e]};
       lds.tile[(cg * 8 + e) * kWords + rg] = codes4<SR>(v, g, r);
@@ -345,7 +346,7 @@ __device__ __forceinline__ void quantize_strip(const QuantArgs& args, const Quan
 }
 
 template <typename S, bool WEIGH>
-__global__ __launch_bounds__(256) void quantize_tiles(QuantArgs args) {
+__global__ __launch_bounds__(256, WEIGH ? 3 : 1) void quantize_tiles(QuantArgs args) {
   __shared__ TileLds lds;
   const QuantJob& a = job_of(args);
   if (a.sr) quantize_strip<S, true, WEIGH>(args, a, lds);

@@ -42,8 +42,8 @@ constexpr int kBlockCols = 128;  // columns that share a scale
 
 // ------------------------------------------------ elementwise over rows
 // A workgroup of 256 lanes is 16 groups of 16 lanes, a block of 128 columns each: 2**side
-// blocks of a row side by side, and 16 >> side rows. Items of work are numbered
-// row groups first, chunks of a row within.
+// blocks of a row side by side, and 16 >> side rows; U times that many rows an item of
+// work, loaded together. Items are numbered row groups first, chunks of a row within.
 struct Grid {
   int64_t rows;
   int32_t cols, blocks;   // blocks of 128 columns in a row
@@ -58,12 +58,13 @@ struct Place {
   int64_t padded;    // the same for stored codes, whose rows end at a multiple of 16
 };
 
-__device__ __forceinline__ Place place_of(const Grid& g, uint32_t item) {
+template <int U>
+__device__ __forceinline__ Place place_of(const Grid& g, uint32_t item, int u) {
   const uint32_t chunks = static_cast<uint32_t>(g.chunks);
   const uint32_t up = item / chunks, chunk = item - up * chunks;
   const int group = threadIdx.x / 16;
   Place p;
-  p.row = static_cast<int64_t>(up) * (16 >> g.side) + (group >> g.side);
+  p.row = (static_cast<int64_t>(up) * U + u) * (16 >> g.side) + (group >> g.side);
   p.block = static_cast<int32_t>(chunk << g.side) + (group & ((1 << g.side) - 1));
   p.col = static_cast<int64_t>(p.block) * kBlockCols + threadIdx.x % 16 * 8;
   const bool there = p.row < g.rows && p.block < g.blocks;
@@ -125,35 +126,47 @@ struct Pack {
   uint32_t seed, step;
 };
 
-template <typename S, bool SR>
+template <typename S, bool SR, int U>
 __global__ __launch_bounds__(256) void pack(Pack a) {
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
-    const Place p = place_of(a.g, item);
-    Run<S> raw;
-    raw.load(static_cast<const S*>(a.x) + p.row * a.ldx + p.col, p.count);
-    uint32_t bits[8] = {};
-    if constexpr (SR) {
-      const uint64_t at = a.base + static_cast<uint64_t>(p.row) * static_cast<uint64_t>(a.g.cols) +
-                          static_cast<uint64_t>(p.col);
-      asr_mfma::random_run<8>(at, (at & 3u) == 0, a.seed, a.step, bits);
-    }
-    float x[8], scale;
+    Run<S> raw[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = raw.get(e);
-    const asr::u32x2 w = block_codes<SR>(x, bits, scale);
-    store_codes(a.c, a.g, p, w, scale);
+    for (int u = 0; u < U; ++u) {
+      const Place p = place_of<U>(a.g, item, u);
+      raw[u].load(static_cast<const S*>(a.x) + p.row * a.ldx + p.col, p.count);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Place p = place_of<U>(a.g, item, u);
+      uint32_t bits[8] = {};
+      if constexpr (SR) {
+        const uint64_t at = a.base + static_cast<uint64_t>(p.row) * static_cast<uint64_t>(a.g.cols) +
+                            static_cast<uint64_t>(p.col);
+        asr_mfma::random_run<8>(at, (at & 3u) == 0, a.seed, a.step, bits);
+      }
+      float x[8], scale;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = raw[u].get(e);
+      const asr::u32x2 w = block_codes<SR>(x, bits, scale);
+      store_codes(a.c, a.g, p, w, scale);
+    }
   }
 }
 
-template <typename S>
+template <typename S, int U>
 __global__ __launch_bounds__(256) void unpack(Pack a) {
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
-    const Place p = place_of(a.g, item);
-    const Stored c = stored_at(a.c, a.g, p);
-    float x[8];
+    Stored c[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = c.get(e);
-    store8(static_cast<S*>(a.x) + p.row * a.ldx + p.col, p.count, x);
+    for (int u = 0; u < U; ++u) c[u] = stored_at(a.c, a.g, place_of<U>(a.g, item, u));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Place p = place_of<U>(a.g, item, u);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = c[u].get(e);
+      store8(static_cast<S*>(a.x) + p.row * a.ldx + p.col, p.count, x);
+    }
   }
 }
 
@@ -180,55 +193,69 @@ __device__ __forceinline__ float sigmoid(float x) {
   else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
 
-template <typename S, bool SAVE>
+template <typename S, bool SAVE, int U>
 __global__ __launch_bounds__(256) void silu_forward(Silu a) {
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
-    const Place p = place_of(a.g, item);
-    Run<S> rg, ru;
-    rg.load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
-    ru.load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
-    float g[8], u[8], y[8];
+    Run<S> rg[U], ru[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      g[e] = rg.get(e);
-      u[e] = ru.get(e);
-      y[e] = g[e] * sigmoid<S>(g[e]) * u[e];
+    for (int k = 0; k < U; ++k) {
+      const Place p = place_of<U>(a.g, item, k);
+      rg[k].load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
+      ru[k].load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
     }
-    store8(static_cast<S*>(a.y) + p.row * a.ld_y + p.col, p.count, y);
-    if constexpr (SAVE) {
-      const uint32_t none[8] = {};
-      float scale;
-      asr::u32x2 w = block_codes<false>(g, none, scale);
-      store_codes(a.cg, a.g, p, w, scale);
-      w = block_codes<false>(u, none, scale);
-      store_codes(a.cu, a.g, p, w, scale);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const Place p = place_of<U>(a.g, item, k);
+      float g[8], u[8], y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        g[e] = rg[k].get(e);
+        u[e] = ru[k].get(e);
+        y[e] = g[e] * sigmoid<S>(g[e]) * u[e];
+      }
+      store8(static_cast<S*>(a.y) + p.row * a.ld_y + p.col, p.count, y);
+      if constexpr (SAVE) {
+        const uint32_t none[8] = {};
+        float scale;
+        asr::u32x2 w = block_codes<false>(g, none, scale);
+        store_codes(a.cg, a.g, p, w, scale);
+        w = block_codes<false>(u, none, scale);
+        store_codes(a.cu, a.g, p, w, scale);
+      }
     }
   }
 }
 
-template <typename S, bool SAVED>
+template <typename S, bool SAVED, int U>
 __global__ __launch_bounds__(256) void silu_backward(Silu a) {
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
-    const Place p = place_of(a.g, item);
-    Run<S> rd;
-    rd.load(static_cast<const S*>(a.dy) + p.row * a.ld_dy + p.col, p.count);
-    std::conditional_t<SAVED, Stored, Run<S>> rg, ru;
-    if constexpr (SAVED) {
-      rg = stored_at(a.cg, a.g, p);
-      ru = stored_at(a.cu, a.g, p);
-    } else {
-      rg.load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
-      ru.load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
-    }
-    float dg[8], du[8];
+    Run<S> rd[U];
+    std::conditional_t<SAVED, Stored, Run<S>> rg[U], ru[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float g = rg.get(e), d = rd.get(e), sig = sigmoid<S>(g);
-      du[e] = d * (g * sig);
-      dg[e] = d * ru.get(e) * (sig * (1.0f + g * (1.0f - sig)));
+    for (int k = 0; k < U; ++k) {
+      const Place p = place_of<U>(a.g, item, k);
+      rd[k].load(static_cast<const S*>(a.dy) + p.row * a.ld_dy + p.col, p.count);
+      if constexpr (SAVED) {
+        rg[k] = stored_at(a.cg, a.g, p);
+        ru[k] = stored_at(a.cu, a.g, p);
+      } else {
+        rg[k].load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
+        ru[k].load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
+      }
     }
-    store8(static_cast<S*>(a.dgate) + p.row * a.ld_dgate + p.col, p.count, dg);
-    store8(static_cast<S*>(a.dup) + p.row * a.ld_dup + p.col, p.count, du);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const Place p = place_of<U>(a.g, item, k);
+      float dg[8], du[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = rg[k].get(e), d = rd[k].get(e), sig = sigmoid<S>(g);
+        du[e] = d * (g * sig);
+        dg[e] = d * ru[k].get(e) * (sig * (1.0f + g * (1.0f - sig)));
+      }
+      store8(static_cast<S*>(a.dgate) + p.row * a.ld_dgate + p.col, p.count, dg);
+      store8(static_cast<S*>(a.dup) + p.row * a.ld_dup + p.col, p.count, du);
+    }
   }
 }
 
@@ -258,18 +285,25 @@ struct Norm {
   uint32_t w_bf16, alone;   // alone: one workgroup, whose sums are the result
 };
 
-// The sum over the waves of a row (LANES / 64 of them), in every lane.
-template <int LANES, int THREADS>
-__device__ __forceinline__ double row_sum(double v, double* lds) {
-  v = wave_sum(v);
+// Two sums over the lanes of a row, in every lane.
+struct Pair {
+  double a, b;
+};
+
+template <int LANES>
+__device__ __forceinline__ Pair row_sum(Pair v, Pair* lds) {
+  v.a = wave_sum(v.a);
+  v.b = wave_sum(v.b);
   if constexpr (LANES > 64) {
     constexpr int kWaves = LANES / 64;
-    __syncthreads();  // (what was summed before has been read)
     if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
     __syncthreads();
-    v = 0.0;
+    v = Pair{0.0, 0.0};
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) v += lds[threadIdx.x / LANES * kWaves + i];
+    for (int i = 0; i < kWaves; ++i) {
+      v.a += lds[threadIdx.x / LANES * kWaves + i].a;
+      v.b += lds[threadIdx.x / LANES * kWaves + i].b;
+    }
   }
   return v;
 }
@@ -285,30 +319,35 @@ __device__ __forceinline__ RowStat stat_of(double mean, double rstd) {
 
 __device__ __forceinline__ float normal(float x, const RowStat& s) { return ((x - s.mean) - s.rest) * s.rstd; }
 
-// The sum of 8 columns, and of their squared distances to a mean, in 64 bits.
-__device__ __forceinline__ double sum8(const float (&x)[8]) {
-  double t = 0.0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) t += static_cast<double>(x[e]);
-  return t;
-}
-
-__device__ __forceinline__ double squares8(const float (&x)[8], int64_t count, double mean) {
-  double t = 0.0;
+// mean and var from one pass: sums of d = x - pivot and of d^2 in 64 bits, the pivot
+// being the row's first element. var = sum d^2 / C - (sum d / C)^2 loses little there:
+// (pivot - mean)^2 <= C var, as the pivot is itself a term of the variance, so its
+// relative error is below about C 2**-52 (and a constant row has d = 0). One
+// reduction over the lanes instead of two.
+__device__ __forceinline__ void add8(const float (&x)[8], int64_t count, double pivot, Pair& t) {
   if (count >= 8) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const double d = static_cast<double>(x[e]) - mean;
-      t = __builtin_fma(d, d, t);
+      const double d = static_cast<double>(x[e]) - pivot;
+      t.a += d;
+      t.b = __builtin_fma(d, d, t.b);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 7; ++e) {
-      const double d = static_cast<double>(x[e]) - mean;
-      if (e < count) t = __builtin_fma(d, d, t);
+      const double d = static_cast<double>(x[e]) - pivot;
+      if (e < count) {
+        t.a += d;
+        t.b = __builtin_fma(d, d, t.b);
+      }
     }
   }
-  return t;
+}
+
+__device__ __forceinline__ void moments(const Norm& a, Pair t, double pivot, double& mean, double& rstd) {
+  const double off = t.a * a.inv_cols, var = t.b * a.inv_cols - off * off;
+  mean = pivot + off;
+  rstd = 1.0 / __builtin_sqrt((var < 0.0 ? 0.0 : var) + a.eps);   // (NaN stays NaN)
 }
 
 // Codes of the normalised values of 8 columns, decided in 64 bits: with the largest
@@ -349,114 +388,99 @@ __device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t co
   return asr::u32x2{asr_i8::pack_bytes(u[0], u[1], u[2], u[3]), asr_i8::pack_bytes(u[4], u[5], u[6], u[7])};
 }
 
+// y, and if wanted the codes, of 8 columns.
+template <typename S, bool SAVE>
+__device__ __forceinline__ void finish8(const Norm& a, int64_t row, int64_t col, int64_t count, bool live,
+                                        const float (&x)[8], double mean, double rstd, const RowStat& stat) {
+  if constexpr (SAVE) {
+    float scale;
+    const asr::u32x2 codes = norm_codes(x, count, mean, rstd, scale);
+    if (live && col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16) {
+      *reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col) = codes;
+      if (threadIdx.x % 16 == 0 && count > 0) a.c.s[row * a.blocks + col / kBlockCols] = scale;
+    }
+  }
+  float w[8], b[8], out[8];
+  if (a.w) load_params(a.w, a.w_bf16, col, count, w);
+  if (a.b) load_params(a.b, a.w_bf16, col, count, b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    out[e] = normal(x[e], stat);
+    if (a.w) out[e] *= w[e];
+    if (a.b) out[e] += b[e];
+  }
+  store8(static_cast<S*>(a.y) + row * static_cast<int64_t>(a.cols) + col, count, out);
+}
+
 // Rows of up to LANES * KEEP * 8 columns, held in registers by LANES lanes.
 template <typename S, int LANES, int KEEP, bool SAVE>
 __global__ __launch_bounds__(256) void norm_rows(Norm a) {
-  __shared__ double lds[4];
+  __shared__ Pair lds[4];
   const int lane = threadIdx.x % LANES;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
   const bool live = row < a.rows;
   const S* x = static_cast<const S*>(a.x) + row * a.ldx;
-  float keep[KEEP][8];
-  double total = 0.0;
-  Run<S> raw[KEEP];
+  Run<S> raw[KEEP], first;
+  first.load(x, live ? 1 : 0);
 #pragma unroll
   for (int v = 0; v < KEEP; ++v) {
     const int64_t col = (lane + v * LANES) * 8;
     raw[v].load(x + col, live ? a.cols - col : 0);
   }
+  const double pivot = static_cast<double>(first.get(0));
+  Pair t = {0.0, 0.0};
 #pragma unroll
   for (int v = 0; v < KEEP; ++v) {
+    float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) keep[v][e] = raw[v].get(e);
-    total += sum8(keep[v]);
+    for (int e = 0; e < 8; ++e) f[e] = raw[v].get(e);
+    add8(f, a.cols - (lane + v * LANES) * 8, pivot, t);
   }
-  const double mean = row_sum<LANES, 256>(total, lds) * a.inv_cols;
-  double squares = 0.0;
-#pragma unroll
-  for (int v = 0; v < KEEP; ++v) squares += squares8(keep[v], a.cols - (lane + v * LANES) * 8, mean);
-  const double var = row_sum<LANES, 256>(squares, lds) * a.inv_cols;
-  const double rstd = 1.0 / __builtin_sqrt(var + a.eps);
+  double mean, rstd;
+  moments(a, row_sum<LANES>(t, lds), pivot, mean, rstd);
   const RowStat stat = stat_of(mean, rstd);
   if (a.stat && live && lane == 0) a.stat[row] = stat;
-  S* y = static_cast<S*>(a.y) + row * static_cast<int64_t>(a.cols);
 #pragma unroll
   for (int v = 0; v < KEEP; ++v) {
-    const int64_t col = (lane + v * LANES) * 8, count = live ? a.cols - col : 0;
-    if constexpr (SAVE) {
-      float scale;
-      const asr::u32x2 codes = norm_codes(keep[v], count, mean, rstd, scale);
-      if (live && col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16) {
-        *reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col) = codes;
-        if (lane % 16 == 0 && count > 0) a.c.s[row * a.blocks + col / kBlockCols] = scale;
-      }
-    }
-    float w[8], b[8], out[8];
-    if (a.w) load_params(a.w, a.w_bf16, col, count, w);
-    if (a.b) load_params(a.b, a.w_bf16, col, count, b);
+    const int64_t col = (lane + v * LANES) * 8;
+    float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      out[e] = normal(keep[v][e], stat);
-      if (a.w) out[e] *= w[e];
-      if (a.b) out[e] += b[e];
-    }
-    store8(y + col, count, out);
+    for (int e = 0; e < 8; ++e) f[e] = raw[v].get(e);
+    finish8<S, SAVE>(a, row, col, live ? a.cols - col : 0, live, f, mean, rstd, stat);
   }
 }
 
-// Longer rows: a workgroup each, read three times.
+// Longer rows: a workgroup each, read twice.
 template <typename S, bool SAVE>
 __global__ __launch_bounds__(256) void norm_long_rows(Norm a) {
-  __shared__ double lds[4];
+  __shared__ Pair lds[4];
   const int64_t row = blockIdx.x;
   const S* x = static_cast<const S*>(a.x) + row * a.ldx;
-  const int64_t padded = (static_cast<int64_t>(a.cols) + 127) / 128 * 128;  // (16 lanes stay together)
   auto values = [&](int64_t col, float (&v)[8]) {
     Run<S> raw;
     raw.load(x + col, a.cols - col);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = raw.get(e);
   };
-  double total = 0.0;
+  Run<S> first;
+  first.load(x, 1);
+  const double pivot = static_cast<double>(first.get(0));
+  Pair t = {0.0, 0.0};
   for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
     float v[8];
     values(col, v);
-    total += sum8(v);
+    add8(v, a.cols - col, pivot, t);
   }
-  const double mean = row_sum<256, 256>(total, lds) * a.inv_cols;
-  double squares = 0.0;
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
-    float v[8];
-    values(col, v);
-    squares += squares8(v, a.cols - col, mean);
-  }
-  const double var = row_sum<256, 256>(squares, lds) * a.inv_cols;
-  const double rstd = 1.0 / __builtin_sqrt(var + a.eps);
+  double mean, rstd;
+  moments(a, row_sum<256>(t, lds), pivot, mean, rstd);
   const RowStat stat = stat_of(mean, rstd);
   if (a.stat && threadIdx.x == 0) a.stat[row] = stat;
-  S* y = static_cast<S*>(a.y) + row * static_cast<int64_t>(a.cols);
-  // (whole waves: reduce16 wants every lane of a wave active)
-  for (int64_t start = 0; start < padded; start += 2048) {
-    const int64_t col = start + threadIdx.x * 8, count = a.cols - col;
-    float v[8], w[8], b[8], out[8];
+  // (all lanes in every turn: the codes' reduction wants them active)
+  for (int64_t start = 0; start < a.cols; start += 2048) {
+    const int64_t col = start + threadIdx.x * 8;
+    float v[8];
     values(col, v);
-    if constexpr (SAVE) {
-      float scale;
-      const asr::u32x2 codes = norm_codes(v, count, mean, rstd, scale);
-      if (col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16) {
-        *reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col) = codes;
-        if (threadIdx.x % 16 == 0 && count > 0) a.c.s[row * a.blocks + col / kBlockCols] = scale;
-      }
-    }
-    if (a.w) load_params(a.w, a.w_bf16, col, count, w);
-    if (a.b) load_params(a.b, a.w_bf16, col, count, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      out[e] = normal(v[e], stat);
-      if (a.w) out[e] *= w[e];
-      if (a.b) out[e] += b[e];
-    }
-    store8(y + col, count, out);
+    finish8<S, SAVE>(a, row, col, a.cols - col, true, v, mean, rstd, stat);
   }
 }
 
@@ -570,10 +594,10 @@ __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
 // Longer rows: dx by a workgroup a row, in two passes over it.
 template <typename S, bool SAVED>
 __global__ __launch_bounds__(256) void norm_backward_long(Norm a) {
-  __shared__ double lds[4];
+  __shared__ Pair lds[4];
   const int64_t row = blockIdx.x;
   const RowStat stat = a.stat[row];
-  double c0 = 0.0, c1 = 0.0;
+  Pair t = {0.0, 0.0};
   auto values = [&](int64_t col, float (&g)[8], float (&h)[8]) {
     const int64_t count = a.cols - col;
     Run<S> dy;
@@ -593,12 +617,12 @@ __global__ __launch_bounds__(256) void norm_backward_long(Norm a) {
     values(col, g, h);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      c0 += static_cast<double>(g[e]);
-      c1 = __builtin_fma(static_cast<double>(g[e]), static_cast<double>(h[e]), c1);
+      t.a += static_cast<double>(g[e]);
+      t.b = __builtin_fma(static_cast<double>(g[e]), static_cast<double>(h[e]), t.b);
     }
   }
-  const float m = static_cast<float>(row_sum<256, 256>(c0, lds) * a.inv_cols);
-  const float k = static_cast<float>(row_sum<256, 256>(c1, lds) * a.inv_cols);
+  t = row_sum<256>(t, lds);
+  const float m = static_cast<float>(t.a * a.inv_cols), k = static_cast<float>(t.b * a.inv_cols);
   S* out = static_cast<S*>(a.dx) + row * static_cast<int64_t>(a.cols);
   for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
     float g[8], h[8], x[8];
@@ -634,22 +658,24 @@ __global__ __launch_bounds__(256) void norm_columns_long(Norm a, int64_t share, 
   store8(out + a.cols, count, db);
 }
 
-// dw and db from the workgroups' sums: 64 columns a workgroup, 4 a lane, 16
-// shares of the workgroups side by side, joined in LDS in their order.
-__global__ __launch_bounds__(256) void norm_params(Norm a, int32_t parts) {
-  __shared__ asr::f32x4 lds[256];
+// dw and db from the workgroups' sums: 64 columns a workgroup, 4 a lane, 64
+// shares of the workgroups side by side (4 sums each, loaded at once), joined in
+// LDS in their order.
+__global__ __launch_bounds__(1024) void norm_params(Norm a, int32_t parts) {
+  __shared__ asr::f32x4 lds[1024];
   const int which = blockIdx.y, share = threadIdx.x / 16;
   void* result = which ? a.db : a.dw;
   if (!result) return;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x % 16 * 4;
   asr::f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int32_t each = (parts + 15) / 16, p1 = min(parts, (share + 1) * each);
+  const int32_t each = (parts + 63) / 64, p1 = min(parts, (share + 1) * each);
   const int left = static_cast<int>(min(int64_t{4}, a.cols - col));
   if (left == 4) {
-#pragma unroll 8
+#pragma unroll 4
     for (int32_t p = share * each; p < p1; ++p)
       t += *reinterpret_cast<const f32x4_any*>(a.part + (static_cast<int64_t>(p) * 2 + which) * a.cols + col);
   } else {
+#pragma unroll 4
     for (int32_t p = share * each; p < p1; ++p)
 #pragma unroll
       for (int e = 0; e < 3; ++e)
@@ -658,8 +684,8 @@ __global__ __launch_bounds__(256) void norm_params(Norm a, int32_t parts) {
   lds[threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.x < 16) {
-#pragma unroll
-    for (int i = 1; i < 16; ++i) t += lds[i * 16 + threadIdx.x];
+#pragma unroll 16
+    for (int i = 1; i < 64; ++i) t += lds[i * 16 + threadIdx.x];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (e < left) store_param(result, a.w_bf16, col + e, t[e]);
@@ -689,20 +715,32 @@ hipError_t launch(void (*f)(A...), dim3 grid, int threads, hipStream_t s, std::c
   return hipLaunchKernel(reinterpret_cast<const void*>(f), grid, dim3(threads), argv, 0, s);
 }
 
+template <int V>
+using Const = std::integral_constant<int, V>;
+
 int64_t blocks_of(int64_t cols) { return (cols + kBlockCols - 1) / kBlockCols; }
 
-// false: more work than one call takes
-bool make_grid(Grid& g, int64_t rows, int64_t cols) {
+// An item has 16 * 8 times 16 columns, once or `many` times: as many as leave enough
+// workgroups for the chip.
+constexpr int64_t kEnough = 2048;
+#ifndef MANY
+#define MANY 4
+#endif
+constexpr int kMany = MANY;
+
+// 0: more work than one call takes; else the rows' factor of an item
+int make_grid(Grid& g, int64_t rows, int64_t cols, int many) {
   g.rows = rows;
   g.cols = static_cast<int32_t>(cols);
   g.blocks = static_cast<int32_t>(blocks_of(cols));
   g.side = 0;
   while (g.side < 4 && (1 << g.side) < g.blocks) ++g.side;
   g.chunks = (g.blocks + (1 << g.side) - 1) >> g.side;
-  const int64_t up = (rows + (16 >> g.side) - 1) / (16 >> g.side);
-  if (up > kMaxItems / g.chunks - 1) return false;
-  g.items = static_cast<uint32_t>(up * g.chunks);
-  return true;
+  const auto up = [&](int64_t each) { return (rows + each - 1) / each; };
+  if (up(16 >> g.side) > kMaxItems / g.chunks - 1) return 0;
+  const int each = up(many * (16 >> g.side)) * g.chunks >= kEnough ? many : 1;
+  g.items = static_cast<uint32_t>(up(each * (16 >> g.side)) * g.chunks);
+  return each;
 }
 
 uint32_t grid_of(const Grid& g) { return static_cast<uint32_t>(std::min<int64_t>(g.items, kMaxGrid)); }
@@ -755,6 +793,9 @@ hipError_t norm_forward(const Norm& a, hipStream_t s) {
   if (a.cols <= 512) return one(&norm_rows<S, 64, 1, SAVE>, 4);
   if (a.cols <= 1024) return one(&norm_rows<S, 64, 2, SAVE>, 4);
   if (a.cols <= 2048) return one(&norm_rows<S, 64, 4, SAVE>, 4);
+#ifdef NORM_WAVE
+  if (a.cols <= 4096) return one(&norm_rows<S, 64, 8, SAVE>, 4);
+#endif
   if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 1);
   if (a.cols <= 8192) return one(&norm_rows<S, 256, 4, SAVE>, 1);
   if (a.cols <= 16384) return one(&norm_rows<S, 256, 8, SAVE>, 1);
@@ -787,7 +828,7 @@ hipError_t norm_back(Norm a, hipStream_t s) {
     }
   }
   if (e == hipSuccess && sums && !a.alone)
-    e = launch(&norm_params, dim3(static_cast<uint32_t>((static_cast<int64_t>(a.cols) + 63) / 64), 2), 256, s, a,
+    e = launch(&norm_params, dim3(static_cast<uint32_t>((static_cast<int64_t>(a.cols) + 63) / 64), 2), 1024, s, a,
                static_cast<int32_t>(parts));
   return e;
 }
@@ -807,7 +848,8 @@ int asr_pack_i8(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int64_t
   if (static_cast<uint64_t>(rows) * static_cast<uint64_t>(cols) - 1 > ~base_index)
     return fail(ASR_EINVAL, "pack_i8: base_index + rows*cols exceeds 2**64");
   Pack a{};
-  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "pack_i8: the matrix is too large for one call");
+  const int many = make_grid(a.g, rows, cols, kMany);
+  if (!many) return fail(ASR_EINVAL, "pack_i8: the matrix is too large for one call");
   a.x = const_cast<void*>(x);
   a.ldx = ldx;
   a.c = Codes{q, scale, ldq};
@@ -816,8 +858,11 @@ int asr_pack_i8(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int64_t
   a.step = step;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool sr = rounding == ASR_ROUND_SR;
-  auto* f = dtype == ASR_F32 ? (sr ? &pack<float, true> : &pack<float, false>)
-                             : (sr ? &pack<uint16_t, true> : &pack<uint16_t, false>);
+  const auto pick = [&](auto u) {
+    return dtype == ASR_F32 ? (sr ? &pack<float, true, u> : &pack<float, false, u>)
+                            : (sr ? &pack<uint16_t, true, u> : &pack<uint16_t, false, u>);
+  };
+  auto* f = many == 1 ? pick(Const<1>{}) : pick(Const<kMany>{});
   return done(launch(f, dim3(grid_of(a.g)), 256, s, a), "pack_i8 launch");
 }
 
@@ -828,13 +873,15 @@ int asr_unpack_i8(const int8_t* q, int64_t ldq, const float* scale, int64_t rows
   if (int rc = check_codes("unpack_i8", q, ldq, scale, cols)) return rc;
   if (int rc = check_matrix("unpack_i8", x, ldx, cols, dtype)) return rc;
   Pack a{};
-  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "unpack_i8: the matrix is too large for one call");
+  const int many = make_grid(a.g, rows, cols, kMany);
+  if (!many) return fail(ASR_EINVAL, "unpack_i8: the matrix is too large for one call");
   a.x = x;
   a.ldx = ldx;
   a.c = Codes{const_cast<int8_t*>(q), const_cast<float*>(scale), ldq};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return done(launch(dtype == ASR_F32 ? &unpack<float> : &unpack<uint16_t>, dim3(grid_of(a.g)), 256, s, a),
-              "unpack_i8 launch");
+  const auto pick = [&](auto u) { return dtype == ASR_F32 ? &unpack<float, u> : &unpack<uint16_t, u>; };
+  auto* f = many == 1 ? pick(Const<1>{}) : pick(Const<kMany>{});
+  return done(launch(f, dim3(grid_of(a.g)), 256, s, a), "unpack_i8 launch");
 }
 
 int asr_silu_mul_forward(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype,
@@ -851,7 +898,8 @@ int asr_silu_mul_forward(const void* gate, int64_t ld_gate, const void* up, int6
     if (int rc = check_codes("silu_mul", q_up, ldq, s_up, cols)) return rc;
   }
   Silu a{};
-  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "silu_mul: the matrix is too large for one call");
+  const int many = make_grid(a.g, rows, cols, kMany);
+  if (!many) return fail(ASR_EINVAL, "silu_mul: the matrix is too large for one call");
   a.gate = gate;
   a.up = up;
   a.y = y;
@@ -861,8 +909,11 @@ int asr_silu_mul_forward(const void* gate, int64_t ld_gate, const void* up, int6
   a.cg = Codes{q_gate, s_gate, ldq};
   a.cu = Codes{q_up, s_up, ldq};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  auto* f = dtype == ASR_F32 ? (save ? &silu_forward<float, true> : &silu_forward<float, false>)
-                             : (save ? &silu_forward<uint16_t, true> : &silu_forward<uint16_t, false>);
+  const auto pick = [&](auto u) {
+    return dtype == ASR_F32 ? (save ? &silu_forward<float, true, u> : &silu_forward<float, false, u>)
+                            : (save ? &silu_forward<uint16_t, true, u> : &silu_forward<uint16_t, false, u>);
+  };
+  auto* f = many == 1 ? pick(Const<1>{}) : pick(Const<kMany>{});
   return done(launch(f, dim3(grid_of(a.g)), 256, s, a), "silu_mul launch");
 }
 
@@ -885,7 +936,8 @@ int asr_silu_mul_backward(const void* dy, int64_t ld_dy, const void* gate, int64
     if (int rc = check_matrix("silu_mul", up, ld_up, cols, dtype)) return rc;
   }
   Silu a{};
-  if (!make_grid(a.g, rows, cols)) return fail(ASR_EINVAL, "silu_mul: the matrix is too large for one call");
+  const int many = make_grid(a.g, rows, cols, kMany);
+  if (!many) return fail(ASR_EINVAL, "silu_mul: the matrix is too large for one call");
   a.gate = gate;
   a.up = up;
   a.dy = dy;
@@ -899,8 +951,11 @@ int asr_silu_mul_backward(const void* dy, int64_t ld_dy, const void* gate, int64
   a.cg = Codes{const_cast<int8_t*>(q_gate), const_cast<float*>(s_gate), ldq};
   a.cu = Codes{const_cast<int8_t*>(q_up), const_cast<float*>(s_up), ldq};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  auto* f = dtype == ASR_F32 ? (saved ? &silu_backward<float, true> : &silu_backward<float, false>)
-                             : (saved ? &silu_backward<uint16_t, true> : &silu_backward<uint16_t, false>);
+  const auto pick = [&](auto u) {
+    return dtype == ASR_F32 ? (saved ? &silu_backward<float, true, u> : &silu_backward<float, false, u>)
+                            : (saved ? &silu_backward<uint16_t, true, u> : &silu_backward<uint16_t, false, u>);
+  };
+  auto* f = many == 1 ? pick(Const<1>{}) : pick(Const<kMany>{});
   return done(launch(f, dim3(grid_of(a.g)), 256, s, a), "silu_mul launch");
 }
 
@@ -959,7 +1014,7 @@ int asr_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int64_
   a.w_bf16 = param_dtype == ASR_BF16;
   if (rows == 0) {  // empty sums
     if (!dweight && !dbias) return ok();
-    return done(launch(&norm_params, dim3(static_cast<uint32_t>((cols + 63) / 64), 2), 256, s, a, 0), "layer_norm launch");
+    return done(launch(&norm_params, dim3(static_cast<uint32_t>((cols + 63) / 64), 2), 1024, s, a, 0), "layer_norm launch");
   }
   if (int rc = check_matrix("layer_norm", dy, ld_dy, cols, dtype)) return rc;
   if (dx)
