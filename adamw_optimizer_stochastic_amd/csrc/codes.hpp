@@ -62,11 +62,11 @@ __device__ __forceinline__ int32_t exact_code(float x, const GroupScale& g, uint
 
 // Codes of 4 elements of one group, packed. With the exact decision for every
 // element its arithmetic is what bounds the kernels, so the usual case is short: |x| * (1/s) is off by less than
-// 2**-15 here, so a value further than that from a border has its code from
-// one multiply-add (to nearest: onto 1.5 * 2**23, whose low byte is then the
-// code; stochastic: floor of the quotient plus 1 + r16/65536). A wave that
-// has an element nearer (1e-4) than that decides these exactly: 40 instructions an
-// element instead of 6. (58.7e6 bf16 values, rows, RN: 43 us, 58 us with the
+// 2.4e-5 here (the reciprocal's 2**-23 and the sum's 2**-24, of 129 at most), so a value
+// further than that from a border has its code from one multiply-add (to nearest:
+// onto 1.5 * 2**23, whose low byte is then the code; stochastic: floor of the
+// quotient plus 1 + r16/65536). A wave that has an element nearer (3e-5) than that
+// decides these exactly: 40 instructions an element instead of 6. (58.7e6 bf16 values, rows, RN: 43 us, 58 us with the
 // exact decision for all.)
 
 // Byte 0 of four words. (As asm: the compiler takes the permutes apart into
@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[4], const GroupScale
   float most = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(off[0]), __builtin_fabsf(off[1])),
                                __builtin_fmaxf(__builtin_fabsf(off[2]), __builtin_fabsf(off[3])));
   // (a scaled group, k != 1, takes the exact way: its inv is that of the scaled s)
-  if (__builtin_amdgcn_ballot_w64(most > 0.4999f || g.k != 1.0f) != 0) {
+  if (__builtin_amdgcn_ballot_w64(most > 0.49997f || g.k != 1.0f) != 0) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       u[e] = static_cast<uint32_t>(exact_code<SR>(g.live ? x[e] : 0.0f, g, r16[e]));

@@ -100,23 +100,45 @@ struct Sort {
   uint32_t tiles, shift, bits, passes;
 };
 
-// The rows of no token: a workgroup writes those of `rows` ids, 256 lanes side by side.
+// The rows of no token among ids [first, last): workgroup g of `groups` takes those of
+// the ids first + g + k * groups, so that neighbours in memory are written at once.
 struct Fill {
   void* dw;
-  int64_t dim, rows;
+  int64_t dim, first, last;
   int32_t log_lanes;
+  uint32_t groups;
 };
 
 template <typename S, typename F>
-__device__ __forceinline__ void fill_rows(const Fill& a, int64_t first, int64_t last, F touched) {
+__device__ __forceinline__ void fill_rows(const Fill& a, uint32_t g, F touched) {
   const int lanes = 1 << a.log_lanes;
   const int64_t lane = threadIdx.x & (lanes - 1);
   const float zero[8] = {};
-  for (int64_t v = first + (threadIdx.x >> a.log_lanes); v < last; v += blockDim.x >> a.log_lanes) {
-    if (touched(v)) continue;
+  for (int64_t k = threadIdx.x >> a.log_lanes;; k += blockDim.x >> a.log_lanes) {
+    const int64_t v = a.first + g + k * a.groups;
+    if (v >= a.last) break;
+    if (touched(k, v)) continue;
     S* row = static_cast<S*>(a.dw) + v * a.dim;
     for (int64_t col = lane * 8; col < a.dim; col += lanes * 8) store8(row + col, a.dim - col, zero);
   }
+}
+
+// The same where no flags tell which ids have a token: the workgroup marks its own
+// in LDS, reading all of the tokens, which come from L2.
+constexpr int kMarks = 32768;   // ids a workgroup looks after at most
+
+template <typename S>
+__device__ __forceinline__ void mark_and_fill(const Fill& a, const Ids& ids, uint32_t g, uint32_t* marks) {
+  for (uint32_t i = threadIdx.x; i < kMarks / 32; i += blockDim.x) marks[i] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < ids.n; i += blockDim.x) {
+    const uint32_t at = key_at(ids, i) - static_cast<uint32_t>(a.first) - g;   // (past the range if below it)
+    const uint32_t k = at / a.groups;
+    if (k * a.groups == at && at < static_cast<uint32_t>(a.last - a.first)) atomicOr(&marks[k / 32], 1u << (k % 32));
+  }
+  __syncthreads();
+  fill_rows<S>(a, g, [&](int64_t k, int64_t) { return (marks[k / 32] >> (k % 32)) & 1u; });
 }
 
 // The place of each of a tile's keys when the tile is ordered by one digit, stable.
@@ -173,28 +195,14 @@ __device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t s
 }
 
 // Up to 1024 R tokens, all passes, by the first workgroup, bound by the latency of
-// its steps (8192 tokens, 3 passes: 27 us). The others meanwhile write the rows of no
-// token: each marks the ids of its own rows in LDS, reading all of the tokens, which come
-// from L2, and stores the rows without a mark.
-constexpr int kMarks = 32768;   // rows a workgroup looks after at most
-
+// its steps (8192 tokens, 3 passes: 27 us). The others meanwhile write rows of no token.
 template <typename S, int R>
 __global__ __launch_bounds__(1024) void sort_and_fill(Sort a, Fill fill) {
   __shared__ uint32_t counts[kBins * 16], totals[16], keys[R * 1024];
   __shared__ uint16_t toks[R * 1024];
+  static_assert(kBins * 16 >= kMarks / 32);
   if (blockIdx.x > 0) {
-    __shared__ uint32_t marks[kMarks / 32];
-    const int64_t first = static_cast<int64_t>(blockIdx.x - 1) * fill.rows, last = min(a.ids.vocab, first + fill.rows);
-    for (int i = threadIdx.x; i < kMarks / 32; i += 1024) marks[i] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t i = r * 1024 + threadIdx.x;
-      const int64_t v = (i < a.ids.n ? static_cast<int64_t>(key_at(a.ids, i)) : last) - first;
-      if (v >= 0 && v < last - first) atomicOr(&marks[v / 32], 1u << (v % 32));
-    }
-    __syncthreads();
-    fill_rows<S>(fill, first, last, [&](int64_t v) { return (marks[(v - first) / 32] >> ((v - first) % 32)) & 1u; });
+    mark_and_fill<S>(fill, a.ids, blockIdx.x - 1, counts);
     return;
   }
   const uint32_t at = (threadIdx.x >> 6) * (64 * R) + (threadIdx.x & 63u);
@@ -318,10 +326,11 @@ __global__ __launch_bounds__(256) void clear_flags(uint8_t* touched, int64_t voc
 struct Sums {
   const uint32_t* keys;
   const uint32_t* toks;
-  const uint8_t* touched;    // flags of the ids with a token, where rows are left to fill
+  const uint8_t* touched;    // flags of the ids with a token (of several tiles)
   const void* dy;
   void* dw;
   float* part;               // [chunk][head, tail][dim]: runs that cross a border
+  Ids ids;
   int64_t n, vocab, dim, ld;
   float scale;
   int32_t chunk;             // sorted positions a chunk, a multiple of 16
@@ -330,16 +339,21 @@ struct Sums {
   Fill fill;
 };
 
-// A workgroup's chunks side by side, each by a row of lanes: 16 positions' keys and
-// tokens go to LDS (one wait for all), then their rows, 8 in flight.
+// A workgroup's chunks side by side, each by a row of 16 or more lanes: 16 positions'
+// keys and tokens go to LDS (one wait for all), then their rows, 8 at once, which each
+// lane puts into its own part of LDS: the loop over the runs then has one copy of its
+// code for all of them (unrolled over rows in registers it was 22 KB, and fetching it
+// was most of a small call's time).
 template <typename S>
 __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
-  constexpr int kBatch = 16, kAhead = 8;
-  __shared__ uint32_t keys[256 * kBatch], toks[256 * kBatch];
+  constexpr int kBatch = 16, kAhead = 8, kSide = 16;
+  __shared__ Run<S> rows[kAhead * 256];
+  __shared__ uint32_t keys[kSide * kBatch], toks[kSide * kBatch];
+  static_assert(sizeof(rows) >= kMarks / 8);
   if (blockIdx.x >= a.sum_blocks) {
-    const int64_t first = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * a.fill.rows;
-    fill_rows<S>(a.fill, first, min(a.vocab, first + a.fill.rows),
-                 [&](int64_t v) { return a.touched && a.touched[v]; });
+    const uint32_t g = blockIdx.x - a.sum_blocks;
+    if (a.touched) fill_rows<S>(a.fill, g, [&](int64_t, int64_t v) { return a.touched[v] != 0; });
+    else mark_and_fill<S>(a.fill, a.ids, g, reinterpret_cast<uint32_t*>(rows));
     return;
   }
   const int lanes = 1 << a.log_lanes, side = 256 >> a.log_lanes;
@@ -352,55 +366,59 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   const S* dy = static_cast<const S*>(a.dy) + col;
   const uint32_t vocab = static_cast<uint32_t>(a.vocab);
   const uint32_t before = there && i0 > 0 ? a.keys[i0 - 1] : kPast, after = there && i1 < a.n ? a.keys[i1] : kPast;
-  uint32_t run = kPast;
+  uint32_t run = kPast;      // of acc; no key of the table before the first
   bool head = false;
   float acc[8] = {};
-  auto flush = [&](bool tail) {
-    if (head || tail) {
-      store8(a.part + (c * 2 + (head ? 0 : 1)) * a.dim + col, count, acc);
-    } else {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = acc[e] * a.scale;
-      store8(static_cast<S*>(a.dw) + static_cast<int64_t>(run) * a.dim + col, count, x);
-    }
-  };
   for (int32_t start = 0; start < a.chunk; start += kBatch) {
     if (start > 0) __syncthreads();   // (the last batch is read)
-    for (int k = threadIdx.x; k < side * kBatch; k += 256) {
-      const int64_t i = (c0 + k / kBatch) * a.chunk + start + k % kBatch;
-      const bool in = i < a.n && c0 + k / kBatch < a.chunks;
-      keys[k] = in ? a.keys[i] : kPast;
-      toks[k] = in ? a.toks[i] : 0;
+    if (static_cast<int>(threadIdx.x) < side * kBatch) {
+      const int64_t i = (c0 + threadIdx.x / kBatch) * a.chunk + start + threadIdx.x % kBatch;
+      const bool in = i < a.n && c0 + threadIdx.x / kBatch < a.chunks;
+      keys[threadIdx.x] = in ? a.keys[i] : kPast;
+      toks[threadIdx.x] = in ? a.toks[i] : 0;
     }
     __syncthreads();
     if (!there) continue;
-#pragma unroll
+    const bool last = start + kBatch >= a.chunk;
     for (int half = 0; half < kBatch; half += kAhead) {
-      uint32_t key[kAhead];
       Run<S> row[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int at = mine * kBatch + half + k;
-        key[k] = keys[at];
-        row[k].load(dy + static_cast<int64_t>(toks[at]) * a.ld, key[k] < vocab ? count : 0);
+        row[k].load(dy + static_cast<int64_t>(toks[at]) * a.ld, keys[at] < vocab ? count : 0);
       }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (key[k] >= vocab) continue;    // (only such follow)
-        if (key[k] != run) {
-          if (run != kPast) flush(false);
-          run = key[k];
+      for (int k = 0; k < kAhead; ++k) rows[k * 256 + threadIdx.x] = row[k];
+      // one turn more after the last position, for the last run
+      const int turns = last && half + kAhead == kBatch ? kAhead + 1 : kAhead;
+#pragma unroll 1
+      for (int k = 0; k < turns; ++k) {
+        const uint32_t key = k < kAhead ? keys[mine * kBatch + half + k] : kPast;
+        if (key != run) {
+          if (run < vocab) {
+            const bool tail = k == kAhead ? after == run : false;
+            if (head || tail) {
+              store8(a.part + (c * 2 + (head ? 0 : 1)) * a.dim + col, count, acc);
+            } else {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = acc[e] * a.scale;
+              store8(static_cast<S*>(a.dw) + static_cast<int64_t>(run) * a.dim + col, count, x);
+            }
+          }
+          run = key;
           head = start + half + k == 0 && run == before;
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
         }
+        if (k < kAhead) {
+          const Run<S> r = rows[k * 256 + threadIdx.x];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += row[k].get(e);
+          for (int e = 0; e < 8; ++e) acc[e] += r.get(e);
+        }
       }
     }
   }
-  if (there && run != kPast) flush(after == run);
 }
 
 // The runs that cross chunks: the chunk where one begins adds its tail and the
@@ -468,6 +486,7 @@ constexpr int64_t kMaxBytes = int64_t{1} << 39;   // of a table: fewer than 2**2
 constexpr int64_t kMaxChunks = 1024;              // of sorted tokens: what the join of one id walks
 constexpr int64_t kFillBytes = 65536;             // of a workgroup that writes rows of no token
 constexpr int64_t kCus = 256;                     // compute units of an MI355X
+constexpr int64_t kBesideSort = 16384;            // bytes written in a token's share of the sort's time
 
 template <typename... A>
 hipError_t launch(void (*f)(A...), dim3 grid, int threads, hipStream_t s, std::common_type_t<A>... args) {
@@ -476,8 +495,8 @@ hipError_t launch(void (*f)(A...), dim3 grid, int threads, hipStream_t s, std::c
 }
 
 // log2 of the lanes of a row: 8 columns each, at most a workgroup
-int32_t lanes_of(int64_t dim) {
-  int32_t l = 0;
+int32_t lanes_of(int64_t dim, int32_t least = 0) {
+  int32_t l = least;
   while (l < 8 && (int64_t{8} << l) < dim) ++l;
   return l;
 }
@@ -541,12 +560,18 @@ Sort sort_args(const Ids& ids, const Buffers& b) {
   return a;
 }
 
+// Workgroups for a range of ids: `most` of them, as long as each has 64 KB to write and
+// no more ids than it can mark.
+void share_out(Fill& fill, int64_t size, int64_t most, bool marks) {
+  const int64_t ids = fill.last - fill.first;
+  int64_t groups = std::clamp<int64_t>(ids * fill.dim * size / kFillBytes, 1, most);
+  if (marks) groups = std::max(groups, (ids + kMarks - 1) / kMarks);
+  fill.groups = ids > 0 ? static_cast<uint32_t>(groups) : 0;
+}
+
 template <typename S>
-hipError_t sort_one_tile(const Sort& a, Fill fill, hipStream_t s) {
-  // two workgroups of 16 waves on each compute unit, as long as each has 64 KB to write
-  const int64_t row = fill.dim * static_cast<int64_t>(sizeof(S));
-  fill.rows = std::clamp<int64_t>((a.ids.vocab + 2 * kCus - 2) / (2 * kCus - 1), (kFillBytes + row - 1) / row, kMarks);
-  const dim3 grid(static_cast<uint32_t>(1 + (a.ids.vocab + fill.rows - 1) / fill.rows));
+hipError_t sort_one_tile(const Sort& a, const Fill& fill, hipStream_t s) {
+  const dim3 grid(1 + fill.groups);
   if (a.ids.n <= 1024) return launch(&sort_and_fill<S, 1>, grid, 1024, s, a, fill);
   if (a.ids.n <= 2048) return launch(&sort_and_fill<S, 2>, grid, 1024, s, a, fill);
   if (a.ids.n <= 4096) return launch(&sort_and_fill<S, 4>, grid, 1024, s, a, fill);
@@ -641,23 +666,27 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
   a.dim = dim;
   a.ld = ld_dy;
   a.scale = static_cast<float>(scale);
-  a.log_lanes = lanes_of(dim);
+  a.log_lanes = lanes_of(dim, 4);
   a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
   const int64_t side = 256 >> a.log_lanes;
-  a.fill = Fill{dtable, dim, std::max<int64_t>(1, (kFillBytes / (dim * size) + side - 1) / side) * side, a.log_lanes};
-  int64_t filling = (vocab + a.fill.rows - 1) / a.fill.rows;
+  a.fill = Fill{dtable, dim, 0, vocab, a.log_lanes, 0};
   hipError_t e = hipSuccess;
   if (n > 0) {
     const Buffers b(workspace, n, vocab, dim);
     const Cut cut(n);
+    a.ids = Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx};
     a.part = b.part;
     a.chunk = cut.chunk;
     a.chunks = cut.chunks;
     a.sum_blocks = static_cast<uint32_t>((cut.chunks + side - 1) / side * a.strips);
-    Sort sort = sort_args(Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, b);
+    Sort sort = sort_args(a.ids, b);
     if (cut.tiles == 1) {
-      e = dtype == ASR_F32 ? sort_one_tile<float>(sort, a.fill, s) : sort_one_tile<uint16_t>(sort, a.fill, s);
-      filling = 0;
+      // beside the sort as many rows as are written in its time, the others beside the sums
+      Fill first = a.fill;
+      first.last = std::min(vocab, n * kBesideSort / (dim * size));
+      a.fill.first = first.last;
+      share_out(first, size, kCus - 1, true);
+      e = dtype == ASR_F32 ? sort_one_tile<float>(sort, first, s) : sort_one_tile<uint16_t>(sort, first, s);
     } else {
       e = sort_tiles(sort, b, cut, s);
       a.touched = b.touched;
@@ -665,8 +694,9 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
     a.keys = sort.keys;
     a.toks = sort.toks;
   }
-  const int64_t grid = a.sum_blocks + filling;
-  if (e == hipSuccess)
+  share_out(a.fill, size, n > 0 && !a.touched ? 4 * kCus : int64_t{1} << 22, !a.touched);
+  const int64_t grid = a.sum_blocks + a.fill.groups;
+  if (e == hipSuccess && grid > 0)
     e = launch(dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>, dim3(static_cast<uint32_t>(grid)), 256, s, a);
   if (e == hipSuccess && a.chunks > 1)
     e = launch(dtype == ASR_F32 ? &join_runs<float> : &join_runs<uint16_t>,

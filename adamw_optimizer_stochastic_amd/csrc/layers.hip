@@ -51,27 +51,60 @@ struct Grid {
   uint32_t items;
 };
 
-struct Place {
-  int64_t row, col;
-  int32_t block;
-  int64_t count;     // columns from col to the row's end, 0 or less: none
-  int64_t padded;    // the same for stored codes, whose rows end at a multiple of 16
+// A lane's place in its item, the same in every item, and an item's own, which is
+// the same for the whole workgroup: addresses are one add of a lane's offset.
+struct Spot {
+  int32_t row, col, block;
+};
+
+__device__ __forceinline__ Spot spot_of(const Grid& g) {
+  const int32_t group = threadIdx.x / 16, block = group & ((1 << g.side) - 1);
+  return Spot{group >> g.side, block * kBlockCols + static_cast<int32_t>(threadIdx.x % 16) * 8, block};
+}
+
+struct Item {
+  int64_t row;          // of the first of the U row groups
+  int32_t col, block;
+  int32_t left, padded; // columns from col to the row's end, and to the next multiple of 16
 };
 
 template <int U>
-__device__ __forceinline__ Place place_of(const Grid& g, uint32_t item, int u) {
+__device__ __forceinline__ Item item_of(const Grid& g, uint32_t item) {
   const uint32_t chunks = static_cast<uint32_t>(g.chunks);
   const uint32_t up = item / chunks, chunk = item - up * chunks;
-  const int group = threadIdx.x / 16;
+  Item i;
+  i.row = static_cast<int64_t>(up) * (U * (16 >> g.side));
+  i.block = static_cast<int32_t>(chunk << g.side);
+  i.col = i.block * kBlockCols;
+  i.left = g.cols - i.col;
+  i.padded = (i.left + 15) / 16 * 16;
+  return i;
+}
+
+// Row group u of an item: its first row, and how many of a lane's columns there are (0
+// or less: none).
+struct Place {
+  int64_t row;
+  int32_t count, padded;
+};
+
+__device__ __forceinline__ Place place_of(const Grid& g, const Item& i, const Spot& s, int u) {
   Place p;
-  p.row = (static_cast<int64_t>(up) * U + u) * (16 >> g.side) + (group >> g.side);
-  p.block = static_cast<int32_t>(chunk << g.side) + (group & ((1 << g.side) - 1));
-  p.col = static_cast<int64_t>(p.block) * kBlockCols + threadIdx.x % 16 * 8;
-  const bool there = p.row < g.rows && p.block < g.blocks;
-  p.count = there ? g.cols - p.col : 0;
-  p.padded = there ? (static_cast<int64_t>(g.cols) + 15) / 16 * 16 - p.col : 0;
+  p.row = i.row + u * (16 >> g.side);
+  const bool there = s.row < static_cast<int32_t>(min(g.rows - p.row, int64_t{16}));
+  p.count = there ? i.left - s.col : 0;
+  p.padded = there ? i.padded - s.col : 0;
   return p;
 }
+
+// A matrix with row stride ld, and a lane's offset in any item.
+template <typename T>
+struct Lanes {
+  T* base;
+  int64_t ld, lane;
+  __device__ __forceinline__ Lanes(T* p, int64_t ld_, const Spot& s) : base(p), ld(ld_), lane(s.row * ld_ + s.col) {}
+  __device__ __forceinline__ T* at(const Item& i, const Place& p) const { return base + (p.row * ld + i.col) + lane; }
+};
 
 // Codes of 8 columns in a block that 16 lanes hold, and the block's scale.
 template <bool SR>
@@ -90,13 +123,8 @@ __device__ __forceinline__ asr::u32x2 block_codes(const float (&x)[8], const uin
 struct Codes {
   int8_t* q;
   float* s;       // rows x blocks
-  int64_t ld;     // of q, a multiple of 8
+  int64_t ld;     // of q, a multiple of 16
 };
-
-__device__ __forceinline__ void store_codes(const Codes& c, const Grid& g, const Place& p, asr::u32x2 w, float scale) {
-  if (p.padded > 0) *reinterpret_cast<asr::u32x2*>(c.q + p.row * c.ld + p.col) = w;
-  if (threadIdx.x % 16 == 0 && p.count > 0) c.s[p.row * g.blocks + p.block] = scale;
-}
 
 // 8 codes and their block's scale as loaded; q's rows are padded to 16 bytes.
 struct Stored {
@@ -111,11 +139,24 @@ struct Stored {
   }
 };
 
-__device__ __forceinline__ Stored stored_at(const Codes& c, const Grid& g, const Place& p) {
-  Stored s;
-  s.load(c.q + p.row * c.ld + p.col, c.s + p.row * g.blocks + p.block, p.count > 0);
-  return s;
-}
+struct CodeLanes {
+  Lanes<int8_t> q;
+  Lanes<float> s;
+  __device__ __forceinline__ CodeLanes(const Codes& c, const Grid& g, const Spot& spot)
+      : q(c.q, c.ld, spot), s(c.s, g.blocks, Spot{spot.row, spot.block, 0}) {}
+  __device__ __forceinline__ float* scale(const Item& i, const Place& p) const {
+    return s.base + (p.row * s.ld + i.block) + s.lane;
+  }
+  __device__ __forceinline__ void store(const Item& i, const Place& p, asr::u32x2 w, float value) const {
+    if (p.padded > 0) *reinterpret_cast<asr::u32x2*>(q.at(i, p)) = w;
+    if (threadIdx.x % 16 == 0 && p.count > 0) *scale(i, p) = value;
+  }
+  __device__ __forceinline__ Stored load(const Item& i, const Place& p) const {
+    Stored c;
+    c.load(q.at(i, p), scale(i, p), p.count > 0);
+    return c;
+  }
+};
 
 struct Pack {
   Grid g;
@@ -128,44 +169,52 @@ struct Pack {
 
 template <typename S, bool SR, int U>
 __global__ __launch_bounds__(256) void pack(Pack a) {
+  const Spot spot = spot_of(a.g);
+  const Lanes<const S> x(static_cast<const S*>(a.x), a.ldx, spot);
+  const CodeLanes c(a.c, a.g, spot);
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
+    const Item i = item_of<U>(a.g, item);
     Run<S> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Place p = place_of<U>(a.g, item, u);
-      raw[u].load(static_cast<const S*>(a.x) + p.row * a.ldx + p.col, p.count);
+      const Place p = place_of(a.g, i, spot, u);
+      raw[u].load(x.at(i, p), p.count);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Place p = place_of<U>(a.g, item, u);
+      const Place p = place_of(a.g, i, spot, u);
       uint32_t bits[8] = {};
       if constexpr (SR) {
-        const uint64_t at = a.base + static_cast<uint64_t>(p.row) * static_cast<uint64_t>(a.g.cols) +
-                            static_cast<uint64_t>(p.col);
+        const uint64_t at = a.base + static_cast<uint64_t>(p.row + spot.row) * static_cast<uint64_t>(a.g.cols) +
+                            static_cast<uint64_t>(i.col + spot.col);
         asr_mfma::random_run<8>(at, (at & 3u) == 0, a.seed, a.step, bits);
       }
-      float x[8], scale;
+      float v[8], scale;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = raw[u].get(e);
-      const asr::u32x2 w = block_codes<SR>(x, bits, scale);
-      store_codes(a.c, a.g, p, w, scale);
+      for (int e = 0; e < 8; ++e) v[e] = raw[u].get(e);
+      const asr::u32x2 w = block_codes<SR>(v, bits, scale);
+      c.store(i, p, w, scale);
     }
   }
 }
 
 template <typename S, int U>
 __global__ __launch_bounds__(256) void unpack(Pack a) {
+  const Spot spot = spot_of(a.g);
+  const Lanes<S> x(static_cast<S*>(a.x), a.ldx, spot);
+  const CodeLanes c(a.c, a.g, spot);
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
-    Stored c[U];
+    const Item i = item_of<U>(a.g, item);
+    Stored in[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) c[u] = stored_at(a.c, a.g, place_of<U>(a.g, item, u));
+    for (int u = 0; u < U; ++u) in[u] = c.load(i, place_of(a.g, i, spot, u));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Place p = place_of<U>(a.g, item, u);
-      float x[8];
+      const Place p = place_of(a.g, i, spot, u);
+      float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = c[u].get(e);
-      store8(static_cast<S*>(a.x) + p.row * a.ldx + p.col, p.count, x);
+      for (int e = 0; e < 8; ++e) v[e] = in[u].get(e);
+      store8(x.at(i, p), p.count, v);
     }
   }
 }
@@ -195,17 +244,22 @@ __device__ __forceinline__ float sigmoid(float x) {
 
 template <typename S, bool SAVE, int U>
 __global__ __launch_bounds__(256) void silu_forward(Silu a) {
+  const Spot spot = spot_of(a.g);
+  const Lanes<const S> gate(static_cast<const S*>(a.gate), a.ld_gate, spot), up(static_cast<const S*>(a.up), a.ld_up, spot);
+  const Lanes<S> out(static_cast<S*>(a.y), a.ld_y, spot);
+  const CodeLanes cg(a.cg, a.g, spot), cu(a.cu, a.g, spot);
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
+    const Item i = item_of<U>(a.g, item);
     Run<S> rg[U], ru[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const Place p = place_of<U>(a.g, item, k);
-      rg[k].load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
-      ru[k].load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
+      const Place p = place_of(a.g, i, spot, k);
+      rg[k].load(gate.at(i, p), p.count);
+      ru[k].load(up.at(i, p), p.count);
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const Place p = place_of<U>(a.g, item, k);
+      const Place p = place_of(a.g, i, spot, k);
       float g[8], u[8], y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -213,14 +267,14 @@ __global__ __launch_bounds__(256) void silu_forward(Silu a) {
         u[e] = ru[k].get(e);
         y[e] = g[e] * sigmoid<S>(g[e]) * u[e];
       }
-      store8(static_cast<S*>(a.y) + p.row * a.ld_y + p.col, p.count, y);
+      store8(out.at(i, p), p.count, y);
       if constexpr (SAVE) {
         const uint32_t none[8] = {};
         float scale;
         asr::u32x2 w = block_codes<false>(g, none, scale);
-        store_codes(a.cg, a.g, p, w, scale);
+        cg.store(i, p, w, scale);
         w = block_codes<false>(u, none, scale);
-        store_codes(a.cu, a.g, p, w, scale);
+        cu.store(i, p, w, scale);
       }
     }
   }
@@ -228,24 +282,30 @@ __global__ __launch_bounds__(256) void silu_forward(Silu a) {
 
 template <typename S, bool SAVED, int U>
 __global__ __launch_bounds__(256) void silu_backward(Silu a) {
+  const Spot spot = spot_of(a.g);
+  const Lanes<const S> gate(static_cast<const S*>(a.gate), a.ld_gate, spot), up(static_cast<const S*>(a.up), a.ld_up, spot),
+      dy(static_cast<const S*>(a.dy), a.ld_dy, spot);
+  const Lanes<S> dgate(static_cast<S*>(a.dgate), a.ld_dgate, spot), dup(static_cast<S*>(a.dup), a.ld_dup, spot);
+  const CodeLanes cg(a.cg, a.g, spot), cu(a.cu, a.g, spot);
   for (uint32_t item = blockIdx.x; item < a.g.items; item += gridDim.x) {
+    const Item i = item_of<U>(a.g, item);
     Run<S> rd[U];
     std::conditional_t<SAVED, Stored, Run<S>> rg[U], ru[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const Place p = place_of<U>(a.g, item, k);
-      rd[k].load(static_cast<const S*>(a.dy) + p.row * a.ld_dy + p.col, p.count);
+      const Place p = place_of(a.g, i, spot, k);
+      rd[k].load(dy.at(i, p), p.count);
       if constexpr (SAVED) {
-        rg[k] = stored_at(a.cg, a.g, p);
-        ru[k] = stored_at(a.cu, a.g, p);
+        rg[k] = cg.load(i, p);
+        ru[k] = cu.load(i, p);
       } else {
-        rg[k].load(static_cast<const S*>(a.gate) + p.row * a.ld_gate + p.col, p.count);
-        ru[k].load(static_cast<const S*>(a.up) + p.row * a.ld_up + p.col, p.count);
+        rg[k].load(gate.at(i, p), p.count);
+        ru[k].load(up.at(i, p), p.count);
       }
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const Place p = place_of<U>(a.g, item, k);
+      const Place p = place_of(a.g, i, spot, k);
       float dg[8], du[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -253,8 +313,8 @@ __global__ __launch_bounds__(256) void silu_backward(Silu a) {
         du[e] = d * (g * sig);
         dg[e] = d * ru[k].get(e) * (sig * (1.0f + g * (1.0f - sig)));
       }
-      store8(static_cast<S*>(a.dgate) + p.row * a.ld_dgate + p.col, p.count, dg);
-      store8(static_cast<S*>(a.dup) + p.row * a.ld_dup + p.col, p.count, du);
+      store8(dgate.at(i, p), p.count, dg);
+      store8(dup.at(i, p), p.count, du);
     }
   }
 }
@@ -317,7 +377,13 @@ __device__ __forceinline__ RowStat stat_of(double mean, double rstd) {
   return s;
 }
 
-__device__ __forceinline__ float normal(float x, const RowStat& s) { return ((x - s.mean) - s.rest) * s.rstd; }
+// (x - mean) rstd, the mean in two parts: x - mean's first is exact or off by half a
+// step of itself, so a mean far larger than the spread costs nothing.
+struct Normal {
+  float mean, rstd, off;
+  __device__ __forceinline__ explicit Normal(const RowStat& s) : mean(s.mean), rstd(s.rstd), off(-s.rest * s.rstd) {}
+  __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(x - mean, rstd, off); }
+};
 
 // mean and var from one pass: sums of d = x - pivot and of d^2 in 64 bits, the pivot
 // being the row's first element. var = sum d^2 / C - (sum d / C)^2 loses little there:
@@ -350,10 +416,14 @@ __device__ __forceinline__ void moments(const Norm& a, Pair t, double pivot, dou
   rstd = 1.0 / __builtin_sqrt((var < 0.0 ? 0.0 : var) + a.eps);   // (NaN stays NaN)
 }
 
-// Codes of the normalised values of 8 columns, decided in 64 bits: with the largest
-// |x - mean| of the block, from its largest and smallest x (16 lanes).
+// Codes of the normalised values of 8 columns, as 64 bits decide them: scale from the
+// largest |x - mean| of the block, which is that of its largest or smallest x (16
+// lanes). A code is the nearest whole number to (x - mean) (rstd / s); in 32 bits
+// that is off by less than 3e-5 (three roundings of 2**-24 of at most 127), so only a
+// wave with an element nearer than 5e-5 to a border decides in 64.
 __device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t count, double mean, double rstd,
-                                                 float& scale) {
+                                                 const Normal& normal, float& scale) {
+  constexpr float kByte = 12582912.0f;  // 1.5 * 2**23: a sum's low byte is its whole part
   float hi = -__builtin_inff(), lo = __builtin_inff();
   if (count >= 8) {
 #pragma unroll
@@ -371,82 +441,119 @@ __device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t co
   hi = reduce16(hi, [](float a, float b) { return __builtin_fmaxf(a, b); });
   lo = reduce16(lo, [](float a, float b) { return __builtin_fminf(a, b); });
   // (a NaN or Inf in the row has made the mean one)
-  const double top = __builtin_fmax(__builtin_fabs(static_cast<double>(hi) - mean),
-                                    __builtin_fabs(static_cast<double>(lo) - mean)) * rstd;
-  const float s = static_cast<float>(top / 127.0);
+  const double most = __builtin_fmax(__builtin_fabs(static_cast<double>(hi) - mean),
+                                     __builtin_fabs(static_cast<double>(lo) - mean));
+  const float s = static_cast<float>(most * rstd / 127.0);
   const bool finite = s < __builtin_inff();    // (false for NaN)
   const bool live = finite && s >= 0x1p-126f;
   scale = finite ? (live ? s : 0.0f) : __uint_as_float(0x7FC00000u);
   const double turn = live ? rstd / static_cast<double>(s) : 0.0;
+  const float turn32 = static_cast<float>(turn), off = normal.off * (turn32 / normal.rstd);
   uint32_t u[8];
+  float far = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const double t = __builtin_rint((static_cast<double>(x[e]) - mean) * turn);
-    const int32_t k = live && e < count ? static_cast<int32_t>(__builtin_fmin(__builtin_fmax(t, -127.0), 127.0)) : 0;
-    u[e] = static_cast<uint32_t>(k);
+    const float t = __builtin_fmaf(x[e] - normal.mean, turn32, off), v = t + kByte;
+    far = __builtin_fmaxf(far, __builtin_fabsf(t - (v - kByte)));
+    u[e] = __float_as_uint(v);
   }
-  return asr::u32x2{asr_i8::pack_bytes(u[0], u[1], u[2], u[3]), asr_i8::pack_bytes(u[4], u[5], u[6], u[7])};
+  // (!(..): also where 32 bits overflow or have no rstd)
+  if (__builtin_amdgcn_ballot_w64(live && !(far < 0.49995f && turn32 < 0x1p100f && off == off)) != 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double t = __builtin_rint((static_cast<double>(x[e]) - mean) * turn);
+      u[e] = static_cast<uint32_t>(static_cast<int32_t>(__builtin_fmin(__builtin_fmax(t, -127.0), 127.0)));
+    }
+  }
+  asr::u32x2 w = {asr_i8::pack_bytes(u[0], u[1], u[2], u[3]), asr_i8::pack_bytes(u[4], u[5], u[6], u[7])};
+  if (count < 8) {   // zeros behind the row's end
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e >= count) w[e / 4] &= ~(0xFFu << (e % 4 * 8));
+  }
+  return live ? w : asr::u32x2{0, 0};
 }
+
+// weight and bias of a lane's columns (1 and 0 where there is none)
+struct Affine {
+  float w[8], b[8];
+  __device__ __forceinline__ void load(const Norm& a, int64_t col) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[e] = 1.0f;
+      b[e] = 0.0f;
+    }
+    if (a.w) load_params(a.w, a.w_bf16, col, a.cols - col, w);
+    if (a.b) load_params(a.b, a.w_bf16, col, a.cols - col, b);
+  }
+};
 
 // y, and if wanted the codes, of 8 columns.
 template <typename S, bool SAVE>
 __device__ __forceinline__ void finish8(const Norm& a, int64_t row, int64_t col, int64_t count, bool live,
-                                        const float (&x)[8], double mean, double rstd, const RowStat& stat) {
+                                        const float (&x)[8], double mean, double rstd, const RowStat& stat,
+                                        const Affine& p) {
+  const Normal normal(stat);
   if constexpr (SAVE) {
     float scale;
-    const asr::u32x2 codes = norm_codes(x, count, mean, rstd, scale);
+    const asr::u32x2 codes = norm_codes(x, count, mean, rstd, normal, scale);
     if (live && col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16) {
       *reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col) = codes;
       if (threadIdx.x % 16 == 0 && count > 0) a.c.s[row * a.blocks + col / kBlockCols] = scale;
     }
   }
-  float w[8], b[8], out[8];
-  if (a.w) load_params(a.w, a.w_bf16, col, count, w);
-  if (a.b) load_params(a.b, a.w_bf16, col, count, b);
+  float out[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    out[e] = normal(x[e], stat);
-    if (a.w) out[e] *= w[e];
-    if (a.b) out[e] += b[e];
-  }
+  for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(normal(x[e]), p.w[e], p.b[e]);
   store8(static_cast<S*>(a.y) + row * static_cast<int64_t>(a.cols) + col, count, out);
 }
 
-// Rows of up to LANES * KEEP * 8 columns, held in registers by LANES lanes.
+// Rows of up to LANES * KEEP * 8 columns, held in registers by LANES lanes; a group of
+// lanes takes `each` rows in a row with its weights and biases in registers, and loads
+// the next row before it joins the sums of this one.
 template <typename S, int LANES, int KEEP, bool SAVE>
-__global__ __launch_bounds__(256) void norm_rows(Norm a) {
-  __shared__ Pair lds[4];
-  const int lane = threadIdx.x % LANES;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  const bool live = row < a.rows;
-  const S* x = static_cast<const S*>(a.x) + row * a.ldx;
-  Run<S> raw[KEEP], first;
-  first.load(x, live ? 1 : 0);
+__global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_rows(Norm a, int32_t each) {
+  constexpr int kThreads = LANES > 256 ? LANES : 256, kGroups = kThreads / LANES;
+  __shared__ Pair lds[2][kThreads / 64];
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  Affine params[KEEP];
 #pragma unroll
-  for (int v = 0; v < KEEP; ++v) {
-    const int64_t col = (lane + v * LANES) * 8;
-    raw[v].load(x + col, live ? a.cols - col : 0);
-  }
-  const double pivot = static_cast<double>(first.get(0));
-  Pair t = {0.0, 0.0};
+  for (int v = 0; v < KEEP; ++v) params[v].load(a, (lane + v * LANES) * 8);
+  Run<S> next[KEEP], first_next;
+  auto fetch = [&](int64_t row) {
+    const bool live = row < a.rows;
+    const S* x = static_cast<const S*>(a.x) + row * a.ldx;
+    first_next.load(x, live ? 1 : 0);
 #pragma unroll
-  for (int v = 0; v < KEEP; ++v) {
-    float f[8];
+    for (int v = 0; v < KEEP; ++v) {
+      const int64_t col = (lane + v * LANES) * 8;
+      next[v].load(x + col, live ? a.cols - col : 0);
+    }
+  };
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * each * kGroups;
+  fetch(start + group);
+  for (int32_t i = 0; i < each; ++i) {
+    const int64_t row = start + static_cast<int64_t>(i) * kGroups + group;
+    const bool live = row < a.rows;
+    const double pivot = static_cast<double>(first_next.get(0));
+    float x[KEEP][8];
+    Pair t = {0.0, 0.0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = raw[v].get(e);
-    add8(f, a.cols - (lane + v * LANES) * 8, pivot, t);
-  }
-  double mean, rstd;
-  moments(a, row_sum<LANES>(t, lds), pivot, mean, rstd);
-  const RowStat stat = stat_of(mean, rstd);
-  if (a.stat && live && lane == 0) a.stat[row] = stat;
+    for (int v = 0; v < KEEP; ++v) {
 #pragma unroll
-  for (int v = 0; v < KEEP; ++v) {
-    const int64_t col = (lane + v * LANES) * 8;
-    float f[8];
+      for (int e = 0; e < 8; ++e) x[v][e] = next[v].get(e);
+      add8(x[v], a.cols - (lane + v * LANES) * 8, pivot, t);
+    }
+    if (i + 1 < each) fetch(row + kGroups);
+    double mean, rstd;
+    moments(a, row_sum<LANES>(t, lds[i % 2]), pivot, mean, rstd);
+    const RowStat stat = stat_of(mean, rstd);
+    if (a.stat && live && lane == 0) a.stat[row] = stat;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = raw[v].get(e);
-    finish8<S, SAVE>(a, row, col, live ? a.cols - col : 0, live, f, mean, rstd, stat);
+    for (int v = 0; v < KEEP; ++v) {
+      const int64_t col = (lane + v * LANES) * 8;
+      finish8<S, SAVE>(a, row, col, live ? a.cols - col : 0, live, x[v], mean, rstd, stat, params[v]);
+    }
   }
 }
 
@@ -479,8 +586,10 @@ __global__ __launch_bounds__(256) void norm_long_rows(Norm a) {
   for (int64_t start = 0; start < a.cols; start += 2048) {
     const int64_t col = start + threadIdx.x * 8;
     float v[8];
+    Affine p;
+    p.load(a, col);
     values(col, v);
-    finish8<S, SAVE>(a, row, col, a.cols - col, true, v, mean, rstd, stat);
+    finish8<S, SAVE>(a, row, col, a.cols - col, true, v, mean, rstd, stat, p);
   }
 }
 
@@ -495,9 +604,9 @@ struct Normalised {
       v.load(static_cast<const S*>(a.x) + row * a.ldx + col, count);
     }
   }
-  __device__ __forceinline__ float get(int e, const RowStat& s) const {
+  __device__ __forceinline__ float get(int e, const Normal& normal) const {
     if constexpr (SAVED) return v.get(e);
-    else return normal(v.get(e), s);
+    else return normal(v.get(e));
   }
 };
 
@@ -545,10 +654,11 @@ __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
     dy = dy_next;
     xh = xh_next;
     if (first + stride < a.rows) fetch(row + stride);
+    const Normal normal(stat);
     f32x2 c = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float d = dy.get(e), h = xh.get(e, stat), g = d * w[e];
+      const float d = dy.get(e), h = xh.get(e, normal), g = d * w[e];
       c.x += g;
       c.y = __builtin_fmaf(g, h, c.y);
       dw[e] = __builtin_fmaf(d, h, dw[e]);
@@ -567,10 +677,12 @@ __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
       }
     }
     if (a.dx) {
-      const float m = c.x * a.inv_cols32, k = c.y * a.inv_cols32;
+      // rstd (g - m - h k) as g rstd - m rstd - h (k rstd)
+      const float m = -c.x * a.inv_cols32 * stat.rstd, k = -c.y * a.inv_cols32 * stat.rstd;
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (dy.get(e) * w[e] - m - xh.get(e, stat) * k) * stat.rstd;
+      for (int e = 0; e < 8; ++e)
+        x[e] = __builtin_fmaf(xh.get(e, normal), k, __builtin_fmaf(dy.get(e) * w[e], stat.rstd, m));
       store8(static_cast<S*>(a.dx) + row * static_cast<int64_t>(a.cols) + col, row < a.rows ? a.cols - col : 0, x);
     }
   }
@@ -597,6 +709,7 @@ __global__ __launch_bounds__(256) void norm_backward_long(Norm a) {
   __shared__ Pair lds[4];
   const int64_t row = blockIdx.x;
   const RowStat stat = a.stat[row];
+  const Normal normal(stat);
   Pair t = {0.0, 0.0};
   auto values = [&](int64_t col, float (&g)[8], float (&h)[8]) {
     const int64_t count = a.cols - col;
@@ -609,7 +722,7 @@ __global__ __launch_bounds__(256) void norm_backward_long(Norm a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       g[e] = a.w ? dy.get(e) * w[e] : dy.get(e);
-      h[e] = xh.get(e, stat);
+      h[e] = xh.get(e, normal);
     }
   };
   for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
@@ -642,14 +755,14 @@ __global__ __launch_bounds__(256) void norm_columns_long(Norm a, int64_t share, 
   const int64_t r0 = part * share, r1 = min(a.rows, r0 + share);
   float dw[8] = {}, db[8] = {};
   for (int64_t row = r0; row < r1; ++row) {
-    const RowStat stat = a.stat[row];
+    const Normal normal(a.stat[row]);
     Run<S> dy;
     Normalised<S, SAVED> xh;
     dy.load(static_cast<const S*>(a.dy) + row * a.ld_dy + col, count);
     xh.load(a, row, col, count);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      dw[e] = __builtin_fmaf(dy.get(e), xh.get(e, stat), dw[e]);
+      dw[e] = __builtin_fmaf(dy.get(e), xh.get(e, normal), dw[e]);
       db[e] += dy.get(e);
     }
   }
@@ -787,19 +900,19 @@ int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
 
 template <typename S, bool SAVE>
 hipError_t norm_forward(const Norm& a, hipStream_t s) {
-  const auto one = [&](auto* f, int rows_each) {
-    return launch(f, dim3(static_cast<uint32_t>((a.rows + rows_each - 1) / rows_each)), 256, s, a);
+  const auto one = [&](auto* f, int lanes) {
+    const int64_t groups = std::max(1, 256 / lanes);
+    // as many rows a workgroup as leave 2048 of them, 8 at most
+    const int32_t each = static_cast<int32_t>(std::clamp<int64_t>(a.rows / (2048 * groups), 1, 8));
+    return launch(f, dim3(static_cast<uint32_t>((a.rows + groups * each - 1) / (groups * each))), std::max(256, lanes), s, a,
+                  each);
   };
-  if (a.cols <= 512) return one(&norm_rows<S, 64, 1, SAVE>, 4);
-  if (a.cols <= 1024) return one(&norm_rows<S, 64, 2, SAVE>, 4);
-  if (a.cols <= 2048) return one(&norm_rows<S, 64, 4, SAVE>, 4);
-#ifdef NORM_WAVE
-  if (a.cols <= 4096) return one(&norm_rows<S, 64, 8, SAVE>, 4);
-#endif
-  if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 1);
-  if (a.cols <= 8192) return one(&norm_rows<S, 256, 4, SAVE>, 1);
-  if (a.cols <= 16384) return one(&norm_rows<S, 256, 8, SAVE>, 1);
-  return one(&norm_long_rows<S, SAVE>, 1);
+  if (a.cols <= 512) return one(&norm_rows<S, 64, 1, SAVE>, 64);
+  if (a.cols <= 1024) return one(&norm_rows<S, 128, 1, SAVE>, 128);
+  if (a.cols <= 2048) return one(&norm_rows<S, 256, 1, SAVE>, 256);
+  if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 256);
+  if (a.cols <= 8192) return one(&norm_rows<S, 512, 2, SAVE>, 512);
+  return launch(&norm_long_rows<S, SAVE>, dim3(static_cast<uint32_t>(a.rows)), 256, s, a);
 }
 
 template <typename S, bool SAVED>
