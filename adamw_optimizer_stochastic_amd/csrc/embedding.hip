@@ -96,49 +96,30 @@ struct Sort {
   uint32_t* keys;
   uint32_t* toks;
   uint32_t* hist;            // [digit][tile], of several tiles
-  uint8_t* touched;          // one byte an id: whether it has a token
+  uint32_t* touched;         // one bit an id: whether it has a token
   uint32_t tiles, shift, bits, passes;
 };
 
-// The rows of no token among ids [first, last): workgroup g of `groups` takes those of
-// the ids first + g + k * groups, so that neighbours in memory are written at once.
+// The rows of no token, by the flags of the ids that have one. A workgroup's lanes
+// store 8 columns each and end: workgroups in the order of memory with one store a
+// lane reach 6.8 TB/s on a table of 1 GB, with 2 to 16 stores 5.5 to 6.0, and as
+// loops over the table 4.0 to 5.5.
 struct Fill {
   void* dw;
-  int64_t dim, first, last;
-  int32_t log_lanes;
-  uint32_t groups;
+  const uint32_t* touched;   // a bit an id; NULL: no id has a token
+  int64_t vocab, dim;
+  int32_t log_lanes;         // lanes a row
+  uint32_t strips;           // of a row
 };
 
-template <typename S, typename F>
-__device__ __forceinline__ void fill_rows(const Fill& a, uint32_t g, F touched) {
-  const int lanes = 1 << a.log_lanes;
-  const int64_t lane = threadIdx.x & (lanes - 1);
-  const float zero[8] = {};
-  for (int64_t k = threadIdx.x >> a.log_lanes;; k += blockDim.x >> a.log_lanes) {
-    const int64_t v = a.first + g + k * a.groups;
-    if (v >= a.last) break;
-    if (touched(k, v)) continue;
-    S* row = static_cast<S*>(a.dw) + v * a.dim;
-    for (int64_t col = lane * 8; col < a.dim; col += lanes * 8) store8(row + col, a.dim - col, zero);
-  }
-}
-
-// The same where no flags tell which ids have a token: the workgroup marks its own
-// in LDS, reading all of the tokens, which come from L2.
-constexpr int kMarks = 32768;   // ids a workgroup looks after at most
-
 template <typename S>
-__device__ __forceinline__ void mark_and_fill(const Fill& a, const Ids& ids, uint32_t g, uint32_t* marks) {
-  for (uint32_t i = threadIdx.x; i < kMarks / 32; i += blockDim.x) marks[i] = 0;
-  __syncthreads();
-#pragma unroll 4
-  for (uint32_t i = threadIdx.x; i < ids.n; i += blockDim.x) {
-    const uint32_t at = key_at(ids, i) - static_cast<uint32_t>(a.first) - g;   // (past the range if below it)
-    const uint32_t k = at / a.groups;
-    if (k * a.groups == at && at < static_cast<uint32_t>(a.last - a.first)) atomicOr(&marks[k / 32], 1u << (k % 32));
-  }
-  __syncthreads();
-  fill_rows<S>(a, g, [&](int64_t k, int64_t) { return (marks[k / 32] >> (k % 32)) & 1u; });
+__device__ __forceinline__ void fill_rows(const Fill& a, uint32_t block) {
+  const uint32_t up = block / a.strips, strip = block - up * a.strips;
+  const int64_t v = static_cast<int64_t>(up) * (blockDim.x >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
+  const int64_t col = ((static_cast<int64_t>(strip) << a.log_lanes) + (threadIdx.x & ((1u << a.log_lanes) - 1))) * 8;
+  if (v >= a.vocab || (a.touched && ((a.touched[v / 32] >> (v % 32)) & 1u))) return;
+  const float zero[8] = {};
+  store8(static_cast<S*>(a.dw) + v * a.dim + col, a.dim - col, zero);
 }
 
 // The place of each of a tile's keys when the tile is ordered by one digit, stable.
@@ -194,15 +175,35 @@ __device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t s
   for (int r = 0; r < R; ++r) place[r] += counts[((key[r] >> shift) & mask) * 16 + wave];
 }
 
+// Which ids have one of up to 8192 tokens: a workgroup marks 2**19 ids in LDS.
+constexpr int kMarks = 1 << 19;
+
+__global__ __launch_bounds__(1024) void flag_tokens(Ids ids, uint32_t* touched) {
+  __shared__ uint32_t marks[kMarks / 32];
+  const uint32_t first = blockIdx.x * static_cast<uint32_t>(kMarks);
+  const uint32_t count = static_cast<uint32_t>(min(ids.vocab - first, int64_t{kMarks}));
+  for (uint32_t i = threadIdx.x; i < (count + 31) / 32; i += 1024) marks[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kTile / 1024; ++r) {
+    const int64_t i = r * 1024 + threadIdx.x;
+    const uint32_t at = i < ids.n ? key_at(ids, i) - first : kPast;   // (past the range if below it)
+    if (at < count) atomicOr(&marks[at / 32], 1u << (at % 32));
+  }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < (count + 31) / 32; i += 1024) touched[first / 32 + i] = marks[i];
+}
+
 // Up to 1024 R tokens, all passes, by the first workgroup, bound by the latency of
-// its steps (8192 tokens, 3 passes: 27 us). The others meanwhile write rows of no token.
+// its steps (8192 tokens, 3 passes: 27 us). The others meanwhile write the rows of
+// no token.
+// (64 registers, so that two workgroups share a compute unit.)
 template <typename S, int R>
-__global__ __launch_bounds__(1024) void sort_and_fill(Sort a, Fill fill) {
+__global__ __launch_bounds__(1024, 8) void sort_and_fill(Sort a, Fill fill) {
   __shared__ uint32_t counts[kBins * 16], totals[16], keys[R * 1024];
   __shared__ uint16_t toks[R * 1024];
-  static_assert(kBins * 16 >= kMarks / 32);
   if (blockIdx.x > 0) {
-    mark_and_fill<S>(fill, a.ids, blockIdx.x - 1, counts);
+    fill_rows<S>(fill, blockIdx.x - 1);
     return;
   }
   const uint32_t at = (threadIdx.x >> 6) * (64 * R) + (threadIdx.x & 63u);
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(1024) void count_digits(Sort a) {
     if (i < a.ids.n) {
       const uint32_t key = sort_key(a, i);
       atomicAdd(&counts[(key >> a.shift) & mask], 1u);
-      if (!a.keys_in && key < a.ids.vocab) a.touched[key] = 1;
+      if (!a.keys_in && key < a.ids.vocab) atomicOr(&a.touched[key / 32], 1u << (key % 32));
     }
   }
   __syncthreads();
@@ -317,20 +318,18 @@ __global__ __launch_bounds__(1024) void scatter_digits(Sort a) {
   }
 }
 
-__global__ __launch_bounds__(256) void clear_flags(uint8_t* touched, int64_t vocab) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < (vocab + 15) / 16; i += static_cast<int64_t>(gridDim.x) * 256)
-    reinterpret_cast<asr::u32x4*>(touched)[i] = asr::u32x4{0, 0, 0, 0};
+__global__ __launch_bounds__(256) void clear_flags(uint32_t* touched, int64_t words) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < words; i += static_cast<int64_t>(gridDim.x) * 256)
+    touched[i] = 0;
 }
 
 // ---------------------------------------------------------------- sums
 struct Sums {
   const uint32_t* keys;
   const uint32_t* toks;
-  const uint8_t* touched;    // flags of the ids with a token (of several tiles)
   const void* dy;
   void* dw;
   float* part;               // [chunk][head, tail][dim]: runs that cross a border
-  Ids ids;
   int64_t n, vocab, dim, ld;
   float scale;
   int32_t chunk;             // sorted positions a chunk, a multiple of 16
@@ -349,11 +348,8 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   constexpr int kBatch = 16, kAhead = 8, kSide = 16;
   __shared__ Run<S> rows[kAhead * 256];
   __shared__ uint32_t keys[kSide * kBatch], toks[kSide * kBatch];
-  static_assert(sizeof(rows) >= kMarks / 8);
   if (blockIdx.x >= a.sum_blocks) {
-    const uint32_t g = blockIdx.x - a.sum_blocks;
-    if (a.touched) fill_rows<S>(a.fill, g, [&](int64_t, int64_t v) { return a.touched[v] != 0; });
-    else mark_and_fill<S>(a.fill, a.ids, g, reinterpret_cast<uint32_t*>(rows));
+    fill_rows<S>(a.fill, blockIdx.x - a.sum_blocks);
     return;
   }
   const int lanes = 1 << a.log_lanes, side = 256 >> a.log_lanes;
@@ -391,9 +387,17 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
       for (int k = 0; k < kAhead; ++k) rows[k * 256 + threadIdx.x] = row[k];
       // one turn more after the last position, for the last run
       const int turns = last && half + kAhead == kBatch ? kAhead + 1 : kAhead;
+      // (keys and rows are read from LDS a turn ahead)
+      uint32_t key_next = keys[mine * kBatch + half];
+      Run<S> row_next = rows[threadIdx.x];
 #pragma unroll 1
       for (int k = 0; k < turns; ++k) {
-        const uint32_t key = k < kAhead ? keys[mine * kBatch + half + k] : kPast;
+        const uint32_t key = k < kAhead ? key_next : kPast;
+        const Run<S> r = row_next;
+        if (k + 1 < kAhead) {
+          key_next = keys[mine * kBatch + half + k + 1];
+          row_next = rows[(k + 1) * 256 + threadIdx.x];
+        }
         if (key != run) {
           if (run < vocab) {
             const bool tail = k == kAhead ? after == run : false;
@@ -411,11 +415,8 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
         }
-        if (k < kAhead) {
-          const Run<S> r = rows[k * 256 + threadIdx.x];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] += r.get(e);
-        }
+        for (int e = 0; e < 8; ++e) acc[e] += r.get(e);   // (what the turn after the last one adds, no one stores)
       }
     }
   }
@@ -423,30 +424,32 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
 
 // The runs that cross chunks: the chunk where one begins adds its tail and the
 // heads of the chunks after it, in 4 shares side by side joined in their order.
+// 256 columns a workgroup, 4 a lane.
 template <typename S>
-__global__ __launch_bounds__(1024) void join_runs(Sums a) {
-  __shared__ asr::f32x4 lds[1024];
+__global__ __launch_bounds__(256) void join_runs(Sums a) {
+  __shared__ asr::f32x4 lds[256];
   const int64_t c = blockIdx.x, i0 = c * a.chunk, i1 = i0 + a.chunk;
   if (i1 >= a.n) return;
-  const uint32_t run = a.keys[i1];
-  if (run >= a.vocab || a.keys[i1 - 1] != run) return;
-  if (i0 > 0 && a.keys[i0 - 1] == run) return;   // it began before
-  // the run starts the chunks up to hi (1024 at most are looked at, all at once)
-  const int64_t mine = c + 1 + threadIdx.x;
-  const int64_t hi = c + 1 + __syncthreads_count(mine < a.chunks && a.keys[mine * a.chunk] == run);
-  const int64_t heads = hi - (c + 1), share = threadIdx.x / 256, each = (heads + 3) / 4;
+  const uint32_t run = a.keys[i1], last = a.keys[i1 - 1], before = i0 > 0 ? a.keys[i0 - 1] : kPast;
+  if (run >= a.vocab || last != run || before == run) return;   // none crosses, or it began before
+  // the run starts the chunks up to hi (of 1024 at most, looked at 256 at once)
+  int64_t hi = c + 1;
+  for (int64_t from = hi; from == hi && from < a.chunks; from += 256) {
+    const int64_t k = from + threadIdx.x;
+    hi += __syncthreads_count(k < a.chunks && a.keys[k * a.chunk] == run);
+  }
+  const int64_t heads = hi - (c + 1), share = threadIdx.x / 64, each = (heads + 3) / 4;
   const int64_t from = c + 1 + share * each, to = min(hi, from + each);
-  const int64_t col = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x % 256) * 4;
+  const int64_t col = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x % 64 * 4;
   const int left = static_cast<int>(max(int64_t{0}, min(int64_t{4}, a.dim - col)));
   asr::f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
   auto add = [&](int64_t slot) {
     const float* p = a.part + slot * a.dim + col;
     if (left == 4) {
       t += *reinterpret_cast<const f32x4_any*>(p);
-    } else {
+    } else if (left > 0) {
 #pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (e < left) t[e] += p[e];
+      for (int e = 0; e < 3; ++e) t[e] += p[min(e, left - 1)];   // (what is past the end no one stores)
     }
   };
   if (share == 0) add(c * 2 + 1);
@@ -454,16 +457,15 @@ __global__ __launch_bounds__(1024) void join_runs(Sums a) {
   for (int64_t k = from; k < to; ++k) add(k * 2);
   lds[threadIdx.x] = t;
   __syncthreads();
-  if (share == 0) {
-    S* out = static_cast<S*>(a.dw) + static_cast<int64_t>(run) * a.dim + col;
+  if (share > 0) return;
+  S* out = static_cast<S*>(a.dw) + static_cast<int64_t>(run) * a.dim + col;
 #pragma unroll
-    for (int k = 1; k < 4; ++k) t += lds[k * 256 + threadIdx.x];
+  for (int k = 1; k < 4; ++k) t += lds[k * 64 + threadIdx.x];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e < left) {
-        if constexpr (std::is_same_v<S, float>) out[e] = t[e] * a.scale;
-        else out[e] = static_cast<uint16_t>(bf16_pair(t[e] * a.scale, 0.0f));
-      }
+  for (int e = 0; e < 4; ++e) {
+    if (e < left) {
+      if constexpr (std::is_same_v<S, float>) out[e] = t[e] * a.scale;
+      else out[e] = static_cast<uint16_t>(bf16_pair(t[e] * a.scale, 0.0f));
     }
   }
 }
@@ -482,11 +484,9 @@ bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 constexpr int64_t kMaxCols = int64_t{1} << 24;
-constexpr int64_t kMaxBytes = int64_t{1} << 39;   // of a table: fewer than 2**24 workgroups write its gradient
+constexpr int64_t kMaxBlocks = 0xFFFFFF;          // of 256 threads in a launch of fewer than 2**32
 constexpr int64_t kMaxChunks = 1024;              // of sorted tokens: what the join of one id walks
-constexpr int64_t kFillBytes = 65536;             // of a workgroup that writes rows of no token
 constexpr int64_t kCus = 256;                     // compute units of an MI355X
-constexpr int64_t kBesideSort = 16384;            // bytes written in a token's share of the sort's time
 
 template <typename... A>
 hipError_t launch(void (*f)(A...), dim3 grid, int threads, hipStream_t s, std::common_type_t<A>... args) {
@@ -519,7 +519,7 @@ struct Buffers {
   char* base;
   int64_t at = 0;
   uint32_t *keys[2], *toks[2], *hist;
-  uint8_t* touched;
+  uint32_t* touched;
   float* part;
   template <typename P>
   P* take(int64_t count) {
@@ -535,7 +535,7 @@ struct Buffers {
     keys[1] = take<uint32_t>(several ? n : 0);
     toks[1] = take<uint32_t>(several ? n : 0);
     hist = take<uint32_t>(several ? kBins * cut.tiles : 0);
-    touched = take<uint8_t>(several ? (vocab + 15) / 16 * 16 : 0);
+    touched = take<uint32_t>((vocab + 31) / 32);
     part = take<float>(static_cast<int64_t>(cut.chunks) * 2 * dim);
   }
 };
@@ -557,21 +557,21 @@ Sort sort_args(const Ids& ids, const Buffers& b) {
   a.bits = (bits + a.passes - 1) / a.passes;
   a.keys = b.keys[0];
   a.toks = b.toks[0];
+  a.touched = b.touched;
   return a;
 }
 
-// Workgroups for a range of ids: `most` of them, as long as each has 64 KB to write and
-// no more ids than it can mark.
-void share_out(Fill& fill, int64_t size, int64_t most, bool marks) {
-  const int64_t ids = fill.last - fill.first;
-  int64_t groups = std::clamp<int64_t>(ids * fill.dim * size / kFillBytes, 1, most);
-  if (marks) groups = std::max(groups, (ids + kMarks - 1) / kMarks);
-  fill.groups = ids > 0 ? static_cast<uint32_t>(groups) : 0;
+// Workgroups that write a table's rows of no token
+int64_t fill_blocks(const Fill& f, int threads) {
+  const int64_t side = threads >> f.log_lanes;
+  return (f.vocab + side - 1) / side * f.strips;
 }
 
 template <typename S>
 hipError_t sort_one_tile(const Sort& a, const Fill& fill, hipStream_t s) {
-  const dim3 grid(1 + fill.groups);
+  hipError_t e = launch(&flag_tokens, dim3(static_cast<uint32_t>((a.ids.vocab + kMarks - 1) / kMarks)), 1024, s, a.ids, a.touched);
+  if (e != hipSuccess) return e;
+  const dim3 grid(static_cast<uint32_t>(1 + fill_blocks(fill, 1024)));
   if (a.ids.n <= 1024) return launch(&sort_and_fill<S, 1>, grid, 1024, s, a, fill);
   if (a.ids.n <= 2048) return launch(&sort_and_fill<S, 2>, grid, 1024, s, a, fill);
   if (a.ids.n <= 4096) return launch(&sort_and_fill<S, 4>, grid, 1024, s, a, fill);
@@ -581,10 +581,10 @@ hipError_t sort_one_tile(const Sort& a, const Fill& fill, hipStream_t s) {
 // Several tiles: a ends with the sorted keys and tokens.
 hipError_t sort_tiles(Sort& a, const Buffers& b, const Cut& cut, hipStream_t s) {
   a.hist = b.hist;
-  a.touched = b.touched;
   a.tiles = static_cast<uint32_t>(cut.tiles);
-  hipError_t e = launch(&clear_flags, dim3(static_cast<uint32_t>(std::min<int64_t>((a.ids.vocab + 4095) / 4096, 1024))), 256, s,
-                        b.touched, a.ids.vocab);
+  const int64_t words = (a.ids.vocab + 31) / 32;
+  hipError_t e = launch(&clear_flags, dim3(static_cast<uint32_t>(std::min<int64_t>((words + 255) / 256, 1024))), 256, s,
+                        b.touched, words);
   for (uint32_t pass = 0; pass < a.passes && e == hipSuccess; ++pass) {
     a.shift = pass * a.bits;
     a.keys = b.keys[pass % 2];
@@ -649,7 +649,13 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
     return fail(ASR_EINVAL, "embedding: padding_idx must be an id of the table, or -1");
   if (vocab == 0 || dim == 0) return ok();
   const int64_t size = dtype == ASR_F32 ? 4 : 2;
-  if (vocab > kMaxBytes / (dim * size)) return fail(ASR_EINVAL, "embedding: the table is too large for one call");
+  Sums a{};
+  a.log_lanes = lanes_of(dim, 4);
+  a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
+  const int64_t side = 256 >> a.log_lanes;
+  a.fill = Fill{dtable, nullptr, vocab, dim, a.log_lanes, a.strips};
+  const int64_t filling = fill_blocks(a.fill, 256), summing = n > 0 ? (Cut(n).chunks + side - 1) / side * a.strips : 0;
+  if (filling + summing > kMaxBlocks) return fail(ASR_EINVAL, "embedding: the table is too large for one call");
   if (!dtable || (n > 0 && (!ids || !dy))) return fail(ASR_EINVAL, "embedding: null pointer");
   if (n > 0 && ld_dy < dim) return fail(ASR_EINVAL, "embedding: a row stride is below the row's length");
   if (!aligned_to(ids, ids_64 ? 8 : 4) || !aligned_to(dy, size) || !aligned_to(dtable, size))
@@ -658,7 +664,6 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
                 workspace_bytes < asr_embedding_backward_workspace_bytes(n, vocab, dim)))
     return fail(ASR_EWORKSPACE, "embedding: workspace NULL, too small or not 256-byte aligned");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  Sums a{};
   a.dy = dy;
   a.dw = dtable;
   a.n = n;
@@ -666,41 +671,31 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
   a.dim = dim;
   a.ld = ld_dy;
   a.scale = static_cast<float>(scale);
-  a.log_lanes = lanes_of(dim, 4);
-  a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
-  const int64_t side = 256 >> a.log_lanes;
-  a.fill = Fill{dtable, dim, 0, vocab, a.log_lanes, 0};
+  a.sum_blocks = static_cast<uint32_t>(summing);
   hipError_t e = hipSuccess;
+  bool filled = false;
   if (n > 0) {
     const Buffers b(workspace, n, vocab, dim);
     const Cut cut(n);
-    a.ids = Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx};
+    a.fill.touched = b.touched;
     a.part = b.part;
     a.chunk = cut.chunk;
     a.chunks = cut.chunks;
-    a.sum_blocks = static_cast<uint32_t>((cut.chunks + side - 1) / side * a.strips);
-    Sort sort = sort_args(a.ids, b);
+    Sort sort = sort_args(Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, b);
     if (cut.tiles == 1) {
-      // beside the sort as many rows as are written in its time, the others beside the sums
-      Fill first = a.fill;
-      first.last = std::min(vocab, n * kBesideSort / (dim * size));
-      a.fill.first = first.last;
-      share_out(first, size, kCus - 1, true);
-      e = dtype == ASR_F32 ? sort_one_tile<float>(sort, first, s) : sort_one_tile<uint16_t>(sort, first, s);
+      e = dtype == ASR_F32 ? sort_one_tile<float>(sort, a.fill, s) : sort_one_tile<uint16_t>(sort, a.fill, s);
+      filled = true;
     } else {
       e = sort_tiles(sort, b, cut, s);
-      a.touched = b.touched;
     }
     a.keys = sort.keys;
     a.toks = sort.toks;
   }
-  share_out(a.fill, size, n > 0 && !a.touched ? 4 * kCus : int64_t{1} << 22, !a.touched);
-  const int64_t grid = a.sum_blocks + a.fill.groups;
-  if (e == hipSuccess && grid > 0)
-    e = launch(dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>, dim3(static_cast<uint32_t>(grid)), 256, s, a);
+  if (e == hipSuccess)
+    e = launch(dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>,
+               dim3(static_cast<uint32_t>(summing + (filled ? 0 : filling))), 256, s, a);
   if (e == hipSuccess && a.chunks > 1)
-    e = launch(dtype == ASR_F32 ? &join_runs<float> : &join_runs<uint16_t>,
-               dim3(static_cast<uint32_t>(a.chunks), static_cast<uint32_t>((dim + 1023) / 1024)), 1024, s, a);
+    e = launch(dtype == ASR_F32 ? &join_runs<float> : &join_runs<uint16_t>, dim3(static_cast<uint32_t>(a.chunks), static_cast<uint32_t>((dim + 255) / 256)), 256, s, a);
   return e == hipSuccess ? ok() : hip_fail(e, "embedding launch");
 }
 

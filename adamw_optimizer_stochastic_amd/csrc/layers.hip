@@ -131,7 +131,7 @@ struct Stored {
   asr::u32x2 w;
   float s;
   __device__ __forceinline__ void load(const int8_t* q, const float* s_, bool there) {
-    w = there ? *reinterpret_cast<const asr::u32x2*>(q) : asr::u32x2{0, 0};
+    w = there ? load_stream(reinterpret_cast<const asr::u32x2*>(q)) : asr::u32x2{0, 0};
     s = there ? *s_ : 0.0f;
   }
   __device__ __forceinline__ float get(int e) const {
@@ -148,7 +148,7 @@ struct CodeLanes {
     return s.base + (p.row * s.ld + i.block) + s.lane;
   }
   __device__ __forceinline__ void store(const Item& i, const Place& p, asr::u32x2 w, float value) const {
-    if (p.padded > 0) *reinterpret_cast<asr::u32x2*>(q.at(i, p)) = w;
+    if (p.padded > 0) store_stream(reinterpret_cast<asr::u32x2*>(q.at(i, p)), w);
     if (threadIdx.x % 16 == 0 && p.count > 0) *scale(i, p) = value;
   }
   __device__ __forceinline__ Stored load(const Item& i, const Place& p) const {
@@ -413,14 +413,19 @@ __device__ __forceinline__ void add8(const float (&x)[8], int64_t count, double 
 __device__ __forceinline__ void moments(const Norm& a, Pair t, double pivot, double& mean, double& rstd) {
   const double off = t.a * a.inv_cols, var = t.b * a.inv_cols - off * off;
   mean = pivot + off;
-  rstd = 1.0 / __builtin_sqrt((var < 0.0 ? 0.0 : var) + a.eps);   // (NaN stays NaN)
+  // 1 / sqrt(v): the instruction's 2**-26 and one Newton step, a quarter of the
+  // instructions of a root and a division (v = 0, Inf and NaN give NaN, and 0
+  // times an Inf is NaN too)
+  const double v = (var < 0.0 ? 0.0 : var) + a.eps, r = __builtin_amdgcn_rsq(v);
+  rstd = __builtin_fma(r * 0.5, __builtin_fma(-v * r, r, 1.0), r);
 }
 
 // Codes of the normalised values of 8 columns, as 64 bits decide them: scale from the
 // largest |x - mean| of the block, which is that of its largest or smallest x (16
 // lanes). A code is the nearest whole number to (x - mean) (rstd / s); in 32 bits
-// that is off by less than 3e-5 (three roundings of 2**-24 of at most 127), so only a
-// wave with an element nearer than 5e-5 to a border decides in 64.
+// that is off by less than 5e-5 (five roundings of 2**-24 of at most 127, the sum's one
+// of 2**-24 of 128), so only a wave with an element nearer than 6e-5 to a border
+// decides in 64.
 __device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t count, double mean, double rstd,
                                                  const Normal& normal, float& scale) {
   constexpr float kByte = 12582912.0f;  // 1.5 * 2**23: a sum's low byte is its whole part
@@ -443,12 +448,13 @@ __device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t co
   // (a NaN or Inf in the row has made the mean one)
   const double most = __builtin_fmax(__builtin_fabs(static_cast<double>(hi) - mean),
                                      __builtin_fabs(static_cast<double>(lo) - mean));
-  const float s = static_cast<float>(most * rstd / 127.0);
+  const float s = static_cast<float>(most * rstd * (1.0 / 127.0));
   const bool finite = s < __builtin_inff();    // (false for NaN)
   const bool live = finite && s >= 0x1p-126f;
   scale = finite ? (live ? s : 0.0f) : __uint_as_float(0x7FC00000u);
-  const double turn = live ? rstd / static_cast<double>(s) : 0.0;
-  const float turn32 = static_cast<float>(turn), off = normal.off * (turn32 / normal.rstd);
+  float inv = __builtin_amdgcn_rcpf(live ? s : 1.0f);
+  inv = __builtin_fmaf(__builtin_fmaf(-s, inv, 1.0f), inv, inv);
+  const float turn32 = live ? normal.rstd * inv : 0.0f, off = normal.off * inv;
   uint32_t u[8];
   float far = 0.0f;
 #pragma unroll
@@ -458,7 +464,8 @@ __device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t co
     u[e] = __float_as_uint(v);
   }
   // (!(..): also where 32 bits overflow or have no rstd)
-  if (__builtin_amdgcn_ballot_w64(live && !(far < 0.49995f && turn32 < 0x1p100f && off == off)) != 0) {
+  if (__builtin_amdgcn_ballot_w64(live && !(far < 0.49994f && turn32 < 0x1p100f && off == off)) != 0) {
+    const double turn = live ? rstd / static_cast<double>(s) : 0.0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const double t = __builtin_rint((static_cast<double>(x[e]) - mean) * turn);
@@ -498,7 +505,7 @@ __device__ __forceinline__ void finish8(const Norm& a, int64_t row, int64_t col,
     float scale;
     const asr::u32x2 codes = norm_codes(x, count, mean, rstd, normal, scale);
     if (live && col < (static_cast<int64_t>(a.cols) + 15) / 16 * 16) {
-      *reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col) = codes;
+      store_stream(reinterpret_cast<asr::u32x2*>(a.c.q + row * a.c.ld + col), codes);
       if (threadIdx.x % 16 == 0 && count > 0) a.c.s[row * a.blocks + col / kBlockCols] = scale;
     }
   }
@@ -789,10 +796,10 @@ __global__ __launch_bounds__(1024) void norm_params(Norm a, int32_t parts) {
       t += *reinterpret_cast<const f32x4_any*>(a.part + (static_cast<int64_t>(p) * 2 + which) * a.cols + col);
   } else {
 #pragma unroll 4
-    for (int32_t p = share * each; p < p1; ++p)
+    for (int32_t p = share * each; p < (left > 0 ? p1 : 0); ++p)
 #pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (e < left) t[e] += a.part[(static_cast<int64_t>(p) * 2 + which) * a.cols + col + e];
+      for (int e = 0; e < 3; ++e)   // (past the row's end its last one again, which no one stores)
+        t[e] += a.part[(static_cast<int64_t>(p) * 2 + which) * a.cols + col + min(e, left - 1)];
   }
   lds[threadIdx.x] = t;
   __syncthreads();

@@ -15,8 +15,20 @@ typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+// Streams are read and written past the caches (non-temporal): what a pass reads
+// once need not push out what others will read again.
+// (Functions of their own for each type: a template would drop the alignment.)
+__device__ __forceinline__ asr::u32x4 load_stream(const u32x4_any* p) { return __builtin_nontemporal_load(p); }
+__device__ __forceinline__ asr::f32x4 load_stream(const f32x4_any* p) { return __builtin_nontemporal_load(p); }
+__device__ __forceinline__ asr::u32x2 load_stream(const asr::u32x2* p) { return __builtin_nontemporal_load(p); }
+__device__ __forceinline__ void store_stream(u32x4_any* p, asr::u32x4 v) { __builtin_nontemporal_store(v, p); }
+__device__ __forceinline__ void store_stream(f32x4_any* p, asr::f32x4 v) { __builtin_nontemporal_store(v, p); }
+__device__ __forceinline__ void store_stream(asr::u32x2* p, asr::u32x2 v) { __builtin_nontemporal_store(v, p); }
+
 // 8 columns of a row as they lie in memory. count: how many of them there are
-// (8 or more: all; the others read as 0).
+// (8 or more: all; the others read as 0). At a row's end the elements are loaded
+// one by one, but all at once: places past the end load the last element again,
+// as a branch for each would wait for every load by itself (5 us for 7 of them).
 template <typename S>
 struct Run;
 template <>
@@ -24,12 +36,16 @@ struct Run<uint16_t> {
   asr::u32x4 w;
   __device__ __forceinline__ void load(const uint16_t* p, int64_t count) {
     if (count >= 8) {
-      w = *reinterpret_cast<const u32x4_any*>(p);
+      w = load_stream(reinterpret_cast<const u32x4_any*>(p));
     } else {
       w = asr::u32x4{0, 0, 0, 0};
+      if (count > 0) {
+        uint32_t t[7];
 #pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e < count) w[e / 2] |= static_cast<uint32_t>(p[e]) << (e % 2 * 16);
+        for (int e = 0; e < 7; ++e) t[e] = p[min(static_cast<int>(count) - 1, e)];
+#pragma unroll
+        for (int e = 0; e < 7; ++e) w[e / 2] |= (e < count ? t[e] : 0u) << (e % 2 * 16);
+      }
     }
   }
   __device__ __forceinline__ float get(int e) const {
@@ -41,13 +57,17 @@ struct Run<float> {
   asr::f32x4 w[2];
   __device__ __forceinline__ void load(const float* p, int64_t count) {
     if (count >= 8) {
-      w[0] = reinterpret_cast<const f32x4_any*>(p)[0];
-      w[1] = reinterpret_cast<const f32x4_any*>(p)[1];
+      w[0] = load_stream(reinterpret_cast<const f32x4_any*>(p));
+      w[1] = load_stream(reinterpret_cast<const f32x4_any*>(p) + 1);
     } else {
       w[0] = w[1] = asr::f32x4{0, 0, 0, 0};
+      if (count > 0) {
+        float t[7];
 #pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e < count) w[e / 4][e % 4] = p[e];
+        for (int e = 0; e < 7; ++e) t[e] = p[min(static_cast<int>(count) - 1, e)];
+#pragma unroll
+        for (int e = 0; e < 7; ++e) w[e / 4][e % 4] = e < count ? t[e] : 0.0f;
+      }
     }
   }
   __device__ __forceinline__ float get(int e) const { return w[e / 4][e % 4]; }
@@ -61,7 +81,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 __device__ __forceinline__ void store8(uint16_t* p, int64_t count, const float (&x)[8]) {
   const asr::u32x4 w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
   if (count >= 8) {
-    *reinterpret_cast<u32x4_any*>(p) = w;
+    store_stream(reinterpret_cast<u32x4_any*>(p), w);
   } else {
 #pragma unroll
     for (int e = 0; e < 7; ++e)
@@ -71,8 +91,8 @@ __device__ __forceinline__ void store8(uint16_t* p, int64_t count, const float (
 
 __device__ __forceinline__ void store8(float* p, int64_t count, const float (&x)[8]) {
   if (count >= 8) {
-    reinterpret_cast<f32x4_any*>(p)[0] = f32x4_any{x[0], x[1], x[2], x[3]};
-    reinterpret_cast<f32x4_any*>(p)[1] = f32x4_any{x[4], x[5], x[6], x[7]};
+    store_stream(reinterpret_cast<f32x4_any*>(p), asr::f32x4{x[0], x[1], x[2], x[3]});
+    store_stream(reinterpret_cast<f32x4_any*>(p) + 1, asr::f32x4{x[4], x[5], x[6], x[7]});
   } else {
 #pragma unroll
     for (int e = 0; e < 7; ++e)

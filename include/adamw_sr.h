@@ -492,7 +492,9 @@ int asr_silu_mul_backward(const void* dy, int64_t ld_dy, const void* gate,
  * [0, vocab) gives a row of NaN and no gradient; padding_idx (-1: none) an
  * ordinary row and no gradient. table: vocab rows, ld elements apart; y and
  * dtable contiguous; dy's rows ld_dy elements apart; all of dtype.
- * Requirements: 0 <= n, vocab < 2**31; 0 <= dim <= 2**24; a table of at most 2**39 bytes;
+ * Requirements: 0 <= n, vocab < 2**31; 0 <= dim <= 2**24; a gradient of
+ * fewer than 2**24 workgroups' work (2048 columns, or rows side by side with 128
+ * columns each at least: 64 GB of bf16 rows of whole 2048 columns);
  * row strides at least dim; pointers aligned to their elements; scale finite
  * in binary32; no output overlaps an input. workspace:
  * asr_embedding_backward_workspace_bytes(n, vocab, dim) bytes of device
