@@ -7,9 +7,10 @@
 // id a pass. Ids outside the table and the padding id get the key `vocab` and end up
 // last. (2) Sorted rows are summed, `chunk` positions by one row of lanes; a run of one
 // id inside a chunk is finished there, one that crosses a chunk's border leaves
-// an f32 partial sum. (3) These are joined in order. Rows of no token, most of
-// a large table, are written beside (1) where one workgroup's LDS holds the sort
-// (up to 8192 tokens), and else beside (2). Every row of dw is written once.
+// an f32 partial sum. (3) These are joined in order. The zeros of rows without a
+// token, most of a large table, are written beside (1), over the whole table, where
+// one workgroup's LDS holds the sort (up to 8192 tokens) and the table is large for
+// its tokens; else beside (2), where flags tell which rows these are.
 #include "rows.hpp"
 #include "status.hpp"
 
@@ -96,43 +97,43 @@ struct Sort {
   uint32_t* keys;
   uint32_t* toks;
   uint32_t* hist;            // [digit][tile], of several tiles
-  uint32_t* touched;         // one bit an id: whether it has a token
+  uint32_t* flags;           // one bit an id: whether it has a token
   uint32_t tiles, shift, bits, passes;
 };
 
-// The rows of no token, by the flags of the ids that have one. A workgroup's lanes
-// store 8 columns each and end: workgroups in the order of memory with one store a
-// lane reach 6.8 TB/s on a table of 1 GB, with 2 to 16 stores 5.5 to 6.0, and as
-// loops over the table 4.0 to 5.5.
+// Zeros for the rows without a token (flags: a bit an id that has one; NULL: for all
+// rows). A workgroup's lanes store 8 columns each and end: workgroups in the order of
+// memory with one store a lane reach 7.2 TB/s on a table of 1 GB, with 2 or 4 stores
+// 6.4 and 5.8, as loops over the table 4.0 to 6.2; the wait for a flag costs a sixth.
 struct Fill {
   void* dw;
-  const uint32_t* touched;   // a bit an id; NULL: no id has a token
+  const uint32_t* flags;
   int64_t vocab, dim;
   int32_t log_lanes;         // lanes a row
   uint32_t strips;           // of a row
 };
 
-template <typename S>
+template <typename S, int THREADS>
 __device__ __forceinline__ void fill_rows(const Fill& a, uint32_t block) {
   const uint32_t up = block / a.strips, strip = block - up * a.strips;
-  const int64_t v = static_cast<int64_t>(up) * (blockDim.x >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
+  const int64_t v = static_cast<int64_t>(up) * (THREADS >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
   const int64_t col = ((static_cast<int64_t>(strip) << a.log_lanes) + (threadIdx.x & ((1u << a.log_lanes) - 1))) * 8;
-  if (v >= a.vocab || (a.touched && ((a.touched[v / 32] >> (v % 32)) & 1u))) return;
+  if (v >= a.vocab || (a.flags && ((a.flags[v / 32] >> (v % 32)) & 1u))) return;
   const float zero[8] = {};
   store8(static_cast<S*>(a.dw) + v * a.dim + col, a.dim - col, zero);
 }
 
 // The place of each of a tile's keys when the tile is ordered by one digit, stable.
-// A thread holds the keys at wave * 64 R + r * 64 + lane; counts[digit][wave]. A
+// A thread of W waves holds the keys at wave * 64 R + r * 64 + lane; counts[digit][wave]. A
 // round of 64 keys finds the lanes of its own digit by ballots, the first of
 // them adds their number to the wave's count. Ends with counts holding the
 // place of each digit's first key of each wave.
-template <int R>
+template <int W, int R>
 __device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t shift, uint32_t bits, uint32_t* counts,
                                             uint32_t* totals, uint32_t (&place)[R]) {
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, mask = (1u << bits) - 1u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) counts[i * 1024 + threadIdx.x] = 0;
+  for (int i = 0; i < 4; ++i) counts[i * 64 * W + threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -145,7 +146,7 @@ __device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t s
     }
     const uint32_t first = static_cast<uint32_t>(__builtin_ctzll(peers));
     uint32_t before = 0;
-    if (lane == first) before = atomicAdd(&counts[digit * 16 + wave], static_cast<uint32_t>(__builtin_popcountll(peers)));
+    if (lane == first) before = atomicAdd(&counts[digit * W + wave], static_cast<uint32_t>(__builtin_popcountll(peers)));
     before = static_cast<uint32_t>(__shfl(static_cast<int>(before), static_cast<int>(first)));
     place[r] = before + static_cast<uint32_t>(__builtin_popcountll(peers & ((uint64_t{1} << lane) - 1)));
   }
@@ -167,18 +168,18 @@ __device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t s
   __syncthreads();
   uint32_t base = upto - sum;
 #pragma unroll
-  for (int i = 0; i < 15; ++i) base += static_cast<uint32_t>(i) < wave ? totals[i] : 0u;
+  for (int i = 0; i < W - 1; ++i) base += static_cast<uint32_t>(i) < wave ? totals[i] : 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) counts[threadIdx.x * 4 + i] = base + c[i];
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < R; ++r) place[r] += counts[((key[r] >> shift) & mask) * 16 + wave];
+  for (int r = 0; r < R; ++r) place[r] += counts[((key[r] >> shift) & mask) * W + wave];
 }
 
 // Which ids have one of up to 8192 tokens: a workgroup marks 2**19 ids in LDS.
 constexpr int kMarks = 1 << 19;
 
-__global__ __launch_bounds__(1024) void flag_tokens(Ids ids, uint32_t* touched) {
+__global__ __launch_bounds__(1024) void flag_tokens(Ids ids, uint32_t* flags) {
   __shared__ uint32_t marks[kMarks / 32];
   const uint32_t first = blockIdx.x * static_cast<uint32_t>(kMarks);
   const uint32_t count = static_cast<uint32_t>(min(ids.vocab - first, int64_t{kMarks}));
@@ -191,19 +192,18 @@ __global__ __launch_bounds__(1024) void flag_tokens(Ids ids, uint32_t* touched) 
     if (at < count) atomicOr(&marks[at / 32], 1u << (at % 32));
   }
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < (count + 31) / 32; i += 1024) touched[first / 32 + i] = marks[i];
+  for (uint32_t i = threadIdx.x; i < (count + 31) / 32; i += 1024) flags[first / 32 + i] = marks[i];
 }
 
-// Up to 1024 R tokens, all passes, by the first workgroup, bound by the latency of
-// its steps (8192 tokens, 3 passes: 27 us). The others meanwhile write the rows of
-// no token.
-// (64 registers, so that two workgroups share a compute unit.)
-template <typename S, int R>
-__global__ __launch_bounds__(1024, 8) void sort_and_fill(Sort a, Fill fill) {
-  __shared__ uint32_t counts[kBins * 16], totals[16], keys[R * 1024];
-  __shared__ uint16_t toks[R * 1024];
+// Up to 64 W R tokens, all passes, by the first workgroup. The others meanwhile write
+// the table's zeros, 1 GB in 152 us by workgroups of 4 waves, 160 of 8, 172 of 16:
+// the sort has as few as its registers allow (32 keys a lane would be 233).
+template <typename S, int W, int R>
+__global__ __launch_bounds__(64 * W) void sort_and_fill(Sort a, Fill fill) {
+  __shared__ uint32_t counts[kBins * W], totals[W], keys[R * 64 * W];
+  __shared__ uint16_t toks[R * 64 * W];
   if (blockIdx.x > 0) {
-    fill_rows<S>(fill, blockIdx.x - 1);
+    fill_rows<S, 64 * W>(fill, blockIdx.x - 1);
     return;
   }
   const uint32_t at = (threadIdx.x >> 6) * (64 * R) + (threadIdx.x & 63u);
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(1024, 8) void sort_and_fill(Sort a, Fill fill) {
     key[r] = tok[r] < a.ids.n ? key_at(a.ids, tok[r]) : kPast;
   }
   for (uint32_t pass = 0; pass < a.passes; ++pass) {
-    tile_places<R>(key, pass * a.bits, a.bits, counts, totals, place);
+    tile_places<W, R>(key, pass * a.bits, a.bits, counts, totals, place);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       keys[place[r]] = key[r];
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(1024) void count_digits(Sort a) {
     if (i < a.ids.n) {
       const uint32_t key = sort_key(a, i);
       atomicAdd(&counts[(key >> a.shift) & mask], 1u);
-      if (!a.keys_in && key < a.ids.vocab) atomicOr(&a.touched[key / 32], 1u << (key % 32));
+      if (!a.keys_in && key < a.ids.vocab) atomicOr(&a.flags[key / 32], 1u << (key % 32));
     }
   }
   __syncthreads();
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(1024) void scatter_digits(Sort a) {
   uint32_t key[8], place[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r) key[r] = sort_key(a, start + at + r * 64);
-  tile_places<8>(key, a.shift, a.bits, counts, totals, place);
+  tile_places<16, 8>(key, a.shift, a.bits, counts, totals, place);
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
     const int64_t i = start + at + r * 64;
@@ -318,9 +318,9 @@ __global__ __launch_bounds__(1024) void scatter_digits(Sort a) {
   }
 }
 
-__global__ __launch_bounds__(256) void clear_flags(uint32_t* touched, int64_t words) {
+__global__ __launch_bounds__(256) void clear_flags(uint32_t* flags, int64_t words) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < words; i += static_cast<int64_t>(gridDim.x) * 256)
-    touched[i] = 0;
+    flags[i] = 0;
 }
 
 // ---------------------------------------------------------------- sums
@@ -349,7 +349,7 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   __shared__ Run<S> rows[kAhead * 256];
   __shared__ uint32_t keys[kSide * kBatch], toks[kSide * kBatch];
   if (blockIdx.x >= a.sum_blocks) {
-    fill_rows<S>(a.fill, blockIdx.x - a.sum_blocks);
+    fill_rows<S, 256>(a.fill, blockIdx.x - a.sum_blocks);
     return;
   }
   const int lanes = 1 << a.log_lanes, side = 256 >> a.log_lanes;
@@ -519,7 +519,7 @@ struct Buffers {
   char* base;
   int64_t at = 0;
   uint32_t *keys[2], *toks[2], *hist;
-  uint32_t* touched;
+  uint32_t* flags;
   float* part;
   template <typename P>
   P* take(int64_t count) {
@@ -535,7 +535,7 @@ struct Buffers {
     keys[1] = take<uint32_t>(several ? n : 0);
     toks[1] = take<uint32_t>(several ? n : 0);
     hist = take<uint32_t>(several ? kBins * cut.tiles : 0);
-    touched = take<uint32_t>((vocab + 31) / 32);
+    flags = take<uint32_t>((vocab + 31) / 32);
     part = take<float>(static_cast<int64_t>(cut.chunks) * 2 * dim);
   }
 };
@@ -557,7 +557,7 @@ Sort sort_args(const Ids& ids, const Buffers& b) {
   a.bits = (bits + a.passes - 1) / a.passes;
   a.keys = b.keys[0];
   a.toks = b.toks[0];
-  a.touched = b.touched;
+  a.flags = b.flags;
   return a;
 }
 
@@ -568,14 +568,14 @@ int64_t fill_blocks(const Fill& f, int threads) {
 }
 
 template <typename S>
-hipError_t sort_one_tile(const Sort& a, const Fill& fill, hipStream_t s) {
-  hipError_t e = launch(&flag_tokens, dim3(static_cast<uint32_t>((a.ids.vocab + kMarks - 1) / kMarks)), 1024, s, a.ids, a.touched);
-  if (e != hipSuccess) return e;
-  const dim3 grid(static_cast<uint32_t>(1 + fill_blocks(fill, 1024)));
-  if (a.ids.n <= 1024) return launch(&sort_and_fill<S, 1>, grid, 1024, s, a, fill);
-  if (a.ids.n <= 2048) return launch(&sort_and_fill<S, 2>, grid, 1024, s, a, fill);
-  if (a.ids.n <= 4096) return launch(&sort_and_fill<S, 4>, grid, 1024, s, a, fill);
-  return launch(&sort_and_fill<S, 8>, grid, 1024, s, a, fill);
+hipError_t sort_one_tile(const Sort& a, const Fill& fill, bool beside, hipStream_t s) {
+  const auto one = [&](auto* f, int threads) {
+    return launch(f, dim3(static_cast<uint32_t>(1 + (beside ? fill_blocks(fill, threads) : 0))), threads, s, a, fill);
+  };
+  if (a.ids.n <= 1024) return one(&sort_and_fill<S, 4, 4>, 256);
+  if (a.ids.n <= 2048) return one(&sort_and_fill<S, 4, 8>, 256);
+  if (a.ids.n <= 4096) return one(&sort_and_fill<S, 4, 16>, 256);
+  return one(&sort_and_fill<S, 8, 16>, 512);
 }
 
 // Several tiles: a ends with the sorted keys and tokens.
@@ -584,7 +584,7 @@ hipError_t sort_tiles(Sort& a, const Buffers& b, const Cut& cut, hipStream_t s) 
   a.tiles = static_cast<uint32_t>(cut.tiles);
   const int64_t words = (a.ids.vocab + 31) / 32;
   hipError_t e = launch(&clear_flags, dim3(static_cast<uint32_t>(std::min<int64_t>((words + 255) / 256, 1024))), 256, s,
-                        b.touched, words);
+                        b.flags, words);
   for (uint32_t pass = 0; pass < a.passes && e == hipSuccess; ++pass) {
     a.shift = pass * a.bits;
     a.keys = b.keys[pass % 2];
@@ -677,17 +677,23 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
   if (n > 0) {
     const Buffers b(workspace, n, vocab, dim);
     const Cut cut(n);
-    a.fill.touched = b.touched;
     a.part = b.part;
     a.chunk = cut.chunk;
     a.chunks = cut.chunks;
     Sort sort = sort_args(Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, b);
-    if (cut.tiles == 1) {
-      e = dtype == ASR_F32 ? sort_one_tile<float>(sort, a.fill, s) : sort_one_tile<uint16_t>(sort, a.fill, s);
-      filled = true;
-    } else {
+    if (cut.tiles > 1) {
       e = sort_tiles(sort, b, cut, s);
+    } else {
+      // Zeros over the whole table beside the sort, where a quarter of its rows at most
+      // are written again (128256 x 4096, 8192 tokens: 186 us, with flags 209).
+      filled = vocab >= 4 * n;
+      if (!filled)
+        e = launch(&flag_tokens, dim3(static_cast<uint32_t>((vocab + kMarks - 1) / kMarks)), 1024, s, sort.ids, b.flags);
+      if (e == hipSuccess)
+        e = dtype == ASR_F32 ? sort_one_tile<float>(sort, a.fill, filled, s)
+                             : sort_one_tile<uint16_t>(sort, a.fill, filled, s);
     }
+    a.fill.flags = b.flags;
     a.keys = sort.keys;
     a.toks = sort.toks;
   }
