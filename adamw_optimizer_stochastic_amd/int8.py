@@ -148,7 +148,7 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr", saved="
     tokens = x.numel() // k if k else x.shape[:-1].numel()
     if max(tokens, n, k) >= 1 << 17:
         raise ValueError("tokens, N and K must be below 2**17")
-    flat = x.reshape(tokens, k)
+    flat = x if x.dim() == 2 else x.reshape(tokens, k)
     if flat.numel() and (flat.stride(1) != 1 or flat.stride(0) < k):
         flat = flat.contiguous()
     if w.numel() and (w.stride(1) != 1 or w.stride(0) < k):
@@ -157,4 +157,4 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr", saved="
         raise ValueError("base_index + tokens*N exceeds 2**64")
     layer = _LinearI8Saved if saved == "i8" and n > 0 and k > 0 else _LinearI8
     y = layer.apply(flat, w, grad_rounding, key)
-    return y.reshape(*x.shape[:-1], n)
+    return y if x.dim() == 2 else y.reshape(*x.shape[:-1], n)

@@ -34,76 +34,99 @@ def _check_floats(t, name, device=None, dtype=None):
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
 
 
-def _rows(t, cols):
-    """t as a matrix of rows of `cols` contiguous elements (a copy where t's
-    strides do not allow it)."""
+def _matrix(t, cols):
+    """(tensor, rows, row stride) of t as a matrix of rows of `cols` contiguous
+    elements: t itself where it is contiguous (no view is made: each costs a
+    microsecond, and a node of autograd's graph), else a view or a copy."""
     if t.is_contiguous():
-        return t.view(-1, cols) if cols else t.reshape(t.shape[:-1].numel(), 0)
+        return t, (t.numel() // cols if cols else t.shape[:-1].numel()), max(cols, 1)
     flat = t.reshape(t.shape[:-1].numel(), cols)
     if flat.numel() and ((cols > 1 and flat.stride(1) != 1) or
                          (flat.shape[0] > 1 and flat.stride(0) < cols)):
         flat = flat.contiguous()
-    return flat
-
-
-def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    return flat, flat.shape[0], ops._row_stride(flat, cols)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+class _Codes:
+    """The buffers a pass keeps for its backward pass, in one allocation: `head`
+    bytes, then scales and codes of `count` matrices of rows x cols."""
+
+    def __init__(self, rows, cols, count, head=0):
+        self.ld = max(ops._padded16(cols), 16)
+        self.scale = head
+        self.step = ops._padded16(rows * ((cols + ops.PACK_COLUMNS - 1) // ops.PACK_COLUMNS) * 4)
+        self.codes = head + count * self.step
+        self.size = rows * self.ld
+        self.bytes = self.codes + count * self.size
+
+    def at(self, base, k):
+        """(codes, scales) of matrix k in the buffer at address base."""
+        return base + self.codes + k * self.size, base + self.scale + k * self.step
+
+
 # ---------------------------------------------------------- layer norm
 def _norm_forward(x, weight, bias, eps, keep, codes):
-    """(y, stat, q, scale) of a matrix; stat with `keep`, the codes with `codes`."""
-    (rows, cols), device = x.shape, x.device
-    y = torch.empty((rows, cols), dtype=x.dtype, device=device)
-    stat = torch.empty((rows, 4), dtype=torch.float32, device=device) if keep else None
-    q, scale = ops._code_buffers(rows, cols, device) if codes else (None, None)
+    """(y, what the backward pass needs, x as a matrix or None)."""
+    cols, device = x.shape[-1], x.device
+    flat, rows, ld = _matrix(x, cols)
+    y = torch.empty_like(x) if flat is x else torch.empty(x.shape, dtype=x.dtype, device=device)
+    buffer = stat = q = scale = None
+    ldq = 0
+    if keep:
+        layout = _Codes(rows, cols, 1 if codes else 0, 16 * rows)
+        buffer = torch.empty(layout.bytes, dtype=torch.uint8, device=device)
+        stat = buffer.data_ptr()
+        if codes:
+            (q, scale), ldq = layout.at(stat, 0), layout.ld
     param = weight if weight is not None else bias
     with ops._on(device):
         _abi.asr_layer_norm_forward(
-            x.data_ptr(), ops._DTYPE_CODE[x.dtype], ops._row_stride(x, cols), rows, cols,
-            _ptr(weight), _ptr(bias), ops._DTYPE_CODE[x.dtype if param is None else param.dtype],
-            eps, y.data_ptr(), _ptr(stat), _ptr(q), q.shape[1] if codes else 0, _ptr(scale),
-            ops._stream(device))
-    return y, stat, q, scale
+            flat.data_ptr(), ops._DTYPE_CODE[x.dtype], ld, rows, cols, _ptr(weight), _ptr(bias),
+            ops._DTYPE_CODE[x.dtype if param is None else param.dtype], eps, y.data_ptr(), stat,
+            q, ldq, scale, ops._stream(device))
+    return y, buffer, None if codes else flat
 
 
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, saved):
-        codes = saved == "i8"
-        y, stat, q, scale = _norm_forward(x, weight, bias, eps, True, codes)
-        ctx.save_for_backward(None if codes else x, weight, stat, q, scale)
+        y, buffer, flat = _norm_forward(x, weight, bias, eps, True, saved == "i8")
+        ctx.save_for_backward(flat, weight, buffer)
         ctx.bias_dtype = None if bias is None else bias.dtype
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, weight, stat, q, scale = ctx.saved_tensors
-        rows, cols = dy.shape
-        dy, device = _rows(dy, cols), dy.device
+        x, weight, buffer = ctx.saved_tensors
+        cols, device, dtype = dy.shape[-1], dy.device, dy.dtype
+        flat, rows, ld = _matrix(dy, cols)
         want_x, want_w, want_b = ctx.needs_input_grad[:3]
-        pdt = dy.dtype
-        if weight is not None or ctx.bias_dtype is not None:
-            pdt = weight.dtype if weight is not None else ctx.bias_dtype
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=device) if want_x else None
-        dw = torch.empty(cols, dtype=pdt, device=device) if want_w else None
+        pdt = weight.dtype if weight is not None else ctx.bias_dtype or dtype
+        dx = torch.empty(dy.shape, dtype=dtype, device=device) if want_x else None
+        dw = torch.empty_like(weight) if want_w else None
         db = torch.empty(cols, dtype=pdt, device=device) if want_b else None
+        stat = buffer.data_ptr()
+        x_ptr = ldx = q = scale = None
+        ldq = 0
+        if x is None:
+            layout = _Codes(rows, cols, 1, 16 * rows)
+            (q, scale), ldq = layout.at(stat, 0), layout.ld
+        else:
+            x_ptr, ldx = x.data_ptr(), cols if x.is_contiguous() else ops._row_stride(x, cols)
         need, ws = 0, None
         if want_w or want_b:
             need = _abi.asr_layer_norm_backward_workspace_bytes(rows, cols)
             ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
             _abi.asr_layer_norm_backward(
-                dy.data_ptr(), ops._row_stride(dy, cols), _ptr(x),
-                ops._row_stride(x, cols) if x is not None else 0, _ptr(q),
-                q.shape[1] if q is not None else 0, _ptr(scale), stat.data_ptr(),
-                ops._DTYPE_CODE[dy.dtype], rows, cols, _ptr(weight), ops._DTYPE_CODE[pdt],
-                _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need, ops._stream(device))
+                flat.data_ptr(), ld, x_ptr, ldx or 0, q, ldq, scale, stat, ops._DTYPE_CODE[dtype],
+                rows, cols, _ptr(weight), ops._DTYPE_CODE[pdt], _ptr(dx), _ptr(dw), _ptr(db),
+                _ptr(ws), need, ops._stream(device))
         return dx, dw, db, None, None
 
 
@@ -129,80 +152,91 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, saved="input"):
     _check_floats(x, "x")
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
-    shape, cols, device = x.shape, x.shape[-1], x.device
+    cols, device = x.shape[-1], x.device
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _check_floats(t, name, device)
             if t.dim() != 1 or t.shape[0] != cols:
                 raise ValueError(f"{name} must have shape ({cols},)")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have the same type")
-    if weight is not None and not weight.is_contiguous():
-        weight = weight.contiguous()
+    if weight is not None:
+        if bias is not None and weight.dtype != bias.dtype:
+            raise TypeError("weight and bias must have the same type")
+        if not weight.is_contiguous():
+            weight = weight.contiguous()
     if bias is not None and not bias.is_contiguous():
         bias = bias.contiguous()
-    flat = _rows(x, cols)
-    if flat.shape[0] >= 1 << 24 or cols > 1 << 24:
+    if cols > 1 << 24 or (x.numel() // cols if cols else x.shape[:-1].numel()) >= 1 << 24:
         raise ValueError("fewer than 2**24 rows and at most 2**24 columns")
-    if _wants_grad(x, weight, bias):
-        return _LayerNorm.apply(flat, weight, bias, eps, saved).reshape(shape)
-    return _norm_forward(flat, weight, bias, eps, False, False)[0].view(shape)
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                                    or (bias is not None and bias.requires_grad)):
+        return _LayerNorm.apply(x, weight, bias, eps, saved)
+    return _norm_forward(x, weight, bias, eps, False, False)[0]
 
 
 # ----------------------------------------------------------- gated SiLU
-def _halves(gate, up):
-    """(gate, up, their row strides, cols); up None: the halves of gate's columns."""
-    if up is not None:
-        cols = gate.shape[1]
-        return (gate.data_ptr(), up.data_ptr(), ops._row_stride(gate, cols),
-                ops._row_stride(up, cols), cols)
-    cols = gate.shape[1] // 2
-    ld = ops._row_stride(gate, 2 * cols)
-    return gate.data_ptr(), gate.data_ptr() + cols * gate.element_size(), ld, ld, cols
-
-
 def _silu_forward(gate, up, codes):
-    g, u, ld_g, ld_u, cols = _halves(gate, up)
-    rows, device = gate.shape[0], gate.device
-    y = torch.empty((rows, cols), dtype=gate.dtype, device=device)
-    (qg, sg), (qu, su) = ((ops._code_buffers(rows, cols, device) for _ in range(2)) if codes
-                          else ((None, None),) * 2)
+    """(y, codes' buffer or None, gate and up as matrices with their row strides)."""
+    width, device, dtype = gate.shape[-1], gate.device, gate.dtype
+    flat, rows, ld = _matrix(gate, width)
+    if up is None:   # the halves of gate's columns
+        cols, u, ld_u = width // 2, None, ld
+        g_ptr = flat.data_ptr()
+        u_ptr = g_ptr + cols * flat.element_size()
+    else:
+        cols = width
+        u, _, ld_u = _matrix(up, cols)
+        g_ptr, u_ptr = flat.data_ptr(), u.data_ptr()
+    y = torch.empty((*gate.shape[:-1], cols), dtype=dtype, device=device)
+    buffer, ldq = None, 0
+    pointers = (None,) * 4
+    if codes:
+        layout = _Codes(rows, cols, 2)
+        buffer = torch.empty(layout.bytes, dtype=torch.uint8, device=device)
+        base, ldq = buffer.data_ptr(), layout.ld
+        pointers = (*layout.at(base, 0), *layout.at(base, 1))
     with ops._on(device):
-        _abi.asr_silu_mul_forward(g, ld_g, u, ld_u, ops._DTYPE_CODE[gate.dtype], rows, cols,
-                                  y.data_ptr(), max(cols, 1), _ptr(qg), _ptr(sg), _ptr(qu),
-                                  _ptr(su), qg.shape[1] if codes else 0, ops._stream(device))
-    return y, qg, sg, qu, su
+        _abi.asr_silu_mul_forward(g_ptr, ld, u_ptr, ld_u, ops._DTYPE_CODE[dtype], rows, cols,
+                                  y.data_ptr(), max(cols, 1), *pointers, ldq,
+                                  ops._stream(device))
+    return y, buffer, flat, u, (ld, ld_u)
 
 
 class _SiluMul(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate, up, saved):
         codes = saved == "i8"
-        y, *packed = _silu_forward(gate, up, codes)
-        ctx.joint = up is None
-        ctx.save_for_backward(*((None, None) if codes else (gate, up)), *packed)
+        y, buffer, g, u, strides = _silu_forward(gate, up, codes)
+        ctx.joint, ctx.strides = up is None, strides
+        ctx.save_for_backward(None if codes else g, None if codes else u, buffer)
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        gate, up, qg, sg, qu, su = ctx.saved_tensors
-        rows, cols = dy.shape
-        dy, device = _rows(dy, cols), dy.device
+        gate, up, buffer = ctx.saved_tensors
+        cols, device, dtype = dy.shape[-1], dy.device, dy.dtype
+        flat, rows, ld = _matrix(dy, cols)
+        half = cols * flat.element_size()
         if ctx.joint:
-            dgate = torch.empty((rows, 2 * cols), dtype=dy.dtype, device=device)
-            dup = None
+            dgate = torch.empty((*dy.shape[:-1], 2 * cols), dtype=dtype, device=device)
+            dup, ld_out = None, max(2 * cols, 1)
+            out_g = dgate.data_ptr()
+            out_u = out_g + half
         else:
-            dgate, dup = (torch.empty((rows, cols), dtype=dy.dtype, device=device)
-                          for _ in range(2))
-        out_g, out_u, ld_dg, ld_du, _ = _halves(dgate, dup)
-        g, u, ld_g, ld_u = _halves(gate, up)[:4] if gate is not None else (None, None, 0, 0)
+            dgate, dup = (torch.empty(dy.shape, dtype=dtype, device=device) for _ in range(2))
+            out_g, out_u, ld_out = dgate.data_ptr(), dup.data_ptr(), max(cols, 1)
+        pointers, ldq, g, u, (ld_g, ld_u) = (None,) * 4, 0, None, None, ctx.strides
+        if buffer is not None:
+            layout = _Codes(rows, cols, 2)
+            base, ldq = buffer.data_ptr(), layout.ld
+            pointers = (*layout.at(base, 0), *layout.at(base, 1))
+        else:
+            g = gate.data_ptr()
+            u = g + half if ctx.joint else up.data_ptr()
         with ops._on(device):
-            _abi.asr_silu_mul_backward(
-                dy.data_ptr(), ops._row_stride(dy, cols), g, ld_g, u, ld_u, _ptr(qg), _ptr(sg),
-                _ptr(qu), _ptr(su), qg.shape[1] if qg is not None else 0,
-                ops._DTYPE_CODE[dy.dtype], rows, cols, out_g, ld_dg, out_u, ld_du,
-                ops._stream(device))
+            _abi.asr_silu_mul_backward(flat.data_ptr(), ld, g, ld_g, u, ld_u, *pointers, ldq,
+                                       ops._DTYPE_CODE[dtype], rows, cols, out_g, ld_out, out_u,
+                                       ld_out, ops._stream(device))
         return dgate, dup, None
 
 
@@ -223,32 +257,27 @@ def silu_mul(gate, up=None, *, saved="inputs"):
     _check_floats(gate, "gate")
     if gate.dim() < 1:
         raise ValueError("gate must have at least one dimension")
-    width = gate.shape[-1]
     if up is None:
-        if width % 2:
+        if gate.shape[-1] % 2:
             raise ValueError("without up, gate's last dimension must be even")
-        cols = width // 2
     else:
-        cols = width
         _check_floats(up, "up", gate.device, gate.dtype)
         if up.shape != gate.shape:
             raise ValueError("gate and up must have the same shape")
-    shape = (*gate.shape[:-1], cols)
-    g, u = _rows(gate, width), None if up is None else _rows(up, width)
-    if _wants_grad(gate, up):
-        return _SiluMul.apply(g, u, saved).reshape(shape)
-    return _silu_forward(g, u, False)[0].view(shape)
+    if torch.is_grad_enabled() and (gate.requires_grad or (up is not None and up.requires_grad)):
+        return _SiluMul.apply(gate, up, saved)
+    return _silu_forward(gate, up, False)[0]
 
 
 # ------------------------------------------------------------ embedding
 def _lookup(ids, weight, scale):
     (vocab, dim), device = weight.shape, weight.device
-    y = torch.empty((ids.numel(), dim), dtype=weight.dtype, device=device)
+    y = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=device)
+    table, _, ld = _matrix(weight, dim)
     with ops._on(device):
         _abi.asr_embedding_forward(ids.data_ptr(), int(ids.dtype == torch.int64), ids.numel(),
-                                   weight.data_ptr(), ops._DTYPE_CODE[weight.dtype],
-                                   ops._row_stride(weight, dim), vocab, dim, scale, y.data_ptr(),
-                                   ops._stream(device))
+                                   table.data_ptr(), ops._DTYPE_CODE[weight.dtype], ld, vocab, dim,
+                                   scale, y.data_ptr(), ops._stream(device))
     return y
 
 
@@ -264,15 +293,16 @@ class _Embedding(torch.autograd.Function):
     def backward(ctx, dy):
         ids, = ctx.saved_tensors
         (vocab, dim), scale, padding = ctx.args
-        dy, device, n = _rows(dy, dim), dy.device, ids.numel()
+        flat, n, ld = _matrix(dy, dim)
+        device = dy.device
         dw = torch.empty((vocab, dim), dtype=dy.dtype, device=device)
         need = _abi.asr_embedding_backward_workspace_bytes(n, vocab, dim)
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
             _abi.asr_embedding_backward(
-                ids.data_ptr(), int(ids.dtype == torch.int64), n, dy.data_ptr(),
-                ops._row_stride(dy, dim), ops._DTYPE_CODE[dy.dtype], vocab, dim, scale, padding,
-                dw.data_ptr(), ws.data_ptr(), need, ops._stream(device))
+                ids.data_ptr(), int(ids.dtype == torch.int64), n, flat.data_ptr(), ld,
+                ops._DTYPE_CODE[dy.dtype], vocab, dim, scale, padding, dw.data_ptr(),
+                ws.data_ptr(), need, ops._stream(device))
         return dw, None, None, None
 
 
@@ -306,13 +336,8 @@ def embedding(ids, weight, *, scale=1.0, padding_idx=None):
         if not -vocab <= padding < vocab:
             raise ValueError("padding_idx must be an id of the table")
         padding %= vocab
-    if not weight.is_contiguous():
-        weight = _rows(weight, dim)
-    flat = ids.reshape(-1)
-    if not flat.is_contiguous():
-        flat = flat.contiguous()
-    if _wants_grad(weight):
-        y = _Embedding.apply(weight, flat, scale, padding)
-    else:
-        y = _lookup(flat, weight, scale)
-    return y.view(*ids.shape, dim)
+    if not ids.is_contiguous():
+        ids = ids.contiguous()
+    if torch.is_grad_enabled() and weight.requires_grad:
+        return _Embedding.apply(weight, ids, scale, padding)
+    return _lookup(ids, weight, scale)
