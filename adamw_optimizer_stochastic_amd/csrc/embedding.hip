@@ -470,6 +470,86 @@ __global__ __launch_bounds__(256) void join_runs(Sums a) {
   }
 }
 
+// Few tokens and a small table in one launch: workgroup g of G takes the ids g, g + G,
+// ... (up to 255: frequent ids are neighbours in many vocabularies), sorts the tokens by
+// them (one digit, the others the last one), and sums and writes its rows: a row
+// of lanes each where an id has up to 16 tokens, all of them together (consecutive
+// shares, joined in their order) where it has more. Without the launches, partial sums
+// and workspace of the above.
+struct Direct {
+  Ids ids;
+  const void* dy;
+  void* dw;
+  int64_t dim, ld;
+  float scale;
+  int32_t log_lanes;         // lanes a row
+  uint32_t strips, groups;   // of a row; G
+};
+
+template <typename S>
+__global__ __launch_bounds__(1024) void sum_direct(Direct a) {
+  constexpr uint32_t kAhead = 8, kLong = 16;
+  __shared__ uint32_t counts[kBins * 16], totals[16];
+  __shared__ uint16_t toks[1024];
+  __shared__ asr::f32x4 joint[2][1024];
+  __shared__ uint32_t longs[1024 / kLong], long_count;
+  const uint32_t up = blockIdx.x / a.strips, strip = blockIdx.x - up * a.strips;
+  const uint32_t vocab = static_cast<uint32_t>(a.ids.vocab), here = (vocab - up + a.groups - 1) / a.groups;
+  const uint32_t id = threadIdx.x < a.ids.n ? key_at(a.ids, threadIdx.x) : vocab;
+  const uint32_t turn = id / a.groups;
+  uint32_t key[1] = {id < vocab && id - turn * a.groups == up ? turn : 255u}, place[1];
+  if (threadIdx.x == 0) long_count = 0;
+  tile_places<16, 1>(key, 0, 8, counts, totals, place);
+  toks[place[0]] = static_cast<uint16_t>(threadIdx.x);
+  if (threadIdx.x < here && counts[(threadIdx.x + 1) * 16] - counts[threadIdx.x * 16] > kLong)
+    longs[atomicAdd(&long_count, 1u)] = threadIdx.x;   // (in any order: each is summed by itself)
+  __syncthreads();
+  const uint32_t lanes = 1u << a.log_lanes, groups = 1024u >> a.log_lanes, group = threadIdx.x >> a.log_lanes;
+  const int64_t col = ((static_cast<int64_t>(strip) << a.log_lanes) + (threadIdx.x & (lanes - 1))) * 8;
+  const int64_t count = a.dim - col;
+  const S* dy = static_cast<const S*>(a.dy) + col;
+  auto sum = [&](uint32_t from, uint32_t to, float (&acc)[8]) {
+    for (uint32_t i = from; i < to; i += kAhead) {
+      Run<S> row[kAhead];
+#pragma unroll
+      for (uint32_t k = 0; k < kAhead; ++k)
+        row[k].load(dy + static_cast<int64_t>(toks[min(i + k, to - 1)]) * a.ld, i + k < to ? count : 0);
+#pragma unroll
+      for (uint32_t k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += row[k].get(e);
+    }
+  };
+  auto finish = [&](uint32_t v, float (&acc)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= a.scale;
+    store8(static_cast<S*>(a.dw) + static_cast<int64_t>(up + v * a.groups) * a.dim + col, count, acc);
+  };
+  for (uint32_t v = group; v < here; v += groups) {
+    const uint32_t from = counts[v * 16], to = counts[(v + 1) * 16];
+    if (to - from > kLong) continue;
+    float acc[8] = {};
+    sum(from, to, acc);
+    finish(v, acc);
+  }
+  for (uint32_t k = 0; k < long_count; ++k) {
+    const uint32_t v = longs[k], from = counts[v * 16], to = counts[(v + 1) * 16];
+    const uint32_t share = (to - from + groups - 1) / groups, mine = min(to, from + group * share);
+    float acc[8] = {};
+    sum(mine, min(to, mine + share), acc);
+    joint[0][threadIdx.x] = asr::f32x4{acc[0], acc[1], acc[2], acc[3]};
+    joint[1][threadIdx.x] = asr::f32x4{acc[4], acc[5], acc[6], acc[7]};
+    __syncthreads();
+    if (group == 0) {
+      for (uint32_t g = 1; g < groups; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += joint[e / 4][(g << a.log_lanes) + threadIdx.x][e % 4];
+      finish(v, acc);
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace asr_embed
 
 // =========================================================== host side
@@ -539,6 +619,14 @@ struct Buffers {
     part = take<float>(static_cast<int64_t>(cut.chunks) * 2 * dim);
   }
 };
+
+// Few tokens (one a thread) and a small table: one launch. (us, that and the launches above,
+// bf16: 16 tokens, 100 x 64: 5.1 and 10.5; 777, 1009 x 333: 8.6 and 24.6; 1024 of one id, 1009
+// x 512: 15.6 and 24.8; 1024, 16000 x 1024: 14.0 and 20.2; 256, 100000 x 64: 10.8 and
+// 17.1. Beyond, the order of the table's zeros counts more.)
+bool direct(int64_t n, int64_t vocab, int64_t dim) {
+  return n > 0 && n <= 1024 && vocab <= int64_t{1} << 17 && vocab * dim <= int64_t{1} << 24;
+}
 
 int check_table(int64_t n, int64_t vocab, int64_t dim, int32_t dtype) {
   if (n < 0 || n >= kMaxDim || vocab < 0 || vocab >= kMaxDim)
@@ -637,7 +725,7 @@ int asr_embedding_forward(const void* ids, int32_t ids_64, int64_t n, const void
 
 size_t asr_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
   if (n <= 0 || n >= kMaxDim || vocab <= 0 || vocab >= kMaxDim || dim <= 0 || dim > kMaxCols) return 0;
-  return static_cast<size_t>(Buffers(nullptr, n, vocab, dim).at);
+  return direct(n, vocab, dim) ? 0 : static_cast<size_t>(Buffers(nullptr, n, vocab, dim).at);
 }
 
 int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const void* dy, int64_t ld_dy, int32_t dtype,
@@ -660,10 +748,22 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
   if (n > 0 && ld_dy < dim) return fail(ASR_EINVAL, "embedding: a row stride is below the row's length");
   if (!aligned_to(ids, ids_64 ? 8 : 4) || !aligned_to(dy, size) || !aligned_to(dtable, size))
     return fail(ASR_EALIGN, "embedding: a pointer is not aligned to its elements");
-  if (n > 0 && (!workspace || !aligned_to(workspace, 256) ||
+  const bool small = direct(n, vocab, dim);
+  if (n > 0 && !small && (!workspace || !aligned_to(workspace, 256) ||
                 workspace_bytes < asr_embedding_backward_workspace_bytes(n, vocab, dim)))
     return fail(ASR_EWORKSPACE, "embedding: workspace NULL, too small or not 256-byte aligned");
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (small) {
+    Direct d{Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, dy, dtable, dim, ld_dy, static_cast<float>(scale),
+             a.log_lanes, a.strips, 1};
+    // about 512 workgroups, as long as every row of lanes has an id and none more than 255
+    const int64_t rows = 1024 >> a.log_lanes;
+    d.groups = static_cast<uint32_t>(std::max(std::min<int64_t>((vocab + rows - 1) / rows, std::max<int64_t>(512 / a.strips, 1)),
+                                              (vocab + 254) / 255));
+    const dim3 grid(d.groups * a.strips);
+    const hipError_t e = launch(dtype == ASR_F32 ? &sum_direct<float> : &sum_direct<uint16_t>, grid, 1024, s, d);
+    return e == hipSuccess ? ok() : hip_fail(e, "embedding launch");
+  }
   a.dy = dy;
   a.dw = dtable;
   a.n = n;

@@ -297,12 +297,12 @@ class _Embedding(torch.autograd.Function):
         device = dy.device
         dw = torch.empty((vocab, dim), dtype=dy.dtype, device=device)
         need = _abi.asr_embedding_backward_workspace_bytes(n, vocab, dim)
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         with ops._on(device):
             _abi.asr_embedding_backward(
                 ids.data_ptr(), int(ids.dtype == torch.int64), n, flat.data_ptr(), ld,
                 ops._DTYPE_CODE[dy.dtype], vocab, dim, scale, padding, dw.data_ptr(),
-                ws.data_ptr(), need, ops._stream(device))
+                _ptr(ws), need, ops._stream(device))
         return dw, None, None, None
 
 

@@ -498,7 +498,8 @@ int asr_silu_mul_backward(const void* dy, int64_t ld_dy, const void* gate,
  * row strides at least dim; pointers aligned to their elements; scale finite
  * in binary32; no output overlaps an input. workspace:
  * asr_embedding_backward_workspace_bytes(n, vocab, dim) bytes of device
- * memory, 256-byte aligned (0 bytes, NULL allowed, for n = 0). Errors:
+ * memory, 256-byte aligned (0 bytes, NULL allowed, for n = 0 and for up to 1024
+ * tokens of a small table). Errors:
  * ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EWORKSPACE, ASR_EHIP. Run on
  * `stream`; do not synchronize.
  */

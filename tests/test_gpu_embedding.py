@@ -83,6 +83,28 @@ def test_tokens(n, vocab):
     _check(rng.integers(0, vocab, n), vocab, 20, "f32")
 
 
+@pytest.mark.parametrize("n", [1, 255, 257, 1000, 1024, 2000, 4000, 8192, 9000])
+def test_tokens_of_a_large_vocabulary(n):
+    """More ids than a call of few tokens takes in one launch; zeros beside the sort."""
+    rng = np.random.default_rng(n)
+    ids = rng.integers(0, 140000, n)
+    ids[n // 2:] = rng.integers(0, 9, n - n // 2)
+    _check(ids, 140000, 20, "bf16", padding=3)
+
+
+@pytest.mark.parametrize("vocab,dim", [(131072, 8), (131073, 8), (255, 300), (256, 300), (300, 2600),
+                                       (70000, 30), (4096, 4096), (4097, 4096)])
+def test_few_tokens(vocab, dim):
+    """The single launch: ids shared out among workgroups, up to 255 each, runs of up to
+    16 tokens and longer ones, at its limits of vocabulary and size."""
+    rng = np.random.default_rng([vocab, dim])
+    for n in (3, 700, 1024):
+        ids = np.where(rng.random(n) < 0.5, rng.integers(0, vocab, n),
+                       np.minimum(rng.geometric(0.03, n) - 1, vocab - 1))
+        ids[:n // 10] = vocab - 1
+        _check(ids, vocab, dim, "bf16" if vocab * dim > 10 ** 6 else "f32", scale=3.0)
+
+
 @pytest.mark.parametrize("n", [300, 5000, 20000])
 @pytest.mark.parametrize("kind", ["one", "two", "blocks", "skewed", "padded", "outside", "all outside"])
 def test_repeated_and_missing_tokens(n, kind):

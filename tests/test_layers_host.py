@@ -145,13 +145,16 @@ def test_embedding_argument_errors():
     assert f(ids=0x1004) == E.ASR_EALIGN and f(ld=59) == E.ASR_EINVAL
     assert f(n=0, ids=0, table=0, y=0) == E.ASR_OK
 
-    need = E.asr_embedding_backward_workspace_bytes(8, 100, 60)
-    assert need >= 8 * 8 + 100 + 2 * 60 * 4
+    need = E.asr_embedding_backward_workspace_bytes(2000, 100, 60)
+    assert need >= 2000 * 8 + 100 // 8 + 125 * 2 * 60 * 4
     assert E.asr_embedding_backward_workspace_bytes(0, 100, 60) == 0
+    assert E.asr_embedding_backward_workspace_bytes(8, 100, 60) == 0       # few tokens, small table
+    assert E.asr_embedding_backward_workspace_bytes(1024, 1 << 17, 128) == 0
+    assert E.asr_embedding_backward_workspace_bytes(1024, (1 << 17) + 1, 128) > 0
     several = E.asr_embedding_backward_workspace_bytes(8193, 100, 60)
     assert several >= 16 * 8193 + 2 * 256 * 4 + 513 * 2 * 60 * 4
 
-    def g(ids=0x1000, wide=1, n=8, dy=0x2000, ld=60, dtype=E.ASR_BF16, vocab=100, dim=60,
+    def g(ids=0x1000, wide=1, n=2000, dy=0x2000, ld=60, dtype=E.ASR_BF16, vocab=100, dim=60,
           scale=1.0, padding=-1, dw=0x8000, ws=0x10000, ws_bytes=need):
         return _status(E.asr_embedding_backward, ids, wide, n, dy, ld, dtype, vocab, dim, scale,
                        padding, dw, ws, ws_bytes, None)
