@@ -2,12 +2,11 @@
 // product's operand, or a block of columns of a stored activation.
 //   s = f32(max|x| / 127),  q = sign(x) * min(127, Q(|x| / s)),
 // Q rounding the EXACT quotient: to nearest, ties to even, or stochastically,
-// floor(|x|/s + r16/65536). The decision needs no division: with c =
-// (k + 1) - r16/65536 (at most 24 bits, so exact in binary32), |x|/s + r16/65536
-// reaches k + 1 exactly when fma(-c, s, |x|) >= 0, and one rounding keeps a
-// sign. k comes from |x| * (1/s), off by at most one, and two such tests
-// settle it; to nearest is the same with r16 = 32768 and a step back from an
-// odd tie.
+// floor(|x|/s + r16/65536). The decision needs no division: with r = r16/65536
+// (1/2 to nearest) and m the whole number nearest to |x| * (1/s) + r, the code is
+// m or m - 1. m - r has at most 24 bits, so it is exact in binary32, and
+// |x|/s + r reaches m exactly when fma(-(m - r), s, |x|) >= 0: one rounding
+// keeps a sign. To nearest, 0 there is a tie: m - 1 if m is odd.
 #pragma once
 
 #include "device.hpp"
@@ -46,28 +45,13 @@ template <bool SR>
 __device__ __forceinline__ int32_t exact_code(float x, const GroupScale& g, uint32_t r16) {
   const float ax = __builtin_fabsf(x) * g.k;
   const float r = SR ? static_cast<float>(r16) * 0x1p-16f : 0.5f;
-  float q = __builtin_floorf(__builtin_fmaf(ax, g.inv, r));
-  if (__builtin_fmaf(-((q + 1.0f) - r), g.s, ax) >= 0.0f) {
-    q += 1.0f;
-  } else if (__builtin_fmaf(-(q - r), g.s, ax) < 0.0f) {
-    q -= 1.0f;
-  }
-  int32_t i = static_cast<int32_t>(q);
-  if constexpr (!SR) {
-    if ((i & 1) && __builtin_fmaf(-(q - 0.5f), g.s, ax) == 0.0f) i -= 1;
-  }
-  i = min(i, 127);
-  return x < 0.0f ? -i : i;
+  const float m = __builtin_rintf(__builtin_fmaf(ax, g.inv, r));
+  const float rest = __builtin_fmaf(-(m - r), g.s, ax);
+  const int32_t i = static_cast<int32_t>(m);
+  const bool down = rest < 0.0f || (!SR && rest == 0.0f && (i & 1));
+  const int32_t q = min(i - (down ? 1 : 0), 127);
+  return x < 0.0f ? -q : q;
 }
-
-// Codes of 4 elements of one group, packed. With the exact decision for every
-// element its arithmetic is what bounds the kernels, so the usual case is short: |x| * (1/s) is off by less than
-// 2.4e-5 here (the reciprocal's 2**-23 and the sum's 2**-24, of 129 at most), so a value
-// further than that from a border has its code from one multiply-add (to nearest:
-// onto 1.5 * 2**23, whose low byte is then the code; stochastic: floor of the
-// quotient plus 1 + r16/65536). A wave that has an element nearer (3e-5) than that
-// decides these exactly: 40 instructions an element instead of 6. (58.7e6 bf16 values, rows, RN: 43 us, 58 us with the
-// exact decision for all.)
 
 // Byte 0 of four words. (As asm: the compiler takes the permutes apart into
 // 16-bit shifts and merges, three times as many instructions.)
@@ -79,32 +63,38 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t u0, uint32_t u1, uint32_
   return all;
 }
 
+// Codes of 4 elements of one group, packed. With the exact decision for every
+// element its arithmetic is what bounds the kernels, so the usual case is short: |x| * (1/s) is off by less than
+// 2.4e-5 here (the reciprocal's 2**-23 and the sum's 2**-24, of 129 at most), so a value
+// further than that from a border has its code from one multiply-add (to nearest:
+// onto 1.5 * 2**23, whose low byte is then the code; stochastic: floor of the
+// quotient plus 1 + r16/65536). A wave that has an element nearer (3e-5) than that
+// decides this one of its lanes' elements exactly, 11 instructions instead of 4. (bf16
+// values equal to half the group's largest are ties but for the rounding of s, so
+// a quarter of the blocks of 128 have such an element: one test for all four
+// elements together cost a third of the instructions of a kernel of codes.)
 template <bool SR>
 __device__ __forceinline__ uint32_t codes4(const float (&x)[4], const GroupScale& g,
                                            const uint32_t (&r16)[4]) {
   constexpr float kByte = 12582912.0f;  // 1.5 * 2**23
+  // (a scaled group, k != 1, takes the exact way: its inv is that of the scaled s)
+  const float near = g.k != 1.0f ? -1.0f : 0.49997f;
   uint32_t u[4];
-  float off[4];  // distance from the middle between two borders
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
+    float off;  // from the middle between two borders
     if constexpr (SR) {
       const float one_r = __uint_as_float(0x3F800000u | (r16[e] << 7));  // 1 + r16 / 65536
       const float v = __builtin_fmaf(__builtin_fabsf(x[e]), g.inv, one_r);
       const float f = __builtin_floorf(v);
-      off[e] = (v - f) - 0.5f;
+      off = (v - f) - 0.5f;
       u[e] = __float_as_uint(__builtin_copysignf(__builtin_fminf(f - 1.0f, 127.0f), x[e]) + kByte);
     } else {
       const float t = __builtin_fmaf(x[e], g.inv, kByte);
-      off[e] = __builtin_fmaf(x[e], g.inv, -(t - kByte));
+      off = __builtin_fmaf(x[e], g.inv, -(t - kByte));
       u[e] = __float_as_uint(t);
     }
-  }
-  float most = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(off[0]), __builtin_fabsf(off[1])),
-                               __builtin_fmaxf(__builtin_fabsf(off[2]), __builtin_fabsf(off[3])));
-  // (a scaled group, k != 1, takes the exact way: its inv is that of the scaled s)
-  if (__builtin_amdgcn_ballot_w64(most > 0.49997f || g.k != 1.0f) != 0) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
+    if (__builtin_amdgcn_ballot_w64(__builtin_fabsf(off) > near) != 0)
       u[e] = static_cast<uint32_t>(exact_code<SR>(g.live ? x[e] : 0.0f, g, r16[e]));
   }
   return pack_bytes(u[0], u[1], u[2], u[3]) & g.live;
