@@ -48,7 +48,7 @@ class _LinearI8(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @ops._once
     def backward(ctx, dy):
         x, w = ctx.saved_tensors
         (t, k), n, device = x.shape, w.shape[0], x.device
@@ -90,7 +90,7 @@ class _LinearI8Saved(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @ops._once
     def backward(ctx, dy):
         q, scale, w = ctx.saved_tensors
         (t, n), k, device = dy.shape, w.shape[1], dy.device

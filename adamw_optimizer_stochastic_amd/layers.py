@@ -100,7 +100,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @ops._once
     def backward(ctx, dy):
         x, weight, buffer = ctx.saved_tensors
         cols, device, dtype = dy.shape[-1], dy.device, dy.dtype
@@ -211,7 +211,7 @@ class _SiluMul(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @ops._once
     def backward(ctx, dy):
         gate, up, buffer = ctx.saved_tensors
         cols, device, dtype = dy.shape[-1], dy.device, dy.dtype
@@ -289,7 +289,7 @@ class _Embedding(torch.autograd.Function):
         return _lookup(ids, weight, scale)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @ops._once
     def backward(ctx, dy):
         ids, = ctx.saved_tensors
         (vocab, dim), scale, padding = ctx.args

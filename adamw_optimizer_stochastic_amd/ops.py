@@ -7,6 +7,7 @@ kernels; there is no CPU path.
 """
 
 import contextlib
+import functools
 import operator
 
 import numpy as np
@@ -51,6 +52,18 @@ def _on(device):
     """A context in which `device` is the current one (no more than a
     comparison where it is already)."""
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _once(backward):
+    """torch's once_differentiable, which turns gradients off and on again in
+    every call, only where a graph of the gradients is asked for (an embedding's
+    small training pass: 89 -> 85 us)."""
+    checked = torch.autograd.function.once_differentiable(backward)
+
+    @functools.wraps(backward)
+    def run(ctx, dy):
+        return checked(ctx, dy) if torch.is_grad_enabled() else backward(ctx, dy)
+    return run
 
 
 def _uint(name, x, bits):
