@@ -166,6 +166,7 @@ def test_embedding_argument_errors():
     assert g(ws=0) == E.ASR_EWORKSPACE and g(ws=0x10010) == E.ASR_EWORKSPACE
     assert g(ws_bytes=need - 1) == E.ASR_EWORKSPACE
     assert g(vocab=2 ** 31 - 1, dim=2 ** 24, ld=2 ** 24) == E.ASR_EINVAL
+    assert g(vocab=1, n=1 << 14, dim=2 ** 24, ld=2 ** 24) == E.ASR_EINVAL   # the join's workgroups
     assert g(vocab=0, n=0, ids=0, dy=0, dw=0) == E.ASR_OK
 
 
