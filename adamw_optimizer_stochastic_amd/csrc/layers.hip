@@ -524,15 +524,19 @@ __device__ __forceinline__ void finish8(const Norm& a, int64_t row, int64_t col,
 }
 
 // Rows of up to LANES * KEEP * 8 columns, held in registers by LANES lanes; a group of
-// lanes takes `each` rows in a row with its weights and biases in registers, and loads
-// the next row before it joins the sums of this one.
-// 8192 x 4096 bf16, 134 MB: 33 us, 4.1 TB/s, where a copy of it takes 24: a row's
+// lanes takes several rows, the workgroups' number apart, with its weights and biases
+// in registers, and loads the next row before it joins the sums of this one.
+// 8192 x 4096 bf16, 134 MB: 29 us, 4.6 TB/s, where a copy of it takes 24: a row's
 // chain of load, sum over its lanes and store is what a workgroup waits for. A wave a
 // row, without a barrier, holds 64 columns a lane and takes 40 us, a workgroup of
-// 512 or 1024 lanes 32 to 47. With codes 49 us, 3.4 TB/s: beside the chain, the
-// arithmetic (64-bit sums and maxima of blocks: 14 us of it).
+// 512 lanes 37. With codes 43 us, 3.9 TB/s: beside the chain, the arithmetic (64-bit
+// sums and maxima of blocks: 14 us of it).
+
+// Waves that the registers of a SIMD hold.
+constexpr int norm_waves(int keep, bool save) { return keep == 1 ? (save ? 5 : 7) : (save ? 3 : 4); }
+
 template <typename S, int LANES, int KEEP, bool SAVE>
-__global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_rows(Norm a, int32_t each) {
+__global__ __launch_bounds__(LANES > 256 ? LANES : 256, norm_waves(KEEP, SAVE)) void norm_rows(Norm a) {
   constexpr int kThreads = LANES > 256 ? LANES : 256, kGroups = kThreads / LANES;
   __shared__ Pair lds[2][kThreads / 64];
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -550,10 +554,11 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_rows(Norm a, i
       next[v].load(x + col, live ? a.cols - col : 0);
     }
   };
-  const int64_t start = static_cast<int64_t>(blockIdx.x) * each * kGroups;
-  fetch(start + group);
-  for (int32_t i = 0; i < each; ++i) {
-    const int64_t row = start + static_cast<int64_t>(i) * kGroups + group;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups;
+  int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups;
+  fetch(first + group);
+  for (int turn = 0; first < a.rows; first += stride, turn ^= 1) {
+    const int64_t row = first + group;
     const bool live = row < a.rows;
     const double pivot = static_cast<double>(first_next.get(0));
     float x[KEEP][8];
@@ -564,9 +569,9 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_rows(Norm a, i
       for (int e = 0; e < 8; ++e) x[v][e] = next[v].get(e);
       add8(x[v], a.cols - (lane + v * LANES) * 8, pivot, t);
     }
-    if (i + 1 < each) fetch(row + kGroups);
+    if (first + stride < a.rows) fetch(row + stride);
     double mean, rstd;
-    moments(a, row_sum<LANES>(t, lds[i % 2]), pivot, mean, rstd);
+    moments(a, row_sum<LANES>(t, lds[turn]), pivot, mean, rstd);
     const RowStat stat = stat_of(mean, rstd);
     if (a.stat && live && lane == 0) a.stat[row] = stat;
 #pragma unroll
@@ -910,6 +915,7 @@ int done(hipError_t e, const char* what) { return e == hipSuccess ? ok() : hip_f
 // The largest number of workgroups whose sums the norm's backward pass joins.
 constexpr int64_t kNormGrid = 256;
 constexpr int64_t kMaxNorm = int64_t{1} << 24;   // columns of a row
+constexpr int64_t kCus = 256;                    // compute units of an MI355X
 
 int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
   if (int rc = check_size("layer_norm", rows, cols, dtype)) return rc;
@@ -921,18 +927,24 @@ int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
 
 template <typename S, bool SAVE>
 hipError_t norm_forward(const Norm& a, hipStream_t s) {
-  const auto one = [&](auto* f, int lanes) {
-    const int64_t groups = std::max(1, 256 / lanes);
-    // as many rows a workgroup as leave 2048 of them, 8 at most
-    const int32_t each = static_cast<int32_t>(std::clamp<int64_t>(a.rows / (2048 * groups), 1, 8));
-    return launch(f, dim3(static_cast<uint32_t>((a.rows + groups * each - 1) / (groups * each))), std::max(256, lanes), s, a,
-                  each);
+  const auto one = [&](auto* f, int lanes, int keep) {
+    // As many workgroups as the chip holds at once, each with the same number of rows
+    // or one fewer: 8192 x 4096 bf16 in 29 us by 1024, 33 by 2048, 37 by 1280 and 45 by
+    // 8192; with codes 43 by 768, 50 by 2048.
+    const int threads = std::max(256, lanes);
+    const int64_t groups = threads / lanes, rows = (a.rows + groups - 1) / groups;
+    const int64_t held = kCus * (4 * norm_waves(keep, SAVE) / (threads / 64)), turns = (rows + held - 1) / held;
+    return launch(f, dim3(static_cast<uint32_t>((rows + turns - 1) / turns)), threads, s, a);
   };
-  if (a.cols <= 512) return one(&norm_rows<S, 64, 1, SAVE>, 64);
-  if (a.cols <= 1024) return one(&norm_rows<S, 128, 1, SAVE>, 128);
-  if (a.cols <= 2048) return one(&norm_rows<S, 256, 1, SAVE>, 256);
-  if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 256);
-  if (a.cols <= 8192) return one(&norm_rows<S, 512, 2, SAVE>, 512);
+  if (a.cols <= 512) return one(&norm_rows<S, 64, 1, SAVE>, 64, 1);
+  if (a.cols <= 1024) return one(&norm_rows<S, 128, 1, SAVE>, 128, 1);
+  if (a.cols <= 2048) return one(&norm_rows<S, 256, 1, SAVE>, 256, 1);
+  if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 256, 2);
+  if constexpr (SAVE) {   // (4096 x 8192 bf16 51 us, 57 by 512 lanes, whose two workgroups a CU no longer holds)
+    if (a.cols <= 8192) return one(&norm_rows<S, 1024, 1, SAVE>, 1024, 1);
+  } else {
+    if (a.cols <= 8192) return one(&norm_rows<S, 512, 2, SAVE>, 512, 2);
+  }
   return launch(&norm_long_rows<S, SAVE>, dim3(static_cast<uint32_t>(a.rows)), 256, s, a);
 }
 
