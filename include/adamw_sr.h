@@ -403,8 +403,9 @@ int asr_linear_i8_backward_saved(const int8_t* q, int64_t ldq,
  * next multiple of 16; scale: rows x ceil(cols / 128) f32, contiguous.
  * Requirements: 0 <= rows < 2**31, 0 <= cols < 2**31 - 4096; ldx >= cols; ldq a
  * multiple of 16 that holds the columns up to a multiple of 16; q 16-byte
- * aligned, x and scale aligned to their elements; fewer than 2**31 times 2048
- * elements' room; base_index + rows*cols <= 2**64; no buffer overlaps another.
+ * aligned, x and scale aligned to their elements; fewer than 2**31 pieces of 2048
+ * elements (16 rows of 128 columns, to one row of 2048 where rows are that long);
+ * base_index + rows*cols <= 2**64; no buffer overlaps another.
  * Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EHIP. Run on `stream`; do not
  * synchronize.
  */

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from oracle import int8 as o8, layers as ol
-from adamw_optimizer_stochastic_amd import embedding, layer_norm, linear_i8, ops, silu_mul
+from adamw_optimizer_stochastic_amd import _abi, embedding, layer_norm, linear_i8, ops, silu_mul
 from _gpu_util import announce, gpu, require_gpu, to_host
 from test_gpu_layers import DTYPES, U, _check_norm, _close, _norm_inputs, _np, _values
 
@@ -181,3 +181,65 @@ def test_inference_gives_the_same():
         assert not got.requires_grad and torch.equal(got, want), name
         with torch.no_grad():
             assert torch.equal(f(x.clone().requires_grad_()), want), name
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(3, 7), (700, 1000), (5, 4096), (40, 5001), (3, 9001)])
+def test_outputs_in_their_inputs_place(rows, cols, dtype):
+    """The overlaps that the interface allows: y in x's, gate's or up's place, the
+    gradients of gate and up in those of dy, gate and up."""
+    announce("in place", rows, cols, dtype)
+    rng = np.random.default_rng([rows, cols])
+    a, b, c = (_values(rng, (rows, cols), DTYPES[dtype])[0] for _ in range(3))
+    w = _values(rng, (cols,), DTYPES[dtype])[0]
+    code, st = ops._DTYPE_CODE[a.dtype], ops._stream(a.device)
+    x = a.clone()
+    _abi.asr_layer_norm_forward(x.data_ptr(), code, cols, rows, cols, w.data_ptr(), None, code, 1e-5,
+                                x.data_ptr(), None, None, 0, None, st)
+    assert torch.equal(x, layer_norm(a, w))
+    want = silu_mul(a, b)
+    for place in range(2):
+        g, u = a.clone(), b.clone()
+        _abi.asr_silu_mul_forward(g.data_ptr(), cols, u.data_ptr(), cols, code, rows, cols,
+                                  (g, u)[place].data_ptr(), cols, None, None, None, None, 0, st)
+        assert torch.equal((g, u)[place], want) and torch.equal((u, g)[place], (b, a)[place])
+    leaves = [a.clone().requires_grad_(), b.clone().requires_grad_()]
+    want = torch.autograd.grad(silu_mul(*leaves), leaves, c)
+    for first, second in ((0, 1), (1, 2), (2, 0), (1, 0)):
+        t = [c.clone(), a.clone(), b.clone()]          # dy, gate, up
+        _abi.asr_silu_mul_backward(t[0].data_ptr(), cols, t[1].data_ptr(), cols, t[2].data_ptr(), cols,
+                                   None, None, None, None, 0, code, rows, cols, t[first].data_ptr(), cols,
+                                   t[second].data_ptr(), cols, st)
+        assert torch.equal(t[first], want[0]) and torch.equal(t[second], want[1])
+
+
+def test_many_layers_at_once_on_many_threads():
+    """Calls from several threads, each on a stream of its own."""
+    announce("threads")
+    import threading
+    calls = _calls(np.random.default_rng(65))
+    want = []
+    for name, f, x in calls:
+        leaf = x.clone().requires_grad_()
+        y = f(leaf)
+        want.append((y, torch.autograd.grad(y, leaf, torch.ones_like(y))[0]))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                for (name, f, x), (y0, d0) in zip(calls, want):
+                    leaf = x.detach().requires_grad_()
+                    y = f(leaf)
+                    d, = torch.autograd.grad(y, leaf, torch.ones_like(y))
+                    torch.cuda.current_stream().synchronize()
+                    if not (torch.equal(y, y0) and torch.equal(d, d0)):
+                        wrong.append(name)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not wrong and not any(t.is_alive() for t in threads)
