@@ -142,7 +142,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, saved="input"):
     saved: "input" keeps x for the backward pass; "i8" keeps the 8-bit codes of
     the normalised rows (``ops.pack_i8``'s of their 64-bit values), a half or a
     quarter of x's bytes, and takes the gradients from what they stand for. A row
-    with an Inf or NaN gives NaN. Up to 2**24 columns, fewer than 2**24 rows.
+    with an Inf or NaN gives NaN; x - mean is formed in binary32 and has to fit
+    there. Up to 2**24 columns, fewer than 2**24 rows.
     """
     if saved not in ("input", "i8"):
         raise ValueError("saved must be 'input' or 'i8'")

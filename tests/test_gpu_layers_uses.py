@@ -243,3 +243,62 @@ def test_many_layers_at_once_on_many_threads():
     for t in threads:
         t.join(60)
     assert not wrong and not any(t.is_alive() for t in threads)
+
+
+@pytest.mark.parametrize("saved", ["input", "i8"])
+@pytest.mark.parametrize("rows,cols", [(1, 64), (37, 1111), (300, 4100), (5, 9001)])
+def test_layer_norm_of_f32_with_bf16_weights(rows, cols, saved):
+    announce("layer_norm f32, bf16 weights", rows, cols, saved)
+    rng = np.random.default_rng([rows, cols])
+    (x, dy, w, b), exact = _norm_inputs(rng, rows, cols, torch.float32, torch.bfloat16, "wb")
+    leaves = [t.requires_grad_() for t in (x, w, b)]
+    y = layer_norm(*leaves, saved=saved)
+    grads = torch.autograd.grad(y, leaves, dy)
+    assert y.dtype == torch.float32 and [g.dtype for g in grads] == [t.dtype for t in leaves]
+    used = None
+    if saved == "i8":
+        used = ol.unpack(*ol.pack(ol.layer_norm(exact[0])[1])).astype(np.float64)
+    _check_norm(*exact, 1e-5, y, *grads, used)
+
+
+@pytest.mark.parametrize("saved", ["input", "i8"])
+def test_linear_of_no_tokens_and_for_some_gradients(saved):
+    announce("linear, no tokens, some gradients", saved)
+    rng = np.random.default_rng(66)
+    x, w = (_values(rng, s, torch.bfloat16)[0].requires_grad_() for s in ((40, 100), (60, 100)))
+    dy = _values(rng, (40, 60), torch.bfloat16)[0]
+    dx, dw = torch.autograd.grad(linear_i8(x, w, seed=1, saved=saved), (x, w), dy)
+    for one, want in ((x, dx), (w, dw)):
+        y = linear_i8(*(t if t is one else t.detach() for t in (x, w)), seed=1, saved=saved)
+        assert torch.equal(torch.autograd.grad(y, one, dy)[0], want)
+    strided = torch.zeros((40, 133), dtype=torch.bfloat16, device="cuda")[:, 7:107].copy_(x.detach()).requires_grad_()
+    y = linear_i8(strided, w.detach().t().contiguous().t().requires_grad_(), seed=1, saved=saved)
+    assert torch.equal(torch.autograd.grad(y, strided, dy)[0], dx)
+    none = torch.empty((0, 100), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    y = linear_i8(none, w, saved=saved)
+    dx, dw = torch.autograd.grad(y, (none, w), torch.empty_like(y))
+    assert y.shape == (0, 60) and dx.shape == (0, 100) and dw.shape == w.shape and not dw.any()
+
+
+def test_layer_norm_of_rows_far_from_zero_and_of_one_value():
+    """Means of 1e6 times the spread, constant rows, one column, and values of the
+    type's whole range (differences that stay in it)."""
+    announce("layer_norm far from zero")
+    rng = np.random.default_rng(67)
+    x = rng.standard_normal((6, 1000)).astype(np.float32)
+    x[0] += np.float32(1e6)
+    x[1] = np.float32(-3e5)
+    x[2] *= np.float32(1e37)
+    x[3] *= np.float32(1e-30)
+    x[4, 1:] = np.float32(1e-3)
+    x[5] = np.where(rng.random(1000) < 0.5, np.float32(1.5e38), np.float32(-1.5e38))
+    t = torch.from_numpy(x).cuda()
+    for saved in ("input", "i8"):
+        leaf = t.clone().requires_grad_()
+        y = layer_norm(leaf, saved=saved)
+        dy, dy64 = _values(rng, x.shape, torch.float32)
+        dx, = torch.autograd.grad(y, leaf, dy)
+        used = None
+        if saved == "i8":
+            used = ol.unpack(*ol.pack(ol.layer_norm(x.astype(np.float64))[1])).astype(np.float64)
+        _check_norm(x.astype(np.float64), dy64, None, None, 1e-5, y, dx, None, None, used)
