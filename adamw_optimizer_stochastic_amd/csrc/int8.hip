@@ -65,9 +65,9 @@ __device__ __forceinline__ const QuantJob& job_of(const QuantArgs& a) {
 // KEEP runs of 8 a lane holds stay in registers between the pass for the
 // maximum and the pass for the codes; a longer row's others are read again.
 // x and w of a linear layer, 4096 and 14336 rows of 4096 bf16 (226 MB with the
-// codes), take 49-57 us, 4.0-4.6 TB/s, 1.35 to 1.55 times a copy's time: a workgroup
+// codes), take 42-46 us, 4.9-5.4 TB/s, 1.15 to 1.25 times a copy's time: a workgroup
 // holds one row from its load through two reductions to its store, with no other
-// in flight. 14336 rows alone: 37-41 us to nearest, 53-58 stochastic (the random
+// in flight. 14336 rows alone: 37-40 us to nearest, 54 stochastic (the random
 // bits). One row of 4096 takes 3 us, its latency.
 template <typename S, bool SR, int LANES>
 __global__ __launch_bounds__(256) void quantize_rows(QuantArgs args) {
@@ -211,7 +211,9 @@ __global__ __launch_bounds__(256) void join_strips(uint32_t* part, int32_t rows,
 // columns, 101 MB in and out, in 38 us (2.6 TB/s), of which the 8.4e6 Philox
 // calls, 20 quarter-rate 64-bit multiply-adds each, come to about 25. A
 // linear layer's backward (dy 4096 x 14336 both ways, x 4096 x 4096 and w 14336 x
-// 4096 by columns; 460 MB) takes 153-178 us.
+// 4096 by columns; 460 MB) takes 153-178 us. With a weight a row (WEIGH: dy times its
+// tokens' scales, without x) 128-147 us: the weights come from LDS and three waves a
+// SIMD are asked for, 152 us before the shorter codes; in registers, two waves, 203.
 struct TileLds {
   uint32_t tile[64 * 33];  // 33 words a column: 32 and one against bank conflicts
   uint32_t tops[256];
