@@ -1187,7 +1187,8 @@ static int linear_backward(const uint16_t* x, int64_t ldx, const int8_t* q, int6
   if (tokens == 0 || n == 0) {  // empty sums
     asr_i8::GemmArgs g = tokens == 0 ? gemm_args(nullptr, 16, nullptr, 16, nullptr, nullptr, dw, lddw, nullptr, n, k, 0)
                                      : gemm_args(nullptr, 16, nullptr, 16, nullptr, nullptr, dx, lddx, nullptr, tokens, k, 0);
-    if (g.c && g.m > 0) e = launch(&asr_i8::clear, std::min<int64_t>((static_cast<int64_t>(g.m) * g.n + 255) / 256, 65536), 256, &g, s);
+    if (g.c && g.m > 0)
+      e = launch(&asr_i8::clear, std::min<int64_t>((static_cast<int64_t>(g.m) * g.n + 255) / 256, 65536), 256, &g, s);
     return e == hipSuccess ? ok() : hip_fail(e, "linear_i8 launch");
   }
   if (!workspace || !aligned_to(workspace, 256) ||
