@@ -582,39 +582,51 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256, norm_waves(KEEP, SAVE)) 
   }
 }
 
-// Longer rows: a workgroup each, read twice (the second time mostly from the caches).
-template <typename S, bool SAVE>
-__global__ __launch_bounds__(256) void norm_long_rows(Norm a) {
-  __shared__ Pair lds[4];
+// Longer rows: a workgroup each, read twice (the second time mostly from the caches), two
+// runs of a lane at once. Bound by the chain of a row's loads, sums and stores: 2048 x
+// 16384 bf16, 134 MB, in 38 us, 3.5 TB/s.
+template <typename S, bool SAVE, int LANES>
+__global__ __launch_bounds__(LANES) void norm_long_rows(Norm a) {
+  constexpr int kCols = LANES * 8;
+  __shared__ Pair lds[LANES / 64];
   const int64_t row = blockIdx.x;
   const S* x = static_cast<const S*>(a.x) + row * a.ldx;
-  auto values = [&](int64_t col, float (&v)[8]) {
-    Run<S> raw;
-    raw.load(x + col, a.cols - col);
+  Run<S> raw[2];
+  auto fetch = [&](int64_t col) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = raw.get(e);
+    for (int u = 0; u < 2; ++u) raw[u].load(x + col + u * kCols, a.cols - col - u * kCols);
   };
-  Run<S> first;
-  first.load(x, 1);
-  const double pivot = static_cast<double>(first.get(0));
+  raw[0].load(x, 1);
+  const double pivot = static_cast<double>(raw[0].get(0));
   Pair t = {0.0, 0.0};
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
-    float v[8];
-    values(col, v);
-    add8(v, a.cols - col, pivot, t);
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2 * kCols) {
+    fetch(col);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = raw[u].get(e);
+      add8(v, a.cols - col - u * kCols, pivot, t);
+    }
   }
   double mean, rstd;
-  moments(a, row_sum<256>(t, lds), pivot, mean, rstd);
+  moments(a, row_sum<LANES>(t, lds), pivot, mean, rstd);
   const RowStat stat = stat_of(mean, rstd);
   if (a.stat && threadIdx.x == 0) a.stat[row] = stat;
   // (all lanes in every turn: the codes' reduction wants them active)
-  for (int64_t start = 0; start < a.cols; start += 2048) {
+  for (int64_t start = 0; start < a.cols; start += 2 * kCols) {
     const int64_t col = start + threadIdx.x * 8;
-    float v[8];
-    Affine p;
-    p.load(a, col);
-    values(col, v);
-    finish8<S, SAVE>(a, row, col, a.cols - col, true, v, mean, rstd, stat, p);
+    fetch(col);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t c = col + u * kCols;
+      float v[8];
+      Affine p;
+      p.load(a, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = raw[u].get(e);
+      finish8<S, SAVE>(a, row, c, a.cols - c, true, v, mean, rstd, stat, p);
+    }
   }
 }
 
@@ -730,67 +742,88 @@ __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
   if (a.db) finish(db, a.db, 1);
 }
 
-// Longer rows: dx by a workgroup a row, in two passes over it.
-template <typename S, bool SAVED>
-__global__ __launch_bounds__(256) void norm_backward_long(Norm a) {
-  __shared__ Pair lds[4];
+// Longer rows: dx by a workgroup a row, in two passes over it, two runs of a lane at once:
+// 2048 x 16384 bf16 in 60 us, and the sums below in 28. Dx and sums each read all of dy and
+// x, where a shorter row's are read once: three times the floor, for widths that are rare.
+template <typename S, bool SAVED, int LANES>
+__global__ __launch_bounds__(LANES) void norm_backward_long(Norm a) {
+  constexpr int kCols = LANES * 8;
+  __shared__ Pair lds[LANES / 64];
   const int64_t row = blockIdx.x;
   const RowStat stat = a.stat[row];
   const Normal normal(stat);
-  Pair t = {0.0, 0.0};
-  auto values = [&](int64_t col, float (&g)[8], float (&h)[8]) {
-    const int64_t count = a.cols - col;
-    Run<S> dy;
-    Normalised<S, SAVED> xh;
-    dy.load(static_cast<const S*>(a.dy) + row * a.ld_dy + col, count);
-    xh.load(a, row, col, count);
-    float w[8];
-    if (a.w) load_params(a.w, a.w_bf16, col, count, w);
+  Run<S> dy[2];
+  Normalised<S, SAVED> xh[2];
+  float w[2][8];
+  auto fetch = [&](int64_t col) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      g[e] = a.w ? dy.get(e) * w[e] : dy.get(e);
-      h[e] = xh.get(e, normal);
+    for (int u = 0; u < 2; ++u) {
+      const int64_t c = col + u * kCols, count = a.cols - c;
+      dy[u].load(static_cast<const S*>(a.dy) + row * a.ld_dy + c, count);
+      xh[u].load(a, row, c, count);
+      if (a.w) load_params(a.w, a.w_bf16, c, count, w[u]);
     }
   };
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
-    float g[8], h[8];
-    values(col, g, h);
+  if (!a.w) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      t.a += static_cast<double>(g[e]);
-      t.b = __builtin_fma(static_cast<double>(g[e]), static_cast<double>(h[e]), t.b);
-    }
+    for (int e = 0; e < 8; ++e) w[0][e] = w[1][e] = 1.0f;
   }
-  t = row_sum<256>(t, lds);
+  Pair t = {0.0, 0.0};
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2 * kCols) {
+    fetch(col);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {   // (past the row's end dy is 0)
+        const float g = dy[u].get(e) * w[u][e], h = xh[u].get(e, normal);
+        t.a += static_cast<double>(g);
+        t.b = __builtin_fma(static_cast<double>(g), static_cast<double>(h), t.b);
+      }
+  }
+  t = row_sum<LANES>(t, lds);
   const float m = static_cast<float>(t.a * a.inv_cols), k = static_cast<float>(t.b * a.inv_cols);
   S* out = static_cast<S*>(a.dx) + row * static_cast<int64_t>(a.cols);
-  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2048) {
-    float g[8], h[8], x[8];
-    values(col, g, h);
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 2 * kCols) {
+    fetch(col);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (g[e] - m - h[e] * k) * stat.rstd;
-    store8(out + col, a.cols - col, x);
+    for (int u = 0; u < 2; ++u) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (dy[u].get(e) * w[u][e] - m - xh[u].get(e, normal) * k) * stat.rstd;
+      store8(out + col + u * kCols, a.cols - col - u * kCols, x);
+    }
   }
 }
 
-// And their sums over rows: a workgroup takes 2048 columns of a share of the rows.
+// And their sums over rows: a workgroup takes 2048 columns of a share of the rows, four
+// rows at once.
 template <typename S, bool SAVED>
 __global__ __launch_bounds__(256) void norm_columns_long(Norm a, int64_t share, int32_t strips) {
+  constexpr int kAhead = 4;
   const int32_t strip = blockIdx.x % strips, part = blockIdx.x / strips;
   const int64_t col = (static_cast<int64_t>(strip) * 256 + threadIdx.x) * 8, count = a.cols - col;
   if (count <= 0) return;
   const int64_t r0 = part * share, r1 = min(a.rows, r0 + share);
   float dw[8] = {}, db[8] = {};
-  for (int64_t row = r0; row < r1; ++row) {
-    const Normal normal(a.stat[row]);
-    Run<S> dy;
-    Normalised<S, SAVED> xh;
-    dy.load(static_cast<const S*>(a.dy) + row * a.ld_dy + col, count);
-    xh.load(a, row, col, count);
+  for (int64_t row = r0; row < r1; row += kAhead) {
+    Run<S> dy[kAhead];
+    Normalised<S, SAVED> xh[kAhead];
+    RowStat stat[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dw[e] = __builtin_fmaf(dy.get(e), xh.get(e, normal), dw[e]);
-      db[e] += dy.get(e);
+    for (int u = 0; u < kAhead; ++u) {
+      const bool in = row + u < r1;
+      stat[u] = in ? a.stat[row + u] : RowStat{0.0f, 0.0f, 0.0f, 0.0f};
+      dy[u].load(static_cast<const S*>(a.dy) + (row + u) * a.ld_dy + col, in ? count : 0);
+      xh[u].load(a, row + u, col, in ? count : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const Normal normal(stat[u]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw[e] = __builtin_fmaf(dy[u].get(e), xh[u].get(e, normal), dw[e]);
+        db[e] += dy[u].get(e);
+      }
     }
   }
   float* out = a.part + static_cast<int64_t>(part) * 2 * a.cols + col;
@@ -916,6 +949,10 @@ int done(hipError_t e, const char* what) { return e == hipSuccess ? ok() : hip_f
 constexpr int64_t kNormGrid = 256;
 constexpr int64_t kMaxNorm = int64_t{1} << 24;   // columns of a row
 constexpr int64_t kCus = 256;                    // compute units of an MI355X
+// Rows of more than 8192 columns from which a workgroup has 256 lanes, not 1024, as several
+// of these share a compute unit: 4096 x 8200 bf16 forward 43 and 52 us, with codes 60 and
+// 96; below it the row's own time counts: 64 x 131072 80 and 34, 512 x 16384 15.5 and 11.9.
+constexpr int64_t kManyLong = 1024;
 
 int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
   if (int rc = check_size("layer_norm", rows, cols, dtype)) return rc;
@@ -945,7 +982,9 @@ hipError_t norm_forward(const Norm& a, hipStream_t s) {
   } else {
     if (a.cols <= 8192) return one(&norm_rows<S, 512, 2, SAVE>, 512, 2);
   }
-  return launch(&norm_long_rows<S, SAVE>, dim3(static_cast<uint32_t>(a.rows)), 256, s, a);
+  const dim3 grid(static_cast<uint32_t>(a.rows));
+  return a.rows < kManyLong ? launch(&norm_long_rows<S, SAVE, 1024>, grid, 1024, s, a)
+                            : launch(&norm_long_rows<S, SAVE, 256>, grid, 256, s, a);
 }
 
 template <typename S, bool SAVED>
@@ -967,7 +1006,10 @@ hipError_t norm_back(Norm a, hipStream_t s) {
   else if (a.cols <= 4096) one(&norm_backward<S, SAVED, 512>, 2);
   else if (a.cols <= 8192) one(&norm_backward<S, SAVED, 1024>, 1);
   else {
-    if (a.dx) e = launch(&norm_backward_long<S, SAVED>, dim3(static_cast<uint32_t>(a.rows)), 256, s, a);
+    const dim3 grid(static_cast<uint32_t>(a.rows));
+    if (a.dx)
+      e = a.rows < kManyLong ? launch(&norm_backward_long<S, SAVED, 1024>, grid, 1024, s, a)
+                             : launch(&norm_backward_long<S, SAVED, 256>, grid, 256, s, a);
     if (e == hipSuccess && sums) {
       parts = std::min<int64_t>(a.rows, kNormGrid);
       const int64_t share = (a.rows + parts - 1) / parts;

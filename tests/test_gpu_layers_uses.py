@@ -302,3 +302,20 @@ def test_layer_norm_of_rows_far_from_zero_and_of_one_value():
         if saved == "i8":
             used = ol.unpack(*ol.pack(ol.layer_norm(x.astype(np.float64))[1])).astype(np.float64)
         _check_norm(x.astype(np.float64), dy64, None, None, 1e-5, y, dx, None, None, used)
+
+
+@pytest.mark.parametrize("saved", ["input", "i8"])
+@pytest.mark.parametrize("rows,cols", [(1023, 8200), (1024, 8200), (1030, 9001), (3, 16385), (2, 40007), (1, 200000)])
+def test_layer_norm_of_long_rows(rows, cols, saved):
+    """Both numbers of lanes, rows that end in a lane's first and second run. (depth:
+    four rows a share, 64 shares of 4; a row's sums are in 64 bits.)"""
+    announce("layer_norm long rows", rows, cols, saved)
+    rng = np.random.default_rng([rows, cols])
+    (x, dy, w, b), exact = _norm_inputs(rng, rows, cols, torch.bfloat16, torch.bfloat16, "wb")
+    leaves = [t.requires_grad_() for t in (x, w, b)]
+    y = layer_norm(*leaves, saved=saved)
+    grads = torch.autograd.grad(y, leaves, dy)
+    used = None
+    if saved == "i8":
+        used = ol.unpack(*ol.pack(ol.layer_norm(exact[0])[1])).astype(np.float64)
+    _check_norm(*exact, 1e-5, y, *grads, used)
