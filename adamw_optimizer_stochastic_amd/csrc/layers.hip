@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void pack(Pack a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const Place p = place_of(a.g, i, spot, u);
-      raw[u].load(x.at(i, p), p.count);
+      raw[u].load_once(x.at(i, p), p.count);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -261,8 +261,8 @@ __global__ __launch_bounds__(256) void silu_forward(Silu a) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const Place p = place_of(a.g, i, spot, k);
-      rg[k].load(gate.at(i, p), p.count);
-      ru[k].load(up.at(i, p), p.count);
+      rg[k].load_once(gate.at(i, p), p.count);
+      ru[k].load_once(up.at(i, p), p.count);
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -302,13 +302,13 @@ __global__ __launch_bounds__(256) void silu_backward(Silu a) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const Place p = place_of(a.g, i, spot, k);
-      rd[k].load(dy.at(i, p), p.count);
+      rd[k].load_once(dy.at(i, p), p.count);
       if constexpr (SAVED) {
         rg[k] = cg.load(i, p);
         ru[k] = cu.load(i, p);
       } else {
-        rg[k].load(gate.at(i, p), p.count);
-        ru[k].load(up.at(i, p), p.count);
+        rg[k].load_once(gate.at(i, p), p.count);
+        ru[k].load_once(up.at(i, p), p.count);
       }
     }
 #pragma unroll
