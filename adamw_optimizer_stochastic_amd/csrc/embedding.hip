@@ -59,7 +59,7 @@ struct Lookup {
 
 // Rows of up to 8 << log_lanes columns side by side, U rows of a lane loaded
 // together; an id outside the table gives NaN. Bound by memory: 8192 rows of 4096
-// bf16, 134 MB, in 25 us, 5.3 TB/s (an id's load comes before its row's, which 4 rows
+// bf16, 134 MB, in 22 us, 6.1 TB/s (an id's load comes before its row's, which 4 rows
 // at once hide); 16 rows 3 us, the two loads' latency.
 template <typename S, int U>
 __global__ __launch_bounds__(256) void lookup(Lookup a) {
@@ -344,7 +344,7 @@ struct Sums {
 // keys and tokens go to LDS (one wait for all), then their rows, 8 at once, which each
 // lane puts into its own part of LDS: the loop over the runs then has one copy of its
 // code for all of them (unrolled over rows in registers it was 22 KB, and fetching it
-// was most of a small call's time). 8192 tokens of 4096 bf16, 134 MB: 24 us, 5.6 TB/s.
+// was most of a small call's time). 8192 tokens of 4096 bf16, 134 MB: 21 us, 6.4 TB/s.
 template <typename S>
 __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   constexpr int kBatch = 16, kAhead = 8, kSide = 16;
@@ -791,7 +791,8 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
       e = sort_tiles(sort, b, cut, s);
     } else {
       // Zeros over the whole table beside the sort, where a quarter of its rows at most
-      // are written again (128256 x 4096, 8192 tokens: 189 us, with flags 209).
+      // are written again (128256 x 4096, 8192 tokens: 189 us, with flags 209;
+      // 182 since the gradients' rows come through the caches).
       filled = vocab >= 4 * n;
       if (!filled)
         e = launch(&flag_tokens, dim3(static_cast<uint32_t>((vocab + kMarks - 1) / kMarks)), 1024, s, sort.ids, b.flags);

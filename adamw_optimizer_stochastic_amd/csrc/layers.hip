@@ -526,11 +526,11 @@ __device__ __forceinline__ void finish8(const Norm& a, int64_t row, int64_t col,
 // Rows of up to LANES * KEEP * 8 columns, held in registers by LANES lanes; a group of
 // lanes takes several rows, the workgroups' number apart, with its weights and biases
 // in registers, and loads the next row before it joins the sums of this one.
-// 8192 x 4096 bf16, 134 MB: 29 us, 4.6 TB/s, where a copy of it takes 24: a row's
-// chain of load, sum over its lanes and store is what a workgroup waits for. A wave a
-// row, without a barrier, holds 64 columns a lane and takes 40 us, a workgroup of
-// 512 lanes 37. With codes 43 us, 3.9 TB/s: beside the chain, the arithmetic (64-bit
-// sums and maxima of blocks: 14 us of it).
+// 8192 x 4096 bf16, 134 MB: 25 us, 5.4 TB/s, where a copy of it takes 22-24: a row's
+// chain of load, sum over its lanes and store is what a workgroup waits for. (Past the
+// caches 29 us, by 512 lanes 37, by a wave a row, without a barrier but with 64
+// columns a lane, 40.) With codes 38-40 us, 4.3 TB/s: beside the chain, the arithmetic
+// (64-bit sums and maxima of blocks: 14 us of it).
 
 // Waves that the registers of a SIMD hold.
 constexpr int norm_waves(int keep, bool save) { return keep == 1 ? (save ? 5 : 7) : (save ? 3 : 4); }
@@ -584,7 +584,7 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256, norm_waves(KEEP, SAVE)) 
 
 // Longer rows: a workgroup each, read twice (the second time mostly from the caches), two
 // runs of a lane at once. Bound by the chain of a row's loads, sums and stores: 2048 x
-// 16384 bf16, 134 MB, in 38 us, 3.5 TB/s.
+// 16384 bf16, 134 MB, in 30 us, 4.4 TB/s.
 template <typename S, bool SAVE, int LANES>
 __global__ __launch_bounds__(LANES) void norm_long_rows(Norm a) {
   constexpr int kCols = LANES * 8;
@@ -658,8 +658,9 @@ __device__ __forceinline__ void store_param(void* p, bool bf16, int64_t i, float
 // next row is loaded while this one is worked on, and one barrier a row joins
 // the waves' sums (two sets of them in turn). In the end the groups' sums meet
 // in LDS. (16 columns a lane would take more registers than 16 waves have.)
-// 8192 x 4096 bf16, 201 MB: 43 us, 4.7 TB/s, with the join below; from codes, 168 MB,
-// 38 us; dx alone 35. Bound by memory and, every row, the barrier's wait.
+// 8192 x 4096 bf16, 201 MB: 43 us, 4.6 TB/s, with the join below; from codes, 168 MB,
+// 35 us; dx alone 36. Bound by memory and, every row, the barrier's wait. Rows of odd
+// width 63 us (8192 x 4091): loads from odd addresses take the vector memory twice as long.
 template <typename S, bool SAVED, int LANES>
 __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
   constexpr int kGroups = 1024 / LANES, kWaves = LANES / 64, kCols = LANES * 8;
@@ -743,7 +744,7 @@ __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
 }
 
 // Longer rows: dx by a workgroup a row, in two passes over it, two runs of a lane at once:
-// 2048 x 16384 bf16 in 60 us, and the sums below in 28. Dx and sums each read all of dy and
+// 2048 x 16384 bf16 with the sums below and their join in 88 us. Dx and sums each read all of dy and
 // x, where a shorter row's are read once: three times the floor, for widths that are rare.
 template <typename S, bool SAVED, int LANES>
 __global__ __launch_bounds__(LANES) void norm_backward_long(Norm a) {
@@ -950,7 +951,7 @@ constexpr int64_t kNormGrid = 256;
 constexpr int64_t kMaxNorm = int64_t{1} << 24;   // columns of a row
 constexpr int64_t kCus = 256;                    // compute units of an MI355X
 // Rows of more than 8192 columns from which a workgroup has 256 lanes, not 1024, as several
-// of these share a compute unit: 4096 x 8200 bf16 forward 43 and 52 us, with codes 60 and
+// of these share a compute unit: (loads past the caches) 4096 x 8200 bf16 forward 43 and 52 us, with codes 60 and
 // 96; below it the row's own time counts: 64 x 131072 80 and 34, 512 x 16384 15.5 and 11.9.
 constexpr int64_t kManyLong = 1024;
 
@@ -966,7 +967,7 @@ template <typename S, bool SAVE>
 hipError_t norm_forward(const Norm& a, hipStream_t s) {
   const auto one = [&](auto* f, int lanes, int keep) {
     // As many workgroups as the chip holds at once, each with the same number of rows
-    // or one fewer: 8192 x 4096 bf16 in 29 us by 1024, 33 by 2048, 37 by 1280 and 45 by
+    // or one fewer: (loads past the caches) 8192 x 4096 bf16 in 29 us by 1024, 33 by 2048, 37 by 1280 and 45 by
     // 8192; with codes 43 by 768, 50 by 2048.
     const int threads = std::max(256, lanes);
     const int64_t groups = threads / lanes, rows = (a.rows + groups - 1) / groups;
