@@ -51,6 +51,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _kept_matrix(t, like, rows, cols):
+    """(tensor, row stride) of a matrix that a pass kept, as it comes back from
+    autograd: hooks on saved tensors (offloading, compression) may give it another
+    layout, so what the forward pass knew of its strides no longer holds."""
+    if t.device != like.device or t.dtype != like.dtype or t.shape[-1:] != (cols,) or \
+            t.numel() != rows * cols:
+        raise RuntimeError(f"a saved tensor came back as {t.dtype} {tuple(t.shape)} on {t.device}, "
+                           f"not as {like.dtype} (..., {cols}) of {rows} rows on {like.device}")
+    flat, _, ld = _matrix(t, cols)
+    return flat, ld
+
+
 class _Codes:
     """The buffers a pass keeps for its backward pass, in one allocation: `head`
     bytes, then scales and codes of `count` matrices of rows x cols."""
@@ -176,7 +188,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, saved="input"):
 
 # ----------------------------------------------------------- gated SiLU
 def _silu_forward(gate, up, codes):
-    """(y, codes' buffer or None, gate and up as matrices with their row strides)."""
+    """(y, codes' buffer or None, gate and up as matrices)."""
     width, device, dtype = gate.shape[-1], gate.device, gate.dtype
     flat, rows, ld = _matrix(gate, width)
     if up is None:   # the halves of gate's columns
@@ -199,15 +211,15 @@ def _silu_forward(gate, up, codes):
         _abi.asr_silu_mul_forward(g_ptr, ld, u_ptr, ld_u, ops._DTYPE_CODE[dtype], rows, cols,
                                   y.data_ptr(), max(cols, 1), *pointers, ldq,
                                   ops._stream(device))
-    return y, buffer, flat, u, (ld, ld_u)
+    return y, buffer, flat, u
 
 
 class _SiluMul(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate, up, saved):
         codes = saved == "i8"
-        y, buffer, g, u, strides = _silu_forward(gate, up, codes)
-        ctx.joint, ctx.strides = up is None, strides
+        y, buffer, g, u = _silu_forward(gate, up, codes)
+        ctx.joint = up is None
         ctx.save_for_backward(None if codes else g, None if codes else u, buffer)
         return y
 
@@ -226,14 +238,19 @@ class _SiluMul(torch.autograd.Function):
         else:
             dgate, dup = (torch.empty(dy.shape, dtype=dtype, device=device) for _ in range(2))
             out_g, out_u, ld_out = dgate.data_ptr(), dup.data_ptr(), max(cols, 1)
-        pointers, ldq, g, u, (ld_g, ld_u) = (None,) * 4, 0, None, None, ctx.strides
+        pointers, ldq, g, ld_g, u, ld_u = (None,) * 4, 0, None, 0, None, 0
         if buffer is not None:
             layout = _Codes(rows, cols, 2)
             base, ldq = buffer.data_ptr(), layout.ld
             pointers = (*layout.at(base, 0), *layout.at(base, 1))
         else:
+            gate, ld_g = _kept_matrix(gate, dy, rows, 2 * cols if ctx.joint else cols)
             g = gate.data_ptr()
-            u = g + half if ctx.joint else up.data_ptr()
+            if ctx.joint:
+                u, ld_u = g + half, ld_g
+            else:
+                up, ld_u = _kept_matrix(up, dy, rows, cols)
+                u = up.data_ptr()
         with ops._on(device):
             _abi.asr_silu_mul_backward(flat.data_ptr(), ld, g, ld_g, u, ld_u, *pointers, ldq,
                                        ops._DTYPE_CODE[dtype], rows, cols, out_g, ld_out, out_u,
