@@ -30,13 +30,38 @@ from . import _abi, ops
 __all__ = ["linear_i8"]
 
 
+def _check_operands(x, w):
+    for t, name in ((x, "x"), (w, "w")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16 (got {t.dtype})")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a GPU (got {t.device})")
+    if x.device != w.device:
+        raise ValueError("x and w must be on the same device")
+
+
+def _rows(t):
+    """t, a matrix, or a copy of it whose rows are contiguous and do not overlap."""
+    return t.contiguous() if t.numel() and (t.stride(1) != 1 or t.stride(0) < t.shape[1]) else t
+
+
+def _kept_rows(t, device, dtype, rows, cols):
+    """A matrix that a pass kept (ops._kept), in any layout, with contiguous rows."""
+    ops._kept(t, device, dtype, rows * cols)
+    if t.shape != (rows, cols):
+        raise RuntimeError(f"a saved tensor came back as {tuple(t.shape)}, not as {(rows, cols)}")
+    return _rows(t)
+
+
 class _LinearI8(torch.autograd.Function):
     """x (T, K) and w (N, K), rows contiguous; the checks are linear_i8's."""
 
     @staticmethod
     def forward(ctx, x, w, grad_rounding, key):
         ctx.save_for_backward(x, w)
-        ctx.grad_rounding, ctx.key = grad_rounding, key
+        ctx.width, ctx.grad_rounding, ctx.key = x.shape[1], grad_rounding, key
         (t, k), n, device = x.shape, w.shape[0], x.device
         y = torch.empty((t, n), dtype=torch.bfloat16, device=device)
         need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 0)
@@ -51,9 +76,9 @@ class _LinearI8(torch.autograd.Function):
     @ops._once
     def backward(ctx, dy):
         x, w = ctx.saved_tensors
-        (t, k), n, device = x.shape, w.shape[0], x.device
-        if dy.stride(1) != 1 or dy.stride(0) < n:
-            dy = dy.contiguous()   # an expanded or transposed gradient
+        (t, n), k, device = dy.shape, ctx.width, dy.device
+        dy = _rows(dy)   # (an expanded or transposed gradient)
+        x, w = (_kept_rows(m, device, dy.dtype, r, k) for m, r in ((x, t), (w, n)))
         want_x, want_w = ctx.needs_input_grad[:2]
         dx = torch.empty((t, k), dtype=torch.bfloat16, device=device) if want_x else None
         dw = torch.empty((n, k), dtype=torch.bfloat16, device=device) if want_w else None
@@ -79,7 +104,7 @@ class _LinearI8Saved(torch.autograd.Function):
         q = torch.empty((t, max(ops._padded16(k), 16)), dtype=torch.int8, device=device)
         scale = torch.empty(t, dtype=torch.float32, device=device)
         ctx.save_for_backward(q, scale, w)
-        ctx.grad_rounding, ctx.key = grad_rounding, key
+        ctx.width, ctx.grad_rounding, ctx.key = k, grad_rounding, key
         need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 0)
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
@@ -93,9 +118,13 @@ class _LinearI8Saved(torch.autograd.Function):
     @ops._once
     def backward(ctx, dy):
         q, scale, w = ctx.saved_tensors
-        (t, n), k, device = dy.shape, w.shape[1], dy.device
-        if dy.stride(1) != 1 or dy.stride(0) < n:
-            dy = dy.contiguous()   # an expanded or transposed gradient
+        (t, n), k, device = dy.shape, ctx.width, dy.device
+        dy, ld = _rows(dy), max(ops._padded16(k), 16)
+        w = _kept_rows(w, device, dy.dtype, n, k)
+        scale = ops._kept(scale, device, torch.float32, t).contiguous()
+        q = _kept_rows(q, device, torch.int8, t, ld)
+        if q.data_ptr() % 16 or ops._row_stride(q, ld) % 16:
+            q = q.clone(memory_format=torch.contiguous_format)
         want_x, want_w = ctx.needs_input_grad[:2]
         dx = torch.empty((t, k), dtype=torch.bfloat16, device=device) if want_x else None
         dw = torch.empty((n, k), dtype=torch.bfloat16, device=device) if want_w else None
@@ -103,9 +132,9 @@ class _LinearI8Saved(torch.autograd.Function):
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
             _abi.asr_linear_i8_backward_saved(
-                q.data_ptr(), q.shape[1], scale.data_ptr(), w.data_ptr(), ops._row_stride(w, k),
-                dy.data_ptr(), ops._row_stride(dy, n), dx.data_ptr() if want_x else None, k,
-                dw.data_ptr() if want_w else None, k, t, n, k,
+                q.data_ptr(), ops._row_stride(q, ld), scale.data_ptr(), w.data_ptr(),
+                ops._row_stride(w, k), dy.data_ptr(), ops._row_stride(dy, n),
+                dx.data_ptr() if want_x else None, k, dw.data_ptr() if want_w else None, k, t, n, k,
                 ops.ROUNDING_CODE[ctx.grad_rounding], *ctx.key, ws.data_ptr(), need,
                 ops._stream(device))
         return dx, dw, None, None
@@ -132,15 +161,7 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr", saved="
     if saved not in ("input", "i8"):
         raise ValueError("saved must be 'input' or 'i8'")
     key = (ops._u32("seed", seed), ops._u32("step", step), ops._u64("base_index", base_index))
-    for t, name in ((x, "x"), (w, "w")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be bfloat16 (got {t.dtype})")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on a GPU (got {t.device})")
-    if x.device != w.device:
-        raise ValueError("x and w must be on the same device")
+    _check_operands(x, w)
     if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"x must be (..., K) and w (N, K): got {tuple(x.shape)} and "
                          f"{tuple(w.shape)}")
@@ -149,10 +170,7 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr", saved="
     if max(tokens, n, k) >= 1 << 17:
         raise ValueError("tokens, N and K must be below 2**17")
     flat = x if x.dim() == 2 else x.reshape(tokens, k)
-    if flat.numel() and (flat.stride(1) != 1 or flat.stride(0) < k):
-        flat = flat.contiguous()
-    if w.numel() and (w.stride(1) != 1 or w.stride(0) < k):
-        w = w.contiguous()
+    flat, w = _rows(flat), _rows(w)
     if key[2] + tokens * n > 1 << 64:
         raise ValueError("base_index + tokens*N exceeds 2**64")
     layer = _LinearI8Saved if saved == "i8" and n > 0 and k > 0 else _LinearI8

@@ -52,13 +52,10 @@ def _ptr(t):
 
 
 def _kept_matrix(t, like, rows, cols):
-    """(tensor, row stride) of a matrix that a pass kept, as it comes back from
-    autograd: hooks on saved tensors (offloading, compression) may give it another
-    layout, so what the forward pass knew of its strides no longer holds."""
-    if t.device != like.device or t.dtype != like.dtype or t.shape[-1:] != (cols,) or \
-            t.numel() != rows * cols:
-        raise RuntimeError(f"a saved tensor came back as {t.dtype} {tuple(t.shape)} on {t.device}, "
-                           f"not as {like.dtype} (..., {cols}) of {rows} rows on {like.device}")
+    """(tensor, row stride) of a matrix that a pass kept (ops._kept), in any layout."""
+    ops._kept(t, like.device, like.dtype, rows * cols)
+    if t.shape[-1:] != (cols,):
+        raise RuntimeError(f"a saved tensor came back as {tuple(t.shape)}, not as (..., {cols})")
     flat, _, ld = _matrix(t, cols)
     return flat, ld
 
@@ -108,7 +105,8 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps, saved):
         y, buffer, flat = _norm_forward(x, weight, bias, eps, True, saved == "i8")
         ctx.save_for_backward(flat, weight, buffer)
-        ctx.bias_dtype = None if bias is None else bias.dtype
+        param = weight if weight is not None else bias
+        ctx.param_dtype = None if param is None else param.dtype
         return y
 
     @staticmethod
@@ -118,25 +116,28 @@ class _LayerNorm(torch.autograd.Function):
         cols, device, dtype = dy.shape[-1], dy.device, dy.dtype
         flat, rows, ld = _matrix(dy, cols)
         want_x, want_w, want_b = ctx.needs_input_grad[:3]
-        pdt = weight.dtype if weight is not None else ctx.bias_dtype or dtype
+        pdt = ctx.param_dtype or dtype
+        if weight is not None:
+            weight = ops._kept(weight, device, pdt, cols).contiguous()
         dx = torch.empty(dy.shape, dtype=dtype, device=device) if want_x else None
         dw = torch.empty_like(weight) if want_w else None
         db = torch.empty(cols, dtype=pdt, device=device) if want_b else None
+        layout = _Codes(rows, cols, 1 if x is None else 0, 16 * rows)
+        buffer = ops._kept_buffer(buffer, device, layout.bytes)
         stat = buffer.data_ptr()
-        x_ptr = ldx = q = scale = None
-        ldq = 0
+        x_ptr, ldx, q, scale, ldq = None, 0, None, None, 0
         if x is None:
-            layout = _Codes(rows, cols, 1, 16 * rows)
             (q, scale), ldq = layout.at(stat, 0), layout.ld
         else:
-            x_ptr, ldx = x.data_ptr(), cols if x.is_contiguous() else ops._row_stride(x, cols)
+            x, ldx = _kept_matrix(x, dy, rows, cols)
+            x_ptr = x.data_ptr()
         need, ws = 0, None
         if want_w or want_b:
             need = _abi.asr_layer_norm_backward_workspace_bytes(rows, cols)
             ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
             _abi.asr_layer_norm_backward(
-                flat.data_ptr(), ld, x_ptr, ldx or 0, q, ldq, scale, stat, ops._DTYPE_CODE[dtype],
+                flat.data_ptr(), ld, x_ptr, ldx, q, ldq, scale, stat, ops._DTYPE_CODE[dtype],
                 rows, cols, _ptr(weight), ops._DTYPE_CODE[pdt], _ptr(dx), _ptr(dw), _ptr(db),
                 _ptr(ws), need, ops._stream(device))
         return dx, dw, db, None, None
@@ -241,6 +242,7 @@ class _SiluMul(torch.autograd.Function):
         pointers, ldq, g, ld_g, u, ld_u = (None,) * 4, 0, None, 0, None, 0
         if buffer is not None:
             layout = _Codes(rows, cols, 2)
+            buffer = ops._kept_buffer(buffer, device, layout.bytes)
             base, ldq = buffer.data_ptr(), layout.ld
             pointers = (*layout.at(base, 0), *layout.at(base, 1))
         else:
@@ -303,16 +305,17 @@ class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, ids, scale, padding):
         ctx.save_for_backward(ids)
-        ctx.args = weight.shape, scale, padding
+        ctx.args = weight.shape, scale, padding, ids.dtype
         return _lookup(ids, weight, scale)
 
     @staticmethod
     @ops._once
     def backward(ctx, dy):
         ids, = ctx.saved_tensors
-        (vocab, dim), scale, padding = ctx.args
+        (vocab, dim), scale, padding, id_type = ctx.args
         flat, n, ld = _matrix(dy, dim)
         device = dy.device
+        ids = ops._kept(ids, device, id_type, n).contiguous()
         dw = torch.empty((vocab, dim), dtype=dy.dtype, device=device)
         need = _abi.asr_embedding_backward_workspace_bytes(n, vocab, dim)
         ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None

@@ -66,6 +66,22 @@ def _once(backward):
     return run
 
 
+def _kept(t, device, dtype, count):
+    """A tensor that a pass kept for its backward pass, as autograd gives it back.
+    Hooks on saved tensors (offloading, compression) may return it in another layout,
+    which callers read anew, or as another kind of tensor, whose address no kernel may take."""
+    if t.device != device or t.dtype != dtype or t.numel() != count:
+        raise RuntimeError(f"a saved tensor came back as {t.dtype} {tuple(t.shape)} on {t.device}, "
+                           f"not as {count} elements of {dtype} on {device}")
+    return t
+
+
+def _kept_buffer(t, device, nbytes):
+    """A pass's own buffer (_kept): its bytes in a row from a 16-byte address."""
+    t = _kept(t, device, torch.uint8, nbytes).contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _uint(name, x, bits):
     """x as a Python int in [0, 2**bits) (the C argument's range), else
     ValueError: ctypes would otherwise wrap it silently."""

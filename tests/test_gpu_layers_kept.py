@@ -7,7 +7,7 @@ import contextlib
 import pytest
 import torch
 
-from adamw_optimizer_stochastic_amd import silu_mul
+from adamw_optimizer_stochastic_amd import embedding, layer_norm, linear_i8, silu_mul
 from _gpu_util import announce, gpu, require_gpu
 
 pytestmark = gpu
@@ -79,3 +79,32 @@ def test_silu_mul(form, saved, dtype):
         return silu_mul(gate, up, saved=saved)
 
     _same(call, [x])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [141, 9001])
+@pytest.mark.parametrize("saved", ["input", "i8"])
+def test_layer_norm(saved, cols, dtype):
+    announce("layer_norm kept", saved, cols, dtype)
+    torch.manual_seed(4)
+    x = torch.randn(37, 2 * cols, device="cuda").to(dtype).requires_grad_()
+    w, b = (torch.randn(cols, device="cuda").to(dtype).requires_grad_() for _ in range(2))
+    _same(lambda: layer_norm((x * 1.5)[:, 3:3 + cols], w * 1.0, b, saved=saved), [x, w, b])
+
+
+@pytest.mark.parametrize("saved", ["input", "i8"])
+def test_linear(saved):
+    announce("linear_i8 kept", saved)
+    torch.manual_seed(5)
+    x = torch.randn(67, 200, device="cuda").bfloat16().requires_grad_()
+    w = torch.randn(45, 100, device="cuda").bfloat16().requires_grad_()
+    _same(lambda: linear_i8((x * 1.5)[:, 3:103], w * 1.0, seed=1, step=2, saved=saved), [x, w])
+
+
+@pytest.mark.parametrize("tokens", [200, 5000])
+def test_embedding(tokens):
+    announce("embedding kept", tokens)
+    torch.manual_seed(6)
+    ids = torch.randint(0, 37, (tokens // 50, 50), device="cuda")
+    w = torch.randn(37, 45, device="cuda").requires_grad_()
+    _same(lambda: embedding(ids, w, scale=0.5, padding_idx=3), [w])
