@@ -6,7 +6,8 @@ their backward pass needs as 8-bit codes with one scale for every 128 columns
 (``ops.pack_i8``'s, 1.03 bytes an element) instead of their inputs; the
 gradients are then the formulas' at the values the codes stand for. Forward
 and backward can be captured into a graph together; as with any operator under
-torch's autograd, no eager graph of the same leaves may be alive then.
+torch's autograd, no eager graph of the same leaves may be alive then. Forward-mode
+derivatives, second derivatives and torch.func's transforms raise.
 """
 
 import math
@@ -181,8 +182,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, saved="input"):
         bias = bias.contiguous()
     if cols > 1 << 24 or (x.numel() // cols if cols else x.shape[:-1].numel()) >= 1 << 24:
         raise ValueError("fewer than 2**24 rows and at most 2**24 columns")
-    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
-                                    or (bias is not None and bias.requires_grad)):
+    if ops._dual_level() or torch.is_grad_enabled() and (
+            x.requires_grad or (weight is not None and weight.requires_grad)
+            or (bias is not None and bias.requires_grad)):
         return _LayerNorm.apply(x, weight, bias, eps, saved)
     return _norm_forward(x, weight, bias, eps, False, False)[0]
 
@@ -284,7 +286,8 @@ def silu_mul(gate, up=None, *, saved="inputs"):
         _check_floats(up, "up", gate.device, gate.dtype)
         if up.shape != gate.shape:
             raise ValueError("gate and up must have the same shape")
-    if torch.is_grad_enabled() and (gate.requires_grad or (up is not None and up.requires_grad)):
+    if ops._dual_level() or torch.is_grad_enabled() and (
+            gate.requires_grad or (up is not None and up.requires_grad)):
         return _SiluMul.apply(gate, up, saved)
     return _silu_forward(gate, up, False)[0]
 
@@ -359,6 +362,6 @@ def embedding(ids, weight, *, scale=1.0, padding_idx=None):
         padding %= vocab
     if not ids.is_contiguous():
         ids = ids.contiguous()
-    if torch.is_grad_enabled() and weight.requires_grad:
+    if ops._dual_level() or torch.is_grad_enabled() and weight.requires_grad:
         return _Embedding.apply(weight, ids, scale, padding)
     return _lookup(ids, weight, scale)

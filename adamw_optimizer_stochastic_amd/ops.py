@@ -54,6 +54,13 @@ def _on(device):
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
+def _dual_level():
+    """Whether forward-mode derivatives are being taken. An input may then have a
+    tangent without requiring a gradient; autograd's function refuses it, where a
+    call past autograd would drop it."""
+    return getattr(torch.autograd.forward_ad, "_current_level", 0) >= 0
+
+
 def _once(backward):
     """torch's once_differentiable, which turns gradients off and on again in
     every call, only where a graph of the gradients is asked for (an embedding's
