@@ -33,12 +33,13 @@ __device__ __forceinline__ void store_stream(asr::u32x2* p, asr::u32x2 v) { __bu
 // (8 or more: all; the others read as 0). At a row's end the elements are loaded
 // one by one, but all at once: places past the end load the last element again,
 // as a branch for each would wait for every load by itself (5 us for 7 of them).
+// load_repeated leaves that element there instead of 0.
 template <typename S>
 struct Run;
 template <>
 struct Run<uint16_t> {
   asr::u32x4 w;
-  template <bool ONCE>
+  template <bool ONCE, bool REPEAT = false>
   __device__ __forceinline__ void load_as(const uint16_t* p, int64_t count) {
     if (count >= 8) {
       const u32x4_any* from = reinterpret_cast<const u32x4_any*>(p);
@@ -50,12 +51,14 @@ struct Run<uint16_t> {
 #pragma unroll
         for (int e = 0; e < 7; ++e) t[e] = p[min(static_cast<int>(count) - 1, e)];
 #pragma unroll
-        for (int e = 0; e < 7; ++e) w[e / 2] |= (e < count ? t[e] : 0u) << (e % 2 * 16);
+        for (int e = 0; e < 7; ++e) w[e / 2] |= (REPEAT || e < count ? t[e] : 0u) << (e % 2 * 16);
+        if (REPEAT) w[3] |= t[6] << 16;
       }
     }
   }
   __device__ __forceinline__ void load(const uint16_t* p, int64_t count) { load_as<false>(p, count); }
   __device__ __forceinline__ void load_once(const uint16_t* p, int64_t count) { load_as<true>(p, count); }
+  __device__ __forceinline__ void load_repeated(const uint16_t* p, int64_t count) { load_as<false, true>(p, count); }
   __device__ __forceinline__ float get(int e) const {
     return __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
   }
@@ -63,7 +66,7 @@ struct Run<uint16_t> {
 template <>
 struct Run<float> {
   asr::f32x4 w[2];
-  template <bool ONCE>
+  template <bool ONCE, bool REPEAT = false>
   __device__ __forceinline__ void load_as(const float* p, int64_t count) {
     if (count >= 8) {
       const f32x4_any* from = reinterpret_cast<const f32x4_any*>(p);
@@ -76,12 +79,14 @@ struct Run<float> {
 #pragma unroll
         for (int e = 0; e < 7; ++e) t[e] = p[min(static_cast<int>(count) - 1, e)];
 #pragma unroll
-        for (int e = 0; e < 7; ++e) w[e / 4][e % 4] = e < count ? t[e] : 0.0f;
+        for (int e = 0; e < 7; ++e) w[e / 4][e % 4] = REPEAT || e < count ? t[e] : 0.0f;
+        if (REPEAT) w[1][3] = t[6];
       }
     }
   }
   __device__ __forceinline__ void load(const float* p, int64_t count) { load_as<false>(p, count); }
   __device__ __forceinline__ void load_once(const float* p, int64_t count) { load_as<true>(p, count); }
+  __device__ __forceinline__ void load_repeated(const float* p, int64_t count) { load_as<false, true>(p, count); }
   __device__ __forceinline__ float get(int e) const { return w[e / 4][e % 4]; }
 };
 

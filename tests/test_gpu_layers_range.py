@@ -1,0 +1,40 @@
+"""The layers at the ends of their types' range: rows whose mean is far larger than
+any spread, differences that overflow, sigmoids next to zero, long sums.
+
+u = 2**-24, half a step of binary32."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import layers as ol
+from adamw_optimizer_stochastic_amd import layer_norm
+from _gpu_util import announce, gpu, require_gpu
+from test_gpu_layers import DTYPES, _check_norm, _np, _values
+
+pytestmark = gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [1, 5, 100, 515, 1100, 2050, 4095, 8190, 9001, 24570])
+def test_gradients_of_rows_of_one_large_value(cols, dtype):
+    """mean * rstd overflows (rstd is 316 where var is 0): nothing past a row's end may
+    come into its sums."""
+    announce("norm of one large value", cols, dtype)
+    rng = np.random.default_rng(cols)
+    x = torch.tensor([1e38, -3e38, 2e36, -1.0, 0.0]).to(DTYPES[dtype])[:, None].expand(5, cols).contiguous().cuda()
+    w, w64 = _values(rng, (cols,), torch.float32)
+    dy, dy64 = _values(rng, (5, cols), DTYPES[dtype])
+    for saved in ("input", "i8"):
+        leaf, weight = x.clone().requires_grad_(), w.clone().requires_grad_()
+        y = layer_norm(leaf, weight, saved=saved)
+        dx, dw = torch.autograd.grad(y, [leaf, weight], dy)
+        used = None
+        if saved == "i8":
+            used = ol.unpack(*ol.pack(ol.layer_norm(_np(x))[1])).astype(np.float64)
+        _check_norm(_np(x), dy64, w64, None, 1e-5, y, dx, dw, None, used)
