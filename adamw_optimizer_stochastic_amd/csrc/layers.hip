@@ -471,8 +471,11 @@ __device__ __forceinline__ asr::u32x2 norm_codes(const float (&x)[8], int64_t co
     far = __builtin_fmaxf(far, __builtin_fabsf(t - (v - kByte)));
     u[e] = __float_as_uint(v);
   }
-  // (!(..): also where 32 bits overflow or have no rstd)
-  if (__builtin_amdgcn_ballot_w64(live && !(far < 0.49994f && turn32 < 0x1p100f && off == off)) != 0) {
+  // (turn32 is 127 over the block's largest difference: from 2**-119 on that one is held by
+  // 32 bits, and far, which says nothing about a NaN, sees none; rstd below its normal
+  // numbers has too few bits)
+  const bool held = turn32 > 0x1p-119f && turn32 < 0x1p100f && normal.rstd >= 0x1p-126f && off == off;
+  if (__builtin_amdgcn_ballot_w64(live && !(far < 0.49994f && held)) != 0) {
     const double turn = live ? rstd / static_cast<double>(s) : 0.0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {

@@ -10,7 +10,7 @@ import torch
 from oracle import layers as ol
 from adamw_optimizer_stochastic_amd import layer_norm
 from _gpu_util import announce, gpu, require_gpu
-from test_gpu_layers import DTYPES, _check_norm, _np, _values
+from test_gpu_layers import DTYPES, _check_norm, _norm_codes, _np, _values
 
 pytestmark = gpu
 
@@ -38,3 +38,25 @@ def test_gradients_of_rows_of_one_large_value(cols, dtype):
         if saved == "i8":
             used = ol.unpack(*ol.pack(ol.layer_norm(_np(x))[1])).astype(np.float64)
         _check_norm(_np(x), dy64, w64, None, 1e-5, y, dx, dw, None, used)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [128, 1000, 3001, 8192, 9001])
+def test_codes_of_rows_whose_differences_overflow(cols, dtype):
+    """x - mean past binary32's range, and rstd below its normal numbers: the codes are
+    those of the 64-bit normalised rows all the same."""
+    announce("norm codes of overflowing differences", cols, dtype)
+    rng = np.random.default_rng(cols + 7)
+    x = np.empty((6, cols))
+    x[0] = 2e38 * rng.uniform(0.9, 1.1, cols)
+    x[0, 3] = -3.2e38
+    x[1] = -x[0]
+    x[2] = rng.choice([-3.3e38, 3.3e38], cols)
+    x[3] = rng.uniform(-3e38, 3e38, cols)
+    x[4] = np.where(rng.random(cols) < 0.9, 3.3e38, rng.uniform(-3.3e38, 3.3e38, cols))
+    x[5] = rng.uniform(-9e37, 9e37, cols)
+    t = torch.from_numpy(x.astype(np.float32)).to(DTYPES[dtype]).cuda()
+    q, s = _norm_codes(t, None, None, 1e-5)
+    want_q, want_s = ol.pack(ol.layer_norm(_np(t))[1])
+    assert np.array_equal(s.cpu().numpy(), want_s)
+    assert np.array_equal(q.cpu().numpy()[:, :cols], want_q)
