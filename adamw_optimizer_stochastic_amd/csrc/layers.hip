@@ -319,7 +319,7 @@ __global__ __launch_bounds__(256) void silu_backward(Silu a) {
       for (int e = 0; e < 8; ++e) {
         const float g = rg[k].get(e), d = rd[k].get(e), sig = sigmoid<S>(g);
         du[e] = d * (g * sig);
-        dg[e] = d * ru[k].get(e) * (sig * (1.0f + g * (1.0f - sig)));
+        dg[e] = d * (ru[k].get(e) * (sig * (1.0f + g * (1.0f - sig))));   // (d u may overflow where this does not)
       }
       store8(dgate.at(i, p), p.count, dg);
       store8(dup.at(i, p), p.count, du);

@@ -8,9 +8,9 @@ import pytest
 import torch
 
 from oracle import layers as ol
-from adamw_optimizer_stochastic_amd import layer_norm
+from adamw_optimizer_stochastic_amd import layer_norm, silu_mul
 from _gpu_util import announce, gpu, require_gpu
-from test_gpu_layers import DTYPES, _check_norm, _norm_codes, _np, _values
+from test_gpu_layers import DTYPES, U, _check_norm, _norm_codes, _np, _values
 
 pytestmark = gpu
 
@@ -60,3 +60,25 @@ def test_codes_of_rows_whose_differences_overflow(cols, dtype):
     want_q, want_s = ol.pack(ol.layer_norm(_np(t))[1])
     assert np.array_equal(s.cpu().numpy(), want_s)
     assert np.array_equal(q.cpu().numpy()[:, :cols], want_q)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("saved", ["inputs", "i8"])
+def test_silu_gradient_whose_factors_overflow_together(saved, dtype):
+    """dy * up past binary32's range where the gradient is not: the sigmoid's factor is
+    there before both of them are. Powers of two, alone in their blocks of codes (whose
+    rounding is up's alone: half a step of 1/127)."""
+    announce("silu_mul of large factors", saved, dtype)
+    gate = torch.tensor([-40.0, -20.0, -10.0, 4.0, 30.0])[:, None].to(DTYPES[dtype]).cuda()
+    up, dy = (torch.full_like(gate, 2.0 ** e) for e in (70, 62))
+    dy[3:] = 2.0 ** 50
+    leaves = [gate.requires_grad_(), up.requires_grad_()]
+    dgate, dup = torch.autograd.grad(silu_mul(*leaves, saved=saved), leaves, dy)
+    want_g, want_u = ol.silu_mul_grads(_np(dy), _np(gate), _np(up))
+    # sigmoids: in bf16 off by (|gate| + 6) 2**-22 of themselves, 46 * 2**-22 at most, in f32
+    # by the functions' 4 u; a gate that its code (127) stands for is off by 2**-23 of
+    # itself, which moves them by 40 * 2**-23. Products 8 u, and half a step of the result.
+    off = 66 * 2.0 ** -22 + 8 * U + (2.0 ** -8 if dtype == "bf16" else 0.0)
+    assert np.all(np.isfinite(want_g)) and np.all(np.abs(want_g) < 3e38)
+    assert np.all(np.abs(_np(dgate) - want_g) <= off * np.abs(want_g))
+    assert np.all(np.abs(_np(dup) - want_u) <= off * np.abs(want_u))
