@@ -236,10 +236,11 @@ struct Silu {
   int64_t ld_gate, ld_up, ld_dy, ld_y, ld_dgate, ld_dup;
 };
 
-// 1 / (1 + exp(-x)). For bf16 values the exponential and reciprocal
-// instructions, which are off by 2**-20 of the value at most for |x| < 16 (and
-// where x is larger by |x| 2**-23): far below the output's 2**-9. f32 values take
-// the accurate functions.
+// 1 / (1 + exp(-x)). For bf16 values the exponential and reciprocal instructions: the
+// argument's two roundings come to |x| 0.9 * 2**-23 of the value, the instructions to a step
+// each, so it is off by (|x| + 3) 2**-23 of itself at most, far below the output's 2**-9. A
+// value below 2**-126 is 0 there. f32 values take the accurate functions (0 from where
+// exp(-x) overflows, x < -88.7).
 template <typename S>
 __device__ __forceinline__ float sigmoid(float x) {
   if constexpr (std::is_same_v<S, float>) return 1.0f / (1.0f + expf(-x));

@@ -12,7 +12,6 @@ namespace asr_rows {
 // so rows of any width and views from any element keep the wide form.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Streams are read and written past the caches (non-temporal): what a pass reads

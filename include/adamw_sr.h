@@ -468,7 +468,7 @@ int asr_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x,
  * Requirements: sizes, codes and alignment as for asr_pack_i8; row strides at least
  * cols; no output overlaps an input, but in the forward call y may be gate or
  * up, and in the backward call dgate may be dy, gate or up, and dup another of them (with the same
- * stride). Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EHIP. Run on
+ * stride). A sig(g) below 2**-126 may be taken as 0. Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EHIP. Run on
  * `stream`; do not synchronize.
  */
 int asr_silu_mul_forward(const void* gate, int64_t ld_gate, const void* up,
