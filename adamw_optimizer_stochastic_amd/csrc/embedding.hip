@@ -1,7 +1,8 @@
 // Embedding: y[t] = scale * w[ids[t]], and the table's gradient
-//   dw[v] = scale * (sum of dy[t] over the tokens t with ids[t] = v, in their order),
-// a row of no token 0. Sums in f32, one rounding at the end; the order of the
-// additions is fixed by ids alone, so equal calls give equal bits.
+//   dw[v] = scale * (sum of dy[t] over the tokens t with ids[t] = v),
+// a row of no token 0. Sums in f32, one rounding at the end: of a run of tokens in their
+// order, of a long one as partial sums of consecutive shares, joined in theirs. The order
+// of the additions is fixed by ids alone, so equal calls give equal bits.
 //
 // The gradient's steps. (1) Tokens are sorted by id, stable: 8 bits (or fewer) of the
 // id a pass. Ids outside the table and the padding id get the key `vocab` and end up
@@ -336,6 +337,7 @@ struct Sums {
   float scale;
   int32_t chunk;             // sorted positions a chunk, a multiple of 16
   int32_t chunks, log_lanes;
+  int32_t fold;              // positions of a first sum
   uint32_t strips, sum_blocks;
   Fill fill;
 };
@@ -366,8 +368,18 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   const uint32_t before = there && i0 > 0 ? a.keys[i0 - 1] : kPast, after = there && i1 < a.n ? a.keys[i1] : kPast;
   uint32_t run = kPast;      // of acc; no key of the table before the first
   bool head = false;
-  float acc[8] = {};
+  float acc[8] = {}, all[8] = {};   // all: of the run's positions before the last fold
+  int32_t held = 0;
   for (int32_t start = 0; start < a.chunk; start += kBatch) {
+    if (held == a.fold) {
+      held = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        all[e] += acc[e];
+        acc[e] = 0.0f;
+      }
+    }
+    held += kBatch;
     if (start > 0) __syncthreads();   // (the last batch is read)
     if (static_cast<int>(threadIdx.x) < side * kBatch) {
       const int64_t i = (c0 + threadIdx.x / kBatch) * a.chunk + start + threadIdx.x % kBatch;
@@ -403,6 +415,10 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
         if (key != run) {
           if (run < vocab) {
             const bool tail = k == kAhead ? after == run : false;
+            if (a.chunk > a.fold) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[e] += all[e];
+            }
             if (head || tail) {
               store8(a.part + (c * 2 + (head ? 0 : 1)) * a.dim + col, count, acc);
             } else {
@@ -415,7 +431,7 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
           run = key;
           head = start + half + k == 0 && run == before;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+          for (int e = 0; e < 8; ++e) acc[e] = all[e] = 0.0f;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += r.get(e);   // (what the turn after the last one adds, no one stores)
@@ -786,6 +802,7 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
     a.part = b.part;
     a.chunk = cut.chunk;
     a.chunks = cut.chunks;
+    a.fold = fold_of(cut.chunk);
     Sort sort = sort_args(Ids{ids, ids_64 ? 1u : 0u, n, vocab, padding_idx}, b);
     if (cut.tiles > 1) {
       e = sort_tiles(sort, b, cut, s);

@@ -352,6 +352,8 @@ struct Norm {
   double eps, inv_cols;
   float inv_cols32;
   uint32_t w_bf16, alone;   // alone: one workgroup, whose sums are the result
+  uint32_t more;            // the workgroups' sums go on top of an earlier launch's
+  int32_t fold;             // rows of a lane's first sum
 };
 
 // Two sums over the lanes of a row, in every lane.
@@ -746,8 +748,9 @@ __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
       float t = 0.0f;
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) t += sums[k * kCols + i];
+      float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + which) * a.cols + i;
       if (a.alone) store_param(result, a.w_bf16, i, t);
-      else a.part[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.cols + i] = t;
+      else *part = a.more ? *part + t : t;
     }
   };
   if (a.dw) finish(dw, a.dw, 0);
@@ -812,13 +815,14 @@ __global__ __launch_bounds__(LANES) void norm_backward_long(Norm a) {
 // And their sums over rows: a workgroup takes 2048 columns of a share of the rows, four
 // rows at once.
 template <typename S, bool SAVED>
-__global__ __launch_bounds__(256) void norm_columns_long(Norm a, int64_t share, int32_t strips) {
+__global__ __launch_bounds__(256) void norm_columns_long(Norm a, int32_t share, int32_t strips) {
   constexpr int kAhead = 4;
   const int32_t strip = blockIdx.x % strips, part = blockIdx.x / strips;
   const int64_t col = (static_cast<int64_t>(strip) * 256 + threadIdx.x) * 8, count = a.cols - col;
   if (count <= 0) return;
-  const int64_t r0 = part * share, r1 = min(a.rows, r0 + share);
-  float dw[8] = {}, db[8] = {};
+  const int64_t r0 = static_cast<int64_t>(part) * share, r1 = min(a.rows, r0 + share);
+  float dw[8] = {}, db[8] = {}, all_dw[8] = {}, all_db[8] = {};
+  int32_t held = 0;
   for (int64_t row = r0; row < r1; row += kAhead) {
     Run<S> dy[kAhead];
     Normalised<S, SAVED> xh[kAhead];
@@ -839,10 +843,20 @@ __global__ __launch_bounds__(256) void norm_columns_long(Norm a, int64_t share, 
         db[e] += dy[u].get(e);
       }
     }
+    held += kAhead;
+    if (held == a.fold || row + kAhead >= r1) {
+      held = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        all_dw[e] += dw[e];
+        all_db[e] += db[e];
+        dw[e] = db[e] = 0.0f;
+      }
+    }
   }
   float* out = a.part + static_cast<int64_t>(part) * 2 * a.cols + col;
-  store8(out, count, dw);
-  store8(out + a.cols, count, db);
+  store8(out, count, all_dw);
+  store8(out + a.cols, count, all_db);
 }
 
 // dw and db from the workgroups' sums: 64 columns a workgroup, 4 a lane, 64
@@ -1012,7 +1026,20 @@ hipError_t norm_back(Norm a, hipStream_t s) {
     // 8.5; 64 x 1024 (8 turns) 10.1 and 7.8.
     parts = sums && a.rows <= 4 * groups ? 1 : std::min<int64_t>((a.rows + groups - 1) / groups, kNormGrid);
     a.alone = sums && parts == 1;
-    e = launch(f, dim3(static_cast<uint32_t>(parts)), 1024, s, a);
+    // A lane's sum takes up to `fold` rows (fold_of); more of them are as many launches,
+    // each adding its workgroups' sums to the last one's.
+    const int64_t turn = parts * groups, slice = turn * fold_of((a.rows + turn - 1) / turn);
+    Norm part = a;
+    for (int64_t r = 0; r < a.rows && e == hipSuccess; r += slice) {
+      part.rows = std::min(slice, a.rows - r);
+      part.more = r > 0;
+      e = launch(f, dim3(static_cast<uint32_t>(std::min(parts, (part.rows + groups - 1) / groups))), 1024, s, part);
+      part.dy = static_cast<const S*>(part.dy) + slice * a.ld_dy;
+      if (a.x) part.x = static_cast<const S*>(part.x) + slice * a.ldx;
+      if (a.dx) part.dx = static_cast<S*>(part.dx) + slice * a.cols;
+      if (a.c.q) part.c = Codes{part.c.q + slice * a.c.ld, part.c.s + slice * a.blocks, a.c.ld};
+      part.stat += slice;
+    }
   };
   if (a.cols <= 512) one(&norm_backward<S, SAVED, 64>, 16);
   else if (a.cols <= 1024) one(&norm_backward<S, SAVED, 128>, 8);
@@ -1026,8 +1053,9 @@ hipError_t norm_back(Norm a, hipStream_t s) {
                              : launch(&norm_backward_long<S, SAVED, 256>, grid, 256, s, a);
     if (e == hipSuccess && sums) {
       parts = std::min<int64_t>(a.rows, kNormGrid);
-      const int64_t share = (a.rows + parts - 1) / parts;
+      const int32_t share = static_cast<int32_t>((a.rows + parts - 1) / parts);
       parts = (a.rows + share - 1) / share;
+      a.fold = fold_of(share);
       const int32_t strips = static_cast<int32_t>((static_cast<int64_t>(a.cols) + 2047) / 2048);
       e = launch(&norm_columns_long<S, SAVED>, dim3(static_cast<uint32_t>(parts * strips)), 256, s, a, share, strips);
     }

@@ -166,4 +166,13 @@ __device__ __forceinline__ V wave_sum(V v) {
   return v + __shfl_xor(v, 32);
 }
 
+// How many terms of a long f32 sum are added before the sum so far goes into a second
+// one: an addition is off by half a step of the sum, so n of them in one chain by up to n
+// half steps, in two levels by 2 sqrt(n) to 3 sqrt(n). Up to 256 terms stay one chain.
+inline int32_t fold_of(int64_t terms) {
+  int64_t f = 256;
+  while (f * f < terms) f *= 2;
+  return static_cast<int32_t>(f);
+}
+
 }  // namespace asr_rows
