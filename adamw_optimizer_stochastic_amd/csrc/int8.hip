@@ -1118,11 +1118,11 @@ static int linear_forward(const uint16_t* x, int64_t ldx, const uint16_t* w, int
     const hipError_t e = launch(&asr_i8::clear, std::min<int64_t>((tokens * n + 255) / 256, 65536), 256, &g, s);
     return e == hipSuccess ? ok() : hip_fail(e, "linear_i8 launch");
   }
-  if (!workspace || !aligned_to(workspace, 256) ||
-      workspace_bytes < asr_linear_i8_workspace_bytes(tokens, n, k, 0))
+  const int64_t room = q ? 1 : tokens;  // x's codes that the workspace has room for
+  if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < asr_linear_i8_workspace_bytes(room, n, k, 0))
     return fail(ASR_EWORKSPACE, "linear_i8: workspace NULL, too small or not 256-byte aligned");
-  LinearForward f(workspace, tokens, n, k);
-  if (q) {  // x's codes go to the caller
+  LinearForward f(workspace, room, n, k);
+  if (q) {  // they go to the caller
     f.qx = q;
     f.sx = scale;
   }

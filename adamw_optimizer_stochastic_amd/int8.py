@@ -105,7 +105,7 @@ class _LinearI8Saved(torch.autograd.Function):
         scale = torch.empty(t, dtype=torch.float32, device=device)
         ctx.save_for_backward(q, scale, w)
         ctx.width, ctx.grad_rounding, ctx.key = k, grad_rounding, key
-        need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 0)
+        need = _abi.asr_linear_i8_workspace_bytes(1, n, k, 0)   # (x's codes are in q)
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
             _abi.asr_linear_i8_forward_saved(

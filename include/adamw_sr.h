@@ -375,7 +375,8 @@ int asr_linear_i8_backward(const uint16_t* x, int64_t ldx, const uint16_t* w,
  * or NaN in x makes all of dw NaN.
  * Requirements: as above; ldq a multiple of 16, at least k up to a multiple of
  * 16 and below 2**23; q 16-byte aligned, scale 4-byte aligned; n > 0 in the
- * forward call. The workspaces are those of the calls above.
+ * forward call. workspace: of asr_linear_i8_workspace_bytes(1, n, k, 0) bytes in
+ * the forward call (x's codes need no room there), in the backward call as above.
  */
 int asr_linear_i8_forward_saved(const uint16_t* x, int64_t ldx,
                                 const uint16_t* w, int64_t ldw, uint16_t* y,

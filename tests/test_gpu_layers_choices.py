@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import layers as ol
-from adamw_optimizer_stochastic_amd import _abi, embedding, layer_norm, ops, silu_mul
+from adamw_optimizer_stochastic_amd import _abi, embedding, layer_norm, linear_i8, ops, silu_mul
 from _gpu_util import announce, gpu, require_gpu, to_host
 from test_gpu_embedding import _check, _check_grad
 from test_gpu_layers import (DTYPES, _check_norm, _close, _esig, _norm_codes, _norm_inputs, _np, _silu_limits,
@@ -225,3 +225,23 @@ def test_layer_norm_gradient_writes_nothing_else(rows, cols, saved, dtype):
         used = ol.unpack(*ol.pack(ol.layer_norm(exact[0])[1])).astype(np.float64)
     _check_norm(*exact, 1e-5, y.as_matrix(f, rows), dx.as_matrix(f, rows), dw.as_matrix(torch.float32, 1)[0],
                 db.as_matrix(torch.float32, 1)[0], used, depth=100)
+
+
+@pytest.mark.parametrize("t,n,k", [(1, 24, 56), (67, 512, 256), (300, 77, 131), (1030, 130, 2000)])
+def test_linear_keeps_no_second_copy_of_its_codes(t, n, k):
+    """The forward call's workspace has w's codes and one token's room, no more."""
+    announce("linear_i8 forward between marks", t, n, k)
+    st = torch.cuda.current_stream().cuda_stream
+    x, w = (torch.randn(*shape, device="cuda").bfloat16() for shape in ((t, k), (n, k)))
+    need, ldq = _abi.asr_linear_i8_workspace_bytes(1, n, k, 0), (k + 15) // 16 * 16
+    assert need <= n * (ldq + 4) + ldq + 4 + 4 * 256
+    y, q, s, ws = Room(t * n * 2), Room(t * ldq), Room(t * 4), Room(need)
+    _abi.asr_linear_i8_forward_saved(x.data_ptr(), k, w.data_ptr(), k, y.ptr, n, q.ptr, ldq, s.ptr, t, n, k, ws.ptr,
+                                     need, st)
+    torch.cuda.synchronize()
+    for room in (y, q, s, ws):
+        room.check()
+    assert torch.equal(y.as_matrix(torch.bfloat16, t), linear_i8(x, w))
+    want_q, want_s = ops.quantize_i8(x)
+    assert torch.equal(q.as_matrix(torch.int8, t)[:, :k], want_q)
+    assert torch.equal(s.as_matrix(torch.float32, 1)[0], want_s)

@@ -142,3 +142,24 @@ def test_codes_keep_their_alignment(calls):
             y = _pass(op, saved)
         y.backward(torch.zeros_like(y))
         assert _last(calls, name)[at] % 16 == 0
+
+
+def test_linear_asks_for_no_second_room_for_its_codes(monkeypatch, calls):
+    """Keeping x's codes, the forward call's workspace is that of one token."""
+    asked = []
+    monkeypatch.setattr(_abi, "asr_linear_i8_workspace_bytes", lambda *args: asked.append(args) or 256)
+    _pass("linear_i8", "i8")
+    _pass("linear_i8", "input")
+    assert asked == [(1, 7, 24, 0), (5, 7, 24, 0)]
+
+
+def test_linear_saved_workspace():
+    from adamw_optimizer_stochastic_amd import _build
+    if not _build.is_built():
+        _build.build()
+    need = _abi.asr_linear_i8_workspace_bytes(1, 24, 56, 0)
+    assert need < _abi.asr_linear_i8_workspace_bytes(400, 24, 56, 0)
+    with pytest.raises(_abi.AsrError) as e:
+        _abi.asr_linear_i8_forward_saved(0x1000, 56, 0x8000, 56, 0x10000, 24, 0x20000, 64, 0x30000, 400, 24, 56,
+                                         0x100000, need - 1, None)
+    assert e.value.status == _abi.ASR_EWORKSPACE
