@@ -982,6 +982,14 @@ constexpr int64_t kCus = 256;                    // compute units of an MI355X
 // 96; below it the row's own time counts: 64 x 131072 80 and 34, 512 x 16384 15.5 and 11.9.
 constexpr int64_t kManyLong = 1024;
 
+// Workgroups' sums in the norm's backward pass: of rows of more than 8192 columns, which
+// workgroups share in strips of 2048, as many as make 8 workgroups a compute unit.
+constexpr int64_t kNormStrip = 2048;
+int64_t norm_parts(int64_t rows, int64_t cols) {
+  const int64_t strips = cols > 8192 ? (cols + kNormStrip - 1) / kNormStrip : 1;
+  return std::min({rows, kNormGrid, (8 * kCus + strips - 1) / strips});
+}
+
 int check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
   if (int rc = check_size("layer_norm", rows, cols, dtype)) return rc;
   if (param_dtype != ASR_F32 && param_dtype != ASR_BF16) return fail(ASR_EDTYPE, "layer_norm: unknown param_dtype");
@@ -1052,11 +1060,11 @@ hipError_t norm_back(Norm a, hipStream_t s) {
       e = a.rows < kManyLong ? launch(&norm_backward_long<S, SAVED, 1024>, grid, 1024, s, a)
                              : launch(&norm_backward_long<S, SAVED, 256>, grid, 256, s, a);
     if (e == hipSuccess && sums) {
-      parts = std::min<int64_t>(a.rows, kNormGrid);
+      parts = norm_parts(a.rows, a.cols);
       const int32_t share = static_cast<int32_t>((a.rows + parts - 1) / parts);
       parts = (a.rows + share - 1) / share;
       a.fold = fold_of(share);
-      const int32_t strips = static_cast<int32_t>((static_cast<int64_t>(a.cols) + 2047) / 2048);
+      const int32_t strips = static_cast<int32_t>((a.cols + kNormStrip - 1) / kNormStrip);
       e = launch(&norm_columns_long<S, SAVED>, dim3(static_cast<uint32_t>(parts * strips)), 256, s, a, share, strips);
     }
   }
@@ -1227,7 +1235,7 @@ int asr_layer_norm_forward(const void* x, int32_t dtype, int64_t ldx, int64_t ro
 
 size_t asr_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || rows > kMaxBlocks || cols > kMaxNorm) return 0;
-  return static_cast<size_t>(std::min<int64_t>(rows, kNormGrid) * 2 * cols * 4);
+  return static_cast<size_t>(norm_parts(rows, cols) * 2 * cols * 4);
 }
 
 int asr_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ldx, const int8_t* q, int64_t ldq,

@@ -427,7 +427,7 @@ int asr_unpack_i8(const int8_t* q, int64_t ldq, const float* scale,
  *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy.
  * mean and rstd are formed in 64 bits, the rest in 32; the sums over rows take an order
  * that depends on the sizes only, in several levels, so that rounding them costs at most
- * (342 + 3 sqrt(rows / 256)) 2**-24 of the sums of the magnitudes. weight, bias: cols elements of param_dtype,
+ * (342 + 3 sqrt(rows / 256 + rows cols / 2**22)) 2**-24 of the sums of the magnitudes. weight, bias: cols elements of param_dtype,
  * NULL: 1 and 0. stat: NULL, or rows x 4 f32 that the backward call takes.
  * q, scale: NULL, or they receive asr_pack_i8's codes (to nearest) of xh,
  * computed in 64 bits; the backward call then takes them, with x NULL, and uses what

@@ -199,7 +199,7 @@ def test_embedding_gradient_writes_nothing_else(n, vocab, dim, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,cols", [(65, 203), (33, 1001), (17, 2001), (9, 4001), (5, 8001), (1300, 203),
-                                       (7, 9001), (600, 8203)])
+                                       (7, 9001), (600, 8203), (130, 40007), (5, 2000003)])
 @pytest.mark.parametrize("saved", ["input", "i8"])
 def test_layer_norm_gradient_writes_nothing_else(rows, cols, saved, dtype):
     """One row more than one workgroup sums, more workgroups than sums, long rows."""

@@ -80,3 +80,16 @@ def test_silu_mul_refuses_a_tensor_of_another_kind(calls):
         with pytest.raises(RuntimeError, match="saved"):
             y.sum().backward()
     assert not [c for c in calls if c[0] == "asr_silu_mul_backward"]
+
+
+def test_layer_norm_workspace_of_wide_rows():
+    """No more of it than the rows themselves are worth: 256 rows of 2**24 columns
+    have enough workgroups without sums of their own."""
+    from adamw_optimizer_stochastic_amd import _build
+    if not _build.is_built():
+        _build.build()
+    need = _abi.asr_layer_norm_backward_workspace_bytes
+    assert need(256, 2 ** 24) == 2 * 2 ** 24 * 4 and need(4, 2 ** 24) == need(256, 2 ** 24)
+    for rows, cols in ((64, 131072), (300, 40007), (5000, 16384), (10 ** 6, 8193)):
+        strips = -(-cols // 2048)
+        assert need(rows, cols) == min(rows, 256, -(-2048 // strips)) * 2 * cols * 4
