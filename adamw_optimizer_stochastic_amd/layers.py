@@ -57,6 +57,8 @@ def _kept_matrix(t, like, rows, cols):
     ops._kept(t, like.device, like.dtype, rows * cols)
     if t.shape[-1:] != (cols,):
         raise RuntimeError(f"a saved tensor came back as {tuple(t.shape)}, not as (..., {cols})")
+    if t.is_contiguous():
+        return t, max(cols, 1)
     flat, _, ld = _matrix(t, cols)
     return flat, ld
 
@@ -86,12 +88,14 @@ def _norm_forward(x, weight, bias, eps, keep, codes):
     y = torch.empty_like(x) if flat is x else torch.empty(x.shape, dtype=x.dtype, device=device)
     buffer = stat = q = scale = None
     ldq = 0
-    if keep:
-        layout = _Codes(rows, cols, 1 if codes else 0, 16 * rows)
+    if codes:
+        layout = _Codes(rows, cols, 1, 16 * rows)
         buffer = torch.empty(layout.bytes, dtype=torch.uint8, device=device)
         stat = buffer.data_ptr()
-        if codes:
-            (q, scale), ldq = layout.at(stat, 0), layout.ld
+        (q, scale), ldq = layout.at(stat, 0), layout.ld
+    elif keep:
+        buffer = torch.empty(16 * rows, dtype=torch.uint8, device=device)
+        stat = buffer.data_ptr()
     param = weight if weight is not None else bias
     with ops._on(device):
         _abi.asr_layer_norm_forward(
@@ -120,18 +124,19 @@ class _LayerNorm(torch.autograd.Function):
         pdt = ctx.param_dtype or dtype
         if weight is not None:
             weight = ops._kept(weight, device, pdt, cols).contiguous()
-        dx = torch.empty(dy.shape, dtype=dtype, device=device) if want_x else None
+        dx = dy.new_empty(dy.shape) if want_x else None
         dw = torch.empty_like(weight) if want_w else None
         db = torch.empty(cols, dtype=pdt, device=device) if want_b else None
-        layout = _Codes(rows, cols, 1 if x is None else 0, 16 * rows)
-        buffer = ops._kept_buffer(buffer, device, layout.bytes)
-        stat = buffer.data_ptr()
         x_ptr, ldx, q, scale, ldq = None, 0, None, None, 0
         if x is None:
-            (q, scale), ldq = layout.at(stat, 0), layout.ld
+            layout = _Codes(rows, cols, 1, 16 * rows)
+            buffer = ops._kept_buffer(buffer, device, layout.bytes)
+            (q, scale), ldq = layout.at(buffer.data_ptr(), 0), layout.ld
         else:
+            buffer = ops._kept_buffer(buffer, device, 16 * rows)
             x, ldx = _kept_matrix(x, dy, rows, cols)
             x_ptr = x.data_ptr()
+        stat = buffer.data_ptr()
         need, ws = 0, None
         if want_w or want_b:
             need = _abi.asr_layer_norm_backward_workspace_bytes(rows, cols)
@@ -320,12 +325,12 @@ class _Embedding(torch.autograd.Function):
         flat, n, ld = _matrix(dy, dim)
         device = dy.device
         ids = ops._kept(ids, device, id_type, n).contiguous()
-        dw = torch.empty((vocab, dim), dtype=dy.dtype, device=device)
+        dw = dy.new_empty((vocab, dim))
         need = _abi.asr_embedding_backward_workspace_bytes(n, vocab, dim)
         ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         with ops._on(device):
             _abi.asr_embedding_backward(
-                ids.data_ptr(), int(ids.dtype == torch.int64), n, flat.data_ptr(), ld,
+                ids.data_ptr(), int(id_type == torch.int64), n, flat.data_ptr(), ld,
                 ops._DTYPE_CODE[dy.dtype], vocab, dim, scale, padding, dw.data_ptr(),
                 _ptr(ws), need, ops._stream(device))
         return dw, None, None, None

@@ -46,12 +46,13 @@ _written = torch.autograd.graph.increment_version
 
 
 _HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(device):
     """A context in which `device` is the current one (no more than a
     comparison where it is already)."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == _current_device() else torch.cuda.device(device)
 
 
 def _dual_level():
