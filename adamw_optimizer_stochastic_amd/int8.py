@@ -43,12 +43,17 @@ def _check_operands(x, w):
 
 
 def _rows(t):
-    """t, a matrix, or a copy of it whose rows are contiguous and do not overlap."""
-    return t.contiguous() if t.numel() and (t.stride(1) != 1 or t.stride(0) < t.shape[1]) else t
+    """(tensor, row stride): the matrix t, or a copy of it if its rows are not contiguous
+    or overlap."""
+    if t.is_contiguous():
+        return t, max(t.shape[1], 1)
+    if t.numel() and (t.stride(1) != 1 or t.stride(0) < t.shape[1]):
+        t = t.contiguous()
+    return t, ops._row_stride(t, t.shape[1])
 
 
 def _kept_rows(t, device, dtype, rows, cols):
-    """A matrix that a pass kept (ops._kept), in any layout, with contiguous rows."""
+    """_rows of a matrix that a pass kept (ops._kept), in any layout."""
     ops._kept(t, device, dtype, rows * cols)
     if t.shape != (rows, cols):
         raise RuntimeError(f"a saved tensor came back as {tuple(t.shape)}, not as {(rows, cols)}")
@@ -77,18 +82,18 @@ class _LinearI8(torch.autograd.Function):
     def backward(ctx, dy):
         x, w = ctx.saved_tensors
         (t, n), k, device = dy.shape, ctx.width, dy.device
-        dy = _rows(dy)   # (an expanded or transposed gradient)
-        x, w = (_kept_rows(m, device, dy.dtype, r, k) for m, r in ((x, t), (w, n)))
+        dy, ld_dy = _rows(dy)   # (an expanded or transposed gradient)
+        x, ld_x = _kept_rows(x, device, torch.bfloat16, t, k)
+        w, ld_w = _kept_rows(w, device, torch.bfloat16, n, k)
         want_x, want_w = ctx.needs_input_grad[:2]
-        dx = torch.empty((t, k), dtype=torch.bfloat16, device=device) if want_x else None
-        dw = torch.empty((n, k), dtype=torch.bfloat16, device=device) if want_w else None
+        dx = dy.new_empty((t, k)) if want_x else None
+        dw = dy.new_empty((n, k)) if want_w else None
         need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 1)
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
             _abi.asr_linear_i8_backward(
-                x.data_ptr(), ops._row_stride(x, k), w.data_ptr(), ops._row_stride(w, k),
-                dy.data_ptr(), ops._row_stride(dy, n), dx.data_ptr() if want_x else None, k,
-                dw.data_ptr() if want_w else None, k, t, n, k,
+                x.data_ptr(), ld_x, w.data_ptr(), ld_w, dy.data_ptr(), ld_dy,
+                dx.data_ptr() if want_x else None, k, dw.data_ptr() if want_w else None, k, t, n, k,
                 ops.ROUNDING_CODE[ctx.grad_rounding], *ctx.key, ws.data_ptr(), need,
                 ops._stream(device))
         return dx, dw, None, None
@@ -119,21 +124,21 @@ class _LinearI8Saved(torch.autograd.Function):
     def backward(ctx, dy):
         q, scale, w = ctx.saved_tensors
         (t, n), k, device = dy.shape, ctx.width, dy.device
-        dy, ld = _rows(dy), max(ops._padded16(k), 16)
-        w = _kept_rows(w, device, dy.dtype, n, k)
+        dy, ld_dy = _rows(dy)   # (an expanded or transposed gradient)
+        w, ld_w = _kept_rows(w, device, torch.bfloat16, n, k)
         scale = ops._kept(scale, device, torch.float32, t).contiguous()
-        q = _kept_rows(q, device, torch.int8, t, ld)
-        if q.data_ptr() % 16 or ops._row_stride(q, ld) % 16:
-            q = q.clone(memory_format=torch.contiguous_format)
+        width = max(ops._padded16(k), 16)
+        q, ld_q = _kept_rows(q, device, torch.int8, t, width)
+        if q.data_ptr() % 16 or ld_q % 16:
+            q, ld_q = q.clone(memory_format=torch.contiguous_format), width
         want_x, want_w = ctx.needs_input_grad[:2]
-        dx = torch.empty((t, k), dtype=torch.bfloat16, device=device) if want_x else None
-        dw = torch.empty((n, k), dtype=torch.bfloat16, device=device) if want_w else None
+        dx = dy.new_empty((t, k)) if want_x else None
+        dw = dy.new_empty((n, k)) if want_w else None
         need = _abi.asr_linear_i8_workspace_bytes(t, n, k, 1)
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         with ops._on(device):
             _abi.asr_linear_i8_backward_saved(
-                q.data_ptr(), ops._row_stride(q, ld), scale.data_ptr(), w.data_ptr(),
-                ops._row_stride(w, k), dy.data_ptr(), ops._row_stride(dy, n),
+                q.data_ptr(), ld_q, scale.data_ptr(), w.data_ptr(), ld_w, dy.data_ptr(), ld_dy,
                 dx.data_ptr() if want_x else None, k, dw.data_ptr() if want_w else None, k, t, n, k,
                 ops.ROUNDING_CODE[ctx.grad_rounding], *ctx.key, ws.data_ptr(), need,
                 ops._stream(device))
@@ -170,7 +175,7 @@ def linear_i8(x, w, *, seed=0, step=0, base_index=0, grad_rounding="sr", saved="
     if max(tokens, n, k) >= 1 << 17:
         raise ValueError("tokens, N and K must be below 2**17")
     flat = x if x.dim() == 2 else x.reshape(tokens, k)
-    flat, w = _rows(flat), _rows(w)
+    flat, w = _rows(flat)[0], _rows(w)[0]
     if key[2] + tokens * n > 1 << 64:
         raise ValueError("base_index + tokens*N exceeds 2**64")
     layer = _LinearI8Saved if saved == "i8" and n > 0 and k > 0 else _LinearI8
