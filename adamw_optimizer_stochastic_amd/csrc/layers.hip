@@ -10,17 +10,17 @@
 //   xh = (x - mean) rstd, y = xh w + b;
 //   with g = dy w: dx = rstd (g - sum g / C - xh sum(g xh) / C),
 //   dw = sum over rows of dy xh, db = sum over rows of dy.
-// mean and var are summed in 64 bits (as fast here as in 32: the passes wait for
-// memory) and kept for the backward pass as two f32 numbers for the mean and
-// one for rstd. Or the pass keeps the 8-bit codes of xh instead of x: their
+// mean and var are summed in 64 bits (so that one pass over the row gives both) and
+// kept for the backward pass as two f32 numbers for the mean and one for rstd. Or the pass keeps the 8-bit codes of xh instead of x: their
 // definition is the codes of the 64-bit xh, so that no rounding on the way
 // decides one, and gradients use what the codes stand for.
 //
 // gated SiLU: y = g sig(g) u, du = dy g sig(g), dg = dy u sig(g) (1 + g (1 - sig(g))),
 // from g and u themselves or from their 8-bit codes.
 //
-// All of it is bound by memory; each kernel reads its inputs once and holds
-// them in registers. 8 columns a lane, so 16 lanes hold a block of codes.
+// Large calls are bound by memory; the kernels read their inputs once and hold them in
+// registers, but for a norm's rows of more than 8192 columns, which are read twice forward
+// and three times backward. 8 columns a lane, so 16 lanes hold a block of codes.
 #include "mfma_loop.hpp"
 #include "rows.hpp"
 #include "status.hpp"
@@ -532,11 +532,11 @@ __device__ __forceinline__ void finish8(const Norm& a, int64_t row, int64_t col,
 // Rows of up to LANES * KEEP * 8 columns, held in registers by LANES lanes; a group of
 // lanes takes several rows, the workgroups' number apart, with its weights and biases
 // in registers, and loads the next row before it joins the sums of this one.
-// 8192 x 4096 bf16, 134 MB: 25 us, 5.4 TB/s, where a copy of it takes 22-24: a row's
+// 8192 x 4096 bf16, 134 MB: 24-25 us, 5.5 TB/s, where a copy of it takes 22-24: a row's
 // chain of load, sum over its lanes and store is what a workgroup waits for. (Past the
 // caches 29 us, by 512 lanes 37, by a wave a row, without a barrier but with 64
-// columns a lane, 40.) With codes 38-40 us, 4.3 TB/s: beside the chain, the arithmetic
-// (64-bit sums and maxima of blocks: 14 us of it).
+// columns a lane, 40.) With codes 36-39 us, 4.5 TB/s: beside the chain, the arithmetic
+// (64-bit sums and maxima of blocks: 14 us of it). f32, 268 MB: 60 us, 4.5 TB/s.
 
 // Waves that the registers of a SIMD hold.
 constexpr int norm_waves(int keep, bool save) { return keep == 1 ? (save ? 5 : 7) : (save ? 3 : 4); }
@@ -666,14 +666,14 @@ __device__ __forceinline__ void store_param(void* p, bool bf16, int64_t i, float
 // next row is loaded while this one is worked on, and one barrier a row joins
 // the waves' sums (two sets of them in turn). In the end the groups' sums meet
 // in LDS. (16 columns a lane would take more registers than 16 waves have.)
-// 8192 x 4096 bf16, 201 MB: 43 us, 4.6 TB/s, with the join below; from codes, 168 MB,
-// 35 us; dx alone 36. Bound by memory and, every row, the barrier's wait. Rows of odd
-// width 63 us (8192 x 4091): loads from odd addresses take the vector memory twice as long.
+// 8192 x 4096 bf16, 201 MB: 37-40 us, 5.0-5.4 TB/s, with the join below; from codes, 168 MB,
+// 35 us. Bound by memory and, every row, the barrier's wait. Rows of odd width 49 us (8192
+// x 4091): loads from odd addresses take the vector memory twice as long. f32: 78 us.
 template <typename S, bool SAVED, int LANES>
 __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
   constexpr int kGroups = 1024 / LANES, kWaves = LANES / 64, kCols = LANES * 8;
   // Lanes with none of the row skip its sums, or have zeros for its statistics: 4096 x
-  // 8192 f32 85 and 105 us (by the registers of the 1024 lanes), 32 x 1024 bf16 6.9 and 6.6.
+  // 8192 f32 83 and 105 us (by the registers of the 1024 lanes), 32 x 1024 bf16 6.9 and 6.6.
   constexpr bool kSkip = LANES == 1024;
   __shared__ float sums[kGroups * kCols];
   __shared__ f32x2 joint[2][16];
@@ -758,7 +758,7 @@ __global__ __launch_bounds__(1024) void norm_backward(Norm a) {
 }
 
 // Longer rows: dx by a workgroup a row, in two passes over it, two runs of a lane at once:
-// 2048 x 16384 bf16 with the sums below and their join in 88 us. Dx and sums each read all of dy and
+// 2048 x 16384 bf16 with the sums below and their join in 85 us. Dx and sums each read all of dy and
 // x, where a shorter row's are read once: three times the floor, for widths that are rare.
 template <typename S, bool SAVED, int LANES>
 __global__ __launch_bounds__(LANES) void norm_backward_long(Norm a) {
@@ -978,8 +978,9 @@ constexpr int64_t kNormGrid = 256;
 constexpr int64_t kMaxNorm = int64_t{1} << 24;   // columns of a row
 constexpr int64_t kCus = 256;                    // compute units of an MI355X
 // Rows of more than 8192 columns from which a workgroup has 256 lanes, not 1024, as several
-// of these share a compute unit: (loads past the caches) 4096 x 8200 bf16 forward 43 and 52 us, with codes 60 and
-// 96; below it the row's own time counts: 64 x 131072 80 and 34, 512 x 16384 15.5 and 11.9.
+// of these share a compute unit (us, bf16 forward, 256 lanes and 1024): 1024 x 9000 9.6 and
+// 13, 4096 x 8200 31 and 49, with codes 45 and 81; below it the row's own time counts: 64 x
+// 131072 49 and 19, 512 x 16384 9.5 and 7.9. (2048 x 16384: 30 and 28.)
 constexpr int64_t kManyLong = 1024;
 
 // Workgroups' sums in the norm's backward pass: of rows of more than 8192 columns, which
@@ -1002,8 +1003,9 @@ template <typename S, bool SAVE>
 hipError_t norm_forward(const Norm& a, hipStream_t s) {
   const auto one = [&](auto* f, int lanes, int keep) {
     // As many workgroups as the chip holds at once, each with the same number of rows
-    // or one fewer: (loads past the caches) 8192 x 4096 bf16 in 29 us by 1024, 33 by 2048, 37 by 1280 and 45 by
-    // 8192; with codes 43 by 768, 50 by 2048.
+    // or one fewer: 8192 x 4096 bf16 in 25 us by 1024, 25 by 2048, 28 by 1280, 29 by 512 and
+    // 31 by 8192; with codes 37 by 768, 37 by 2048 and 42 by 512; 4096 x 8192 23 us by 512, 26
+    // by 2048 and 32 by 4096. (f32 rows go the other way: 8192 x 4096 60 us by 1024, 47 by 8192.)
     const int threads = std::max(256, lanes);
     const int64_t groups = threads / lanes, rows = (a.rows + groups - 1) / groups;
     const int64_t held = kCus * (4 * norm_waves(keep, SAVE) / (threads / 64)), turns = (rows + held - 1) / held;
@@ -1013,7 +1015,7 @@ hipError_t norm_forward(const Norm& a, hipStream_t s) {
   if (a.cols <= 1024) return one(&norm_rows<S, 128, 1, SAVE>, 128, 1);
   if (a.cols <= 2048) return one(&norm_rows<S, 256, 1, SAVE>, 256, 1);
   if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 256, 2);
-  if constexpr (SAVE) {   // (4096 x 8192 bf16 51 us, 57 by 512 lanes, whose two workgroups a CU no longer holds)
+  if constexpr (SAVE) {   // (4096 x 8192 f32 54 us, 62 by 512 lanes; bf16 49 and 46, 4096 x 5000 45 and 46)
     if (a.cols <= 8192) return one(&norm_rows<S, 1024, 1, SAVE>, 1024, 1);
   } else {
     if (a.cols <= 8192) return one(&norm_rows<S, 512, 2, SAVE>, 512, 2);
@@ -1030,8 +1032,8 @@ hipError_t norm_back(Norm a, hipStream_t s) {
   hipError_t e = hipSuccess;
   const auto one = [&](auto* f, int groups) {
     // Up to four turns of one workgroup cost less than the launch that joins several
-    // ones' sums: 32 rows of 1024 columns 6.6 us alone, 7.8 joined; 8 x 4096 7.5 and
-    // 8.5; 64 x 1024 (8 turns) 10.1 and 7.8.
+    // ones' sums: 32 rows of 1024 columns 6.7 us alone, 8.1 joined; 8 x 4096 7.6 and
+    // 8.7; 64 x 1024 (8 turns) 10.3 and 8.2.
     parts = sums && a.rows <= 4 * groups ? 1 : std::min<int64_t>((a.rows + groups - 1) / groups, kNormGrid);
     a.alone = sums && parts == 1;
     // A lane's sum takes up to `fold` rows (fold_of); more of them are as many launches,
