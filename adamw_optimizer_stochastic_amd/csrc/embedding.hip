@@ -10,8 +10,8 @@
 // id inside a chunk is finished there, one that crosses a chunk's border leaves
 // an f32 partial sum. (3) These are joined in order. The zeros of rows without a
 // token, most of a large table, are written beside (1), over the whole table, where
-// one workgroup's LDS holds the sort (up to 8192 tokens) and the table is large for
-// its tokens; else beside (2), where flags tell which rows these are.
+// one workgroup's LDS holds the sort (up to 8192 tokens); else beside (2), where flags
+// tell which rows these are.
 #include "rows.hpp"
 #include "status.hpp"
 
@@ -60,8 +60,8 @@ struct Lookup {
 
 // Rows of up to 8 << log_lanes columns side by side, U rows of a lane loaded
 // together; an id outside the table gives NaN. Bound by memory: 8192 rows of 4096
-// bf16, 134 MB, in 22 us, 6.1 TB/s (an id's load comes before its row's, which 4 rows
-// at once hide); 16 rows 3 us, the two loads' latency.
+// bf16, 134 MB, in 21 us, 6.3 TB/s (by one row a lane as well); f32, 268 MB, in 53 us, by
+// one row 55; 16 rows 3 us, the latency of an id's load and its row's.
 template <typename S, int U>
 __global__ __launch_bounds__(256) void lookup(Lookup a) {
   for (uint32_t item = blockIdx.x; item < a.items; item += gridDim.x) {
@@ -106,7 +106,7 @@ struct Sort {
 
 // Zeros for the rows without a token (flags: a bit an id that has one; NULL: for all
 // rows). A workgroup's lanes store 8 columns each and end: workgroups in the order of
-// memory with one store a lane reach 7.2 TB/s on a table of 1 GB, with 2 or 4 stores
+// memory with one store a lane (bf16) reach 7.2 TB/s on a table of 1 GB, with 2 or 4 stores
 // 6.4 and 5.8, as loops over the table 4.0 to 6.2; the wait for a flag costs a sixth.
 struct Fill {
   void* dw;
@@ -120,10 +120,29 @@ template <typename S, int THREADS>
 __device__ __forceinline__ void fill_rows(const Fill& a, uint32_t block) {
   const uint32_t up = block / a.strips, strip = block - up * a.strips;
   const int64_t v = static_cast<int64_t>(up) * (THREADS >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
-  const int64_t col = ((static_cast<int64_t>(strip) << a.log_lanes) + (threadIdx.x & ((1u << a.log_lanes) - 1))) * 8;
+  const int32_t lanes = 1 << a.log_lanes, lane = threadIdx.x & (lanes - 1);
   if (v >= a.vocab || (a.flags && ((a.flags[v / 32] >> (v % 32)) & 1u))) return;
-  const float zero[8] = {};
-  store8(static_cast<S*>(a.dw) + v * a.dim + col, a.dim - col, zero);
+  S* row = static_cast<S*>(a.dw) + v * a.dim;
+  const int64_t first = (static_cast<int64_t>(strip) << a.log_lanes) * 8;
+  if constexpr (std::is_same_v<S, float>) {
+    // 16 bytes of a lane next to its neighbour's, so that a store covers whole lines (32
+    // bytes a lane in two stores: 128256 x 4096 beside the sort 965 us, so 440)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t col = first + (k * lanes + lane) * 4;
+      if (col + 4 <= a.dim) {
+        store_stream(reinterpret_cast<f32x4_any*>(row + col), asr::f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (col + e < a.dim) row[col + e] = 0.0f;
+      }
+    }
+  } else {
+    const float zero[8] = {};
+    const int64_t col = first + lane * 8;
+    store8(row + col, a.dim - col, zero);
+  }
 }
 
 // The place of each of a tile's keys when the tile is ordered by one digit, stable.
@@ -177,25 +196,6 @@ __device__ __forceinline__ void tile_places(const uint32_t (&key)[R], uint32_t s
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) place[r] += counts[((key[r] >> shift) & mask) * W + wave];
-}
-
-// Which ids have one of up to 8192 tokens: a workgroup marks 2**19 ids in LDS.
-constexpr int kMarks = 1 << 19;
-
-__global__ __launch_bounds__(1024) void flag_tokens(Ids ids, uint32_t* flags) {
-  __shared__ uint32_t marks[kMarks / 32];
-  const uint32_t first = blockIdx.x * static_cast<uint32_t>(kMarks);
-  const uint32_t count = static_cast<uint32_t>(min(ids.vocab - first, int64_t{kMarks}));
-  for (uint32_t i = threadIdx.x; i < (count + 31) / 32; i += 1024) marks[i] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < kTile / 1024; ++r) {
-    const int64_t i = r * 1024 + threadIdx.x;
-    const uint32_t at = i < ids.n ? key_at(ids, i) - first : kPast;   // (past the range if below it)
-    if (at < count) atomicOr(&marks[at / 32], 1u << (at % 32));
-  }
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < (count + 31) / 32; i += 1024) flags[first / 32 + i] = marks[i];
 }
 
 // Up to 64 W R tokens, all passes, by the first workgroup. The others meanwhile write
@@ -368,18 +368,21 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   const uint32_t before = there && i0 > 0 ? a.keys[i0 - 1] : kPast, after = there && i1 < a.n ? a.keys[i1] : kPast;
   uint32_t run = kPast;      // of acc; no key of the table before the first
   bool head = false;
-  float acc[8] = {}, all[8] = {};   // all: of the run's positions before the last fold
+  float acc[8] = {};
+  float all[8] = {};   // of the run's positions before the last fold
   int32_t held = 0;
   for (int32_t start = 0; start < a.chunk; start += kBatch) {
-    if (held == a.fold) {
-      held = 0;
+    {
+      if (held == a.fold) {
+        held = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        all[e] += acc[e];
-        acc[e] = 0.0f;
+        for (int e = 0; e < 8; ++e) {
+          all[e] += acc[e];
+          acc[e] = 0.0f;
+        }
       }
+      held += kBatch;
     }
-    held += kBatch;
     if (start > 0) __syncthreads();   // (the last batch is read)
     if (static_cast<int>(threadIdx.x) < side * kBatch) {
       const int64_t i = (c0 + threadIdx.x / kBatch) * a.chunk + start + threadIdx.x % kBatch;
@@ -431,7 +434,11 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
           run = key;
           head = start + half + k == 0 && run == before;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = all[e] = 0.0f;
+          for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+          if (a.chunk > a.fold) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) all[e] = 0.0f;
+          }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += r.get(e);   // (what the turn after the last one adds, no one stores)
@@ -635,7 +642,7 @@ struct Buffers {
     keys[1] = take<uint32_t>(several ? n : 0);
     toks[1] = take<uint32_t>(several ? n : 0);
     hist = take<uint32_t>(several ? kBins * cut.tiles : 0);
-    flags = take<uint32_t>((vocab + 31) / 32);
+    flags = take<uint32_t>(several ? (vocab + 31) / 32 : 0);
     part = take<float>(static_cast<int64_t>(cut.chunks) * 2 * dim);
   }
 };
@@ -676,9 +683,9 @@ int64_t fill_blocks(const Fill& f, int threads) {
 }
 
 template <typename S>
-hipError_t sort_one_tile(const Sort& a, const Fill& fill, bool beside, hipStream_t s) {
+hipError_t sort_one_tile(const Sort& a, const Fill& fill, hipStream_t s) {
   const auto one = [&](auto* f, int threads) {
-    return launch(f, dim3(static_cast<uint32_t>(1 + (beside ? fill_blocks(fill, threads) : 0))), threads, s, a, fill);
+    return launch(f, dim3(static_cast<uint32_t>(1 + fill_blocks(fill, threads))), threads, s, a, fill);
   };
   if (a.ids.n <= 1024) return one(&sort_and_fill<S, 4, 4>, 256);
   if (a.ids.n <= 2048) return one(&sort_and_fill<S, 4, 8>, 256);
@@ -729,7 +736,8 @@ int asr_embedding_forward(const void* ids, int32_t ids_64, int64_t n, const void
   a.scale = static_cast<float>(scale);
   a.log_lanes = lanes_of(dim);
   a.strips = static_cast<uint32_t>((dim + (int64_t{8} << a.log_lanes) - 1) / (int64_t{8} << a.log_lanes));
-  // 4 rows of a lane, as long as that leaves enough workgroups for the chip
+  // 4 rows of a lane, as long as that leaves enough workgroups for the chip (4 of them a
+  // compute unit; 512 to 2048 rows of 4096 take 3.5 to 5.1 us either way)
   const int64_t rows = 256 >> a.log_lanes;
   const bool many = (n + 4 * rows - 1) / (4 * rows) * a.strips >= 4 * kCus;
   const int64_t up = (n + (many ? 4 : 1) * rows - 1) / ((many ? 4 : 1) * rows);
@@ -807,23 +815,20 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
     if (cut.tiles > 1) {
       e = sort_tiles(sort, b, cut, s);
     } else {
-      // Zeros over the whole table beside the sort, where a quarter of its rows at most
-      // are written again (128256 x 4096, 8192 tokens: 189 us, with flags 209;
-      // 182 since the gradients' rows come through the caches).
-      filled = vocab >= 4 * n;
-      if (!filled)
-        e = launch(&flag_tokens, dim3(static_cast<uint32_t>((vocab + kMarks - 1) / kMarks)), 1024, s, sort.ids, b.flags);
-      if (e == hipSuccess)
-        e = dtype == ASR_F32 ? sort_one_tile<float>(sort, a.fill, filled, s)
-                             : sort_one_tile<uint16_t>(sort, a.fill, filled, s);
+      // Zeros over the whole table beside the sort, those of rows with tokens too (8192
+      // tokens; beside it and after it by flags: 128256 x 4096 bf16 183 us and 216, f32 440
+      // and 430, 8000 x 4096 bf16 58 and 61, 30000 x 1024 f32 50 and 64).
+      e = dtype == ASR_F32 ? sort_one_tile<float>(sort, a.fill, s) : sort_one_tile<uint16_t>(sort, a.fill, s);
+      filled = true;
     }
     a.fill.flags = b.flags;
     a.keys = sort.keys;
     a.toks = sort.toks;
   }
-  if (e == hipSuccess)
-    e = launch(dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>,
-               dim3(static_cast<uint32_t>(summing + (filled ? 0 : filling))), 256, s, a);
+  if (e == hipSuccess) {
+    auto* f = dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>;
+    e = launch(f, dim3(static_cast<uint32_t>(summing + (filled ? 0 : filling))), 256, s, a);
+  }
   if (e == hipSuccess && a.chunks > 1)
     e = launch(dtype == ASR_F32 ? &join_runs<float> : &join_runs<uint16_t>,
                dim3(static_cast<uint32_t>(a.chunks), static_cast<uint32_t>(strips4)), 256, s, a);

@@ -67,7 +67,7 @@ __device__ __forceinline__ const QuantJob& job_of(const QuantArgs& a) {
 // x and w of a linear layer, 4096 and 14336 rows of 4096 bf16 (226 MB with the
 // codes), take 42-46 us, 4.9-5.4 TB/s, 1.15 to 1.25 times a copy's time: a workgroup
 // holds one row from its load through two reductions to its store, with no other
-// in flight. 14336 rows alone: 37-40 us to nearest, 54 stochastic (the random
+// in flight. 14336 rows alone: 35-36 us to nearest, 50 stochastic (the random
 // bits). One row of 4096 takes 3 us, its latency.
 template <typename S, bool SR, int LANES>
 __global__ __launch_bounds__(256) void quantize_rows(QuantArgs args) {
