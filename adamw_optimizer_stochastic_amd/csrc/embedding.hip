@@ -347,7 +347,9 @@ struct Sums {
 // lane puts into its own part of LDS: the loop over the runs then has one copy of its
 // code for all of them (unrolled over rows in registers it was 22 KB, and fetching it
 // was most of a small call's time). 8192 tokens of 4096 bf16, 134 MB: 21 us, 6.4 TB/s.
-template <typename S>
+// FOLDS: chunks of more than `fold` positions, whose runs are summed in two levels (8 more
+// registers and their additions, a few per cent of a call of few thousand tokens).
+template <typename S, bool FOLDS>
 __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   constexpr int kBatch = 16, kAhead = 8, kSide = 16;
   __shared__ Run<S> rows[kAhead * 256];
@@ -369,10 +371,10 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
   uint32_t run = kPast;      // of acc; no key of the table before the first
   bool head = false;
   float acc[8] = {};
-  float all[8] = {};   // of the run's positions before the last fold
-  int32_t held = 0;
+  [[maybe_unused]] float all[8] = {};   // of the run's positions before the last fold
+  [[maybe_unused]] int32_t held = 0;
   for (int32_t start = 0; start < a.chunk; start += kBatch) {
-    {
+    if constexpr (FOLDS) {
       if (held == a.fold) {
         held = 0;
 #pragma unroll
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
         if (key != run) {
           if (run < vocab) {
             const bool tail = k == kAhead ? after == run : false;
-            if (a.chunk > a.fold) {
+            if constexpr (FOLDS) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) acc[e] += all[e];
             }
@@ -435,7 +437,7 @@ __global__ __launch_bounds__(256) void sum_and_fill(Sums a) {
           head = start + half + k == 0 && run == before;
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-          if (a.chunk > a.fold) {
+          if constexpr (FOLDS) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) all[e] = 0.0f;
           }
@@ -826,7 +828,9 @@ int asr_embedding_backward(const void* ids, int32_t ids_64, int64_t n, const voi
     a.toks = sort.toks;
   }
   if (e == hipSuccess) {
-    auto* f = dtype == ASR_F32 ? &sum_and_fill<float> : &sum_and_fill<uint16_t>;
+    const bool folds = a.chunk > a.fold;
+    auto* f = dtype == ASR_F32 ? (folds ? &sum_and_fill<float, true> : &sum_and_fill<float, false>)
+                               : (folds ? &sum_and_fill<uint16_t, true> : &sum_and_fill<uint16_t, false>);
     e = launch(f, dim3(static_cast<uint32_t>(summing + (filled ? 0 : filling))), 256, s, a);
   }
   if (e == hipSuccess && a.chunks > 1)
