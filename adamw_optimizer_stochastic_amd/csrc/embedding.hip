@@ -650,8 +650,8 @@ struct Buffers {
 };
 
 // Few tokens (one a thread) and a small table: one launch. (us, that and the launches above,
-// bf16: 16 tokens, 100 x 64: 5.0 and 11; 777, 1009 x 333: 6.7 and 25; 1024 of one id, 1009
-// x 512: 15.6 and 25; 1024, 16000 x 1024: 13.5 and 19.5; 256, 100000 x 64: 11 and 18.
+// bf16: 16 tokens, 100 x 64: 5.0 and 11; 777, 1009 x 333: 6.7 and 22; 1024 of one id, 1009
+// x 512: 15.7 and 21; 1024, 16000 x 1024: 13.6 and 17.7; 256, 100000 x 64: 11 and 17.
 // Beyond, the order of the table's zeros counts more.)
 bool direct(int64_t n, int64_t vocab, int64_t dim) {
   return n > 0 && n <= 1024 && vocab <= int64_t{1} << 17 && vocab * dim <= int64_t{1} << 24;

@@ -1005,7 +1005,7 @@ hipError_t norm_forward(const Norm& a, hipStream_t s) {
   const auto one = [&](auto* f, int lanes, int keep) {
     // As many workgroups as the chip holds at once, each with the same number of rows
     // or one fewer: 8192 x 4096 bf16 in 25 us by 1024, 25 by 2048, 28 by 1280, 29 by 512 and
-    // 31 by 8192; with codes 37 by 768, 37 by 2048 and 42 by 512; 4096 x 8192 23 us by 512, 26
+    // 31 by 8192; with codes 37 by 768, 37 by 2048 and 41 by 512; 4096 x 8192 23 us by 512, 26
     // by 2048 and 32 by 4096. (f32 rows go the other way: 8192 x 4096 60 us by 1024, 47 by 8192.)
     const int threads = std::max(256, lanes);
     const int64_t groups = threads / lanes, rows = (a.rows + groups - 1) / groups;
@@ -1016,7 +1016,7 @@ hipError_t norm_forward(const Norm& a, hipStream_t s) {
   if (a.cols <= 1024) return one(&norm_rows<S, 128, 1, SAVE>, 128, 1);
   if (a.cols <= 2048) return one(&norm_rows<S, 256, 1, SAVE>, 256, 1);
   if (a.cols <= 4096) return one(&norm_rows<S, 256, 2, SAVE>, 256, 2);
-  if constexpr (SAVE) {   // (4096 x 8192 f32 54 us, 62 by 512 lanes; bf16 49 and 46, 4096 x 5000 45 and 46)
+  if constexpr (SAVE) {   // (4096 x 8192 f32 55 us, 63 by 512 lanes; bf16 46-49 and 46, 4096 x 5000 45 and 46)
     if (a.cols <= 8192) return one(&norm_rows<S, 1024, 1, SAVE>, 1024, 1);
   } else {
     if (a.cols <= 8192) return one(&norm_rows<S, 512, 2, SAVE>, 512, 2);
