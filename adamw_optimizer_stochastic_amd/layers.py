@@ -162,7 +162,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, saved="input"):
     the normalised rows (``ops.pack_i8``'s of their 64-bit values), a half or a
     quarter of x's bytes, and takes the gradients from what they stand for. A row
     with an Inf or NaN gives NaN; x - mean is formed in binary32 and has to fit
-    there. Up to 2**24 columns, fewer than 2**24 rows.
+    there, as has 1 / sqrt(var + eps). Up to 2**24 columns, fewer than 2**24 rows.
     """
     if saved not in ("input", "i8"):
         raise ValueError("saved must be 'input' or 'i8'")
@@ -277,7 +277,7 @@ def silu_mul(gate, up=None, *, saved="inputs"):
 
     saved: "inputs" keeps gate and up for the backward pass; "i8" their 8-bit
     codes (``ops.pack_i8``'s, to nearest), and takes the gradients from what
-    these stand for. Where the sigmoid is below 2**-126 (a gate under -87) it may be
+    these stand for. Both gradients are computed together. Where the sigmoid is below 2**-126 (a gate under -87) it may be
     taken as 0.
     """
     if saved not in ("inputs", "i8"):
