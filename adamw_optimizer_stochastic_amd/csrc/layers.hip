@@ -11,9 +11,10 @@
 //   with g = dy w: dx = rstd (g - sum g / C - xh sum(g xh) / C),
 //   dw = sum over rows of dy xh, db = sum over rows of dy.
 // mean and var are summed in 64 bits (so that one pass over the row gives both) and
-// kept for the backward pass as two f32 numbers for the mean and one for rstd. Or the pass keeps the 8-bit codes of xh instead of x: their
-// definition is the codes of the 64-bit xh, so that no rounding on the way
-// decides one, and gradients use what the codes stand for.
+// kept for the backward pass as two f32 numbers for the mean and one for rstd. Or the
+// pass keeps the 8-bit codes of xh instead of x: their definition is the codes of the
+// 64-bit xh, so that no rounding on the way decides one, and gradients use what the
+// codes stand for.
 //
 // gated SiLU: y = g sig(g) u, du = dy g sig(g), dg = dy u sig(g) (1 + g (1 - sig(g))),
 // from g and u themselves or from their 8-bit codes.

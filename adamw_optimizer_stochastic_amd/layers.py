@@ -277,8 +277,8 @@ def silu_mul(gate, up=None, *, saved="inputs"):
 
     saved: "inputs" keeps gate and up for the backward pass; "i8" their 8-bit
     codes (``ops.pack_i8``'s, to nearest), and takes the gradients from what
-    these stand for. Both gradients are computed together. Where the sigmoid is below 2**-126 (a gate under -87) it may be
-    taken as 0.
+    these stand for. Both gradients are computed together. Where the sigmoid is
+    below 2**-126 (a gate under -87) it may be taken as 0.
     """
     if saved not in ("inputs", "i8"):
         raise ValueError("saved must be 'inputs' or 'i8'")

@@ -427,7 +427,8 @@ int asr_unpack_i8(const int8_t* q, int64_t ldq, const float* scale,
  *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy.
  * mean and rstd are formed in 64 bits, the rest in 32; the sums over rows take an order
  * that depends on the sizes only, in several levels, so that rounding them costs at most
- * (342 + 3 sqrt(rows / 256 + rows cols / 2**22)) 2**-24 of the sums of the magnitudes. weight, bias: cols elements of param_dtype,
+ * (342 + 3 sqrt(rows / 256 + rows cols / 2**22)) 2**-24 of the sums of the magnitudes.
+ * x - mean and rstd have to fit binary32. weight, bias: cols elements of param_dtype,
  * NULL: 1 and 0. stat: NULL, or rows x 4 f32 that the backward call takes.
  * q, scale: NULL, or they receive asr_pack_i8's codes (to nearest) of xh,
  * computed in 64 bits; the backward call then takes them, with x NULL, and uses what
@@ -470,8 +471,8 @@ int asr_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x,
  * Requirements: sizes, codes and alignment as for asr_pack_i8; row strides at least
  * cols; no output overlaps an input, but in the forward call y may be gate or
  * up, and in the backward call dgate may be dy, gate or up, and dup another of them (with the same
- * stride). A sig(g) below 2**-126 may be taken as 0. Errors: ASR_EINVAL, ASR_EDTYPE, ASR_EALIGN, ASR_EHIP. Run on
- * `stream`; do not synchronize.
+ * stride). A sig(g) below 2**-126 may be taken as 0. Errors: ASR_EINVAL, ASR_EDTYPE,
+ * ASR_EALIGN, ASR_EHIP. Run on `stream`; do not synchronize.
  */
 int asr_silu_mul_forward(const void* gate, int64_t ld_gate, const void* up,
                          int64_t ld_up, int32_t dtype, int64_t rows,
